@@ -14,7 +14,8 @@
  *   pkv_advance[_batch]         once per step, after the last layer
  *
  * Conventions
- *   - All float data are IEEE f32, row-major.  Q and out are [rows, n_heads*head_dim];
+ *   - All float data are IEEE f32 unless a declaration names another type,
+ *     row-major.  Q and out are [rows, n_heads*head_dim];
  *     K_new and V_new are [rows, n_kv_heads*head_dim] ("nx_f32_gqa_attention.nx
  *     source", header).  Query head h reads kv head h / (n_heads / n_kv_heads).
  *   - Device pointers are CUDA device addresses, 16-byte aligned when head_dim
@@ -108,6 +109,46 @@ typedef void *pkv_stream_t; /* cudaStream_t */
 PKV_API pkv_pool *pkv_pool_new(int32_t n_blocks, int32_t n_layers, int32_t kv_dim, int32_t block_size,
                        void *k_pool_dev, void *v_pool_dev, int32_t max_seqs,
                        int32_t max_blocks_per_seq, pkv_stream_t stream, uint32_t flags);
+
+/* A pool of 8-bit elements with a scale for every (block, layer, kv head), K
+ * and V apart (no counterpart on the pages).  The stored element u, 1 .. 255,
+ * stands for (u - 128) * s with s the scale of its block and head, a power of
+ * two, so the values a call reads are exact in f32 and only the storage
+ * rounding differs from an f32 pool.  Layout: elements
+ * [n_blocks][n_layers][block_size][n_kv_heads * head_dim] bytes, scales f32
+ * [n_blocks][n_layers][n_kv_heads].
+ *
+ * Appending rows to a block: with m the largest magnitude among the new rows
+ * of a head, need(m) is the least e >= -126 with m <= 127 * 2^e.  A block
+ * written from its first row takes the scale 2^need(m); later rows take the
+ * larger of that and the present scale, and where the scale grows the rows
+ * already in the block are rounded to the new step.  Rounding is to nearest,
+ * ties to even.  A stored value is within half a step of the appended one, and
+ * within one step after any growths.  A value that is not finite makes the
+ * scale NaN: the block's values of that head then read as NaN until the block
+ * is written from its first row again (an attention output that depends on
+ * them is NaN; in a call with n_q >= 32 rows of one sequence, other queries of
+ * the same sequence may be too).
+ *
+ * Every pool call works on it: pkv_attn_batch and its forms (n_kv_heads and
+ * head_dim as given here, PKV_ERR_BAD_DIM otherwise), pkv_append_layer,
+ * fork / copy-on-append (scales included), truncate, the image cache, shared
+ * prefixes.  There is no fused append.  A call with 2 to 31 queries of a row
+ * reads that row's keys once for several queries.  Attention and append calls
+ * on this pool cannot be captured into a CUDA graph (PKV_ERR_ARG).
+ *
+ * k_pool_dev / v_pool_dev (16-byte aligned) and k_scale_dev / v_scale_dev:
+ * caller-owned device buffers, all four or none (the library then allocates
+ * them).  n_kv_heads * head_dim a multiple of 4, head_dim <= 256.  flags: 0 or
+ * PKV_POOL_HOST_ONLY.  NULL on failure. */
+PKV_API pkv_pool *pkv_pool_new_q8(int32_t n_blocks, int32_t n_layers, int32_t n_kv_heads, int32_t head_dim,
+                                  int32_t block_size, void *k_pool_dev, void *v_pool_dev, float *k_scale_dev,
+                                  float *v_scale_dev, int32_t max_seqs, int32_t max_blocks_per_seq,
+                                  pkv_stream_t stream, uint32_t flags);
+
+/* Device addresses of an 8-bit pool's scales; NULL for any other pool. */
+PKV_API float *pkv_pool_k_scales(const pkv_pool *pool);
+PKV_API float *pkv_pool_v_scales(const pkv_pool *pool);
 
 /* Release the pool, every sequence still alive in it, and library-owned memory.
  * Waits for the pool stream first. */
@@ -352,6 +393,64 @@ PKV_API int pkv_attn_contiguous_noalloc(const float *Q, const float *Kc, const f
                                         int32_t n_q, int32_t total_k, int32_t n_heads,
                                         int32_t n_kv_heads, int32_t head_dim, int32_t causal,
                                         float scale, float *out, pkv_stream_t stream);
+
+/* -------------------------------------------------------- packed prompts ---- */
+
+/* Element types of packed rows. */
+enum pkv_dtype {
+    PKV_F32 = 0,
+    PKV_BF16 = 1,
+    PKV_F16 = 2
+};
+
+/* Attention over whole prompts that lie behind one another (no counterpart on
+ * the pages; the prompt half of a prefill, before any page is involved).
+ * Sequence s owns lens[s] consecutive rows (lens: host array, entries >= 0) of
+ * Q, K, V and out, in order from row 0; its query i attends keys j <= i of the
+ * same sequence (causal != 0) or all of them:
+ *   out[i, h] = softmax_j(scale * <Q[i, h], K[j, kv(h)]>) V[j, kv(h)],
+ * kv(h) = h / (n_heads / n_kv_heads).  Row i of Q starts q_stride elements
+ * after row i - 1 (heads side by side inside a row), and likewise K, V and out,
+ * so columns of a fused projection's output can be passed as they are.  dtype:
+ * PKV_BF16 or PKV_F16, for all four.  Scores, softmax statistics and the
+ * output accumulate in f32; the probabilities are rounded to dtype before they
+ * meet V, and the output once at the end.  A key that a query does not see
+ * never reaches it, whatever it holds.  Rows of out past the last sequence
+ * are left as they were; out may not overlap the inputs.
+ *
+ * head_dim a multiple of 8, at most 128, with pointers and strides on 16-byte
+ * boundaries runs on the tensor cores; any other head_dim <= 256 or alignment
+ * (to the element) on a general kernel.  Needs no scratch, uploads nothing and
+ * can be captured into a CUDA graph (the lengths are then part of the graph),
+ * provided that an earlier call outside a capture set up the device's error
+ * word.  Runs on `stream` and the current device.  Checks, in order: sizes
+ * -> PKV_ERR_BAD_DIM, grouping -> PKV_ERR_BAD_GQA, dtype, strides, pointers ->
+ * PKV_ERR_ARG.  Failures found on the device: pkv_contiguous_sync_error. */
+PKV_API int pkv_attn_packed(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, const void *V,
+                            int64_t v_stride, int32_t dtype, const int32_t *lens, int32_t n_seqs,
+                            int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t causal,
+                            float scale, void *out, int64_t out_stride, pkv_stream_t stream);
+
+/* pkv_append_layer for a batch of sequences and rows of any type: writes n[r]
+ * rows of K and V at positions len .. len + n[r] - 1 of sequence r, converted
+ * to the pool's element as an append converts them (f32 -> itself, bf16, fp8
+ * or the 8-bit form).  The batch's rows are packed in order; row i starts
+ * stride elements after row i - 1.  dtype: PKV_F32, PKV_BF16 or PKV_F16,
+ * pointers aligned to it.  The rows must have been ensured (PKV_ERR_SEQ);
+ * duplicate sequences -> PKV_ERR_ARG.  Cannot be captured into a graph. */
+PKV_API int pkv_append_packed(pkv_seq *const *seqs, int32_t M, const int32_t *n, int32_t layer, const void *K,
+                              int64_t k_stride, const void *V, int64_t v_stride, int32_t dtype);
+
+/* The reverse: rows start[r] .. start[r] + n[r] - 1 of each sequence, as the
+ * values they stand for, packed in batch order into K and V (each rounded once
+ * to dtype; PKV_F16 overflows to infinity past 65504).  For swapping a
+ * sequence out, or moving it to a pool of another kind with pkv_append_packed.
+ * The rows must lie in the sequence's pages (PKV_ERR_SEQ); rows that no call
+ * wrote read as whatever the pages hold.  A sequence may appear several times.
+ * Cannot be captured into a graph. */
+PKV_API int pkv_read_packed(pkv_seq *const *seqs, int32_t M, const int32_t *start, const int32_t *n,
+                            int32_t layer, void *K, int64_t k_stride, void *V, int64_t v_stride,
+                            int32_t dtype);
 
 /* ---------------------------------------------------------- diagnostics ---- */
 

@@ -22,6 +22,8 @@ Contents
                       ties to even; ``kv_format.py``).
 ``round_e4m3``        the fp8 pool's stored-and-read value (e4m3 of x/scale,
                       nearest, ties to even, saturating; ``kv_format.py``).
+``q8_append``         the 8-bit pool's elements and exponent of one block and
+                      kv head after an append (``kv_format.py``).
 
 Every function cites the passage of the pages it follows; the pages are the
 source listings "nx_f32_attn_paged.nx source", "nx_f32_gqa_attention.nx
@@ -135,7 +137,7 @@ from .contiguous_cache import ContiguousCache  # noqa: E402
 from .pool_model import PoolModel, SeqModel  # noqa: E402
 from . import pool_model  # noqa: E402
 from .rope import rope_neox, rope_neox_f32  # noqa: E402
-from .kv_format import round_bf16, round_e4m3  # noqa: E402
+from .kv_format import q8_append, q8_exponent, round_bf16, round_e4m3  # noqa: E402
 
 __all__ = ["attend", "build", "set_threads", "ContiguousCache", "PoolModel", "SeqModel", "pool_model",
            "OK", "ERR_BAD_DIM", "ERR_BAD_GQA"]

@@ -54,3 +54,31 @@ def round_e4m3(x, scale: float = 1.0) -> np.ndarray:
     r = np.rint(mag / ulp) * ulp                             # nearest, ties to even
     r = np.minimum(r, E4M3_MAX)                              # satfinite
     return (np.sign(a) * r * float(scale)).astype(np.float32)
+
+
+def q8_exponent(m: float) -> int:
+    """The least e >= -126 with m <= 127 * 2^e (an 8-bit block whose largest
+    new magnitude is m); every comparison is exact in binary64."""
+    e = -126
+    if m > 0:
+        e = max(-126, int(np.frexp(m)[1]) - 9)   # 127 * 2^e < m for certain, or the floor
+        while m > 127.0 * 2.0 ** e:
+            e += 1
+    return e
+
+
+def q8_append(elems, exponent, x, off):
+    """An 8-bit block of one kv head after rows x ([n, hd], finite) were written
+    at row offset off: (signed elements, exponent).  elems: the block's present
+    signed elements [bs, hd]; exponent: its present one (not looked at where
+    off is 0).  The first row's write takes the exponent the rows need, a later
+    one the larger of that and the present one; kept rows are rounded to the
+    new step; rounding to nearest, ties to even."""
+    x = np.asarray(x, dtype=np.float64)
+    q = np.array(elems, dtype=np.float64)
+    e = q8_exponent(float(np.abs(x).max()))
+    if off:
+        e = max(e, int(exponent))
+        q[:off] = np.rint(q[:off] * 2.0 ** (int(exponent) - e))
+    q[off:off + len(x)] = np.rint(x * 2.0 ** -e)
+    return q, e

@@ -40,6 +40,10 @@ PKV_POOL_BF16 = 2
 PKV_POOL_FP8 = 4
 PKV_NOALLOC_SCRATCH_BYTES = 16 << 20
 
+PKV_F32 = 0
+PKV_BF16 = 1
+PKV_F16 = 2
+
 PKV_KERNEL_APPEND = 0
 PKV_KERNEL_DECODE = 1
 PKV_KERNEL_MERGE = 2
@@ -73,6 +77,13 @@ _pi32 = ctypes.POINTER(ctypes.c_int32)
 
 _SIGS = {
     "pkv_pool_new": (_vp, [_i32, _i32, _i32, _i32, _vp, _vp, _i32, _i32, _vp, _u32]),
+    "pkv_pool_new_q8": (_vp, [_i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _u32]),
+    "pkv_pool_k_scales": (_vp, [_vp]),
+    "pkv_pool_v_scales": (_vp, [_vp]),
+    "pkv_attn_packed": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i32, _pi32, _i32, _i32, _i32, _i32, _i32, _f32,
+                               _vp, _i64, _vp]),
+    "pkv_append_packed": (_int, [_vp, _i32, _pi32, _i32, _vp, _i64, _vp, _i64, _i32]),
+    "pkv_read_packed": (_int, [_vp, _i32, _pi32, _pi32, _i32, _vp, _i64, _vp, _i64, _i32]),
     "pkv_pool_free": (None, [_vp]),
     "pkv_pool_set_stream": (_int, [_vp, _vp]),
     "pkv_pool_k_data": (_vp, [_vp]),
@@ -158,6 +169,30 @@ def _dev(t, name="tensor", dtypes=("float32",)):
     return t.data_ptr()
 
 
+_PACKED = {"float32": PKV_F32, "bfloat16": PKV_BF16, "float16": PKV_F16}
+
+
+def _rows(t, name, width=None):
+    """(address, row stride, element type) of packed rows: a CUDA tensor
+    [rows, width] whose rows are contiguous (columns of a wider one are fine)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
+        raise TypeError("%s must be a CUDA tensor [rows, width]" % name)
+    kind = _PACKED.get(str(t.dtype).replace("torch.", ""))
+    if kind is None:
+        raise TypeError("%s must be float32, bfloat16 or float16" % name)
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise TypeError("%s must have contiguous rows" % name)
+    if width is not None and t.shape[1] != width:
+        raise TypeError("%s must be %d wide" % (name, width))
+    return t.data_ptr(), max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0), kind
+
+
+def _enough(t, rows, name):
+    if t.shape[0] < rows:
+        raise TypeError("%s has %d rows, %d are needed" % (name, t.shape[0], rows))
+
+
 def _host(a, name="array"):
     """Host address of a contiguous f32 numpy array or CPU tensor."""
     if a is None:
@@ -217,6 +252,25 @@ def pkv_pool_new(n_blocks, n_layers, kv_dim, block_size, k_pool=None, v_pool=Non
     return _lib.pkv_pool_new(n_blocks, n_layers, kv_dim, block_size, _dev(k_pool, "k_pool", want),
                              _dev(v_pool, "v_pool", want), max_seqs, max_blocks_per_seq,
                              _stream(stream), flags)
+
+
+def pkv_pool_new_q8(n_blocks, n_layers, n_kv_heads, head_dim, block_size, k_pool=None, v_pool=None,
+                    k_scale=None, v_scale=None, max_seqs=1024, max_blocks_per_seq=4096, stream=None,
+                    flags=0):
+    """k_pool / v_pool: uint8 tensors [n_blocks, n_layers, block_size, n_kv_heads * head_dim],
+    k_scale / v_scale: float32 [n_blocks, n_layers, n_kv_heads]; all four or none."""
+    return _lib.pkv_pool_new_q8(n_blocks, n_layers, n_kv_heads, head_dim, block_size,
+                                _dev(k_pool, "k_pool", ("uint8",)), _dev(v_pool, "v_pool", ("uint8",)),
+                                _dev(k_scale, "k_scale"), _dev(v_scale, "v_scale"), max_seqs,
+                                max_blocks_per_seq, _stream(stream), flags)
+
+
+def pkv_pool_k_scales(pool):
+    return _lib.pkv_pool_k_scales(pool)
+
+
+def pkv_pool_v_scales(pool):
+    return _lib.pkv_pool_v_scales(pool)
 
 
 def pkv_pool_free(pool):
@@ -352,6 +406,51 @@ def pkv_attn_contiguous_noalloc(Q, Kc, Vc, n_q, total_k, n_heads, n_kv_heads, he
     return _lib.pkv_attn_contiguous_noalloc(_dev(Q, "Q"), _dev(Kc, "Kc"), _dev(Vc, "Vc"), n_q,
                                             total_k, n_heads, n_kv_heads, head_dim, causal, scale,
                                             _dev(out, "out"), _stream(stream))
+
+
+def pkv_attn_packed(Q, K, V, lens, n_heads, n_kv_heads, head_dim, causal, scale, out, stream=None):
+    """Q, out: [tokens, n_heads * head_dim], K, V: [tokens, n_kv_heads * head_dim], bfloat16 or
+    float16 CUDA tensors with contiguous rows (any row stride); lens: tokens per sequence."""
+    arr = _i32_array(lens)
+    n = len(lens)
+    total = sum(arr[:n])
+    q, qs, t = _rows(Q, "Q", n_heads * head_dim)
+    k, ks, tk = _rows(K, "K", n_kv_heads * head_dim)
+    v, vs, tv = _rows(V, "V", n_kv_heads * head_dim)
+    o, os_, to = _rows(out, "out", n_heads * head_dim)
+    if not t == tk == tv == to:
+        raise TypeError("Q, K, V and out must have one element type")
+    for x, name in ((Q, "Q"), (K, "K"), (V, "V"), (out, "out")):
+        _enough(x, total, name)
+    return _lib.pkv_attn_packed(q, qs, k, ks, v, vs, t, arr, n, n_heads, n_kv_heads, head_dim, causal,
+                                scale, o, os_, _stream(stream))
+
+
+def pkv_append_packed(seqs, n, layer, K, V):
+    """K, V: [rows, kv_dim] float32, bfloat16 or float16 CUDA tensors with contiguous rows (any
+    row stride), the batch's rows in order."""
+    arr = _i32_array(n)
+    k, ks, t = _rows(K, "K")
+    v, vs, tv = _rows(V, "V")
+    if t != tv or K.shape[1] != V.shape[1]:
+        raise TypeError("K and V must have one element type and width")
+    total = sum(arr[:len(n)])
+    _enough(K, total, "K")
+    _enough(V, total, "V")
+    return _lib.pkv_append_packed(_seq_array(seqs), len(seqs), arr, layer, k, ks, v, vs, t)
+
+
+def pkv_read_packed(seqs, start, n, layer, K, V):
+    """Rows start[r] .. start[r] + n[r] - 1 of each sequence into K, V (as for pkv_append_packed)."""
+    arr = _i32_array(n)
+    k, ks, t = _rows(K, "K")
+    v, vs, tv = _rows(V, "V")
+    if t != tv or K.shape[1] != V.shape[1]:
+        raise TypeError("K and V must have one element type and width")
+    total = sum(arr[:len(n)])
+    _enough(K, total, "K")
+    _enough(V, total, "V")
+    return _lib.pkv_read_packed(_seq_array(seqs), len(seqs), _i32_array(start), arr, layer, k, ks, v, vs, t)
 
 
 def pkv_sync_error(pool):

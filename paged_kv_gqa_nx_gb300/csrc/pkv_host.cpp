@@ -25,6 +25,7 @@
 #include <functional>
 #include <list>
 #include <mutex>
+#include <new>
 #include <string>
 #include <unordered_map>
 #include <vector>
@@ -249,6 +250,16 @@ struct DevGuard {
     }
 };
 
+// Bodies of entry points that allocate on the host: a C caller never sees an exception.
+template <class F>
+int guarded(F &&f) {
+    try {
+        return f();
+    } catch (const std::bad_alloc &) {
+        return fail(PKV_ERR_ARG, "out of host memory");
+    }
+}
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
@@ -324,6 +335,10 @@ struct pkv_pool {
     bool bf16 = false;  // storage element: f32, or bf16 (PKV_POOL_BF16)
     bool fp8 = false;   // or fp8 e4m3 of x / kv_scale (PKV_POOL_FP8)
     float kv_scale = 1.f;
+    bool q8 = false;    // or 8-bit with a scale per (block, layer, kv head) (pkv_pool_new_q8)
+    int32_t n_kv = 0, hd = 0;                 // 8-bit pools: kv heads and head width
+    float *k_scale = nullptr, *v_scale = nullptr;  // [n_blocks][n_layers][n_kv]
+    bool owns_scale = false;
     int32_t *pt_dev = nullptr;
     int32_t *err_dev = nullptr;
     cudaStream_t stream = nullptr;
@@ -341,12 +356,12 @@ struct pkv_pool {
     std::vector<pkv_seq *> dirty;      // sequences with page-table entries not yet uploaded
 
     Stager stager;
-    DevBuf desc, part, io_in, io_out, qrot, img;
+    DevBuf desc, part, io_in, io_out, qrot, krot, img;
     Blob blob;
 
     int64_t block_floats() const { return static_cast<int64_t>(n_layers) * bs * kv_dim; }  // elements
-    size_t elem_bytes() const { return fp8 ? 1 : bf16 ? 2 : 4; }
-    bool narrow() const { return bf16 || fp8; }  // a storage element other than f32
+    size_t elem_bytes() const { return fp8 || q8 ? 1 : bf16 ? 2 : 4; }
+    bool narrow() const { return bf16 || fp8 || q8; }  // a storage element other than f32
 };
 
 struct pkv_seq {
@@ -431,6 +446,29 @@ PagedAddr paged_addr(const pkv_pool *p, int32_t layer) {
     a.max_blocks = p->max_blocks;
     a.n_blocks = p->n_blocks;
     return a;
+}
+
+Q8Addr q8_addr(const pkv_pool *p, int32_t layer) {
+    Q8Addr q;
+    q.a = paged_addr(p, layer);
+    q.ks = p->k_scale + static_cast<int64_t>(layer) * p->n_kv;
+    q.vs = p->v_scale + static_cast<int64_t>(layer) * p->n_kv;
+    q.scale_stride = static_cast<int64_t>(p->n_layers) * p->n_kv;
+    q.n_kv = p->n_kv;
+    q.hd = p->hd;
+    return q;
+}
+
+// The pages that rows [pos, pos + n) of a sequence fall in, as items whose
+// packed rows start at row0.
+void put_page_items(const pkv_seq *s, int32_t pos, int32_t n, int32_t row0, std::vector<PageItem> &items) {
+    const int32_t bs = s->pool->bs, end = pos + n;
+    while (pos < end) {
+        const int32_t off = pos % bs, m = std::min(bs - off, end - pos);
+        items.push_back({s->pt[pos / bs], off, m, row0});
+        pos += m;
+        row0 += m;
+    }
 }
 
 // Rows [len, len+n) lie in existing blocks of refcount 1.
@@ -688,7 +726,7 @@ void place_pairs(const std::vector<std::array<PrefillTile, 2>> &pairs, const std
         }
 }
 
-// S: keys per split-K decode unit; prefill_split: keys per split of the
+// qblock: queries per decode unit (1 but on 8-bit pools); S: keys per split-K decode unit; prefill_split: keys per split of the
 // tensor-core prefill rows (0: kPrefillSplitFactor * S); prefix_split: keys
 // per split of the shared-prefix pass (0: S); allow_tc false: every row to the
 // split-K decode kernels; n_kv, n_sm: kv heads and the device's SMs, for the
@@ -696,7 +734,7 @@ void place_pairs(const std::vector<std::array<PrefillTile, 2>> &pairs, const std
 void build_work(std::vector<RowDesc> &rows, int causal, int32_t S, int32_t head_dim,
                 int32_t group, WorkList &w, const std::vector<Cascade> &cas = {},
                 int32_t prefix_split = 0, int32_t prefill_split = 0, bool allow_tc = true,
-                int32_t n_kv = 0, int32_t n_sm = 0) {
+                int32_t n_kv = 0, int32_t n_sm = 0, int32_t qblock = 1) {
     std::vector<UnitDesc> tail;
     w.units.clear();
     w.tiles.clear();
@@ -760,8 +798,10 @@ void build_work(std::vector<RowDesc> &rows, int causal, int32_t S, int32_t head_
             }
             continue;
         }
-        for (int32_t i = 0; i < rd.n_q; ++i) {
-            const int32_t q_pos = total_k - rd.n_q + i;
+        for (int32_t i = 0; i < rd.n_q; i += qblock) {
+            // a unit takes qblock consecutive queries; its last one sees the most keys
+            const int32_t nb = std::min(qblock, rd.n_q - i);
+            const int32_t q_pos = total_k - rd.n_q + i + nb - 1;
             const int32_t nk = causal ? q_pos + 1 : total_k;
             const int32_t ns = ceil_div(nk, S);
             if (ns == 1) {
@@ -769,8 +809,8 @@ void build_work(std::vector<RowDesc> &rows, int causal, int32_t S, int32_t head_
             } else {
                 const int32_t part0 = static_cast<int32_t>(w.n_part);
                 const int32_t item = static_cast<int32_t>(w.merges.size());
-                w.n_part += ns;
-                w.merges.push_back({r, i, part0, ns});
+                w.n_part += static_cast<int64_t>(ns) * nb;
+                for (int32_t t = 0; t < nb; ++t) w.merges.push_back({r, i + t, part0 + t * ns, ns});
                 for (int32_t s = 0; s + 1 < ns; ++s) w.units.push_back({r, i, s, item});
                 tail.push_back({r, i, ns - 1, item});
             }
@@ -855,6 +895,22 @@ const T *dptr(const pkv_pool *p, size_t off) {
     return reinterpret_cast<const T *>(static_cast<unsigned char *>(p->desc.p) + off);
 }
 
+// A call that uploads descriptors through the staging ring cannot be replayed:
+// a graph would read the ring's later contents.
+int refuse_capture(cudaStream_t s) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    const cudaError_t e = cudaStreamIsCapturing(s, &st);
+    if (e == cudaErrorStreamCaptureImplicit) {
+        cudaGetLastError();
+        st = cudaStreamCaptureStatusActive;
+    } else if (e != cudaSuccess) {
+        return cuda_fail(e, "capture status");
+    }
+    if (st != cudaStreamCaptureStatusNone)
+        return fail(PKV_ERR_ARG, "this call uploads its work list and cannot be captured into a graph");
+    return PKV_OK;
+}
+
 // Argument checks of a layer call, before it changes anything, in the order
 // of nx_f32_attn_with_paged: sizes, grouping, sequence.
 int validate_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *Q,
@@ -884,6 +940,8 @@ int validate_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const fl
                         n_kv_heads * head_dim, p->kv_dim);
         if (head_dim > kMaxHeadDim)
             return fail(PKV_ERR_BAD_DIM, "head_dim %d > %d is not supported", head_dim, kMaxHeadDim);
+        if (p->q8 && (n_kv_heads != p->n_kv || head_dim != p->hd))
+            return fail(PKV_ERR_BAD_DIM, "the pool's scales are laid out for %d kv heads of %d", p->n_kv, p->hd);
         if (p->fp8 && head_dim == 128 && (p->kv_dim % 16) != 0)
             return fail(PKV_ERR_BAD_DIM, "an fp8 pool with head_dim 128 needs kv_dim %% 16 == 0");
     }
@@ -925,14 +983,25 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
     pkv_pool *p = seqs[0]->pool;
     DevGuard dg(p->device);
     cudaStream_t st = p->stream;
+    if (p->q8) {
+        const int rc = refuse_capture(st);
+        if (rc) return rc;
+    }
     const int32_t q_dim = n_heads * head_dim;
     const int32_t kv_dim = p->kv_dim;
 
     std::vector<RowDesc> rows(M);
-    std::vector<AppendDesc> app;
+    std::vector<AppendDesc> app;    // per token, or
+    std::vector<PageItem> pages;    // per page on an 8-bit pool, whose append scales whole pages
     int64_t T = 0;
     for (int32_t r = 0; r < M; ++r) {
         rows[r] = {seqs[r]->slot, seqs[r]->len, n_q[r], static_cast<int32_t>(T)};
+        if (p->q8) {
+            if (T + n_q[r] > 0x7fffffffLL / std::max(q_dim, kv_dim)) return fail(PKV_ERR_BAD_DIM, "batch too large");
+            put_page_items(seqs[r], seqs[r]->len, n_q[r], static_cast<int32_t>(T), pages);
+            T += n_q[r];
+            continue;
+        }
         for (int32_t t = 0; t < n_q[r]; ++t) {
             const int32_t pos = seqs[r]->len + t;
             app.push_back({seqs[r]->slot, pos, static_cast<int32_t>(T + t), seqs[r]->pt[pos / p->bs]});
@@ -947,7 +1016,7 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
     // rows, 2 S of bf16, 4 S of fp8 (so a unit's fixed work -- the query
     // pieces, the 4-warp merge -- is amortised alike).  It depends on the
     // pool only, so a row's split boundaries are the same in any batch.
-    const int32_t S_dec = std::min<int32_t>(65536, S * (p->fp8 ? 4 : p->bf16 ? 2 : 1));
+    const int32_t S_dec = std::min<int32_t>(65536, S * (p->fp8 || p->q8 ? 4 : p->bf16 ? 2 : 1));
     const int32_t group = attend ? n_heads / n_kv_heads : 0;
     std::vector<Cascade> cas;
     if (attend && g_cascade.load() != 0 && prefill_shape(head_dim, group))
@@ -955,10 +1024,10 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
     const int32_t Sp = cas.empty() ? 0 : prefix_split_keys(cas, group, n_kv_heads, p->n_sm);
     if (attend)
         build_work(rows, causal, S_dec, head_dim, group, w, cas, Sp, S * kPrefillSplitFactor, true, n_kv_heads,
-                   p->n_sm);
+                   p->n_sm, p->q8 ? q8_query_block(head_dim, group) : 1);
     // the decode kernels that take the append themselves: the f32 kernel for
     // groups 1, 2, 4 and the narrow-pool kernel for its shapes (head_dim 128)
-    const bool fuse_shape = head_dim == 128 &&
+    const bool fuse_shape = head_dim == 128 && !p->q8 &&
                             (p->narrow() ? decode_mma_shape(head_dim, group, p->bf16, p->fp8)
                                          : (group == 1 || group == 2 || group == 4));
     const bool fuse = attend && rope_base == 0.0 && g_fused_append.load() != 0 && w.tiles.empty() &&
@@ -985,6 +1054,7 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
 
     // the pages this call writes get new generations
     for (const AppendDesc &ad : app) bump_gen(p, ad.blk, layer);
+    for (const PageItem &it : pages) bump_gen(p, it.blk, layer);
 
     // operand images for the tensor-core launches: every 64-key tile of each
     // row with prefill tiles (real rows and shared-prefix virtual rows).  Tile
@@ -1066,6 +1136,7 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
     const size_t tile0_off = blob.put(img_tile0.data(), img_tile0.size());
     const size_t slot_off = blob.put(img_slot.data(), img_slot.size());
     const size_t split_off = blob.put(split_items.data(), split_items.size());
+    const size_t pages_off = blob.put(pages.data(), pages.size());
 
     cudaError_t e = upload_blob(p);
     if (e != cudaSuccess) return cuda_fail(e, "descriptor upload");
@@ -1112,7 +1183,21 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
         pr.hd = head_dim;
         Qd = pr.Q_rot;  // the attention kernels read the rotated queries
     }
-    if (!fuse) {
+    if (p->q8) {
+        if (pr.rope_base > 0.0) {
+            e = p->krot.ensure(static_cast<size_t>(T) * kv_dim * sizeof(float), st, p->device);
+            if (e != cudaSuccess) return cuda_fail(e, "rotated-key buffer");
+            const RopeArgs ra{pr.Q, Kd, pr.Q_rot, static_cast<float *>(p->krot.p), dptr<RowDesc>(p, rows_off), M,
+                              static_cast<int32_t>(T), q_dim, kv_dim, head_dim, rope_base};
+            e = launch(PKV_KERNEL_APPEND, st, [&] { return launch_rope_rows(ra, st); });
+            if (e != cudaSuccess) return cuda_fail(e, "rotation kernel");
+            Kd = ra.K_rot;
+        }
+        PagesArgs ap{dptr<PageItem>(p, pages_off), static_cast<int32_t>(pages.size()), const_cast<float *>(Kd),
+                     const_cast<float *>(Vd), kv_dim, kv_dim, Elem::f32, pr.runs, pr.vals, n_runs, p->err_dev};
+        e = launch(PKV_KERNEL_APPEND, st, [&] { return launch_append_pages_q8(ap, q8_addr(p, layer), st); });
+        if (e != cudaSuccess) return cuda_fail(e, "append kernel");
+    } else if (!fuse) {
         e = launch(PKV_KERNEL_APPEND, st, [&] { return launch_prep(pr, addr, st); });
         if (e != cudaSuccess) return cuda_fail(e, "prep kernel");
     }
@@ -1160,7 +1245,9 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
     if (!split_items.empty()) {
         const SplitArgs sa{a.rows, dptr<SplitItem>(p, split_off), static_cast<int32_t>(split_items.size()),
                            n_kv_heads, img, p->err_dev};
-        e = launch(PKV_KERNEL_SPLIT, st, [&] { return launch_split_paged(sa, addr, st); });
+        e = launch(PKV_KERNEL_SPLIT, st, [&] {
+            return p->q8 ? launch_split_q8(sa, q8_addr(p, layer), st) : launch_split_paged(sa, addr, st);
+        });
         if (e != cudaSuccess) {
             if (cached) p->icache.reset(p->icache.n_slots);  // the missed images were not made
             return cuda_fail(e, "split kernel");
@@ -1191,7 +1278,9 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
         if (e != cudaSuccess) return cuda_fail(e, "shared-prefix kernel");
     }
     if (!w.units.empty()) {
-        e = launch(PKV_KERNEL_DECODE, st, [&] { return launch_decode_paged(a, addr, st); });
+        e = launch(PKV_KERNEL_DECODE, st, [&] {
+            return p->q8 ? launch_decode_q8(a, q8_addr(p, layer), st) : launch_decode_paged(a, addr, st);
+        });
         if (e != cudaSuccess) return cuda_fail(e, "decode kernel");
     }
     if (!w.merges.empty()) {
@@ -1340,9 +1429,19 @@ extern "C" {
 
 const char *pkv_last_error(void) { return g_last_error.c_str(); }
 
-pkv_pool *pkv_pool_new(int32_t n_blocks, int32_t n_layers, int32_t kv_dim, int32_t block_size,
-                       void *k_pool_dev, void *v_pool_dev, int32_t max_seqs,
-                       int32_t max_blocks_per_seq, pkv_stream_t stream, uint32_t flags) {
+}  // extern "C"
+
+namespace {
+
+// Head layout and scale storage of an 8-bit pool.
+struct Q8Spec {
+    int32_t n_kv, hd;
+    float *k_scale, *v_scale;
+};
+
+pkv_pool *make_pool(int32_t n_blocks, int32_t n_layers, int32_t kv_dim, int32_t block_size,
+                    void *k_pool_dev, void *v_pool_dev, int32_t max_seqs,
+                    int32_t max_blocks_per_seq, pkv_stream_t stream, uint32_t flags, const Q8Spec *q8) {
     if (n_blocks <= 0 || n_layers <= 0 || kv_dim <= 0 || block_size <= 0 || max_seqs <= 0 ||
         max_blocks_per_seq <= 0) {
         fail(PKV_ERR_BAD_DIM, "pool sizes must be positive");
@@ -1377,6 +1476,11 @@ pkv_pool *pkv_pool_new(int32_t n_blocks, int32_t n_layers, int32_t kv_dim, int32
         fail(PKV_ERR_BAD_DIM, "an fp8 pool needs kv_dim to be a multiple of 4");
         delete p;
         return nullptr;
+    }
+    if (q8) {
+        p->q8 = true;
+        p->n_kv = q8->n_kv;
+        p->hd = q8->hd;
     }
     p->free_stack.resize(n_blocks);
     for (int32_t i = 0; i < n_blocks; ++i) p->free_stack[i] = n_blocks - 1 - i;
@@ -1419,6 +1523,23 @@ pkv_pool *pkv_pool_new(int32_t n_blocks, int32_t n_layers, int32_t kv_dim, int32
         }
         p->owns_kv = true;
     }
+    if (q8) {
+        p->k_scale = q8->k_scale;
+        p->v_scale = q8->v_scale;
+        if (!p->k_scale) {
+            const size_t n = static_cast<size_t>(n_blocks) * n_layers * p->n_kv * sizeof(float);
+            p->owns_scale = true;
+            e = cudaMalloc(&p->k_scale, n);
+            if (e == cudaSuccess) e = cudaMalloc(&p->v_scale, n);
+            if (e == cudaSuccess) e = cudaMemsetAsync(p->k_scale, 0, n, p->stream);
+            if (e == cudaSuccess) e = cudaMemsetAsync(p->v_scale, 0, n, p->stream);
+            if (e != cudaSuccess) {
+                cuda_fail(e, "scale allocation");
+                pkv_pool_free(p);
+                return nullptr;
+            }
+        }
+    }
     e = cudaMalloc(&p->pt_dev, static_cast<size_t>(max_seqs) * max_blocks_per_seq * sizeof(int32_t));
     if (e == cudaSuccess) e = cudaMalloc(&p->err_dev, sizeof(int32_t));
     if (e == cudaSuccess)
@@ -1433,6 +1554,48 @@ pkv_pool *pkv_pool_new(int32_t n_blocks, int32_t n_layers, int32_t kv_dim, int32
     return p;
 }
 
+}  // namespace
+
+extern "C" {
+
+pkv_pool *pkv_pool_new(int32_t n_blocks, int32_t n_layers, int32_t kv_dim, int32_t block_size,
+                       void *k_pool_dev, void *v_pool_dev, int32_t max_seqs,
+                       int32_t max_blocks_per_seq, pkv_stream_t stream, uint32_t flags) {
+    return make_pool(n_blocks, n_layers, kv_dim, block_size, k_pool_dev, v_pool_dev, max_seqs, max_blocks_per_seq,
+                     stream, flags, nullptr);
+}
+
+pkv_pool *pkv_pool_new_q8(int32_t n_blocks, int32_t n_layers, int32_t n_kv_heads, int32_t head_dim,
+                          int32_t block_size, void *k_pool_dev, void *v_pool_dev, float *k_scale_dev,
+                          float *v_scale_dev, int32_t max_seqs, int32_t max_blocks_per_seq,
+                          pkv_stream_t stream, uint32_t flags) {
+    pkv_pool *p = nullptr;
+    guarded([&] {
+        if (n_kv_heads <= 0 || head_dim <= 0) return fail(PKV_ERR_BAD_DIM, "n_kv_heads and head_dim must be positive");
+        if (head_dim > kMaxHeadDim)
+            return fail(PKV_ERR_BAD_DIM, "head_dim %d > %d is not supported", head_dim, kMaxHeadDim);
+        const int64_t kv_dim = static_cast<int64_t>(n_kv_heads) * head_dim;
+        if (kv_dim > 0x7fffffff || kv_dim % 4 != 0)
+            return fail(PKV_ERR_BAD_DIM, "an 8-bit pool needs n_kv_heads * head_dim to be a multiple of 4");
+        if ((flags & ~PKV_POOL_HOST_ONLY) != 0)
+            return fail(PKV_ERR_ARG, "an 8-bit pool takes no flag but PKV_POOL_HOST_ONLY");
+        if (!(flags & PKV_POOL_HOST_ONLY)) {
+            const int n = (k_pool_dev ? 1 : 0) + (v_pool_dev ? 1 : 0) + (k_scale_dev ? 1 : 0) + (v_scale_dev ? 1 : 0);
+            if (n != 0 && n != 4) return fail(PKV_ERR_ARG, "pass both pool buffers and both scale buffers, or none");
+            if (!aligned4(k_scale_dev) || !aligned4(v_scale_dev))
+                return fail(PKV_ERR_ARG, "scale buffers must be 4-byte aligned");
+        }
+        const Q8Spec spec{n_kv_heads, head_dim, k_scale_dev, v_scale_dev};
+        p = make_pool(n_blocks, n_layers, static_cast<int32_t>(kv_dim), block_size, k_pool_dev, v_pool_dev, max_seqs,
+                      max_blocks_per_seq, stream, flags, &spec);
+        return 0;
+    });
+    return p;
+}
+
+float *pkv_pool_k_scales(const pkv_pool *p) { return p ? p->k_scale : nullptr; }
+float *pkv_pool_v_scales(const pkv_pool *p) { return p ? p->v_scale : nullptr; }
+
 void pkv_pool_free(pkv_pool *p) {
     if (!p) return;
     for (pkv_seq *s : p->slot_owner) delete s;
@@ -1444,6 +1607,7 @@ void pkv_pool_free(pkv_pool *p) {
         p->io_in.release(p->stream);
         p->io_out.release(p->stream);
         p->qrot.release(p->stream);
+        p->krot.release(p->stream);
         p->img.release(p->stream);
         p->icache.buf.release(p->stream);
         cudaStreamSynchronize(p->stream);
@@ -1452,6 +1616,10 @@ void pkv_pool_free(pkv_pool *p) {
         if (p->owns_kv) {
             cudaFree(p->k);
             cudaFree(p->v);
+        }
+        if (p->owns_scale) {
+            cudaFree(p->k_scale);
+            cudaFree(p->v_scale);
         }
         cudaFree(p->pt_dev);
         cudaFree(p->err_dev);
@@ -1711,6 +1879,12 @@ int pkv_ensure_append_batch(pkv_seq *const *seqs, int32_t M, const int32_t *n) {
                                   p->block_floats() * static_cast<int64_t>(p->elem_bytes()) / 4,
                                   p->n_blocks, p->err_dev, p->stream);
     });
+    if (e == cudaSuccess && p->q8)
+        e = launch(PKV_KERNEL_COPY, p->stream, [&] {  // the blocks' scales
+            return launch_copy_blocks(p->k_scale, p->v_scale, dptr<CopyDesc>(p, off),
+                                      static_cast<int32_t>(copies.size()),
+                                      static_cast<int64_t>(p->n_layers) * p->n_kv, p->n_blocks, p->err_dev, p->stream);
+        });
     if (e != cudaSuccess) return cuda_fail(e, "copy-on-append kernel");
     return PKV_OK;
 }
@@ -1891,6 +2065,211 @@ int pkv_attn_contiguous(const float *Q, const float *Kc, const float *Vc, int32_
     cudaFreeAsync(mem, st);
     if (e != cudaSuccess) return cuda_fail(e, "contiguous attention kernels");
     return PKV_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+bool type_of(int32_t dtype, Elem *t, int32_t *bytes) {
+    if (dtype == PKV_F32) *t = Elem::f32, *bytes = 4;
+    else if (dtype == PKV_BF16) *t = Elem::bf16, *bytes = 2;
+    else if (dtype == PKV_F16) *t = Elem::f16, *bytes = 2;
+    else return false;
+    return true;
+}
+
+// Shared body of pkv_append_packed (start NULL: rows go to positions len ..)
+// and pkv_read_packed.
+int run_pages(pkv_seq *const *seqs, int32_t M, const int32_t *start, const int32_t *n, int32_t layer, void *K,
+              int64_t k_stride, void *V, int64_t v_stride, int32_t dtype, bool append) {
+    if (M <= 0 || !n || (!append && !start)) return fail(PKV_ERR_BAD_DIM, "M must be positive and the counts non-NULL");
+    for (int32_t r = 0; r < M; ++r)
+        if (n[r] <= 0) return fail(PKV_ERR_BAD_DIM, "n[%d] = %d must be positive", r, n[r]);
+    if (!seqs) return fail(PKV_ERR_SEQ, "seqs is NULL");
+    for (int32_t r = 0; r < M; ++r)
+        if (!seqs[r] || !seqs[r]->pool) return fail(PKV_ERR_SEQ, "sequence %d is NULL", r);
+    pkv_pool *p = seqs[0]->pool;
+    for (int32_t r = 1; r < M; ++r)
+        if (seqs[r]->pool != p) return fail(PKV_ERR_ARG, "sequences of different pools in one batch");
+    if (p->host_only) return fail(PKV_ERR_ARG, "host-only pool has no device storage");
+    if (layer < 0 || layer >= p->n_layers) return fail(PKV_ERR_ARG, "layer %d outside [0, %d)", layer, p->n_layers);
+    Elem type;
+    int32_t bytes;
+    if (!type_of(dtype, &type, &bytes)) return fail(PKV_ERR_ARG, "unknown element type %d", dtype);
+    if (!K || !V) return fail(PKV_ERR_ARG, "NULL data pointer");
+    auto at = [&](const void *q) { return reinterpret_cast<uintptr_t>(q) % static_cast<uintptr_t>(bytes) == 0; };
+    if (!at(K) || !at(V)) return fail(PKV_ERR_ARG, "rows must be aligned to their element");
+    if (k_stride < p->kv_dim || v_stride < p->kv_dim)
+        return fail(PKV_ERR_ARG, "a row stride below the pool's kv_dim %d makes rows overlap", p->kv_dim);
+    int64_t T = 0;
+    for (int32_t r = 0; r < M; ++r) T += n[r];
+    if (T > 0x7fffffffLL || std::max(k_stride, v_stride) > (1LL << 40))
+        return fail(PKV_ERR_BAD_DIM, "batch too large");
+    if (append) {
+        const int rc = check_dup(p, seqs, M);
+        if (rc) return rc;
+        for (int32_t r = 0; r < M; ++r)
+            if (!can_append(seqs[r], n[r]))
+                return fail(PKV_ERR_SEQ, "rows [%d, %lld) of batch row %d are not ensured (call pkv_ensure_append)",
+                            seqs[r]->len, static_cast<long long>(seqs[r]->len) + n[r], r);
+    } else {
+        for (int32_t r = 0; r < M; ++r)
+            if (start[r] < 0 ||
+                static_cast<int64_t>(start[r]) + n[r] > static_cast<int64_t>(seqs[r]->pt.size()) * p->bs)
+                return fail(PKV_ERR_SEQ, "rows [%d, %lld) of batch row %d are not in the sequence's pages", start[r],
+                            static_cast<long long>(start[r]) + n[r], r);
+    }
+    DevGuard dg(p->device);
+    cudaStream_t st = p->stream;
+    {
+        const int rc = refuse_capture(st);
+        if (rc) return rc;
+    }
+    std::vector<PageItem> items;
+    items.reserve(static_cast<size_t>(T / p->bs) + 2 * static_cast<size_t>(M));
+    int32_t row0 = 0;
+    for (int32_t r = 0; r < M; ++r) {
+        put_page_items(seqs[r], append ? seqs[r]->len : start[r], n[r], row0, items);
+        row0 += n[r];
+    }
+    if (static_cast<int64_t>(items.size()) * std::max(1, p->q8 ? p->n_kv : ceil_div(p->kv_dim, 128)) > 0x3fffffffLL)
+        return fail(PKV_ERR_BAD_DIM, "batch too large");
+    Blob &blob = p->blob;
+    blob.clear();
+    PagesArgs a{};
+    size_t runs_off = 0, vals_off = 0;
+    if (append) {
+        for (const PageItem &it : items) bump_gen(p, it.blk, layer);
+        put_pt_runs(p, blob, &runs_off, &a.n_runs, &vals_off);
+    }
+    const size_t items_off = blob.put(items.data(), items.size());
+    cudaError_t e = upload_blob(p);
+    if (e != cudaSuccess) return cuda_fail(e, "descriptor upload");
+    a.items = dptr<PageItem>(p, items_off);
+    a.n_items = static_cast<int32_t>(items.size());
+    a.K = K;
+    a.V = V;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.type = type;
+    a.runs = dptr<PtRun>(p, runs_off);
+    a.vals = dptr<int32_t>(p, vals_off);
+    a.err = p->err_dev;
+    e = launch(append ? PKV_KERNEL_APPEND : PKV_KERNEL_COPY, st, [&] {
+        if (p->q8)
+            return append ? launch_append_pages_q8(a, q8_addr(p, layer), st)
+                          : launch_read_pages_q8(a, q8_addr(p, layer), st);
+        return append ? launch_append_pages(a, paged_addr(p, layer), st)
+                      : launch_read_pages(a, paged_addr(p, layer), st);
+    });
+    if (e != cudaSuccess) return cuda_fail(e, append ? "packed append kernel" : "packed read kernel");
+    return PKV_OK;
+}
+
+int run_packed(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, const void *V, int64_t v_stride,
+               int32_t dtype, const int32_t *lens, int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads,
+               int32_t head_dim, int32_t causal, float scale, void *out, int64_t out_stride, cudaStream_t st) {
+    if (n_seqs <= 0 || !lens) return fail(PKV_ERR_BAD_DIM, "n_seqs must be positive and lens non-NULL");
+    for (int32_t s = 0; s < n_seqs; ++s)
+        if (lens[s] < 0) return fail(PKV_ERR_BAD_DIM, "lens[%d] = %d must not be negative", s, lens[s]);
+    int rc = check_heads(n_heads, n_kv_heads, head_dim);
+    if (rc) return rc;
+    if (head_dim > kMaxHeadDim)
+        return fail(PKV_ERR_BAD_DIM, "head_dim %d > %d is not supported", head_dim, kMaxHeadDim);
+    const int64_t q_dim = static_cast<int64_t>(n_heads) * head_dim, kv_dim = static_cast<int64_t>(n_kv_heads) * head_dim;
+    if (q_dim > 0x7fffffffLL) return fail(PKV_ERR_BAD_DIM, "n_heads * head_dim too large");
+    if (dtype != PKV_BF16 && dtype != PKV_F16)
+        return fail(PKV_ERR_ARG, "packed attention takes PKV_BF16 or PKV_F16 rows (f32: pkv_attn_contiguous)");
+    int64_t T = 0;
+    for (int32_t s = 0; s < n_seqs; ++s) T += lens[s];
+    if (T > 0x7fffff00LL) return fail(PKV_ERR_BAD_DIM, "%lld tokens are too many", static_cast<long long>(T));
+    if (q_stride < q_dim || out_stride < q_dim || k_stride < kv_dim || v_stride < kv_dim)
+        return fail(PKV_ERR_ARG, "a row stride below the row's width makes rows overlap");
+    if (std::max(std::max(q_stride, out_stride), std::max(k_stride, v_stride)) > (1LL << 38))
+        return fail(PKV_ERR_BAD_DIM, "row stride too large");
+    if (T == 0) return PKV_OK;
+    if (!Q || !K || !V || !out) return fail(PKV_ERR_ARG, "NULL data pointer");
+    for (const void *q : {Q, K, V, static_cast<const void *>(out)})
+        if (reinterpret_cast<uintptr_t>(q) % 2 != 0) return fail(PKV_ERR_ARG, "rows must be aligned to their element");
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (dev < 0 || dev >= 64) return fail(PKV_ERR_ARG, "device index out of range");
+    int32_t *err_word = nullptr;
+    {
+        std::lock_guard<std::mutex> lk(g_contig_mu);
+        if (!g_contig_err[dev]) {
+            rc = refuse_capture(st);  // the word's set-up allocates; a later call captures
+            if (rc) return rc;
+        }
+        e = contig_error_word(dev, &err_word);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "error word");
+
+    // sequences with tokens, longest first (the grid then ends on its shortest)
+    std::vector<int32_t> order, start(n_seqs), len_s, start_s;
+    int32_t at = 0;
+    for (int32_t s = 0; s < n_seqs; ++s) {
+        start[s] = at;
+        at += lens[s];
+        if (lens[s] > 0) order.push_back(s);
+    }
+    std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return lens[x] > lens[y]; });
+    for (int32_t s : order) {
+        start_s.push_back(start[s]);
+        len_s.push_back(lens[s]);
+    }
+    PackedArgs a{};
+    a.Q = Q;
+    a.K = K;
+    a.V = V;
+    a.out = out;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.o_stride = out_stride;
+    a.n_heads = n_heads;
+    a.n_kv = n_kv_heads;
+    a.hd = head_dim;
+    a.causal = causal ? 1 : 0;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.n_tokens = T;
+    a.type = dtype == PKV_BF16 ? Elem::bf16 : Elem::f16;
+    a.err = err_word;
+    for (size_t i = 0; i < order.size(); i += kPackedSeqs) {
+        const int32_t m = static_cast<int32_t>(std::min<size_t>(kPackedSeqs, order.size() - i));
+        e = launch(PKV_KERNEL_PREFILL, st, [&] { return launch_packed(a, &start_s[i], &len_s[i], m, st); });
+        if (e != cudaSuccess) return cuda_fail(e, "packed attention kernel");
+    }
+    return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pkv_append_packed(pkv_seq *const *seqs, int32_t M, const int32_t *n, int32_t layer, const void *K,
+                      int64_t k_stride, const void *V, int64_t v_stride, int32_t dtype) {
+    return guarded([&] {
+        return run_pages(seqs, M, nullptr, n, layer, const_cast<void *>(K), k_stride, const_cast<void *>(V), v_stride,
+                         dtype, true);
+    });
+}
+
+int pkv_read_packed(pkv_seq *const *seqs, int32_t M, const int32_t *start, const int32_t *n, int32_t layer, void *K,
+                    int64_t k_stride, void *V, int64_t v_stride, int32_t dtype) {
+    return guarded([&] { return run_pages(seqs, M, start, n, layer, K, k_stride, V, v_stride, dtype, false); });
+}
+
+int pkv_attn_packed(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, const void *V,
+                    int64_t v_stride, int32_t dtype, const int32_t *lens, int32_t n_seqs, int32_t n_heads,
+                    int32_t n_kv_heads, int32_t head_dim, int32_t causal, float scale, void *out,
+                    int64_t out_stride, pkv_stream_t stream) {
+    return guarded([&] {
+        return run_packed(Q, q_stride, K, k_stride, V, v_stride, dtype, lens, n_seqs, n_heads, n_kv_heads, head_dim,
+                          causal, scale, out, out_stride, static_cast<cudaStream_t>(stream));
+    });
 }
 
 int pkv_sync_error(pkv_pool *p) {

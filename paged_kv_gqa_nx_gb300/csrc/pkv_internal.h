@@ -66,6 +66,71 @@ struct PagedAddr {
     float kv_scale = 1.f;  // power of two; 1 unless fp8
 };
 
+// An 8-bit pool with block scales: the element u (1 .. 255) of a row of kv head
+// h in block b stands for (u - 128) * s, s the scale of (b, layer, h), a power
+// of two (NaN: the block took a value that is not finite).
+struct Q8Addr {
+    PagedAddr a;               // k, v: one byte per element
+    float *ks, *vs;            // scales of the layer's first head: block b, head h at b * scale_stride + h
+    int64_t scale_stride;      // floats per block: n_layers * n_kv
+    int32_t n_kv, hd;
+};
+
+// The rows of one page that a packed append writes, or a packed read returns:
+// offsets off .. off + n - 1 of block blk <-> packed rows row0 ..
+struct PageItem {
+    int32_t blk, off, n, row0;
+};
+
+// Element types of packed rows (pkv_dtype) and of pool storage.
+enum class Elem : int32_t { f32 = 0, bf16 = 1, f16 = 2, fp8 = 3, q8 = 4 };
+
+// Packed rows <-> pages.  Append: also uploads n_runs page-table runs (as the
+// prep launch does).  Row r of K starts k_stride elements after row r - 1.
+struct PagesArgs {
+    const PageItem *items;
+    int32_t n_items;
+    void *K, *V;               // packed rows (the read writes them, the append reads them)
+    int64_t k_stride, v_stride;
+    Elem type;                 // of the packed rows
+    const PtRun *runs = nullptr;
+    const int32_t *vals = nullptr;
+    int32_t n_runs = 0;
+    int32_t *err = nullptr;
+};
+
+// Rotated copies of the new rows (RoPE on append over an 8-bit pool, whose
+// append needs the rotated keys of a whole block before it can scale them).
+struct RopeArgs {
+    const float *Q, *K;
+    float *Q_rot, *K_rot;
+    const RowDesc *rows;       // past_len, n_q, q_row0
+    int32_t n_rows, n_tok, q_dim, kv_dim, hd;
+    double base;
+};
+
+// Packed prompt attention: sequence s holds tokens start[s] .. start[s + 1) of
+// the packed rows.  The list travels in the launch's parameters (no upload, no
+// scratch), so a launch takes at most kPackedSeqs sequences.
+constexpr int32_t kPackedSeqs = 2000;
+template <int N>
+struct PackedSeqs {
+    int32_t n;
+    int32_t start[N];          // first token
+    int32_t len[N];            // tokens (> 0), longest sequence first
+    int32_t tile0[N + 1];      // query tiles of the sequences before s
+};
+struct PackedArgs {
+    const void *Q, *K, *V;
+    void *out;
+    int64_t q_stride, k_stride, v_stride, o_stride;  // elements per token
+    int32_t n_heads, n_kv, hd, causal;
+    float scale_log2;
+    int64_t n_tokens;          // rows of Q, K, V and out that belong to some sequence (from row 0)
+    Elem type;
+    int32_t *err;
+};
+
 // Address of a key/value row in a contiguous history: base[pos][kv_head*hd ...]
 struct ContigAddr {
     const float *k, *v;
@@ -230,6 +295,23 @@ cudaError_t launch_prefill_contig(const PrefillArgs &a, const ContigAddr &addr, 
 // from the pool's rows or from a contiguous K/V pair.
 cudaError_t launch_split_paged(const SplitArgs &a, const PagedAddr &addr, cudaStream_t s);
 cudaError_t launch_split_contig(const SplitArgs &a, const ContigAddr &addr, cudaStream_t s);
+
+// Packed rows into and out of the pages (pkv_pages.cu).
+cudaError_t launch_append_pages(const PagesArgs &a, const PagedAddr &addr, cudaStream_t s);
+cudaError_t launch_append_pages_q8(const PagesArgs &a, const Q8Addr &addr, cudaStream_t s);
+cudaError_t launch_read_pages(const PagesArgs &a, const PagedAddr &addr, cudaStream_t s);
+cudaError_t launch_read_pages_q8(const PagesArgs &a, const Q8Addr &addr, cudaStream_t s);
+cudaError_t launch_rope_rows(const RopeArgs &a, cudaStream_t s);
+// Attention over an 8-bit pool with block scales (pkv_q8.cu): split-K decode
+// units of up to q8_query_block consecutive queries each (the unit's query qi
+// is its first; the queries of a unit with several splits have consecutive
+// merge items), and the split pass of the tensor-core launches.
+cudaError_t launch_decode_q8(const AttnArgs &a, const Q8Addr &addr, cudaStream_t s);
+cudaError_t launch_split_q8(const SplitArgs &a, const Q8Addr &addr, cudaStream_t s);
+int q8_query_block(int head_dim, int group);
+// Packed prompt attention (pkv_packed.cu); sequences sorted longest first.
+cudaError_t launch_packed(const PackedArgs &a, const int32_t *start, const int32_t *len, int32_t n_seqs,
+                          cudaStream_t s);
 
 // Rows with at least this many queries take the tensor-core prefill kernel
 // (when head_dim is 128 and the group is 1, 2, 4 or 8); its key split is

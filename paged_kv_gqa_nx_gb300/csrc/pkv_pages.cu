@@ -1,0 +1,473 @@
+// pkv_pages.cu -- packed rows into and out of the pages of a pool.
+//
+//   append_pages   K / V rows (f32, bf16 or f16, packed with a row stride) into
+//                  the pages of their sequences, converted to the pool's
+//                  element; on an 8-bit pool with block scales also the scales
+//   read_pages     the reverse: rows as the values they stand for
+//   rope_rows      rotated copies of new Q and K rows (RoPE on append over an
+//                  8-bit pool)
+//
+// One warp per (page item, group of columns, K or V); a group is one kv head
+// on an 8-bit pool and kColGroup columns elsewhere.  Both directions are pure
+// copies with a conversion, bound by HBM: every element is read and written
+// once, in 16-byte accesses of the packed side where its alignment allows.
+//
+// Quantisation (8-bit pool).  With m the largest magnitude of the page's new
+// rows of a head, need(m) is the least e >= -126 with m <= 127 * 2^e; a page
+// whose rows start here (offset 0) takes e = need(m), any other page the
+// larger of need(m) and its present exponent, and rows it already holds are
+// rounded to the new step.  Steps are powers of two, so every stored value is
+// exact in f32 and a growth of the step by 2^k moves a kept element by at most
+// half the new step; as steps at least double, those halves add up to less
+// than one step however often the page grows.
+#include "pkv_elem.h"
+#include "pkv_internal.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kColGroup = 128;
+
+using f16 = __half;
+
+// eight consecutive packed elements as f32 (16-byte aligned)
+__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const bf16 *p, float (&x)[8]) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void load8(const f16 *p, float (&x)[8]) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+__device__ __forceinline__ float load1(const float *p) { return __ldg(p); }
+__device__ __forceinline__ float load1(const bf16 *p) { return to_f32(*p); }
+__device__ __forceinline__ float load1(const f16 *p) { return __half2float(*p); }
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// eight consecutive elements, rounded once to nearest even
+__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(bf16 *p, const float (&x)[8]) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                                               pack_bf16(x[6], x[7]));
+}
+__device__ __forceinline__ void store8(f16 *p, const float (&x)[8]) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]), pack_f16(x[4], x[5]),
+                                               pack_f16(x[6], x[7]));
+}
+__device__ __forceinline__ void store8(fp8 *p, const float (&x)[8]) {
+    store4(p, make_float4(x[0], x[1], x[2], x[3]));
+    store4(p + 4, make_float4(x[4], x[5], x[6], x[7]));
+}
+__device__ __forceinline__ void put1(float *p, float x) { *p = x; }
+__device__ __forceinline__ void put1(bf16 *p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void put1(f16 *p, float x) { *p = __float2half_rn(x); }
+__device__ __forceinline__ void put1(fp8 *p, float x) { store1(p, x); }
+
+// eight pool elements as f32
+__device__ __forceinline__ void pool8(const float *p, float (&x)[8]) { load8(p, x); }
+__device__ __forceinline__ void pool8(const bf16 *p, float (&x)[8]) { load8(p, x); }
+__device__ __forceinline__ void pool8(const fp8 *p, float (&x)[8]) {
+    const float4 a = ldg4(p), b = ldg4(p + 4);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ float pool1(const float *p) { return ldg1(p); }
+__device__ __forceinline__ float pool1(const bf16 *p) { return ldg1(p); }
+__device__ __forceinline__ float pool1(const fp8 *p) { return ldg1(p); }
+
+__device__ __forceinline__ float pow2f(int e) {  // 2^e, e in [-126, 127]
+    return __int_as_float((e + 127) << 23);
+}
+
+// ---------------------------------------------------------- quantisation ----
+
+// The least e >= -126 with m <= 127 * 2^e, from the bits of a finite m >= 0:
+// m = 1.f * 2^k and 127 * 2^e = 1.984375 * 2^(e+6), so e = k - 6, or k - 5
+// where 1.f > 1.984375 (fraction bits above 0x7e0000).
+__device__ __forceinline__ int need_exp(uint32_t m_bits) {
+    const int k = static_cast<int>(m_bits >> 23) - 127;
+    return max(-126, k - 6 + ((m_bits & 0x7fffffu) > 0x7e0000u ? 1 : 0));
+}
+constexpr uint32_t kInfBits = 0x7f800000u;
+// The exponent of a stored scale (a power of two; 0 reads as the least one).
+__device__ __forceinline__ int scale_exp(float s) {
+    return max(-126, static_cast<int>((__float_as_uint(s) >> 23) & 255u) - 127);
+}
+// the element of the value x at step 1 / inv: |x * inv| <= 127, the product exact
+__device__ __forceinline__ uint32_t q8_elem(float x, float inv) {
+    return static_cast<uint32_t>(__float2int_rn(x * inv) + 128) & 255u;
+}
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// ----------------------------------------------------------------- append ----
+
+struct RowSpan {  // what one warp works on
+    PageItem it;
+    int32_t c0, cw;  // columns c0 .. c0 + cw - 1
+    bool is_v, ok;
+};
+
+__device__ __forceinline__ RowSpan row_span(const PagesArgs &p, const PagedAddr &a, int group, int n_groups, int w) {
+    RowSpan r;
+    const int per_item = 2 * n_groups;
+    r.it = p.items[w / per_item];
+    int x = w % per_item;
+    r.is_v = x >= n_groups;
+    x -= r.is_v ? n_groups : 0;
+    r.c0 = x * group;
+    r.cw = min(group, a.kv_dim - r.c0);
+    r.ok = static_cast<unsigned>(r.it.blk) < static_cast<unsigned>(a.n_blocks) && r.it.off >= 0 && r.it.n > 0 &&
+           r.it.off + r.it.n <= a.bs;
+    return r;
+}
+
+__device__ __forceinline__ bool upload_runs(const PagesArgs &p, const PagedAddr &a) {
+    if (static_cast<int>(blockIdx.x) >= p.n_runs) return false;
+    const PtRun r = p.runs[blockIdx.x];
+    int32_t *dst = a.pt + static_cast<size_t>(r.slot) * a.max_blocks + r.start;
+    for (int i = threadIdx.x; i < r.count; i += blockDim.x) dst[i] = p.vals[r.voff + i];
+    return true;
+}
+
+template <class S, class E, bool kVec>
+__global__ void __launch_bounds__(256) append_pages_kernel(PagesArgs p, PagedAddr a, int n_groups) {
+    if (upload_runs(p, a)) return;
+    const int w = (static_cast<int>(blockIdx.x) - p.n_runs) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (w >= p.n_items * 2 * n_groups) return;
+    const RowSpan r = row_span(p, a, kColGroup, n_groups, w);
+    if (!r.ok) {
+        if (lane == 0 && p.err) atomicOr(p.err, 1);
+        return;
+    }
+    const int64_t stride = r.is_v ? p.v_stride : p.k_stride;
+    const S *src = static_cast<const S *>(r.is_v ? p.V : p.K) + static_cast<int64_t>(r.it.row0) * stride + r.c0;
+    E *dst = static_cast<E *>(r.is_v ? a.v : a.k) + static_cast<size_t>(r.it.blk) * a.block_stride + a.layer_off +
+             static_cast<size_t>(r.it.off) * a.kv_dim + r.c0;
+    const float inv = 1.f / a.kv_scale;  // a power of two (1 except on fp8 pools)
+    if constexpr (kVec) {
+        const int cpr = r.cw >> 3;
+        for (int i = lane; i < r.it.n * cpr; i += 32) {
+            const int row = i / cpr, c = (i - row * cpr) * 8;
+            float x[8];
+            load8(src + row * stride + c, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= inv;
+            store8(dst + static_cast<size_t>(row) * a.kv_dim + c, x);
+        }
+    } else {
+        for (int i = lane; i < r.it.n * r.cw; i += 32) {
+            const int row = i / r.cw, c = i - row * r.cw;
+            put1(dst + static_cast<size_t>(row) * a.kv_dim + c, load1(src + row * stride + c) * inv);
+        }
+    }
+}
+
+template <class S, bool kVec>
+__global__ void __launch_bounds__(256) append_pages_q8_kernel(PagesArgs p, Q8Addr q) {
+    const PagedAddr &a = q.a;
+    if (upload_runs(p, a)) return;
+    const int w = (static_cast<int>(blockIdx.x) - p.n_runs) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (w >= p.n_items * 2 * q.n_kv) return;
+    const RowSpan r = row_span(p, a, q.hd, q.n_kv, w);
+    if (!r.ok) {
+        if (lane == 0 && p.err) atomicOr(p.err, 1);
+        return;
+    }
+    const int64_t stride = r.is_v ? p.v_stride : p.k_stride;
+    const S *src = static_cast<const S *>(r.is_v ? p.V : p.K) + static_cast<int64_t>(r.it.row0) * stride + r.c0;
+    uint8_t *page = static_cast<uint8_t *>(r.is_v ? a.v : a.k) + static_cast<size_t>(r.it.blk) * a.block_stride +
+                    a.layer_off + r.c0;
+    uint8_t *dst = page + static_cast<size_t>(r.it.off) * a.kv_dim;
+    float *scale = (r.is_v ? q.vs : q.ks) + static_cast<int64_t>(r.it.blk) * q.scale_stride + r.c0 / q.hd;
+    const float old = r.it.off > 0 ? *scale : 0.f;
+
+    uint32_t m = 0;
+    if constexpr (kVec) {
+        const int cpr = r.cw >> 3;
+        for (int i = lane; i < r.it.n * cpr; i += 32) {
+            const int row = i / cpr, c = (i - row * cpr) * 8;
+            float x[8];
+            load8(src + row * stride + c, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = max(m, abs_bits(x[j]));
+        }
+    } else {
+        for (int i = lane; i < r.it.n * r.cw; i += 32) {
+            const int row = i / r.cw, c = i - row * r.cw;
+            m = max(m, abs_bits(load1(src + row * stride + c)));
+        }
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    // a value that is not finite has no element: the scale becomes NaN, which
+    // every read of the block and head returns until its first row is written again
+    const bool bad = m >= kInfBits || abs_bits(old) >= kInfBits;
+    const int e_old = scale_exp(old);
+    const int e = bad ? 0 : r.it.off > 0 ? max(e_old, need_exp(m)) : need_exp(m);
+    const float inv = pow2f(-e);
+    if (lane == 0) *scale = bad ? __uint_as_float(0x7fc00000u) : pow2f(e);
+    if (r.it.off > 0 && !bad && e > e_old) {  // the step grew: the kept rows in the new step
+        const float f = pow2f(max(-126, e_old - e));
+        for (int i = lane; i < r.it.off * r.cw; i += 32) {
+            const int row = i / r.cw, c = i - row * r.cw;
+            uint8_t *u = page + static_cast<size_t>(row) * a.kv_dim + c;
+            *u = static_cast<uint8_t>(q8_elem(static_cast<float>(static_cast<int>(*u) - 128), f));
+        }
+    }
+    if constexpr (kVec) {
+        const int cpr = r.cw >> 3;
+        for (int i = lane; i < r.it.n * cpr; i += 32) {
+            const int row = i / cpr, c = (i - row * cpr) * 8;
+            float x[8];
+            load8(src + row * stride + c, x);
+            uint32_t lo = 0x80808080u, hi = 0x80808080u;
+            if (!bad) {
+                lo = q8_elem(x[0], inv) | q8_elem(x[1], inv) << 8 | q8_elem(x[2], inv) << 16 | q8_elem(x[3], inv) << 24;
+                hi = q8_elem(x[4], inv) | q8_elem(x[5], inv) << 8 | q8_elem(x[6], inv) << 16 | q8_elem(x[7], inv) << 24;
+            }
+            *reinterpret_cast<uint2 *>(dst + static_cast<size_t>(row) * a.kv_dim + c) = make_uint2(lo, hi);
+        }
+    } else {
+        for (int i = lane; i < r.it.n * r.cw; i += 32) {
+            const int row = i / r.cw, c = i - row * r.cw;
+            dst[static_cast<size_t>(row) * a.kv_dim + c] =
+                bad ? 128 : static_cast<uint8_t>(q8_elem(load1(src + row * stride + c), inv));
+        }
+    }
+}
+
+// ------------------------------------------------------------------- read ----
+
+template <class D, class E, bool kVec>
+__global__ void __launch_bounds__(256) read_pages_kernel(PagesArgs p, PagedAddr a, int n_groups) {
+    const int w = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (w >= p.n_items * 2 * n_groups) return;
+    const RowSpan r = row_span(p, a, kColGroup, n_groups, w);
+    if (!r.ok) {
+        if (lane == 0 && p.err) atomicOr(p.err, 1);
+        return;
+    }
+    const int64_t stride = r.is_v ? p.v_stride : p.k_stride;
+    D *dst = static_cast<D *>(r.is_v ? p.V : p.K) + static_cast<int64_t>(r.it.row0) * stride + r.c0;
+    const E *src = static_cast<const E *>(r.is_v ? a.v : a.k) + static_cast<size_t>(r.it.blk) * a.block_stride +
+                   a.layer_off + static_cast<size_t>(r.it.off) * a.kv_dim + r.c0;
+    if constexpr (kVec) {
+        const int cpr = r.cw >> 3;
+        for (int i = lane; i < r.it.n * cpr; i += 32) {
+            const int row = i / cpr, c = (i - row * cpr) * 8;
+            float x[8];
+            pool8(src + static_cast<size_t>(row) * a.kv_dim + c, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= a.kv_scale;
+            store8(dst + row * stride + c, x);
+        }
+    } else {
+        for (int i = lane; i < r.it.n * r.cw; i += 32) {
+            const int row = i / r.cw, c = i - row * r.cw;
+            put1(dst + row * stride + c, pool1(src + static_cast<size_t>(row) * a.kv_dim + c) * a.kv_scale);
+        }
+    }
+}
+
+template <class D, bool kVec>
+__global__ void __launch_bounds__(256) read_pages_q8_kernel(PagesArgs p, Q8Addr q) {
+    const PagedAddr &a = q.a;
+    const int w = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (w >= p.n_items * 2 * q.n_kv) return;
+    const RowSpan r = row_span(p, a, q.hd, q.n_kv, w);
+    if (!r.ok) {
+        if (lane == 0 && p.err) atomicOr(p.err, 1);
+        return;
+    }
+    const int64_t stride = r.is_v ? p.v_stride : p.k_stride;
+    D *dst = static_cast<D *>(r.is_v ? p.V : p.K) + static_cast<int64_t>(r.it.row0) * stride + r.c0;
+    const uint8_t *src = static_cast<const uint8_t *>(r.is_v ? a.v : a.k) +
+                         static_cast<size_t>(r.it.blk) * a.block_stride + a.layer_off +
+                         static_cast<size_t>(r.it.off) * a.kv_dim + r.c0;
+    const float sc = __ldg((r.is_v ? q.vs : q.ks) + static_cast<int64_t>(r.it.blk) * q.scale_stride + r.c0 / q.hd);
+    if constexpr (kVec) {
+        const int cpr = r.cw >> 3;
+        for (int i = lane; i < r.it.n * cpr; i += 32) {
+            const int row = i / cpr, c = (i - row * cpr) * 8;
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src + static_cast<size_t>(row) * a.kv_dim + c));
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                x[j] = static_cast<float>(static_cast<int>((j < 4 ? u.x : u.y) >> (8 * (j & 3)) & 255u) - 128) * sc;
+            store8(dst + row * stride + c, x);
+        }
+    } else {
+        for (int i = lane; i < r.it.n * r.cw; i += 32) {
+            const int row = i / r.cw, c = i - row * r.cw;
+            put1(dst + row * stride + c,
+                 static_cast<float>(static_cast<int>(src[static_cast<size_t>(row) * a.kv_dim + c]) - 128) * sc);
+        }
+    }
+}
+
+// ------------------------------------------------------------------- rope ----
+
+// One warp per token: lane l turns the pairs (i, i + hd/2), i = l, l + 32, ...
+// of every query and key head by pos * base^(-2i/hd), with the arithmetic of
+// the append kernel's rotation (angle, cosine and sine in double precision,
+// the products and sums each rounded to f32).
+__global__ void __launch_bounds__(256) rope_rows_kernel(RopeArgs p) {
+    const int t = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (t >= p.n_tok) return;
+    int lo = 0, hi = p.n_rows - 1;  // the batch row of token t
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.rows[mid].q_row0 <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    const int pos = p.rows[lo].past_len + (t - p.rows[lo].q_row0);
+    const int half = p.hd >> 1, nq = p.q_dim / p.hd, nk = p.kv_dim / p.hd;
+    const double lb = log(p.base);
+    for (int i = lane; i < half; i += 32) {
+        double sd, cd;
+        sincos(static_cast<double>(pos) * exp(-2.0 * i / p.hd * lb), &sd, &cd);
+        const float c = static_cast<float>(cd), sn = static_cast<float>(sd);
+        for (int h = 0; h < nq + nk; ++h) {
+            const bool is_k = h >= nq;
+            const size_t o = is_k ? static_cast<size_t>(t) * p.kv_dim + static_cast<size_t>(h - nq) * p.hd
+                                  : static_cast<size_t>(t) * p.q_dim + static_cast<size_t>(h) * p.hd;
+            const float *src = (is_k ? p.K : p.Q) + o;
+            float *dst = (is_k ? p.K_rot : p.Q_rot) + o;
+            const float x0 = src[i], x1 = src[i + half];
+            dst[i] = __fsub_rn(__fmul_rn(x0, c), __fmul_rn(x1, sn));
+            dst[i + half] = __fadd_rn(__fmul_rn(x0, sn), __fmul_rn(x1, c));
+        }
+    }
+}
+
+// ---------------------------------------------------------------- dispatch ----
+
+size_t type_bytes(Elem t) { return t == Elem::f32 ? 4 : t == Elem::bf16 || t == Elem::f16 ? 2 : 1; }
+
+// 16-byte accesses of eight packed elements, and of the pool's: the packed
+// rows' bases and strides and the columns of a group all on such boundaries.
+bool vec_ok(const PagesArgs &p, const PagedAddr &a, int group) {
+    const size_t e = type_bytes(p.type);
+    auto al = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
+    return al(p.K) && al(p.V) && (p.k_stride * e) % 16 == 0 && (p.v_stride * e) % 16 == 0 && a.kv_dim % 8 == 0 &&
+           group % 8 == 0 && al(a.k) && al(a.v);
+}
+
+bool grid_of(long long warps, int n_runs, unsigned *grid) {
+    const long long b = (warps + 7) / 8 + n_runs;
+    if (b <= 0 || b > 0x7fffffffLL) return false;
+    *grid = static_cast<unsigned>(b);
+    return true;
+}
+
+template <class S, class E>
+cudaError_t append_as(const PagesArgs &p, const PagedAddr &a, cudaStream_t s) {
+    const int n_groups = (a.kv_dim + kColGroup - 1) / kColGroup;
+    unsigned grid;
+    if (!grid_of(2LL * p.n_items * n_groups, p.n_runs, &grid)) return cudaErrorInvalidConfiguration;
+    if (vec_ok(p, a, kColGroup)) append_pages_kernel<S, E, true><<<grid, 256, 0, s>>>(p, a, n_groups);
+    else append_pages_kernel<S, E, false><<<grid, 256, 0, s>>>(p, a, n_groups);
+    return cudaGetLastError();
+}
+template <class S>
+cudaError_t append_from(const PagesArgs &p, const PagedAddr &a, cudaStream_t s) {
+    if (a.fp8) return append_as<S, fp8>(p, a, s);
+    if (a.bf16) return append_as<S, bf16>(p, a, s);
+    return append_as<S, float>(p, a, s);
+}
+template <class S>
+cudaError_t append_q8_from(const PagesArgs &p, const Q8Addr &q, cudaStream_t s) {
+    unsigned grid;
+    if (!grid_of(2LL * p.n_items * q.n_kv, p.n_runs, &grid)) return cudaErrorInvalidConfiguration;
+    if (vec_ok(p, q.a, q.hd)) append_pages_q8_kernel<S, true><<<grid, 256, 0, s>>>(p, q);
+    else append_pages_q8_kernel<S, false><<<grid, 256, 0, s>>>(p, q);
+    return cudaGetLastError();
+}
+template <class D, class E>
+cudaError_t read_as(const PagesArgs &p, const PagedAddr &a, cudaStream_t s) {
+    const int n_groups = (a.kv_dim + kColGroup - 1) / kColGroup;
+    unsigned grid;
+    if (!grid_of(2LL * p.n_items * n_groups, 0, &grid)) return cudaErrorInvalidConfiguration;
+    if (vec_ok(p, a, kColGroup)) read_pages_kernel<D, E, true><<<grid, 256, 0, s>>>(p, a, n_groups);
+    else read_pages_kernel<D, E, false><<<grid, 256, 0, s>>>(p, a, n_groups);
+    return cudaGetLastError();
+}
+template <class D>
+cudaError_t read_to(const PagesArgs &p, const PagedAddr &a, cudaStream_t s) {
+    if (a.fp8) return read_as<D, fp8>(p, a, s);
+    if (a.bf16) return read_as<D, bf16>(p, a, s);
+    return read_as<D, float>(p, a, s);
+}
+template <class D>
+cudaError_t read_q8_to(const PagesArgs &p, const Q8Addr &q, cudaStream_t s) {
+    unsigned grid;
+    if (!grid_of(2LL * p.n_items * q.n_kv, 0, &grid)) return cudaErrorInvalidConfiguration;
+    if (vec_ok(p, q.a, q.hd)) read_pages_q8_kernel<D, true><<<grid, 256, 0, s>>>(p, q);
+    else read_pages_q8_kernel<D, false><<<grid, 256, 0, s>>>(p, q);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_append_pages(const PagesArgs &p, const PagedAddr &a, cudaStream_t s) {
+    switch (p.type) {
+        case Elem::f32: return append_from<float>(p, a, s);
+        case Elem::bf16: return append_from<bf16>(p, a, s);
+        case Elem::f16: return append_from<f16>(p, a, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+cudaError_t launch_append_pages_q8(const PagesArgs &p, const Q8Addr &q, cudaStream_t s) {
+    switch (p.type) {
+        case Elem::f32: return append_q8_from<float>(p, q, s);
+        case Elem::bf16: return append_q8_from<bf16>(p, q, s);
+        case Elem::f16: return append_q8_from<f16>(p, q, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+cudaError_t launch_read_pages(const PagesArgs &p, const PagedAddr &a, cudaStream_t s) {
+    switch (p.type) {
+        case Elem::f32: return read_to<float>(p, a, s);
+        case Elem::bf16: return read_to<bf16>(p, a, s);
+        case Elem::f16: return read_to<f16>(p, a, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+cudaError_t launch_read_pages_q8(const PagesArgs &p, const Q8Addr &q, cudaStream_t s) {
+    switch (p.type) {
+        case Elem::f32: return read_q8_to<float>(p, q, s);
+        case Elem::bf16: return read_q8_to<bf16>(p, q, s);
+        case Elem::f16: return read_q8_to<f16>(p, q, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+cudaError_t launch_rope_rows(const RopeArgs &p, cudaStream_t s) {
+    if (p.n_tok <= 0) return cudaErrorInvalidValue;
+    rope_rows_kernel<<<(p.n_tok + 7) / 8, 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace pkv
