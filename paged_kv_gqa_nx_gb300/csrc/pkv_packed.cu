@@ -13,13 +13,17 @@
 // graph.
 #include "pkv_elem.h"
 #include "pkv_internal.h"
+#include "pkv_tcgen05.h"
 
+#include <cuda.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 namespace pkv {
 namespace {
 
 using f16 = __half;
+using namespace tc;
 
 __device__ __forceinline__ float widen(bf16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float widen(f16 x) { return __half2float(x); }
@@ -36,6 +40,426 @@ __device__ __forceinline__ int seq_of_tile(const PackedSeqs<N> &l, int t) {
         else hi = mid - 1;
     }
     return lo;
+}
+
+// ------------------------------------------------------------ tensor cores ----
+//
+// One CTA = two tiles of 128 query rows of one sequence (two softmax chains
+// that share every K/V tile).  A tile is 128/P consecutive tokens x P heads of
+// one kv head, P the largest power of two (at most 16) that divides the group,
+// so the rows of a tile need the same keys and a causal tile's masked corner
+// is only 128/P tokens deep.  Row m of chain c is token m / P, head m % P, TMEM
+// lane m and thread m of warps 4c .. 4c + 3.
+//
+//   S_c [128 x 128] = Q_c K_j^T    A, B from shared memory (K-major)
+//   O_c [128 x D]  += P_c V_j      A from TMEM (P over S, two values a column),
+//                                  B from shared memory (V as stored: MN-major)
+//
+// Warps 8 and 10 issue chain 0's and chain 1's MMAs, warp 9 the TMA loads
+// (Q once; K_0, V_0, K_1, ... through a ring of slots), warp 11 looks over the
+// V tiles that a query does not see whole.  A chain runs QK(j), softmax(j),
+// PV(j) and QK(j + 1) back to back; while one chain's softmax runs, the tensor
+// core works on the other's products.  P of tile j is read by PV(j) before
+// QK(j + 1), issued by the same thread, writes over it.
+//
+// Probabilities are rounded to the operand type (half a step, 2^-9 or 2^-12
+// relative to p, against outputs of the same type); sums use them unrounded.
+// The reference maximum moves, and O is rescaled, only where a tile's maximum
+// passes it by more than 2^8, which keeps every p at most 256.
+//
+// A zero probability times an infinity is NaN, so V rows behind a sequence's
+// end or in a query's future must not hold one: on the (at most two) tiles
+// that some row of the CTA does not see whole, warp 11 replaces values that
+// are not finite by 0 and, where it found any, the compute threads add those
+// products for the keys that their row does see.
+constexpr int kKeys = 128;  // keys per tile
+constexpr int kTcThreads = 384;
+constexpr int kWarpMma0 = 8, kWarpLoad = 9, kWarpLook = 11;  // warp 10: chain 1's MMAs
+// registers per thread: at launch, then of warps 8-11 and of the compute warps
+constexpr int kTcLaunchRegs = 168, kTcOtherRegs = 88, kTcComputeRegs = 208;
+static_assert(256 * kTcComputeRegs + 128 * kTcOtherRegs <= kTcThreads * kTcLaunchRegs, "register split");
+constexpr uint32_t kTcCols = 512;           // O_c at c * 128, S_c / P_c at 256 + c * 128
+constexpr float kGrow = 8.f;                // log2 headroom of the reference maximum
+
+template <int D>
+struct TcCfg {
+    static constexpr uint32_t kTile = kKeys * D * 2;         // bytes of a Q, K or V tile
+    static constexpr uint32_t kBlock = kKeys * 128;          // 64 columns of it
+    static constexpr int kSlots = D == 128 ? 5 : 8;
+    static constexpr size_t kSmem = (2 + kSlots) * kTile + 1024;  // + alignment slack
+};
+
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];\n" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(mbar)
+        : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {  // 2^x to about 2^-22 relative; 0 for -inf
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack2(bf16, float lo, float hi) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&t);
+}
+__device__ __forceinline__ uint32_t pack2(f16, float lo, float hi) {
+    const __half2 t = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&t);
+}
+__device__ __forceinline__ float half_of(bf16, uint32_t w, int i) {
+    return __uint_as_float(i ? w & 0xffff0000u : w << 16);
+}
+__device__ __forceinline__ float half_of(f16, uint32_t w, int i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return i ? f.y : f.x;
+}
+// the element's bits are an infinity or a NaN
+template <class T>
+__device__ __forceinline__ bool not_finite(uint32_t b16) {
+    constexpr uint32_t e = std::is_same<T, bf16>::value ? 0x7f80u : 0x7c00u;
+    return (b16 & e) == e;
+}
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n" : "=r"(r) : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+    return r;
+}
+// Shared-memory matrix descriptor of a V tile, MN-major with 128-byte swizzle:
+// 64 columns of a key in 128 bytes, 8 keys 1024 bytes apart (stride offset),
+// the next 64 columns kBlock bytes on (leading offset).
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t block) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(block >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+// Instruction descriptor: f32 accumulator, M = 128, A K-major, B K- or MN-major.
+template <class T>
+__host__ __device__ constexpr uint32_t idesc16(uint32_t n, bool b_mn) {
+    constexpr uint32_t f = std::is_same<T, bf16>::value ? 1u : 0u;
+    return (1u << 4) | (f << 7) | (f << 10) | (b_mn ? 1u << 16 : 0u) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+template <int D, class T, int N>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    packed_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ PackedArgs a,
+                     const __grid_constant__ PackedSeqs<N> l, int log_p) {
+    using C = TcCfg<D>;
+    constexpr int NS = C::kSlots;
+    extern __shared__ __align__(1024) unsigned char smraw[];
+    unsigned char *sm = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smraw) + 1023) & ~static_cast<uintptr_t>(1023));
+    unsigned char *ring = sm + 2 * C::kTile;  // Q_c at c * kTile
+    __shared__ uint64_t bar_full[NS], bar_free[NS], bar_q, bar_s[2], bar_p[2], bar_o[2], bar_look[2], bar_go[2];
+    __shared__ uint32_t tslot, dirty[2], held[2];  // held[c]: O_c already holds something before PV(0)
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int P = 1 << log_p, TQ = 128 >> log_p;
+    const int n_ht = a.n_heads >> log_p;
+    const int t = blockIdx.x / n_ht, ht = blockIdx.x - t * n_ht;
+    const int s = seq_of_tile(l, t);
+    const int len = l.len[s], row0 = l.start[s];
+    // the last queries, which see the most keys, come first
+    const int q0 = (l.tile0[s + 1] - l.tile0[s] - 1 - (t - l.tile0[s])) * 2 * TQ;
+    const int h0 = ht << log_p, kvh = h0 / (a.n_heads / a.n_kv);
+    const int kend0 = a.causal ? min(len, q0 + TQ) : len;
+    const int kend1 = q0 + TQ >= len ? 0 : a.causal ? min(len, q0 + 2 * TQ) : len;
+    const int n0 = (kend0 + kKeys - 1) / kKeys, n1 = (kend1 + kKeys - 1) / kKeys;
+    const int n_max = max(n0, n1);
+    // tiles from this one on hold a key that some row does not see
+    const int look0 = a.causal ? q0 / kKeys : len / kKeys;
+
+    auto wait_w = [&](uint64_t *bar, uint32_t parity) {  // lane 0 waits (bounded), the warp learns the outcome
+        return __shfl_sync(0xffffffffu, lane == 0 ? mbar_wait(smem_u32(bar), parity) : true, 0) != 0;
+    };
+    auto rph = [](int i) { return static_cast<uint32_t>(i / NS) & 1u; };  // ring item i: slot i % NS
+
+    if (warp == 0) {
+        tmem_alloc(smem_u32(&tslot), kTcCols);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(smem_u32(&bar_full[i]), 1);
+            mbar_init(smem_u32(&bar_free[i]), 2);  // both chains' MMA warps
+        }
+        mbar_init(smem_u32(&bar_q), 1);
+        for (int c = 0; c < 2; ++c) {
+            mbar_init(smem_u32(&bar_s[c]), 1);
+            mbar_init(smem_u32(&bar_p[c]), 4);
+            mbar_init(smem_u32(&bar_o[c]), 1);
+            mbar_init(smem_u32(&bar_look[c]), 1);
+            mbar_init(smem_u32(&bar_go[c]), 1);
+            dirty[c] = 0;
+            held[c] = 0;
+        }
+        fence_proxy_async();  // the barriers, before the TMA unit uses them
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tbase = tslot;
+    bool ok = true;
+
+    if (warp >= 8) {
+        setmaxnreg_dec<kTcOtherRegs>();
+        if (warp == kWarpLoad) {
+            // ---------------- loads (lane 0): Q of both chains, then K_0, V_0, K_1, ... ----------------
+            if (lane == 0) {
+                const int nq = n1 > 0 ? 2 : 1;
+                mbar_expect_tx(smem_u32(&bar_q), nq * C::kTile);
+                for (int c = 0; c < nq; ++c)
+                    for (int x = 0; x < D / 64; ++x)
+                        tma_load3(smem_u32(sm + c * C::kTile + x * C::kBlock), &mq, 64 * x, h0, row0 + q0 + c * TQ,
+                                  smem_u32(&bar_q));
+            }
+            int issued = 0;
+            for (int i = 0; i < 2 * n_max; ++i) {
+                const int sl = i % NS;
+                if (i >= NS && !wait_w(&bar_free[sl], rph(i - NS))) break;
+                if (lane == 0) {
+                    mbar_expect_tx(smem_u32(&bar_full[sl]), C::kTile);
+                    for (int x = 0; x < D / 64; ++x)
+                        tma_load3(smem_u32(ring + sl * C::kTile + x * C::kBlock), (i & 1) ? &mv : &mk, 64 * x, kvh,
+                                  row0 + (i >> 1) * kKeys, smem_u32(&bar_full[sl]));
+                    if ((i & 1) && (i >> 1) >= look0) mbar_arrive(smem_u32(&bar_go[((i >> 1) - look0) & 1]));
+                }
+                issued = i + 1;
+            }
+            // the last copies land before the CTA's shared memory is given up (bounded)
+            wait_w(&bar_q, 0);
+            for (int i = max(0, issued - NS); i < issued; ++i) wait_w(&bar_full[i % NS], rph(i));
+        } else if (warp == kWarpLook) {
+            // ---------------- values that are not finite in partly seen V tiles ----------------
+            for (int j = look0; j < n_max && ok; ++j) {
+                // this warp follows no earlier item, so it learns from the loading warp
+                // that the slot is at item i before it looks at the slot's phase
+                const int i = 2 * j + 1, sl = i % NS;
+                ok = wait_w(&bar_go[(j - look0) & 1], 0) && wait_w(&bar_full[sl], rph(i));
+                if (!ok) break;
+                uint4 *v = reinterpret_cast<uint4 *>(ring + sl * C::kTile);
+                bool found = false;
+                for (int x = lane; x < static_cast<int>(C::kTile / 16); x += 32) {
+                    uint4 w = v[x];
+                    uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    bool any = false;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (not_finite<T>(u[k])) u[k] &= 0xffff0000u, any = true;
+                        if (not_finite<T>(u[k] >> 16)) u[k] &= 0xffffu, any = true;
+                    }
+                    if (any) v[x] = make_uint4(u[0], u[1], u[2], u[3]);
+                    found = found || any;
+                }
+                fence_proxy_async();  // before the MMAs read the tile
+                found = __any_sync(0xffffffffu, found);
+                if (lane == 0) {
+                    if (found) dirty[(j - look0) & 1] = 1;
+                    mbar_arrive(smem_u32(&bar_look[(j - look0) & 1]));
+                }
+                __syncwarp();
+            }
+            if (!ok && lane == 0 && a.err) atomicOr(a.err, 2);
+        } else {
+            // ---------------- MMA issue: chain c (lane 0) ----------------
+            const int c = warp == kWarpMma0 ? 0 : 1, n = c ? n1 : n0;
+            const uint32_t tS = tbase + 256 + 128 * c, tO = tbase + 128 * c;
+            const uint64_t dQ = desc_sw128(smem_u32(sm + c * C::kTile));
+            auto qk = [&](int j) {  // S_c = Q_c K_j^T, then the slot's and the scores' barriers
+                const int sl = (2 * j) % NS;
+                const uint64_t dK = desc_sw128(smem_u32(ring + sl * C::kTile));
+                if (lane == 0) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t o = ((k >> 2) * C::kBlock + (k & 3) * 32u) >> 4;
+                        mma_f16(tS, dQ + o, dK + o, idesc16<T>(kKeys, false), k > 0);
+                    }
+                    mma_commit(smem_u32(&bar_s[c]));
+                    mma_commit(smem_u32(&bar_free[sl]));
+                }
+                __syncwarp();
+            };
+            if (n > 0) {
+                ok = wait_w(&bar_q, 0) && wait_w(&bar_full[0], 0);
+                if (ok) {
+                    fence_after_sync();
+                    qk(0);
+                }
+            }
+            for (int j = 0; j < n && ok; ++j) {
+                const int iv = 2 * j + 1, sv = iv % NS;
+                ok = wait_w(&bar_full[sv], rph(iv));
+                if (ok && j >= look0) ok = wait_w(&bar_look[(j - look0) & 1], 0);
+                if (ok && j + 1 < n) ok = wait_w(&bar_full[(2 * j + 2) % NS], rph(2 * j + 2));
+                if (ok) ok = wait_w(&bar_p[c], j & 1);
+                if (!ok) break;
+                fence_after_sync();
+                const uint64_t dV = desc_mn(smem_u32(ring + sv * C::kTile), C::kBlock);
+                const uint32_t acc = j > 0 ? 1u : *static_cast<volatile uint32_t *>(&held[c]);
+                if (lane == 0) {
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k)
+                        mma_f16_ts(tO, tS + 8 * k, dV + ((k * 2048u) >> 4), idesc16<T>(D, true), k > 0 ? 1u : acc);
+                    mma_commit(smem_u32(&bar_free[sv]));
+                    if (j + 1 == n) mma_commit(smem_u32(&bar_o[c]));
+                }
+                __syncwarp();
+                if (j + 1 < n) qk(j + 1);
+            }
+            // items past the chain's last tile are free as far as this chain goes
+            // (counted once they have landed, so that each counts for its own phase)
+            for (int i = 2 * n; i < 2 * n_max && ok; ++i) {
+                ok = wait_w(&bar_full[i % NS], rph(i));
+                if (ok && lane == 0) mbar_arrive(smem_u32(&bar_free[i % NS]));
+            }
+            if (!ok && lane == 0 && a.err) atomicOr(a.err, 2);
+        }
+    } else {
+        // -------------- compute warps: one thread per row and chain --------------
+        setmaxnreg_inc<kTcComputeRegs>();
+        const int c = warp >> 2, n = c ? n1 : n0, m = tid & 127;
+        const int tok = q0 + c * TQ + (m >> log_p);
+        const bool valid = tok < len;
+        const int lim = a.causal ? min(tok + 1, len) : len;  // keys this row sees
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t tS = tbase + lanes + 256 + 128 * c, tO = tbase + lanes + 128 * c;
+        const float cs = a.scale_log2;  // > 0
+        float m_ref = -INFINITY, l_run = 0.f;
+        for (int j = 0; j < n; ++j) {
+            ok = wait_w(&bar_s[c], j & 1);
+            if (!ok) break;
+            fence_after_sync();
+            float x[kKeys];
+#pragma unroll
+            for (int i = 0; i < kKeys / 32; ++i) {
+                float h[32];
+                tmem_ld32(tS + 32 * i, h);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[32 * i + k] = h[k];
+            }
+            const int base = j * kKeys;
+            if (base + kKeys > lim) {
+#pragma unroll
+                for (int i = 0; i < kKeys; ++i) x[i] = base + i < lim ? x[i] : -INFINITY;
+            }
+            float mx[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx[i] = x[i];
+#pragma unroll
+            for (int i = 4; i < kKeys; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs;
+            const bool move = top > m_ref + kGrow || m_ref == -INFINITY;
+            const float m_use = move ? top : m_ref;
+            const float nm = m_use == -INFINITY ? 0.f : -m_use;
+            // O moves with the reference (QK(j), already done, followed PV(j - 1))
+            const float f = move && m_ref != -INFINITY ? ex2(m_ref - m_use) : 1.f;
+            if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+                for (int i = 0; i < D / 16; ++i) {
+                    float o[16];
+                    tmem_ld16(tO + 16 * i, o);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) o[k] *= f;
+                    tmem_st16(tO + 16 * i, o);
+                }
+            }
+            m_ref = m_use;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < kKeys / 64; ++i) {
+                uint32_t p[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    const float p0 = ex2(fmaf(x[64 * i + 2 * k], cs, nm)), p1 = ex2(fmaf(x[64 * i + 2 * k + 1], cs, nm));
+                    sum[2 * (k & 1)] += p0;
+                    sum[2 * (k & 1) + 1] += p1;
+                    p[k] = pack2(T{}, p0, p1);
+                }
+                tmem_st32u(tS + 32 * i, p);
+            }
+            l_run = fmaf(l_run, f, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+            tmem_st_wait();
+            if (j >= look0) {
+                ok = wait_w(&bar_look[(j - look0) & 1], 0);
+                if (!ok) break;
+                if (*static_cast<volatile uint32_t *>(&dirty[(j - look0) & 1])) {
+                    // this tile's V values that are not finite, key by key
+                    const T *v = static_cast<const T *>(a.V) + static_cast<int64_t>(row0 + base) * a.v_stride +
+                                 static_cast<int64_t>(kvh) * a.hd;
+                    const int see = valid ? min(kKeys, lim - base) : 0;
+#pragma unroll 1
+                    for (int i = 0; i < D / 16; ++i) {
+                        float o[16];
+                        if (j > 0) {
+                            tmem_ld16(tO + 16 * i, o);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = 0.f;
+                        }
+#pragma unroll 1
+                        for (int kk = 0; kk < kKeys / 2; ++kk) {
+                            const uint32_t w = tmem_ld1(tS + kk);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                if (2 * kk + e >= see) continue;
+                                const unsigned short *vr = reinterpret_cast<const unsigned short *>(
+                                    v + static_cast<int64_t>(2 * kk + e) * a.v_stride) + 16 * i;
+                                const float p = half_of(T{}, w, e);
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) {
+                                    if (16 * i + k >= a.hd) continue;
+                                    const uint32_t b = __ldg(vr + k);
+                                    if (not_finite<T>(b)) o[k] = fmaf(p, half_of(T{}, b, 0), o[k]);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        tmem_st16(tO + 16 * i, o);
+                    }
+                    if (j == 0 && m == 0) *static_cast<volatile uint32_t *>(&held[c]) = 1;
+                    tmem_st_wait();
+                }
+            }
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar_p[c]));
+        }
+        if (n > 0) {
+            if (ok) ok = wait_w(&bar_o[c], 0);
+            if (!ok) {
+                if (lane == 0 && a.err) atomicOr(a.err, 2);
+            } else {
+                fence_after_sync();
+                const float inv = 1.f / l_run;
+                T *dst = static_cast<T *>(a.out) + static_cast<int64_t>(row0 + (valid ? tok : 0)) * a.o_stride +
+                         static_cast<int64_t>(h0 + (m & (P - 1))) * a.hd;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    float o[32];
+                    tmem_ld32(tO + 32 * i, o);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (valid && 32 * i + 8 * k < a.hd)
+                            *reinterpret_cast<uint4 *>(dst + 32 * i + 8 * k) =
+                                make_uint4(pack2(T{}, o[8 * k] * inv, o[8 * k + 1] * inv),
+                                           pack2(T{}, o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                                           pack2(T{}, o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                                           pack2(T{}, o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+                }
+            }
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tbase, kTcCols);
 }
 
 // ---------------------------------------------------------------- general ----
@@ -163,6 +587,92 @@ cudaError_t launch_general_n(const PackedArgs &a, const int32_t *start, const in
     return cudaGetLastError();
 }
 
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+cudaError_t encode_fn(EncodeFn *out) {
+    static std::atomic<EncodeFn> known{nullptr};
+    EncodeFn f = known.load(std::memory_order_acquire);
+    if (!f) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+        if (e != cudaSuccess) return e;
+        if (!p || q != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
+        f = reinterpret_cast<EncodeFn>(p);
+        known.store(f, std::memory_order_release);
+    }
+    *out = f;
+    return cudaSuccess;
+}
+
+// Rows [tokens][heads][hd] with a token stride, in boxes of 64 columns x
+// box_heads x box_tokens; columns past hd and tokens past the last read as 0.
+cudaError_t rows_map(CUtensorMap *m, EncodeFn f, const PackedArgs &a, const void *base, int64_t stride, int heads,
+                     int box_heads, int box_tokens) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.hd), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(a.n_tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.hd) * 2, static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+    const cuuint32_t one[3] = {1, 1, 1};
+    const CUresult r = f(m, a.type == Elem::bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                         const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Whether the tensor-core kernel takes the call: TMA's alignment rules, a
+// positive finite scale (the kernel masks with -inf before it scales).
+bool tc_takes(const PackedArgs &a) {
+    auto ok = [](const void *p, int64_t stride) {
+        return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0 && stride < (1LL << 38);
+    };
+    return a.hd % 8 == 0 && a.hd <= 128 && ok(a.Q, a.q_stride) && ok(a.K, a.k_stride) && ok(a.V, a.v_stride) &&
+           ok(a.out, a.o_stride) && a.scale_log2 > 0.f && a.scale_log2 <= 3e38f;
+}
+
+template <int D, class T, int N>
+cudaError_t launch_tc_n(const PackedArgs &a, const int32_t *start, const int32_t *len, int32_t n, cudaStream_t s) {
+    using C = TcCfg<D>;
+    static PerDeviceOnce configured;  // the attributes are per function and device
+    const cudaError_t ce = configured.run([&]() -> cudaError_t {
+        // setmaxnreg.inc waits for registers of the launch's own: launch only
+        // if the kernel starts with what the split was sized for
+        cudaFuncAttributes fa{};
+        cudaError_t e = cudaFuncGetAttributes(&fa, packed_tc_kernel<D, T, N>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs < kTcLaunchRegs || fa.maxThreadsPerBlock < kTcThreads) return cudaErrorInvalidConfiguration;
+        return cudaFuncSetAttribute(packed_tc_kernel<D, T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(C::kSmem));
+    });
+    if (ce != cudaSuccess) return ce;
+    const int group = a.n_heads / a.n_kv;
+    int log_p = 0;
+    while (log_p < 4 && group % (2 << log_p) == 0) ++log_p;
+    EncodeFn f;
+    cudaError_t e = encode_fn(&f);
+    CUtensorMap mq, mk, mv;
+    if (e == cudaSuccess) e = rows_map(&mq, f, a, a.Q, a.q_stride, a.n_heads, 1 << log_p, 128 >> log_p);
+    if (e == cudaSuccess) e = rows_map(&mk, f, a, a.K, a.k_stride, a.n_kv, 1, kKeys);
+    if (e == cudaSuccess) e = rows_map(&mv, f, a, a.V, a.v_stride, a.n_kv, 1, kKeys);
+    if (e != cudaSuccess) return e;
+    PackedSeqs<N> l;
+    fill_seqs(l, start, len, n, 2 * (128 >> log_p));
+    const long long grid = static_cast<long long>(l.tile0[n]) * (a.n_heads >> log_p);
+    if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    packed_tc_kernel<D, T, N><<<static_cast<unsigned>(grid), kTcThreads, C::kSmem, s>>>(mq, mk, mv, a, l, log_p);
+    return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t launch_tc(const PackedArgs &a, const int32_t *start, const int32_t *len, int32_t n, cudaStream_t s) {
+    if (a.hd <= 64)
+        return n <= 64 ? launch_tc_n<64, T, 64>(a, start, len, n, s) : launch_tc_n<64, T, kPackedSeqs>(a, start, len, n, s);
+    return n <= 64 ? launch_tc_n<128, T, 64>(a, start, len, n, s) : launch_tc_n<128, T, kPackedSeqs>(a, start, len, n, s);
+}
+
 template <class T>
 cudaError_t launch_general(const PackedArgs &a, const int32_t *start, const int32_t *len, int32_t n, cudaStream_t s) {
     if (n <= 64) return launch_general_n<T, 64>(a, start, len, n, s);
@@ -174,6 +684,10 @@ cudaError_t launch_general(const PackedArgs &a, const int32_t *start, const int3
 cudaError_t launch_packed(const PackedArgs &a, const int32_t *start, const int32_t *len, int32_t n_seqs,
                           cudaStream_t s) {
     if (n_seqs <= 0 || n_seqs > kPackedSeqs) return cudaErrorInvalidValue;
+    if (tc_takes(a)) {
+        if (a.type == Elem::bf16) return launch_tc<bf16>(a, start, len, n_seqs, s);
+        if (a.type == Elem::f16) return launch_tc<f16>(a, start, len, n_seqs, s);
+    }
     if (a.type == Elem::bf16) return launch_general<bf16>(a, start, len, n_seqs, s);
     if (a.type == Elem::f16) return launch_general<f16>(a, start, len, n_seqs, s);
     return cudaErrorInvalidValue;
