@@ -1278,6 +1278,7 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
         if (e != cudaSuccess) return cuda_fail(e, "shared-prefix kernel");
     }
     if (!w.units.empty()) {
+        for (const UnitDesc &u : w.units) a.max_q = std::max(a.max_q, rows[u.row].n_q);
         e = launch(PKV_KERNEL_DECODE, st, [&] {
             return p->q8 ? launch_decode_q8(a, q8_addr(p, layer), st) : launch_decode_paged(a, addr, st);
         });

@@ -157,6 +157,7 @@ struct AttnArgs {
     const float *K_new = nullptr, *V_new = nullptr;
     const AppendDesc *app = nullptr;
     int32_t pt_write = 0;
+    int32_t max_q = 1;  // the most queries a row of this launch's units has (8-bit pools)
 };
 
 // One tensor-core prefill tile: queries q0 .. q0 + 128/G - 1 of row `row`

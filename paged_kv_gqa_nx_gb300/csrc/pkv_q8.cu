@@ -12,6 +12,7 @@
 #include "pkv_internal.h"
 #include "pkv_rows.h"
 
+#include <algorithm>
 #include <cuda_fp16.h>
 
 namespace pkv {
@@ -162,6 +163,422 @@ cudaError_t launch_generic(const AttnArgs &a, const Q8Addr &q, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+// ------------------------------------------------------------- fast decode ----
+//
+// Head widths that are multiples of 16 up to 128, any group: both products of
+// a key tile on warp-level m16n8k16 MMAs (f16 operands, f32 accumulators) with
+// the keys and the dims on the 16-row side, so no row of an MMA is wasted:
+//
+//   S^T [16 keys x 8]  = (U_K - 128) [16 x hd] . Q^T [hd x 8]
+//   O^T [16 dims x 8] += (U_V - 128)^T [16 x keys] . W^T [keys x 8]
+//
+// The 8 columns are four (query, head) pairs with the two f16 pieces of each
+// f32 value (x = x0 + x1, 22 significant bits): columns 2c and 2c + 1 hold
+// pair c's pieces, so a lane owns whole pairs: lane 4g + c holds pair c's
+// scores of keys g and g + 8 and needs no shuffle to add the pieces.  The f16
+// pairs of W (a key's two pieces) become the B fragment of the second product
+// by one 8 x 8 transpose (movmatrix).  Elements widen from bytes to f16 by two
+// byte permutes (1024 + u) and two subtractions (1152) for four values, exact;
+// the transposed loads of V hand out two dims x two keys a word, which the
+// same permutes sort into even and odd dims.
+//
+// CTA = 4 warps = one (unit, kv head, block of pairs); warp w takes the unit's
+// tiles w, w + 4, ... of 32 keys through its own two-stage cp.async ring and
+// keeps its own online softmax per pair; the warps' states merge at the end.
+// The reference maximum of a pair moves only where a score passes it by more
+// than 2^8 (one warp vote per tile finds out); sums stay per lane until the
+// end.  W = p * vs / 2^c with c an exponent of the warp that follows the
+// largest V scale of the tiles (O holds 2^-c times the sum), which keeps W in
+// f16's range: W <= 2^14 after a factor 2^6, and blocks of one 32-key tile may
+// differ by 2^12 in scale before W's pieces lose bits below 2^-19 of p.
+//
+// Shared memory rows keep their 16-byte chunks XOR-swizzled by the key, so
+// that the 8 rows of an ldmatrix fall in distinct bank groups.
+
+constexpr int kW = 4;            // warps per CTA
+constexpr int kT = 32;           // keys per tile
+constexpr int kStages = 2;
+constexpr float kGrowQ = 8.f;    // log2 headroom of the reference maximum
+constexpr float kWScale = 64.f;  // W's factor: 2^8 * 2^6 = 2^14
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    return y;
+}
+// bytes i and j of w as (u - 128) in the halves of an f16 pair: 0x6400 | u is 1024 + u
+template <int kSel>
+__device__ __forceinline__ uint32_t widen2(uint32_t w) {
+    const uint32_t b = __byte_perm(w, 0x64646464u, kSel);
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&b), __half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ float ex2f(float x) {  // 2^x to about 2^-22 relative; 0 for -inf
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+// the two f16 pieces of x as a pair (x0 in the low half)
+__device__ __forceinline__ uint32_t pieces2(float x) {
+    const __half h0 = __float2half_rn(x);
+    const __half2 h = __halves2half2(h0, __float2half_rn(x - __half2float(h0)));
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ void cp_async16z(uint32_t dst, const void *src, uint32_t n) {  // n = 16, or 0: zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+// Columns of a CTA: pair x = 4 * nt + c of its block is (query qi + x / gb,
+// head h0 + x % gb) with gb heads per block.
+template <int HD>
+struct FastQ8 {
+    static constexpr int kStage = 2 * kT * HD;  // bytes: K rows, V rows
+    static constexpr int kChunks = HD / 16;     // 16-byte chunks of a row
+    // chunk c of key j sits at chunk position c ^ swz(j)
+    static __device__ __forceinline__ int swz(int j) {
+        return HD == 128 ? (j & 7) : HD == 64 ? ((j >> 1) & 3) : HD == 32 ? ((j >> 2) & 1) : 0;
+    }
+};
+
+template <int HD, int NB>
+__global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2) decode_q8_kernel(AttnArgs a, Q8Addr q, int gb, int qb) {
+    using F = FastQ8<HD>;
+    constexpr int NC = F::kChunks;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float2 sc_tile[kW][kStages][kT];  // K and V scales of a tile's keys
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int n_hb = (a.group + gb - 1) / gb;  // head blocks of a kv head
+    int b = blockIdx.x;
+    const int hb = b % n_hb;
+    b /= n_hb;
+    const int kvh = b % a.n_kv, ui = b / a.n_kv;
+    const UnitDesc u = a.units[ui];
+    const RowDesc rd = a.rows[u.row];
+    const int h0 = kvh * a.group + hb * gb, nh = min(gb, a.group - hb * gb);
+    const int nq = min(qb, rd.n_q - u.qi);  // queries of this unit
+    const int total_k = rd.past_len + rd.n_q;
+    const int kbeg = rd.k0 + (u.split - rd.s0) * a.split_keys;
+    const int kend = min(kbeg + a.split_keys, a.causal ? rd.past_len + u.qi + nq : total_k);
+    const int n_tiles = (kend - kbeg + kT - 1) / kT;
+    const int my_n = warp < n_tiles ? (n_tiles - warp + kW - 1) / kW : 0;
+    unsigned char *wbase = smem + warp * kStages * F::kStage;
+    const uint32_t wbase_s = static_cast<uint32_t>(__cvta_generic_to_shared(wbase));
+    const uint8_t *const kp = static_cast<const uint8_t *>(q.a.k), *const vp = static_cast<const uint8_t *>(q.a.v);
+
+    // Tile loads: lane j finds key j's row and scales; the lanes then copy the
+    // rows' chunks, K and V, each a 16-byte cp.async (zeros past the unit, and
+    // where the page lookup failed, with scale 0).
+    auto load_tile = [&](int kl, int st) {
+        const int pos = kbeg + (warp + kl * kW) * kT + lane;
+        int64_t off = -1;
+        float2 sc = make_float2(0.f, 0.f);
+        if (pos < kend) {
+            const int blk = block_of(q.a, rd.slot, pos, a.err);
+            if (blk >= 0) {
+                off = static_cast<int64_t>(blk) * q.a.block_stride + q.a.layer_off +
+                      static_cast<int64_t>(block_off(q.a, pos)) * q.a.kv_dim + static_cast<int64_t>(kvh) * HD;
+                sc = make_float2(__ldg(q.ks + blk * q.scale_stride + kvh), __ldg(q.vs + blk * q.scale_stride + kvh));
+            }
+        }
+        sc_tile[warp][st][lane] = sc;
+        const uint32_t dst = wbase_s + st * F::kStage;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {  // kT * NC chunks over 32 lanes, K and V
+            const int x = lane + 32 * i, j = x / NC, ch = x - j * NC;
+            const int64_t o = __shfl_sync(kFull, off, j);
+            const uint32_t d = dst + j * HD + ((ch ^ F::swz(j)) << 4), n = o >= 0 ? 16u : 0u;
+            cp_async16z(d, kp + (o >= 0 ? o + 16 * ch : 0), n);
+            cp_async16z(d + kT * HD, vp + (o >= 0 ? o + 16 * ch : 0), n);
+        }
+    };
+    if (0 < my_n) load_tile(0, 0);
+    cp_async_commit();
+
+    // Q^T fragments: pair x's pieces in columns 2c, 2c + 1 of n-tile x / 4.  As
+    // a B fragment lane 4g + c holds column g = pair g / 2, piece g % 2, dims
+    // 16s + 4c + (0, 1 | 2, 3) (the order in which ldmatrix hands out a row's
+    // bytes).  Each pair is scaled by a power of two that puts its largest
+    // entry into [2^14, 2^15).
+    uint32_t qf[NB][NC][2];
+    float qinv[NB];  // of this lane's own pair, 4 * nb + c
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const int x = 4 * nb + (g >> 1), qi = x / gb, hi = x - qi * gb;
+        const bool on = qi < nq && hi < nh;
+        const float *row = a.Q + static_cast<size_t>(rd.q_row0 + u.qi + (on ? qi : 0)) * (a.n_heads * HD) +
+                           static_cast<size_t>(h0 + (on ? hi : 0)) * HD;
+        float v[NC][4], mx = 0.f;
+#pragma unroll
+        for (int s = 0; s < NC; ++s) {
+            const float4 t = on ? __ldg(reinterpret_cast<const float4 *>(row + 16 * s + 4 * c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[s][0] = t.x * a.scale_log2, v[s][1] = t.y * a.scale_log2;
+            v[s][2] = t.z * a.scale_log2, v[s][3] = t.w * a.scale_log2;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(v[s][i]));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+        int e = 0;
+        if (mx > 0.f && mx <= 3.4e38f)
+            e = max(-126, min(126, 14 - (static_cast<int>((__float_as_uint(mx) >> 23) & 255u) - 127)));
+        const float up = pow2f(e);
+        qinv[nb] = __shfl_sync(kFull, pow2f(-e), 8 * c);  // lane 8c holds columns of pair c
+#pragma unroll
+        for (int s = 0; s < NC; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t p0 = pieces2(v[s][2 * i] * up), p1 = pieces2(v[s][2 * i + 1] * up);
+                qf[nb][s][i] = __byte_perm(p0, p1, (g & 1) ? 0x7632 : 0x5410);  // this column's piece of both dims
+            }
+    }
+
+    // ldmatrix addresses of this lane: matrix mi = lane / 8, row mr of it
+    //   K: keys 8 (mi & 1) + mr, chunk + (mi >> 1);  V (transposed): the same
+    const int mi = lane >> 3, mr = lane & 7, key_of = 8 * (mi & 1) + mr, ch_of = mi >> 1;
+
+    float m_run[NB], l_run[NB], o[NB][NC][4];
+    int c_exp = 0, c_top = -126;  // O holds 2^-c_exp times the sum (and kWScale); c_top: the largest exponent seen
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        m_run[nb] = -INFINITY;
+        l_run[nb] = 0.f;
+#pragma unroll
+        for (int s = 0; s < NC; ++s) o[nb][s][0] = o[nb][s][1] = o[nb][s][2] = o[nb][s][3] = 0.f;
+    }
+    // keys that this lane's pairs see: below lim
+    int lim[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const int qi = (4 * nb + c) / gb;
+        lim[nb] = a.causal ? min(kend, rd.past_len + u.qi + min(qi, nq - 1) + 1) : kend;
+    }
+
+    for (int k = 0; k < my_n; ++k) {
+        if (k + 1 < my_n) load_tile(k + 1, (k + 1) % kStages);
+        cp_async_commit();
+        cp_async_wait<1>();
+        __syncwarp();
+        const int st = k % kStages, pos0 = kbeg + (warp + k * kW) * kT;
+        const uint32_t Ks = wbase_s + st * F::kStage, Vs = Ks + kT * HD;
+
+        float sv[NB][4];  // scores of keys g, g + 8, g + 16, g + 24
+#pragma unroll
+        for (int kg = 0; kg < 2; ++kg) {
+            float acc[NB][4];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) acc[nb][0] = acc[nb][1] = acc[nb][2] = acc[nb][3] = 0.f;
+            const int key = 16 * kg + key_of;
+            const uint32_t row = Ks + key * HD;
+#pragma unroll
+            for (int s = 0; s < NC; s += 2) {
+                uint32_t r[4];
+                // the last pair of an odd chunk count reads the last chunk twice
+                const int ch = min(s + ch_of, NC - 1);
+                ldsm4(r, row + ((ch ^ F::swz(key)) << 4));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (s + h >= NC) continue;
+                    const uint32_t af[4] = {widen2<0x4140>(r[2 * h]), widen2<0x4140>(r[2 * h + 1]),
+                                            widen2<0x4342>(r[2 * h]), widen2<0x4342>(r[2 * h + 1])};
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) mma_f16(acc[nb], af, qf[nb][s + h][0], qf[nb][s + h][1]);
+                }
+            }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                sv[nb][2 * kg] = acc[nb][0] + acc[nb][1];
+                sv[nb][2 * kg + 1] = acc[nb][2] + acc[nb][3];
+            }
+        }
+        // scales and mask; the maximum's move, when some lane asks for it
+        float vsc[4];
+        bool grow = false;
+        float es = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 sc = sc_tile[warp][st][g + 8 * i];
+            vsc[i] = sc.y;
+            es = fmaxf(es, sc.y);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const float x = sv[nb][i] * (qinv[nb] * sc.x);
+                sv[nb][i] = pos0 + g + 8 * i < lim[nb] ? x : -INFINITY;
+                grow = grow || sv[nb][i] > m_run[nb] + kGrowQ;
+            }
+        }
+        // the tile's largest V scale (a power of two, the same in every lane)
+        const int e_tile = static_cast<int>(__reduce_max_sync(kFull, __float_as_uint(es) >> 23)) - 127;
+        c_top = max(c_top, e_tile);
+        const int want = max(e_tile, c_top - 60);  // O keeps within f32 when c goes down
+        const bool first = k == 0;
+        const bool move_c = first || want > c_exp || want < c_exp - 6;
+        if (move_c || __any_sync(kFull, grow)) {
+            const int c_new = move_c ? max(want, -126) : c_exp;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                float top = fmaxf(fmaxf(sv[nb][0], sv[nb][1]), fmaxf(sv[nb][2], sv[nb][3]));
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
+                const float mn = top > m_run[nb] + kGrowQ || m_run[nb] == -INFINITY ? top : m_run[nb];
+                const float al = mn == m_run[nb] || m_run[nb] == -INFINITY ? 1.f : ex2f(m_run[nb] - mn);
+                m_run[nb] = mn;
+                l_run[nb] *= al;
+                if (!first) {
+                    // a lane's accumulators belong to pair c's columns
+                    const int d = c_exp - c_new;  // two exact steps
+                    const float f1 = pow2f(d / 2), f2 = pow2f(d - d / 2) * al;
+#pragma unroll
+                    for (int s = 0; s < NC; ++s)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[nb][s][i] = o[nb][s][i] * f1 * f2;
+                }
+            }
+            c_exp = c_new;
+        }
+        // W, its pieces transposed into B fragments: bf[nb][kg] = keys 16 kg + (0-7 | 8-15)
+        uint32_t bf[NB][4];
+        const float down = pow2f(-c_exp);  // c_exp in [-126, 122]
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float vw = vsc[i] * down * kWScale;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                const float p = ex2f(sv[nb][i] - (m_run[nb] == -INFINITY ? 0.f : m_run[nb]));
+                l_run[nb] += p;
+                bf[nb][i] = transpose8(pieces2(sv[nb][i] == -INFINITY ? 0.f : p * vw));
+            }
+        }
+        // O^T += (U_V - 128)^T W^T
+#pragma unroll
+        for (int kg = 0; kg < 2; ++kg) {
+            const int key = 16 * kg + key_of;
+            const uint32_t row = Vs + key * HD;
+#pragma unroll
+            for (int s = 0; s < NC; s += 2) {
+                uint32_t r[4];
+                const int ch = min(s + ch_of, NC - 1);
+                ldsm4t(r, row + ((ch ^ F::swz(key)) << 4));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (s + h >= NC) continue;
+                    // rows 0-7: the chunk's even dims, rows 8-15: its odd dims
+                    const uint32_t af[4] = {widen2<0x4240>(r[2 * h]), widen2<0x4341>(r[2 * h]),
+                                            widen2<0x4240>(r[2 * h + 1]), widen2<0x4341>(r[2 * h + 1])};
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) mma_f16(o[nb][s + h], af, bf[nb][2 * kg], bf[nb][2 * kg + 1]);
+                }
+            }
+        }
+        __syncwarp();
+    }
+    cp_async_wait<0>();
+    __syncthreads();  // every warp is done with its stages
+
+    // publish each warp's (O, m, l), pair by pair: O[pair][dim] behind one another
+    constexpr int NP = 4 * NB;
+    float *R = reinterpret_cast<float *>(smem) + warp * NP * (HD + 2);
+    const float o1 = pow2f(c_exp / 2) * (1.f / kWScale), o2 = pow2f(c_exp - c_exp / 2);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        float l = l_run[nb];
+        l += __shfl_xor_sync(kFull, l, 4);
+        l += __shfl_xor_sync(kFull, l, 8);
+        l += __shfl_xor_sync(kFull, l, 16);
+        float *Rp = R + (4 * nb + c) * (HD + 2);
+#pragma unroll
+        for (int s = 0; s < NC; ++s) {
+            Rp[16 * s + 2 * g] = (o[nb][s][0] + o[nb][s][1]) * o1 * o2;
+            Rp[16 * s + 2 * g + 1] = (o[nb][s][2] + o[nb][s][3]) * o1 * o2;
+        }
+        if (g == 0) {
+            Rp[HD] = m_run[nb];
+            Rp[HD + 1] = l;
+        }
+    }
+    __syncthreads();
+    for (int x = warp; x < NP; x += kW) {  // warp per pair
+        const int qi = x / gb, hi = x - qi * gb;
+        if (qi >= nq || hi >= nh) continue;
+        const float *R0 = reinterpret_cast<const float *>(smem) + x * (HD + 2);
+        float M = -INFINITY, den = 0.f, wt[kW];
+#pragma unroll
+        for (int w = 0; w < kW; ++w) M = fmaxf(M, R0[w * NP * (HD + 2) + HD]);
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+            // a warp that saw no key of the pair has l = 0 (one that saw only NaN
+            // scores has no maximum either, and l = NaN)
+            const float mw = R0[w * NP * (HD + 2) + HD], lw = R0[w * NP * (HD + 2) + HD + 1];
+            wt[w] = lw == 0.f ? 0.f : mw == -INFINITY ? 1.f : exp2f(mw - M);
+            if (wt[w] != 0.f) den = fmaf(wt[w], lw, den);
+        }
+        const int h = h0 + hi;
+        const size_t ph = u.item < 0 ? 0 : static_cast<size_t>(a.merges[u.item + qi].part0 + u.split) * a.n_heads + h;
+        float *dst = u.item < 0 ? a.out + static_cast<size_t>(rd.q_row0 + u.qi + qi) * (a.n_heads * HD) + static_cast<size_t>(h) * HD
+                                : a.pacc + ph * HD;
+        for (int d = lane; d < HD; d += 32) {
+            float num = 0.f;
+#pragma unroll
+            for (int w = 0; w < kW; ++w) {
+                const float *Rw = R0 + w * NP * (HD + 2);
+                if (wt[w] != 0.f) num = fmaf(wt[w], Rw[d], num);
+            }
+            dst[d] = u.item < 0 ? num / den : num;
+        }
+        if (u.item >= 0 && lane == 0) {
+            a.pm[ph] = M;
+            a.pl[ph] = den;
+        }
+    }
+}
+
+template <int HD, int NB>
+cudaError_t launch_fast(const AttnArgs &a, const Q8Addr &q, int gb, int qb, cudaStream_t s) {
+    using F = FastQ8<HD>;
+    constexpr size_t smem = static_cast<size_t>(kW) * kStages * F::kStage;
+    static_assert(smem >= static_cast<size_t>(kW) * 4 * NB * (HD + 2) * sizeof(float), "the merge fits the stages");
+    static PerDeviceOnce configured;  // the attribute is per function and device
+    const cudaError_t ce = configured.run([&]() -> cudaError_t {
+        return cudaFuncSetAttribute(decode_q8_kernel<HD, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(smem));
+    });
+    if (ce != cudaSuccess) return ce;
+    const long long grid = static_cast<long long>(a.n_units) * a.n_kv * ((a.group + gb - 1) / gb);
+    if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    decode_q8_kernel<HD, NB><<<static_cast<unsigned>(grid), 32 * kW, smem, s>>>(a, q, gb, qb);
+    return cudaGetLastError();
+}
+
+// Heads per CTA and queries per unit: up to 16 (query, head) pairs share a
+// unit's keys.  A group of more than 16 heads is cut into blocks of 16.
+bool fast_shape(int head_dim) { return head_dim % 16 == 0 && head_dim <= 128; }
+int heads_per_block(int group) { return group < 16 ? group : 16; }
+
+template <int HD>
+cudaError_t launch_fast_hd(const AttnArgs &a, const Q8Addr &q, cudaStream_t s) {
+    const int gb = heads_per_block(a.group), qb = q8_query_block(a.hd, a.group);
+    // the widest unit of the call decides; a unit of fewer pairs leaves columns idle
+    const int pairs = gb * std::min(qb, a.max_q);
+    if (pairs <= 4) return launch_fast<HD, 1>(a, q, gb, qb, s);
+    if (pairs <= 8) return launch_fast<HD, 2>(a, q, gb, qb, s);
+    return launch_fast<HD, 4>(a, q, gb, qb, s);
+}
+
 // -------------------------------------------------------------- split pass ----
 //
 // Operand images for the tensor-core launches (the layout of kImageBytes): one
@@ -247,9 +664,23 @@ __global__ void __launch_bounds__(256) split_q8_kernel(SplitArgs p, Q8Addr q) {
 
 }  // namespace
 
-int q8_query_block(int, int) { return 1; }
+int q8_query_block(int head_dim, int group) {
+    return fast_shape(head_dim) ? std::max(1, 16 / heads_per_block(group)) : 1;
+}
 
-cudaError_t launch_decode_q8(const AttnArgs &a, const Q8Addr &q, cudaStream_t s) { return launch_generic(a, q, s); }
+cudaError_t launch_decode_q8(const AttnArgs &a, const Q8Addr &q, cudaStream_t s) {
+    switch (fast_shape(a.hd) ? a.hd : 0) {
+        case 16: return launch_fast_hd<16>(a, q, s);
+        case 32: return launch_fast_hd<32>(a, q, s);
+        case 48: return launch_fast_hd<48>(a, q, s);
+        case 64: return launch_fast_hd<64>(a, q, s);
+        case 80: return launch_fast_hd<80>(a, q, s);
+        case 96: return launch_fast_hd<96>(a, q, s);
+        case 112: return launch_fast_hd<112>(a, q, s);
+        case 128: return launch_fast_hd<128>(a, q, s);
+        default: return launch_generic(a, q, s);
+    }
+}
 
 cudaError_t launch_split_q8(const SplitArgs &a, const Q8Addr &q, cudaStream_t s) {
     constexpr size_t smem = static_cast<size_t>(kKeyTile) * (kHDI + 1) * sizeof(float);
