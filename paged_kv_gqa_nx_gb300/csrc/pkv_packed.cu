@@ -96,6 +96,29 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *map, 
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(mbar)
         : "memory");
 }
+// Bounded wait of the calling thread for the phase of the given parity: the
+// clock is not read before the wait has gone on for a while (that read is
+// slower than a whole uncontended wait).
+__device__ __forceinline__ bool wait_phase(uint32_t mbar, uint32_t parity) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 0; it < (1u << 26); ++it) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(done)
+            : "r"(mbar), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if ((it & 255u) == 255u) {
+            const uint64_t t = globaltimer_ns();
+            if (t0 == 0) t0 = t;
+            else if (t - t0 > 1000000000ull) return false;
+        }
+    }
+    return false;
+}
 __device__ __forceinline__ float ex2(float x) {  // 2^x to about 2^-22 relative; 0 for -inf
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -128,6 +151,59 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
     asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
     return r;
 }
+// Columns x0 .. x0 + 31 of this thread's lane, issued without a wait; the
+// registers belong to the load until tmem_ld_done has passed over them.
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tie32(uint32_t *r) {
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&r)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; i += 32) tie32(r + i);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// pairs of f32 in one instruction: a * b + c, and a + b
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(f.x), "=f"(f.y) : "l"(x));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 // Shared-memory matrix descriptor of a V tile, MN-major with 128-byte swizzle:
 // 64 columns of a key in 128 bytes, 8 keys 1024 bytes apart (stride offset),
 // the next 64 columns kBlock bytes on (leading offset).
@@ -158,7 +234,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     unsigned char *sm = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smraw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *ring = sm + 2 * C::kTile;  // Q_c at c * kTile
-    __shared__ uint64_t bar_full[NS], bar_free[NS], bar_q, bar_s[2], bar_p[2], bar_o[2], bar_look[2], bar_go[2];
+    __shared__ uint64_t bar_full[NS], bar_free[NS], bar_q, bar_s[2], bar_p[2], bar_o[2], bar_look[2], bar_go[2], bar_turn[2];
     __shared__ uint32_t tslot, dirty[2], held[2];  // held[c]: O_c already holds something before PV(0)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -177,8 +253,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // tiles from this one on hold a key that some row does not see
     const int look0 = a.causal ? q0 / kKeys : len / kKeys;
 
-    auto wait_w = [&](uint64_t *bar, uint32_t parity) {  // lane 0 waits (bounded), the warp learns the outcome
-        return __shfl_sync(0xffffffffu, lane == 0 ? mbar_wait(smem_u32(bar), parity) : true, 0) != 0;
+    auto wait_w = [&](uint64_t *bar, uint32_t parity) {  // bounded; the warp agrees on the outcome
+        return __all_sync(0xffffffffu, wait_phase(smem_u32(bar), parity)) != 0;
     };
     auto rph = [](int i) { return static_cast<uint32_t>(i / NS) & 1u; };  // ring item i: slot i % NS
 
@@ -194,7 +270,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_init(smem_u32(&bar_q), 1);
         for (int c = 0; c < 2; ++c) {
             mbar_init(smem_u32(&bar_s[c]), 1);
-            mbar_init(smem_u32(&bar_p[c]), 4);
+            mbar_init(smem_u32(&bar_p[c]), 4);  // the chain's four compute warps
+            mbar_init(smem_u32(&bar_turn[c]), 1);
             mbar_init(smem_u32(&bar_o[c]), 1);
             mbar_init(smem_u32(&bar_look[c]), 1);
             mbar_init(smem_u32(&bar_go[c]), 1);
@@ -245,22 +322,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int i = 2 * j + 1, sl = i % NS;
                 ok = wait_w(&bar_go[(j - look0) & 1], 0) && wait_w(&bar_full[sl], rph(i));
                 if (!ok) break;
+                // keys up to key0 of the tile are seen by every row; of each 64
+                // columns, a key's 128 bytes are 8 chunks
                 uint4 *v = reinterpret_cast<uint4 *>(ring + sl * C::kTile);
-                bool found = false;
-                for (int x = lane; x < static_cast<int>(C::kTile / 16); x += 32) {
-                    uint4 w = v[x];
-                    uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                    bool any = false;
+                const int key0 = max(0, (a.causal ? q0 + 1 : len) - j * kKeys);
+                constexpr uint32_t kE = std::is_same<T, bf16>::value ? 0x7f807f80u : 0x7c007c00u;
+                constexpr uint32_t kOne = std::is_same<T, bf16>::value ? 0x00800080u : 0x04000400u;
+                uint32_t seen = 0;  // a half's exponent is all ones where adding one to it reaches the sign bit
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (not_finite<T>(u[k])) u[k] &= 0xffff0000u, any = true;
-                        if (not_finite<T>(u[k] >> 16)) u[k] &= 0xffffu, any = true;
+                for (int cb = 0; cb < D / 64; ++cb) {
+#pragma unroll 8
+                    for (int x = cb * 1024 + key0 * 8 + lane; x < (cb + 1) * 1024; x += 32) {
+                        const uint4 w = v[x];
+                        seen |= ((w.x & kE) + kOne) | ((w.y & kE) + kOne) | ((w.z & kE) + kOne) | ((w.w & kE) + kOne);
                     }
-                    if (any) v[x] = make_uint4(u[0], u[1], u[2], u[3]);
-                    found = found || any;
+                }
+                const bool found = __any_sync(0xffffffffu, (seen & 0x80008000u) != 0);
+                if (found) {
+                    for (int x = lane; x < static_cast<int>(C::kTile / 16); x += 32) {
+                        const uint4 w = v[x];
+                        uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (not_finite<T>(u[k])) u[k] &= 0xffff0000u;
+                            if (not_finite<T>(u[k] >> 16)) u[k] &= 0xffffu;
+                        }
+                        v[x] = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
                 }
                 fence_proxy_async();  // before the MMAs read the tile
-                found = __any_sync(0xffffffffu, found);
+                __syncwarp();
                 if (lane == 0) {
                     if (found) dirty[(j - look0) & 1] = 1;
                     mbar_arrive(smem_u32(&bar_look[(j - look0) & 1]));
@@ -299,6 +390,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ok = wait_w(&bar_full[sv], rph(iv));
                 if (ok && j >= look0) ok = wait_w(&bar_look[(j - look0) & 1], 0);
                 if (ok && j + 1 < n) ok = wait_w(&bar_full[(2 * j + 2) % NS], rph(2 * j + 2));
+                // this chain's turn: the other chain's products before these have
+                // been issued (chain 0's of tile j, chain 1's of tile j - 1)
+                if (ok && (c ? j < n0 : j > 0 && j - 1 < n1)) ok = wait_w(&bar_turn[c], c ? j & 1 : (j - 1) & 1);
                 if (ok) ok = wait_w(&bar_p[c], j & 1);
                 if (!ok) break;
                 fence_after_sync();
@@ -313,6 +407,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 __syncwarp();
                 if (j + 1 < n) qk(j + 1);
+                if (lane == 0) mbar_arrive(smem_u32(&bar_turn[c ^ 1]));
+                __syncwarp();
             }
             // items past the chain's last tile are free as far as this chain goes
             // (counted once they have landed, so that each counts for its own phase)
@@ -337,24 +433,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             ok = wait_w(&bar_s[c], j & 1);
             if (!ok) break;
             fence_after_sync();
-            float x[kKeys];
+            uint32_t x[kKeys];  // the row's scores (f32 bits)
 #pragma unroll
-            for (int i = 0; i < kKeys / 32; ++i) {
-                float h[32];
-                tmem_ld32(tS + 32 * i, h);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) x[32 * i + k] = h[k];
-            }
+            for (int i = 0; i < kKeys; i += 32) tmem_ld32_issue(tS + i, x + i);
+            tmem_ld_done(x);
+            auto xf = [&](int i) { return __uint_as_float(x[i]); };
             const int base = j * kKeys;
             if (base + kKeys > lim) {
 #pragma unroll
-                for (int i = 0; i < kKeys; ++i) x[i] = base + i < lim ? x[i] : -INFINITY;
+                for (int i = 0; i < kKeys; ++i) x[i] = base + i < lim ? x[i] : 0xff800000u;
             }
             float mx[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mx[i] = x[i];
+            for (int i = 0; i < 4; ++i) mx[i] = fmaxf(xf(2 * i), xf(2 * i + 1));
 #pragma unroll
-            for (int i = 4; i < kKeys; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+            for (int i = 8; i < kKeys; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], xf(i), xf(i + 1));
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs;
             const bool move = top > m_ref + kGrow || m_ref == -INFINITY;
             const float m_use = move ? top : m_ref;
@@ -372,20 +465,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
             m_ref = m_use;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            // P over S
+            uint64_t sum[2] = {0, 0};
+            const uint64_t cs2 = pair(cs, cs), nm2 = pair(nm, nm);
 #pragma unroll
-            for (int i = 0; i < kKeys / 64; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 uint32_t p[32];
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
-                    const float p0 = ex2(fmaf(x[64 * i + 2 * k], cs, nm)), p1 = ex2(fmaf(x[64 * i + 2 * k + 1], cs, nm));
-                    sum[2 * (k & 1)] += p0;
-                    sum[2 * (k & 1) + 1] += p1;
+                    const float2 e = unpair(fma2(pair(xf(64 * i + 2 * k), xf(64 * i + 2 * k + 1)), cs2, nm2));
+                    const float p0 = ex2(e.x), p1 = ex2(e.y);
+                    sum[k & 1] = add2(sum[k & 1], pair(p0, p1));
                     p[k] = pack2(T{}, p0, p1);
                 }
                 tmem_st32u(tS + 32 * i, p);
             }
-            l_run = fmaf(l_run, f, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+            const float2 s2 = unpair(add2(sum[0], sum[1]));
+            l_run = fmaf(l_run, f, s2.x + s2.y);
             tmem_st_wait();
             if (j >= look0) {
                 ok = wait_w(&bar_look[(j - look0) & 1], 0);
