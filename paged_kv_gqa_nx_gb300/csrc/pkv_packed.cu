@@ -56,11 +56,12 @@ __device__ __forceinline__ int seq_of_tile(const PackedSeqs<N> &l, int t) {
 //                                  B from shared memory (V as stored: MN-major)
 //
 // Warps 8 and 10 issue chain 0's and chain 1's MMAs, warp 9 the TMA loads
-// (Q once; K_0, V_0, K_1, ... through a ring of slots), warp 11 looks over the
-// V tiles that a query does not see whole.  A chain runs QK(j), softmax(j),
-// PV(j) and QK(j + 1) back to back; while one chain's softmax runs, the tensor
-// core works on the other's products.  P of tile j is read by PV(j) before
-// QK(j + 1), issued by the same thread, writes over it.
+// (Q once; K_0, V_0, K_1, ... through a ring of slots).  A chain runs QK(j),
+// softmax(j), PV(j) and QK(j + 1) back to back; while one chain's softmax runs,
+// the tensor core works on the other's products.  The issuing warps take turns:
+// without turns the core interleaved both chains' MMAs, so both softmaxes ran
+// at once and then both waited.  P of tile j is read by PV(j) before QK(j + 1),
+// issued by the same thread, writes over it.
 //
 // Probabilities are rounded to the operand type (half a step, 2^-9 or 2^-12
 // relative to p, against outputs of the same type); sums use them unrounded.
@@ -69,16 +70,20 @@ __device__ __forceinline__ int seq_of_tile(const PackedSeqs<N> &l, int t) {
 //
 // A zero probability times an infinity is NaN, so V rows behind a sequence's
 // end or in a query's future must not hold one: on the (at most two) tiles
-// that some row of the CTA does not see whole, warp 11 replaces values that
-// are not finite by 0 and, where it found any, the compute threads add those
-// products for the keys that their row does see.
+// that some row of the CTA does not see whole, the compute threads of one chain
+// replace values that are not finite by 0 and, where they found any, every
+// thread adds those products for the keys that its row does see.
 constexpr int kKeys = 128;  // keys per tile
 constexpr int kTcThreads = 384;
-constexpr int kWarpMma0 = 8, kWarpLoad = 9, kWarpLook = 11;  // warp 10: chain 1's MMAs
+constexpr int kWarpMma0 = 8, kWarpLoad = 9, kWarpSpare = 11;  // warp 10: chain 1's MMAs
 // registers per thread: at launch, then of warps 8-11 and of the compute warps
 constexpr int kTcLaunchRegs = 168, kTcOtherRegs = 88, kTcComputeRegs = 208;
 static_assert(256 * kTcComputeRegs + 128 * kTcOtherRegs <= kTcThreads * kTcLaunchRegs, "register split");
 constexpr uint32_t kTcCols = 512;           // O_c at c * 128, S_c / P_c at 256 + c * 128
+#ifndef PASS_LEFT
+#define PASS_LEFT 2
+#endif
+constexpr int kPassLeft = PASS_LEFT;
 constexpr float kGrow = 8.f;                // log2 headroom of the reference maximum
 
 template <int D>
@@ -234,7 +239,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     unsigned char *sm = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smraw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *ring = sm + 2 * C::kTile;  // Q_c at c * kTile
-    __shared__ uint64_t bar_full[NS], bar_free[NS], bar_q, bar_s[2], bar_p[2], bar_o[2], bar_look[2], bar_go[2], bar_turn[2];
+    __shared__ uint64_t bar_full[NS], bar_free[NS], bar_q, bar_s[2], bar_p[2], bar_o[2], bar_look[2], bar_go[2];
     __shared__ uint32_t tslot, dirty[2], held[2];  // held[c]: O_c already holds something before PV(0)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -270,10 +275,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_init(smem_u32(&bar_q), 1);
         for (int c = 0; c < 2; ++c) {
             mbar_init(smem_u32(&bar_s[c]), 1);
-            mbar_init(smem_u32(&bar_p[c]), 4);  // the chain's four compute warps
-            mbar_init(smem_u32(&bar_turn[c]), 1);
+            mbar_init(smem_u32(&bar_p[c]), 5);  // the chain's four compute warps, and its turn
             mbar_init(smem_u32(&bar_o[c]), 1);
-            mbar_init(smem_u32(&bar_look[c]), 1);
+            mbar_init(smem_u32(&bar_look[c]), 4);  // the looking chain's compute warps
             mbar_init(smem_u32(&bar_go[c]), 1);
             dirty[c] = 0;
             held[c] = 0;
@@ -314,57 +318,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // the last copies land before the CTA's shared memory is given up (bounded)
             wait_w(&bar_q, 0);
             for (int i = max(0, issued - NS); i < issued; ++i) wait_w(&bar_full[i % NS], rph(i));
-        } else if (warp == kWarpLook) {
-            // ---------------- values that are not finite in partly seen V tiles ----------------
-            for (int j = look0; j < n_max && ok; ++j) {
-                // this warp follows no earlier item, so it learns from the loading warp
-                // that the slot is at item i before it looks at the slot's phase
-                const int i = 2 * j + 1, sl = i % NS;
-                ok = wait_w(&bar_go[(j - look0) & 1], 0) && wait_w(&bar_full[sl], rph(i));
-                if (!ok) break;
-                // keys up to key0 of the tile are seen by every row; of each 64
-                // columns, a key's 128 bytes are 8 chunks
-                uint4 *v = reinterpret_cast<uint4 *>(ring + sl * C::kTile);
-                const int key0 = max(0, (a.causal ? q0 + 1 : len) - j * kKeys);
-                constexpr uint32_t kE = std::is_same<T, bf16>::value ? 0x7f807f80u : 0x7c007c00u;
-                constexpr uint32_t kOne = std::is_same<T, bf16>::value ? 0x00800080u : 0x04000400u;
-                uint32_t seen = 0;  // a half's exponent is all ones where adding one to it reaches the sign bit
-#pragma unroll
-                for (int cb = 0; cb < D / 64; ++cb) {
-#pragma unroll 8
-                    for (int x = cb * 1024 + key0 * 8 + lane; x < (cb + 1) * 1024; x += 32) {
-                        const uint4 w = v[x];
-                        seen |= ((w.x & kE) + kOne) | ((w.y & kE) + kOne) | ((w.z & kE) + kOne) | ((w.w & kE) + kOne);
-                    }
-                }
-                const bool found = __any_sync(0xffffffffu, (seen & 0x80008000u) != 0);
-                if (found) {
-                    for (int x = lane; x < static_cast<int>(C::kTile / 16); x += 32) {
-                        const uint4 w = v[x];
-                        uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if (not_finite<T>(u[k])) u[k] &= 0xffff0000u;
-                            if (not_finite<T>(u[k] >> 16)) u[k] &= 0xffffu;
-                        }
-                        v[x] = make_uint4(u[0], u[1], u[2], u[3]);
-                    }
-                }
-                fence_proxy_async();  // before the MMAs read the tile
-                __syncwarp();
-                if (lane == 0) {
-                    if (found) dirty[(j - look0) & 1] = 1;
-                    mbar_arrive(smem_u32(&bar_look[(j - look0) & 1]));
-                }
-                __syncwarp();
-            }
-            if (!ok && lane == 0 && a.err) atomicOr(a.err, 2);
+        } else if (warp == kWarpSpare) {
+            // nothing to do
         } else {
             // ---------------- MMA issue: chain c (lane 0) ----------------
             const int c = warp == kWarpMma0 ? 0 : 1, n = c ? n1 : n0;
             const uint32_t tS = tbase + 256 + 128 * c, tO = tbase + 128 * c;
             const uint64_t dQ = desc_sw128(smem_u32(sm + c * C::kTile));
-            auto qk = [&](int j) {  // S_c = Q_c K_j^T, then the slot's and the scores' barriers
+            // S_c = Q_c K_j^T, then the slot's and the scores' barriers; on the way
+            // the turn passes to the other chain, whose issuing warp needs a while
+            // to see it
+            auto qk = [&](int j, bool pass) {
                 const int sl = (2 * j) % NS;
                 const uint64_t dK = desc_sw128(smem_u32(ring + sl * C::kTile));
                 if (lane == 0) {
@@ -372,6 +336,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int k = 0; k < D / 16; ++k) {
                         const uint64_t o = ((k >> 2) * C::kBlock + (k & 3) * 32u) >> 4;
                         mma_f16(tS, dQ + o, dK + o, idesc16<T>(kKeys, false), k > 0);
+                        if (k == D / 16 - kPassLeft && pass) mbar_arrive(smem_u32(&bar_p[c ^ 1]));
                     }
                     mma_commit(smem_u32(&bar_s[c]));
                     mma_commit(smem_u32(&bar_free[sl]));
@@ -382,7 +347,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ok = wait_w(&bar_q, 0) && wait_w(&bar_full[0], 0);
                 if (ok) {
                     fence_after_sync();
-                    qk(0);
+                    qk(0, false);
                 }
             }
             for (int j = 0; j < n && ok; ++j) {
@@ -390,9 +355,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ok = wait_w(&bar_full[sv], rph(iv));
                 if (ok && j >= look0) ok = wait_w(&bar_look[(j - look0) & 1], 0);
                 if (ok && j + 1 < n) ok = wait_w(&bar_full[(2 * j + 2) % NS], rph(2 * j + 2));
-                // this chain's turn: the other chain's products before these have
-                // been issued (chain 0's of tile j, chain 1's of tile j - 1)
-                if (ok && (c ? j < n0 : j > 0 && j - 1 < n1)) ok = wait_w(&bar_turn[c], c ? j & 1 : (j - 1) & 1);
+                // P, and this chain's turn: the other chain's products before these
+                // (chain 0's of tile j, chain 1's of tile j - 1), or the most of
+                // them, have been issued; a chain without such products takes it
+                if (lane == 0 && !(c ? j < n0 : j > 0 && j - 1 < n1)) mbar_arrive(smem_u32(&bar_p[c]));
                 if (ok) ok = wait_w(&bar_p[c], j & 1);
                 if (!ok) break;
                 fence_after_sync();
@@ -406,8 +372,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (j + 1 == n) mma_commit(smem_u32(&bar_o[c]));
                 }
                 __syncwarp();
-                if (j + 1 < n) qk(j + 1);
-                if (lane == 0) mbar_arrive(smem_u32(&bar_turn[c ^ 1]));
+                const bool pass = c ? j + 1 < n0 : j < n1;  // the other chain's products follow
+                if (j + 1 < n) qk(j + 1, pass);
+                else if (pass && lane == 0) mbar_arrive(smem_u32(&bar_p[c ^ 1]));
                 __syncwarp();
             }
             // items past the chain's last tile are free as far as this chain goes
@@ -430,6 +397,44 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float cs = a.scale_log2;  // > 0
         float m_ref = -INFINITY, l_run = 0.f;
         for (int j = 0; j < n; ++j) {
+            if (j >= look0 && (c == 1 || j >= n1)) {
+                // this chain looks over V_j: keys up to key0 are seen by every row; a
+                // key's 128 bytes of each 64 columns are 8 chunks.  (The loading warp
+                // tells when the slot is at V_j: these warps follow no earlier item.)
+                const int i = 2 * j + 1, sl = i % NS, w = (j - look0) & 1;
+                ok = wait_w(&bar_go[w], 0) && wait_w(&bar_full[sl], rph(i));
+                if (!ok) break;
+                uint4 *v = reinterpret_cast<uint4 *>(ring + sl * C::kTile);
+                const int key0 = max(0, (a.causal ? q0 + 1 : len) - j * kKeys);
+                constexpr uint32_t kE = std::is_same<T, bf16>::value ? 0x7f807f80u : 0x7c007c00u;
+                constexpr uint32_t kOne = std::is_same<T, bf16>::value ? 0x00800080u : 0x04000400u;
+                uint32_t seen = 0;  // a half's exponent is all ones where adding one to it reaches the sign bit
+#pragma unroll
+                for (int x0 = 0; x0 < static_cast<int>(C::kTile / 16); x0 += 128) {
+                    const int x = x0 + m;
+                    if ((x & 1023) >= key0 * 8) {
+                        const uint4 y = v[x];
+                        seen |= ((y.x & kE) + kOne) | ((y.y & kE) + kOne) | ((y.z & kE) + kOne) | ((y.w & kE) + kOne);
+                    }
+                }
+                if (seen & 0x80008000u) {
+                    for (int x = m; x < static_cast<int>(C::kTile / 16); x += 128) {
+                        if ((x & 1023) < key0 * 8) continue;
+                        const uint4 y = v[x];
+                        uint32_t u[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (not_finite<T>(u[k])) u[k] &= 0xffff0000u;
+                            if (not_finite<T>(u[k] >> 16)) u[k] &= 0xffffu;
+                        }
+                        v[x] = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                    *static_cast<volatile uint32_t *>(&dirty[w]) = 1;
+                }
+                fence_proxy_async();  // before the MMAs read the tile
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar_look[w]));
+            }
             ok = wait_w(&bar_s[c], j & 1);
             if (!ok) break;
             fence_after_sync();
