@@ -129,6 +129,7 @@ struct PackedArgs {
     int64_t n_tokens;          // rows of Q, K, V and out that belong to some sequence (from row 0)
     Elem type;
     int32_t *err;
+    int32_t out32 = 0;         // out's rows and heads start on 32-byte boundaries (set by the launcher)
 };
 
 // Address of a key/value row in a contiguous history: base[pos][kv_head*hd ...]

@@ -44,8 +44,13 @@ __device__ __forceinline__ int seq_of_tile(const PackedSeqs<N> &l, int t) {
 
 // ------------------------------------------------------------ tensor cores ----
 //
-// One CTA = two tiles of 128 query rows of one sequence (two softmax chains
-// that share every K/V tile).  A tile is 128/P consecutive tokens x P heads of
+// A piece of work = two tiles of 128 query rows of one sequence (two softmax
+// chains that share every K/V tile).  The grid has a block per piece, and a
+// block that runs takes over further pieces from blocks that have not started
+// (the loading warp asks once a piece's last load is on its way), so that the loads of the next piece and its
+// first QK run under the last softmax and the output of this one: a block per
+// piece spent ~14,000 of ~29,000 clocks of an average piece of a ragged batch
+// outside its loop.  A tile is 128/P consecutive tokens x P heads of
 // one kv head, P the largest power of two (at most 16) that divides the group,
 // so the rows of a tile need the same keys and a causal tile's masked corner
 // is only 128/P tokens deep.  Row m of chain c is token m / P, head m % P, TMEM
@@ -80,10 +85,7 @@ constexpr int kWarpMma0 = 8, kWarpLoad = 9, kWarpSpare = 11;  // warp 10: chain 
 constexpr int kTcLaunchRegs = 168, kTcOtherRegs = 88, kTcComputeRegs = 208;
 static_assert(256 * kTcComputeRegs + 128 * kTcOtherRegs <= kTcThreads * kTcLaunchRegs, "register split");
 constexpr uint32_t kTcCols = 512;           // O_c at c * 128, S_c / P_c at 256 + c * 128
-#ifndef PASS_LEFT
-#define PASS_LEFT 2
-#endif
-constexpr int kPassLeft = PASS_LEFT;
+constexpr int kPassLeft = 2;                // MMAs of QK still to issue when the turn passes
 constexpr float kGrow = 8.f;                // log2 headroom of the reference maximum
 
 template <int D>
@@ -228,6 +230,67 @@ __host__ __device__ constexpr uint32_t idesc16(uint32_t n, bool b_mn) {
     return (1u << 4) | (f << 7) | (f << 10) | (b_mn ? 1u << 16 : 0u) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
+// Asks for the index of a block of this grid that has not started yet: if there
+// is one it will not start, and this block does its work.  The 16-byte answer
+// comes with 16 bytes of the barrier's transaction count.
+__device__ __forceinline__ void ask_work(uint32_t answer, uint32_t mbar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];\n" ::"r"(
+                     answer),
+                 "r"(mbar)
+                 : "memory");
+}
+// The answer: a block's index, or -1.
+__device__ __forceinline__ int work_of(uint32_t answer) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}\n"
+        : "=r"(got), "=r"(x)
+        : "r"(answer)
+        : "memory");
+    return got ? static_cast<int>(x) : -1;
+}
+
+// What block index w of the grid stands for.
+struct Piece {
+    int len, row0, q0, h0, kvh;  // sequence, first token of chain 0's tile, heads
+    int n0, n1, look0;           // key tiles of each chain; tiles from look0 on hold a key that some row does not see
+    __device__ __forceinline__ int n_max() const { return max(n0, n1); }
+    __device__ __forceinline__ int looks() const { return max(0, n_max() - look0); }
+};
+template <int N>
+__device__ __forceinline__ Piece piece_of(const PackedArgs &a, const PackedSeqs<N> &l, int log_p, int w) {
+    Piece p;
+    const int TQ = 128 >> log_p, n_ht = a.n_heads >> log_p;
+    const int t = w / n_ht, ht = w - t * n_ht, s = seq_of_tile(l, t);
+    p.len = l.len[s];
+    p.row0 = l.start[s];
+    // the last queries, which see the most keys, come first
+    p.q0 = (l.tile0[s + 1] - l.tile0[s] - 1 - (t - l.tile0[s])) * 2 * TQ;
+    p.h0 = ht << log_p;
+    p.kvh = p.h0 / (a.n_heads / a.n_kv);
+    const int kend0 = a.causal ? min(p.len, p.q0 + TQ) : p.len;
+    const int kend1 = p.q0 + TQ >= p.len ? 0 : a.causal ? min(p.len, p.q0 + 2 * TQ) : p.len;
+    p.n0 = (kend0 + kKeys - 1) / kKeys;
+    p.n1 = (kend1 + kKeys - 1) / kKeys;
+    p.look0 = a.causal ? p.q0 / kKeys : p.len / kKeys;
+    return p;
+}
+
+// Barriers.  Every role counts ring items (K_0, V_0, K_1, ... of one piece after
+// another; item i in slot i % NS), tiles of its chain, pieces of its chain and
+// looked-over tiles alike, and takes phases from those counts.
+//   full[slot] / free[slot]  item landed / both issuing warps' reads of it done
+//   q[c] / qfree[c]          Q_c landed / the piece's last QK_c done
+//   s[c]                     QK_c done: S_c readable
+//   p[c]                     P_c written (four warps) and the chain's turn (one)
+//   o[c] / ofree[c]          the piece's last PV_c done / O_c read (four warps)
+//   go[x], look[x]           V of a partly seen tile loaded / looked over
+//   work[x] / wfree[x]       answer there / read by the eleven working warps
 template <int D, class T, int N>
 __global__ void __launch_bounds__(kTcThreads, 1)
     packed_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -239,97 +302,130 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     unsigned char *sm = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smraw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *ring = sm + 2 * C::kTile;  // Q_c at c * kTile
-    __shared__ uint64_t bar_full[NS], bar_free[NS], bar_q, bar_s[2], bar_p[2], bar_o[2], bar_look[2], bar_go[2];
-    __shared__ uint32_t tslot, dirty[2], held[2];  // held[c]: O_c already holds something before PV(0)
+    __shared__ uint64_t bar_full[NS], bar_free[NS], bar_q[2], bar_qfree[2], bar_s[2], bar_p[2], bar_o[2], bar_ofree[2];
+    __shared__ uint64_t bar_go[4], bar_look[4], bar_work[2], bar_wfree[2];
+    __shared__ __align__(16) uint4 answer[2];
+    __shared__ uint32_t tslot, dirty[4], held[2];  // held[c]: O_c already holds something before PV(0)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int P = 1 << log_p, TQ = 128 >> log_p;
-    const int n_ht = a.n_heads >> log_p;
-    const int t = blockIdx.x / n_ht, ht = blockIdx.x - t * n_ht;
-    const int s = seq_of_tile(l, t);
-    const int len = l.len[s], row0 = l.start[s];
-    // the last queries, which see the most keys, come first
-    const int q0 = (l.tile0[s + 1] - l.tile0[s] - 1 - (t - l.tile0[s])) * 2 * TQ;
-    const int h0 = ht << log_p, kvh = h0 / (a.n_heads / a.n_kv);
-    const int kend0 = a.causal ? min(len, q0 + TQ) : len;
-    const int kend1 = q0 + TQ >= len ? 0 : a.causal ? min(len, q0 + 2 * TQ) : len;
-    const int n0 = (kend0 + kKeys - 1) / kKeys, n1 = (kend1 + kKeys - 1) / kKeys;
-    const int n_max = max(n0, n1);
-    // tiles from this one on hold a key that some row does not see
-    const int look0 = a.causal ? q0 / kKeys : len / kKeys;
-
     auto wait_w = [&](uint64_t *bar, uint32_t parity) {  // bounded; the warp agrees on the outcome
-        return __all_sync(0xffffffffu, wait_phase(smem_u32(bar), parity)) != 0;
+        return __all_sync(0xffffffffu, wait_phase(smem_u32(bar), parity & 1u)) != 0;
     };
-    auto rph = [](int i) { return static_cast<uint32_t>(i / NS) & 1u; };  // ring item i: slot i % NS
+    auto slot = [](uint32_t i) { return static_cast<int>(i % NS); };
+    auto rph = [](uint32_t i) { return i / NS; };
 
     if (warp == 0) {
         tmem_alloc(smem_u32(&tslot), kTcCols);
         tmem_relinquish();
     }
-    if (tid == 0) {
+    if (tid == 32 * kWarpLoad) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(smem_u32(&bar_full[i]), 1);
-            mbar_init(smem_u32(&bar_free[i]), 2);  // both chains' MMA warps
+            mbar_init(smem_u32(&bar_free[i]), 2);
         }
-        mbar_init(smem_u32(&bar_q), 1);
         for (int c = 0; c < 2; ++c) {
+            mbar_init(smem_u32(&bar_q[c]), 1);
+            mbar_init(smem_u32(&bar_qfree[c]), 1);
             mbar_init(smem_u32(&bar_s[c]), 1);
-            mbar_init(smem_u32(&bar_p[c]), 5);  // the chain's four compute warps, and its turn
+            mbar_init(smem_u32(&bar_p[c]), 5);
             mbar_init(smem_u32(&bar_o[c]), 1);
-            mbar_init(smem_u32(&bar_look[c]), 4);  // the looking chain's compute warps
-            mbar_init(smem_u32(&bar_go[c]), 1);
-            dirty[c] = 0;
+            mbar_init(smem_u32(&bar_ofree[c]), 4);
+            mbar_init(smem_u32(&bar_work[c]), 1);
+            mbar_init(smem_u32(&bar_wfree[c]), 11);
             held[c] = 0;
         }
-        fence_proxy_async();  // the barriers, before the TMA unit uses them
+        for (int x = 0; x < 4; ++x) {
+            mbar_init(smem_u32(&bar_go[x]), 1);
+            mbar_init(smem_u32(&bar_look[x]), 4);
+            dirty[x] = 0;
+        }
+        fence_proxy_async();  // the barriers, before the asynchronous units use them
     }
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
     const uint32_t tbase = tslot;
     bool ok = true;
+    uint32_t wi = 0;  // answers taken
+    auto next_work = [&]() {
+        const int x = wi & 1;
+        if (!wait_w(&bar_work[x], wi >> 1)) {
+            ok = false;
+            return -1;
+        }
+        const int w = work_of(smem_u32(&answer[x]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_wfree[x]));
+        ++wi;
+        return w;
+    };
 
     if (warp >= 8) {
         setmaxnreg_dec<kTcOtherRegs>();
-        if (warp == kWarpLoad) {
-            // ---------------- loads (lane 0): Q of both chains, then K_0, V_0, K_1, ... ----------------
-            if (lane == 0) {
-                const int nq = n1 > 0 ? 2 : 1;
-                mbar_expect_tx(smem_u32(&bar_q), nq * C::kTile);
-                for (int c = 0; c < nq; ++c)
-                    for (int x = 0; x < D / 64; ++x)
-                        tma_load3(smem_u32(sm + c * C::kTile + x * C::kBlock), &mq, 64 * x, h0, row0 + q0 + c * TQ,
-                                  smem_u32(&bar_q));
-            }
-            int issued = 0;
-            for (int i = 0; i < 2 * n_max; ++i) {
-                const int sl = i % NS;
-                if (i >= NS && !wait_w(&bar_free[sl], rph(i - NS))) break;
-                if (lane == 0) {
-                    mbar_expect_tx(smem_u32(&bar_full[sl]), C::kTile);
-                    for (int x = 0; x < D / 64; ++x)
-                        tma_load3(smem_u32(ring + sl * C::kTile + x * C::kBlock), (i & 1) ? &mv : &mk, 64 * x, kvh,
-                                  row0 + (i >> 1) * kKeys, smem_u32(&bar_full[sl]));
-                    if ((i & 1) && (i >> 1) >= look0) mbar_arrive(smem_u32(&bar_go[((i >> 1) - look0) & 1]));
+        if (warp == kWarpSpare) {
+            // nothing to do
+        } else if (warp == kWarpLoad) {
+            // ---------------- loads (lane 0): of each piece K_0, Q, V_0, K_1, ... ----------------
+            uint32_t it = 0, lk = 0, qn[2] = {0, 0};
+            for (int w = blockIdx.x; w >= 0 && ok; w = next_work()) {
+                const Piece p = piece_of(a, l, log_p, w);
+                for (int i = 0; i < 2 * p.n_max() && ok; ++i, ++it) {
+                    const int sl = slot(it);
+                    if (it >= NS) ok = wait_w(&bar_free[sl], rph(it) - 1);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mbar_expect_tx(smem_u32(&bar_full[sl]), C::kTile);
+#pragma unroll
+                        for (int x = 0; x < D / 64; ++x)
+                            tma_load3(smem_u32(ring + sl * C::kTile + x * C::kBlock), (i & 1) ? &mv : &mk, 64 * x, p.kvh,
+                                      p.row0 + (i >> 1) * kKeys, smem_u32(&bar_full[sl]));
+                        if ((i & 1) && (i >> 1) >= p.look0) {
+                            mbar_arrive(smem_u32(&bar_go[lk & 3]));
+                            ++lk;
+                        }
+                    }
+                    __syncwarp();
+                    if (i == 0) {
+                        for (int c = 0; c < (p.n1 > 0 ? 2 : 1) && ok; ++c) {
+                            if (qn[c] > 0) ok = wait_w(&bar_qfree[c], qn[c] - 1);
+                            if (!ok) break;
+                            if (lane == 0) {
+                                mbar_expect_tx(smem_u32(&bar_q[c]), C::kTile);
+#pragma unroll
+                                for (int x = 0; x < D / 64; ++x)
+                                    tma_load3(smem_u32(sm + c * C::kTile + x * C::kBlock), &mq, 64 * x, p.h0,
+                                              p.row0 + p.q0 + c * (128 >> log_p), smem_u32(&bar_q[c]));
+                            }
+                            ++qn[c];
+                            __syncwarp();
+                        }
+                    }
                 }
-                issued = i + 1;
+                // With its last load on the way the piece has a few tiles left to go:
+                // time for an answer, and late enough that short pieces take the most.
+                const int x = wi & 1;
+                if (ok && wi >= 2) ok = wait_w(&bar_wfree[x], (wi >> 1) - 1);
+                if (ok && lane == 0) {
+                    fence_proxy_async();  // the answer's readers are done
+                    mbar_expect_tx(smem_u32(&bar_work[x]), 16);
+                    ask_work(smem_u32(&answer[x]), smem_u32(&bar_work[x]));
+                }
+                __syncwarp();
             }
             // the last copies land before the CTA's shared memory is given up (bounded)
-            wait_w(&bar_q, 0);
-            for (int i = max(0, issued - NS); i < issued; ++i) wait_w(&bar_full[i % NS], rph(i));
-        } else if (warp == kWarpSpare) {
-            // nothing to do
+            for (int c = 0; c < 2; ++c)
+                if (qn[c] > 0) wait_w(&bar_q[c], qn[c] - 1);
+            for (uint32_t i = it > NS ? it - NS : 0; i < it; ++i) wait_w(&bar_full[slot(i)], rph(i));
+            if (!ok && lane == 0 && a.err) atomicOr(a.err, 2);
         } else {
             // ---------------- MMA issue: chain c (lane 0) ----------------
-            const int c = warp == kWarpMma0 ? 0 : 1, n = c ? n1 : n0;
+            const int c = warp == kWarpMma0 ? 0 : 1;
             const uint32_t tS = tbase + 256 + 128 * c, tO = tbase + 128 * c;
             const uint64_t dQ = desc_sw128(smem_u32(sm + c * C::kTile));
-            // S_c = Q_c K_j^T, then the slot's and the scores' barriers; on the way
-            // the turn passes to the other chain, whose issuing warp needs a while
-            // to see it
-            auto qk = [&](int j, bool pass) {
-                const int sl = (2 * j) % NS;
+            // S_c = Q_c K^T (ring item i), then the barriers; on the way the turn
+            // passes to the other chain, whose issuing warp needs a while to see it
+            auto qk = [&](uint32_t i, bool pass, bool last) {
+                const int sl = slot(i);
                 const uint64_t dK = desc_sw128(smem_u32(ring + sl * C::kTile));
                 if (lane == 0) {
 #pragma unroll
@@ -340,223 +436,266 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     mma_commit(smem_u32(&bar_s[c]));
                     mma_commit(smem_u32(&bar_free[sl]));
+                    if (last) mma_commit(smem_u32(&bar_qfree[c]));
                 }
                 __syncwarp();
             };
-            if (n > 0) {
-                ok = wait_w(&bar_q, 0) && wait_w(&bar_full[0], 0);
-                if (ok) {
+            uint32_t it = 0, lk = 0, tiles = 0, pieces = 0;  // of the ring, looked over, of the chain
+            bool owed = false;  // chain 0: the piece before ends with a turn from chain 1
+            for (int w = blockIdx.x; w >= 0 && ok; w = next_work()) {
+                const Piece p = piece_of(a, l, log_p, w);
+                const int n = c ? p.n1 : p.n0, n_max = p.n_max();
+                if (n > 0) {
+                    ok = wait_w(&bar_q[c], pieces) && wait_w(&bar_full[slot(it)], rph(it));
+                    if (!ok) break;
                     fence_after_sync();
-                    qk(0, false);
+                    qk(it, false, n == 1);
                 }
-            }
-            for (int j = 0; j < n && ok; ++j) {
-                const int iv = 2 * j + 1, sv = iv % NS;
-                ok = wait_w(&bar_full[sv], rph(iv));
-                if (ok && j >= look0) ok = wait_w(&bar_look[(j - look0) & 1], 0);
-                if (ok && j + 1 < n) ok = wait_w(&bar_full[(2 * j + 2) % NS], rph(2 * j + 2));
-                // P, and this chain's turn: the other chain's products before these
-                // (chain 0's of tile j, chain 1's of tile j - 1), or the most of
-                // them, have been issued; a chain without such products takes it
-                if (lane == 0 && !(c ? j < n0 : j > 0 && j - 1 < n1)) mbar_arrive(smem_u32(&bar_p[c]));
-                if (ok) ok = wait_w(&bar_p[c], j & 1);
-                if (!ok) break;
-                fence_after_sync();
-                const uint64_t dV = desc_mn(smem_u32(ring + sv * C::kTile), C::kBlock);
-                const uint32_t acc = j > 0 ? 1u : *static_cast<volatile uint32_t *>(&held[c]);
-                if (lane == 0) {
+                for (int j = 0; j < n && ok; ++j, ++tiles) {
+                    const uint32_t iv = it + 2 * j + 1;
+                    const int sv = slot(iv);
+                    ok = wait_w(&bar_full[sv], rph(iv));
+                    if (ok && j + 1 < n) ok = wait_w(&bar_full[slot(iv + 1)], rph(iv + 1));
+                    if (ok && j == 0 && pieces > 0) ok = wait_w(&bar_ofree[c], pieces - 1);
+                    if (ok && j >= p.look0) {
+                        const uint32_t x = lk + j - p.look0;
+                        ok = wait_w(&bar_look[x & 3], x >> 2);
+                    }
+                    // P, and this chain's turn: the other chain's products before these
+                    // (chain 0's of tile j, chain 1's of tile j - 1 or of the piece
+                    // before), or the most of them, have been issued; where there are
+                    // none the chain takes its turn itself
+                    const bool given = c ? j < p.n0 : j > 0 ? j - 1 < p.n1 : owed;
+                    if (ok && lane == 0 && !given) mbar_arrive(smem_u32(&bar_p[c]));
+                    if (ok) ok = wait_w(&bar_p[c], tiles);
+                    if (!ok) break;
+                    fence_after_sync();
+                    const uint64_t dV = desc_mn(smem_u32(ring + sv * C::kTile), C::kBlock);
+                    uint32_t acc = 1u;
+                    if (j == 0) {
+                        acc = *static_cast<volatile uint32_t *>(&held[c]);
+                        __syncwarp();
+                        if (lane == 0) *static_cast<volatile uint32_t *>(&held[c]) = 0;
+                    }
+                    if (lane == 0) {
 #pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)
-                        mma_f16_ts(tO, tS + 8 * k, dV + ((k * 2048u) >> 4), idesc16<T>(D, true), k > 0 ? 1u : acc);
-                    mma_commit(smem_u32(&bar_free[sv]));
-                    if (j + 1 == n) mma_commit(smem_u32(&bar_o[c]));
+                        for (int k = 0; k < kKeys / 16; ++k)
+                            mma_f16_ts(tO, tS + 8 * k, dV + ((k * 2048u) >> 4), idesc16<T>(D, true), k > 0 ? 1u : acc);
+                        mma_commit(smem_u32(&bar_free[sv]));
+                        if (j + 1 == n) mma_commit(smem_u32(&bar_o[c]));
+                    }
+                    __syncwarp();
+                    // the other chain's products follow (chain 1's last are followed
+                    // by chain 0's first of the next piece)
+                    const bool pass = c ? j + 1 < p.n0 || j + 1 == n : j < p.n1;
+                    if (j + 1 < n) qk(iv + 1, pass, j + 2 == n);
+                    else if (pass && lane == 0) mbar_arrive(smem_u32(&bar_p[c ^ 1]));
+                    __syncwarp();
                 }
-                __syncwarp();
-                const bool pass = c ? j + 1 < n0 : j < n1;  // the other chain's products follow
-                if (j + 1 < n) qk(j + 1, pass);
-                else if (pass && lane == 0) mbar_arrive(smem_u32(&bar_p[c ^ 1]));
-                __syncwarp();
-            }
-            // items past the chain's last tile are free as far as this chain goes
-            // (counted once they have landed, so that each counts for its own phase)
-            for (int i = 2 * n; i < 2 * n_max && ok; ++i) {
-                ok = wait_w(&bar_full[i % NS], rph(i));
-                if (ok && lane == 0) mbar_arrive(smem_u32(&bar_free[i % NS]));
+                // items past the chain's last tile are free as far as this chain goes
+                // (counted once they have landed, so that each counts for its own phase)
+                for (uint32_t i = it + 2 * n; i < it + 2 * n_max && ok; ++i) {
+                    ok = wait_w(&bar_full[slot(i)], rph(i));
+                    if (ok && lane == 0) mbar_arrive(smem_u32(&bar_free[slot(i)]));
+                }
+                it += 2 * n_max;
+                lk += p.looks();
+                if (n > 0) ++pieces;
+                owed = p.n1 > 0;
             }
             if (!ok && lane == 0 && a.err) atomicOr(a.err, 2);
         }
     } else {
         // -------------- compute warps: one thread per row and chain --------------
         setmaxnreg_inc<kTcComputeRegs>();
-        const int c = warp >> 2, n = c ? n1 : n0, m = tid & 127;
-        const int tok = q0 + c * TQ + (m >> log_p);
-        const bool valid = tok < len;
-        const int lim = a.causal ? min(tok + 1, len) : len;  // keys this row sees
+        const int c = warp >> 2, m = tid & 127, P = 1 << log_p, TQ = 128 >> log_p;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t tS = tbase + lanes + 256 + 128 * c, tO = tbase + lanes + 128 * c;
         const float cs = a.scale_log2;  // > 0
-        float m_ref = -INFINITY, l_run = 0.f;
-        for (int j = 0; j < n; ++j) {
-            if (j >= look0 && (c == 1 || j >= n1)) {
-                // this chain looks over V_j: keys up to key0 are seen by every row; a
-                // key's 128 bytes of each 64 columns are 8 chunks.  (The loading warp
-                // tells when the slot is at V_j: these warps follow no earlier item.)
-                const int i = 2 * j + 1, sl = i % NS, w = (j - look0) & 1;
-                ok = wait_w(&bar_go[w], 0) && wait_w(&bar_full[sl], rph(i));
-                if (!ok) break;
-                uint4 *v = reinterpret_cast<uint4 *>(ring + sl * C::kTile);
-                const int key0 = max(0, (a.causal ? q0 + 1 : len) - j * kKeys);
-                constexpr uint32_t kE = std::is_same<T, bf16>::value ? 0x7f807f80u : 0x7c007c00u;
-                constexpr uint32_t kOne = std::is_same<T, bf16>::value ? 0x00800080u : 0x04000400u;
-                uint32_t seen = 0;  // a half's exponent is all ones where adding one to it reaches the sign bit
+        uint32_t it = 0, lk = 0, tiles = 0, pieces = 0;
+        for (int w = blockIdx.x; w >= 0 && ok; w = next_work()) {
+            const Piece p = piece_of(a, l, log_p, w);
+            const int n = c ? p.n1 : p.n0;
+            const int tok = p.q0 + c * TQ + (m >> log_p);
+            const bool valid = tok < p.len;
+            const int lim = a.causal ? min(tok + 1, p.len) : p.len;  // keys this row sees
+            float m_ref = -INFINITY, l_run = 0.f;
+            for (int j = 0; j < n; ++j, ++tiles) {
+                const uint32_t look = lk + j - p.look0;
+                if (j >= p.look0 && (c == 1 || j >= p.n1)) {
+                    // this chain looks over V_j: keys up to key0 are seen by every row; a
+                    // key's 128 bytes of each 64 columns are 8 chunks.  (The loading warp
+                    // tells when the slot is at V_j: these warps follow no earlier item.)
+                    const uint32_t i = it + 2 * j + 1;
+                    ok = wait_w(&bar_go[look & 3], look >> 2) && wait_w(&bar_full[slot(i)], rph(i));
+                    if (!ok) break;
+                    uint4 *v = reinterpret_cast<uint4 *>(ring + slot(i) * C::kTile);
+                    const int key0 = max(0, (a.causal ? p.q0 + 1 : p.len) - j * kKeys);
+                    constexpr uint32_t kE = std::is_same<T, bf16>::value ? 0x7f807f80u : 0x7c007c00u;
+                    constexpr uint32_t kOne = std::is_same<T, bf16>::value ? 0x00800080u : 0x04000400u;
+                    uint32_t seen = 0;  // a half's exponent is all ones where adding one to it reaches the sign bit
 #pragma unroll
-                for (int x0 = 0; x0 < static_cast<int>(C::kTile / 16); x0 += 128) {
-                    const int x = x0 + m;
-                    if ((x & 1023) >= key0 * 8) {
-                        const uint4 y = v[x];
-                        seen |= ((y.x & kE) + kOne) | ((y.y & kE) + kOne) | ((y.z & kE) + kOne) | ((y.w & kE) + kOne);
-                    }
-                }
-                if (seen & 0x80008000u) {
-                    for (int x = m; x < static_cast<int>(C::kTile / 16); x += 128) {
-                        if ((x & 1023) < key0 * 8) continue;
-                        const uint4 y = v[x];
-                        uint32_t u[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if (not_finite<T>(u[k])) u[k] &= 0xffff0000u;
-                            if (not_finite<T>(u[k] >> 16)) u[k] &= 0xffffu;
+                    for (int x0 = 0; x0 < static_cast<int>(C::kTile / 16); x0 += 128) {
+                        const int x = x0 + m;
+                        if ((x & 1023) >= key0 * 8) {
+                            const uint4 y = v[x];
+                            seen |= ((y.x & kE) + kOne) | ((y.y & kE) + kOne) | ((y.z & kE) + kOne) | ((y.w & kE) + kOne);
                         }
-                        v[x] = make_uint4(u[0], u[1], u[2], u[3]);
                     }
-                    *static_cast<volatile uint32_t *>(&dirty[w]) = 1;
+                    if (seen & 0x80008000u) {
+                        for (int x = m; x < static_cast<int>(C::kTile / 16); x += 128) {
+                            if ((x & 1023) < key0 * 8) continue;
+                            const uint4 y = v[x];
+                            uint32_t u[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if (not_finite<T>(u[k])) u[k] &= 0xffff0000u;
+                                if (not_finite<T>(u[k] >> 16)) u[k] &= 0xffffu;
+                            }
+                            v[x] = make_uint4(u[0], u[1], u[2], u[3]);
+                        }
+                        // the flag holds the count of the look it belongs to (+ 1)
+                        *static_cast<volatile uint32_t *>(&dirty[look & 3]) = look + 1;
+                    }
+                    fence_proxy_async();  // before the MMAs read the tile
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bar_look[look & 3]));
                 }
-                fence_proxy_async();  // before the MMAs read the tile
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar_look[w]));
-            }
-            ok = wait_w(&bar_s[c], j & 1);
-            if (!ok) break;
-            fence_after_sync();
-            uint32_t x[kKeys];  // the row's scores (f32 bits)
-#pragma unroll
-            for (int i = 0; i < kKeys; i += 32) tmem_ld32_issue(tS + i, x + i);
-            tmem_ld_done(x);
-            auto xf = [&](int i) { return __uint_as_float(x[i]); };
-            const int base = j * kKeys;
-            if (base + kKeys > lim) {
-#pragma unroll
-                for (int i = 0; i < kKeys; ++i) x[i] = base + i < lim ? x[i] : 0xff800000u;
-            }
-            float mx[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mx[i] = fmaxf(xf(2 * i), xf(2 * i + 1));
-#pragma unroll
-            for (int i = 8; i < kKeys; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], xf(i), xf(i + 1));
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs;
-            const bool move = top > m_ref + kGrow || m_ref == -INFINITY;
-            const float m_use = move ? top : m_ref;
-            const float nm = m_use == -INFINITY ? 0.f : -m_use;
-            // O moves with the reference (QK(j), already done, followed PV(j - 1))
-            const float f = move && m_ref != -INFINITY ? ex2(m_ref - m_use) : 1.f;
-            if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll 1
-                for (int i = 0; i < D / 16; ++i) {
-                    float o[16];
-                    tmem_ld16(tO + 16 * i, o);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) o[k] *= f;
-                    tmem_st16(tO + 16 * i, o);
-                }
-            }
-            m_ref = m_use;
-            // P over S
-            uint64_t sum[2] = {0, 0};
-            const uint64_t cs2 = pair(cs, cs), nm2 = pair(nm, nm);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t p[32];
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    const float2 e = unpair(fma2(pair(xf(64 * i + 2 * k), xf(64 * i + 2 * k + 1)), cs2, nm2));
-                    const float p0 = ex2(e.x), p1 = ex2(e.y);
-                    sum[k & 1] = add2(sum[k & 1], pair(p0, p1));
-                    p[k] = pack2(T{}, p0, p1);
-                }
-                tmem_st32u(tS + 32 * i, p);
-            }
-            const float2 s2 = unpair(add2(sum[0], sum[1]));
-            l_run = fmaf(l_run, f, s2.x + s2.y);
-            tmem_st_wait();
-            if (j >= look0) {
-                ok = wait_w(&bar_look[(j - look0) & 1], 0);
+                ok = wait_w(&bar_s[c], tiles);
                 if (!ok) break;
-                if (*static_cast<volatile uint32_t *>(&dirty[(j - look0) & 1])) {
-                    // this tile's V values that are not finite, key by key
-                    const T *v = static_cast<const T *>(a.V) + static_cast<int64_t>(row0 + base) * a.v_stride +
-                                 static_cast<int64_t>(kvh) * a.hd;
-                    const int see = valid ? min(kKeys, lim - base) : 0;
+                fence_after_sync();
+                uint32_t x[kKeys];  // the row's scores (f32 bits)
+#pragma unroll
+                for (int i = 0; i < kKeys; i += 32) tmem_ld32_issue(tS + i, x + i);
+                tmem_ld_done(x);
+                auto xf = [&](int i) { return __uint_as_float(x[i]); };
+                const int base = j * kKeys;
+                if (base + kKeys > lim) {
+#pragma unroll
+                    for (int i = 0; i < kKeys; ++i) x[i] = base + i < lim ? x[i] : 0xff800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mx[i] = fmaxf(xf(2 * i), xf(2 * i + 1));
+#pragma unroll
+                for (int i = 8; i < kKeys; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], xf(i), xf(i + 1));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs;
+                const bool move = top > m_ref + kGrow || m_ref == -INFINITY;
+                const float m_use = move ? top : m_ref;
+                const float nm = m_use == -INFINITY ? 0.f : -m_use;
+                // O moves with the reference (QK(j), already done, followed PV(j - 1))
+                const float f = move && m_ref != -INFINITY ? ex2(m_ref - m_use) : 1.f;
+                if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
                     for (int i = 0; i < D / 16; ++i) {
                         float o[16];
-                        if (j > 0) {
-                            tmem_ld16(tO + 16 * i, o);
-                        } else {
+                        tmem_ld16(tO + 16 * i, o);
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = 0.f;
-                        }
-#pragma unroll 1
-                        for (int kk = 0; kk < kKeys / 2; ++kk) {
-                            const uint32_t w = tmem_ld1(tS + kk);
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                if (2 * kk + e >= see) continue;
-                                const unsigned short *vr = reinterpret_cast<const unsigned short *>(
-                                    v + static_cast<int64_t>(2 * kk + e) * a.v_stride) + 16 * i;
-                                const float p = half_of(T{}, w, e);
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) {
-                                    if (16 * i + k >= a.hd) continue;
-                                    const uint32_t b = __ldg(vr + k);
-                                    if (not_finite<T>(b)) o[k] = fmaf(p, half_of(T{}, b, 0), o[k]);
-                                }
-                            }
-                            __syncwarp();
-                        }
+                        for (int k = 0; k < 16; ++k) o[k] *= f;
                         tmem_st16(tO + 16 * i, o);
                     }
-                    if (j == 0 && m == 0) *static_cast<volatile uint32_t *>(&held[c]) = 1;
-                    tmem_st_wait();
                 }
+                m_ref = m_use;
+                // P over S
+                uint64_t sum[2] = {0, 0};
+                const uint64_t cs2 = pair(cs, cs), nm2 = pair(nm, nm);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t pr[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float2 e = unpair(fma2(pair(xf(64 * i + 2 * k), xf(64 * i + 2 * k + 1)), cs2, nm2));
+                        const float p0 = ex2(e.x), p1 = ex2(e.y);
+                        sum[k & 1] = add2(sum[k & 1], pair(p0, p1));
+                        pr[k] = pack2(T{}, p0, p1);
+                    }
+                    tmem_st32u(tS + 32 * i, pr);
+                }
+                const float2 s2 = unpair(add2(sum[0], sum[1]));
+                l_run = fmaf(l_run, f, s2.x + s2.y);
+                tmem_st_wait();
+                if (j >= p.look0) {
+                    ok = wait_w(&bar_look[look & 3], look >> 2);
+                    if (!ok) break;
+                    if (*static_cast<volatile uint32_t *>(&dirty[look & 3]) == look + 1) {
+                        // this tile's V values that are not finite, key by key (PV(0) of
+                        // the piece writes over O, unless told that O holds something;
+                        // O is this piece's from then on: its reader is this thread)
+                        const T *v = static_cast<const T *>(a.V) + static_cast<int64_t>(p.row0 + base) * a.v_stride +
+                                     static_cast<int64_t>(p.kvh) * a.hd;
+                        const int see = valid ? min(kKeys, lim - base) : 0;
+#pragma unroll 1
+                        for (int i = 0; i < D / 16; ++i) {
+                            float o[16];
+                            if (j > 0) {
+                                tmem_ld16(tO + 16 * i, o);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) o[k] = 0.f;
+                            }
+#pragma unroll 1
+                            for (int kk = 0; kk < kKeys / 2; ++kk) {
+                                const uint32_t pw = tmem_ld1(tS + kk);
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    if (2 * kk + e >= see) continue;
+                                    const unsigned short *vr = reinterpret_cast<const unsigned short *>(
+                                        v + static_cast<int64_t>(2 * kk + e) * a.v_stride) + 16 * i;
+                                    const float pe = half_of(T{}, pw, e);
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) {
+                                        if (16 * i + k >= a.hd) continue;
+                                        const uint32_t b = __ldg(vr + k);
+                                        if (not_finite<T>(b)) o[k] = fmaf(pe, half_of(T{}, b, 0), o[k]);
+                                    }
+                                }
+                                __syncwarp();
+                            }
+                            tmem_st16(tO + 16 * i, o);
+                        }
+                        if (j == 0 && m == 0) *static_cast<volatile uint32_t *>(&held[c]) = 1;
+                        tmem_st_wait();
+                    }
+                }
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar_p[c]));
             }
-            fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bar_p[c]));
-        }
-        if (n > 0) {
-            if (ok) ok = wait_w(&bar_o[c], 0);
-            if (!ok) {
-                if (lane == 0 && a.err) atomicOr(a.err, 2);
-            } else {
+            if (n > 0 && ok) {
+                ok = wait_w(&bar_o[c], pieces);
+                if (!ok) break;
                 fence_after_sync();
+                uint32_t o[D];
+#pragma unroll
+                for (int i = 0; i < D; i += 32) tmem_ld32_issue(tO + i, o + i);
+                tmem_ld_done(o);
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar_ofree[c]));
                 const float inv = 1.f / l_run;
-                T *dst = static_cast<T *>(a.out) + static_cast<int64_t>(row0 + (valid ? tok : 0)) * a.o_stride +
-                         static_cast<int64_t>(h0 + (m & (P - 1))) * a.hd;
+                T *dst = static_cast<T *>(a.out) + static_cast<int64_t>(p.row0 + (valid ? tok : 0)) * a.o_stride +
+                         static_cast<int64_t>(p.h0 + (m & (P - 1))) * a.hd;
+                auto two = [&](int i) { return pack2(T{}, __uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv); };
+                if (a.out32) {  // whole 32-byte sectors
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    float o[32];
-                    tmem_ld32(tO + 32 * i, o);
+                    for (int i = 0; i < D; i += 16)
+                        if (valid && i < a.hd)
+                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + i),
+                                         "r"(two(i)), "r"(two(i + 2)), "r"(two(i + 4)), "r"(two(i + 6)), "r"(two(i + 8)),
+                                         "r"(two(i + 10)), "r"(two(i + 12)), "r"(two(i + 14))
+                                         : "memory");
+                } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (valid && 32 * i + 8 * k < a.hd)
-                            *reinterpret_cast<uint4 *>(dst + 32 * i + 8 * k) =
-                                make_uint4(pack2(T{}, o[8 * k] * inv, o[8 * k + 1] * inv),
-                                           pack2(T{}, o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                                           pack2(T{}, o[8 * k + 4] * inv, o[8 * k + 5] * inv),
-                                           pack2(T{}, o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+                    for (int i = 0; i < D; i += 8)
+                        if (valid && i < a.hd)
+                            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(two(i), two(i + 2), two(i + 4), two(i + 6));
                 }
+                ++pieces;
             }
+            it += 2 * p.n_max();
+            lk += p.looks();
         }
+        if (!ok && lane == 0 && a.err) atomicOr(a.err, 2);
     }
     fence_before_sync();
     __syncthreads();
@@ -763,7 +902,9 @@ cudaError_t launch_tc_n(const PackedArgs &a, const int32_t *start, const int32_t
     fill_seqs(l, start, len, n, 2 * (128 >> log_p));
     const long long grid = static_cast<long long>(l.tile0[n]) * (a.n_heads >> log_p);
     if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    packed_tc_kernel<D, T, N><<<static_cast<unsigned>(grid), kTcThreads, C::kSmem, s>>>(mq, mk, mv, a, l, log_p);
+    PackedArgs b = a;
+    b.out32 = a.hd % 16 == 0 && a.o_stride % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+    packed_tc_kernel<D, T, N><<<static_cast<unsigned>(grid), kTcThreads, C::kSmem, s>>>(mq, mk, mv, b, l, log_p);
     return cudaGetLastError();
 }
 
