@@ -290,7 +290,8 @@ __device__ __forceinline__ Piece piece_of(const PackedArgs &a, const PackedSeqs<
 //   p[c]                     P_c written (four warps) and the chain's turn (one)
 //   o[c] / ofree[c]          the piece's last PV_c done / O_c read (four warps)
 //   go[x], look[x]           V of a partly seen tile loaded / looked over
-//   work[x] / wfree[x]       answer there / read by the eleven working warps
+//   answer                   the number of a further piece
+//   work[x] / wfree[x]       piece handed out / read by the other ten warps
 template <int D, class T, int N>
 __global__ void __launch_bounds__(kTcThreads, 1)
     packed_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -303,11 +304,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         (reinterpret_cast<uintptr_t>(smraw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char *ring = sm + 2 * C::kTile;  // Q_c at c * kTile
     __shared__ uint64_t bar_full[NS], bar_free[NS], bar_q[2], bar_qfree[2], bar_s[2], bar_p[2], bar_o[2], bar_ofree[2];
-    __shared__ uint64_t bar_go[4], bar_look[4], bar_work[2], bar_wfree[2];
-    __shared__ __align__(16) uint4 answer[2];
+    __shared__ uint64_t bar_go[4], bar_look[4], bar_answer, bar_work[2], bar_wfree[2];
+    __shared__ __align__(16) uint4 answer;
+    __shared__ int4 pieces_s[2][2];  // decoded by the loading warp for the others
     __shared__ uint32_t tslot, dirty[4], held[2];  // held[c]: O_c already holds something before PV(0)
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (values that the compiler knows to be the same in a warp stay in uniform
+    // registers, where the MMA instructions want their operands)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     auto wait_w = [&](uint64_t *bar, uint32_t parity) {  // bounded; the warp agrees on the outcome
         return __all_sync(0xffffffffu, wait_phase(smem_u32(bar), parity & 1u)) != 0;
     };
@@ -331,9 +335,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(smem_u32(&bar_o[c]), 1);
             mbar_init(smem_u32(&bar_ofree[c]), 4);
             mbar_init(smem_u32(&bar_work[c]), 1);
-            mbar_init(smem_u32(&bar_wfree[c]), 11);
+            mbar_init(smem_u32(&bar_wfree[c]), 10);
             held[c] = 0;
         }
+        mbar_init(smem_u32(&bar_answer), 1);
         for (int x = 0; x < 4; ++x) {
             mbar_init(smem_u32(&bar_go[x]), 1);
             mbar_init(smem_u32(&bar_look[x]), 4);
@@ -344,20 +349,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    const uint32_t tbase = tslot;
+    const uint32_t tbase = __shfl_sync(0xffffffffu, tslot, 0);
     bool ok = true;
-    uint32_t wi = 0;  // answers taken
-    auto next_work = [&]() {
+    uint32_t wi = 0;  // pieces taken from the loading warp
+    // The next piece (false: none is left, or a wait ran out).
+    auto next_piece = [&](Piece &p) {
         const int x = wi & 1;
-        if (!wait_w(&bar_work[x], wi >> 1)) {
-            ok = false;
-            return -1;
-        }
-        const int w = work_of(smem_u32(&answer[x]));
+        ok = ok && wait_w(&bar_work[x], wi >> 1);
+        if (!ok) return false;
+        const int4 u = pieces_s[x][0], v = pieces_s[x][1];
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bar_wfree[x]));
         ++wi;
-        return w;
+        auto same = [](int y) { return __shfl_sync(0xffffffffu, y, 0); };
+        p = Piece{same(u.x), same(u.y), same(u.z), same(u.w), same(v.x), same(v.y), same(v.z), same(v.w)};
+        return p.len > 0;
     };
 
     if (warp >= 8) {
@@ -366,9 +372,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // nothing to do
         } else if (warp == kWarpLoad) {
             // ---------------- loads (lane 0): of each piece K_0, Q, V_0, K_1, ... ----------------
-            uint32_t it = 0, lk = 0, qn[2] = {0, 0};
-            for (int w = blockIdx.x; w >= 0 && ok; w = next_work()) {
-                const Piece p = piece_of(a, l, log_p, w);
+            uint32_t it = 0, lk = 0, asked = 0, qn[2] = {0, 0};
+            if (lane == 0) {
+                for (const CUtensorMap *m : {&mq, &mk, &mv})
+                    asm volatile("prefetch.tensormap [%0];\n" ::"l"(m) : "memory");
+            }
+            Piece p = piece_of(a, l, log_p, blockIdx.x);
+            for (;;) {
+                // the others' copy (len 0: nothing is left)
+                {
+                    const int x = wi & 1;
+                    if (wi >= 2) ok = wait_w(&bar_wfree[x], (wi >> 1) - 1);
+                    if (ok && lane == 0) {
+                        pieces_s[x][0] = make_int4(p.len, p.row0, p.q0, p.h0);
+                        pieces_s[x][1] = make_int4(p.kvh, p.n0, p.n1, p.look0);
+                        mbar_arrive(smem_u32(&bar_work[x]));
+                    }
+                    __syncwarp();
+                    ++wi;
+                }
+                if (!ok || p.len == 0) break;
                 for (int i = 0; i < 2 * p.n_max() && ok; ++i, ++it) {
                     const int sl = slot(it);
                     if (it >= NS) ok = wait_w(&bar_free[sl], rph(it) - 1);
@@ -402,15 +425,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                 }
                 // With its last load on the way the piece has a few tiles left to go:
-                // time for an answer, and late enough that short pieces take the most.
-                const int x = wi & 1;
-                if (ok && wi >= 2) ok = wait_w(&bar_wfree[x], (wi >> 1) - 1);
-                if (ok && lane == 0) {
-                    fence_proxy_async();  // the answer's readers are done
-                    mbar_expect_tx(smem_u32(&bar_work[x]), 16);
-                    ask_work(smem_u32(&answer[x]), smem_u32(&bar_work[x]));
+                // time to ask for the next, late enough that short pieces take the most.
+                if (!ok) break;
+                if (lane == 0) {
+                    fence_proxy_async();  // the answer before this one has been read
+                    mbar_expect_tx(smem_u32(&bar_answer), 16);
+                    ask_work(smem_u32(&answer), smem_u32(&bar_answer));
                 }
                 __syncwarp();
+                ok = wait_w(&bar_answer, asked++);
+                if (!ok) break;
+                const int w = __shfl_sync(0xffffffffu, work_of(smem_u32(&answer)), 0);
+                __syncwarp();
+                if (w >= 0) p = piece_of(a, l, log_p, w);
+                else p.len = 0;
             }
             // the last copies land before the CTA's shared memory is given up (bounded)
             for (int c = 0; c < 2; ++c)
@@ -442,8 +470,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             };
             uint32_t it = 0, lk = 0, tiles = 0, pieces = 0;  // of the ring, looked over, of the chain
             bool owed = false;  // chain 0: the piece before ends with a turn from chain 1
-            for (int w = blockIdx.x; w >= 0 && ok; w = next_work()) {
-                const Piece p = piece_of(a, l, log_p, w);
+            Piece p;
+            while (next_piece(p)) {
                 const int n = c ? p.n1 : p.n0, n_max = p.n_max();
                 if (n > 0) {
                     ok = wait_w(&bar_q[c], pieces) && wait_w(&bar_full[slot(it)], rph(it));
@@ -513,8 +541,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t tS = tbase + lanes + 256 + 128 * c, tO = tbase + lanes + 128 * c;
         const float cs = a.scale_log2;  // > 0
         uint32_t it = 0, lk = 0, tiles = 0, pieces = 0;
-        for (int w = blockIdx.x; w >= 0 && ok; w = next_work()) {
-            const Piece p = piece_of(a, l, log_p, w);
+        Piece p;
+        while (next_piece(p)) {
             const int n = c ? p.n1 : p.n0;
             const int tok = p.q0 + c * TQ + (m >> log_p);
             const bool valid = tok < p.len;
