@@ -211,6 +211,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+// One lane of a converged warp, chosen in a way that leaves the operands of the
+// instructions it issues in uniform registers (a test of the lane number does
+// not: eight MMAs then took 440 clocks to issue instead of 270).
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}\n" : "=r"(p));
+    return p != 0;
+}
 // Shared-memory matrix descriptor of a V tile, MN-major with 128-byte swizzle:
 // 64 columns of a key in 128 bytes, 8 keys 1024 bytes apart (stride offset),
 // the next 64 columns kBlock bytes on (leading offset).
@@ -446,7 +454,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (uint32_t i = it > NS ? it - NS : 0; i < it; ++i) wait_w(&bar_full[slot(i)], rph(i));
             if (!ok && lane == 0 && a.err) atomicOr(a.err, 2);
         } else {
-            // ---------------- MMA issue: chain c (lane 0) ----------------
+            // ---------------- MMA issue: chain c (one lane) ----------------
             const int c = warp == kWarpMma0 ? 0 : 1;
             const uint32_t tS = tbase + 256 + 128 * c, tO = tbase + 128 * c;
             const uint64_t dQ = desc_sw128(smem_u32(sm + c * C::kTile));
@@ -455,7 +463,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             auto qk = [&](uint32_t i, bool pass, bool last) {
                 const int sl = slot(i);
                 const uint64_t dK = desc_sw128(smem_u32(ring + sl * C::kTile));
-                if (lane == 0) {
+                if (elect_lane()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint64_t o = ((k >> 2) * C::kBlock + (k & 3) * 32u) >> 4;
@@ -494,7 +502,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // before), or the most of them, have been issued; where there are
                     // none the chain takes its turn itself
                     const bool given = c ? j < p.n0 : j > 0 ? j - 1 < p.n1 : owed;
-                    if (ok && lane == 0 && !given) mbar_arrive(smem_u32(&bar_p[c]));
+                    if (ok && !given && elect_lane()) mbar_arrive(smem_u32(&bar_p[c]));
                     if (ok) ok = wait_w(&bar_p[c], tiles);
                     if (!ok) break;
                     fence_after_sync();
@@ -503,9 +511,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (j == 0) {
                         acc = *static_cast<volatile uint32_t *>(&held[c]);
                         __syncwarp();
-                        if (lane == 0) *static_cast<volatile uint32_t *>(&held[c]) = 0;
+                        if (elect_lane()) *static_cast<volatile uint32_t *>(&held[c]) = 0;
                     }
-                    if (lane == 0) {
+                    if (elect_lane()) {
 #pragma unroll
                         for (int k = 0; k < kKeys / 16; ++k)
                             mma_f16_ts(tO, tS + 8 * k, dV + ((k * 2048u) >> 4), idesc16<T>(D, true), k > 0 ? 1u : acc);
@@ -517,14 +525,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // by chain 0's first of the next piece)
                     const bool pass = c ? j + 1 < p.n0 || j + 1 == n : j < p.n1;
                     if (j + 1 < n) qk(iv + 1, pass, j + 2 == n);
-                    else if (pass && lane == 0) mbar_arrive(smem_u32(&bar_p[c ^ 1]));
+                    else if (pass && elect_lane()) mbar_arrive(smem_u32(&bar_p[c ^ 1]));
                     __syncwarp();
                 }
                 // items past the chain's last tile are free as far as this chain goes
                 // (counted once they have landed, so that each counts for its own phase)
                 for (uint32_t i = it + 2 * n; i < it + 2 * n_max && ok; ++i) {
                     ok = wait_w(&bar_full[slot(i)], rph(i));
-                    if (ok && lane == 0) mbar_arrive(smem_u32(&bar_free[slot(i)]));
+                    if (ok && elect_lane()) mbar_arrive(smem_u32(&bar_free[slot(i)]));
                 }
                 it += 2 * n_max;
                 lk += p.looks();
