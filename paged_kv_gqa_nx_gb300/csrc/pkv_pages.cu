@@ -23,6 +23,9 @@
 #include "pkv_elem.h"
 #include "pkv_internal.h"
 
+#include <algorithm>
+#include <type_traits>
+
 namespace pkv {
 namespace {
 
@@ -53,6 +56,63 @@ __device__ __forceinline__ void load8(const f16 *p, float (&x)[8]) {
         x[2 * i] = f.x;
         x[2 * i + 1] = f.y;
     }
+}
+// The same in two steps, so that many chunks can be on their way before one is used.
+template <class S>
+struct Raw8 {
+    uint4 a, b;  // b: f32 only
+};
+template <class S>
+__device__ __forceinline__ Raw8<S> fetch8(const S *p) {
+    Raw8<S> r;
+    r.a = __ldg(reinterpret_cast<const uint4 *>(p));
+    if constexpr (sizeof(S) == 4) r.b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+    return r;
+}
+__device__ __forceinline__ void widen8(const Raw8<float> &r, float (&x)[8]) {
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+}
+__device__ __forceinline__ void widen8(const Raw8<bf16> &r, float (&x)[8]) {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void widen8(const Raw8<f16> &r, float (&x)[8]) {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+// The largest magnitude so far, as bits: of f32 a word, of 16-bit types two
+// halves (a magnitude's bits are ordered as the magnitude is, infinities and
+// NaN above every finite one); max_bits: of everything, as the bits of an f32.
+__device__ __forceinline__ uint32_t max_raw(uint32_t m, const Raw8<float> &r) {
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+    return m;
+}
+template <class S>
+__device__ __forceinline__ uint32_t max_raw(uint32_t m, const Raw8<S> &r) {
+    m = __vmaxu2(m, r.a.x & 0x7fff7fffu);
+    m = __vmaxu2(m, r.a.y & 0x7fff7fffu);
+    m = __vmaxu2(m, r.a.z & 0x7fff7fffu);
+    return __vmaxu2(m, r.a.w & 0x7fff7fffu);
+}
+template <class S>
+__device__ __forceinline__ uint32_t max_bits(uint32_t m) {
+    if constexpr (sizeof(S) == 4) return m;
+    const uint32_t h = max(m & 0xffffu, m >> 16);
+    if constexpr (std::is_same<S, bf16>::value) return h << 16;
+    return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(h))));
 }
 __device__ __forceinline__ float load1(const float *p) { return __ldg(p); }
 __device__ __forceinline__ float load1(const bf16 *p) { return to_f32(*p); }
@@ -121,9 +181,35 @@ __device__ __forceinline__ int scale_exp(float s) {
 __device__ __forceinline__ uint32_t q8_elem(float x, float inv) {
     return static_cast<uint32_t>(__float2int_rn(x * inv) + 128) & 255u;
 }
+// Four elements in a word.  Adding 1.5 * 2^23 leaves the sum's integer part in
+// the low mantissa bits, rounded to nearest even as the sum is (the 128 that
+// comes along is even, so ties fall as they would without it): one FFMA a
+// value where a conversion instruction would run at a quarter of its rate.
+__device__ __forceinline__ uint32_t q8_word(float a, float b, float c, float d, float inv) {
+    constexpr float kMagic = 12582912.f + 128.f;
+    const uint32_t ta = __float_as_uint(fmaf(a, inv, kMagic)), tb = __float_as_uint(fmaf(b, inv, kMagic));
+    const uint32_t tc = __float_as_uint(fmaf(c, inv, kMagic)), td = __float_as_uint(fmaf(d, inv, kMagic));
+    return __byte_perm(__byte_perm(ta, tb, 0x0040), __byte_perm(tc, td, 0x0040), 0x5410);
+}
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 // ----------------------------------------------------------------- append ----
+
+// A lane's chunks of eight, 32 apart: row and column without a division each.
+struct ChunkWalk {
+    int row, c, dr, dc, cpr;  // c in chunks
+    __device__ __forceinline__ ChunkWalk(int lane, int cpr_) : cpr(cpr_) {
+        dr = 32 / cpr;
+        dc = 32 - dr * cpr;
+        row = lane / cpr;
+        c = lane - row * cpr;
+    }
+    __device__ __forceinline__ void next() {
+        row += dr;
+        c += dc;
+        if (c >= cpr) c -= cpr, ++row;
+    }
+};
 
 struct RowSpan {  // what one warp works on
     PageItem it;
@@ -153,6 +239,30 @@ __device__ __forceinline__ bool upload_runs(const PagesArgs &p, const PagedAddr 
     return true;
 }
 
+// The step of a page's head after rows of largest magnitude m (f32 bits) come
+// to offset off: stores the scale, brings the rows before them into a step that
+// grew, and returns 1 / step -- or 0 where there is none: a value that is not
+// finite has no element, so the scale becomes NaN, which every read of the
+// block and head returns until its first row is written again.
+__device__ __forceinline__ float new_step(uint32_t m, float old, int off, int cw, float *scale, uint8_t *page,
+                                          int kv_dim, int lane) {
+    if (m >= kInfBits || abs_bits(old) >= kInfBits) {
+        if (lane == 0) *scale = __uint_as_float(0x7fc00000u);
+        return 0.f;
+    }
+    const int e_old = scale_exp(old), e = off > 0 ? max(e_old, need_exp(m)) : need_exp(m);
+    if (lane == 0) *scale = pow2f(e);
+    if (off > 0 && e > e_old) {
+        const float f = pow2f(max(-126, e_old - e));
+        for (int i = lane; i < off * cw; i += 32) {
+            const int row = i / cw, c = i - row * cw;
+            uint8_t *u = page + static_cast<size_t>(row) * kv_dim + c;
+            *u = static_cast<uint8_t>(q8_elem(static_cast<float>(static_cast<int>(*u) - 128), f));
+        }
+    }
+    return pow2f(-e);
+}
+
 template <class S, class E, bool kVec>
 __global__ void __launch_bounds__(256) append_pages_kernel(PagesArgs p, PagedAddr a, int n_groups) {
     if (upload_runs(p, a)) return;
@@ -170,8 +280,10 @@ __global__ void __launch_bounds__(256) append_pages_kernel(PagesArgs p, PagedAdd
     const float inv = 1.f / a.kv_scale;  // a power of two (1 except on fp8 pools)
     if constexpr (kVec) {
         const int cpr = r.cw >> 3;
-        for (int i = lane; i < r.it.n * cpr; i += 32) {
-            const int row = i / cpr, c = (i - row * cpr) * 8;
+        ChunkWalk w8(lane, cpr);
+#pragma unroll 4
+        for (int i = lane; i < r.it.n * cpr; i += 32, w8.next()) {
+            const int row = w8.row, c = w8.c * 8;
             float x[8];
             load8(src + row * stride + c, x);
 #pragma unroll
@@ -205,16 +317,14 @@ __global__ void __launch_bounds__(256) append_pages_q8_kernel(PagesArgs p, Q8Add
     float *scale = (r.is_v ? q.vs : q.ks) + static_cast<int64_t>(r.it.blk) * q.scale_stride + r.c0 / q.hd;
     const float old = r.it.off > 0 ? *scale : 0.f;
 
+    // the rows are read twice, for their largest magnitude and to store them
+    const int cpr = kVec ? r.cw >> 3 : 1, n_ch = r.it.n * cpr;
     uint32_t m = 0;
     if constexpr (kVec) {
-        const int cpr = r.cw >> 3;
-        for (int i = lane; i < r.it.n * cpr; i += 32) {
-            const int row = i / cpr, c = (i - row * cpr) * 8;
-            float x[8];
-            load8(src + row * stride + c, x);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m = max(m, abs_bits(x[j]));
-        }
+        ChunkWalk w8(lane, cpr);
+#pragma unroll 4
+        for (int i = lane; i < n_ch; i += 32, w8.next()) m = max_raw(m, fetch8(src + w8.row * stride + w8.c * 8));
+        m = max_bits<S>(m);
     } else {
         for (int i = lane; i < r.it.n * r.cw; i += 32) {
             const int row = i / r.cw, c = i - row * r.cw;
@@ -222,39 +332,115 @@ __global__ void __launch_bounds__(256) append_pages_q8_kernel(PagesArgs p, Q8Add
         }
     }
     m = __reduce_max_sync(0xffffffffu, m);
-    // a value that is not finite has no element: the scale becomes NaN, which
-    // every read of the block and head returns until its first row is written again
-    const bool bad = m >= kInfBits || abs_bits(old) >= kInfBits;
-    const int e_old = scale_exp(old);
-    const int e = bad ? 0 : r.it.off > 0 ? max(e_old, need_exp(m)) : need_exp(m);
-    const float inv = pow2f(-e);
-    if (lane == 0) *scale = bad ? __uint_as_float(0x7fc00000u) : pow2f(e);
-    if (r.it.off > 0 && !bad && e > e_old) {  // the step grew: the kept rows in the new step
-        const float f = pow2f(max(-126, e_old - e));
-        for (int i = lane; i < r.it.off * r.cw; i += 32) {
-            const int row = i / r.cw, c = i - row * r.cw;
-            uint8_t *u = page + static_cast<size_t>(row) * a.kv_dim + c;
-            *u = static_cast<uint8_t>(q8_elem(static_cast<float>(static_cast<int>(*u) - 128), f));
-        }
-    }
+    const float inv = new_step(m, old, r.it.off, r.cw, scale, page, a.kv_dim, lane);
+    const bool bad = inv == 0.f;
     if constexpr (kVec) {
-        const int cpr = r.cw >> 3;
-        for (int i = lane; i < r.it.n * cpr; i += 32) {
-            const int row = i / cpr, c = (i - row * cpr) * 8;
+        ChunkWalk w8(lane, cpr);
+#pragma unroll 4
+        for (int i = lane; i < n_ch; i += 32, w8.next()) {
             float x[8];
-            load8(src + row * stride + c, x);
-            uint32_t lo = 0x80808080u, hi = 0x80808080u;
-            if (!bad) {
-                lo = q8_elem(x[0], inv) | q8_elem(x[1], inv) << 8 | q8_elem(x[2], inv) << 16 | q8_elem(x[3], inv) << 24;
-                hi = q8_elem(x[4], inv) | q8_elem(x[5], inv) << 8 | q8_elem(x[6], inv) << 16 | q8_elem(x[7], inv) << 24;
-            }
-            *reinterpret_cast<uint2 *>(dst + static_cast<size_t>(row) * a.kv_dim + c) = make_uint2(lo, hi);
+            widen8(fetch8(src + w8.row * stride + w8.c * 8), x);
+            uint2 u = make_uint2(q8_word(x[0], x[1], x[2], x[3], inv), q8_word(x[4], x[5], x[6], x[7], inv));
+            if (bad) u = make_uint2(0x80808080u, 0x80808080u);
+            *reinterpret_cast<uint2 *>(dst + static_cast<size_t>(w8.row) * a.kv_dim + w8.c * 8) = u;
         }
     } else {
         for (int i = lane; i < r.it.n * r.cw; i += 32) {
             const int row = i / r.cw, c = i - row * r.cw;
             dst[static_cast<size_t>(row) * a.kv_dim + c] =
                 bad ? 128 : static_cast<uint8_t>(q8_elem(load1(src + row * stride + c), inv));
+        }
+    }
+}
+
+// The same where a head's chunks of eight divide a warp and a page's fit in
+// kHold a lane (16 rows of 128): a warp keeps its (head, K or V) and walks the
+// items with a stride, holding one item's rows in registers while the next
+// one's are on their way, so that every warp has a page in flight all the time.
+// (With one item a warp, loads in flight only part of its life, an append of
+// 130,000 rows took 183 us; held in registers without the walk 188-218.)
+template <class S, int kHold, bool kAhead>
+__global__ void __launch_bounds__(256, 2) append_stream_q8_kernel(PagesArgs p, Q8Addr q, int n_warps) {
+    const PagedAddr &a = q.a;
+    if (upload_runs(p, a)) return;
+    const int w = (static_cast<int>(blockIdx.x) - p.n_runs) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int per_item = 2 * q.n_kv, step = n_warps / per_item;  // n_warps: a multiple of per_item
+    int it = w / per_item;
+    const int sub = w - it * per_item;
+    if (it >= p.n_items) return;
+    const bool is_v = sub >= q.n_kv;
+    const int head = is_v ? sub - q.n_kv : sub;
+    const int64_t stride = is_v ? p.v_stride : p.k_stride;
+    const int cpr = q.hd >> 3, dr = 32 / cpr, row0 = lane / cpr, c0 = (lane - row0 * cpr) * 8;
+    const S *const src = static_cast<const S *>(is_v ? p.V : p.K) + head * q.hd + row0 * stride + c0;
+    uint8_t *const pool = static_cast<uint8_t *>(is_v ? a.v : a.k) + a.layer_off + head * q.hd;
+    float *const scales = (is_v ? q.vs : q.ks) + head;
+    auto item = [&](int i) {
+        const int4 x = __ldg(reinterpret_cast<const int4 *>(p.items + i));
+        PageItem t{x.x, x.y, x.z, x.w};
+        if (static_cast<unsigned>(t.blk) >= static_cast<unsigned>(a.n_blocks) || t.off < 0 || t.n <= 0 ||
+            t.off + t.n > a.bs) {
+            if (lane == 0 && p.err) atomicOr(p.err, 1);
+            t.n = 0;
+        }
+        return t;
+    };
+    auto fetch = [&](const PageItem &t, Raw8<S> (&h)[kHold]) {
+        const S *at = src + static_cast<int64_t>(t.row0) * stride;
+#pragma unroll
+        for (int k = 0; k < kHold; ++k)
+            if (row0 + k * dr < t.n) h[k] = fetch8(at + k * dr * stride);
+    };
+    auto put = [&](const PageItem &t, const Raw8<S> (&h)[kHold]) {
+        if (t.n == 0) return;
+        float *scale = scales + static_cast<int64_t>(t.blk) * q.scale_stride;
+        uint8_t *page = pool + static_cast<size_t>(t.blk) * a.block_stride;
+        const float old = t.off > 0 ? *scale : 0.f;
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < kHold; ++k)
+            if (row0 + k * dr < t.n) m = max_raw(m, h[k]);
+        m = __reduce_max_sync(0xffffffffu, max_bits<S>(m));
+        const float inv = new_step(m, old, t.off, q.hd, scale, page, a.kv_dim, lane);
+        uint8_t *dst = page + static_cast<size_t>(t.off + row0) * a.kv_dim + c0;
+#pragma unroll
+        for (int k = 0; k < kHold; ++k) {
+            if (row0 + k * dr >= t.n) continue;
+            float x[8];
+            widen8(h[k], x);
+            uint2 u = make_uint2(q8_word(x[0], x[1], x[2], x[3], inv), q8_word(x[4], x[5], x[6], x[7], inv));
+            if (inv == 0.f) u = make_uint2(0x80808080u, 0x80808080u);
+            *reinterpret_cast<uint2 *>(dst + static_cast<size_t>(k * dr) * a.kv_dim) = u;
+        }
+    };
+    Raw8<S> h0[kHold];
+    if constexpr (!kAhead) {
+        for (; it < p.n_items; it += step) {
+            const PageItem t = item(it);
+            fetch(t, h0);
+            put(t, h0);
+        }
+        return;
+    } else {
+        Raw8<S> h1[kHold];
+        PageItem t0 = item(it), t1;
+        fetch(t0, h0);
+        while (true) {  // two items a turn, each buffer's registers its own
+            const bool more1 = it + step < p.n_items;
+            if (more1) {
+                t1 = item(it + step);
+                fetch(t1, h1);
+            }
+            put(t0, h0);
+            if (!more1) return;
+            it += 2 * step;
+            const bool more0 = it < p.n_items;
+            if (more0) {
+                t0 = item(it);
+                fetch(t0, h0);
+            }
+            put(t1, h1);
+            if (!more0) return;
         }
     }
 }
@@ -276,8 +462,10 @@ __global__ void __launch_bounds__(256) read_pages_kernel(PagesArgs p, PagedAddr 
                    a.layer_off + static_cast<size_t>(r.it.off) * a.kv_dim + r.c0;
     if constexpr (kVec) {
         const int cpr = r.cw >> 3;
-        for (int i = lane; i < r.it.n * cpr; i += 32) {
-            const int row = i / cpr, c = (i - row * cpr) * 8;
+        ChunkWalk w8(lane, cpr);
+#pragma unroll 4
+        for (int i = lane; i < r.it.n * cpr; i += 32, w8.next()) {
+            const int row = w8.row, c = w8.c * 8;
             float x[8];
             pool8(src + static_cast<size_t>(row) * a.kv_dim + c, x);
 #pragma unroll
@@ -309,15 +497,24 @@ __global__ void __launch_bounds__(256) read_pages_q8_kernel(PagesArgs p, Q8Addr 
                          static_cast<size_t>(r.it.off) * a.kv_dim + r.c0;
     const float sc = __ldg((r.is_v ? q.vs : q.ks) + static_cast<int64_t>(r.it.blk) * q.scale_stride + r.c0 / q.hd);
     if constexpr (kVec) {
-        const int cpr = r.cw >> 3;
-        for (int i = lane; i < r.it.n * cpr; i += 32) {
-            const int row = i / cpr, c = (i - row * cpr) * 8;
-            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src + static_cast<size_t>(row) * a.kv_dim + c));
-            float x[8];
+        constexpr int kFly = 8;  // chunks on the way at once
+        const int cpr = r.cw >> 3, n_ch = r.it.n * cpr;
+        ChunkWalk wl(lane, cpr), ws = wl;
+        for (int i0 = lane; i0 < n_ch; i0 += 32 * kFly) {
+            uint2 u[kFly];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                x[j] = static_cast<float>(static_cast<int>((j < 4 ? u.x : u.y) >> (8 * (j & 3)) & 255u) - 128) * sc;
-            store8(dst + row * stride + c, x);
+            for (int k = 0; k < kFly; ++k, wl.next())
+                if (i0 + 32 * k < n_ch)
+                    u[k] = __ldg(reinterpret_cast<const uint2 *>(src + static_cast<size_t>(wl.row) * a.kv_dim + wl.c * 8));
+#pragma unroll
+            for (int k = 0; k < kFly; ++k, ws.next()) {
+                if (i0 + 32 * k >= n_ch) continue;
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    x[j] = static_cast<float>(static_cast<int>((j < 4 ? u[k].x : u[k].y) >> (8 * (j & 3)) & 255u) - 128) * sc;
+                store8(dst + ws.row * stride + ws.c * 8, x);
+            }
         }
     } else {
         for (int i = lane; i < r.it.n * r.cw; i += 32) {
@@ -401,6 +598,17 @@ cudaError_t append_from(const PagesArgs &p, const PagedAddr &a, cudaStream_t s) 
 template <class S>
 cudaError_t append_q8_from(const PagesArgs &p, const Q8Addr &q, cudaStream_t s) {
     unsigned grid;
+    constexpr int kHold = 8;
+    const int cpr = q.hd / 8;
+    if (vec_ok(p, q.a, q.hd) && q.a.kv_dim % 8 == 0 && cpr <= 32 && 32 % cpr == 0 && q.a.bs * cpr <= 32 * kHold) {
+        // a whole number of items (and blocks) per round of warps, two blocks a SM
+        const long long warps = 2LL * p.n_items * q.n_kv, round = 16LL * q.n_kv;  // 8 items, 2 n_kv blocks
+        const long long want = std::min<long long>((warps + round - 1) / round, std::max<long long>(1, 2LL * 152 * 8 / round));
+        const int n_warps = static_cast<int>(want * round);
+        if (!grid_of(n_warps, p.n_runs, &grid)) return cudaErrorInvalidConfiguration;
+        append_stream_q8_kernel<S, kHold, sizeof(S) == 2><<<grid, 256, 0, s>>>(p, q, n_warps);
+        return cudaGetLastError();
+    }
     if (!grid_of(2LL * p.n_items * q.n_kv, p.n_runs, &grid)) return cudaErrorInvalidConfiguration;
     if (vec_ok(p, q.a, q.hd)) append_pages_q8_kernel<S, true><<<grid, 256, 0, s>>>(p, q);
     else append_pages_q8_kernel<S, false><<<grid, 256, 0, s>>>(p, q);

@@ -582,84 +582,117 @@ cudaError_t launch_fast_hd(const AttnArgs &a, const Q8Addr &q, cudaStream_t s) {
 // -------------------------------------------------------------- split pass ----
 //
 // Operand images for the tensor-core launches (the layout of kImageBytes): one
-// CTA per (64-key tile, kv head, K or V).  The tile's values go to shared
-// memory as f32 (zero past the row's keys), the block finds their largest
-// magnitude, and each value times the tile's power of two is an f16 value --
-// seven bits, unless it lies more than 2^28 below the tile's largest -- so
-// piece 1 is left out, as on the other narrow pools.
+// CTA per (64-key tile, kv head).  The images' power of two needs no look at
+// the values: with 2^t the tile's largest scale every magnitude is at most
+// 127 * 2^t, so 2^(8 - t) brings them below 2^15, and (u - 128) * 2^(8 - t + e)
+// is an f16 value, seven bits -- unless the key's scale 2^e lies more than 2^25
+// below the tile's, where its last bits are dropped -- so piece 1 is left out,
+// as on the other narrow pools.  K goes straight to its image; V's bytes turn
+// through shared memory.
 
 constexpr int kHDI = 128;
+constexpr int kVPitch = 132;  // bytes from key to key: four keys on, another bank
 
-__device__ __forceinline__ uint32_t f16x2(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
+// four bytes as (u - 128) times the pair of powers of two s2, in f16 (exact)
+__device__ __forceinline__ uint2 widen4(uint32_t w, __half2 s2) {
+    const uint32_t lo = widen2<0x4140>(w), hi = widen2<0x4342>(w);
+    const __half2 a = __hmul2(*reinterpret_cast<const __half2 *>(&lo), s2), b = __hmul2(*reinterpret_cast<const __half2 *>(&hi), s2);
+    return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
 __global__ void __launch_bounds__(256) split_q8_kernel(SplitArgs p, Q8Addr q) {
-    extern __shared__ __align__(16) float raw[];
-    __shared__ float wmax[8];
-    const int part = blockIdx.x & 1;  // 0: K, 1: V
-    const int ik = blockIdx.x >> 1, it = ik / p.n_kv, kvh = ik - it * p.n_kv;
+    __shared__ __align__(16) uint8_t vs[kKeyTile * kVPitch];
+    __shared__ int64_t row_of[kKeyTile];
+    __shared__ __half kf[kKeyTile], vf[kKeyTile];  // each key's factor
+    __shared__ float top[2][2];
+    const int it = blockIdx.x / p.n_kv, kvh = blockIdx.x - it * p.n_kv;
     const SplitItem t = p.items[it];
     const RowDesc rd = p.rows[t.row];
-    const int total_k = rd.past_len + rd.n_q, key0 = t.kt * kKeyTile;
-    const int ld = part ? kHDI + 1 : kHDI;  // V is read transposed: an odd pitch has no bank conflicts
-    const uint8_t *base = static_cast<const uint8_t *>(part ? q.a.v : q.a.k);
-    const float *scales = part ? q.vs : q.ks;
-    float mx = 0.f;
-#pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {  // 64 keys x 8 chunks of 16 elements
-        const int i = threadIdx.x + 256 * pass, key = i >> 3, ch = i & 7, pos = key0 + key;
-        uint4 u = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-        float sc = 0.f;
-        if (pos < total_k) {
+    const int tid = threadIdx.x;
+    float ks = 0.f, vsc = 0.f;
+    if (tid < kKeyTile) {  // two warps: the keys' rows and scales
+        const int pos = t.kt * kKeyTile + tid;
+        int64_t o = -1;
+        if (pos < rd.past_len + rd.n_q) {
             const int blk = block_of(q.a, rd.slot, pos, p.err);
             if (blk >= 0) {
-                u = __ldg(reinterpret_cast<const uint4 *>(base + static_cast<size_t>(blk) * q.a.block_stride +
-                                                          q.a.layer_off +
-                                                          static_cast<size_t>(block_off(q.a, pos)) * q.a.kv_dim +
-                                                          static_cast<size_t>(kvh) * kHDI + 16 * ch));
-                sc = __ldg(scales + blk * q.scale_stride + kvh);
+                o = static_cast<int64_t>(blk) * q.a.block_stride + q.a.layer_off +
+                    static_cast<int64_t>(block_off(q.a, pos)) * q.a.kv_dim + static_cast<int64_t>(kvh) * kHDI;
+                ks = __ldg(q.ks + blk * q.scale_stride + kvh);
+                vsc = __ldg(q.vs + blk * q.scale_stride + kvh);
             }
         }
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        float *d = raw + key * ld + 16 * ch;
+        row_of[tid] = o;
+        float mk = ks, mv = vsc;  // fmaxf passes over a NaN scale
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float x = static_cast<float>(static_cast<int>(w[j >> 2] >> (8 * (j & 3)) & 255u) - 128) * sc;
-            mx = fmaxf(mx, fabsf(x));
-            d[j] = x;
+        for (int x = 16; x > 0; x >>= 1) {
+            mk = fmaxf(mk, __shfl_xor_sync(kFull, mk, x));
+            mv = fmaxf(mv, __shfl_xor_sync(kFull, mv, x));
         }
+        if ((tid & 31) == 0) top[0][tid >> 5] = mk, top[1][tid >> 5] = mv;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-    if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = mx;
     __syncthreads();
-    mx = wmax[0];
+    int ex[2];
 #pragma unroll
-    for (int w = 1; w < 8; ++w) mx = fmaxf(mx, wmax[w]);
-    // the power of two that brings the largest magnitude into [2^14, 2^15)
-    const int ex = max(-113, min(126, 14 - (static_cast<int>((__float_as_uint(mx) >> 23) & 255u) - 127)));
-    const float sc = pow2f(ex);
-    unsigned char *img = p.img + (static_cast<size_t>(t.slot) * p.n_kv + kvh) * kImageBytes;
-    unsigned char *out = img + static_cast<size_t>(part) * 2 * kImagePlane;
-    for (int c = threadIdx.x; c < static_cast<int>(kImagePlane / 16); c += blockDim.x) {
-        float x[8];
-        if (part == 0) {  // K: k-block c >> 9 (64 dims), key (c >> 3) & 63, swizzled chunk c & 7
-            const int r = (c >> 3) & 63;
-            const float *src = raw + r * kHDI + (c >> 9) * 64 + ((c & 7) ^ (r & 7)) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = src[j];
-        } else {          // V^T: dim c >> 3, swizzled chunk c & 7 (8 keys)
-            const int d = c >> 3, k0 = ((c & 7) ^ (d & 7)) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = raw[(k0 + j) * (kHDI + 1) + d];
-        }
-        *reinterpret_cast<uint4 *>(out + c * 16) =
-            make_uint4(f16x2(x[0] * sc, x[1] * sc), f16x2(x[2] * sc, x[3] * sc), f16x2(x[4] * sc, x[5] * sc),
-                       f16x2(x[6] * sc, x[7] * sc));
+    for (int i = 0; i < 2; ++i) {
+        const float m = fmaxf(top[i][0], top[i][1]);
+        ex[i] = max(-113, min(126, 8 - (static_cast<int>((__float_as_uint(m) >> 23) & 255u) - 127)));
     }
-    if (threadIdx.x == 0) reinterpret_cast<int32_t *>(img + kImageExpOff)[part] = ex;
+    if (tid < kKeyTile) {
+        // scale * 2^ex <= 2^8; f16 keeps 2^-24, and a NaN
+        kf[tid] = __float2half_rn(ks * pow2f(ex[0]));
+        vf[tid] = __float2half_rn(vsc * pow2f(ex[1]));
+    }
+    // V's bytes (and zeros, u = 128, past the row's keys)
+    for (int i = tid; i < kKeyTile * 8; i += 256) {
+        const int key = i >> 3, ch = i & 7;
+        const int64_t o = row_of[key];
+        uint4 u = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+        if (o >= 0) u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(q.a.v) + o + 16 * ch));
+        uint32_t *d = reinterpret_cast<uint32_t *>(vs + key * kVPitch + 16 * ch);
+        d[0] = u.x, d[1] = u.y, d[2] = u.z, d[3] = u.w;
+    }
+    __syncthreads();
+    unsigned char *img = p.img + (static_cast<size_t>(t.slot) * p.n_kv + kvh) * kImageBytes;
+    // K: k-block c >> 9 (64 dims), key (c >> 3) & 63, swizzled chunk c & 7
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(kImagePlane / 16) / 256; ++i) {
+        const int c = tid + 256 * i, r = (c >> 3) & 63;
+        const int64_t o = row_of[r];
+        uint2 u = make_uint2(0x80808080u, 0x80808080u);
+        if (o >= 0)
+            u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(q.a.k) + o + (c >> 9) * 64 +
+                                                      ((c & 7) ^ (r & 7)) * 8));
+        const __half2 f = __half2half2(kf[r]);
+        const uint2 a = widen4(u.x, f), b = widen4(u.y, f);
+        *reinterpret_cast<uint4 *>(img + c * 16) = make_uint4(a.x, a.y, b.x, b.y);
+    }
+    // V^T: four dims d .. d + 3 of eight keys k0 .. at a time: a word of each key,
+    // each dim's eight values together one chunk of the image (dim row, chunk
+    // k0 / 8 at its swizzled place)
+    const int d = 4 * (tid >> 3), k0 = 8 * (tid & 7);
+    uint32_t w[8];
+    __half2 f[4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = *reinterpret_cast<const uint32_t *>(vs + (k0 + j) * kVPitch + d);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = __halves2half2(vf[k0 + 2 * j], vf[k0 + 2 * j + 1]);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        uint32_t y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            // byte x of two keys' words beside one another
+            const uint32_t two = __byte_perm(w[2 * j], w[2 * j + 1], x | (4 + x) << 4);
+            const uint32_t h = widen2<0x4140>(two);
+            const __half2 z = __hmul2(*reinterpret_cast<const __half2 *>(&h), f[j]);
+            y[j] = *reinterpret_cast<const uint32_t *>(&z);
+        }
+        const int dd = d + x;
+        *reinterpret_cast<uint4 *>(img + 2 * kImagePlane + (dd * 8 + ((k0 >> 3) ^ (dd & 7))) * 16) =
+            make_uint4(y[0], y[1], y[2], y[3]);
+    }
+    if (tid < 2) reinterpret_cast<int32_t *>(img + kImageExpOff)[tid] = ex[tid];
 }
 
 }  // namespace
@@ -683,11 +716,10 @@ cudaError_t launch_decode_q8(const AttnArgs &a, const Q8Addr &q, cudaStream_t s)
 }
 
 cudaError_t launch_split_q8(const SplitArgs &a, const Q8Addr &q, cudaStream_t s) {
-    constexpr size_t smem = static_cast<size_t>(kKeyTile) * (kHDI + 1) * sizeof(float);
     if (q.hd != kHDI) return cudaErrorInvalidValue;
-    const long long grid = static_cast<long long>(a.n_items) * a.n_kv * 2;
+    const long long grid = static_cast<long long>(a.n_items) * a.n_kv;
     if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    split_q8_kernel<<<static_cast<unsigned>(grid), 256, smem, s>>>(a, q);
+    split_q8_kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(a, q);
     return cudaGetLastError();
 }
 
