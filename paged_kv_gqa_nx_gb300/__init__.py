@@ -169,28 +169,35 @@ def _dev(t, name="tensor", dtypes=("float32",)):
     return t.data_ptr()
 
 
-_PACKED = {"float32": PKV_F32, "bfloat16": PKV_BF16, "float16": PKV_F16}
+_packed = {}  # torch dtype -> PKV_F32 ..., filled at the first use
 
 
-def _rows(t, name, width=None):
-    """(address, row stride, element type) of packed rows: a CUDA tensor
-    [rows, width] whose rows are contiguous (columns of a wider one are fine)."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
+def _rows(t, name, rows, width=None):
+    """(address, row stride, element type, width) of packed rows: a CUDA tensor
+    [at least `rows`, width] whose rows are contiguous (columns of a wider one
+    are fine)."""
+    if not _packed:
+        import torch
+        _packed.update({torch.float32: PKV_F32, torch.bfloat16: PKV_BF16, torch.float16: PKV_F16})
+    try:
+        kind, on_gpu, (n, w), (stride, inner) = _packed.get(t.dtype), t.is_cuda, t.shape, t.stride()
+    except (AttributeError, TypeError, ValueError):
+        raise TypeError("%s must be a CUDA tensor [rows, width]" % name) from None
+    if not on_gpu:
         raise TypeError("%s must be a CUDA tensor [rows, width]" % name)
-    kind = _PACKED.get(str(t.dtype).replace("torch.", ""))
     if kind is None:
         raise TypeError("%s must be float32, bfloat16 or float16" % name)
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if inner != 1 and w > 1:
         raise TypeError("%s must have contiguous rows" % name)
-    if width is not None and t.shape[1] != width:
+    if width is not None and w != width:
         raise TypeError("%s must be %d wide" % (name, width))
-    return t.data_ptr(), max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0), kind
+    if n < rows:
+        raise TypeError("%s has %d rows, %d are needed" % (name, n, rows))
+    return t.data_ptr(), stride if n > 1 else max(stride, w), kind, w
 
 
-def _enough(t, rows, name):
-    if t.shape[0] < rows:
-        raise TypeError("%s has %d rows, %d are needed" % (name, t.shape[0], rows))
+def _total(arr, n):
+    return arr[0] if n == 1 else sum(arr[:n])
 
 
 def _host(a, name="array"):
@@ -413,15 +420,13 @@ def pkv_attn_packed(Q, K, V, lens, n_heads, n_kv_heads, head_dim, causal, scale,
     float16 CUDA tensors with contiguous rows (any row stride); lens: tokens per sequence."""
     arr = _i32_array(lens)
     n = len(lens)
-    total = sum(arr[:n])
-    q, qs, t = _rows(Q, "Q", n_heads * head_dim)
-    k, ks, tk = _rows(K, "K", n_kv_heads * head_dim)
-    v, vs, tv = _rows(V, "V", n_kv_heads * head_dim)
-    o, os_, to = _rows(out, "out", n_heads * head_dim)
+    total = _total(arr, n)
+    q, qs, t, _ = _rows(Q, "Q", total, n_heads * head_dim)
+    k, ks, tk, _ = _rows(K, "K", total, n_kv_heads * head_dim)
+    v, vs, tv, _ = _rows(V, "V", total, n_kv_heads * head_dim)
+    o, os_, to, _ = _rows(out, "out", total, n_heads * head_dim)
     if not t == tk == tv == to:
         raise TypeError("Q, K, V and out must have one element type")
-    for x, name in ((Q, "Q"), (K, "K"), (V, "V"), (out, "out")):
-        _enough(x, total, name)
     return _lib.pkv_attn_packed(q, qs, k, ks, v, vs, t, arr, n, n_heads, n_kv_heads, head_dim, causal,
                                 scale, o, os_, _stream(stream))
 
@@ -430,26 +435,22 @@ def pkv_append_packed(seqs, n, layer, K, V):
     """K, V: [rows, kv_dim] float32, bfloat16 or float16 CUDA tensors with contiguous rows (any
     row stride), the batch's rows in order."""
     arr = _i32_array(n)
-    k, ks, t = _rows(K, "K")
-    v, vs, tv = _rows(V, "V")
-    if t != tv or K.shape[1] != V.shape[1]:
+    total = _total(arr, len(n))
+    k, ks, t, w = _rows(K, "K", total)
+    v, vs, tv, wv = _rows(V, "V", total)
+    if t != tv or w != wv:
         raise TypeError("K and V must have one element type and width")
-    total = sum(arr[:len(n)])
-    _enough(K, total, "K")
-    _enough(V, total, "V")
     return _lib.pkv_append_packed(_seq_array(seqs), len(seqs), arr, layer, k, ks, v, vs, t)
 
 
 def pkv_read_packed(seqs, start, n, layer, K, V):
     """Rows start[r] .. start[r] + n[r] - 1 of each sequence into K, V (as for pkv_append_packed)."""
     arr = _i32_array(n)
-    k, ks, t = _rows(K, "K")
-    v, vs, tv = _rows(V, "V")
-    if t != tv or K.shape[1] != V.shape[1]:
+    total = _total(arr, len(n))
+    k, ks, t, w = _rows(K, "K", total)
+    v, vs, tv, wv = _rows(V, "V", total)
+    if t != tv or w != wv:
         raise TypeError("K and V must have one element type and width")
-    total = sum(arr[:len(n)])
-    _enough(K, total, "K")
-    _enough(V, total, "V")
     return _lib.pkv_read_packed(_seq_array(seqs), len(seqs), _i32_array(start), arr, layer, k, ks, v, vs, t)
 
 

@@ -357,6 +357,7 @@ struct pkv_pool {
 
     Stager stager;
     DevBuf desc, part, io_in, io_out, qrot, krot, img;
+    DevBuf counters;  // of the 8-bit decode kernels: zero between launches
     Blob blob;
 
     int64_t block_floats() const { return static_cast<int64_t>(n_layers) * bs * kv_dim; }  // elements
@@ -497,8 +498,18 @@ struct WorkList {
     std::vector<PrefillTile> ctiles;  // shared-prefix pass (non-causal, split S)
     std::vector<MergeDesc> merges;   // queries with several splits (decode first, then prefill)
     std::vector<MergeDesc> pmerges;  // prefill items while building
+    size_t n_dec_merges = 0;         // items of decode units, first in `merges`
     int64_t n_part = 0;
 };
+
+// Rows of an 8-bit pool with few keys are cut into shorter splits than long
+// ones: a row's splits depend on its own length alone.
+struct ShortRows {
+    int32_t len = 0, S = 0;  // rows of at most len keys take splits of S
+};
+int32_t split_of(const RowDesc &rd, int32_t S, const ShortRows &sh) {
+    return rd.k0 == 0 && rd.past_len + rd.n_q <= sh.len ? sh.S : S;
+}
 
 // A run of consecutive single-query rows whose page tables start with the
 // same Lp / bs pages (shared through forks: a page id common to two live
@@ -734,7 +745,7 @@ void place_pairs(const std::vector<std::array<PrefillTile, 2>> &pairs, const std
 void build_work(std::vector<RowDesc> &rows, int causal, int32_t S, int32_t head_dim,
                 int32_t group, WorkList &w, const std::vector<Cascade> &cas = {},
                 int32_t prefix_split = 0, int32_t prefill_split = 0, bool allow_tc = true,
-                int32_t n_kv = 0, int32_t n_sm = 0, int32_t qblock = 1) {
+                int32_t n_kv = 0, int32_t n_sm = 0, int32_t qblock = 1, const ShortRows &short_rows = {}) {
     std::vector<UnitDesc> tail;
     w.units.clear();
     w.tiles.clear();
@@ -803,7 +814,7 @@ void build_work(std::vector<RowDesc> &rows, int causal, int32_t S, int32_t head_
             const int32_t nb = std::min(qblock, rd.n_q - i);
             const int32_t q_pos = total_k - rd.n_q + i + nb - 1;
             const int32_t nk = causal ? q_pos + 1 : total_k;
-            const int32_t ns = ceil_div(nk, S);
+            const int32_t ns = ceil_div(nk, split_of(rd, S, short_rows));
             if (ns == 1) {
                 tail.push_back({r, i, 0, -1});
             } else {
@@ -823,15 +834,47 @@ void build_work(std::vector<RowDesc> &rows, int causal, int32_t S, int32_t head_
     {
         std::vector<std::pair<int32_t, int32_t>> key(w.units.size());
         for (size_t i = 0; i < w.units.size(); ++i)
-            key[i] = {-unit_keys(w.units[i], rows[w.units[i].row], causal, S), static_cast<int32_t>(i)};
+            key[i] = {-unit_keys(w.units[i], rows[w.units[i].row], causal,
+                                 split_of(rows[w.units[i].row], S, short_rows)),
+                      static_cast<int32_t>(i)};
         std::sort(key.begin(), key.end());
         std::vector<UnitDesc> sorted(w.units.size());
         for (size_t i = 0; i < key.size(); ++i) sorted[i] = w.units[key[i].second];
         w.units.swap(sorted);
     }
     // one merge list: decode items first (units refer to them by index), then prefill items
+    w.n_dec_merges = w.merges.size();
     w.merges.insert(w.merges.end(), w.pmerges.begin(), w.pmerges.end());
     w.pmerges.clear();
+}
+
+// The decode units of an 8-bit pool's call as its kernels take them: ranges
+// worked out, every block of units with its merge records and its counters
+// (n_cnt of them a block).
+void q8_units(const WorkList &w, const std::vector<RowDesc> &rows, int32_t causal, int32_t S, const ShortRows &sh,
+              int32_t qblock, int32_t n_cnt, std::vector<Q8Unit> &out, int32_t *max_q, int64_t *counters) {
+    std::vector<int32_t> block_of(w.n_dec_merges, -1);
+    int32_t blocks = 0;
+    out.reserve(w.units.size());
+    for (const UnitDesc &u : w.units) {
+        const RowDesc &rd = rows[u.row];
+        const int32_t nb = std::min(qblock, rd.n_q - u.qi), S_r = split_of(rd, S, sh);
+        const int32_t kbeg = rd.k0 + (u.split - rd.s0) * S_r;
+        const int32_t lim = causal ? rd.past_len + u.qi + nb : rd.past_len + rd.n_q;
+        Q8Unit x{rd.slot, rd.q_row0 + u.qi, nb, rd.past_len + u.qi + 1, kbeg, std::min(kbeg + S_r, lim), -1, 0, 0, 0, 0, 0};
+        if (u.item >= 0) {
+            const MergeDesc &m = w.merges[u.item];
+            if (block_of[u.item] < 0) block_of[u.item] = blocks++;
+            x.part0 = m.part0;
+            x.n_rec = m.n_split;
+            x.rec = u.split;
+            x.n_dec = m.n_split - rd.s0;
+            x.cnt = block_of[u.item] * n_cnt;
+        }
+        *max_q = std::max(*max_q, nb);
+        out.push_back(x);
+    }
+    *counters = static_cast<int64_t>(blocks) * n_cnt;
 }
 
 // The fused append may replace the page-table upload when every pending
@@ -888,6 +931,12 @@ cudaError_t upload_blob(pkv_pool *p) {
     cudaError_t e = p->desc.ensure(p->blob.size(), p->stream, p->device);
     if (e != cudaSuccess) return e;
     return p->stager.upload(p->desc.p, p->blob.b.data(), p->blob.b.size(), p->stream);
+}
+
+// An offset into an inline blob, in place of an address.
+template <class T>
+const T *blob_off(size_t off) {
+    return reinterpret_cast<const T *>(off);
 }
 
 template <class T>
@@ -1017,6 +1066,8 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
     // pieces, the 4-warp merge -- is amortised alike).  It depends on the
     // pool only, so a row's split boundaries are the same in any batch.
     const int32_t S_dec = std::min<int32_t>(65536, S * (p->fp8 || p->q8 ? 4 : p->bf16 ? 2 : 1));
+    ShortRows short_rows;
+    if (p->q8) short_rows = {8 * S, std::min<int32_t>(65536, 2 * S)};
     const int32_t group = attend ? n_heads / n_kv_heads : 0;
     std::vector<Cascade> cas;
     if (attend && g_cascade.load() != 0 && prefill_shape(head_dim, group))
@@ -1024,7 +1075,7 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
     const int32_t Sp = cas.empty() ? 0 : prefix_split_keys(cas, group, n_kv_heads, p->n_sm);
     if (attend)
         build_work(rows, causal, S_dec, head_dim, group, w, cas, Sp, S * kPrefillSplitFactor, true, n_kv_heads,
-                   p->n_sm, p->q8 ? q8_query_block(head_dim, group) : 1);
+                   p->n_sm, p->q8 ? q8_query_block(head_dim, group) : 1, short_rows);
     // the decode kernels that take the append themselves: the f32 kernel for
     // groups 1, 2, 4 and the narrow-pool kernel for its shapes (head_dim 128)
     const bool fuse_shape = head_dim == 128 && !p->q8 &&
@@ -1120,6 +1171,13 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
         p->last_work[8] = static_cast<int64_t>(split_items.size());
     }
 
+    std::vector<Q8Unit> qunits;
+    int32_t q8_max_q = 1;
+    int64_t n_counters = 0;
+    if (p->q8 && attend)
+        q8_units(w, rows, causal, S_dec, short_rows, q8_query_block(head_dim, group),
+                 q8_counters(head_dim, group, n_kv_heads), qunits, &q8_max_q, &n_counters);
+
     Blob &blob = p->blob;
     blob.clear();
     size_t runs_off = 0, vals_off = 0;
@@ -1127,18 +1185,27 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
     bool pt_write = false;
     if (fuse) pt_write = clear_dirty(p);
     else put_pt_runs(p, blob, &runs_off, &n_runs, &vals_off);
-    const size_t rows_off = blob.put(rows.data(), rows.size());
+    const bool tensor = !w.tiles.empty() || !w.ctiles.empty();
+    // an 8-bit pool's decode kernels join their splits themselves
+    const size_t first_merge = p->q8 ? w.n_dec_merges : 0, n_merges = w.merges.size() - first_merge;
+    const size_t rows_off = blob.put(rows.data(), p->q8 && !tensor && rope_base == 0.0 ? 0 : rows.size());
     const size_t app_off = blob.put(app.data(), app.size());
-    const size_t units_off = blob.put(w.units.data(), w.units.size());
+    const size_t units_off = blob.put(w.units.data(), p->q8 ? 0 : w.units.size());
+    const size_t qunits_off = blob.put(qunits.data(), qunits.size());
     const size_t tiles_off = blob.put(w.tiles.data(), w.tiles.size());
     const size_t ctiles_off = blob.put(w.ctiles.data(), w.ctiles.size());
-    const size_t merges_off = blob.put(w.merges.data(), w.merges.size());
+    const size_t merges_off = blob.put(w.merges.data() + first_merge, n_merges);
     const size_t tile0_off = blob.put(img_tile0.data(), img_tile0.size());
     const size_t slot_off = blob.put(img_slot.data(), img_slot.size());
     const size_t split_off = blob.put(split_items.data(), split_items.size());
     const size_t pages_off = blob.put(pages.data(), pages.size());
 
-    cudaError_t e = upload_blob(p);
+    // few descriptors of an 8-bit pool's append and decode travel with the launches
+    InlineBlob inl;
+    const bool inlined = p->q8 && !tensor && rope_base == 0.0 && blob.b.size() <= sizeof inl.b;
+    cudaError_t e = cudaSuccess;
+    if (inlined) std::memcpy(inl.b, blob.b.data(), blob.b.size());
+    else e = upload_blob(p);
     if (e != cudaSuccess) return cuda_fail(e, "descriptor upload");
 
     const float *Qd = Q, *Kd = K_new, *Vd = V_new;
@@ -1195,6 +1262,12 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
         }
         PagesArgs ap{dptr<PageItem>(p, pages_off), static_cast<int32_t>(pages.size()), const_cast<float *>(Kd),
                      const_cast<float *>(Vd), kv_dim, kv_dim, Elem::f32, pr.runs, pr.vals, n_runs, p->err_dev};
+        if (inlined) {
+            ap.items = blob_off<PageItem>(pages_off);
+            ap.runs = blob_off<PtRun>(runs_off);
+            ap.vals = blob_off<int32_t>(vals_off);
+            ap.blob = &inl;
+        }
         e = launch(PKV_KERNEL_APPEND, st, [&] { return launch_append_pages_q8(ap, q8_addr(p, layer), st); });
         if (e != cudaSuccess) return cuda_fail(e, "append kernel");
     } else if (!fuse) {
@@ -1278,15 +1351,39 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
         if (e != cudaSuccess) return cuda_fail(e, "shared-prefix kernel");
     }
     if (!w.units.empty()) {
-        for (const UnitDesc &u : w.units) a.max_q = std::max(a.max_q, rows[u.row].n_q);
+        if (p->q8 && n_counters > 0) {
+            const size_t had = p->counters.cap;
+            e = p->counters.ensure(static_cast<size_t>(n_counters) * sizeof(uint32_t), st, p->device);
+            if (e == cudaSuccess && p->counters.cap != had) e = cudaMemsetAsync(p->counters.p, 0, p->counters.cap, st);
+            if (e != cudaSuccess) return cuda_fail(e, "merge counters");
+        }
         e = launch(PKV_KERNEL_DECODE, st, [&] {
-            return p->q8 ? launch_decode_q8(a, q8_addr(p, layer), st) : launch_decode_paged(a, addr, st);
+            if (!p->q8) return launch_decode_paged(a, addr, st);
+            Q8Args x{};
+            x.Q = Qd;
+            x.out = Od;
+            x.units = inlined ? blob_off<Q8Unit>(qunits_off) : dptr<Q8Unit>(p, qunits_off);
+            x.n_units = static_cast<int32_t>(qunits.size());
+            x.max_q = q8_max_q;
+            x.pm = a.pm;
+            x.pl = a.pl;
+            x.pacc = a.pacc;
+            x.cnt = static_cast<uint32_t *>(p->counters.p);
+            x.n_heads = n_heads;
+            x.n_kv = n_kv_heads;
+            x.hd = head_dim;
+            x.group = a.group;
+            x.causal = a.causal;
+            x.scale_log2 = a.scale_log2;
+            x.err = p->err_dev;
+            x.blob = inlined ? &inl : nullptr;
+            return launch_decode_q8(x, q8_addr(p, layer), st);
         });
         if (e != cudaSuccess) return cuda_fail(e, "decode kernel");
     }
-    if (!w.merges.empty()) {
+    if (n_merges > 0) {
         MergeArgs m{a.pm, a.pl, a.pacc, Od, a.rows, dptr<MergeDesc>(p, merges_off),
-                    static_cast<int32_t>(w.merges.size()), n_heads, head_dim};
+                    static_cast<int32_t>(n_merges), n_heads, head_dim};
         e = launch(PKV_KERNEL_MERGE, st, [&] { return launch_merge(m, st); });
         if (e != cudaSuccess) return cuda_fail(e, "merge kernel");
     }
@@ -1609,6 +1706,7 @@ void pkv_pool_free(pkv_pool *p) {
         p->io_out.release(p->stream);
         p->qrot.release(p->stream);
         p->krot.release(p->stream);
+        p->counters.release(p->stream);
         p->img.release(p->stream);
         p->icache.buf.release(p->stream);
         cudaStreamSynchronize(p->stream);
@@ -2145,17 +2243,24 @@ int run_pages(pkv_seq *const *seqs, int32_t M, const int32_t *start, const int32
         put_pt_runs(p, blob, &runs_off, &a.n_runs, &vals_off);
     }
     const size_t items_off = blob.put(items.data(), items.size());
-    cudaError_t e = upload_blob(p);
+    InlineBlob inl;
+    cudaError_t e = cudaSuccess;
+    if (blob.b.size() <= sizeof inl.b) {  // few descriptors travel with the launch
+        std::memcpy(inl.b, blob.b.data(), blob.b.size());
+        a.blob = &inl;
+    } else {
+        e = upload_blob(p);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "descriptor upload");
-    a.items = dptr<PageItem>(p, items_off);
+    a.items = a.blob ? blob_off<PageItem>(items_off) : dptr<PageItem>(p, items_off);
     a.n_items = static_cast<int32_t>(items.size());
     a.K = K;
     a.V = V;
     a.k_stride = k_stride;
     a.v_stride = v_stride;
     a.type = type;
-    a.runs = dptr<PtRun>(p, runs_off);
-    a.vals = dptr<int32_t>(p, vals_off);
+    a.runs = a.blob ? blob_off<PtRun>(runs_off) : dptr<PtRun>(p, runs_off);
+    a.vals = a.blob ? blob_off<int32_t>(vals_off) : dptr<int32_t>(p, vals_off);
     a.err = p->err_dev;
     e = launch(append ? PKV_KERNEL_APPEND : PKV_KERNEL_COPY, st, [&] {
         if (p->q8)

@@ -82,6 +82,25 @@ struct PageItem {
     int32_t blk, off, n, row0;
 };
 
+// One decode unit over an 8-bit pool, as the host lays it out: queries q_row ..
+// q_row + nq - 1 (rows of Q and out), of which query t sees the keys below
+// see0 + t (causal) or kend, over keys [kbeg, kend).  part0 < 0: the unit is its
+// queries' only one and writes out; else its partial of query t is record
+// part0 + t * n_rec + rec, and the last of the block's n_dec units to finish (by
+// the counters cnt .. of the block) joins all n_rec records of each query.
+struct Q8Unit {
+    int32_t slot, q_row, nq, see0;
+    int32_t kbeg, kend, part0, n_rec;
+    int32_t rec, n_dec, cnt, pad;
+};
+
+// A call's descriptors where they are few: they travel in the launch's
+// parameters instead of through an upload.
+constexpr int32_t kInlineBytes = 3840;
+struct alignas(16) InlineBlob {
+    unsigned char b[kInlineBytes];
+};
+
 // Element types of packed rows (pkv_dtype) and of pool storage.
 enum class Elem : int32_t { f32 = 0, bf16 = 1, f16 = 2, fp8 = 3, q8 = 4 };
 
@@ -97,6 +116,23 @@ struct PagesArgs {
     const int32_t *vals = nullptr;
     int32_t n_runs = 0;
     int32_t *err = nullptr;
+    // With an inline blob, items, runs and vals are byte offsets into it (held
+    // in the pointers), which the kernels turn into addresses.
+    const InlineBlob *blob = nullptr;
+};
+
+// The decode launch over an 8-bit pool.
+struct Q8Args {
+    const float *Q;
+    float *out;
+    const Q8Unit *units;  // or a byte offset into the inline blob
+    int32_t n_units, max_q;
+    float *pm, *pl, *pacc;
+    uint32_t *cnt;        // zero between launches: the joining unit clears its own
+    int32_t n_heads, n_kv, hd, group, causal;
+    float scale_log2;
+    int32_t *err;
+    const InlineBlob *blob = nullptr;
 };
 
 // Rotated copies of the new rows (RoPE on append over an 8-bit pool, whose
@@ -158,7 +194,6 @@ struct AttnArgs {
     const float *K_new = nullptr, *V_new = nullptr;
     const AppendDesc *app = nullptr;
     int32_t pt_write = 0;
-    int32_t max_q = 1;  // the most queries a row of this launch's units has (8-bit pools)
 };
 
 // One tensor-core prefill tile: queries q0 .. q0 + 128/G - 1 of row `row`
@@ -305,10 +340,12 @@ cudaError_t launch_read_pages(const PagesArgs &a, const PagedAddr &addr, cudaStr
 cudaError_t launch_read_pages_q8(const PagesArgs &a, const Q8Addr &addr, cudaStream_t s);
 cudaError_t launch_rope_rows(const RopeArgs &a, cudaStream_t s);
 // Attention over an 8-bit pool with block scales (pkv_q8.cu): split-K decode
-// units of up to q8_query_block consecutive queries each (the unit's query qi
-// is its first; the queries of a unit with several splits have consecutive
-// merge items), and the split pass of the tensor-core launches.
-cudaError_t launch_decode_q8(const AttnArgs &a, const Q8Addr &addr, cudaStream_t s);
+// units of up to q8_query_block consecutive queries each, and the split pass of
+// the tensor-core launches.  The decode launch may start while the launch
+// before it on the stream (the append) still runs; q8_counters: the counters a
+// block of units needs.
+cudaError_t launch_decode_q8(const Q8Args &a, const Q8Addr &addr, cudaStream_t s);
+int q8_counters(int head_dim, int group, int n_kv);
 cudaError_t launch_split_q8(const SplitArgs &a, const Q8Addr &addr, cudaStream_t s);
 int q8_query_block(int head_dim, int group);
 // Packed prompt attention (pkv_packed.cu); sequences sorted longest first.

@@ -231,6 +231,20 @@ __device__ __forceinline__ RowSpan row_span(const PagesArgs &p, const PagedAddr 
     return r;
 }
 
+// Descriptors in device memory (NoBlob) or in the launch's parameters.
+struct NoBlob {};
+template <class B>
+__device__ __forceinline__ void place(PagesArgs &p, const B &blob) {
+    if constexpr (std::is_same<B, InlineBlob>::value) {
+        p.items = reinterpret_cast<const PageItem *>(blob.b + reinterpret_cast<uintptr_t>(p.items));
+        p.runs = reinterpret_cast<const PtRun *>(blob.b + reinterpret_cast<uintptr_t>(p.runs));
+        p.vals = reinterpret_cast<const int32_t *>(blob.b + reinterpret_cast<uintptr_t>(p.vals));
+    }
+}
+// A launch that may start while this one runs waits for its end before it
+// reads what this one writes; it may set itself up from now on.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
 __device__ __forceinline__ bool upload_runs(const PagesArgs &p, const PagedAddr &a) {
     if (static_cast<int>(blockIdx.x) >= p.n_runs) return false;
     const PtRun r = p.runs[blockIdx.x];
@@ -263,8 +277,10 @@ __device__ __forceinline__ float new_step(uint32_t m, float old, int off, int cw
     return pow2f(-e);
 }
 
-template <class S, class E, bool kVec>
-__global__ void __launch_bounds__(256) append_pages_kernel(PagesArgs p, PagedAddr a, int n_groups) {
+template <class B, class S, class E, bool kVec>
+__global__ void __launch_bounds__(256) append_pages_kernel(PagesArgs p, PagedAddr a, int n_groups, const __grid_constant__ B blob) {
+    place(p, blob);
+    let_next_start();
     if (upload_runs(p, a)) return;
     const int w = (static_cast<int>(blockIdx.x) - p.n_runs) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (w >= p.n_items * 2 * n_groups) return;
@@ -298,8 +314,10 @@ __global__ void __launch_bounds__(256) append_pages_kernel(PagesArgs p, PagedAdd
     }
 }
 
-template <class S, bool kVec>
-__global__ void __launch_bounds__(256) append_pages_q8_kernel(PagesArgs p, Q8Addr q) {
+template <class B, class S, bool kVec>
+__global__ void __launch_bounds__(256) append_pages_q8_kernel(PagesArgs p, Q8Addr q, const __grid_constant__ B blob) {
+    place(p, blob);
+    let_next_start();
     const PagedAddr &a = q.a;
     if (upload_runs(p, a)) return;
     const int w = (static_cast<int>(blockIdx.x) - p.n_runs) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -359,8 +377,10 @@ __global__ void __launch_bounds__(256) append_pages_q8_kernel(PagesArgs p, Q8Add
 // one's are on their way, so that every warp has a page in flight all the time.
 // (With one item a warp, loads in flight only part of its life, an append of
 // 130,000 rows took 183 us; held in registers without the walk 188-218.)
-template <class S, int kHold, bool kAhead>
-__global__ void __launch_bounds__(256, 2) append_stream_q8_kernel(PagesArgs p, Q8Addr q, int n_warps) {
+template <class B, class S, int kHold, bool kAhead>
+__global__ void __launch_bounds__(256, 2) append_stream_q8_kernel(PagesArgs p, Q8Addr q, int n_warps, const __grid_constant__ B blob) {
+    place(p, blob);
+    let_next_start();
     const PagedAddr &a = q.a;
     if (upload_runs(p, a)) return;
     const int w = (static_cast<int>(blockIdx.x) - p.n_runs) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -376,7 +396,7 @@ __global__ void __launch_bounds__(256, 2) append_stream_q8_kernel(PagesArgs p, Q
     uint8_t *const pool = static_cast<uint8_t *>(is_v ? a.v : a.k) + a.layer_off + head * q.hd;
     float *const scales = (is_v ? q.vs : q.ks) + head;
     auto item = [&](int i) {
-        const int4 x = __ldg(reinterpret_cast<const int4 *>(p.items + i));
+        const int4 x = *reinterpret_cast<const int4 *>(p.items + i);
         PageItem t{x.x, x.y, x.z, x.w};
         if (static_cast<unsigned>(t.blk) >= static_cast<unsigned>(a.n_blocks) || t.off < 0 || t.n <= 0 ||
             t.off + t.n > a.bs) {
@@ -447,8 +467,9 @@ __global__ void __launch_bounds__(256, 2) append_stream_q8_kernel(PagesArgs p, Q
 
 // ------------------------------------------------------------------- read ----
 
-template <class D, class E, bool kVec>
-__global__ void __launch_bounds__(256) read_pages_kernel(PagesArgs p, PagedAddr a, int n_groups) {
+template <class B, class D, class E, bool kVec>
+__global__ void __launch_bounds__(256) read_pages_kernel(PagesArgs p, PagedAddr a, int n_groups, const __grid_constant__ B blob) {
+    place(p, blob);
     const int w = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (w >= p.n_items * 2 * n_groups) return;
     const RowSpan r = row_span(p, a, kColGroup, n_groups, w);
@@ -480,8 +501,9 @@ __global__ void __launch_bounds__(256) read_pages_kernel(PagesArgs p, PagedAddr 
     }
 }
 
-template <class D, bool kVec>
-__global__ void __launch_bounds__(256) read_pages_q8_kernel(PagesArgs p, Q8Addr q) {
+template <class B, class D, bool kVec>
+__global__ void __launch_bounds__(256) read_pages_q8_kernel(PagesArgs p, Q8Addr q, const __grid_constant__ B blob) {
+    place(p, blob);
     const PagedAddr &a = q.a;
     const int w = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (w >= p.n_items * 2 * q.n_kv) return;
@@ -580,14 +602,24 @@ bool grid_of(long long warps, int n_runs, unsigned *grid) {
     return true;
 }
 
+// Calls f with the inline blob, or with none.
+template <class F>
+cudaError_t with_blob(const PagesArgs &p, F &&f) {
+    if (p.blob) f(*p.blob);
+    else f(NoBlob{});
+    return cudaGetLastError();
+}
+
 template <class S, class E>
 cudaError_t append_as(const PagesArgs &p, const PagedAddr &a, cudaStream_t s) {
     const int n_groups = (a.kv_dim + kColGroup - 1) / kColGroup;
     unsigned grid;
     if (!grid_of(2LL * p.n_items * n_groups, p.n_runs, &grid)) return cudaErrorInvalidConfiguration;
-    if (vec_ok(p, a, kColGroup)) append_pages_kernel<S, E, true><<<grid, 256, 0, s>>>(p, a, n_groups);
-    else append_pages_kernel<S, E, false><<<grid, 256, 0, s>>>(p, a, n_groups);
-    return cudaGetLastError();
+    return with_blob(p, [&](const auto &b) {
+        using B = std::decay_t<decltype(b)>;
+        if (vec_ok(p, a, kColGroup)) append_pages_kernel<B, S, E, true><<<grid, 256, 0, s>>>(p, a, n_groups, b);
+        else append_pages_kernel<B, S, E, false><<<grid, 256, 0, s>>>(p, a, n_groups, b);
+    });
 }
 template <class S>
 cudaError_t append_from(const PagesArgs &p, const PagedAddr &a, cudaStream_t s) {
@@ -606,22 +638,28 @@ cudaError_t append_q8_from(const PagesArgs &p, const Q8Addr &q, cudaStream_t s) 
         const long long want = std::min<long long>((warps + round - 1) / round, std::max<long long>(1, 2LL * 152 * 8 / round));
         const int n_warps = static_cast<int>(want * round);
         if (!grid_of(n_warps, p.n_runs, &grid)) return cudaErrorInvalidConfiguration;
-        append_stream_q8_kernel<S, kHold, sizeof(S) == 2><<<grid, 256, 0, s>>>(p, q, n_warps);
-        return cudaGetLastError();
+        return with_blob(p, [&](const auto &b) {
+            append_stream_q8_kernel<std::decay_t<decltype(b)>, S, kHold, sizeof(S) == 2>
+                <<<grid, 256, 0, s>>>(p, q, n_warps, b);
+        });
     }
     if (!grid_of(2LL * p.n_items * q.n_kv, p.n_runs, &grid)) return cudaErrorInvalidConfiguration;
-    if (vec_ok(p, q.a, q.hd)) append_pages_q8_kernel<S, true><<<grid, 256, 0, s>>>(p, q);
-    else append_pages_q8_kernel<S, false><<<grid, 256, 0, s>>>(p, q);
-    return cudaGetLastError();
+    return with_blob(p, [&](const auto &b) {
+        using B = std::decay_t<decltype(b)>;
+        if (vec_ok(p, q.a, q.hd)) append_pages_q8_kernel<B, S, true><<<grid, 256, 0, s>>>(p, q, b);
+        else append_pages_q8_kernel<B, S, false><<<grid, 256, 0, s>>>(p, q, b);
+    });
 }
 template <class D, class E>
 cudaError_t read_as(const PagesArgs &p, const PagedAddr &a, cudaStream_t s) {
     const int n_groups = (a.kv_dim + kColGroup - 1) / kColGroup;
     unsigned grid;
     if (!grid_of(2LL * p.n_items * n_groups, 0, &grid)) return cudaErrorInvalidConfiguration;
-    if (vec_ok(p, a, kColGroup)) read_pages_kernel<D, E, true><<<grid, 256, 0, s>>>(p, a, n_groups);
-    else read_pages_kernel<D, E, false><<<grid, 256, 0, s>>>(p, a, n_groups);
-    return cudaGetLastError();
+    return with_blob(p, [&](const auto &b) {
+        using B = std::decay_t<decltype(b)>;
+        if (vec_ok(p, a, kColGroup)) read_pages_kernel<B, D, E, true><<<grid, 256, 0, s>>>(p, a, n_groups, b);
+        else read_pages_kernel<B, D, E, false><<<grid, 256, 0, s>>>(p, a, n_groups, b);
+    });
 }
 template <class D>
 cudaError_t read_to(const PagesArgs &p, const PagedAddr &a, cudaStream_t s) {
@@ -633,9 +671,11 @@ template <class D>
 cudaError_t read_q8_to(const PagesArgs &p, const Q8Addr &q, cudaStream_t s) {
     unsigned grid;
     if (!grid_of(2LL * p.n_items * q.n_kv, 0, &grid)) return cudaErrorInvalidConfiguration;
-    if (vec_ok(p, q.a, q.hd)) read_pages_q8_kernel<D, true><<<grid, 256, 0, s>>>(p, q);
-    else read_pages_q8_kernel<D, false><<<grid, 256, 0, s>>>(p, q);
-    return cudaGetLastError();
+    return with_blob(p, [&](const auto &b) {
+        using B = std::decay_t<decltype(b)>;
+        if (vec_ok(p, q.a, q.hd)) read_pages_q8_kernel<B, D, true><<<grid, 256, 0, s>>>(p, q, b);
+        else read_pages_q8_kernel<B, D, false><<<grid, 256, 0, s>>>(p, q, b);
+    });
 }
 
 }  // namespace

@@ -14,6 +14,8 @@
 
 #include <algorithm>
 #include <cuda_fp16.h>
+#include <type_traits>
+#include <utility>
 
 namespace pkv {
 namespace {
@@ -38,6 +40,51 @@ __device__ __forceinline__ int block_off(const PagedAddr &a, int pos) {
     return a.bs_shift >= 0 ? (pos & (a.bs - 1)) : (pos % a.bs);
 }
 
+// ------------------------------------------------------------------ units ----
+
+struct NoBlob {};
+template <class B>
+__device__ __forceinline__ Q8Unit unit_of(const Q8Args &a, const B &blob, int i) {
+    const Q8Unit *u = a.units;
+    if constexpr (std::is_same<B, InlineBlob>::value)
+        u = reinterpret_cast<const Q8Unit *>(blob.b + reinterpret_cast<uintptr_t>(u));
+    return u[i];
+}
+// Waits for the end of the launch that this one was allowed to overlap.
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+
+// Whether this CTA's unit is the last of its block to finish; then every record
+// of the block can be read (through L2: other SMs wrote them).
+__device__ __forceinline__ bool last_of_block(const Q8Args &a, const Q8Unit &u, int part) {
+    __shared__ bool last;
+    __syncthreads();  // this CTA's records are written
+    if (threadIdx.x == 0) {
+        __threadfence();
+        uint32_t *c = a.cnt + u.cnt + part;
+        last = atomicAdd(c, 1u) == static_cast<uint32_t>(u.n_dec) - 1u;
+        if (last) *c = 0;
+        __threadfence();
+    }
+    __syncthreads();
+    return last;
+}
+// One (query, head) of a block by one warp: out = sum_s 2^(m_s - M) acc_s / sum_s
+// 2^(m_s - M) l_s over its records in ascending order.
+__device__ __forceinline__ void join_records(const Q8Args &a, const Q8Unit &u, int qi, int h, int lane) {
+    const int hd = a.hd;
+    auto rec = [&](int s) { return static_cast<size_t>(u.part0 + qi * u.n_rec + s) * a.n_heads + h; };
+    float M = -INFINITY, den = 0.f;
+    for (int s = 0; s < u.n_rec; ++s) M = fmaxf(M, __ldcg(a.pm + rec(s)));
+    for (int s = 0; s < u.n_rec; ++s) den = fmaf(exp2f(__ldcg(a.pm + rec(s)) - M), __ldcg(a.pl + rec(s)), den);
+    float *o = a.out + static_cast<size_t>(u.q_row + qi) * (a.n_heads * hd) + static_cast<size_t>(h) * hd;
+    for (int d = lane; d < hd; d += 32) {
+        float num = 0.f;
+#pragma unroll 4
+        for (int s = 0; s < u.n_rec; ++s) num = fmaf(exp2f(__ldcg(a.pm + rec(s)) - M), __ldcg(a.pacc + rec(s) * hd + d), num);
+        o[d] = num / den;
+    }
+}
+
 // --------------------------------------------------------- generic decode ----
 //
 // Any head width up to 256 and any group: CTA = 4 warps = one (unit, kv head,
@@ -47,33 +94,34 @@ __device__ __forceinline__ int block_off(const PagedAddr &a, int pos) {
 
 constexpr int kGW = 4, kGHeads = 16, kGDims = kMaxHeadDim / 32;
 
-__global__ void __launch_bounds__(128) decode_q8_generic_kernel(AttnArgs a, Q8Addr q, int hpc) {
+template <class B>
+__global__ void __launch_bounds__(128) decode_q8_generic_kernel(Q8Args a, Q8Addr q, int hpc,
+                                                                const __grid_constant__ B blob) {
     extern __shared__ __align__(16) float sm[];
     const int n_chunks = (a.group + hpc - 1) / hpc;
     int b = blockIdx.x;
     const int chunk = b % n_chunks;
     b /= n_chunks;
     const int kvh = b % a.n_kv, ui = b / a.n_kv;
-    const UnitDesc u = a.units[ui];
-    const RowDesc rd = a.rows[u.row];
-    const UnitRange ur = unit_range(u, rd, a.causal, a.split_keys);
+    const Q8Unit u = unit_of(a, blob, ui);  // one query
     const int hd = a.hd, h0 = kvh * a.group + chunk * hpc, nh = min(hpc, a.group - chunk * hpc);
     float *qs = sm;                       // [hpc][hd]
     float *accs = qs + hpc * hd;          // [kGW][hpc][hd]
     float *ms = accs + kGW * hpc * hd;    // [kGW][hpc]
     float *ls = ms + kGW * hpc;           // [kGW][hpc]
-    const float *qrow = a.Q + static_cast<size_t>(rd.q_row0 + u.qi) * (a.n_heads * hd) + static_cast<size_t>(h0) * hd;
+    const float *qrow = a.Q + static_cast<size_t>(u.q_row) * (a.n_heads * hd) + static_cast<size_t>(h0) * hd;
     for (int t = threadIdx.x; t < nh * hd; t += blockDim.x) qs[t] = qrow[t] * a.scale_log2;
     for (int t = threadIdx.x; t < kGW * hpc * hd; t += blockDim.x) accs[t] = 0.f;
     __syncthreads();
+    wait_previous();
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float m[kGHeads], l[kGHeads];
 #pragma unroll
     for (int g = 0; g < kGHeads; ++g) m[g] = -INFINITY, l[g] = 0.f;
     float *acc = accs + warp * hpc * hd;
-    for (int j = ur.kbeg + warp; j < ur.kend; j += kGW) {
-        const int blk = block_of(q.a, rd.slot, j, a.err);
+    for (int j = u.kbeg + warp; j < u.kend; j += kGW) {
+        const int blk = block_of(q.a, u.slot, j, a.err);
         if (blk < 0) continue;
         const size_t o = static_cast<size_t>(blk) * q.a.block_stride + q.a.layer_off +
                          static_cast<size_t>(block_off(q.a, j)) * q.a.kv_dim + static_cast<size_t>(kvh) * hd;
@@ -134,10 +182,10 @@ __global__ void __launch_bounds__(128) decode_q8_generic_kernel(AttnArgs a, Q8Ad
             }
         }
         const int h = h0 + g;
-        if (u.item < 0) {
-            a.out[static_cast<size_t>(rd.q_row0 + u.qi) * (a.n_heads * hd) + static_cast<size_t>(h) * hd + d] = num / den;
+        if (u.part0 < 0) {
+            a.out[static_cast<size_t>(u.q_row) * (a.n_heads * hd) + static_cast<size_t>(h) * hd + d] = num / den;
         } else {
-            const size_t ph = static_cast<size_t>(a.merges[u.item].part0 + u.split) * a.n_heads + h;
+            const size_t ph = static_cast<size_t>(u.part0 + u.rec) * a.n_heads + h;
             a.pacc[ph * hd + d] = num;
             if (d == 0) {
                 a.pm[ph] = M;
@@ -145,22 +193,40 @@ __global__ void __launch_bounds__(128) decode_q8_generic_kernel(AttnArgs a, Q8Ad
             }
         }
     }
+    if (u.part0 >= 0 && last_of_block(a, u, kvh * n_chunks + chunk))
+        for (int g = warp; g < nh; g += kGW) join_records(a, u, 0, h0 + g, lane);
 }
 
-cudaError_t launch_generic(const AttnArgs &a, const Q8Addr &q, cudaStream_t s) {
+// A launch that may start while the one before it on the stream still runs.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s, A &&...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+template <class B>
+cudaError_t launch_generic(const Q8Args &a, const Q8Addr &q, const B &blob, cudaStream_t s) {
     const int hpc = a.group < kGHeads ? a.group : kGHeads;
     auto bytes = [](int n, int hd) { return (static_cast<size_t>(n) * hd * (1 + kGW) + 2 * kGW * n) * sizeof(float); };
     static PerDeviceOnce configured;  // the attribute is per function and device
     const cudaError_t ce = configured.run([&]() -> cudaError_t {
-        return cudaFuncSetAttribute(decode_q8_generic_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(decode_q8_generic_kernel<B>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(bytes(kGHeads, kMaxHeadDim)));
     });
     if (ce != cudaSuccess) return ce;
     const int n_chunks = (a.group + hpc - 1) / hpc;
     const long long grid = static_cast<long long>(a.n_units) * a.n_kv * n_chunks;
     if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    decode_q8_generic_kernel<<<static_cast<unsigned>(grid), 128, bytes(hpc, a.hd), s>>>(a, q, hpc);
-    return cudaGetLastError();
+    return launch_early(decode_q8_generic_kernel<B>, static_cast<unsigned>(grid), 128, bytes(hpc, a.hd), s, a, q, hpc, blob);
 }
 
 // ------------------------------------------------------------- fast decode ----
@@ -255,8 +321,9 @@ struct FastQ8 {
     }
 };
 
-template <int HD, int NB>
-__global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2) decode_q8_kernel(AttnArgs a, Q8Addr q, int gb, int qb) {
+template <int HD, int NB, class B>
+__global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2)
+    decode_q8_kernel(Q8Args a, Q8Addr q, int gb, const __grid_constant__ B blob) {
     using F = FastQ8<HD>;
     constexpr int NC = F::kChunks;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -267,13 +334,9 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2) decode_q8_kernel(Att
     const int hb = b % n_hb;
     b /= n_hb;
     const int kvh = b % a.n_kv, ui = b / a.n_kv;
-    const UnitDesc u = a.units[ui];
-    const RowDesc rd = a.rows[u.row];
+    const Q8Unit u = unit_of(a, blob, ui);
     const int h0 = kvh * a.group + hb * gb, nh = min(gb, a.group - hb * gb);
-    const int nq = min(qb, rd.n_q - u.qi);  // queries of this unit
-    const int total_k = rd.past_len + rd.n_q;
-    const int kbeg = rd.k0 + (u.split - rd.s0) * a.split_keys;
-    const int kend = min(kbeg + a.split_keys, a.causal ? rd.past_len + u.qi + nq : total_k);
+    const int nq = u.nq, kbeg = u.kbeg, kend = u.kend;
     const int n_tiles = (kend - kbeg + kT - 1) / kT;
     const int my_n = warp < n_tiles ? (n_tiles - warp + kW - 1) / kW : 0;
     unsigned char *wbase = smem + warp * kStages * F::kStage;
@@ -288,7 +351,7 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2) decode_q8_kernel(Att
         int64_t off = -1;
         float2 sc = make_float2(0.f, 0.f);
         if (pos < kend) {
-            const int blk = block_of(q.a, rd.slot, pos, a.err);
+            const int blk = block_of(q.a, u.slot, pos, a.err);
             if (blk >= 0) {
                 off = static_cast<int64_t>(blk) * q.a.block_stride + q.a.layer_off +
                       static_cast<int64_t>(block_off(q.a, pos)) * q.a.kv_dim + static_cast<int64_t>(kvh) * HD;
@@ -306,9 +369,8 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2) decode_q8_kernel(Att
             cp_async16z(d + kT * HD, vp + (o >= 0 ? o + 16 * ch : 0), n);
         }
     };
-    if (0 < my_n) load_tile(0, 0);
-    cp_async_commit();
 
+    // The queries are no work of the launch before this one; the pages may be.
     // Q^T fragments: pair x's pieces in columns 2c, 2c + 1 of n-tile x / 4.  As
     // a B fragment lane 4g + c holds column g = pair g / 2, piece g % 2, dims
     // 16s + 4c + (0, 1 | 2, 3) (the order in which ldmatrix hands out a row's
@@ -320,7 +382,7 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2) decode_q8_kernel(Att
     for (int nb = 0; nb < NB; ++nb) {
         const int x = 4 * nb + (g >> 1), qi = x / gb, hi = x - qi * gb;
         const bool on = qi < nq && hi < nh;
-        const float *row = a.Q + static_cast<size_t>(rd.q_row0 + u.qi + (on ? qi : 0)) * (a.n_heads * HD) +
+        const float *row = a.Q + static_cast<size_t>(u.q_row + (on ? qi : 0)) * (a.n_heads * HD) +
                            static_cast<size_t>(h0 + (on ? hi : 0)) * HD;
         float v[NC][4], mx = 0.f;
 #pragma unroll
@@ -347,6 +409,10 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2) decode_q8_kernel(Att
             }
     }
 
+    wait_previous();
+    if (0 < my_n) load_tile(0, 0);
+    cp_async_commit();
+
     // ldmatrix addresses of this lane: matrix mi = lane / 8, row mr of it
     //   K: keys 8 (mi & 1) + mr, chunk + (mi >> 1);  V (transposed): the same
     const int mi = lane >> 3, mr = lane & 7, key_of = 8 * (mi & 1) + mr, ch_of = mi >> 1;
@@ -365,7 +431,7 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2) decode_q8_kernel(Att
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
         const int qi = (4 * nb + c) / gb;
-        lim[nb] = a.causal ? min(kend, rd.past_len + u.qi + min(qi, nq - 1) + 1) : kend;
+        lim[nb] = a.causal ? min(kend, u.see0 + min(qi, nq - 1)) : kend;
     }
 
     for (int k = 0; k < my_n; ++k) {
@@ -528,9 +594,9 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2) decode_q8_kernel(Att
             if (wt[w] != 0.f) den = fmaf(wt[w], lw, den);
         }
         const int h = h0 + hi;
-        const size_t ph = u.item < 0 ? 0 : static_cast<size_t>(a.merges[u.item + qi].part0 + u.split) * a.n_heads + h;
-        float *dst = u.item < 0 ? a.out + static_cast<size_t>(rd.q_row0 + u.qi + qi) * (a.n_heads * HD) + static_cast<size_t>(h) * HD
-                                : a.pacc + ph * HD;
+        const size_t ph = u.part0 < 0 ? 0 : static_cast<size_t>(u.part0 + qi * u.n_rec + u.rec) * a.n_heads + h;
+        float *dst = u.part0 < 0 ? a.out + static_cast<size_t>(u.q_row + qi) * (a.n_heads * HD) + static_cast<size_t>(h) * HD
+                                 : a.pacc + ph * HD;
         for (int d = lane; d < HD; d += 32) {
             float num = 0.f;
 #pragma unroll
@@ -538,30 +604,34 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2) decode_q8_kernel(Att
                 const float *Rw = R0 + w * NP * (HD + 2);
                 if (wt[w] != 0.f) num = fmaf(wt[w], Rw[d], num);
             }
-            dst[d] = u.item < 0 ? num / den : num;
+            dst[d] = u.part0 < 0 ? num / den : num;
         }
-        if (u.item >= 0 && lane == 0) {
+        if (u.part0 >= 0 && lane == 0) {
             a.pm[ph] = M;
             a.pl[ph] = den;
         }
     }
+    if (u.part0 >= 0 && last_of_block(a, u, kvh * n_hb + hb))
+        for (int x = warp; x < NP; x += kW) {
+            const int qi = x / gb, hi = x - qi * gb;
+            if (qi < nq && hi < nh) join_records(a, u, qi, h0 + hi, lane);
+        }
 }
 
-template <int HD, int NB>
-cudaError_t launch_fast(const AttnArgs &a, const Q8Addr &q, int gb, int qb, cudaStream_t s) {
+template <int HD, int NB, class B>
+cudaError_t launch_fast(const Q8Args &a, const Q8Addr &q, int gb, const B &blob, cudaStream_t s) {
     using F = FastQ8<HD>;
     constexpr size_t smem = static_cast<size_t>(kW) * kStages * F::kStage;
     static_assert(smem >= static_cast<size_t>(kW) * 4 * NB * (HD + 2) * sizeof(float), "the merge fits the stages");
     static PerDeviceOnce configured;  // the attribute is per function and device
     const cudaError_t ce = configured.run([&]() -> cudaError_t {
-        return cudaFuncSetAttribute(decode_q8_kernel<HD, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(decode_q8_kernel<HD, NB, B>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(smem));
     });
     if (ce != cudaSuccess) return ce;
     const long long grid = static_cast<long long>(a.n_units) * a.n_kv * ((a.group + gb - 1) / gb);
     if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    decode_q8_kernel<HD, NB><<<static_cast<unsigned>(grid), 32 * kW, smem, s>>>(a, q, gb, qb);
-    return cudaGetLastError();
+    return launch_early(decode_q8_kernel<HD, NB, B>, static_cast<unsigned>(grid), 32 * kW, smem, s, a, q, gb, blob);
 }
 
 // Heads per CTA and queries per unit: up to 16 (query, head) pairs share a
@@ -569,14 +639,29 @@ cudaError_t launch_fast(const AttnArgs &a, const Q8Addr &q, int gb, int qb, cuda
 bool fast_shape(int head_dim) { return head_dim % 16 == 0 && head_dim <= 128; }
 int heads_per_block(int group) { return group < 16 ? group : 16; }
 
-template <int HD>
-cudaError_t launch_fast_hd(const AttnArgs &a, const Q8Addr &q, cudaStream_t s) {
-    const int gb = heads_per_block(a.group), qb = q8_query_block(a.hd, a.group);
+template <int HD, class B>
+cudaError_t launch_fast_hd(const Q8Args &a, const Q8Addr &q, const B &blob, cudaStream_t s) {
+    const int gb = heads_per_block(a.group);
     // the widest unit of the call decides; a unit of fewer pairs leaves columns idle
-    const int pairs = gb * std::min(qb, a.max_q);
-    if (pairs <= 4) return launch_fast<HD, 1>(a, q, gb, qb, s);
-    if (pairs <= 8) return launch_fast<HD, 2>(a, q, gb, qb, s);
-    return launch_fast<HD, 4>(a, q, gb, qb, s);
+    const int pairs = gb * a.max_q;
+    if (pairs <= 4) return launch_fast<HD, 1>(a, q, gb, blob, s);
+    if (pairs <= 8) return launch_fast<HD, 2>(a, q, gb, blob, s);
+    return launch_fast<HD, 4>(a, q, gb, blob, s);
+}
+
+template <class B>
+cudaError_t launch_decode_with(const Q8Args &a, const Q8Addr &q, const B &blob, cudaStream_t s) {
+    switch (fast_shape(a.hd) ? a.hd : 0) {
+        case 16: return launch_fast_hd<16>(a, q, blob, s);
+        case 32: return launch_fast_hd<32>(a, q, blob, s);
+        case 48: return launch_fast_hd<48>(a, q, blob, s);
+        case 64: return launch_fast_hd<64>(a, q, blob, s);
+        case 80: return launch_fast_hd<80>(a, q, blob, s);
+        case 96: return launch_fast_hd<96>(a, q, blob, s);
+        case 112: return launch_fast_hd<112>(a, q, blob, s);
+        case 128: return launch_fast_hd<128>(a, q, blob, s);
+        default: return launch_generic(a, q, blob, s);
+    }
 }
 
 // -------------------------------------------------------------- split pass ----
@@ -701,18 +786,13 @@ int q8_query_block(int head_dim, int group) {
     return fast_shape(head_dim) ? std::max(1, 16 / heads_per_block(group)) : 1;
 }
 
-cudaError_t launch_decode_q8(const AttnArgs &a, const Q8Addr &q, cudaStream_t s) {
-    switch (fast_shape(a.hd) ? a.hd : 0) {
-        case 16: return launch_fast_hd<16>(a, q, s);
-        case 32: return launch_fast_hd<32>(a, q, s);
-        case 48: return launch_fast_hd<48>(a, q, s);
-        case 64: return launch_fast_hd<64>(a, q, s);
-        case 80: return launch_fast_hd<80>(a, q, s);
-        case 96: return launch_fast_hd<96>(a, q, s);
-        case 112: return launch_fast_hd<112>(a, q, s);
-        case 128: return launch_fast_hd<128>(a, q, s);
-        default: return launch_generic(a, q, s);
-    }
+int q8_counters(int head_dim, int group, int n_kv) {
+    const int per = fast_shape(head_dim) ? heads_per_block(group) : group < kGHeads ? group : kGHeads;
+    return n_kv * ((group + per - 1) / per);
+}
+
+cudaError_t launch_decode_q8(const Q8Args &a, const Q8Addr &q, cudaStream_t s) {
+    return a.blob ? launch_decode_with(a, q, *a.blob, s) : launch_decode_with(a, q, NoBlob{}, s);
 }
 
 cudaError_t launch_split_q8(const SplitArgs &a, const Q8Addr &q, cudaStream_t s) {
