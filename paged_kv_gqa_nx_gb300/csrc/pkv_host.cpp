@@ -12,6 +12,7 @@
 // pool behaviour: "nx_paged_kv_gate.nx source" (KAT, FORK, REWIND sections).
 #include "../../include/pkv.h"
 #include "pkv_internal.h"
+#include "pkv_tma.h"
 
 #include <cuda_runtime.h>
 
@@ -339,6 +340,8 @@ struct pkv_pool {
     int32_t n_kv = 0, hd = 0;                 // 8-bit pools: kv heads and head width
     float *k_scale = nullptr, *v_scale = nullptr;  // [n_blocks][n_layers][n_kv]
     bool owns_scale = false;
+    Q8Maps maps{};
+    bool has_maps = false;
     int32_t *pt_dev = nullptr;
     int32_t *err_dev = nullptr;
     cudaStream_t stream = nullptr;
@@ -457,6 +460,7 @@ Q8Addr q8_addr(const pkv_pool *p, int32_t layer) {
     q.scale_stride = static_cast<int64_t>(p->n_layers) * p->n_kv;
     q.n_kv = p->n_kv;
     q.hd = p->hd;
+    q.maps = p->has_maps ? &p->maps : nullptr;
     return q;
 }
 
@@ -1636,6 +1640,14 @@ pkv_pool *make_pool(int32_t n_blocks, int32_t n_layers, int32_t kv_dim, int32_t 
                 pkv_pool_free(p);
                 return nullptr;
             }
+        }
+    }
+    if (q8) {
+        e = make_q8_maps(&p->maps, q8_addr(p, 0), n_layers, &p->has_maps);
+        if (e != cudaSuccess) {
+            cuda_fail(e, "page maps");
+            pkv_pool_free(p);
+            return nullptr;
         }
     }
     e = cudaMalloc(&p->pt_dev, static_cast<size_t>(max_seqs) * max_blocks_per_seq * sizeof(int32_t));

@@ -74,6 +74,7 @@ struct Q8Addr {
     float *ks, *vs;            // scales of the layer's first head: block b, head h at b * scale_stride + h
     int64_t scale_stride;      // floats per block: n_layers * n_kv
     int32_t n_kv, hd;
+    const void *maps = nullptr;  // host: the pool's Q8Maps where its pages can be loaded by TMA
 };
 
 // The rows of one page that a packed append writes, or a packed read returns:
@@ -346,6 +347,8 @@ cudaError_t launch_rope_rows(const RopeArgs &a, cudaStream_t s);
 // block of units needs.
 cudaError_t launch_decode_q8(const Q8Args &a, const Q8Addr &addr, cudaStream_t s);
 int q8_counters(int head_dim, int group, int n_kv);
+struct Q8Maps;
+cudaError_t make_q8_maps(Q8Maps *m, const Q8Addr &addr, int n_layers, bool *usable);
 cudaError_t launch_split_q8(const SplitArgs &a, const Q8Addr &addr, cudaStream_t s);
 int q8_query_block(int head_dim, int group);
 // Packed prompt attention (pkv_packed.cu); sequences sorted longest first.

@@ -14,8 +14,8 @@
 #include "pkv_elem.h"
 #include "pkv_internal.h"
 #include "pkv_tcgen05.h"
+#include "pkv_tma.h"
 
-#include <cuda.h>
 #include <cuda_fp16.h>
 #include <type_traits>
 
@@ -863,29 +863,9 @@ cudaError_t launch_general_n(const PackedArgs &a, const int32_t *start, const in
     return cudaGetLastError();
 }
 
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-cudaError_t encode_fn(EncodeFn *out) {
-    static std::atomic<EncodeFn> known{nullptr};
-    EncodeFn f = known.load(std::memory_order_acquire);
-    if (!f) {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
-        if (e != cudaSuccess) return e;
-        if (!p || q != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
-        f = reinterpret_cast<EncodeFn>(p);
-        known.store(f, std::memory_order_release);
-    }
-    *out = f;
-    return cudaSuccess;
-}
-
 // Rows [tokens][heads][hd] with a token stride, in boxes of 64 columns x
 // box_heads x box_tokens; columns past hd and tokens past the last read as 0.
-cudaError_t rows_map(CUtensorMap *m, EncodeFn f, const PackedArgs &a, const void *base, int64_t stride, int heads,
+cudaError_t rows_map(CUtensorMap *m, EncodeTiled f, const PackedArgs &a, const void *base, int64_t stride, int heads,
                      int box_heads, int box_tokens) {
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.hd), static_cast<cuuint64_t>(heads),
                                 static_cast<cuuint64_t>(a.n_tokens)};
@@ -927,8 +907,8 @@ cudaError_t launch_tc_n(const PackedArgs &a, const int32_t *start, const int32_t
     const int group = a.n_heads / a.n_kv;
     int log_p = 0;
     while (log_p < 4 && group % (2 << log_p) == 0) ++log_p;
-    EncodeFn f;
-    cudaError_t e = encode_fn(&f);
+    EncodeTiled f;
+    cudaError_t e = encode_tiled(&f);
     CUtensorMap mq, mk, mv;
     if (e == cudaSuccess) e = rows_map(&mq, f, a, a.Q, a.q_stride, a.n_heads, 1 << log_p, 128 >> log_p);
     if (e == cudaSuccess) e = rows_map(&mk, f, a, a.K, a.k_stride, a.n_kv, 1, kKeys);
@@ -958,6 +938,22 @@ cudaError_t launch_general(const PackedArgs &a, const int32_t *start, const int3
 }
 
 }  // namespace
+
+cudaError_t encode_tiled(EncodeTiled *out) {
+    static std::atomic<EncodeTiled> known{nullptr};
+    EncodeTiled f = known.load(std::memory_order_acquire);
+    if (!f) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+        if (e != cudaSuccess) return e;
+        if (!p || q != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
+        f = reinterpret_cast<EncodeTiled>(p);
+        known.store(f, std::memory_order_release);
+    }
+    *out = f;
+    return cudaSuccess;
+}
 
 cudaError_t launch_packed(const PackedArgs &a, const int32_t *start, const int32_t *len, int32_t n_seqs,
                           cudaStream_t s) {

@@ -632,7 +632,8 @@ cudaError_t append_q8_from(const PagesArgs &p, const Q8Addr &q, cudaStream_t s) 
     unsigned grid;
     constexpr int kHold = 8;
     const int cpr = q.hd / 8;
-    if (vec_ok(p, q.a, q.hd) && q.a.kv_dim % 8 == 0 && cpr <= 32 && 32 % cpr == 0 && q.a.bs * cpr <= 32 * kHold) {
+    // (fewer than four items a walking warp: one item a warp, more warps a SM)
+    if (2LL * p.n_items * q.n_kv >= 4LL * 2 * 152 * 8 && vec_ok(p, q.a, q.hd) && cpr <= 32 && 32 % cpr == 0 && q.a.bs * cpr <= 32 * kHold) {
         // a whole number of items (and blocks) per round of warps, two blocks a SM
         const long long warps = 2LL * p.n_items * q.n_kv, round = 16LL * q.n_kv;  // 8 items, 2 n_kv blocks
         const long long want = std::min<long long>((warps + round - 1) / round, std::max<long long>(1, 2LL * 152 * 8 / round));

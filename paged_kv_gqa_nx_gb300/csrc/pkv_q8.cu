@@ -11,6 +11,8 @@
 #include "pkv_elem.h"
 #include "pkv_internal.h"
 #include "pkv_rows.h"
+#include "pkv_tcgen05.h"
+#include "pkv_tma.h"
 
 #include <algorithm>
 #include <cuda_fp16.h>
@@ -309,6 +311,14 @@ __device__ __forceinline__ void cp_async16z(uint32_t dst, const void *src, uint3
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, int head, int off, int page, uint32_t mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];\n" ::"r"(dst),
+        "l"(map), "r"(0), "r"(head), "r"(off), "r"(page), "r"(mbar)
+        : "memory");
+}
+
 // Columns of a CTA: pair x = 4 * nt + c of its block is (query qi + x / gb,
 // head h0 + x % gb) with gb heads per block.
 template <int HD>
@@ -321,13 +331,16 @@ struct FastQ8 {
     }
 };
 
-template <int HD, int NB, class B>
+template <int HD, int NB, bool kTma, class B>
 __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2)
-    decode_q8_kernel(Q8Args a, Q8Addr q, int gb, const __grid_constant__ B blob) {
+    decode_q8_kernel(Q8Args a, Q8Addr q, int gb, const __grid_constant__ Q8Maps maps, const __grid_constant__ B blob) {
     using F = FastQ8<HD>;
     constexpr int NC = F::kChunks;
-    extern __shared__ __align__(128) unsigned char smem[];
+    extern __shared__ __align__(1024) unsigned char smraw[];
+    unsigned char *const smem = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smraw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ float2 sc_tile[kW][kStages][kT];  // K and V scales of a tile's keys
+    __shared__ uint64_t bars[kW][kStages];       // tile landed (TMA loads)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const int n_hb = (a.group + gb - 1) / gb;  // head blocks of a kv head
     int b = blockIdx.x;
@@ -343,23 +356,42 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2)
     const uint32_t wbase_s = static_cast<uint32_t>(__cvta_generic_to_shared(wbase));
     const uint8_t *const kp = static_cast<const uint8_t *>(q.a.k), *const vp = static_cast<const uint8_t *>(q.a.v);
 
-    // Tile loads: lane j finds key j's row and scales; the lanes then copy the
-    // rows' chunks, K and V, each a 16-byte cp.async (zeros past the unit, and
-    // where the page lookup failed, with scale 0).
-    auto load_tile = [&](int kl, int st) {
-        const int pos = kbeg + (warp + kl * kW) * kT + lane;
-        int64_t off = -1;
-        float2 sc = make_float2(0.f, 0.f);
-        if (pos < kend) {
-            const int blk = block_of(q.a, u.slot, pos, a.err);
-            if (blk >= 0) {
-                off = static_cast<int64_t>(blk) * q.a.block_stride + q.a.layer_off +
-                      static_cast<int64_t>(block_off(q.a, pos)) * q.a.kv_dim + static_cast<int64_t>(kvh) * HD;
-                sc = make_float2(__ldg(q.ks + blk * q.scale_stride + kvh), __ldg(q.vs + blk * q.scale_stride + kvh));
-            }
-        }
-        sc_tile[warp][st][lane] = sc;
+    // Tile loads.  Lane j finds key j's block a tile ahead of the copies and its
+    // scales a tile ahead of their use, so that no lookup is waited for; the lanes
+    // copy the rows' chunks, K and V, each a 16-byte cp.async (zeros past the
+    // unit, and where the page lookup failed, with scale 0).
+    // With whole sixteens of keys in every page, lanes 0 and 1 load their half of
+    // a tile, K and V, as one TMA box each (a page's sixteen rows of this head, in
+    // the same swizzle), and each half has one scale.
+    auto find = [&](int kl) {  // the block of this lane's key (half) in tile kl, or -1
+        const int pos = kbeg + (warp + kl * kW) * kT + (kTma ? 16 * lane : lane);
+        return kl < my_n && pos < kend && (!kTma || lane < 2) ? block_of(q.a, u.slot, pos, a.err) : -1;
+    };
+    auto scales_of = [&](int blk) {
+        return blk >= 0 ? make_float2(__ldg(q.ks + blk * q.scale_stride + kvh), __ldg(q.vs + blk * q.scale_stride + kvh))
+                        : make_float2(0.f, 0.f);
+    };
+    auto load_tile = [&](int kl, int st, int blk) {
         const uint32_t dst = wbase_s + st * F::kStage;
+        if constexpr (kTma) {
+            if (lane < 2) {
+                const int off = block_off(q.a, kbeg + (warp + kl * kW) * kT + 16 * lane);
+                const uint32_t bar = static_cast<uint32_t>(__cvta_generic_to_shared(&bars[warp][st]));
+                if (blk >= 0) {
+                    tc::mbar_expect_tx(bar, 2 * 16 * HD);
+                    tma_page(dst + lane * 16 * HD, &maps.k, kvh, off, blk * maps.n_layers + maps.layer, bar);
+                    tma_page(dst + (kT + lane * 16) * HD, &maps.v, kvh, off, blk * maps.n_layers + maps.layer, bar);
+                } else {
+                    tc::mbar_arrive(bar);  // the half keeps what it holds: its keys are masked, its scale is 0
+                }
+            }
+            return;
+        }
+        const int pos = kbeg + (warp + kl * kW) * kT + lane;
+        const int64_t off = blk < 0 ? -1
+                                    : static_cast<int64_t>(blk) * q.a.block_stride + q.a.layer_off +
+                                          static_cast<int64_t>(block_off(q.a, pos)) * q.a.kv_dim +
+                                          static_cast<int64_t>(kvh) * HD;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {  // kT * NC chunks over 32 lanes, K and V
             const int x = lane + 32 * i, j = x / NC, ch = x - j * NC;
@@ -369,30 +401,53 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2)
             cp_async16z(d + kT * HD, vp + (o >= 0 ? o + 16 * ch : 0), n);
         }
     };
+    if constexpr (kTma) {
+        if (lane < kStages) tc::mbar_init(static_cast<uint32_t>(__cvta_generic_to_shared(&bars[warp][lane])), 2);
+        tc::fence_proxy_async();  // the barriers (this warp's own), before TMA uses them
+        __syncwarp();
+    }
 
-    // The queries are no work of the launch before this one; the pages may be.
     // Q^T fragments: pair x's pieces in columns 2c, 2c + 1 of n-tile x / 4.  As
     // a B fragment lane 4g + c holds column g = pair g / 2, piece g % 2, dims
     // 16s + 4c + (0, 1 | 2, 3) (the order in which ldmatrix hands out a row's
     // bytes).  Each pair is scaled by a power of two that puts its largest
-    // entry into [2^14, 2^15).
-    uint32_t qf[NB][NC][2];
-    float qinv[NB];  // of this lane's own pair, 4 * nb + c
+    // entry into [2^14, 2^15).  The queries are no work of the launch before
+    // this one, the pages may be; the first tile loads while the pieces are made.
+    float qv[NB][NC][4];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
         const int x = 4 * nb + (g >> 1), qi = x / gb, hi = x - qi * gb;
         const bool on = qi < nq && hi < nh;
         const float *row = a.Q + static_cast<size_t>(u.q_row + (on ? qi : 0)) * (a.n_heads * HD) +
                            static_cast<size_t>(h0 + (on ? hi : 0)) * HD;
-        float v[NC][4], mx = 0.f;
 #pragma unroll
         for (int s = 0; s < NC; ++s) {
             const float4 t = on ? __ldg(reinterpret_cast<const float4 *>(row + 16 * s + 4 * c)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[s][0] = t.x * a.scale_log2, v[s][1] = t.y * a.scale_log2;
-            v[s][2] = t.z * a.scale_log2, v[s][3] = t.w * a.scale_log2;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(v[s][i]));
+            qv[nb][s][0] = t.x, qv[nb][s][1] = t.y, qv[nb][s][2] = t.z, qv[nb][s][3] = t.w;
         }
+    }
+    wait_previous();
+    int blk_next;
+    float2 sc_cur, sc_next = make_float2(0.f, 0.f);
+    {
+        const int blk = find(0);
+        blk_next = find(1);
+        if (0 < my_n) load_tile(0, 0, blk);
+        if constexpr (!kTma) cp_async_commit();
+        sc_cur = scales_of(blk);
+    }
+    uint32_t qf[NB][NC][2];
+    float qinv[NB];  // of this lane's own pair, 4 * nb + c
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        float mx = 0.f;
+#pragma unroll
+        for (int s = 0; s < NC; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                qv[nb][s][i] *= a.scale_log2;
+                mx = fmaxf(mx, fabsf(qv[nb][s][i]));
+            }
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
         int e = 0;
@@ -404,18 +459,20 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2)
         for (int s = 0; s < NC; ++s)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint32_t p0 = pieces2(v[s][2 * i] * up), p1 = pieces2(v[s][2 * i + 1] * up);
+                const uint32_t p0 = pieces2(qv[nb][s][2 * i] * up), p1 = pieces2(qv[nb][s][2 * i + 1] * up);
                 qf[nb][s][i] = __byte_perm(p0, p1, (g & 1) ? 0x7632 : 0x5410);  // this column's piece of both dims
             }
     }
 
-    wait_previous();
-    if (0 < my_n) load_tile(0, 0);
-    cp_async_commit();
-
     // ldmatrix addresses of this lane: matrix mi = lane / 8, row mr of it
     //   K: keys 8 (mi & 1) + mr, chunk + (mi >> 1);  V (transposed): the same
     const int mi = lane >> 3, mr = lane & 7, key_of = 8 * (mi & 1) + mr, ch_of = mi >> 1;
+    // chunk pair s / 2 of key key_of (and of key_of + 16: the swizzle repeats
+    // every eight keys); the last pair of an odd chunk count reads the last twice
+    uint32_t at[(NC + 1) / 2];
+#pragma unroll
+    for (int s = 0; s < NC; s += 2) at[s / 2] = key_of * HD + ((min(s + ch_of, NC - 1) ^ F::swz(key_of)) << 4);
+    bool landed = true;
 
     float m_run[NB], l_run[NB], o[NB][NC][4];
     int c_exp = 0, c_top = -126;  // O holds 2^-c_exp times the sum (and kWScale); c_top: the largest exponent seen
@@ -435,11 +492,28 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2)
     }
 
     for (int k = 0; k < my_n; ++k) {
-        if (k + 1 < my_n) load_tile(k + 1, (k + 1) % kStages);
-        cp_async_commit();
-        cp_async_wait<1>();
-        __syncwarp();
-        const int st = k % kStages, pos0 = kbeg + (warp + k * kW) * kT;
+        if (k + 1 < my_n) load_tile(k + 1, (k + 1) % kStages, blk_next);
+        if constexpr (!kTma) cp_async_commit();
+        sc_next = scales_of(blk_next);
+        blk_next = find(k + 2);
+        const int st = k % kStages;
+        float ksc[2], vsc2[2];  // TMA: of the tile's halves
+        if constexpr (kTma) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                ksc[h] = __shfl_sync(kFull, sc_cur.x, h);
+                vsc2[h] = __shfl_sync(kFull, sc_cur.y, h);
+            }
+            landed = __all_sync(kFull, tc::mbar_wait(static_cast<uint32_t>(__cvta_generic_to_shared(&bars[warp][st])),
+                                                     (k / kStages) & 1));
+            if (!landed) break;
+        } else {
+            sc_tile[warp][st][lane] = sc_cur;
+            cp_async_wait<1>();
+            __syncwarp();
+        }
+        sc_cur = sc_next;
+        const int pos0 = kbeg + (warp + k * kW) * kT;
         const uint32_t Ks = wbase_s + st * F::kStage, Vs = Ks + kT * HD;
 
         float sv[NB][4];  // scores of keys g, g + 8, g + 16, g + 24
@@ -448,14 +522,10 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2)
             float acc[NB][4];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) acc[nb][0] = acc[nb][1] = acc[nb][2] = acc[nb][3] = 0.f;
-            const int key = 16 * kg + key_of;
-            const uint32_t row = Ks + key * HD;
 #pragma unroll
             for (int s = 0; s < NC; s += 2) {
                 uint32_t r[4];
-                // the last pair of an odd chunk count reads the last chunk twice
-                const int ch = min(s + ch_of, NC - 1);
-                ldsm4(r, row + ((ch ^ F::swz(key)) << 4));
+                ldsm4(r, Ks + at[s / 2] + 16 * kg * HD);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (s + h >= NC) continue;
@@ -477,7 +547,7 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2)
         float es = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 sc = sc_tile[warp][st][g + 8 * i];
+            const float2 sc = kTma ? make_float2(ksc[i >> 1], vsc2[i >> 1]) : sc_tile[warp][st][g + 8 * i];
             vsc[i] = sc.y;
             es = fmaxf(es, sc.y);
 #pragma unroll
@@ -533,13 +603,10 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2)
         // O^T += (U_V - 128)^T W^T
 #pragma unroll
         for (int kg = 0; kg < 2; ++kg) {
-            const int key = 16 * kg + key_of;
-            const uint32_t row = Vs + key * HD;
 #pragma unroll
             for (int s = 0; s < NC; s += 2) {
                 uint32_t r[4];
-                const int ch = min(s + ch_of, NC - 1);
-                ldsm4t(r, row + ((ch ^ F::swz(key)) << 4));
+                ldsm4t(r, Vs + at[s / 2] + 16 * kg * HD);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (s + h >= NC) continue;
@@ -553,7 +620,8 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2)
         }
         __syncwarp();
     }
-    cp_async_wait<0>();
+    if constexpr (!kTma) cp_async_wait<0>();
+    if (!landed && lane == 0) flag_error(a.err, 2);
     __syncthreads();  // every warp is done with its stages
 
     // publish each warp's (O, m, l), pair by pair: O[pair][dim] behind one another
@@ -618,20 +686,25 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2)
         }
 }
 
-template <int HD, int NB, class B>
+template <int HD, int NB, bool kTma, class B>
 cudaError_t launch_fast(const Q8Args &a, const Q8Addr &q, int gb, const B &blob, cudaStream_t s) {
     using F = FastQ8<HD>;
-    constexpr size_t smem = static_cast<size_t>(kW) * kStages * F::kStage;
-    static_assert(smem >= static_cast<size_t>(kW) * 4 * NB * (HD + 2) * sizeof(float), "the merge fits the stages");
+    constexpr size_t smem = static_cast<size_t>(kW) * kStages * F::kStage + 1024;  // + alignment slack
+    static_assert(smem - 1024 >= static_cast<size_t>(kW) * 4 * NB * (HD + 2) * sizeof(float), "the merge fits the stages");
     static PerDeviceOnce configured;  // the attribute is per function and device
     const cudaError_t ce = configured.run([&]() -> cudaError_t {
-        return cudaFuncSetAttribute(decode_q8_kernel<HD, NB, B>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(decode_q8_kernel<HD, NB, kTma, B>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(smem));
     });
     if (ce != cudaSuccess) return ce;
     const long long grid = static_cast<long long>(a.n_units) * a.n_kv * ((a.group + gb - 1) / gb);
     if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return launch_early(decode_q8_kernel<HD, NB, B>, static_cast<unsigned>(grid), 32 * kW, smem, s, a, q, gb, blob);
+    Q8Maps maps{};
+    if (kTma) {
+        maps = *static_cast<const Q8Maps *>(q.maps);
+        maps.layer = static_cast<int>(q.a.layer_off / (static_cast<int64_t>(q.a.bs) * q.a.kv_dim));
+    }
+    return launch_early(decode_q8_kernel<HD, NB, kTma, B>, static_cast<unsigned>(grid), 32 * kW, smem, s, a, q, gb, maps, blob);
 }
 
 // Heads per CTA and queries per unit: up to 16 (query, head) pairs share a
@@ -644,9 +717,15 @@ cudaError_t launch_fast_hd(const Q8Args &a, const Q8Addr &q, const B &blob, cuda
     const int gb = heads_per_block(a.group);
     // the widest unit of the call decides; a unit of fewer pairs leaves columns idle
     const int pairs = gb * a.max_q;
-    if (pairs <= 4) return launch_fast<HD, 1>(a, q, gb, blob, s);
-    if (pairs <= 8) return launch_fast<HD, 2>(a, q, gb, blob, s);
-    return launch_fast<HD, 4>(a, q, gb, blob, s);
+    if constexpr (HD == 64 || HD == 128)
+        if (q.maps) {
+            if (pairs <= 4) return launch_fast<HD, 1, true>(a, q, gb, blob, s);
+            if (pairs <= 8) return launch_fast<HD, 2, true>(a, q, gb, blob, s);
+            return launch_fast<HD, 4, true>(a, q, gb, blob, s);
+        }
+    if (pairs <= 4) return launch_fast<HD, 1, false>(a, q, gb, blob, s);
+    if (pairs <= 8) return launch_fast<HD, 2, false>(a, q, gb, blob, s);
+    return launch_fast<HD, 4, false>(a, q, gb, blob, s);
 }
 
 template <class B>
@@ -784,6 +863,29 @@ __global__ void __launch_bounds__(256) split_q8_kernel(SplitArgs p, Q8Addr q) {
 
 int q8_query_block(int head_dim, int group) {
     return fast_shape(head_dim) ? std::max(1, 16 / heads_per_block(group)) : 1;
+}
+
+cudaError_t make_q8_maps(Q8Maps *m, const Q8Addr &q, int n_layers, bool *usable) {
+    *usable = false;
+    m->n_layers = n_layers;
+    if ((q.hd != 64 && q.hd != 128) || q.a.bs % 16 != 0 ||
+        static_cast<int64_t>(q.a.n_blocks) * n_layers > 0x7fffffff)
+        return cudaSuccess;
+    EncodeTiled f;
+    const cudaError_t e = encode_tiled(&f);
+    if (e != cudaSuccess) return e;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(q.hd), static_cast<cuuint64_t>(q.n_kv),
+                                static_cast<cuuint64_t>(q.a.bs), static_cast<cuuint64_t>(q.a.n_blocks) * n_layers};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(q.hd), static_cast<cuuint64_t>(q.a.kv_dim),
+                                   static_cast<cuuint64_t>(q.a.bs) * q.a.kv_dim};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(q.hd), 1, 16, 1}, one[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 2; ++i)
+        if (f(i ? &m->v : &m->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, i ? q.a.v : q.a.k, dims, strides, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, q.hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    *usable = true;
+    return cudaSuccess;
 }
 
 int q8_counters(int head_dim, int group, int n_kv) {
