@@ -506,7 +506,12 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2)
             }
             landed = __all_sync(kFull, tc::mbar_wait(static_cast<uint32_t>(__cvta_generic_to_shared(&bars[warp][st])),
                                                      (k / kStages) & 1));
-            if (!landed) break;
+            if (!landed) {  // one more bounded wait for the copies in flight, this tile's and the next's
+                for (int t = k; t <= k + 1 && t < my_n; ++t)
+                    tc::mbar_wait(static_cast<uint32_t>(__cvta_generic_to_shared(&bars[warp][t % kStages])),
+                                  (t / kStages) & 1);
+                break;
+            }
         } else {
             sc_tile[warp][st][lane] = sc_cur;
             cp_async_wait<1>();
