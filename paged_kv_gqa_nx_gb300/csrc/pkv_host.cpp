@@ -657,7 +657,12 @@ int32_t unit_keys(const UnitDesc &u, const RowDesc &rd, int causal, int32_t S) {
 // Cost of a tensor-core prefill CTA in units of ~100 SM clocks, from clock64
 // timelines of the kernel: ~3.9k clocks per 64-key tile with two chains,
 // ~2.7k with one, ~15k per CTA besides (query rows, first copies, output).
-constexpr int64_t kPairTileCost = 39, kSingleTileCost = 27, kCtaCost = 150;
+struct TileCost {
+    int64_t pair = 39, single = 27, cta = 150;
+};
+// The 8-bit pools' kernel (pkv_prefill_q8.cu): a lone tile is bound by its own
+// chain of products and softmax, so it takes as long as two.
+constexpr TileCost kTileCostQ8{22, 20, 120};
 
 // Tile pairs -> the CTA list (two entries per CTA, the second may be absent).
 // mode 0: one tile per CTA; 1: every pair; 2: pairs, with the last k of the
@@ -669,7 +674,7 @@ constexpr int64_t kPairTileCost = 39, kSingleTileCost = 27, kCtaCost = 150;
 // same bits in every mode.
 void place_pairs(const std::vector<std::array<PrefillTile, 2>> &pairs, const std::vector<int32_t> &len0,
                  const std::vector<int32_t> &len1, int32_t mode, int32_t n_kv, int32_t n_sm,
-                 std::vector<PrefillTile> &out) {
+                 const TileCost &cost_of, std::vector<PrefillTile> &out) {
     const size_t np = pairs.size();
     if (mode == 0) {
         for (const auto &pr : pairs)
@@ -705,12 +710,12 @@ void place_pairs(const std::vector<std::array<PrefillTile, 2>> &pairs, const std
             for (size_t i = 0; i < np; ++i) {
                 if (split[i]) continue;
                 const bool two = pairs[i][1].row >= 0;
-                put(two ? kPairTileCost * std::max(len0[i], len1[i]) + kCtaCost
-                        : kSingleTileCost * len0[i] + kCtaCost);
+                put(two ? cost_of.pair * std::max(len0[i], len1[i]) + cost_of.cta
+                        : cost_of.single * len0[i] + cost_of.cta);
             }
             for (int32_t i = k - 1; i >= 0; --i) {
-                put(kSingleTileCost * len0[full[i]] + kCtaCost);
-                put(kSingleTileCost * len1[full[i]] + kCtaCost);
+                put(cost_of.single * len0[full[i]] + cost_of.cta);
+                put(cost_of.single * len1[full[i]] + cost_of.cta);
             }
             return *std::max_element(heap.begin(), heap.end());
         };
@@ -749,7 +754,8 @@ void place_pairs(const std::vector<std::array<PrefillTile, 2>> &pairs, const std
 void build_work(std::vector<RowDesc> &rows, int causal, int32_t S, int32_t head_dim,
                 int32_t group, WorkList &w, const std::vector<Cascade> &cas = {},
                 int32_t prefix_split = 0, int32_t prefill_split = 0, bool allow_tc = true,
-                int32_t n_kv = 0, int32_t n_sm = 0, int32_t qblock = 1, const ShortRows &short_rows = {}) {
+                int32_t n_kv = 0, int32_t n_sm = 0, int32_t qblock = 1, const ShortRows &short_rows = {},
+                const TileCost &cost_of = {}) {
     std::vector<UnitDesc> tail;
     w.units.clear();
     w.tiles.clear();
@@ -831,7 +837,7 @@ void build_work(std::vector<RowDesc> &rows, int causal, int32_t S, int32_t head_
             }
         }
     }
-    place_pairs(pairs, len0, len1, g_prefill_pairing.load(), n_kv, n_sm, w.tiles);
+    place_pairs(pairs, len0, len1, g_prefill_pairing.load(), n_kv, n_sm, cost_of, w.tiles);
     w.units.insert(w.units.end(), tail.begin(), tail.end());
     // longest units first, so that the grid's last CTAs are its shortest and
     // the launch drains quickly (the order changes no result)
@@ -1079,7 +1085,7 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
     const int32_t Sp = cas.empty() ? 0 : prefix_split_keys(cas, group, n_kv_heads, p->n_sm);
     if (attend)
         build_work(rows, causal, S_dec, head_dim, group, w, cas, Sp, S * kPrefillSplitFactor, true, n_kv_heads,
-                   p->n_sm, p->q8 ? q8_query_block(head_dim, group) : 1, short_rows);
+                   p->n_sm, p->q8 ? q8_query_block(head_dim, group) : 1, short_rows, p->q8 ? kTileCostQ8 : TileCost{});
     // the decode kernels that take the append themselves: the f32 kernel for
     // groups 1, 2, 4 and the narrow-pool kernel for its shapes (head_dim 128)
     const bool fuse_shape = head_dim == 128 && !p->q8 &&
@@ -1302,7 +1308,8 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
         a.pt_write = pt_write ? 1 : 0;
     }
     if (w.n_part > 0) {
-        const size_t pf = static_cast<size_t>(w.n_part) * n_heads;
+        // (a multiple of four, so that the sums of V start on a 16-byte boundary)
+        const size_t pf = (static_cast<size_t>(w.n_part) * n_heads + 3) & ~static_cast<size_t>(3);
         e = p->part.ensure(pf * (2 + head_dim) * sizeof(float), st, p->device);
         if (e != cudaSuccess) return cuda_fail(e, "partials buffer");
         a.pm = static_cast<float *>(p->part.p);
@@ -1339,7 +1346,9 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
         pa.img_tile0 = dptr<int32_t>(p, tile0_off);
         pa.img_slot = dptr<int32_t>(p, slot_off);
         pa.lo_zero = p->narrow() ? 1 : 0;
-        e = launch(PKV_KERNEL_PREFILL, st, [&] { return launch_prefill_paged(pa, addr, st); });
+        e = launch(PKV_KERNEL_PREFILL, st, [&] {
+            return p->q8 ? launch_prefill_q8(pa, st) : launch_prefill_paged(pa, addr, st);
+        });
         if (e != cudaSuccess) return cuda_fail(e, "prefill kernel");
     }
     if (!w.ctiles.empty()) {
@@ -1351,7 +1360,9 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
         pa.img_tile0 = dptr<int32_t>(p, tile0_off);
         pa.img_slot = dptr<int32_t>(p, slot_off);
         pa.lo_zero = p->narrow() ? 1 : 0;
-        e = launch(PKV_KERNEL_PREFILL, st, [&] { return launch_prefill_paged(pa, addr, st); });
+        e = launch(PKV_KERNEL_PREFILL, st, [&] {
+            return p->q8 ? launch_prefill_q8(pa, st) : launch_prefill_paged(pa, addr, st);
+        });
         if (e != cudaSuccess) return cuda_fail(e, "shared-prefix kernel");
     }
     if (!w.units.empty()) {
@@ -2108,7 +2119,7 @@ int pkv_attn_contiguous(const float *Q, const float *Kc, const float *Vc, int32_
     const size_t tile0_off = blob.put(img_tile0.data(), img_tile0.size());
     const size_t slot_off = blob.put(img_slot.data(), img_slot.size());
     const size_t desc_bytes = (blob.size() + 255) & ~static_cast<size_t>(255);
-    const size_t pf = static_cast<size_t>(w.n_part) * n_heads;
+    const size_t pf = (static_cast<size_t>(w.n_part) * n_heads + 3) & ~static_cast<size_t>(3);  // keeps 16-byte alignment
     const size_t part_bytes = (pf * (2 + head_dim) * sizeof(float) + 255) & ~static_cast<size_t>(255);
     const size_t img_bytes = img_slot.size() * static_cast<size_t>(n_kv_heads) * kImageBytes;
     const size_t total = desc_bytes + part_bytes + img_bytes;

@@ -350,6 +350,9 @@ int q8_counters(int head_dim, int group, int n_kv);
 struct Q8Maps;
 cudaError_t make_q8_maps(Q8Maps *m, const Q8Addr &addr, int n_layers, bool *usable);
 cudaError_t launch_split_q8(const SplitArgs &a, const Q8Addr &addr, cudaStream_t s);
+// Tensor-core attention over an 8-bit pool's images (pkv_prefill_q8.cu): the
+// contract of launch_prefill_paged with one-piece images.
+cudaError_t launch_prefill_q8(const PrefillArgs &a, cudaStream_t s);
 int q8_query_block(int head_dim, int group);
 // Packed prompt attention (pkv_packed.cu); sequences sorted longest first.
 cudaError_t launch_packed(const PackedArgs &a, const int32_t *start, const int32_t *len, int32_t n_seqs,

@@ -1,0 +1,455 @@
+// pkv_prefill_q8.cu -- tensor-core attention of rows with many queries (and of
+// shared prefixes) over an 8-bit pool.
+//
+// The contract, the operand images and the arithmetic are those of the prefill
+// kernel on one-piece images: f32 queries and probabilities as two f16 pieces
+// (x times a power of two = x0 + x1, 22 bits), K and V values exact in f16 times
+// their tile's power of two, so a product is x0*y + x1*y; the largest-score
+// reference moves, and the accumulator is rescaled, only where a tile's maximum
+// passes it by 2^8; probabilities times 2^(C - c), c the exponent of their V
+// tile and C one of the chain that only falls.
+//
+// A key tile is two images (128 keys), which keeps every MMA at N = 128:
+//
+//   S_c [128 x 128] = (Q0_c + Q1_c) K_j^T    16 MMAs, A and B from shared memory
+//   D_c [128 x 128] += (P0_c + P1_c) V_j     16 MMAs, A from TMEM over S_c
+//
+// (at 64 keys the QK MMAs run at two thirds of their rate).  One CTA = two tiles
+// of 128 query rows that share every K/V tile, one softmax chain each; row m of
+// a tile is token m / G, head m % G, TMEM lane m, thread m of the chain's four
+// warps.  Each chain has one S buffer and runs QK(j), softmax(j), PV(j), QK(j+1)
+// in turn, its products issued by its own warp (8 and 10); the chains alternate
+// by turns, so that one's softmax runs under the other's 2052 clocks of MMAs.
+// Warp 9 copies the images (K_0, V_0, K_1, ... through three slots of 32 KiB).
+// Shared memory: Q pieces 128 KiB, slots 96 KiB.  TMEM: D_c at 128c, S_c / P_c
+// at 256 + 128c (P0 in its first 64 columns, P1 in the others).
+#include "pkv_elem.h"
+#include "pkv_internal.h"
+#include "pkv_softmax_tc.h"
+#include "pkv_tcgen05.h"
+
+namespace pkv {
+namespace {
+
+using namespace tc;
+
+constexpr int kHD = 128, kKeys = 128;
+constexpr int kThreads = 384;
+constexpr int kWarpMma0 = 8, kWarpLoad = 9, kWarpSpare = 11;  // warp 10: chain 1's MMAs
+// registers per thread: at launch, then of warps 8-11 and of the compute warps
+constexpr int kLaunchRegs = 168, kOtherRegs = 88, kComputeRegs = 208;
+static_assert(256 * kComputeRegs + 128 * kOtherRegs <= kThreads * kLaunchRegs, "register split");
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kQPiece = 32 * 1024;         // two k-blocks of 128 rows x 64 f16
+constexpr uint32_t kSlot = 32 * 1024;           // K: two k-blocks of 128 keys; V^T: two of 128 dims
+constexpr uint32_t kBlock = 16 * 1024;          // one k-block
+constexpr int kSlots = 3;
+constexpr size_t kSmem = 4 * kQPiece + kSlots * kSlot + 1024;  // + alignment slack
+constexpr float kGrow = 8.f;                    // log2 headroom of the reference maximum
+constexpr int kPExp = 7;                        // C <= kPExp + c: p * 2^(C - c) <= 2^15
+static_assert(kKeyTile == 64, "a key tile is two images");
+
+__device__ __forceinline__ float pow2f(int n) { return __uint_as_float(static_cast<uint32_t>(n + 127) << 23); }
+__device__ __forceinline__ float mul_pow2(float x, int n) {  // n in [-252, 254], two exact steps
+    return x * pow2f(n / 2) * pow2f(n - n / 2);
+}
+__device__ __forceinline__ int f16_scale_exp(float m) {  // brings m into [2^14, 2^15)
+    return max(-113, min(126, 14 - (static_cast<int>((__float_as_uint(m) >> 23) & 255u) - 127)));
+}
+// a pair of f32 as f16 pieces, each pair packed (a in the low half)
+__device__ __forceinline__ void split2(float a, float b, uint32_t &p0, uint32_t &p1) {
+    const __half2 h0 = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h0);
+    const __half2 h1 = __floats2half2_rn(a - f.x, b - f.y);
+    p0 = *reinterpret_cast<const uint32_t *>(&h0);
+    p1 = *reinterpret_cast<const uint32_t *>(&h1);
+}
+
+template <int G>
+__global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) {
+    constexpr int TQ = 128 / G;  // tokens per tile
+    extern __shared__ __align__(1024) unsigned char smraw[];
+    unsigned char *sm = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smraw) + 1023) & ~static_cast<uintptr_t>(1023));
+    unsigned char *ring = sm + 4 * kQPiece;  // chain c's Q0 at 2c pieces, Q1 one on
+    __shared__ uint64_t bar_full[kSlots], bar_free[kSlots], bar_q[2], bar_s[2], bar_p[2], bar_o[2];
+    __shared__ uint32_t tslot;
+
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    const int pi = blockIdx.x / a.n_kv, kvh = blockIdx.x - pi * a.n_kv;
+    // the pair's tiles: one row and one split; the second may be absent
+    const PrefillTile t0 = a.tiles[2 * pi], t1 = a.tiles[2 * pi + 1];
+    const RowDesc rd = a.rows[t0.row];
+    const int total_k = rd.past_len + rd.n_q;
+    const int kbeg = t0.split * a.split_keys, kt0 = kbeg / kKeyTile, n_img = (total_k + kKeyTile - 1) / kKeyTile;
+    auto tile_end = [&](const PrefillTile &t) {  // past the tile's last visible key of the split
+        const int nv = min(TQ, rd.n_q - t.q0);
+        return min(kbeg + a.split_keys, a.causal ? min(total_k, total_k - rd.n_q + t.q0 + nv) : total_k);
+    };
+    const int kend0 = tile_end(t0);
+    int kend1 = kbeg;
+    if (t1.row >= 0) {
+        if (t1.row == t0.row && t1.split == t0.split) kend1 = tile_end(t1);
+        else if (tid == 0 && a.err) atomicOr(a.err, 1);  // not a pair: the second tile is dropped
+    }
+    const int n0 = max(0, (kend0 - kbeg + kKeys - 1) / kKeys), n1 = max(0, (kend1 - kbeg + kKeys - 1) / kKeys);
+    const int n_max = max(n0, n1);
+    auto wait_w = [&](uint64_t *bar, uint32_t parity) {  // bounded; the warp agrees on the outcome
+        return __all_sync(0xffffffffu, wait_phase(smem_u32(bar), parity & 1u)) != 0;
+    };
+    auto slot = [](int i) { return i % kSlots; };
+    auto rph = [](int i) { return static_cast<uint32_t>(i / kSlots); };
+
+    if (warp == 0) {
+        tmem_alloc(smem_u32(&tslot), kTmemCols);
+        tmem_relinquish();
+    }
+    if (tid == 32 * kWarpLoad) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(smem_u32(&bar_full[i]), 1);
+            mbar_init(smem_u32(&bar_free[i]), 2);  // both issuing warps
+        }
+        for (int c = 0; c < 2; ++c) {
+            mbar_init(smem_u32(&bar_q[c]), 4);
+            mbar_init(smem_u32(&bar_s[c]), 1);
+            mbar_init(smem_u32(&bar_p[c]), 5);     // four compute warps, and the chain's turn
+            mbar_init(smem_u32(&bar_o[c]), 1);
+        }
+        fence_proxy_async();
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tbase = __shfl_sync(0xffffffffu, tslot, 0);
+    bool ok = true;
+    const int32_t *slots = a.img_slot + a.img_tile0[t0.row];
+    auto image = [&](int kt) {
+        return a.img + (static_cast<size_t>(__ldg(slots + kt)) * a.n_kv + kvh) * kImageBytes;
+    };
+    // a tile's second image: past the row's last one the first stands in (its
+    // keys are masked; what counts is that the bytes are a tile's values)
+    auto second = [&](int kt) { return kt + 1 < n_img ? kt + 1 : kt; };
+
+    if (warp >= 8) {
+        setmaxnreg_dec<kOtherRegs>();
+        if (warp == kWarpSpare) {
+            // nothing to do
+        } else if (warp == kWarpLoad) {
+            // ---------------- copies (one lane): K_0, V_0, K_1, ... ----------------
+            int issued = 0;
+            for (int i = 0; i < 2 * n_max; ++i) {
+                const int sl = slot(i);
+                if (i >= kSlots && !wait_w(&bar_free[sl], rph(i) - 1)) break;
+                if (elect_lane()) {
+                    const int kt = kt0 + 2 * (i >> 1);
+                    const unsigned char *ia = image(kt), *ib = image(second(kt));
+                    const uint32_t dst = smem_u32(ring + sl * kSlot), bar = smem_u32(&bar_full[sl]);
+                    mbar_expect_tx(bar, kSlot);
+                    if (i & 1) {  // V^T: a k-block of 64 keys each
+                        bulk_g2s(dst, ia + 2 * kImagePlane, kBlock, bar);
+                        bulk_g2s(dst + kBlock, ib + 2 * kImagePlane, kBlock, bar);
+                    } else {      // K: of each k-block of 64 dims, 64 keys each
+                        for (int kb = 0; kb < 2; ++kb) {
+                            bulk_g2s(dst + kb * kBlock, ia + kb * (kBlock / 2), kBlock / 2, bar);
+                            bulk_g2s(dst + kb * kBlock + kBlock / 2, ib + kb * (kBlock / 2), kBlock / 2, bar);
+                        }
+                    }
+                }
+                __syncwarp();
+                issued = i + 1;
+            }
+            // the last copies land before the CTA's shared memory is given up (bounded)
+            for (int i = max(0, issued - kSlots); i < issued; ++i) wait_w(&bar_full[slot(i)], rph(i));
+        } else {
+            // ---------------- MMA issue: chain c (one lane) ----------------
+            const int c = warp == kWarpMma0 ? 0 : 1, n = c ? n1 : n0;
+            const uint32_t tS = tbase + 256 + 128 * c, tO = tbase + 128 * c;
+            constexpr uint32_t idesc = idesc_f16(128, 128);
+            const uint64_t dQ0 = desc_sw128(smem_u32(sm + 2 * c * kQPiece)), dQ1 = desc_sw128(smem_u32(sm + (2 * c + 1) * kQPiece));
+            // S_c = Q_c K_j^T, then the barriers; on the way the turn passes
+            auto qk = [&](int j, bool pass) {
+                const int sl = slot(2 * j);
+                const uint64_t dK = desc_sw128(smem_u32(ring + sl * kSlot));
+                if (elect_lane()) {
+#pragma unroll
+                    for (int k = 0; k < kHD / 16; ++k) {
+                        const uint64_t o = ((k >> 2) * kBlock + (k & 3) * 32u) >> 4;
+                        mma_f16(tS, dQ0 + o, dK + o, idesc, k > 0);
+                        mma_f16(tS, dQ1 + o, dK + o, idesc, 1);
+                        if (k == kHD / 16 - 2 && pass) mbar_arrive(smem_u32(&bar_p[c ^ 1]));
+                    }
+                    mma_commit(smem_u32(&bar_s[c]));
+                    mma_commit(smem_u32(&bar_free[sl]));
+                }
+                __syncwarp();
+            };
+            if (n > 0) {
+                ok = wait_w(&bar_q[c], 0) && wait_w(&bar_full[0], 0);
+                if (ok) {
+                    fence_after_sync();
+                    qk(0, false);
+                }
+            }
+            for (int j = 0; j < n && ok; ++j) {
+                const int iv = 2 * j + 1, sv = slot(iv);
+                ok = wait_w(&bar_full[sv], rph(iv));
+                if (ok && j + 1 < n) ok = wait_w(&bar_full[slot(iv + 1)], rph(iv + 1));
+                // P, and the chain's turn: the other chain's products before these
+                // (chain 0's of tile j, chain 1's of tile j - 1), or the most of
+                // them, have been issued; a chain without such products takes it
+                if (ok && !(c ? j < n0 : j > 0 && j - 1 < n1) && elect_lane()) mbar_arrive(smem_u32(&bar_p[c]));
+                if (ok) ok = wait_w(&bar_p[c], j);
+                if (!ok) break;
+                fence_after_sync();
+                const uint64_t dV = desc_sw128(smem_u32(ring + sv * kSlot));
+                if (elect_lane()) {
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k) {
+                        const uint64_t o = ((k >> 2) * kBlock + (k & 3) * 32u) >> 4;
+                        mma_f16_ts(tO, tS + 8 * k, dV + o, idesc, j > 0 || k > 0);
+                        mma_f16_ts(tO, tS + 64 + 8 * k, dV + o, idesc, 1);
+                    }
+                    mma_commit(smem_u32(&bar_free[sv]));
+                    if (j + 1 == n) mma_commit(smem_u32(&bar_o[c]));
+                }
+                __syncwarp();
+                const bool pass = c ? j + 1 < n0 : j < n1;  // the other chain's products follow
+                if (j + 1 < n) qk(j + 1, pass);
+                else if (pass && elect_lane()) mbar_arrive(smem_u32(&bar_p[c ^ 1]));
+                __syncwarp();
+            }
+            // items past the chain's last tile are free as far as this chain goes
+            // (counted once they have landed, so that each counts for its own phase)
+            for (int i = 2 * n; i < 2 * n_max && ok; ++i) {
+                ok = wait_w(&bar_full[slot(i)], rph(i));
+                if (ok && elect_lane()) mbar_arrive(smem_u32(&bar_free[slot(i)]));
+            }
+            if (!ok && lane == 0 && a.err) atomicOr(a.err, 2);
+        }
+    } else {
+        // -------------- compute warps: one thread per tile row and chain --------------
+        setmaxnreg_inc<kComputeRegs>();
+        const int c = warp >> 2, n = c ? n1 : n0, m = tid & 127;
+        const int tq = m / G, g = m - tq * G, qi = (c ? t1.q0 : t0.q0) + tq;
+        const bool valid = qi < rd.n_q;
+        const int klim = min(valid ? (a.causal ? total_k - rd.n_q + qi + 1 : total_k) : 1, c ? kend1 : kend0);
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t tS = tbase + lanes + 256 + 128 * c, tO = tbase + lanes + 128 * c;
+        if (n > 0) {
+            // the query row in base-2 units, times its power of two, as two pieces
+            int qexp;
+            {
+                const float4 *qrow = reinterpret_cast<const float4 *>(
+                    a.Q + static_cast<size_t>(rd.q_row0 + (valid ? qi : 0)) * (a.n_heads * kHD) +
+                    static_cast<size_t>(kvh * G + g) * kHD);
+                float4 q[kHD / 4];
+#pragma unroll
+                for (int i = 0; i < kHD / 4; ++i) q[i] = valid ? __ldg(qrow + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                float mx = 0.f;
+#pragma unroll
+                for (int i = 0; i < kHD / 4; ++i) {
+                    q[i].x *= a.scale_log2, q[i].y *= a.scale_log2, q[i].z *= a.scale_log2, q[i].w *= a.scale_log2;
+                    mx = fmaxf(fmaxf(mx, fmaxf(fabsf(q[i].x), fabsf(q[i].y))), fmaxf(fabsf(q[i].z), fabsf(q[i].w)));
+                }
+                qexp = f16_scale_exp(mx);
+                const float up = pow2f(qexp);
+#pragma unroll
+                for (int i = 0; i < kHD / 8; ++i) {  // dims 8i .. 8i + 7: k-block i / 8, chunk i % 8
+                    const float4 x = q[2 * i], y = q[2 * i + 1];
+                    uint4 c0, c1;
+                    split2(x.x * up, x.y * up, c0.x, c1.x);
+                    split2(x.z * up, x.w * up, c0.y, c1.y);
+                    split2(y.x * up, y.y * up, c0.z, c1.z);
+                    split2(y.z * up, y.w * up, c0.w, c1.w);
+                    unsigned char *d = sm + 2 * c * kQPiece + (i >> 3) * kBlock + sw128_chunk(m, i & 7);
+                    *reinterpret_cast<uint4 *>(d) = c0;
+                    *reinterpret_cast<uint4 *>(d + kQPiece) = c1;
+                }
+            }
+            fence_proxy_async();  // before the MMAs read them
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bar_q[c]));
+
+            float m_ref = -INFINITY, l_run = 0.f;
+            int cexp = 0;  // C: D holds 2^C x the output's sum
+            auto exps = [&](int kt) { return __ldg(reinterpret_cast<const int2 *>(image(kt) + kImageExpOff)); };
+            int2 ea = exps(kt0), eb = exps(second(kt0));  // the images' exponents (K, V), a tile ahead
+            for (int j = 0; j < n; ++j) {
+                const int base = kbeg + j * kKeys;
+                const int ke[2] = {ea.x, eb.x}, ve[2] = {ea.y, eb.y};
+                if (j + 1 < n) {
+                    const int kt = kt0 + 2 * (j + 1);
+                    ea = exps(kt);
+                    eb = exps(second(kt));
+                }
+                ok = wait_w(&bar_s[c], j);
+                if (!ok) break;
+                fence_after_sync();
+                uint32_t x[kKeys];  // the row's scores (f32 bits)
+#pragma unroll
+                for (int i = 0; i < kKeys; i += 32) tmem_ld32_issue(tS + i, x + i);
+                tmem_ld_done(x);
+                auto xf = [&](int i) { return __uint_as_float(x[i]); };
+                // scores to base-2 units: one exact factor 2^sn a half (two steps
+                // where 2^sn is not a normal f32)
+                float fsc[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int sn = -(qexp + ke[h]);
+                    const bool one = sn >= -126 && sn <= 127;
+                    fsc[h] = one ? pow2f(sn) : 1.f;
+                    if (!one) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) x[64 * h + i] = __float_as_uint(mul_pow2(xf(64 * h + i), sn));
+                    }
+                }
+                if (base + kKeys > klim) {
+#pragma unroll
+                    for (int i = 0; i < kKeys; ++i) x[i] = base + i < klim ? x[i] : 0xff800000u;
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float mx[2] = {fmaxf(xf(64 * h), xf(64 * h + 1)), fmaxf(xf(64 * h + 2), xf(64 * h + 3))};
+#pragma unroll
+                    for (int i = 4; i < 64; i += 2) mx[(i >> 1) & 1] = max3(mx[(i >> 1) & 1], xf(64 * h + i), xf(64 * h + i + 1));
+                    top = fmaxf(top, fmaxf(mx[0], mx[1]) * fsc[h]);
+                }
+                const bool move = m_ref != -INFINITY && top > m_ref + kGrow;
+                const float m_use = m_ref == -INFINITY || move ? top : m_ref;
+                const float nm = m_use == -INFINITY ? 0.f : -m_use;
+                const int vmin = min(ve[0], ve[1]);
+                const int c_new = j == 0 ? kPExp + vmin : min(cexp, kPExp + vmin);
+                const float f = move ? ex2(m_ref - m_use) : 1.f;
+                // D moves with the reference or with C (QK(j), done, followed PV(j - 1));
+                // the whole warp takes the branch, as TMEM accesses are the warp's
+                if (j > 0 && (c_new != cexp || __any_sync(0xffffffffu, move))) {
+                    const int d = c_new - cexp;
+#pragma unroll 1
+                    for (int i = 0; i < kHD / 16; ++i) {
+                        float v[16];
+                        tmem_ld16(tO + 16 * i, v);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) v[k] = mul_pow2(v[k] * f, d);
+                        tmem_st16(tO + 16 * i, v);
+                    }
+                }
+                m_ref = m_use;
+                cexp = c_new;
+                // P over S, half by half: two pieces of p * 2^(C - c)
+                uint64_t sum[2] = {0, 0};
+                const uint64_t nm2 = pair(nm, nm);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int pe = cexp - ve[h];  // <= kPExp
+                    const float pf = pe >= -126 ? pow2f(pe) : 0.f;
+                    const uint64_t f2 = pair(fsc[h], fsc[h]), pf2 = pair(pf, pf);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {  // 32 keys
+                        uint32_t p0[16], p1[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const int i = 64 * h + 32 * r + 2 * k;
+                            const float2 e = unpair(fma2(pair(xf(i), xf(i + 1)), f2, nm2));
+                            const uint64_t p = pair(ex2(e.x), ex2(e.y));
+                            sum[k & 1] = add2(sum[k & 1], p);
+                            const float2 y = unpair(mul2(p, pf2));
+                            split2(y.x, y.y, p0[k], p1[k]);
+                        }
+                        tmem_st16u(tS + 32 * h + 16 * r, p0);
+                        tmem_st16u(tS + 64 + 32 * h + 16 * r, p1);
+                    }
+                }
+                const float2 s2 = unpair(add2(sum[0], sum[1]));
+                l_run = fmaf(l_run, f, s2.x + s2.y);
+                tmem_st_wait();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar_p[c]));
+            }
+            if (ok) ok = wait_w(&bar_o[c], 0);
+            if (!ok) {
+                if (lane == 0 && a.err) atomicOr(a.err, 2);
+            } else {
+                fence_after_sync();
+                // the result: D / l, then 2^-C (exact; in this order it does not
+                // overflow where D * 2^-C, up to l times it, would)
+                const PrefillTile tile = c ? t1 : t0;
+                const bool direct = tile.part0 < 0;
+                const int h = kvh * G + g;
+                float *dst;
+                size_t pidx = 0;
+                if (direct) {
+                    dst = a.out + static_cast<size_t>(rd.q_row0 + (valid ? qi : 0)) * (a.n_heads * kHD) + static_cast<size_t>(h) * kHD;
+                } else {
+                    const int nv = min(TQ, rd.n_q - tile.q0);
+                    const int kend_tile = a.causal ? min(total_k, total_k - rd.n_q + tile.q0 + nv) : total_k;
+                    const int stride = tile.stride > 0 ? tile.stride : (kend_tile + a.split_keys - 1) / a.split_keys;
+                    pidx = static_cast<size_t>(tile.part0 + (valid ? tq : 0) * stride + tile.split) * a.n_heads + h;
+                    dst = a.pacc + pidx * kHD;
+                }
+                const float scl = direct ? 1.f / l_run : 1.f;
+                // records need not start on a 16-byte boundary
+                const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15) == 0;
+#pragma unroll
+                for (int i = 0; i < kHD / 32; ++i) {
+                    float v[32];
+                    tmem_ld32(tO + 32 * i, v);
+                    if (!valid) continue;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = mul_pow2(v[k] * scl, -cexp);
+                    if (vec) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<float4 *>(dst + 32 * i + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) dst[32 * i + k] = v[k];
+                    }
+                }
+                if (valid && !direct) {
+                    a.pm[pidx] = m_ref;
+                    a.pl[pidx] = l_run;
+                }
+            }
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tbase, kTmemCols);
+}
+
+template <int G>
+cudaError_t launch_g(const PrefillArgs &a, cudaStream_t s) {
+    static PerDeviceOnce configured;  // the attributes are per function and device
+    const cudaError_t ce = configured.run([&]() -> cudaError_t {
+        // setmaxnreg.inc waits for registers of the launch's own: launch only
+        // if the kernel starts with what the split was sized for
+        cudaFuncAttributes fa{};
+        cudaError_t e = cudaFuncGetAttributes(&fa, prefill_q8_kernel<G>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs < kLaunchRegs || fa.maxThreadsPerBlock < kThreads) return cudaErrorInvalidConfiguration;
+        return cudaFuncSetAttribute(prefill_q8_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(kSmem));
+    });
+    if (ce != cudaSuccess) return ce;
+    if (a.n_tiles <= 0 || (a.n_tiles & 1) || !a.img || !a.img_tile0 || !a.img_slot) return cudaErrorInvalidValue;
+    const long long grid = static_cast<long long>(a.n_tiles / 2) * a.n_kv;
+    if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    prefill_q8_kernel<G><<<static_cast<unsigned>(grid), kThreads, kSmem, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_q8(const PrefillArgs &a, cudaStream_t s) {
+    switch (a.group) {
+        case 1: return launch_g<1>(a, s);
+        case 2: return launch_g<2>(a, s);
+        case 4: return launch_g<4>(a, s);
+        case 8: return launch_g<8>(a, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace pkv

@@ -399,9 +399,20 @@ def test_short_chunks(nq, causal, H, KV, hd):
 
 
 @pytest.mark.parametrize("G", [1, 2, 4, 8])
-def test_prefill_chunks(G):
-    w = attend_case(2 * G, 2, 128, 16, [0, 100, 7, 2000], [40, 64, 1, 150], seed=G)
+@pytest.mark.parametrize("bs,causal", [(16, 1), (16, 0), (5, 1)])
+def test_prefill_chunks(G, bs, causal):
+    w = attend_case(2 * G, 2, 128, bs, [0, 100, 7, 2000, 63, 64, 65], [40, 64, 1, 150, 65, 64, 300], seed=G, causal=causal)
     assert w["prefill_tiles"] > 0
+
+
+@pytest.mark.parametrize("scales", [(8, 0), (0, 12), (12, 12)])
+def test_prefill_blocks_of_very_different_scales(scales):
+    attend_case(8, 2, 128, 4, [300, 90], [70, 33], seed=3, scales=scales)
+
+
+@pytest.mark.parametrize("mul", [0.0, 10.0, 100.0])
+def test_prefill_score_ranges(mul):
+    attend_case(8, 2, 128, 16, [300, 90], [70, 33], seed=4, mul=mul)
 
 
 def test_splits_and_merge():
@@ -413,6 +424,10 @@ def test_splits_and_merge():
         attend_case(8, 2, 128, 16, [700, 129, 0, 300], [1, 1, 1, 6], seed=2)
         attend_case(4, 1, 64, 5, [700, 129], [1, 9], seed=3, causal=0)
         attend_case(3, 1, 20, 16, [700, 129], [1, 9], seed=4)
+        # tensor-core rows with several splits, an odd number of records
+        attend_case(8, 2, 128, 16, [1200, 129, 0], [70, 33, 40], seed=5)
+        attend_case(3, 3, 128, 16, [1000, 129], [35, 33], seed=6)
+        attend_case(8, 1, 128, 7, [1000, 129], [35, 61], seed=7, causal=0)
     finally:
         pkv.check(pkv.pkv_set_split_keys(old))
 
