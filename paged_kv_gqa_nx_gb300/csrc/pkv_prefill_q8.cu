@@ -97,6 +97,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
     auto wait_w = [&](uint64_t *bar, uint32_t parity) {  // bounded; the warp agrees on the outcome
         return __all_sync(0xffffffffu, wait_phase(smem_u32(bar), parity & 1u)) != 0;
     };
+    auto there = [&](uint64_t *bar, uint32_t parity) {  // without waiting
+        return __all_sync(0xffffffffu, test_phase(smem_u32(bar), parity & 1u)) != 0;
+    };
     auto slot = [](int i) { return i % kSlots; };
     auto rph = [](int i) { return static_cast<uint32_t>(i / kSlots); };
 
@@ -138,11 +141,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
             // ---------------- copies (one lane): K_0, V_0, K_1, ... ----------------
             int issued = 0;
             for (int i = 0; i < 2 * n_max; ++i) {
-                const int sl = slot(i);
+                const int sl = slot(i), kt = kt0 + 2 * (i >> 1);
+                const unsigned char *ia = image(kt), *ib = image(second(kt));  // looked up before the slot is free
                 if (i >= kSlots && !wait_w(&bar_free[sl], rph(i) - 1)) break;
                 if (elect_lane()) {
-                    const int kt = kt0 + 2 * (i >> 1);
-                    const unsigned char *ia = image(kt), *ib = image(second(kt));
                     const uint32_t dst = smem_u32(ring + sl * kSlot), bar = smem_u32(&bar_full[sl]);
                     mbar_expect_tx(bar, kSlot);
                     if (i & 1) {  // V^T: a k-block of 64 keys each
@@ -193,7 +195,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
             for (int j = 0; j < n && ok; ++j) {
                 const int iv = 2 * j + 1, sv = slot(iv);
                 ok = wait_w(&bar_full[sv], rph(iv));
-                if (ok && j + 1 < n) ok = wait_w(&bar_full[slot(iv + 1)], rph(iv + 1));
+                // (a K tile that is not there yet is waited for after PV)
+                const bool k_there = ok && j + 1 < n && there(&bar_full[slot(iv + 1)], rph(iv + 1));
                 // P, and the chain's turn: the other chain's products before these
                 // (chain 0's of tile j, chain 1's of tile j - 1), or the most of
                 // them, have been issued; a chain without such products takes it
@@ -214,6 +217,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                 }
                 __syncwarp();
                 const bool pass = c ? j + 1 < n0 : j < n1;  // the other chain's products follow
+                if (j + 1 < n && !k_there) ok = wait_w(&bar_full[slot(iv + 1)], rph(iv + 1));
+                if (!ok) break;
+                fence_after_sync();
                 if (j + 1 < n) qk(j + 1, pass);
                 else if (pass && elect_lane()) mbar_arrive(smem_u32(&bar_p[c ^ 1]));
                 __syncwarp();
@@ -236,34 +242,41 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t tS = tbase + lanes + 256 + 128 * c, tO = tbase + lanes + 128 * c;
         if (n > 0) {
-            // the query row in base-2 units, times its power of two, as two pieces
-            int qexp;
+            // the query rows in base-2 units, times a power of two each, as two
+            // pieces.  A warp reads its 32 rows one after another, 512 bytes at
+            // once (a row a thread took ~16,000 clocks for a CTA); lane l
+            // holds dims 4l .. 4l + 3 and keeps row l's exponent.
+            int qexp = 0;
             {
-                const float4 *qrow = reinterpret_cast<const float4 *>(
-                    a.Q + static_cast<size_t>(rd.q_row0 + (valid ? qi : 0)) * (a.n_heads * kHD) +
-                    static_cast<size_t>(kvh * G + g) * kHD);
-                float4 q[kHD / 4];
+                const int w0 = 32 * (warp & 3), q0 = c ? t1.q0 : t0.q0;
+                const float *qb = a.Q + static_cast<size_t>(rd.q_row0) * (a.n_heads * kHD) + static_cast<size_t>(kvh * G) * kHD + 4 * lane;
+                unsigned char *d = sm + 2 * c * kQPiece + (lane >> 4) * kBlock + (lane & 1) * 8;  // k-block lane / 16
+#pragma unroll 1
+                for (int r0 = 0; r0 < 32; r0 += 8) {
+                    float4 q[8];
 #pragma unroll
-                for (int i = 0; i < kHD / 4; ++i) q[i] = valid ? __ldg(qrow + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-                float mx = 0.f;
+                    for (int r = 0; r < 8; ++r) {
+                        const int row = w0 + r0 + r, t = q0 + row / G;
+                        q[r] = t < rd.n_q ? __ldg(reinterpret_cast<const float4 *>(
+                                                qb + static_cast<size_t>(t) * (a.n_heads * kHD) + (row % G) * kHD))
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
 #pragma unroll
-                for (int i = 0; i < kHD / 4; ++i) {
-                    q[i].x *= a.scale_log2, q[i].y *= a.scale_log2, q[i].z *= a.scale_log2, q[i].w *= a.scale_log2;
-                    mx = fmaxf(fmaxf(mx, fmaxf(fabsf(q[i].x), fabsf(q[i].y))), fmaxf(fabsf(q[i].z), fabsf(q[i].w)));
-                }
-                qexp = f16_scale_exp(mx);
-                const float up = pow2f(qexp);
-#pragma unroll
-                for (int i = 0; i < kHD / 8; ++i) {  // dims 8i .. 8i + 7: k-block i / 8, chunk i % 8
-                    const float4 x = q[2 * i], y = q[2 * i + 1];
-                    uint4 c0, c1;
-                    split2(x.x * up, x.y * up, c0.x, c1.x);
-                    split2(x.z * up, x.w * up, c0.y, c1.y);
-                    split2(y.x * up, y.y * up, c0.z, c1.z);
-                    split2(y.z * up, y.w * up, c0.w, c1.w);
-                    unsigned char *d = sm + 2 * c * kQPiece + (i >> 3) * kBlock + sw128_chunk(m, i & 7);
-                    *reinterpret_cast<uint4 *>(d) = c0;
-                    *reinterpret_cast<uint4 *>(d + kQPiece) = c1;
+                    for (int r = 0; r < 8; ++r) {
+                        float4 x = q[r];
+                        x.x *= a.scale_log2, x.y *= a.scale_log2, x.z *= a.scale_log2, x.w *= a.scale_log2;
+                        // largest magnitude as bits; a NaN or an infinity counts as none (its products are not finite)
+                        const float mx = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+                        const int e = f16_scale_exp(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx))));
+                        if (lane == r0 + r) qexp = e;
+                        const float up = pow2f(e);
+                        uint2 c0, c1;
+                        split2(x.x * up, x.y * up, c0.x, c1.x);
+                        split2(x.z * up, x.w * up, c0.y, c1.y);
+                        const uint32_t off = sw128_chunk(w0 + r0 + r, (lane >> 1) & 7);
+                        *reinterpret_cast<uint2 *>(d + off) = c0;
+                        *reinterpret_cast<uint2 *>(d + off + kQPiece) = c1;
+                    }
                 }
             }
             fence_proxy_async();  // before the MMAs read them
@@ -389,8 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                     dst = a.pacc + pidx * kHD;
                 }
                 const float scl = direct ? 1.f / l_run : 1.f;
-                // records need not start on a 16-byte boundary
-                const bool vec = (reinterpret_cast<uintptr_t>(dst) & 15) == 0;
+                const bool vec = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;  // whole 32-byte sectors
 #pragma unroll
                 for (int i = 0; i < kHD / 32; ++i) {
                     float v[32];
@@ -400,11 +412,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                     for (int k = 0; k < 32; ++k) v[k] = mul_pow2(v[k] * scl, -cexp);
                     if (vec) {
 #pragma unroll
-                        for (int k = 0; k < 32; k += 4)
-                            *reinterpret_cast<float4 *>(dst + 32 * i + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                        for (int k = 0; k < 32; k += 8)
+                            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + 32 * i + k),
+                                         "f"(v[k]), "f"(v[k + 1]), "f"(v[k + 2]), "f"(v[k + 3]), "f"(v[k + 4]), "f"(v[k + 5]),
+                                         "f"(v[k + 6]), "f"(v[k + 7])
+                                         : "memory");
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) dst[32 * i + k] = v[k];
+                        for (int k = 0; k < 32; k += 4)
+                            *reinterpret_cast<float4 *>(dst + 32 * i + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
                     }
                 }
                 if (valid && !direct) {

@@ -31,6 +31,18 @@ __device__ __forceinline__ bool wait_phase(uint32_t mbar, uint32_t parity) {
     }
     return false;
 }
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool test_phase(uint32_t mbar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(mbar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
 __device__ __forceinline__ float ex2(float x) {  // 2^x to about 2^-22 relative; 0 for -inf
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
