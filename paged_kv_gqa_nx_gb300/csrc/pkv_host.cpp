@@ -660,9 +660,9 @@ int32_t unit_keys(const UnitDesc &u, const RowDesc &rd, int causal, int32_t S) {
 struct TileCost {
     int64_t pair = 39, single = 27, cta = 150;
 };
-// The 8-bit pools' kernel (pkv_prefill_q8.cu): a lone tile is bound by its own
-// chain of products and softmax, so it takes as long as two.
-constexpr TileCost kTileCostQ8{22, 20, 120};
+// The 8-bit pools' kernel (pkv_prefill_q8.cu), likewise: a lone tile is bound by
+// its own chain of products and softmax, so it takes nearly as long as two.
+constexpr TileCost kTileCostQ8{26, 23, 190};
 
 // Tile pairs -> the CTA list (two entries per CTA, the second may be absent).
 // mode 0: one tile per CTA; 1: every pair; 2: pairs, with the last k of the
@@ -862,29 +862,34 @@ void build_work(std::vector<RowDesc> &rows, int causal, int32_t S, int32_t head_
 // worked out, every block of units with its merge records and its counters
 // (n_cnt of them a block).
 void q8_units(const WorkList &w, const std::vector<RowDesc> &rows, int32_t causal, int32_t S, const ShortRows &sh,
-              int32_t qblock, int32_t n_cnt, std::vector<Q8Unit> &out, int32_t *max_q, int64_t *counters) {
+              int32_t qblock, int32_t n_cnt, std::vector<Q8Block> &blocks, std::vector<Q8Part> &out, int32_t *max_q,
+              int64_t *counters) {
     std::vector<int32_t> block_of(w.n_dec_merges, -1);
-    int32_t blocks = 0;
+    int64_t joins = 0;
     out.reserve(w.units.size());
     for (const UnitDesc &u : w.units) {
         const RowDesc &rd = rows[u.row];
         const int32_t nb = std::min(qblock, rd.n_q - u.qi), S_r = split_of(rd, S, sh);
         const int32_t kbeg = rd.k0 + (u.split - rd.s0) * S_r;
         const int32_t lim = causal ? rd.past_len + u.qi + nb : rd.past_len + rd.n_q;
-        Q8Unit x{rd.slot, rd.q_row0 + u.qi, nb, rd.past_len + u.qi + 1, kbeg, std::min(kbeg + S_r, lim), -1, 0, 0, 0, 0, 0};
-        if (u.item >= 0) {
-            const MergeDesc &m = w.merges[u.item];
-            if (block_of[u.item] < 0) block_of[u.item] = blocks++;
-            x.part0 = m.part0;
-            x.n_rec = m.n_split;
-            x.rec = u.split;
-            x.n_dec = m.n_split - rd.s0;
-            x.cnt = block_of[u.item] * n_cnt;
+        int32_t b = u.item >= 0 ? block_of[u.item] : -1;
+        if (b < 0) {
+            b = static_cast<int32_t>(blocks.size());
+            Q8Block x{rd.slot, rd.q_row0 + u.qi, nb, rd.past_len + u.qi + 1, -1, 0, 0, 0};
+            if (u.item >= 0) {
+                const MergeDesc &m = w.merges[u.item];
+                block_of[u.item] = b;
+                x.part0 = m.part0;
+                x.n_rec = m.n_split;
+                x.n_dec = m.n_split - rd.s0;
+                x.cnt = static_cast<int32_t>(joins++) * n_cnt;
+            }
+            blocks.push_back(x);
         }
         *max_q = std::max(*max_q, nb);
-        out.push_back(x);
+        out.push_back({b, kbeg, std::min(kbeg + S_r, lim), u.item >= 0 ? u.split : 0});
     }
-    *counters = static_cast<int64_t>(blocks) * n_cnt;
+    *counters = joins * n_cnt;
 }
 
 // The fused append may replace the page-table upload when every pending
@@ -1181,12 +1186,13 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
         p->last_work[8] = static_cast<int64_t>(split_items.size());
     }
 
-    std::vector<Q8Unit> qunits;
+    std::vector<Q8Block> qblocks;
+    std::vector<Q8Part> qunits;
     int32_t q8_max_q = 1;
     int64_t n_counters = 0;
     if (p->q8 && attend)
         q8_units(w, rows, causal, S_dec, short_rows, q8_query_block(head_dim, group),
-                 q8_counters(head_dim, group, n_kv_heads), qunits, &q8_max_q, &n_counters);
+                 q8_counters(head_dim, group, n_kv_heads), qblocks, qunits, &q8_max_q, &n_counters);
 
     Blob &blob = p->blob;
     blob.clear();
@@ -1201,6 +1207,7 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
     const size_t rows_off = blob.put(rows.data(), p->q8 && !tensor && rope_base == 0.0 ? 0 : rows.size());
     const size_t app_off = blob.put(app.data(), app.size());
     const size_t units_off = blob.put(w.units.data(), p->q8 ? 0 : w.units.size());
+    const size_t qblocks_off = blob.put(qblocks.data(), qblocks.size());
     const size_t qunits_off = blob.put(qunits.data(), qunits.size());
     const size_t tiles_off = blob.put(w.tiles.data(), w.tiles.size());
     const size_t ctiles_off = blob.put(w.ctiles.data(), w.ctiles.size());
@@ -1210,12 +1217,14 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
     const size_t split_off = blob.put(split_items.data(), split_items.size());
     const size_t pages_off = blob.put(pages.data(), pages.size());
 
-    // few descriptors of an 8-bit pool's append and decode travel with the launches
-    InlineBlob inl;
-    const bool inlined = p->q8 && !tensor && rope_base == 0.0 && blob.b.size() <= sizeof inl.b;
+    // few descriptors of an 8-bit pool's append and decode travel with the
+    // launches; the append stores them for the tensor-core launches behind it
+    InlineBlob<kInlineLarge> inl;
+    const bool inlined = p->q8 && rope_base == 0.0 && blob.b.size() <= sizeof inl.b;
     cudaError_t e = cudaSuccess;
-    if (inlined) std::memcpy(inl.b, blob.b.data(), blob.b.size());
-    else e = upload_blob(p);
+    if (!inlined) e = upload_blob(p);
+    else std::memcpy(inl.b, blob.b.data(), blob.b.size());
+    if (inlined && tensor) e = p->desc.ensure(sizeof inl.b, p->stream, p->device);
     if (e != cudaSuccess) return cuda_fail(e, "descriptor upload");
 
     const float *Qd = Q, *Kd = K_new, *Vd = V_new;
@@ -1277,6 +1286,8 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
             ap.runs = blob_off<PtRun>(runs_off);
             ap.vals = blob_off<int32_t>(vals_off);
             ap.blob = &inl;
+            ap.blob_n = blob.b.size();
+            ap.blob_dst = tensor ? p->desc.p : nullptr;
         }
         e = launch(PKV_KERNEL_APPEND, st, [&] { return launch_append_pages_q8(ap, q8_addr(p, layer), st); });
         if (e != cudaSuccess) return cuda_fail(e, "append kernel");
@@ -1377,7 +1388,8 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
             Q8Args x{};
             x.Q = Qd;
             x.out = Od;
-            x.units = inlined ? blob_off<Q8Unit>(qunits_off) : dptr<Q8Unit>(p, qunits_off);
+            x.blocks = inlined ? blob_off<Q8Block>(qblocks_off) : dptr<Q8Block>(p, qblocks_off);
+            x.units = inlined ? blob_off<Q8Part>(qunits_off) : dptr<Q8Part>(p, qunits_off);
             x.n_units = static_cast<int32_t>(qunits.size());
             x.max_q = q8_max_q;
             x.pm = a.pm;
@@ -1392,6 +1404,7 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
             x.scale_log2 = a.scale_log2;
             x.err = p->err_dev;
             x.blob = inlined ? &inl : nullptr;
+            x.blob_n = blob.b.size();
             return launch_decode_q8(x, q8_addr(p, layer), st);
         });
         if (e != cudaSuccess) return cuda_fail(e, "decode kernel");
@@ -2266,11 +2279,12 @@ int run_pages(pkv_seq *const *seqs, int32_t M, const int32_t *start, const int32
         put_pt_runs(p, blob, &runs_off, &a.n_runs, &vals_off);
     }
     const size_t items_off = blob.put(items.data(), items.size());
-    InlineBlob inl;
+    InlineBlob<kInlineLarge> inl;
     cudaError_t e = cudaSuccess;
     if (blob.b.size() <= sizeof inl.b) {  // few descriptors travel with the launch
         std::memcpy(inl.b, blob.b.data(), blob.b.size());
         a.blob = &inl;
+        a.blob_n = blob.b.size();
     } else {
         e = upload_blob(p);
     }

@@ -83,24 +83,53 @@ struct PageItem {
     int32_t blk, off, n, row0;
 };
 
-// One decode unit over an 8-bit pool, as the host lays it out: queries q_row ..
-// q_row + nq - 1 (rows of Q and out), of which query t sees the keys below
-// see0 + t (causal) or kend, over keys [kbeg, kend).  part0 < 0: the unit is its
-// queries' only one and writes out; else its partial of query t is record
-// part0 + t * n_rec + rec, and the last of the block's n_dec units to finish (by
-// the counters cnt .. of the block) joins all n_rec records of each query.
-struct Q8Unit {
+// A block of queries over an 8-bit pool, and one decode unit of it (two lists,
+// as the host lays them out).  Queries q_row .. q_row + nq - 1 (rows of Q and
+// out), of which query t sees the keys below see0 + t (causal) or kend; the unit
+// takes keys [kbeg, kend).  part0 < 0: the unit is the block's only one and
+// writes out; else its partial of query t is record part0 + t * n_rec + rec, and
+// the last of the block's n_dec units to finish (by the counters cnt ..) joins
+// all n_rec records of each query.
+struct Q8Block {
     int32_t slot, q_row, nq, see0;
-    int32_t kbeg, kend, part0, n_rec;
-    int32_t rec, n_dec, cnt, pad;
+    int32_t part0, n_rec, n_dec, cnt;
+};
+struct Q8Part {
+    int32_t block, kbeg, kend, rec;
+};
+struct Q8Unit : Q8Block {
+    int32_t kbeg, kend, rec;
 };
 
 // A call's descriptors where they are few: they travel in the launch's
-// parameters instead of through an upload.
-constexpr int32_t kInlineBytes = 3840;
+// parameters instead of through an upload, which the launch waits 7 us for
+// (prompts of 9,000 rows: 37.7 -> 22.6 us for their append and read; decode
+// of 64 sequences 54.9 -> 47.2 us).  A launch takes longer with more of them
+// (one token of 64 sequences: 16.3 us with the small blob, 19.3 with the
+// large), so there are two sizes; a launch's parameters end at 32,764 bytes.
+constexpr int32_t kInlineSmall = 3840, kInlineLarge = 31744;
+template <int N>
 struct alignas(16) InlineBlob {
-    unsigned char b[kInlineBytes];
+    unsigned char b[N];
 };
+struct NoBlob {};  // descriptors in device memory
+// An address in device memory, or a byte offset into the inline blob held in
+// the pointer.
+template <class T>
+__host__ __device__ __forceinline__ const T *blob_at(const T *p, const NoBlob &) {
+    return p;
+}
+template <class T, int N>
+__host__ __device__ __forceinline__ const T *blob_at(const T *p, const InlineBlob<N> &blob) {
+    return reinterpret_cast<const T *>(blob.b + reinterpret_cast<uintptr_t>(p));
+}
+// Calls f with the blob of n bytes at p (room for the large one), or with none.
+template <class F>
+auto with_blob(const InlineBlob<kInlineLarge> *p, size_t n, F &&f) {
+    if (!p) return f(NoBlob{});
+    if (n <= kInlineSmall) return f(*reinterpret_cast<const InlineBlob<kInlineSmall> *>(p));
+    return f(*p);
+}
 
 // Element types of packed rows (pkv_dtype) and of pool storage.
 enum class Elem : int32_t { f32 = 0, bf16 = 1, f16 = 2, fp8 = 3, q8 = 4 };
@@ -117,23 +146,29 @@ struct PagesArgs {
     const int32_t *vals = nullptr;
     int32_t n_runs = 0;
     int32_t *err = nullptr;
-    // With an inline blob, items, runs and vals are byte offsets into it (held
-    // in the pointers), which the kernels turn into addresses.
-    const InlineBlob *blob = nullptr;
+    // With an inline blob (of blob_n bytes), items, runs and vals are byte
+    // offsets into it, which the kernels turn into addresses.
+    const InlineBlob<kInlineLarge> *blob = nullptr;
+    size_t blob_n = 0;
+    // With blob_dst the append also stores the blob there, for launches behind it.
+    void *blob_dst = nullptr;
+    int32_t n_pre = 0;  // leading blocks that upload runs or the blob (set by the launch)
 };
 
 // The decode launch over an 8-bit pool.
 struct Q8Args {
     const float *Q;
     float *out;
-    const Q8Unit *units;  // or a byte offset into the inline blob
+    const Q8Block *blocks;  // these two: or byte offsets into the inline blob
+    const Q8Part *units;
     int32_t n_units, max_q;
     float *pm, *pl, *pacc;
     uint32_t *cnt;        // zero between launches: the joining unit clears its own
     int32_t n_heads, n_kv, hd, group, causal;
     float scale_log2;
     int32_t *err;
-    const InlineBlob *blob = nullptr;
+    const InlineBlob<kInlineLarge> *blob = nullptr;
+    size_t blob_n = 0;
 };
 
 // Rotated copies of the new rows (RoPE on append over an 8-bit pool, whose

@@ -232,14 +232,11 @@ __device__ __forceinline__ RowSpan row_span(const PagesArgs &p, const PagedAddr 
 }
 
 // Descriptors in device memory (NoBlob) or in the launch's parameters.
-struct NoBlob {};
 template <class B>
 __device__ __forceinline__ void place(PagesArgs &p, const B &blob) {
-    if constexpr (std::is_same<B, InlineBlob>::value) {
-        p.items = reinterpret_cast<const PageItem *>(blob.b + reinterpret_cast<uintptr_t>(p.items));
-        p.runs = reinterpret_cast<const PtRun *>(blob.b + reinterpret_cast<uintptr_t>(p.runs));
-        p.vals = reinterpret_cast<const int32_t *>(blob.b + reinterpret_cast<uintptr_t>(p.vals));
-    }
+    p.items = blob_at(p.items, blob);
+    p.runs = blob_at(p.runs, blob);
+    p.vals = blob_at(p.vals, blob);
 }
 // A launch that may start while this one runs waits for its end before it
 // reads what this one writes; it may set itself up from now on.
@@ -251,6 +248,18 @@ __device__ __forceinline__ bool upload_runs(const PagesArgs &p, const PagedAddr 
     int32_t *dst = a.pt + static_cast<size_t>(r.slot) * a.max_blocks + r.start;
     for (int i = threadIdx.x; i < r.count; i += blockDim.x) dst[i] = p.vals[r.voff + i];
     return true;
+}
+template <class B>
+__device__ __forceinline__ bool before_items(const PagesArgs &p, const PagedAddr &a, const B &blob) {
+    if constexpr (!std::is_same<B, NoBlob>::value) {
+        if (p.n_pre > p.n_runs && static_cast<int>(blockIdx.x) == p.n_runs) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(blob.b);
+            for (int i = threadIdx.x; i < static_cast<int>((p.blob_n + 15) / 16); i += blockDim.x)
+                static_cast<uint4 *>(p.blob_dst)[i] = src[i];
+            return true;
+        }
+    }
+    return upload_runs(p, a);
 }
 
 // The step of a page's head after rows of largest magnitude m (f32 bits) come
@@ -319,8 +328,8 @@ __global__ void __launch_bounds__(256) append_pages_q8_kernel(PagesArgs p, Q8Add
     place(p, blob);
     let_next_start();
     const PagedAddr &a = q.a;
-    if (upload_runs(p, a)) return;
-    const int w = (static_cast<int>(blockIdx.x) - p.n_runs) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (before_items(p, a, blob)) return;
+    const int w = (static_cast<int>(blockIdx.x) - p.n_pre) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (w >= p.n_items * 2 * q.n_kv) return;
     const RowSpan r = row_span(p, a, q.hd, q.n_kv, w);
     if (!r.ok) {
@@ -382,8 +391,8 @@ __global__ void __launch_bounds__(256, 2) append_stream_q8_kernel(PagesArgs p, Q
     place(p, blob);
     let_next_start();
     const PagedAddr &a = q.a;
-    if (upload_runs(p, a)) return;
-    const int w = (static_cast<int>(blockIdx.x) - p.n_runs) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (before_items(p, a, blob)) return;
+    const int w = (static_cast<int>(blockIdx.x) - p.n_pre) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int per_item = 2 * q.n_kv, step = n_warps / per_item;  // n_warps: a multiple of per_item
     int it = w / per_item;
     const int sub = w - it * per_item;
@@ -602,11 +611,9 @@ bool grid_of(long long warps, int n_runs, unsigned *grid) {
     return true;
 }
 
-// Calls f with the inline blob, or with none.
 template <class F>
-cudaError_t with_blob(const PagesArgs &p, F &&f) {
-    if (p.blob) f(*p.blob);
-    else f(NoBlob{});
+cudaError_t launch_with(const PagesArgs &p, F &&f) {
+    with_blob(p.blob, p.blob_n, f);
     return cudaGetLastError();
 }
 
@@ -615,7 +622,7 @@ cudaError_t append_as(const PagesArgs &p, const PagedAddr &a, cudaStream_t s) {
     const int n_groups = (a.kv_dim + kColGroup - 1) / kColGroup;
     unsigned grid;
     if (!grid_of(2LL * p.n_items * n_groups, p.n_runs, &grid)) return cudaErrorInvalidConfiguration;
-    return with_blob(p, [&](const auto &b) {
+    return launch_with(p, [&](const auto &b) {
         using B = std::decay_t<decltype(b)>;
         if (vec_ok(p, a, kColGroup)) append_pages_kernel<B, S, E, true><<<grid, 256, 0, s>>>(p, a, n_groups, b);
         else append_pages_kernel<B, S, E, false><<<grid, 256, 0, s>>>(p, a, n_groups, b);
@@ -628,7 +635,9 @@ cudaError_t append_from(const PagesArgs &p, const PagedAddr &a, cudaStream_t s) 
     return append_as<S, float>(p, a, s);
 }
 template <class S>
-cudaError_t append_q8_from(const PagesArgs &p, const Q8Addr &q, cudaStream_t s) {
+cudaError_t append_q8_from(const PagesArgs &args, const Q8Addr &q, cudaStream_t s) {
+    PagesArgs p = args;
+    p.n_pre = p.n_runs + (p.blob && p.blob_dst ? 1 : 0);
     unsigned grid;
     constexpr int kHold = 8;
     const int cpr = q.hd / 8;
@@ -638,14 +647,14 @@ cudaError_t append_q8_from(const PagesArgs &p, const Q8Addr &q, cudaStream_t s) 
         const long long warps = 2LL * p.n_items * q.n_kv, round = 16LL * q.n_kv;  // 8 items, 2 n_kv blocks
         const long long want = std::min<long long>((warps + round - 1) / round, std::max<long long>(1, 2LL * 152 * 8 / round));
         const int n_warps = static_cast<int>(want * round);
-        if (!grid_of(n_warps, p.n_runs, &grid)) return cudaErrorInvalidConfiguration;
-        return with_blob(p, [&](const auto &b) {
+        if (!grid_of(n_warps, p.n_pre, &grid)) return cudaErrorInvalidConfiguration;
+        return launch_with(p, [&](const auto &b) {
             append_stream_q8_kernel<std::decay_t<decltype(b)>, S, kHold, sizeof(S) == 2>
                 <<<grid, 256, 0, s>>>(p, q, n_warps, b);
         });
     }
-    if (!grid_of(2LL * p.n_items * q.n_kv, p.n_runs, &grid)) return cudaErrorInvalidConfiguration;
-    return with_blob(p, [&](const auto &b) {
+    if (!grid_of(2LL * p.n_items * q.n_kv, p.n_pre, &grid)) return cudaErrorInvalidConfiguration;
+    return launch_with(p, [&](const auto &b) {
         using B = std::decay_t<decltype(b)>;
         if (vec_ok(p, q.a, q.hd)) append_pages_q8_kernel<B, S, true><<<grid, 256, 0, s>>>(p, q, b);
         else append_pages_q8_kernel<B, S, false><<<grid, 256, 0, s>>>(p, q, b);
@@ -656,7 +665,7 @@ cudaError_t read_as(const PagesArgs &p, const PagedAddr &a, cudaStream_t s) {
     const int n_groups = (a.kv_dim + kColGroup - 1) / kColGroup;
     unsigned grid;
     if (!grid_of(2LL * p.n_items * n_groups, 0, &grid)) return cudaErrorInvalidConfiguration;
-    return with_blob(p, [&](const auto &b) {
+    return launch_with(p, [&](const auto &b) {
         using B = std::decay_t<decltype(b)>;
         if (vec_ok(p, a, kColGroup)) read_pages_kernel<B, D, E, true><<<grid, 256, 0, s>>>(p, a, n_groups, b);
         else read_pages_kernel<B, D, E, false><<<grid, 256, 0, s>>>(p, a, n_groups, b);
@@ -672,7 +681,7 @@ template <class D>
 cudaError_t read_q8_to(const PagesArgs &p, const Q8Addr &q, cudaStream_t s) {
     unsigned grid;
     if (!grid_of(2LL * p.n_items * q.n_kv, 0, &grid)) return cudaErrorInvalidConfiguration;
-    return with_blob(p, [&](const auto &b) {
+    return launch_with(p, [&](const auto &b) {
         using B = std::decay_t<decltype(b)>;
         if (vec_ok(p, q.a, q.hd)) read_pages_q8_kernel<B, D, true><<<grid, 256, 0, s>>>(p, q, b);
         else read_pages_q8_kernel<B, D, false><<<grid, 256, 0, s>>>(p, q, b);

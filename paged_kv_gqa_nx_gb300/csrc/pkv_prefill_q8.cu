@@ -23,6 +23,15 @@
 // Warp 9 copies the images (K_0, V_0, K_1, ... through three slots of 32 KiB).
 // Shared memory: Q pieces 128 KiB, slots 96 KiB.  TMEM: D_c at 128c, S_c / P_c
 // at 256 + 128c (P0 in its first 64 columns, P1 in the others).
+//
+// Measured (8 rows of 512 queries behind 2,048 keys, 32 heads over 8, 568
+// CTAs of 18.5 key tiles on average): 252 us, 1.21 PFLOP/s of f16 products.  A
+// key tile takes 5,200 clocks where its MMAs alone take 4,104: what is left is
+// the wait of a chain for its own softmax (2,100 to 2,400 clocks from S to P)
+// and for the slots; 17,000 clocks a CTA go to its start and its output.
+// Measured and not taken: six slots of 16 KiB (286 us), PV begun at the first
+// half of P (no gain on either), 8 or 32 query rows in flight a warp (258 and
+// 259 us).
 #include "pkv_elem.h"
 #include "pkv_internal.h"
 #include "pkv_softmax_tc.h"
@@ -252,17 +261,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                 const float *qb = a.Q + static_cast<size_t>(rd.q_row0) * (a.n_heads * kHD) + static_cast<size_t>(kvh * G) * kHD + 4 * lane;
                 unsigned char *d = sm + 2 * c * kQPiece + (lane >> 4) * kBlock + (lane & 1) * 8;  // k-block lane / 16
 #pragma unroll 1
-                for (int r0 = 0; r0 < 32; r0 += 8) {
-                    float4 q[8];
+                for (int r0 = 0; r0 < 32; r0 += 16) {
+                    float4 q[16];
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) {
+                    for (int r = 0; r < 16; ++r) {
                         const int row = w0 + r0 + r, t = q0 + row / G;
                         q[r] = t < rd.n_q ? __ldg(reinterpret_cast<const float4 *>(
                                                 qb + static_cast<size_t>(t) * (a.n_heads * kHD) + (row % G) * kHD))
                                           : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) {
+                    for (int r = 0; r < 16; ++r) {
                         float4 x = q[r];
                         x.x *= a.scale_log2, x.y *= a.scale_log2, x.z *= a.scale_log2, x.w *= a.scale_log2;
                         // largest magnitude as bits; a NaN or an infinity counts as none (its products are not finite)
@@ -407,10 +416,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                 for (int i = 0; i < kHD / 32; ++i) {
                     float v[32];
                     tmem_ld32(tO + 32 * i, v);
-                    if (!valid) continue;
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = mul_pow2(v[k] * scl, -cexp);
-                    if (vec) {
+                    if (!valid) {
+                        // nothing to write
+                    } else if (vec) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 8)
                             asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + 32 * i + k),
@@ -422,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                         for (int k = 0; k < 32; k += 4)
                             *reinterpret_cast<float4 *>(dst + 32 * i + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
                     }
+                    __syncwarp();  // TMEM loads are the warp's
                 }
                 if (valid && !direct) {
                     a.pm[pidx] = m_ref;

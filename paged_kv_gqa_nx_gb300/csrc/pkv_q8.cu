@@ -44,13 +44,10 @@ __device__ __forceinline__ int block_off(const PagedAddr &a, int pos) {
 
 // ------------------------------------------------------------------ units ----
 
-struct NoBlob {};
 template <class B>
 __device__ __forceinline__ Q8Unit unit_of(const Q8Args &a, const B &blob, int i) {
-    const Q8Unit *u = a.units;
-    if constexpr (std::is_same<B, InlineBlob>::value)
-        u = reinterpret_cast<const Q8Unit *>(blob.b + reinterpret_cast<uintptr_t>(u));
-    return u[i];
+    const Q8Part p = blob_at(a.units, blob)[i];
+    return Q8Unit{blob_at(a.blocks, blob)[p.block], p.kbeg, p.kend, p.rec};
 }
 // Waits for the end of the launch that this one was allowed to overlap.
 __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
@@ -899,7 +896,7 @@ int q8_counters(int head_dim, int group, int n_kv) {
 }
 
 cudaError_t launch_decode_q8(const Q8Args &a, const Q8Addr &q, cudaStream_t s) {
-    return a.blob ? launch_decode_with(a, q, *a.blob, s) : launch_decode_with(a, q, NoBlob{}, s);
+    return with_blob(a.blob, a.blob_n, [&](const auto &b) { return launch_decode_with(a, q, b, s); });
 }
 
 cudaError_t launch_split_q8(const SplitArgs &a, const Q8Addr &q, cudaStream_t s) {
