@@ -432,6 +432,38 @@ def test_splits_and_merge():
         pkv.check(pkv.pkv_set_split_keys(old))
 
 
+@pytest.mark.parametrize("rows", [20, 150, 900])
+@pytest.mark.parametrize("chunk", [1, 40])
+def test_few_and_many_rows(rows, chunk):
+    """Descriptors that travel with the launches (two sizes) and that are uploaded, also for tensor-core rows."""
+    past = [(37 * r) % 45 for r in range(rows)]
+    attend_case(2, 1, 128, 16, past, [chunk] + [1 + r % 2 for r in range(1, rows)], seed=8, check_alone=rows < 50)
+
+
+@pytest.mark.parametrize("rows", [20, 150, 900])
+def test_packed_rows_of_few_and_many_sequences(rows):
+    """The same of append and read; a row comes back within half a step of its block."""
+    pool = Q8Pool(3 * rows, 1, 1, 64, 4, max_seqs=rows + 1)
+    try:
+        n = [1 + r % 9 for r in range(rows)]
+        seqs = [pool.seq(m) for m in n]
+        x, y = randn(sum(n), 64, seed=1), randn(sum(n), 64, seed=2)
+        pool.append(seqs, x, y, n)
+        k, v = torch.full_like(x, float("nan")), torch.full_like(y, float("nan"))
+        pkv.check(pkv.pkv_read_packed(seqs, [0] * rows, n, 0, k, v))
+        pool.ok()
+        at = 0
+        for s, m in zip(seqs, n):
+            K, V = pool.values(s, m)
+            assert torch.equal(k[at:at + m].double(), K[:, 0]) and torch.equal(v[at:at + m].double(), V[:, 0])
+            ids = torch.tensor(pkv.pkv_seq_page_table(s), device="cuda")[torch.arange(m, device="cuda") // 4]
+            assert bool(((K[:, 0] - x[at:at + m]).abs() <= pool.Ks[ids, 0] / 2).all())
+            assert bool(((V[:, 0] - y[at:at + m]).abs() <= pool.Vs[ids, 0] / 2).all())
+            at += m
+    finally:
+        pool.close()
+
+
 @pytest.mark.parametrize("scales", [(6, 0), (0, 10), (10, 10)])
 @pytest.mark.parametrize("bs", [1, 16])
 def test_blocks_of_very_different_scales(scales, bs):
