@@ -52,8 +52,9 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kQPiece = 32 * 1024;         // two k-blocks of 128 rows x 64 f16
 constexpr uint32_t kSlot = 32 * 1024;           // K: two k-blocks of 128 keys; V^T: two of 128 dims
 constexpr uint32_t kBlock = 16 * 1024;          // one k-block
-constexpr int kSlots = 3;
+constexpr int kSlots = 3, kLoneSlots = kSlots + 2;  // a lone tile's has the other's query pieces' place too
 constexpr size_t kSmem = 4 * kQPiece + kSlots * kSlot + 1024;  // + alignment slack
+static_assert(2 * kQPiece == (kLoneSlots - kSlots) * kSlot, "the second tile's pieces are whole slots");
 constexpr float kGrow = 8.f;                    // log2 headroom of the reference maximum
 constexpr int kPExp = 7;                        // C <= kPExp + c: p * 2^(C - c) <= 2^15
 static_assert(kKeyTile == 64, "a key tile is two images");
@@ -80,8 +81,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
     extern __shared__ __align__(1024) unsigned char smraw[];
     unsigned char *sm = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smraw) + 1023) & ~static_cast<uintptr_t>(1023));
-    unsigned char *ring = sm + 4 * kQPiece;  // chain c's Q0 at 2c pieces, Q1 one on
-    __shared__ uint64_t bar_full[kSlots], bar_free[kSlots], bar_q[2], bar_s[2], bar_p[2], bar_o[2];
+    __shared__ uint64_t bar_full[kLoneSlots], bar_free[kLoneSlots], bar_q[2], bar_s[2], bar_p[2], bar_o[2], bar_v;
     __shared__ uint32_t tslot;
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -103,28 +103,32 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
     }
     const int n0 = max(0, (kend0 - kbeg + kKeys - 1) / kKeys), n1 = max(0, (kend1 - kbeg + kKeys - 1) / kKeys);
     const int n_max = max(n0, n1);
+    const bool lone = n1 == 0;  // chain 0 alone, on both S buffers
+    const int ns = lone ? kLoneSlots : kSlots;
+    unsigned char *ring = sm + (lone ? 2 : 4) * kQPiece;  // chain c's Q0 at 2c pieces, Q1 one on
     auto wait_w = [&](uint64_t *bar, uint32_t parity) {  // bounded; the warp agrees on the outcome
         return __all_sync(0xffffffffu, wait_phase(smem_u32(bar), parity & 1u)) != 0;
     };
     auto there = [&](uint64_t *bar, uint32_t parity) {  // without waiting
         return __all_sync(0xffffffffu, test_phase(smem_u32(bar), parity & 1u)) != 0;
     };
-    auto slot = [](int i) { return i % kSlots; };
-    auto rph = [](int i) { return static_cast<uint32_t>(i / kSlots); };
+    auto slot = [&](int i) { return lone ? i % kLoneSlots : i % kSlots; };
+    auto rph = [&](int i) { return static_cast<uint32_t>(lone ? i / kLoneSlots : i / kSlots); };
 
     if (warp == 0) {
         tmem_alloc(smem_u32(&tslot), kTmemCols);
         tmem_relinquish();
     }
     if (tid == 32 * kWarpLoad) {
-        for (int i = 0; i < kSlots; ++i) {
+        for (int i = 0; i < ns; ++i) {
             mbar_init(smem_u32(&bar_full[i]), 1);
-            mbar_init(smem_u32(&bar_free[i]), 2);  // both issuing warps
+            mbar_init(smem_u32(&bar_free[i]), lone ? 1 : 2);  // the issuing warps
         }
+        mbar_init(smem_u32(&bar_v), 1);
         for (int c = 0; c < 2; ++c) {
             mbar_init(smem_u32(&bar_q[c]), 4);
             mbar_init(smem_u32(&bar_s[c]), 1);
-            mbar_init(smem_u32(&bar_p[c]), 5);     // four compute warps, and the chain's turn
+            mbar_init(smem_u32(&bar_p[c]), lone ? 4 : 5);  // four compute warps, and the chain's turn
             mbar_init(smem_u32(&bar_o[c]), 1);
         }
         fence_proxy_async();
@@ -152,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
             for (int i = 0; i < 2 * n_max; ++i) {
                 const int sl = slot(i), kt = kt0 + 2 * (i >> 1);
                 const unsigned char *ia = image(kt), *ib = image(second(kt));  // looked up before the slot is free
-                if (i >= kSlots && !wait_w(&bar_free[sl], rph(i) - 1)) break;
+                if (i >= ns && !wait_w(&bar_free[sl], rph(i) - 1)) break;
                 if (elect_lane()) {
                     const uint32_t dst = smem_u32(ring + sl * kSlot), bar = smem_u32(&bar_full[sl]);
                     mbar_expect_tx(bar, kSlot);
@@ -170,15 +174,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                 issued = i + 1;
             }
             // the last copies land before the CTA's shared memory is given up (bounded)
-            for (int i = max(0, issued - kSlots); i < issued; ++i) wait_w(&bar_full[slot(i)], rph(i));
+            for (int i = max(0, issued - ns); i < issued; ++i) wait_w(&bar_full[slot(i)], rph(i));
         } else {
             // ---------------- MMA issue: chain c (one lane) ----------------
             const int c = warp == kWarpMma0 ? 0 : 1, n = c ? n1 : n0;
-            const uint32_t tS = tbase + 256 + 128 * c, tO = tbase + 128 * c;
+            const uint32_t tO = tbase + 128 * c;
             constexpr uint32_t idesc = idesc_f16(128, 128);
             const uint64_t dQ0 = desc_sw128(smem_u32(sm + 2 * c * kQPiece)), dQ1 = desc_sw128(smem_u32(sm + (2 * c + 1) * kQPiece));
             // S_c = Q_c K_j^T, then the barriers; on the way the turn passes
-            auto qk = [&](int j, bool pass) {
+            // (b: the S buffer, a chain's own or a lone chain's of the tile)
+            auto qk = [&](int j, int b, bool pass) {
+                const uint32_t tS = tbase + 256 + 128 * b;
                 const int sl = slot(2 * j);
                 const uint64_t dK = desc_sw128(smem_u32(ring + sl * kSlot));
                 if (elect_lane()) {
@@ -189,8 +195,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                         mma_f16(tS, dQ1 + o, dK + o, idesc, 1);
                         if (k == kHD / 16 - 2 && pass) mbar_arrive(smem_u32(&bar_p[c ^ 1]));
                     }
-                    mma_commit(smem_u32(&bar_s[c]));
+                    mma_commit(smem_u32(&bar_s[b]));
                     mma_commit(smem_u32(&bar_free[sl]));
+                }
+                __syncwarp();
+            };
+            // D_c += P_c V_j
+            auto pv = [&](int j, int b) {
+                const uint32_t tS = tbase + 256 + 128 * b;
+                const int sv = slot(2 * j + 1);
+                const uint64_t dV = desc_sw128(smem_u32(ring + sv * kSlot));
+                if (elect_lane()) {
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k) {
+                        const uint64_t o = ((k >> 2) * kBlock + (k & 3) * 32u) >> 4;
+                        mma_f16_ts(tO, tS + 8 * k, dV + o, idesc, j > 0 || k > 0);
+                        mma_f16_ts(tO, tS + 64 + 8 * k, dV + o, idesc, 1);
+                    }
+                    mma_commit(smem_u32(&bar_free[sv]));
+                    if (lone) mma_commit(smem_u32(&bar_v));
+                    if (j + 1 == n) mma_commit(smem_u32(&bar_o[c]));
                 }
                 __syncwarp();
             };
@@ -198,10 +222,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                 ok = wait_w(&bar_q[c], 0) && wait_w(&bar_full[0], 0);
                 if (ok) {
                     fence_after_sync();
-                    qk(0, false);
+                    qk(0, c, false);
                 }
             }
-            for (int j = 0; j < n && ok; ++j) {
+            // a lone chain: QK(j + 1) runs under softmax(j).  A compute warp may be
+            // a tile ahead of another, so S and P have a barrier a buffer.
+            for (int j = 0; lone && j < n && ok; ++j) {
+                const int iv = 2 * j + 1;
+                if (j + 1 < n) {
+                    ok = wait_w(&bar_full[slot(iv + 1)], rph(iv + 1));
+                    if (!ok) break;
+                    fence_after_sync();
+                    qk(j + 1, (j + 1) & 1, false);
+                }
+                ok = wait_w(&bar_full[slot(iv)], rph(iv)) && wait_w(&bar_p[j & 1], j >> 1);
+                if (!ok) break;
+                fence_after_sync();
+                pv(j, j & 1);
+            }
+            for (int j = 0; !lone && j < n && ok; ++j) {
                 const int iv = 2 * j + 1, sv = slot(iv);
                 ok = wait_w(&bar_full[sv], rph(iv));
                 // (a K tile that is not there yet is waited for after PV)
@@ -213,29 +252,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                 if (ok) ok = wait_w(&bar_p[c], j);
                 if (!ok) break;
                 fence_after_sync();
-                const uint64_t dV = desc_sw128(smem_u32(ring + sv * kSlot));
-                if (elect_lane()) {
-#pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k) {
-                        const uint64_t o = ((k >> 2) * kBlock + (k & 3) * 32u) >> 4;
-                        mma_f16_ts(tO, tS + 8 * k, dV + o, idesc, j > 0 || k > 0);
-                        mma_f16_ts(tO, tS + 64 + 8 * k, dV + o, idesc, 1);
-                    }
-                    mma_commit(smem_u32(&bar_free[sv]));
-                    if (j + 1 == n) mma_commit(smem_u32(&bar_o[c]));
-                }
-                __syncwarp();
+                pv(j, c);
                 const bool pass = c ? j + 1 < n0 : j < n1;  // the other chain's products follow
                 if (j + 1 < n && !k_there) ok = wait_w(&bar_full[slot(iv + 1)], rph(iv + 1));
                 if (!ok) break;
                 fence_after_sync();
-                if (j + 1 < n) qk(j + 1, pass);
+                if (j + 1 < n) qk(j + 1, c, pass);
                 else if (pass && elect_lane()) mbar_arrive(smem_u32(&bar_p[c ^ 1]));
                 __syncwarp();
             }
             // items past the chain's last tile are free as far as this chain goes
             // (counted once they have landed, so that each counts for its own phase)
-            for (int i = 2 * n; i < 2 * n_max && ok; ++i) {
+            for (int i = 2 * n; !lone && i < 2 * n_max && ok; ++i) {
                 ok = wait_w(&bar_full[slot(i)], rph(i));
                 if (ok && elect_lane()) mbar_arrive(smem_u32(&bar_free[slot(i)]));
             }
@@ -249,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
         const bool valid = qi < rd.n_q;
         const int klim = min(valid ? (a.causal ? total_k - rd.n_q + qi + 1 : total_k) : 1, c ? kend1 : kend0);
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-        const uint32_t tS = tbase + lanes + 256 + 128 * c, tO = tbase + lanes + 128 * c;
+        const uint32_t tO = tbase + lanes + 128 * c;
         if (n > 0) {
             // the query rows in base-2 units, times a power of two each, as two
             // pieces.  A warp reads its 32 rows one after another, 512 bytes at
@@ -304,7 +332,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                     ea = exps(kt);
                     eb = exps(second(kt));
                 }
-                ok = wait_w(&bar_s[c], j);
+                const int b = lone ? j & 1 : c;
+                const uint32_t tS = tbase + lanes + 256 + 128 * b;
+                ok = wait_w(&bar_s[b], lone ? j >> 1 : j);
                 if (!ok) break;
                 fence_after_sync();
                 uint32_t x[kKeys];  // the row's scores (f32 bits)
@@ -343,9 +373,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                 const int vmin = min(ve[0], ve[1]);
                 const int c_new = j == 0 ? kPExp + vmin : min(cexp, kPExp + vmin);
                 const float f = move ? ex2(m_ref - m_use) : 1.f;
-                // D moves with the reference or with C (QK(j), done, followed PV(j - 1));
-                // the whole warp takes the branch, as TMEM accesses are the warp's
+                // D moves with the reference or with C (after PV(j - 1): QK(j), done,
+                // followed it, but for a lone chain's); the whole warp takes the
+                // branch, as TMEM accesses are the warp's
                 if (j > 0 && (c_new != cexp || __any_sync(0xffffffffu, move))) {
+                    if (lone) {
+                        ok = wait_w(&bar_v, j - 1);
+                        if (!ok) break;
+                        fence_after_sync();
+                    }
                     const int d = c_new - cexp;
 #pragma unroll 1
                     for (int i = 0; i < kHD / 16; ++i) {
@@ -387,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                 tmem_st_wait();
                 fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar_p[c]));
+                if (lane == 0) mbar_arrive(smem_u32(&bar_p[b]));
             }
             if (ok) ok = wait_w(&bar_o[c], 0);
             if (!ok) {
