@@ -660,9 +660,9 @@ int32_t unit_keys(const UnitDesc &u, const RowDesc &rd, int causal, int32_t S) {
 struct TileCost {
     int64_t pair = 39, single = 27, cta = 150;
 };
-// The 8-bit pools' kernel (pkv_prefill_q8.cu), likewise: a lone tile is bound by
-// its own chain of products and softmax, so it takes nearly as long as two.
-constexpr TileCost kTileCostQ8{26, 23, 190};
+// The 8-bit pools' kernel (pkv_prefill_q8.cu), likewise: 5.2k clocks a 128-key
+// tile with two chains, 2.9k with one, 20k a CTA and 5k until the next starts.
+constexpr TileCost kTileCostQ8{26, 15, 250};
 
 // Tile pairs -> the CTA list (two entries per CTA, the second may be absent).
 // mode 0: one tile per CTA; 1: every pair; 2: pairs, with the last k of the

@@ -24,14 +24,19 @@
 // Shared memory: Q pieces 128 KiB, slots 96 KiB.  TMEM: D_c at 128c, S_c / P_c
 // at 256 + 128c (P0 in its first 64 columns, P1 in the others).
 //
-// Measured (8 rows of 512 queries behind 2,048 keys, 32 heads over 8, 568
-// CTAs of 18.5 key tiles on average): 252 us, 1.21 PFLOP/s of f16 products.  A
-// key tile takes 5,200 clocks where its MMAs alone take 4,104: what is left is
-// the wait of a chain for its own softmax (2,100 to 2,400 clocks from S to P)
-// and for the slots; 17,000 clocks a CTA go to its start and its output.
-// Measured and not taken: six slots of 16 KiB (286 us), PV begun at the first
-// half of P (no gain on either), 8 or 32 query rows in flight a warp (258 and
-// 259 us).
+// A CTA with one tile gives its chain both S buffers and the other's query
+// pieces as two further slots, so that QK(j + 1) runs under softmax(j): 2,900
+// clocks a key tile instead of 4,600.  The chain's arithmetic is the same.
+//
+// Measured (8 rows of 512 queries behind 2,048 keys, 32 heads over 8, 568 CTAs
+// of 18.5 key tiles on average): 237 us, 1.29 PFLOP/s of f16 products.  With two
+// tiles a key tile takes 5,200 clocks where its MMAs alone take 4,104: what is
+// left is a chain's wait for its own softmax (2,100 to 2,400 clocks from S to
+// P) and for the slots.  A CTA spends 14,000 clocks on its start, 5,000 on its
+// output and 7,000 pass before the next one runs; the rest is the last round.
+// Measured and not taken: six slots of 16 KiB (286 us against 257 at the time),
+// PV begun at the first half of P (no gain), 8 or 32 query rows in flight a
+// warp (258 and 259 us against 252).
 #include "pkv_elem.h"
 #include "pkv_internal.h"
 #include "pkv_softmax_tc.h"
