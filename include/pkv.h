@@ -137,8 +137,8 @@ PKV_API pkv_pool *pkv_pool_new(int32_t n_blocks, int32_t n_layers, int32_t kv_di
  * reads that row's keys once for several queries.  Attention and append calls
  * on this pool cannot be captured into a CUDA graph (PKV_ERR_ARG).
  *
- * k_pool_dev / v_pool_dev (16-byte aligned) and k_scale_dev / v_scale_dev:
- * caller-owned device buffers, all four or none (the library then allocates
+ * k_pool_dev / v_pool_dev and k_scale_dev / v_scale_dev: caller-owned device
+ * buffers, 16-byte aligned, all four or none (the library then allocates
  * them).  n_kv_heads * head_dim a multiple of 4, head_dim <= 256.  flags: 0 or
  * PKV_POOL_HOST_ONLY.  NULL on failure. */
 PKV_API pkv_pool *pkv_pool_new_q8(int32_t n_blocks, int32_t n_layers, int32_t n_kv_heads, int32_t head_dim,

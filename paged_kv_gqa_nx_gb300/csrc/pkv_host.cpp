@@ -1716,8 +1716,8 @@ pkv_pool *pkv_pool_new_q8(int32_t n_blocks, int32_t n_layers, int32_t n_kv_heads
         if (!(flags & PKV_POOL_HOST_ONLY)) {
             const int n = (k_pool_dev ? 1 : 0) + (v_pool_dev ? 1 : 0) + (k_scale_dev ? 1 : 0) + (v_scale_dev ? 1 : 0);
             if (n != 0 && n != 4) return fail(PKV_ERR_ARG, "pass both pool buffers and both scale buffers, or none");
-            if (!aligned4(k_scale_dev) || !aligned4(v_scale_dev))
-                return fail(PKV_ERR_ARG, "scale buffers must be 4-byte aligned");
+            if (!aligned16(k_scale_dev) || !aligned16(v_scale_dev))  // block copies move four scales at once
+                return fail(PKV_ERR_ARG, "scale buffers must be 16-byte aligned");
         }
         const Q8Spec spec{n_kv_heads, head_dim, k_scale_dev, v_scale_dev};
         p = make_pool(n_blocks, n_layers, static_cast<int32_t>(kv_dim), block_size, k_pool_dev, v_pool_dev, max_seqs,

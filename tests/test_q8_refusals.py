@@ -65,6 +65,15 @@ def test_q8_pool_refuses(args):
     assert pkv.pkv_last_error()
 
 
+@pytest.mark.parametrize("which", ["k_scale", "v_scale"])
+def test_q8_pool_refuses_scales_off_16_byte_boundaries(which):
+    # a copy of a block moves its scales four at a time
+    a = dict(k_pool=4096, v_pool=4096, k_scale=4096, v_scale=4096)
+    a[which] += 4
+    assert not pkv.pkv_pool_new_q8(4, 2, 2, 16, 4, max_seqs=2, max_blocks_per_seq=4, **a)
+    assert "16-byte" in pkv.pkv_last_error()
+
+
 @pytest.fixture
 def host_pool():
     p = pkv.pkv_pool_new_q8(8, 2, 2, 16, 4, max_seqs=3, max_blocks_per_seq=4, flags=pkv.PKV_POOL_HOST_ONLY)
