@@ -27,11 +27,13 @@ __device__ __forceinline__ float pow2f(int e) {  // 2^e, e in [-126, 127]
 }
 
 // The block of position pos, or -1 (and the error flag) where the page index
-// or the block id is out of range.
+// or the block id is out of range.  (Page table and scales are read through L2:
+// a decode launch starts while the append before it still writes them, so they
+// are not constant for its life, and a line of the SM's L1 may be older.)
 __device__ __forceinline__ int block_of(const PagedAddr &a, int slot, int pos, int32_t *err) {
     const int bi = a.bs_shift >= 0 ? (pos >> a.bs_shift) : (pos / a.bs);
     int blk = -1;
-    if (bi < a.max_blocks) blk = __ldg(a.pt + static_cast<size_t>(slot) * a.max_blocks + bi);
+    if (bi < a.max_blocks) blk = __ldcg(a.pt + static_cast<size_t>(slot) * a.max_blocks + bi);
     if (static_cast<unsigned>(blk) >= static_cast<unsigned>(a.n_blocks)) {
         flag_error(err, 1);
         return -1;
@@ -125,13 +127,13 @@ __global__ void __launch_bounds__(128) decode_q8_generic_kernel(Q8Args a, Q8Addr
         const size_t o = static_cast<size_t>(blk) * q.a.block_stride + q.a.layer_off +
                          static_cast<size_t>(block_off(q.a, j)) * q.a.kv_dim + static_cast<size_t>(kvh) * hd;
         const uint8_t *kr = static_cast<const uint8_t *>(q.a.k) + o, *vr = static_cast<const uint8_t *>(q.a.v) + o;
-        const float ks = __ldg(q.ks + blk * q.scale_stride + kvh), vs = __ldg(q.vs + blk * q.scale_stride + kvh);
+        const float ks = __ldcg(q.ks + blk * q.scale_stride + kvh), vs = __ldcg(q.vs + blk * q.scale_stride + kvh);
         float kx[kGDims], vx[kGDims];
 #pragma unroll
         for (int i = 0; i < kGDims; ++i) {
             const int d = lane + 32 * i;
-            kx[i] = d < hd ? static_cast<float>(static_cast<int>(kr[d]) - 128) : 0.f;
-            vx[i] = d < hd ? static_cast<float>(static_cast<int>(vr[d]) - 128) : 0.f;
+            kx[i] = d < hd ? static_cast<float>(static_cast<int>(__ldcg(kr + d)) - 128) : 0.f;
+            vx[i] = d < hd ? static_cast<float>(static_cast<int>(__ldcg(vr + d)) - 128) : 0.f;
         }
 #pragma unroll
         for (int g = 0; g < kGHeads; ++g) {
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(32 * kW, NB <= 2 ? 3 : 2)
         return kl < my_n && pos < kend && (!kTma || lane < 2) ? block_of(q.a, u.slot, pos, a.err) : -1;
     };
     auto scales_of = [&](int blk) {
-        return blk >= 0 ? make_float2(__ldg(q.ks + blk * q.scale_stride + kvh), __ldg(q.vs + blk * q.scale_stride + kvh))
+        return blk >= 0 ? make_float2(__ldcg(q.ks + blk * q.scale_stride + kvh), __ldcg(q.vs + blk * q.scale_stride + kvh))
                         : make_float2(0.f, 0.f);
     };
     auto load_tile = [&](int kl, int st, int blk) {
