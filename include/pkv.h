@@ -256,6 +256,9 @@ PKV_API int32_t pkv_seq_page_table(const pkv_seq *seq, int32_t *out, int32_t cap
 /* Pool slot of the sequence's page-table row on the device (0..max_seqs-1), or -1. */
 PKV_API int32_t pkv_seq_slot(const pkv_seq *seq);
 
+/* Values in a K or V row of the sequence's pool; -1 for NULL. */
+PKV_API int32_t pkv_seq_kv_dim(const pkv_seq *seq);
+
 /* Make positions [len, len+n) writable, once per step before layer 0
  * ("nx_f32_attn_paged.nx source", caller contract; "nx_f32_llama_v4b.nx
  * source", Stack section).  Shared blocks among those the rows fall in are

@@ -100,6 +100,7 @@ _SIGS = {
     "pkv_seq_len": (_i32, [_vp]),
     "pkv_seq_page_table": (_i32, [_vp, _pi32, _i32]),
     "pkv_seq_slot": (_i32, [_vp]),
+    "pkv_seq_kv_dim": (_i32, [_vp]),
     "pkv_ensure_append": (_int, [_vp, _i32]),
     "pkv_ensure_append_batch": (_int, [_vp, _i32, _pi32]),
     "pkv_advance": (_int, [_vp, _i32]),
@@ -198,6 +199,29 @@ def _rows(t, name, rows, width=None):
 
 def _total(arr, n):
     return arr[0] if n == 1 else sum(arr[:n])
+
+
+def _same_device(*tensors):
+    """Of a call that runs on the current device."""
+    import torch
+    try:
+        d = {t.get_device() for t in tensors}
+    except AttributeError:
+        raise TypeError("rows must be CUDA tensors") from None
+    if len(d) != 1 or (-1 not in d and torch.cuda.current_device() not in d):
+        raise TypeError("the tensors must be on the current device")
+
+
+def _pages(seqs, arr, m, n, K, V):
+    """K and V of a packed append or read: addresses, strides, element type."""
+    if n != m:
+        raise TypeError("start and n need an entry for each of the %d sequences" % m)
+    total, width = _total(arr, n) if n else 0, _lib.pkv_seq_kv_dim(seqs[0]) if m else -1
+    k, ks, t, w = _rows(K, "K", total, width if width > 0 else None)
+    v, vs, tv, wv = _rows(V, "V", total, w)
+    if t != tv:
+        raise TypeError("K and V must have one element type")
+    return k, ks, v, vs, t
 
 
 def _host(a, name="array"):
@@ -340,6 +364,10 @@ def pkv_seq_slot(seq):
     return _lib.pkv_seq_slot(seq)
 
 
+def pkv_seq_kv_dim(seq):
+    return _lib.pkv_seq_kv_dim(seq)
+
+
 def pkv_seq_page_table(seq):
     """The page table as a list of block ids."""
     n = _lib.pkv_seq_page_table(seq, None, 0)
@@ -421,6 +449,7 @@ def pkv_attn_packed(Q, K, V, lens, n_heads, n_kv_heads, head_dim, causal, scale,
     arr = _i32_array(lens)
     n = len(lens)
     total = _total(arr, n)
+    _same_device(Q, K, V, out)
     q, qs, t, _ = _rows(Q, "Q", total, n_heads * head_dim)
     k, ks, tk, _ = _rows(K, "K", total, n_kv_heads * head_dim)
     v, vs, tv, _ = _rows(V, "V", total, n_kv_heads * head_dim)
@@ -434,24 +463,18 @@ def pkv_attn_packed(Q, K, V, lens, n_heads, n_kv_heads, head_dim, causal, scale,
 def pkv_append_packed(seqs, n, layer, K, V):
     """K, V: [rows, kv_dim] float32, bfloat16 or float16 CUDA tensors with contiguous rows (any
     row stride), the batch's rows in order."""
-    arr = _i32_array(n)
-    total = _total(arr, len(n))
-    k, ks, t, w = _rows(K, "K", total)
-    v, vs, tv, wv = _rows(V, "V", total)
-    if t != tv or w != wv:
-        raise TypeError("K and V must have one element type and width")
-    return _lib.pkv_append_packed(_seq_array(seqs), len(seqs), arr, layer, k, ks, v, vs, t)
+    arr, m = _i32_array(n), len(seqs)
+    k, ks, v, vs, t = _pages(seqs, arr, m, len(n), K, V)
+    return _lib.pkv_append_packed(_seq_array(seqs), m, arr, layer, k, ks, v, vs, t)
 
 
 def pkv_read_packed(seqs, start, n, layer, K, V):
     """Rows start[r] .. start[r] + n[r] - 1 of each sequence into K, V (as for pkv_append_packed)."""
-    arr = _i32_array(n)
-    total = _total(arr, len(n))
-    k, ks, t, w = _rows(K, "K", total)
-    v, vs, tv, wv = _rows(V, "V", total)
-    if t != tv or w != wv:
-        raise TypeError("K and V must have one element type and width")
-    return _lib.pkv_read_packed(_seq_array(seqs), len(seqs), _i32_array(start), arr, layer, k, ks, v, vs, t)
+    arr, m = _i32_array(n), len(seqs)
+    if len(start) != m:
+        raise TypeError("start and n need an entry for each of the %d sequences" % m)
+    k, ks, v, vs, t = _pages(seqs, arr, m, len(n), K, V)
+    return _lib.pkv_read_packed(_seq_array(seqs), m, _i32_array(start), arr, layer, k, ks, v, vs, t)
 
 
 def pkv_sync_error(pool):

@@ -23,10 +23,10 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <exception>
 #include <functional>
 #include <list>
 #include <mutex>
-#include <new>
 #include <string>
 #include <unordered_map>
 #include <vector>
@@ -256,7 +256,7 @@ template <class F>
 int guarded(F &&f) {
     try {
         return f();
-    } catch (const std::bad_alloc &) {
+    } catch (const std::exception &) {  // bad_alloc, or length_error of a size no vector has
         return fail(PKV_ERR_ARG, "out of host memory");
     }
 }
@@ -1933,6 +1933,7 @@ int pkv_seq_truncate_batch(pkv_seq *const *seqs, int32_t M, const int32_t *new_l
 }
 
 int32_t pkv_seq_len(const pkv_seq *s) { return s ? s->len : -1; }
+int32_t pkv_seq_kv_dim(const pkv_seq *seq) { return seq && seq->pool ? seq->pool->kv_dim : -1; }
 int32_t pkv_seq_slot(const pkv_seq *s) { return s ? s->slot : -1; }
 
 int32_t pkv_seq_page_table(const pkv_seq *s, int32_t *out, int32_t cap) {

@@ -5,6 +5,7 @@ import math
 
 import numpy as np
 import pytest
+import torch
 
 import oracle
 import paged_kv_gqa_nx_gb300 as pkv
@@ -117,6 +118,60 @@ def test_packed_pages_refuse(host_pool, read):
     if read:
         assert call(start=None) == pkv.PKV_ERR_BAD_DIM
     assert call() == pkv.PKV_ERR_ARG and "host-only" in pkv.pkv_last_error()
+
+
+class Rows:
+    """A stand-in for packed rows on a GPU."""
+
+    def __init__(self, n, w, device=0, stride=None, dtype=torch.bfloat16):
+        self.shape, self.dtype, self.is_cuda, self.device, self.s = (n, w), dtype, True, device, stride or w
+
+    def stride(self):
+        return self.s, 1
+
+    def data_ptr(self):
+        return 4096
+
+    def get_device(self):
+        return self.device
+
+
+def test_packed_attention_wants_the_current_device(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(pkv, "_lib", type("Lib", (), {"pkv_attn_packed": staticmethod(lambda *a: 0)}))
+
+    def call(*dev, lens=(2, 3)):
+        q, k, v, o = (Rows(5, 64 if i in (0, 3) else 32, d) for i, d in enumerate(dev))
+        return pkv.pkv_attn_packed(q, k, v, lens, 4, 2, 16, 1, 0.25, o)
+
+    assert call(0, 0, 0, 0) == 0
+    for dev in [(1, 1, 1, 1), (1, 0, 0, 0), (0, 0, 1, 0), (0, 0, 0, 1)]:
+        with pytest.raises(TypeError, match="current device"):
+            call(*dev)
+    with pytest.raises(TypeError, match="rows"):
+        call(0, 0, 0, 0, lens=(2, 4))
+
+
+def test_packed_pages_want_counts_and_widths_that_fit(host_pool):
+    s = pkv.pkv_seq_new(host_pool, 16)
+    assert pkv.pkv_seq_kv_dim(s) == 32 and pkv.pkv_seq_kv_dim(None) == -1
+    ok = Rows(4, 32)
+    assert pkv.pkv_append_packed([s], [2], 0, ok, ok) == pkv.PKV_ERR_ARG and "host-only" in pkv.pkv_last_error()
+    assert pkv.pkv_read_packed([s], [0], [2], 0, ok, ok) == pkv.PKV_ERR_ARG
+    assert pkv.pkv_append_packed([None], [2], 0, ok, ok) == pkv.PKV_ERR_SEQ
+    for args in [([s], [2, 2]), ([s, s], [2])]:
+        with pytest.raises(TypeError, match="entry"):
+            pkv.pkv_append_packed(*args, 0, ok, ok)
+        with pytest.raises(TypeError, match="entry"):
+            pkv.pkv_read_packed(args[0], [0] * len(args[0]), args[1], 0, ok, ok)
+    with pytest.raises(TypeError, match="entry"):
+        pkv.pkv_read_packed([s], [0, 0], [2], 0, ok, ok)
+    narrow = Rows(4, 16, stride=64)             # columns of a wider tensor, but too few of them
+    for k, v in [(narrow, narrow), (ok, narrow), (narrow, ok)]:
+        with pytest.raises(TypeError, match="wide"):
+            pkv.pkv_append_packed([s], [2], 0, k, v)
+    with pytest.raises(TypeError, match="element type"):
+        pkv.pkv_append_packed([s], [2], 0, ok, Rows(4, 32, dtype=torch.float16))
 
 
 @pytest.mark.parametrize("m,e", [
