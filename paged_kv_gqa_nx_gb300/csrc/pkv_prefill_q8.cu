@@ -194,11 +194,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                 const uint64_t dK = desc_sw128(smem_u32(ring + sl * kSlot));
                 if (elect_lane()) {
 #pragma unroll
-                    for (int k = 0; k < kHD / 16; ++k) {
-                        const uint64_t o = ((k >> 2) * kBlock + (k & 3) * 32u) >> 4;
-                        mma_f16(tS, dQ0 + o, dK + o, idesc, k > 0);
-                        mma_f16(tS, dQ1 + o, dK + o, idesc, 1);
-                        if (k == kHD / 16 - 2 && pass) mbar_arrive(smem_u32(&bar_p[c ^ 1]));
+                    for (int k = 0; k < 2 * (kHD / 16); ++k) {  // the small pieces first: fewer additions to a large sum
+                        const uint64_t o = (((k >> 2) & 1) * kBlock + (k & 3) * 32u) >> 4;
+                        mma_f16(tS, (k < kHD / 16 ? dQ1 : dQ0) + o, dK + o, idesc, k > 0);
+                        if (k == 2 * (kHD / 16) - 3 && pass) mbar_arrive(smem_u32(&bar_p[c ^ 1]));
                     }
                     mma_commit(smem_u32(&bar_s[b]));
                     mma_commit(smem_u32(&bar_free[sl]));
