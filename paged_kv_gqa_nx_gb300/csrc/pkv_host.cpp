@@ -1220,7 +1220,7 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
     // few descriptors of an 8-bit pool's append and decode travel with the
     // launches; the append stores them for the tensor-core launches behind it
     InlineBlob<kInlineLarge> inl;
-    const bool inlined = p->q8 && rope_base == 0.0 && blob.b.size() <= sizeof inl.b;
+    const bool inlined = p->q8 && blob.b.size() <= sizeof inl.b;
     cudaError_t e = cudaSuccess;
     if (!inlined) e = upload_blob(p);
     else std::memcpy(inl.b, blob.b.data(), blob.b.size());
@@ -1273,8 +1273,13 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
         if (pr.rope_base > 0.0) {
             e = p->krot.ensure(static_cast<size_t>(T) * kv_dim * sizeof(float), st, p->device);
             if (e != cudaSuccess) return cuda_fail(e, "rotated-key buffer");
-            const RopeArgs ra{pr.Q, Kd, pr.Q_rot, static_cast<float *>(p->krot.p), dptr<RowDesc>(p, rows_off), M,
-                              static_cast<int32_t>(T), q_dim, kv_dim, head_dim, rope_base};
+            RopeArgs ra{pr.Q, Kd, pr.Q_rot, static_cast<float *>(p->krot.p), dptr<RowDesc>(p, rows_off), M,
+                        static_cast<int32_t>(T), q_dim, kv_dim, head_dim, rope_base};
+            if (inlined) {
+                ra.rows = blob_off<RowDesc>(rows_off);
+                ra.blob = &inl;
+                ra.blob_n = blob.b.size();
+            }
             e = launch(PKV_KERNEL_APPEND, st, [&] { return launch_rope_rows(ra, st); });
             if (e != cudaSuccess) return cuda_fail(e, "rotation kernel");
             Kd = ra.K_rot;

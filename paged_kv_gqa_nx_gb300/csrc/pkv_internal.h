@@ -179,6 +179,8 @@ struct RopeArgs {
     const RowDesc *rows;       // past_len, n_q, q_row0
     int32_t n_rows, n_tok, q_dim, kv_dim, hd;
     double base;
+    const InlineBlob<kInlineLarge> *blob = nullptr;  // rows: an offset into it
+    size_t blob_n = 0;
 };
 
 // Packed prompt attention: sequence s holds tokens start[s] .. start[s + 1) of

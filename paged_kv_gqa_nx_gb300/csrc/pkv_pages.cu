@@ -558,35 +558,48 @@ __global__ void __launch_bounds__(256) read_pages_q8_kernel(PagesArgs p, Q8Addr 
 
 // ------------------------------------------------------------------- rope ----
 
-// One warp per token: lane l turns the pairs (i, i + hd/2), i = l, l + 32, ...
-// of every query and key head by pos * base^(-2i/hd), with the arithmetic of
-// the append kernel's rotation (angle, cosine and sine in double precision,
-// the products and sums each rounded to f32).
-__global__ void __launch_bounds__(256) rope_rows_kernel(RopeArgs p) {
-    const int t = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (t >= p.n_tok) return;
-    int lo = 0, hi = p.n_rows - 1;  // the batch row of token t
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.rows[mid].q_row0 <= t) lo = mid;
-        else hi = mid - 1;
-    }
-    const int pos = p.rows[lo].past_len + (t - p.rows[lo].q_row0);
-    const int half = p.hd >> 1, nq = p.q_dim / p.hd, nk = p.kv_dim / p.hd;
-    const double lb = log(p.base);
-    for (int i = lane; i < half; i += 32) {
-        double sd, cd;
-        sincos(static_cast<double>(pos) * exp(-2.0 * i / p.hd * lb), &sd, &cd);
-        const float c = static_cast<float>(cd), sn = static_cast<float>(sd);
-        for (int h = 0; h < nq + nk; ++h) {
-            const bool is_k = h >= nq;
-            const size_t o = is_k ? static_cast<size_t>(t) * p.kv_dim + static_cast<size_t>(h - nq) * p.hd
-                                  : static_cast<size_t>(t) * p.q_dim + static_cast<size_t>(h) * p.hd;
-            const float *src = (is_k ? p.K : p.Q) + o;
-            float *dst = (is_k ? p.K_rot : p.Q_rot) + o;
-            const float x0 = src[i], x1 = src[i + half];
-            dst[i] = __fsub_rn(__fmul_rn(x0, c), __fmul_rn(x1, sn));
-            dst[i + half] = __fadd_rn(__fmul_rn(x0, sn), __fmul_rn(x1, c));
+// The pairs (i, i + hd/2) of every query and key head of a token turned by pos *
+// base^(-2i/hd), with the arithmetic of the append kernel's rotation (angle,
+// cosine and sine in double precision, the products and sums each rounded to
+// f32).  A CTA takes tokens blockIdx.x, + gridDim.x, ...: thread i < hd/2 keeps
+// its frequency and makes the token's i'th cosine and sine, then all turn the
+// heads' pairs.  Bound by the double-precision cosines where tokens are many
+// (hd/2 a token), by latency where they are few.
+constexpr int kRopeThreads = 256;
+template <class B>
+__global__ void __launch_bounds__(kRopeThreads) rope_rows_kernel(RopeArgs p, const __grid_constant__ B blob) {
+    __shared__ float2 turn[kMaxHeadDim / 2];
+    const RowDesc *rows = blob_at(p.rows, blob);
+    const int half = p.hd >> 1, tid = threadIdx.x;
+    const int n_pairs = (p.q_dim + p.kv_dim) / p.hd * half, nq = p.q_dim / p.hd * half;
+    const double freq = tid < half ? exp(-2.0 * tid / p.hd * log(p.base)) : 0.0;
+    for (int t = blockIdx.x; t < p.n_tok; t += gridDim.x) {
+        int lo = 0, hi = p.n_rows - 1;  // the batch row of token t
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (rows[mid].q_row0 <= t) lo = mid;
+            else hi = mid - 1;
+        }
+        const int pos = rows[lo].past_len + (t - rows[lo].q_row0);
+        __syncthreads();  // the token before this one is done with its turns
+        if (tid < half) {
+            double sd, cd;
+            sincos(static_cast<double>(pos) * freq, &sd, &cd);
+            turn[tid] = make_float2(static_cast<float>(cd), static_cast<float>(sd));
+        }
+        __syncthreads();
+        const float *Q = p.Q + static_cast<size_t>(t) * p.q_dim, *K = p.K + static_cast<size_t>(t) * p.kv_dim;
+        float *Qr = p.Q_rot + static_cast<size_t>(t) * p.q_dim, *Kr = p.K_rot + static_cast<size_t>(t) * p.kv_dim;
+#pragma unroll 4
+        for (int x = tid; x < n_pairs; x += kRopeThreads) {
+            const bool is_k = x >= nq;
+            const int y = is_k ? x - nq : x, h = y / half, i = y - h * half, o = h * p.hd + i;
+            const float *src = is_k ? K : Q;
+            float *dst = is_k ? Kr : Qr;
+            const float x0 = __ldg(src + o), x1 = __ldg(src + o + half);
+            const float2 r = turn[i];
+            dst[o] = __fsub_rn(__fmul_rn(x0, r.x), __fmul_rn(x1, r.y));
+            dst[o + half] = __fadd_rn(__fmul_rn(x0, r.y), __fmul_rn(x1, r.x));
         }
     }
 }
@@ -723,8 +736,10 @@ cudaError_t launch_read_pages_q8(const PagesArgs &p, const Q8Addr &q, cudaStream
     }
 }
 cudaError_t launch_rope_rows(const RopeArgs &p, cudaStream_t s) {
-    if (p.n_tok <= 0) return cudaErrorInvalidValue;
-    rope_rows_kernel<<<(p.n_tok + 7) / 8, 256, 0, s>>>(p);
+    if (p.n_tok <= 0 || p.hd > kMaxHeadDim) return cudaErrorInvalidValue;
+    // eight blocks a SM, so that many tokens share a block's frequencies
+    const unsigned grid = static_cast<unsigned>(std::min(p.n_tok, 8 * 152));
+    with_blob(p.blob, p.blob_n, [&](const auto &b) { rope_rows_kernel<<<grid, kRopeThreads, 0, s>>>(p, b); });
     return cudaGetLastError();
 }
 
