@@ -746,7 +746,7 @@ void place_pairs(const std::vector<std::array<PrefillTile, 2>> &pairs, const std
         }
 }
 
-// qblock: queries per decode unit (1 but on 8-bit pools); S: keys per split-K decode unit; prefill_split: keys per split of the
+// q8: an 8-bit pool's call; qblock: queries per decode unit (1 but there); S: keys per split-K decode unit; prefill_split: keys per split of the
 // tensor-core prefill rows (0: kPrefillSplitFactor * S); prefix_split: keys
 // per split of the shared-prefix pass (0: S); allow_tc false: every row to the
 // split-K decode kernels; n_kv, n_sm: kv heads and the device's SMs, for the
@@ -754,8 +754,8 @@ void place_pairs(const std::vector<std::array<PrefillTile, 2>> &pairs, const std
 void build_work(std::vector<RowDesc> &rows, int causal, int32_t S, int32_t head_dim,
                 int32_t group, WorkList &w, const std::vector<Cascade> &cas = {},
                 int32_t prefix_split = 0, int32_t prefill_split = 0, bool allow_tc = true,
-                int32_t n_kv = 0, int32_t n_sm = 0, int32_t qblock = 1, const ShortRows &short_rows = {},
-                const TileCost &cost_of = {}) {
+                int32_t n_kv = 0, int32_t n_sm = 0, bool q8 = false, int32_t qblock = 1,
+                const ShortRows &short_rows = {}) {
     std::vector<UnitDesc> tail;
     w.units.clear();
     w.tiles.clear();
@@ -766,7 +766,7 @@ void build_work(std::vector<RowDesc> &rows, int causal, int32_t S, int32_t head_
     const int32_t n_real = static_cast<int32_t>(rows.size());
     const std::vector<char> member =
         add_cascades(rows, cas, S, prefix_split > 0 ? prefix_split : S, group, w, tail);
-    const bool tc_shape = allow_tc && prefill_shape(head_dim, group);
+    const bool tc_shape = allow_tc && (q8 ? prefill_shape_q8(head_dim, group) : prefill_shape(head_dim, group));
     const int32_t TQ = tc_shape ? 128 / group : 0;
     const int32_t Sp = prefill_split > 0 ? prefill_split : S * kPrefillSplitFactor;
     std::vector<std::array<PrefillTile, 2>> pairs;
@@ -837,7 +837,7 @@ void build_work(std::vector<RowDesc> &rows, int causal, int32_t S, int32_t head_
             }
         }
     }
-    place_pairs(pairs, len0, len1, g_prefill_pairing.load(), n_kv, n_sm, cost_of, w.tiles);
+    place_pairs(pairs, len0, len1, g_prefill_pairing.load(), n_kv, n_sm, q8 ? kTileCostQ8 : TileCost{}, w.tiles);
     w.units.insert(w.units.end(), tail.begin(), tail.end());
     // longest units first, so that the grid's last CTAs are its shortest and
     // the launch drains quickly (the order changes no result)
@@ -1085,12 +1085,13 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
     if (p->q8) short_rows = {8 * S, std::min<int32_t>(65536, 2 * S)};
     const int32_t group = attend ? n_heads / n_kv_heads : 0;
     std::vector<Cascade> cas;
-    if (attend && g_cascade.load() != 0 && prefill_shape(head_dim, group))
+    const bool tc_shape = attend && (p->q8 ? prefill_shape_q8(head_dim, group) : prefill_shape(head_dim, group));
+    if (tc_shape && g_cascade.load() != 0)
         cas = find_cascades(seqs, M, n_q, p->bs);
     const int32_t Sp = cas.empty() ? 0 : prefix_split_keys(cas, group, n_kv_heads, p->n_sm);
     if (attend)
         build_work(rows, causal, S_dec, head_dim, group, w, cas, Sp, S * kPrefillSplitFactor, true, n_kv_heads,
-                   p->n_sm, p->q8 ? q8_query_block(head_dim, group) : 1, short_rows, p->q8 ? kTileCostQ8 : TileCost{});
+                   p->n_sm, p->q8, p->q8 ? q8_query_block(head_dim, group) : 1, short_rows);
     // the decode kernels that take the append themselves: the f32 kernel for
     // groups 1, 2, 4 and the narrow-pool kernel for its shapes (head_dim 128)
     const bool fuse_shape = head_dim == 128 && !p->q8 &&
@@ -1104,7 +1105,7 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
         int64_t pairs = 0, ppairs = 0;
         for (int32_t r = 0; r < M; ++r) {
             const RowDesc &rd = rows[r];
-            if (rd.n_q < kPrefillMinQueries || !prefill_shape(head_dim, group)) continue;
+            if (rd.n_q < kPrefillMinQueries || !tc_shape) continue;
             const int64_t n = rd.n_q, b = rd.past_len;
             pairs += causal ? n * b + n * (n + 1) / 2 : n * (b + n);
         }
@@ -1363,7 +1364,7 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
         pa.img_slot = dptr<int32_t>(p, slot_off);
         pa.lo_zero = p->narrow() ? 1 : 0;
         e = launch(PKV_KERNEL_PREFILL, st, [&] {
-            return p->q8 ? launch_prefill_q8(pa, st) : launch_prefill_paged(pa, addr, st);
+            return p->q8 ? launch_prefill_q8(pa, head_dim, st) : launch_prefill_paged(pa, addr, st);
         });
         if (e != cudaSuccess) return cuda_fail(e, "prefill kernel");
     }
@@ -1377,7 +1378,7 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
         pa.img_slot = dptr<int32_t>(p, slot_off);
         pa.lo_zero = p->narrow() ? 1 : 0;
         e = launch(PKV_KERNEL_PREFILL, st, [&] {
-            return p->q8 ? launch_prefill_q8(pa, st) : launch_prefill_paged(pa, addr, st);
+            return p->q8 ? launch_prefill_q8(pa, head_dim, st) : launch_prefill_paged(pa, addr, st);
         });
         if (e != cudaSuccess) return cuda_fail(e, "shared-prefix kernel");
     }
@@ -1463,7 +1464,7 @@ int run_layer_host(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const fl
     auto usable = [&](const void *q) { return q && (vec ? aligned16(q) : aligned4(q)); };
     const int32_t group = n_heads / n_kv_heads;
     bool prefill = false, cascade = false;
-    if (prefill_shape(head_dim, group)) {
+    if (p->q8 ? prefill_shape_q8(head_dim, group) : prefill_shape(head_dim, group)) {
         for (int32_t r = 0; r < M && !prefill; ++r) prefill = n_q[r] >= kPrefillMinQueries;
         if (!prefill && g_cascade.load() != 0) cascade = !find_cascades(seqs, M, n_q, p->bs).empty();
     }
@@ -1773,7 +1774,7 @@ int pkv_pool_set_image_cache(pkv_pool *p, int64_t max_bytes) {
     DevGuard dg(p->device);
     ImageCache &ic = p->icache;
     // one slot: a 64-key tile's images for every kv head of head_dim 128
-    const size_t slot_bytes = static_cast<size_t>(ceil_div(p->kv_dim, 128)) * kImageBytes;
+    const size_t slot_bytes = static_cast<size_t>(p->q8 ? p->n_kv : ceil_div(p->kv_dim, 128)) * kImageBytes;
     const int64_t n = max_bytes / static_cast<int64_t>(slot_bytes);
     ic.reset(0);
     ic.buf.release(p->stream);

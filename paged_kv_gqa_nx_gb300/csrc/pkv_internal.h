@@ -389,7 +389,7 @@ cudaError_t make_q8_maps(Q8Maps *m, const Q8Addr &addr, int n_layers, bool *usab
 cudaError_t launch_split_q8(const SplitArgs &a, const Q8Addr &addr, cudaStream_t s);
 // Tensor-core attention over an 8-bit pool's images (pkv_prefill_q8.cu): the
 // contract of launch_prefill_paged with one-piece images.
-cudaError_t launch_prefill_q8(const PrefillArgs &a, cudaStream_t s);
+cudaError_t launch_prefill_q8(const PrefillArgs &a, int hd, cudaStream_t s);
 int q8_query_block(int head_dim, int group);
 // Packed prompt attention (pkv_packed.cu); sequences sorted longest first.
 cudaError_t launch_packed(const PackedArgs &a, const int32_t *start, const int32_t *len, int32_t n_seqs,
@@ -402,6 +402,12 @@ constexpr int kPrefillMinQueries = 32;
 constexpr int kPrefillSplitFactor = 16;
 __host__ __device__ constexpr bool prefill_shape(int head_dim, int group) {
     return head_dim == 128 && (group == 1 || group == 2 || group == 4 || group == 8);
+}
+
+// Likewise over an 8-bit pool: any group whose heads fit a tile several tokens
+// deep, any head width of whole 16s.
+__host__ __device__ constexpr bool prefill_shape_q8(int head_dim, int group) {
+    return head_dim % 16 == 0 && head_dim <= 128 && group <= 64;
 }
 
 // Host-core helpers for entry points defined in other translation units

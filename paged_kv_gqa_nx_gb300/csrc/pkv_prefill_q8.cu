@@ -47,7 +47,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kHD = 128, kKeys = 128;
+constexpr int kMaxHD = 128, kKeys = 128;
 constexpr int kThreads = 384;
 constexpr int kWarpMma0 = 8, kWarpLoad = 9, kWarpSpare = 11;  // warp 10: chain 1's MMAs
 // registers per thread: at launch, then of warps 8-11 and of the compute warps
@@ -80,9 +80,11 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &p0, uint32_t 
     p1 = *reinterpret_cast<const uint32_t *>(&h1);
 }
 
-template <int G>
-__global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) {
-    constexpr int TQ = 128 / G;  // tokens per tile
+// Gc, Hc: the group and the head width where compiled in (0: taken from g_arg, hd_arg)
+template <int Gc, int Hc>
+__global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a, int g_arg, int hd_arg) {
+    const int G = Gc ? Gc : g_arg, kHD = Hc ? Hc : hd_arg;
+    const int TQ = 128 / G;  // tokens per tile; rows past TQ * G stay empty
     extern __shared__ __align__(1024) unsigned char smraw[];
     unsigned char *sm = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smraw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -164,12 +166,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                 if (i >= ns && !wait_w(&bar_free[sl], rph(i) - 1)) break;
                 if (elect_lane()) {
                     const uint32_t dst = smem_u32(ring + sl * kSlot), bar = smem_u32(&bar_full[sl]);
-                    mbar_expect_tx(bar, kSlot);
+                    const uint32_t n_kb = kHD > 64 ? 2 : 1, v_bytes = kHD * 128;
+                    mbar_expect_tx(bar, (i & 1) ? 2 * v_bytes : n_kb * kBlock);
                     if (i & 1) {  // V^T: a k-block of 64 keys each
-                        bulk_g2s(dst, ia + 2 * kImagePlane, kBlock, bar);
-                        bulk_g2s(dst + kBlock, ib + 2 * kImagePlane, kBlock, bar);
+                        bulk_g2s(dst, ia + 2 * kImagePlane, v_bytes, bar);
+                        bulk_g2s(dst + kBlock, ib + 2 * kImagePlane, v_bytes, bar);
                     } else {      // K: of each k-block of 64 dims, 64 keys each
-                        for (int kb = 0; kb < 2; ++kb) {
+                        for (uint32_t kb = 0; kb < n_kb; ++kb) {
                             bulk_g2s(dst + kb * kBlock, ia + kb * (kBlock / 2), kBlock / 2, bar);
                             bulk_g2s(dst + kb * kBlock + kBlock / 2, ib + kb * (kBlock / 2), kBlock / 2, bar);
                         }
@@ -185,6 +188,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
             const int c = warp == kWarpMma0 ? 0 : 1, n = c ? n1 : n0;
             const uint32_t tO = tbase + 128 * c;
             constexpr uint32_t idesc = idesc_f16(128, 128);
+            const uint32_t idesc_v = idesc_f16(128, kHD);
+            const int nk = kHD / 16;
             const uint64_t dQ0 = desc_sw128(smem_u32(sm + 2 * c * kQPiece)), dQ1 = desc_sw128(smem_u32(sm + (2 * c + 1) * kQPiece));
             // S_c = Q_c K_j^T, then the barriers; on the way the turn passes
             // (b: the S buffer, a chain's own or a lone chain's of the tile)
@@ -194,10 +199,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                 const uint64_t dK = desc_sw128(smem_u32(ring + sl * kSlot));
                 if (elect_lane()) {
 #pragma unroll
-                    for (int k = 0; k < 2 * (kHD / 16); ++k) {  // the small pieces first: fewer additions to a large sum
-                        const uint64_t o = (((k >> 2) & 1) * kBlock + (k & 3) * 32u) >> 4;
-                        mma_f16(tS, (k < kHD / 16 ? dQ1 : dQ0) + o, dK + o, idesc, k > 0);
-                        if (k == 2 * (kHD / 16) - 3 && pass) mbar_arrive(smem_u32(&bar_p[c ^ 1]));
+                    for (int k = 0; k < 2 * (kMaxHD / 16); ++k) {  // the small pieces first: fewer additions to a large sum
+                        const int x = k & 7;
+                        const uint64_t o = ((x >> 2) * kBlock + (x & 3) * 32u) >> 4;
+                        if (x < nk) mma_f16(tS, (k < 8 ? dQ1 : dQ0) + o, dK + o, idesc, k > 0);
+                        if (k == 8 + max(0, nk - 3) && pass) mbar_arrive(smem_u32(&bar_p[c ^ 1]));
                     }
                     mma_commit(smem_u32(&bar_s[b]));
                     mma_commit(smem_u32(&bar_free[sl]));
@@ -213,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k) {
                         const uint64_t o = ((k >> 2) * kBlock + (k & 3) * 32u) >> 4;
-                        mma_f16_ts(tO, tS + 8 * k, dV + o, idesc, j > 0 || k > 0);
-                        mma_f16_ts(tO, tS + 64 + 8 * k, dV + o, idesc, 1);
+                        mma_f16_ts(tO, tS + 8 * k, dV + o, idesc_v, j > 0 || k > 0);
+                        mma_f16_ts(tO, tS + 64 + 8 * k, dV + o, idesc_v, 1);
                     }
                     mma_commit(smem_u32(&bar_free[sv]));
                     if (lone) mma_commit(smem_u32(&bar_v));
@@ -278,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
         setmaxnreg_inc<kComputeRegs>();
         const int c = warp >> 2, n = c ? n1 : n0, m = tid & 127;
         const int tq = m / G, g = m - tq * G, qi = (c ? t1.q0 : t0.q0) + tq;
-        const bool valid = qi < rd.n_q;
+        const bool valid = tq < TQ && qi < rd.n_q;
         const int klim = min(valid ? (a.causal ? total_k - rd.n_q + qi + 1 : total_k) : 1, c ? kend1 : kend0);
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t tO = tbase + lanes + 128 * c;
@@ -298,7 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
                         const int row = w0 + r0 + r, t = q0 + row / G;
-                        q[r] = t < rd.n_q ? __ldg(reinterpret_cast<const float4 *>(
+                        q[r] = row / G < TQ && t < rd.n_q && 4 * lane < kHD
+                                   ? __ldg(reinterpret_cast<const float4 *>(
                                                 qb + static_cast<size_t>(t) * (a.n_heads * kHD) + (row % G) * kHD))
                                           : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
@@ -315,8 +322,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                         split2(x.x * up, x.y * up, c0.x, c1.x);
                         split2(x.z * up, x.w * up, c0.y, c1.y);
                         const uint32_t off = sw128_chunk(w0 + r0 + r, (lane >> 1) & 7);
-                        *reinterpret_cast<uint2 *>(d + off) = c0;
-                        *reinterpret_cast<uint2 *>(d + off + kQPiece) = c1;
+                        if (4 * lane < kHD) {
+                            *reinterpret_cast<uint2 *>(d + off) = c0;
+                            *reinterpret_cast<uint2 *>(d + off + kQPiece) = c1;
+                        }
                     }
                 }
             }
@@ -453,7 +462,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                 const float scl = direct ? 1.f / l_run : 1.f;
                 const bool vec = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;  // whole 32-byte sectors
 #pragma unroll
-                for (int i = 0; i < kHD / 32; ++i) {
+                for (int i = 0; i < kMaxHD / 32; ++i) {
+                    if (32 * i >= kHD) continue;
+                    const int nd = min(32, kHD - 32 * i);  // 16 or 32 dims
                     float v[32];
                     tmem_ld32(tO + 32 * i, v);
 #pragma unroll
@@ -463,14 +474,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
                     } else if (vec) {
 #pragma unroll
                         for (int k = 0; k < 32; k += 8)
-                            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + 32 * i + k),
+                            if (k < nd) asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + 32 * i + k),
                                          "f"(v[k]), "f"(v[k + 1]), "f"(v[k + 2]), "f"(v[k + 3]), "f"(v[k + 4]), "f"(v[k + 5]),
                                          "f"(v[k + 6]), "f"(v[k + 7])
                                          : "memory");
                     } else {
 #pragma unroll
                         for (int k = 0; k < 32; k += 4)
-                            *reinterpret_cast<float4 *>(dst + 32 * i + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                            if (k < nd) *reinterpret_cast<float4 *>(dst + 32 * i + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
                     }
                     __syncwarp();  // TMEM loads are the warp's
                 }
@@ -486,36 +497,38 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a) 
     if (warp == 0) tmem_dealloc(tbase, kTmemCols);
 }
 
-template <int G>
-cudaError_t launch_g(const PrefillArgs &a, cudaStream_t s) {
+template <int G, int HD>
+cudaError_t launch_g(const PrefillArgs &a, int hd, cudaStream_t s) {
     static PerDeviceOnce configured;  // the attributes are per function and device
     const cudaError_t ce = configured.run([&]() -> cudaError_t {
         // setmaxnreg.inc waits for registers of the launch's own: launch only
         // if the kernel starts with what the split was sized for
         cudaFuncAttributes fa{};
-        cudaError_t e = cudaFuncGetAttributes(&fa, prefill_q8_kernel<G>);
+        cudaError_t e = cudaFuncGetAttributes(&fa, prefill_q8_kernel<G, HD>);
         if (e != cudaSuccess) return e;
         if (fa.numRegs < kLaunchRegs || fa.maxThreadsPerBlock < kThreads) return cudaErrorInvalidConfiguration;
-        return cudaFuncSetAttribute(prefill_q8_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(prefill_q8_kernel<G, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(kSmem));
     });
     if (ce != cudaSuccess) return ce;
     if (a.n_tiles <= 0 || (a.n_tiles & 1) || !a.img || !a.img_tile0 || !a.img_slot) return cudaErrorInvalidValue;
     const long long grid = static_cast<long long>(a.n_tiles / 2) * a.n_kv;
     if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    prefill_q8_kernel<G><<<static_cast<unsigned>(grid), kThreads, kSmem, s>>>(a);
+    prefill_q8_kernel<G, HD><<<static_cast<unsigned>(grid), kThreads, kSmem, s>>>(a, a.group, hd);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_prefill_q8(const PrefillArgs &a, cudaStream_t s) {
+cudaError_t launch_prefill_q8(const PrefillArgs &a, int hd, cudaStream_t s) {
+    if (!prefill_shape_q8(hd, a.group)) return cudaErrorInvalidValue;
+    if (hd != kMaxHD) return launch_g<0, 0>(a, hd, s);
     switch (a.group) {
-        case 1: return launch_g<1>(a, s);
-        case 2: return launch_g<2>(a, s);
-        case 4: return launch_g<4>(a, s);
-        case 8: return launch_g<8>(a, s);
-        default: return cudaErrorInvalidValue;
+        case 1: return launch_g<1, kMaxHD>(a, hd, s);
+        case 2: return launch_g<2, kMaxHD>(a, hd, s);
+        case 4: return launch_g<4, kMaxHD>(a, hd, s);
+        case 8: return launch_g<8, kMaxHD>(a, hd, s);
+        default: return launch_g<0, kMaxHD>(a, hd, s);
     }
 }
 

@@ -758,7 +758,6 @@ cudaError_t launch_decode_with(const Q8Args &a, const Q8Addr &q, const B &blob, 
 // as on the other narrow pools.  K goes straight to its image; V's bytes turn
 // through shared memory.
 
-constexpr int kHDI = 128;
 constexpr int kVPitch = 132;  // bytes from key to key: four keys on, another bank
 
 // four bytes as (u - 128) times the pair of powers of two s2, in f16 (exact)
@@ -785,7 +784,7 @@ __global__ void __launch_bounds__(256) split_q8_kernel(SplitArgs p, Q8Addr q) {
             const int blk = block_of(q.a, rd.slot, pos, p.err);
             if (blk >= 0) {
                 o = static_cast<int64_t>(blk) * q.a.block_stride + q.a.layer_off +
-                    static_cast<int64_t>(block_off(q.a, pos)) * q.a.kv_dim + static_cast<int64_t>(kvh) * kHDI;
+                    static_cast<int64_t>(block_off(q.a, pos)) * q.a.kv_dim + static_cast<int64_t>(kvh) * q.hd;
                 ks = __ldg(q.ks + blk * q.scale_stride + kvh);
                 vsc = __ldg(q.vs + blk * q.scale_stride + kvh);
             }
@@ -814,6 +813,7 @@ __global__ void __launch_bounds__(256) split_q8_kernel(SplitArgs p, Q8Addr q) {
     // V's bytes (and zeros, u = 128, past the row's keys)
     for (int i = tid; i < kKeyTile * 8; i += 256) {
         const int key = i >> 3, ch = i & 7;
+        if (16 * ch >= q.hd) continue;
         const int64_t o = row_of[key];
         uint4 u = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
         if (o >= 0) u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(q.a.v) + o + 16 * ch));
@@ -825,12 +825,12 @@ __global__ void __launch_bounds__(256) split_q8_kernel(SplitArgs p, Q8Addr q) {
     // K: k-block c >> 9 (64 dims), key (c >> 3) & 63, swizzled chunk c & 7
 #pragma unroll
     for (int i = 0; i < static_cast<int>(kImagePlane / 16) / 256; ++i) {
-        const int c = tid + 256 * i, r = (c >> 3) & 63;
+        const int c = tid + 256 * i, r = (c >> 3) & 63, dim = (c >> 9) * 64 + ((c & 7) ^ (r & 7)) * 8;
+        if (dim >= q.hd) continue;
         const int64_t o = row_of[r];
         uint2 u = make_uint2(0x80808080u, 0x80808080u);
         if (o >= 0)
-            u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(q.a.k) + o + (c >> 9) * 64 +
-                                                      ((c & 7) ^ (r & 7)) * 8));
+            u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(q.a.k) + o + dim));
         const __half2 f = __half2half2(kf[r]);
         const uint2 a = widen4(u.x, f), b = widen4(u.y, f);
         *reinterpret_cast<uint4 *>(img + c * 16) = make_uint4(a.x, a.y, b.x, b.y);
@@ -838,7 +838,9 @@ __global__ void __launch_bounds__(256) split_q8_kernel(SplitArgs p, Q8Addr q) {
     // V^T: four dims d .. d + 3 of eight keys k0 .. at a time: a word of each key,
     // each dim's eight values together one chunk of the image (dim row, chunk
     // k0 / 8 at its swizzled place)
+    if (tid < 2) reinterpret_cast<int32_t *>(img + kImageExpOff)[tid] = ex[tid];
     const int d = 4 * (tid >> 3), k0 = 8 * (tid & 7);
+    if (d >= q.hd) return;
     uint32_t w[8];
     __half2 f[4];
 #pragma unroll
@@ -860,7 +862,6 @@ __global__ void __launch_bounds__(256) split_q8_kernel(SplitArgs p, Q8Addr q) {
         *reinterpret_cast<uint4 *>(img + 2 * kImagePlane + (dd * 8 + ((k0 >> 3) ^ (dd & 7))) * 16) =
             make_uint4(y[0], y[1], y[2], y[3]);
     }
-    if (tid < 2) reinterpret_cast<int32_t *>(img + kImageExpOff)[tid] = ex[tid];
 }
 
 }  // namespace
@@ -902,7 +903,7 @@ cudaError_t launch_decode_q8(const Q8Args &a, const Q8Addr &q, cudaStream_t s) {
 }
 
 cudaError_t launch_split_q8(const SplitArgs &a, const Q8Addr &q, cudaStream_t s) {
-    if (q.hd != kHDI) return cudaErrorInvalidValue;
+    if (q.hd % 16 != 0 || q.hd > 128) return cudaErrorInvalidValue;
     const long long grid = static_cast<long long>(a.n_items) * a.n_kv;
     if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     split_q8_kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(a, q);

@@ -405,6 +405,21 @@ def test_prefill_chunks(G, bs, causal):
     assert w["prefill_tiles"] > 0
 
 
+@pytest.mark.parametrize("G,KV,hd", [(4, 2, 64), (1, 5, 80), (4, 3, 96), (2, 1, 16), (3, 2, 32), (16, 1, 48), (7, 1, 112),
+                                     (5, 2, 128), (12, 1, 128), (64, 1, 64), (1, 1, 128)])
+@pytest.mark.parametrize("causal", [1, 0])
+def test_prefill_head_widths_and_groups(G, KV, hd, causal):
+    """Tiles whose rows are not all used, operands narrower than the images; lone and paired tiles, splits."""
+    old = pkv.pkv_get_split_keys()
+    try:
+        w = attend_case(G * KV, KV, hd, 16, [0, 100, 7, 700, 63], [40, 64, 1, 150, 33], seed=G, causal=causal)
+        assert w["prefill_tiles"] > 0
+        pkv.check(pkv.pkv_set_split_keys(32))
+        attend_case(G * KV, KV, hd, 5, [600, 0], [35, 45], seed=G + 1, causal=causal)
+    finally:
+        pkv.check(pkv.pkv_set_split_keys(old))
+
+
 @pytest.mark.parametrize("scales", [(8, 0), (0, 12), (12, 12)])
 def test_prefill_blocks_of_very_different_scales(scales):
     attend_case(8, 2, 128, 4, [300, 90], [70, 33], seed=3, scales=scales)
@@ -483,10 +498,11 @@ def test_layers_host_buffers_and_rope():
     attend_case(4, 2, 64, 5, [100, 7], [1, 3], rope=500.0, seed=4)
 
 
-def test_shared_prefix_and_image_cache():
+@pytest.mark.parametrize("H,KV,hd", [(8, 2, 128), (8, 2, 64), (15, 3, 96)])
+def test_shared_prefix_and_image_cache(H, KV, hd):
     """Forks of one long prefix take the shared-prefix pass; its result agrees with each row's own, with and without
     cached images."""
-    H, KV, hd, bs, n = 8, 2, 128, 16, 20
+    bs, n = 16, 20
     pool = Q8Pool(600, 1, KV, hd, bs, max_seqs=n + 2)
     try:
         a = pool.seq(2600)
