@@ -127,14 +127,16 @@ PKV_API pkv_pool *pkv_pool_new(int32_t n_blocks, int32_t n_layers, int32_t kv_di
  * within one step after any growths.  A value that is not finite makes the
  * scale NaN: the block's values of that head then read as NaN until the block
  * is written from its first row again (an attention output that depends on
- * them is NaN; in a call with n_q >= 32 rows of one sequence, other queries of
- * the same sequence may be too).
+ * them is NaN; where a row's queries share tensor-core tiles, see below, other
+ * queries of the same sequence may be too).
  *
  * Every pool call works on it: pkv_attn_batch and its forms (n_kv_heads and
  * head_dim as given here, PKV_ERR_BAD_DIM otherwise), pkv_append_layer,
  * fork / copy-on-append (scales included), truncate, the image cache, shared
- * prefixes.  There is no fused append.  A call with 2 to 31 queries of a row
- * reads that row's keys once for several queries.  Attention and append calls
+ * prefixes.  There is no fused append.  A row of n_q >= 32 queries, or of n_q *
+ * head_dim * (n_heads / n_kv_heads) >= 12288, takes tensor-core tiles where
+ * head_dim is a multiple of 16 up to 128 and a kv head serves at most 64 heads;
+ * a shorter one reads its keys once for several queries.  Attention and append calls
  * on this pool cannot be captured into a CUDA graph (PKV_ERR_ARG).
  *
  * k_pool_dev / v_pool_dev and k_scale_dev / v_scale_dev: caller-owned device

@@ -646,6 +646,19 @@ std::vector<char> add_cascades(std::vector<RowDesc> &rows, const std::vector<Cas
     return member;
 }
 
+// Queries from which a row takes the tensor-core tiles.  On an 8-bit pool a
+// decode unit takes up to 16 (query, head) pairs, so a row reads its keys n_q *
+// group / 16 times there; on the tiles its images cost about two such reads and
+// a CTA a fixed 26,000 clocks.  Measured at 128-wide heads, decode / tiles, us:
+// 64 rows of 512 .. 4,096 keys in groups of 4, 12 queries 274 / 322, 20 446 /
+// 324; in groups of 8, 7 queries 354 / 329, 12 527 / 322; 8 rows of 20,000 in
+// groups of 8, 7 queries 434 / 513, 12 615 / 519; 64-wide, groups of 8, 12
+// queries 179 / 186 and 234 / 411, 31 queries 492 / 221 and 513 / 528.
+constexpr int32_t kPrefillMinQ8 = 96 * 128;  // n_q * group * head_dim
+int32_t prefill_min(bool q8, int32_t group, int32_t head_dim) {
+    return q8 ? std::max(2, std::min(kPrefillMinQueries, ceil_div(kPrefillMinQ8, group * head_dim))) : kPrefillMinQueries;
+}
+
 // Keys of one decode unit (the host's copy of the kernels' unit_range).
 int32_t unit_keys(const UnitDesc &u, const RowDesc &rd, int causal, int32_t S) {
     const int32_t total_k = rd.past_len + rd.n_q;
@@ -783,7 +796,7 @@ void build_work(std::vector<RowDesc> &rows, int causal, int32_t S, int32_t head_
         if (member[r]) continue;
         const RowDesc &rd = rows[r];
         const int32_t total_k = rd.past_len + rd.n_q;
-        if (tc_shape && rd.n_q >= kPrefillMinQueries) {
+        if (tc_shape && rd.n_q >= prefill_min(q8, group, head_dim)) {
             // query tiles latest first (part0 -1: one split, written directly)
             struct QTile {
                 int32_t q0, ns, part0;
@@ -1105,7 +1118,7 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
         int64_t pairs = 0, ppairs = 0;
         for (int32_t r = 0; r < M; ++r) {
             const RowDesc &rd = rows[r];
-            if (rd.n_q < kPrefillMinQueries || !tc_shape) continue;
+            if (rd.n_q < prefill_min(p->q8, group, head_dim) || !tc_shape) continue;
             const int64_t n = rd.n_q, b = rd.past_len;
             pairs += causal ? n * b + n * (n + 1) / 2 : n * (b + n);
         }
@@ -1465,7 +1478,7 @@ int run_layer_host(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const fl
     const int32_t group = n_heads / n_kv_heads;
     bool prefill = false, cascade = false;
     if (p->q8 ? prefill_shape_q8(head_dim, group) : prefill_shape(head_dim, group)) {
-        for (int32_t r = 0; r < M && !prefill; ++r) prefill = n_q[r] >= kPrefillMinQueries;
+        for (int32_t r = 0; r < M && !prefill; ++r) prefill = n_q[r] >= prefill_min(p->q8, group, head_dim);
         if (!prefill && g_cascade.load() != 0) cascade = !find_cascades(seqs, M, n_q, p->bs).empty();
     }
     float *Ov = prefill ? nullptr : static_cast<float *>(device_view(outh));

@@ -26,8 +26,6 @@ namespace {
 using f16 = __half;
 using namespace tc;
 
-__device__ __forceinline__ float widen(bf16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float widen(f16 x) { return __half2float(x); }
 __device__ __forceinline__ void narrow(bf16 *p, float x) { *p = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void narrow(f16 *p, float x) { *p = __float2half_rn(x); }
 
@@ -79,6 +77,15 @@ __device__ __forceinline__ int seq_of_tile(const PackedSeqs<N> &l, int t) {
 // that some row of the CTA does not see whole, the compute threads of one chain
 // replace values that are not finite by 0 and, where they found any, every
 // thread adds those products for the keys that its row does see.
+//
+// Measured: 16,384 tokens, causal, 32 heads over 8 of 128, f16: 1,356 us (1,622
+// TFLOP/s; 2,400 clocks a pair of tiles and key tile, of which the MMAs take
+// 2,048).  24 prompts of 16 .. 4,096, bf16: 84 us, 4.4 key tiles a piece, 3,000
+// clocks each and 5,000 to 6,000 a piece for its first scores and its output.
+// 64-wide heads, 16 prompts of 64 .. 1,024: 49 to 57 us, 2,600 clocks a key tile
+// (a third score buffer, with scores two steps ahead, gave 58).  Also not taken:
+// pieces of one tile (ragged 114: twice the reads of K and V), a part of the
+// exponentials on the FMA units (1,409 us and more on the long prompt).
 constexpr int kKeys = 128;  // keys per tile
 constexpr int kTcThreads = 384;
 constexpr int kWarpMma0 = 8, kWarpLoad = 9, kWarpSpare = 11;  // warp 10: chain 1's MMAs
@@ -652,96 +659,215 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // ---------------------------------------------------------------- general ----
 //
-// Any head width up to 256, any strides and alignment.  CTA = 128 threads = 32
-// queries of one head; four neighbouring threads share a query.  Keys go
-// through shared memory 32 at a time; thread t of a query scores keys t, t + 4,
-// ... and owns the output dims t, t + 4, ....  A key that a query does not see
-// is skipped, never multiplied by a zero probability, so infinities and NaN
-// there do not reach it.  Bound by the shared-memory reads of its products.
+// Any head width up to 256, any strides and alignment, any scale.  CTA = 4 warps
+// = 64 queries of one head, 16 a warp; keys go through shared memory 32 at a
+// time (rows padded with zeros to DP dims, and by 16 bytes, so that ldmatrix
+// meets no bank twice); both products on m16n8k16 MMAs:
+//
+//   S [16 x 32] = Q K^T          A, B by ldmatrix
+//   O [16 x DP] += P V           A from S's accumulators, B by transposed ldmatrix
+//
+// Scores are scaled in f32.  A key that a query does not see has probability 0;
+// as zero times an infinity is NaN, a tile that some row does not see whole is
+// looked over, and where it holds a value that is not finite its products are
+// made one by one, over the keys that the row sees.
+//
+// Measured (causal, 32 heads over 8, 24 prompts of 16 .. 4,096): 95 TFLOP/s at
+// 160-wide heads (3.65 ms; f32 products from shared memory took 67.7), 108 at
+// 256 (16 heads), 76 at 128 off 16-byte boundaries (element loads).  Bound by
+// the loads, which wait for the tile before them: two to five CTAs a SM overlap.
 
-constexpr int kGQ = 32, kGK = 32, kGOwn = kMaxHeadDim / 4;
+constexpr int kGQ = 64, kGK = 32;
 
-template <class T, int N>
+template <int DP>
+struct GenCfg {
+    static constexpr int kPitch = DP + 8;  // elements
+    static constexpr size_t kSmem = static_cast<size_t>(kGQ + 2 * kGK) * kPitch * 2 + kGQ * (kGK + 1) * sizeof(float);
+};
+
+template <class T>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same<T, bf16>::value)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool kTrans>
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const void *p) {
+    const uint32_t a = smem_u32(p);
+    if constexpr (kTrans)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(a)
+                     : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(a)
+                     : "memory");
+}
+// Rows 0 .. rows - 1 of hd elements into padded shared rows, zeros elsewhere;
+// whether a value was not finite (of this thread's).
+template <class T, int DP, bool kVec>
+__device__ __forceinline__ bool load_rows(unsigned short *dst, const T *src, int64_t stride, int rows, int n_rows, int hd) {
+    bool bad = false;
+    if constexpr (kVec) {
+        for (int i = threadIdx.x; i < n_rows * (DP / 8); i += 128) {
+            const int r = i / (DP / 8), c = i - r * (DP / 8);
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (r < rows && 8 * c < hd) x = __ldg(reinterpret_cast<const uint4 *>(src + r * stride + 8 * c));
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) bad = bad || not_finite<T>(w[k]) || not_finite<T>(w[k] >> 16);
+            *reinterpret_cast<uint4 *>(dst + r * GenCfg<DP>::kPitch + 8 * c) = x;
+        }
+    } else {
+        for (int i = threadIdx.x; i < n_rows * DP; i += 128) {
+            const int r = i / DP, d = i - r * DP;
+            unsigned short x = 0;
+            if (r < rows && d < hd) x = __ldg(reinterpret_cast<const unsigned short *>(src) + r * stride + d);
+            bad = bad || not_finite<T>(x);
+            dst[r * GenCfg<DP>::kPitch + d] = x;
+        }
+    }
+    return bad;
+}
+
+template <class T, int DP, bool kVec, int N>
 __global__ void __launch_bounds__(128) packed_general_kernel(const __grid_constant__ PackedArgs a,
                                                              const __grid_constant__ PackedSeqs<N> l) {
-    extern __shared__ __align__(16) float sm[];
-    const int hd = a.hd, pitch = hd + 1;
-    float *Qs = sm, *Ks = Qs + kGQ * pitch, *Vs = Ks + kGK * pitch, *Ps = Vs + kGK * pitch;  // Ps: [kGQ][kGK + 1]
-    const int h = blockIdx.x % a.n_heads, t = blockIdx.x / a.n_heads;
+    using C = GenCfg<DP>;
+    extern __shared__ __align__(1024) unsigned char smraw[];
+    unsigned short *Qs = reinterpret_cast<unsigned short *>(smraw), *Ks = Qs + kGQ * C::kPitch, *Vs = Ks + kGK * C::kPitch;
+    float *Ps = reinterpret_cast<float *>(Vs + kGK * C::kPitch);  // [kGQ][kGK + 1], of tiles made one by one
+    const int hd = a.hd, h = blockIdx.x % a.n_heads, t = blockIdx.x / a.n_heads;
     const int s = seq_of_tile(l, t);
     const int len = l.len[s];
-    const int n_tiles = l.tile0[s + 1] - l.tile0[s];
-    const int q0 = (n_tiles - 1 - (t - l.tile0[s])) * kGQ;  // the last queries, with the most keys, first
+    const int q0 = (l.tile0[s + 1] - l.tile0[s] - 1 - (t - l.tile0[s])) * kGQ;  // the last queries, with the most keys, first
     const int64_t row0 = l.start[s];
     const int kvh = h / (a.n_heads / a.n_kv);
-    const T *Q = static_cast<const T *>(a.Q) + row0 * a.q_stride + static_cast<int64_t>(h) * hd;
+    const T *Q = static_cast<const T *>(a.Q) + (row0 + q0) * a.q_stride + static_cast<int64_t>(h) * hd;
     const T *K = static_cast<const T *>(a.K) + row0 * a.k_stride + static_cast<int64_t>(kvh) * hd;
     const T *V = static_cast<const T *>(a.V) + row0 * a.v_stride + static_cast<int64_t>(kvh) * hd;
-    const int tid = threadIdx.x, qi = tid >> 2, part = tid & 3;
-    const bool valid = q0 + qi < len;
-    for (int i = tid; i < kGQ * hd; i += 128) {
-        const int r = i / hd, d = i - r * hd;
-        Qs[r * pitch + d] = q0 + r < len ? widen(Q[(q0 + r) * a.q_stride + d]) * a.scale_log2 : 0.f;
-    }
-    const int lim = !valid ? 0 : a.causal ? q0 + qi + 1 : len;             // keys this query sees
-    const int kend = a.causal ? min(len, q0 + kGQ) : len;                  // keys the tile sees
-    float m = -INFINITY, sum = 0.f, o[kGOwn];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, mi = lane >> 3, mr = lane & 7;
+    load_rows<T, DP, kVec>(Qs, Q, a.q_stride, min(kGQ, len - q0), kGQ, hd);
+    // rows g and g + 8 of the warp's sixteen: the keys that they see, running maximum and sum
+    int lim[2];
+    float m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < kGOwn; ++i) o[i] = 0.f;
+    for (int x = 0; x < 2; ++x) {
+        const int q = q0 + 16 * warp + g + 8 * x;
+        lim[x] = q >= len ? 0 : a.causal ? q + 1 : len;
+    }
+    float o[DP / 8][4];
+#pragma unroll
+    for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    const int kend = a.causal ? min(len, q0 + kGQ) : len;  // keys that the tile sees
+    const int whole = a.causal ? q0 + 1 : len;             // keys that all of its rows see
     for (int k0 = 0; k0 < kend; k0 += kGK) {
-        const int nk = min(kGK, kend - k0);
         __syncthreads();
-        for (int i = tid; i < nk * hd; i += 128) {
-            const int r = i / hd, d = i - r * hd;
-            Ks[r * pitch + d] = widen(K[(k0 + r) * a.k_stride + d]);
-            Vs[r * pitch + d] = widen(V[(k0 + r) * a.v_stride + d]);
-        }
-        __syncthreads();
-        const int see = min(nk, lim - k0);  // keys of the tile below the query's limit
-        float sc[kGK / 4];
-        float top = -INFINITY;
+        load_rows<T, DP, kVec>(Ks, K + k0 * a.k_stride, a.k_stride, min(kGK, len - k0), kGK, hd);
+        const bool odd = load_rows<T, DP, kVec>(Vs, V + k0 * a.v_stride, a.v_stride, min(kGK, len - k0), kGK, hd);
+        const bool single = __syncthreads_or(odd && k0 + kGK > whole);
+        float sc[kGK / 8][4];
 #pragma unroll
-        for (int j = 0; j < kGK / 4; ++j) {
-            const int k = part + 4 * j;
-            sc[j] = -INFINITY;
-            if (k < see) {
-                float x = 0.f;
-                for (int d = 0; d < hd; ++d) x = fmaf(Qs[qi * pitch + d], Ks[k * pitch + d], x);
-                sc[j] = x;
+        for (int i = 0; i < kGK / 8; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+#pragma unroll
+        for (int d = 0; d < DP; d += 16) {
+            uint32_t qa[4];  // rows mr (+ 8), dims d (+ 8)
+            ldsm4<false>(qa, Qs + (16 * warp + mr + 8 * (mi & 1)) * C::kPitch + d + 8 * (mi >> 1));
+#pragma unroll
+            for (int n = 0; n < kGK / 16; ++n) {
+                uint32_t kb[4];
+                ldsm4<false>(kb, Ks + (16 * n + mr + 8 * (mi >> 1)) * C::kPitch + d + 8 * (mi & 1));
+                mma16<T>(sc[2 * n], qa, kb[0], kb[1]);
+                mma16<T>(sc[2 * n + 1], qa, kb[2], kb[3]);
             }
-            top = fmaxf(top, sc[j]);
         }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float mn = fmaxf(m, top);
-        const float al = mn == m ? 1.f : exp2f(m - mn);
-        float ps = 0.f;
+        float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int j = 0; j < kGK / 4; ++j) {
-            const int k = part + 4 * j;
-            const float p = k < see ? exp2f(sc[j] - (mn == -INFINITY ? 0.f : mn)) : 0.f;
-            Ps[qi * (kGK + 1) + k] = p;
-            ps += p;
+        for (int i = 0; i < kGK / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = k0 + 8 * i + 2 * c + (e & 1);
+                sc[i][e] = key < lim[e >> 1] ? sc[i][e] * a.scale_log2 : -INFINITY;
+                top[e >> 1] = fmaxf(top[e >> 1], sc[i][e]);
+            }
+        uint32_t p[kGK / 16][4];  // as A: keys 16 n + (2c, 2c + 1) and + 8, rows g and g + 8
+        float al[2], ps[2] = {0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+            top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
+            const float mn = fmaxf(m[x], top[x]);
+            al[x] = mn == m[x] ? 1.f : ex2(m[x] - mn);
+            m[x] = mn;
         }
-        ps += __shfl_xor_sync(0xffffffffu, ps, 1);
-        ps += __shfl_xor_sync(0xffffffffu, ps, 2);
-        sum = fmaf(sum, al, ps);
-        m = mn;
-        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < kGOwn; ++i) o[i] *= al;
-        for (int k = 0; k < see; ++k) {
-            const float p = Ps[qi * (kGK + 1) + k];
+        for (int i = 0; i < kGK / 8; ++i) {
 #pragma unroll
-            for (int i = 0; i < kGOwn; ++i)
-                if (part + 4 * i < hd) o[i] = fmaf(p, Vs[k * pitch + part + 4 * i], o[i]);
+            for (int e = 0; e < 4; ++e) {
+                const float mn = m[e >> 1];
+                sc[i][e] = sc[i][e] == -INFINITY ? 0.f : ex2(sc[i][e] - (mn == -INFINITY ? 0.f : mn));
+                ps[e >> 1] += sc[i][e];
+            }
+            p[i >> 1][2 * (i & 1)] = pack2(T{}, sc[i][0], sc[i][1]);
+            p[i >> 1][2 * (i & 1) + 1] = pack2(T{}, sc[i][2], sc[i][3]);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) sum[x] = fmaf(sum[x], al[x], ps[x]);
+#pragma unroll
+        for (int i = 0; i < DP / 8; ++i) o[i][0] *= al[0], o[i][1] *= al[0], o[i][2] *= al[1], o[i][3] *= al[1];
+        if (!single) {
+#pragma unroll
+            for (int n = 0; n < kGK / 16; ++n)
+#pragma unroll
+                for (int d = 0; d < DP; d += 16) {
+                    uint32_t vb[4];
+                    ldsm4<true>(vb, Vs + (16 * n + mr + 8 * (mi & 1)) * C::kPitch + d + 8 * (mi >> 1));
+                    mma16<T>(o[d / 8], p[n], vb[0], vb[1]);
+                    mma16<T>(o[d / 8 + 1], p[n], vb[2], vb[3]);
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kGK / 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    Ps[(16 * warp + g + 8 * (e >> 1)) * (kGK + 1) + 8 * i + 2 * c + (e & 1)] =
+                        half_of(T{}, p[i >> 1][2 * (i & 1) + (e >> 1)], e & 1);
+            __syncwarp();
+#pragma unroll 1
+            for (int k = 0; k < kGK; ++k)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (k0 + k >= lim[x]) continue;
+                    const float pk = Ps[(16 * warp + g + 8 * x) * (kGK + 1) + k];
+#pragma unroll
+                    for (int i = 0; i < DP / 8; ++i) {
+                        const uint32_t v = *reinterpret_cast<const uint32_t *>(Vs + k * C::kPitch + 8 * i + 2 * c);
+                        o[i][2 * x] = fmaf(pk, half_of(T{}, v, 0), o[i][2 * x]);
+                        o[i][2 * x + 1] = fmaf(pk, half_of(T{}, v, 1), o[i][2 * x + 1]);
+                    }
+                }
         }
     }
-    if (!valid) return;
-    T *out = static_cast<T *>(a.out) + (row0 + q0 + qi) * a.o_stride + static_cast<int64_t>(h) * hd;
 #pragma unroll
-    for (int i = 0; i < kGOwn; ++i)
-        if (part + 4 * i < hd) narrow(out + part + 4 * i, o[i] / sum);
+    for (int x = 0; x < 2; ++x) {
+        sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
+        sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
+        const int q = q0 + 16 * warp + g + 8 * x;
+        if (q >= len) continue;
+        T *out = static_cast<T *>(a.out) + (row0 + q) * a.o_stride + static_cast<int64_t>(h) * hd;
+#pragma unroll
+        for (int i = 0; i < DP / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (8 * i + 2 * c + e < hd) narrow(out + 8 * i + 2 * c + e, o[i][2 * x + e] / sum[x]);
+    }
 }
 
 template <int N>
@@ -757,21 +883,19 @@ void fill_seqs(PackedSeqs<N> &l, const int32_t *start, const int32_t *len, int32
     l.tile0[n] = at;
 }
 
-template <class T, int N>
+template <class T, int DP, bool kVec, int N>
 cudaError_t launch_general_n(const PackedArgs &a, const int32_t *start, const int32_t *len, int32_t n, cudaStream_t s) {
     PackedSeqs<N> l;
     fill_seqs(l, start, len, n, kGQ);
-    const size_t smem = (static_cast<size_t>(kGQ + 2 * kGK) * (a.hd + 1) + kGQ * (kGK + 1)) * sizeof(float);
     static PerDeviceOnce configured;  // the attribute is per function and device
     const cudaError_t ce = configured.run([&]() -> cudaError_t {
-        return cudaFuncSetAttribute(packed_general_kernel<T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>((static_cast<size_t>(kGQ + 2 * kGK) * (kMaxHeadDim + 1) +
-                                                      kGQ * (kGK + 1)) * sizeof(float)));
+        return cudaFuncSetAttribute(packed_general_kernel<T, DP, kVec, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(GenCfg<DP>::kSmem));
     });
     if (ce != cudaSuccess) return ce;
     const long long grid = static_cast<long long>(l.tile0[n]) * a.n_heads;
     if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    packed_general_kernel<T, N><<<static_cast<unsigned>(grid), 128, smem, s>>>(a, l);
+    packed_general_kernel<T, DP, kVec, N><<<static_cast<unsigned>(grid), 128, GenCfg<DP>::kSmem, s>>>(a, l);
     return cudaGetLastError();
 }
 
@@ -843,10 +967,19 @@ cudaError_t launch_tc(const PackedArgs &a, const int32_t *start, const int32_t *
     return n <= 64 ? launch_tc_n<128, T, 64>(a, start, len, n, s) : launch_tc_n<128, T, kPackedSeqs>(a, start, len, n, s);
 }
 
+template <class T, int DP>
+cudaError_t launch_general_d(const PackedArgs &a, const int32_t *start, const int32_t *len, int32_t n, cudaStream_t s) {
+    auto ok = [](const void *p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0; };
+    if (a.hd % 8 == 0 && ok(a.Q, a.q_stride) && ok(a.K, a.k_stride) && ok(a.V, a.v_stride))
+        return launch_general_n<T, DP, true, kPackedSeqs>(a, start, len, n, s);
+    return launch_general_n<T, DP, false, kPackedSeqs>(a, start, len, n, s);
+}
 template <class T>
 cudaError_t launch_general(const PackedArgs &a, const int32_t *start, const int32_t *len, int32_t n, cudaStream_t s) {
-    if (n <= 64) return launch_general_n<T, 64>(a, start, len, n, s);
-    return launch_general_n<T, kPackedSeqs>(a, start, len, n, s);
+    if (a.hd <= 64) return launch_general_d<T, 64>(a, start, len, n, s);
+    if (a.hd <= 128) return launch_general_d<T, 128>(a, start, len, n, s);
+    if (a.hd <= 192) return launch_general_d<T, 192>(a, start, len, n, s);
+    return launch_general_d<T, 256>(a, start, len, n, s);
 }
 
 }  // namespace

@@ -91,7 +91,8 @@ __device__ __forceinline__ void join_records(const Q8Args &a, const Q8Unit &u, i
 // Any head width up to 256 and any group: CTA = 4 warps = one (unit, kv head,
 // chunk of up to 16 query heads); warp w takes the unit's keys w, w + 4, ...,
 // the lanes hold the dims d = lane, lane + 32, ....  Bound by the instructions
-// it issues (a shuffle sum per key and head).
+// it issues (a shuffle sum per key and head): 64 sequences of 512 .. 4,096 with
+// 32 heads of 160 over 8 in 1,320 us (0.2 TB/s).
 
 constexpr int kGW = 4, kGHeads = 16, kGDims = kMaxHeadDim / 32;
 
@@ -261,6 +262,13 @@ cudaError_t launch_generic(const Q8Args &a, const Q8Addr &q, const B &blob, cuda
 //
 // Shared memory rows keep their 16-byte chunks XOR-swizzled by the key, so
 // that the 8 rows of an ldmatrix fall in distinct bank groups.
+//
+// Measured (32 heads over 8 of 128, pages of 16, append included): 256
+// sequences of 128 .. 32,768 in 492 us (6.27 TB/s, 0.92 of the copy peak; the
+// loads alone take 473), 64 of 512 .. 4,096 in 47.6, one of 700 in 12.3; with
+// pages of 5 (cp.async instead of TMA) 63 against 59 us on a like batch.  Two
+// stages and four warps: three stages leave 2 CTAs a SM (585 us at 256
+// sequences against 486 at the time), 1, 2 and 6 warps were slower too.
 
 constexpr int kW = 4;            // warps per CTA
 constexpr int kT = 32;           // keys per tile
@@ -756,7 +764,8 @@ cudaError_t launch_decode_with(const Q8Args &a, const Q8Addr &q, const B &blob, 
 // is an f16 value, seven bits -- unless the key's scale 2^e lies more than 2^25
 // below the tile's, where its last bits are dropped -- so piece 1 is left out,
 // as on the other narrow pools.  K goes straight to its image; V's bytes turn
-// through shared memory.
+// through shared memory.  Bound by the images' writes: 25 us for 320 tiles of 8
+// heads of 128 (42 MB read, 84 MB written).
 
 constexpr int kVPitch = 132;  // bytes from key to key: four keys on, another bank
 
@@ -767,7 +776,9 @@ __device__ __forceinline__ uint2 widen4(uint32_t w, __half2 s2) {
     return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
+template <bool kFull>  // head width 128
 __global__ void __launch_bounds__(256) split_q8_kernel(SplitArgs p, Q8Addr q) {
+    const int hd = kFull ? 128 : q.hd;
     __shared__ __align__(16) uint8_t vs[kKeyTile * kVPitch];
     __shared__ int64_t row_of[kKeyTile];
     __shared__ __half kf[kKeyTile], vf[kKeyTile];  // each key's factor
@@ -784,7 +795,7 @@ __global__ void __launch_bounds__(256) split_q8_kernel(SplitArgs p, Q8Addr q) {
             const int blk = block_of(q.a, rd.slot, pos, p.err);
             if (blk >= 0) {
                 o = static_cast<int64_t>(blk) * q.a.block_stride + q.a.layer_off +
-                    static_cast<int64_t>(block_off(q.a, pos)) * q.a.kv_dim + static_cast<int64_t>(kvh) * q.hd;
+                    static_cast<int64_t>(block_off(q.a, pos)) * q.a.kv_dim + static_cast<int64_t>(kvh) * hd;
                 ks = __ldg(q.ks + blk * q.scale_stride + kvh);
                 vsc = __ldg(q.vs + blk * q.scale_stride + kvh);
             }
@@ -813,7 +824,7 @@ __global__ void __launch_bounds__(256) split_q8_kernel(SplitArgs p, Q8Addr q) {
     // V's bytes (and zeros, u = 128, past the row's keys)
     for (int i = tid; i < kKeyTile * 8; i += 256) {
         const int key = i >> 3, ch = i & 7;
-        if (16 * ch >= q.hd) continue;
+        if (16 * ch >= hd) continue;
         const int64_t o = row_of[key];
         uint4 u = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
         if (o >= 0) u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(q.a.v) + o + 16 * ch));
@@ -826,7 +837,7 @@ __global__ void __launch_bounds__(256) split_q8_kernel(SplitArgs p, Q8Addr q) {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(kImagePlane / 16) / 256; ++i) {
         const int c = tid + 256 * i, r = (c >> 3) & 63, dim = (c >> 9) * 64 + ((c & 7) ^ (r & 7)) * 8;
-        if (dim >= q.hd) continue;
+        if (dim >= hd) continue;
         const int64_t o = row_of[r];
         uint2 u = make_uint2(0x80808080u, 0x80808080u);
         if (o >= 0)
@@ -840,7 +851,7 @@ __global__ void __launch_bounds__(256) split_q8_kernel(SplitArgs p, Q8Addr q) {
     // k0 / 8 at its swizzled place)
     if (tid < 2) reinterpret_cast<int32_t *>(img + kImageExpOff)[tid] = ex[tid];
     const int d = 4 * (tid >> 3), k0 = 8 * (tid & 7);
-    if (d >= q.hd) return;
+    if (d >= hd) return;
     uint32_t w[8];
     __half2 f[4];
 #pragma unroll
@@ -906,7 +917,8 @@ cudaError_t launch_split_q8(const SplitArgs &a, const Q8Addr &q, cudaStream_t s)
     if (q.hd % 16 != 0 || q.hd > 128) return cudaErrorInvalidValue;
     const long long grid = static_cast<long long>(a.n_items) * a.n_kv;
     if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    split_q8_kernel<<<static_cast<unsigned>(grid), 256, 0, s>>>(a, q);
+    if (q.hd == 128) split_q8_kernel<true><<<static_cast<unsigned>(grid), 256, 0, s>>>(a, q);
+    else split_q8_kernel<false><<<static_cast<unsigned>(grid), 256, 0, s>>>(a, q);
     return cudaGetLastError();
 }
 

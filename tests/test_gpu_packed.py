@@ -105,6 +105,14 @@ def test_heads_and_widths(H, KV, hd):
     check(*make(lens, H, KV, hd, torch.float16, seed=hd + 1, fused=True), lens, H, KV, hd, causal=False)
 
 
+@pytest.mark.parametrize("hd", [20, 60, 131, 136, 160, 192, 200, 256])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+def test_widths_off_the_tensor_core_tiles(hd, causal, dtype):
+    lens = [1, 31, 32, 33, 64, 65, 129]
+    check(*make(lens, 4, 2, hd, dtype), lens, 4, 2, hd, causal)
+
+
 @pytest.mark.parametrize("hd,shift", [(128, 0), (128, 8), (128, 1), (64, 3), (40, 8)])
 def test_strides_and_alignment(hd, shift):
     """Columns of wider rows; shift 1 and 3 leave the 16-byte boundaries."""
@@ -123,7 +131,7 @@ def test_strides_and_alignment(hd, shift):
     assert bool((wide[:, :shift + 8] == 7).all()) and bool((wide[:, shift + 8 + qd:] == 7).all())
 
 
-@pytest.mark.parametrize("hd", [128, 64, 20])
+@pytest.mark.parametrize("hd", [128, 64, 20, 160, 256])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("causal", [True, False])
 def test_values_that_are_not_finite_stay_where_they_are_seen(hd, bad, causal):
