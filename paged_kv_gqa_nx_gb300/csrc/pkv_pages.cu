@@ -193,6 +193,11 @@ __device__ __forceinline__ uint32_t q8_word(float a, float b, float c, float d, 
     const uint32_t tc = __float_as_uint(fmaf(c, inv, kMagic)), td = __float_as_uint(fmaf(d, inv, kMagic));
     return __byte_perm(__byte_perm(ta, tb, 0x0040), __byte_perm(tc, td, 0x0040), 0x5410);
 }
+// Element j of a word as u - 128, exact: 2^23 + u is the float of bits 0x4b000000
+// | u (conversion instructions run at a quarter of the rate).
+__device__ __forceinline__ float q8_value(uint32_t w, int j) {
+    return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 | j)) - (8388608.f + 128.f);
+}
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 // ----------------------------------------------------------------- append ----
@@ -545,7 +550,7 @@ __global__ void __launch_bounds__(256) read_pages_q8_kernel(PagesArgs p, Q8Addr 
                 float x[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    x[j] = static_cast<float>(static_cast<int>((j < 4 ? u[k].x : u[k].y) >> (8 * (j & 3)) & 255u) - 128) * sc;
+                    x[j] = q8_value(j < 4 ? u[k].x : u[k].y, j & 3) * sc;
                 store8(dst + ws.row * stride + ws.c * 8, x);
             }
         }
