@@ -12,7 +12,7 @@
 // copies with a conversion, bound by HBM: every element is read and written
 // once, in 16-byte accesses of the packed side where its alignment allows.
 // Measured on an 8-bit pool (bf16 rows, 8 heads of 128): 130,000 rows appended
-// in 141 us and read back in 142 (5.6 TB/s; 0.83 of the copy peak), 9,000 rows in 10 each.
+// in 142 us and read back in 137 (5.7 TB/s; 0.84 of the copy peak), 9,000 rows in 10 each.
 //
 // Quantisation (8-bit pool).  With m the largest magnitude of the page's new
 // rows of a head, need(m) is the least e >= -126 with m <= 127 * 2^e; a page
