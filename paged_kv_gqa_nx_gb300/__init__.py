@@ -201,14 +201,22 @@ def _total(arr, n):
     return arr[0] if n == 1 else sum(arr[:n])
 
 
-def _same_device(*tensors):
+_current_device = None  # the CUDA runtime's current device, bound at the first use
+
+
+def _same_device(a, b, c, d):
     """Of a call that runs on the current device."""
-    import torch
+    global _current_device
+    if _current_device is None:
+        import torch
+        # (torch.cuda.current_device() costs 2 us a call around this one)
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     try:
-        d = {t.get_device() for t in tensors}
+        n = a.get_device()
+        same = n == b.get_device() == c.get_device() == d.get_device()
     except AttributeError:
         raise TypeError("rows must be CUDA tensors") from None
-    if len(d) != 1 or (-1 not in d and torch.cuda.current_device() not in d):
+    if not same or (n >= 0 and n != _current_device()):
         raise TypeError("the tensors must be on the current device")
 
 

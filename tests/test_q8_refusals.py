@@ -137,7 +137,7 @@ class Rows:
 
 
 def test_packed_attention_wants_the_current_device(monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(pkv, "_current_device", lambda: 0)
     monkeypatch.setattr(pkv, "_lib", type("Lib", (), {"pkv_attn_packed": staticmethod(lambda *a: 0)}))
 
     def call(*dev, lens=(2, 3)):
