@@ -34,6 +34,9 @@
 // left is a chain's wait for its own softmax (2,100 to 2,400 clocks from S to
 // P) and for the slots.  A CTA spends 14,000 clocks on its start, 5,000 on its
 // output and 7,000 pass before the next one runs; the rest is the last round.
+// The error is 5.9e-6 of the output's norm there (plain f32: 1.3e-6): the tensor
+// core rounds its f32 sums toward zero, ~300 additions an output.  Sums set aside
+// after every four key tiles give 1.5e-6, and 380 us, by way of L2.
 // Measured and not taken: six slots of 16 KiB (286 us against 257 at the time),
 // PV begun at the first half of P (no gain), 8 or 32 query rows in flight a
 // warp (258 and 259 us against 252).
