@@ -535,6 +535,58 @@ def test_shared_prefix_and_image_cache(H, KV, hd):
         pool.close()
 
 
+def test_pools_on_streams_of_their_own():
+    """Steps of two pools issued in turn on two streams return what each returns alone."""
+    H, KV, hd, bs, past = 8, 2, 128, 16, [700, 33, 5000, 64]
+    nqs = [[1, 1, 1, 1], [40, 1, 3, 33], [1, 20, 1, 1], [1, 1, 1, 1]]
+    kd, qd = KV * hd, H * hd
+
+    def step(pool, seqs, i, seed):
+        nq = nqs[i]
+        q, x, y = (randn(sum(nq), w, seed=seed + 7 * i + j) for j, w in enumerate((qd, kd, kd)))
+        torch.cuda.current_stream().synchronize()
+        pkv.check(pkv.pkv_ensure_append_batch(seqs, nq))
+        out = torch.empty(sum(nq), qd, device="cuda")
+        pkv.check(pkv.pkv_attn_batch(seqs, nq, q, x, y, H, KV, hd, 0, 1, hd ** -0.5, out))
+        pkv.check(pkv.pkv_advance_batch(seqs, nq))
+        return out, (q, x, y)
+
+    def start(seed):
+        pool = Q8Pool(500, 1, KV, hd, bs)
+        seqs = [pool.seq(p + 200) for p in past]
+        pool.append(seqs, randn(sum(past), kd, seed=seed), randn(sum(past), kd, seed=seed + 1), past)
+        torch.cuda.current_stream().synchronize()
+        return pool, seqs
+
+    alone, pools = [], []
+    try:
+        for k in range(2):
+            pool, seqs = start(50 * k)
+            pools.append(pool)
+            alone.append([step(pool, seqs, i, 50 * k)[0] for i in range(len(nqs))])
+            pool.ok()
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        torch.cuda.synchronize()
+        both = []
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                both.append(start(50 * k))
+                pools.append(both[-1][0])
+        outs = [[], []]
+        for i in range(len(nqs)):
+            for k, st in enumerate(streams):
+                with torch.cuda.stream(st):
+                    outs[k].append(step(*both[k], i, 50 * k))
+        torch.cuda.synchronize()
+        for k in range(2):
+            both[k][0].ok()
+            for i in range(len(nqs)):
+                assert torch.equal(alone[k][i], outs[k][i][0]), (k, i)
+    finally:
+        for p in pools:
+            p.close()
+
+
 def test_bad_pages_are_skipped():
     """An id outside the pool in the caller's page table cannot come from the host core; the kernels still check: rows
     past the table's end are refused before any launch."""
