@@ -764,7 +764,7 @@ cudaError_t launch_decode_with(const Q8Args &a, const Q8Addr &q, const B &blob, 
 // is an f16 value, seven bits -- unless the key's scale 2^e lies more than 2^25
 // below the tile's, where its last bits are dropped -- so piece 1 is left out,
 // as on the other narrow pools.  K goes straight to its image; V's bytes turn
-// through shared memory.  Bound by the images' writes: 25 us for 320 tiles of 8
+// through shared memory.  Bound by the images' writes: 24 us for 320 tiles of 8
 // heads of 128 (42 MB read, 84 MB written).
 
 constexpr int kVPitch = 132;  // bytes from key to key: four keys on, another bank
@@ -821,29 +821,38 @@ __global__ void __launch_bounds__(256) split_q8_kernel(SplitArgs p, Q8Addr q) {
         kf[tid] = __float2half_rn(ks * pow2f(ex[0]));
         vf[tid] = __float2half_rn(vsc * pow2f(ex[1]));
     }
-    // V's bytes (and zeros, u = 128, past the row's keys)
-    for (int i = tid; i < kKeyTile * 8; i += 256) {
-        const int key = i >> 3, ch = i & 7;
-        if (16 * ch >= hd) continue;
+    // V's and K's bytes (and zeros, u = 128, past the row's keys), all on the way at
+    // once.  K: k-block c >> 9 (64 dims), key (c >> 3) & 63, swizzled chunk c & 7
+    constexpr int kKC = static_cast<int>(kImagePlane / 16) / 256;
+    uint4 vw[2];
+    uint2 kw[kKC];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int key = (tid + 256 * i) >> 3, ch = tid & 7;
         const int64_t o = row_of[key];
-        uint4 u = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-        if (o >= 0) u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(q.a.v) + o + 16 * ch));
-        uint32_t *d = reinterpret_cast<uint32_t *>(vs + key * kVPitch + 16 * ch);
-        d[0] = u.x, d[1] = u.y, d[2] = u.z, d[3] = u.w;
+        vw[i] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+        if (o >= 0 && 16 * ch < hd) vw[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(q.a.v) + o + 16 * ch));
+    }
+#pragma unroll
+    for (int i = 0; i < kKC; ++i) {
+        const int c = tid + 256 * i, r = (c >> 3) & 63, dim = (c >> 9) * 64 + ((c & 7) ^ (r & 7)) * 8;
+        const int64_t o = row_of[r];
+        kw[i] = make_uint2(0x80808080u, 0x80808080u);
+        if (o >= 0 && dim < hd) kw[i] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(q.a.k) + o + dim));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t *d = reinterpret_cast<uint32_t *>(vs + ((tid + 256 * i) >> 3) * kVPitch + 16 * (tid & 7));
+        d[0] = vw[i].x, d[1] = vw[i].y, d[2] = vw[i].z, d[3] = vw[i].w;
     }
     __syncthreads();
     unsigned char *img = p.img + (static_cast<size_t>(t.slot) * p.n_kv + kvh) * kImageBytes;
-    // K: k-block c >> 9 (64 dims), key (c >> 3) & 63, swizzled chunk c & 7
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(kImagePlane / 16) / 256; ++i) {
+    for (int i = 0; i < kKC; ++i) {
         const int c = tid + 256 * i, r = (c >> 3) & 63, dim = (c >> 9) * 64 + ((c & 7) ^ (r & 7)) * 8;
         if (dim >= hd) continue;
-        const int64_t o = row_of[r];
-        uint2 u = make_uint2(0x80808080u, 0x80808080u);
-        if (o >= 0)
-            u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(q.a.k) + o + dim));
         const __half2 f = __half2half2(kf[r]);
-        const uint2 a = widen4(u.x, f), b = widen4(u.y, f);
+        const uint2 a = widen4(kw[i].x, f), b = widen4(kw[i].y, f);
         *reinterpret_cast<uint4 *>(img + c * 16) = make_uint4(a.x, a.y, b.x, b.y);
     }
     // V^T: four dims d .. d + 3 of eight keys k0 .. at a time: a word of each key,
