@@ -29,10 +29,10 @@
 // clocks a key tile instead of 4,600.  The chain's arithmetic is the same.
 //
 // Measured (8 rows of 512 queries behind 2,048 keys, 32 heads over 8, 568 CTAs
-// of 18.5 key tiles on average): 237 us, 1.29 PFLOP/s of f16 products.  With two
+// of 18.5 key tiles on average): 232 us, 1.32 PFLOP/s of f16 products.  With two
 // tiles a key tile takes 5,200 clocks where its MMAs alone take 4,104: what is
 // left is a chain's wait for its own softmax (2,100 to 2,400 clocks from S to
-// P) and for the slots.  A CTA spends 14,000 clocks on its start, 5,000 on its
+// P) and for the slots.  A CTA spends 12,000 clocks on its start, 5,000 on its
 // output and 7,000 pass before the next one runs; the rest is the last round.
 // The error is 5.9e-6 of the output's norm there (plain f32: 1.3e-6): the tensor
 // core rounds its f32 sums toward zero, ~300 additions an output.  Sums set aside
@@ -301,19 +301,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a, 
                 const int w0 = 32 * (warp & 3), q0 = c ? t1.q0 : t0.q0;
                 const float *qb = a.Q + static_cast<size_t>(rd.q_row0) * (a.n_heads * kHD) + static_cast<size_t>(kvh * G) * kHD + 4 * lane;
                 unsigned char *d = sm + 2 * c * kQPiece + (lane >> 4) * kBlock + (lane & 1) * 8;  // k-block lane / 16
-#pragma unroll 1
-                for (int r0 = 0; r0 < 32; r0 += 16) {
-                    float4 q[16];
+                auto load = [&](int r0, float4 (&q)[8]) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
+                    for (int r = 0; r < 8; ++r) {
                         const int row = w0 + r0 + r, t = q0 + row / G;
                         q[r] = row / G < TQ && t < rd.n_q && 4 * lane < kHD
                                    ? __ldg(reinterpret_cast<const float4 *>(
-                                                qb + static_cast<size_t>(t) * (a.n_heads * kHD) + (row % G) * kHD))
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                                         qb + static_cast<size_t>(t) * (a.n_heads * kHD) + (row % G) * kHD))
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
+                };
+                auto store = [&](int r0, const float4 (&q)[8]) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
+                    for (int r = 0; r < 8; ++r) {
                         float4 x = q[r];
                         x.x *= a.scale_log2, x.y *= a.scale_log2, x.z *= a.scale_log2, x.w *= a.scale_log2;
                         // largest magnitude as bits; a NaN or an infinity counts as none (its products are not finite)
@@ -330,6 +330,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a, 
                             *reinterpret_cast<uint2 *>(d + off + kQPiece) = c1;
                         }
                     }
+                };
+                float4 qa[8], qc[8];  // sixteen rows on the way
+                load(0, qa);
+                load(8, qc);
+#pragma unroll 1
+                for (int r0 = 0; r0 < 32; r0 += 16) {
+                    store(r0, qa);
+                    if (r0 == 0) load(16, qa);
+                    store(r0 + 8, qc);
+                    if (r0 == 0) load(24, qc);
                 }
             }
             fence_proxy_async();  // before the MMAs read them
