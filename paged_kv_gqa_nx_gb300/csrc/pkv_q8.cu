@@ -776,9 +776,10 @@ __device__ __forceinline__ uint2 widen4(uint32_t w, __half2 s2) {
     return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
-template <bool kFull>  // head width 128
+template <bool kWide>  // head width 128
 __global__ void __launch_bounds__(256) split_q8_kernel(SplitArgs p, Q8Addr q) {
-    const int hd = kFull ? 128 : q.hd;
+    static_assert(sizeof(kFull) == 4 && kFull == 0xffffffffu, "the shuffles below are whole warps'");
+    const int hd = kWide ? 128 : q.hd;
     __shared__ __align__(16) uint8_t vs[kKeyTile * kVPitch];
     __shared__ int64_t row_of[kKeyTile];
     __shared__ __half kf[kKeyTile], vf[kKeyTile];  // each key's factor
