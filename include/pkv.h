@@ -261,6 +261,10 @@ PKV_API int32_t pkv_seq_slot(const pkv_seq *seq);
 /* Values in a K or V row of the sequence's pool; -1 for NULL. */
 PKV_API int32_t pkv_seq_kv_dim(const pkv_seq *seq);
 
+/* CUDA device of the sequence's pool, whose kernels take every pointer of a
+ * call as an address there; -1 for NULL or a host-only pool. */
+PKV_API int32_t pkv_seq_device(const pkv_seq *seq);
+
 /* Make positions [len, len+n) writable, once per step before layer 0
  * ("nx_f32_attn_paged.nx source", caller contract; "nx_f32_llama_v4b.nx
  * source", Stack section).  Shared blocks among those the rows fall in are

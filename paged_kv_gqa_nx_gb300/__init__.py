@@ -101,6 +101,7 @@ _SIGS = {
     "pkv_seq_page_table": (_i32, [_vp, _pi32, _i32]),
     "pkv_seq_slot": (_i32, [_vp]),
     "pkv_seq_kv_dim": (_i32, [_vp]),
+    "pkv_seq_device": (_i32, [_vp]),
     "pkv_ensure_append": (_int, [_vp, _i32]),
     "pkv_ensure_append_batch": (_int, [_vp, _i32, _pi32]),
     "pkv_advance": (_int, [_vp, _i32]),
@@ -229,6 +230,9 @@ def _pages(seqs, arr, m, n, K, V):
     v, vs, tv, wv = _rows(V, "V", total, w)
     if t != tv:
         raise TypeError("K and V must have one element type")
+    dev = _lib.pkv_seq_device(seqs[0]) if m else -1
+    if K.get_device() != V.get_device() or (dev >= 0 and K.get_device() != dev):
+        raise TypeError("K and V must be on the pool's device")
     return k, ks, v, vs, t
 
 
@@ -374,6 +378,10 @@ def pkv_seq_slot(seq):
 
 def pkv_seq_kv_dim(seq):
     return _lib.pkv_seq_kv_dim(seq)
+
+
+def pkv_seq_device(seq):
+    return _lib.pkv_seq_device(seq)
 
 
 def pkv_seq_page_table(seq):

@@ -1953,6 +1953,9 @@ int pkv_seq_truncate_batch(pkv_seq *const *seqs, int32_t M, const int32_t *new_l
 
 int32_t pkv_seq_len(const pkv_seq *s) { return s ? s->len : -1; }
 int32_t pkv_seq_kv_dim(const pkv_seq *seq) { return seq && seq->pool ? seq->pool->kv_dim : -1; }
+int32_t pkv_seq_device(const pkv_seq *seq) {
+    return seq && seq->pool && !seq->pool->host_only ? seq->pool->device : -1;
+}
 int32_t pkv_seq_slot(const pkv_seq *s) { return s ? s->slot : -1; }
 
 int32_t pkv_seq_page_table(const pkv_seq *s, int32_t *out, int32_t cap) {
