@@ -1338,8 +1338,7 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
         a.pt_write = pt_write ? 1 : 0;
     }
     if (w.n_part > 0) {
-        // (a multiple of four, so that the sums of V start on a 16-byte boundary)
-        const size_t pf = (static_cast<size_t>(w.n_part) * n_heads + 3) & ~static_cast<size_t>(3);
+        const size_t pf = record_floats(w.n_part, n_heads);
         e = p->part.ensure(pf * (2 + head_dim) * sizeof(float), st, p->device);
         if (e != cudaSuccess) return cuda_fail(e, "partials buffer");
         a.pm = static_cast<float *>(p->part.p);
@@ -2155,7 +2154,7 @@ int pkv_attn_contiguous(const float *Q, const float *Kc, const float *Vc, int32_
     const size_t tile0_off = blob.put(img_tile0.data(), img_tile0.size());
     const size_t slot_off = blob.put(img_slot.data(), img_slot.size());
     const size_t desc_bytes = (blob.size() + 255) & ~static_cast<size_t>(255);
-    const size_t pf = (static_cast<size_t>(w.n_part) * n_heads + 3) & ~static_cast<size_t>(3);  // keeps 16-byte alignment
+    const size_t pf = record_floats(w.n_part, n_heads);
     const size_t part_bytes = (pf * (2 + head_dim) * sizeof(float) + 255) & ~static_cast<size_t>(255);
     const size_t img_bytes = img_slot.size() * static_cast<size_t>(n_kv_heads) * kImageBytes;
     const size_t total = desc_bytes + part_bytes + img_bytes;

@@ -294,6 +294,13 @@ struct SplitArgs {
     int32_t *err;
 };
 
+// Floats of the maxima, and of the sums, of n_part partial records of every
+// head: a multiple of four, so that the sums of V behind both start on a 16-byte
+// boundary (the tensor-core kernels store them sixteen bytes at a time).
+inline size_t record_floats(int64_t n_part, int32_t n_heads) {
+    return (static_cast<size_t>(n_part) * static_cast<size_t>(n_heads) + 3) & ~static_cast<size_t>(3);
+}
+
 struct MergeArgs {
     const float *pm, *pl, *pacc;
     float *out;

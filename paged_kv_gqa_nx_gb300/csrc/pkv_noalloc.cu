@@ -169,7 +169,7 @@ extern "C" int pkv_attn_contiguous_noalloc(const float *Q, const float *Kc, cons
         slot_off = round256(tile0_off + img_tile0.size() * sizeof(int32_t));
         desc_end = round256(slot_off + img_slot.size() * sizeof(int32_t));
         part_off = desc_end;
-        pf = static_cast<size_t>(n_part) * n_heads;
+        pf = record_floats(n_part, n_heads);
         img_off = round256(part_off + pf * (2 + static_cast<size_t>(head_dim)) * sizeof(float));
         total = img_off + img_slot.size() * static_cast<size_t>(n_kv_heads) * kImageBytes;
     };
