@@ -1472,6 +1472,10 @@ int run_layer_host(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const fl
     if (rc) return rc;
     pkv_pool *p = seqs[0]->pool;
     DevGuard dg(p->device);
+    if (p->q8) {  // before the staging copies, and before their buffer grows out of a graph's memory
+        rc = refuse_capture(p->stream);
+        if (rc) return rc;
+    }
     const bool vec = (head_dim % 4) == 0;
     auto usable = [&](const void *q) { return q && (vec ? aligned16(q) : aligned4(q)); };
     const int32_t group = n_heads / n_kv_heads;
