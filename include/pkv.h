@@ -136,8 +136,10 @@ PKV_API pkv_pool *pkv_pool_new(int32_t n_blocks, int32_t n_layers, int32_t kv_di
  * prefixes.  There is no fused append.  A row of n_q >= 32 queries, or of n_q *
  * head_dim * (n_heads / n_kv_heads) >= 12288, takes tensor-core tiles where
  * head_dim is a multiple of 16 up to 128 and a kv head serves at most 64 heads;
- * a shorter one reads its keys once for several queries.  Attention and append calls
- * on this pool cannot be captured into a CUDA graph (PKV_ERR_ARG).
+ * a shorter one reads its keys once for several queries.  Calls that enqueue work
+ * on this pool (attention, append, read back, the copies of pkv_ensure_append,
+ * pkv_pool_flush) cannot be captured into a CUDA graph: PKV_ERR_ARG, and nothing
+ * changes.
  *
  * k_pool_dev / v_pool_dev and k_scale_dev / v_scale_dev: caller-owned device
  * buffers, 16-byte aligned, all four or none (the library then allocates

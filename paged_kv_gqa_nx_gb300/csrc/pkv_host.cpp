@@ -2008,6 +2008,11 @@ int pkv_ensure_append_batch(pkv_seq *const *seqs, int32_t M, const int32_t *n) {
             return fail(PKV_ERR_EXHAUSTED, "pool exhausted (%lld blocks needed, %lld free)",
                         static_cast<long long>(needed), static_cast<long long>(avail));
     }
+    if (p->q8 && !p->host_only && !dec.empty()) {  // there are blocks to copy
+        DevGuard dg(p->device);
+        const int rc = refuse_capture(p->stream);
+        if (rc) return rc;
+    }
     // pass 2: apply
     std::vector<CopyDesc> copies;
     for (int32_t r = 0; r < M; ++r) {
@@ -2505,6 +2510,10 @@ int pkv_pool_flush(pkv_pool *p) {
     if (!p) return fail(PKV_ERR_ARG, "NULL pool");
     if (p->host_only || p->dirty.empty()) return PKV_OK;
     DevGuard dg(p->device);
+    if (p->q8) {
+        const int rc = refuse_capture(p->stream);
+        if (rc) return rc;
+    }
     p->blob.clear();
     size_t runs_off, vals_off;
     int32_t n_runs;

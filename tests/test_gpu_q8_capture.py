@@ -60,3 +60,45 @@ def test_host_buffers(pinned, n_q):
         assert torch.equal(out, exp.cpu())
     finally:
         pool.close()
+
+
+def test_copies_and_page_tables():
+    """pkv_ensure_append where it would copy a shared block, and pkv_pool_flush: the same step afterwards reads right."""
+    pool = Q8Pool(40, 1, KV, hd, bs)
+    try:
+        s = pool.seq(200)
+        x, y = randn(100, KV * hd, seed=1), randn(100, KV * hd, seed=2)
+        pool.append([s], x, y, [100])
+        f = pkv.pkv_seq_fork(s)
+        fresh = pool.seq(50)
+        before = [t.clone() for t in pool.values(s, 100)]
+        table, free = pkv.pkv_seq_page_table(f), pkv.pkv_pool_free_blocks(pool.p)
+        with Captured(pool):
+            rcs = [pkv.pkv_ensure_append(f, 1)]
+            pkv.check(pkv.pkv_ensure_append(fresh, 20))        # nothing to copy: the host's lists alone
+            rcs.append(pkv.pkv_pool_flush(pool.p))
+        assert rcs == [pkv.PKV_ERR_ARG] * 2
+        assert pkv.pkv_seq_page_table(f) == table and pkv.pkv_pool_free_blocks(pool.p) == free - 2
+        n = [1, 20]
+        pkv.check(pkv.pkv_ensure_append(f, 1))
+        q, x, y = (randn(21, w * hd, seed=3 + w) for w in (H, KV, KV))
+        out = torch.empty(21, H * hd, device="cuda")
+        pkv.check(pkv.pkv_attn_batch([f, fresh], n, q, x, y, H, KV, hd, 0, 1, scale, out))
+        pool.ok()
+        assert all(torch.equal(a, b) for a, b in zip(pool.values(s, 100), before))
+        # the fork's copy holds the parent's rows, in the step that the new row asks for
+        step = pool.Ks[pkv.pkv_seq_page_table(f)[-1], 0].max().item()
+        assert (pool.values(f, 100)[0] - before[0]).abs().max().item() <= step / 2
+        exp = torch.empty_like(out)
+        other = Q8Pool(40, 1, KV, hd, bs)
+        try:
+            a, b = other.seq(200), other.seq(50)
+            other.append([a], randn(100, KV * hd, seed=1), randn(100, KV * hd, seed=2), [100])
+            pkv.check(pkv.pkv_ensure_append_batch([a, b], n))
+            pkv.check(pkv.pkv_attn_batch([a, b], n, q, x, y, H, KV, hd, 0, 1, scale, exp))
+            other.ok()
+        finally:
+            other.close()
+        assert torch.equal(out, exp)
+    finally:
+        pool.close()
