@@ -29,14 +29,22 @@
 // clocks a key tile instead of 4,600.  The chain's arithmetic is the same.
 //
 // Measured (8 rows of 512 queries behind 2,048 keys, 32 heads over 8, 568 CTAs
-// of 18.5 key tiles on average): 232 us, 1.32 PFLOP/s of f16 products.  With two
+// of 18.5 key tiles on average): 244 us, 1.25 PFLOP/s of f16 products.  With two
 // tiles a key tile takes 5,200 clocks where its MMAs alone take 4,104: what is
 // left is a chain's wait for its own softmax (2,100 to 2,400 clocks from S to
 // P) and for the slots.  A CTA spends 12,000 clocks on its start, 5,000 on its
 // output and 7,000 pass before the next one runs; the rest is the last round.
-// The error is 5.9e-6 of the output's norm there (plain f32: 1.3e-6): the tensor
-// core rounds its f32 sums toward zero, ~300 additions an output.  Sums set aside
-// after every four key tiles give 1.5e-6, and 380 us, by way of L2.
+//
+// The tensor core rounds its f32 sums toward zero, twice a 16 keys, which on
+// values of one sign took 1.1e-5 of an output after 2,300 keys and 1e-4 after
+// 16,000.  So after kHold key tiles the compute threads take the leading part of D
+// into 32 registers, a byte a dim in units of the row's own power of two, and leave
+// D the rest, below 1/64 of the row's largest; it comes back at the end.  With 12
+// tiles (192 additions) the error is 6.2e-6 at most on values of one sign and 2.9e-6
+// of the norm on random ones, whatever the length (10 tiles: 5.0e-6 and 2.4e-6, and
+// 2% more time on long rows).  It takes 12 of the 244 us above, 7% behind 16,000
+// keys and nothing up to 1,536 keys.  Sums set aside whole instead, in the result's
+// place, took 13 to 40 us more: they leave L2 between two looks.
 // Measured and not taken: six slots of 16 KiB (286 us against 257 at the time),
 // PV begun at the first half of P (no gain), 8 or 32 query rows in flight a
 // warp (258 and 259 us against 252).
@@ -65,6 +73,7 @@ constexpr size_t kSmem = 4 * kQPiece + kSlots * kSlot + 1024;  // + alignment sl
 static_assert(2 * kQPiece == (kLoneSlots - kSlots) * kSlot, "the second tile's pieces are whole slots");
 constexpr float kGrow = 8.f;                    // log2 headroom of the reference maximum
 constexpr int kPExp = 7;                        // C <= kPExp + c: p * 2^(C - c) <= 2^15
+constexpr int kHold = 12;                       // key tiles until D's leading part is set aside
 static_assert(kKeyTile == 64, "a key tile is two images");
 
 __device__ __forceinline__ float pow2f(int n) { return __uint_as_float(static_cast<uint32_t>(n + 127) << 23); }
@@ -81,6 +90,11 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &p0, uint32_t 
     const __half2 h1 = __floats2half2_rn(a - f.x, b - f.y);
     p0 = *reinterpret_cast<const uint32_t *>(&h0);
     p1 = *reinterpret_cast<const uint32_t *>(&h1);
+}
+
+// Byte k of a word, h + 128, as h (2^23 + u is the float of bits 0x4b000000 | u).
+__device__ __forceinline__ float held(uint32_t w, int k) {
+    return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 | k)) - (8388608.f + 128.f);
 }
 
 // Gc, Hc: the group and the head width where compiled in (0: taken from g_arg, hd_arg)
@@ -347,109 +361,160 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a, 
             if (lane == 0) mbar_arrive(smem_u32(&bar_q[c]));
 
             float m_ref = -INFINITY, l_run = 0.f;
-            int cexp = 0;  // C: D holds 2^C x the output's sum
+            int cexp = 0;  // C: D and h * unit, h of hold's bytes, hold 2^C x the output's sum
+            uint32_t hold[kMaxHD / 4];
+            float unit = 0.f;
+#pragma unroll
+            for (int i = 0; i < kMaxHD / 4; ++i) hold[i] = 0x80808080u;
             auto exps = [&](int kt) { return __ldg(reinterpret_cast<const int2 *>(image(kt) + kImageExpOff)); };
             int2 ea = exps(kt0), eb = exps(second(kt0));  // the images' exponents (K, V), a tile ahead
-            for (int j = 0; j < n; ++j) {
-                const int base = kbeg + j * kKeys;
-                const int ke[2] = {ea.x, eb.x}, ve[2] = {ea.y, eb.y};
-                if (j + 1 < n) {
-                    const int kt = kt0 + 2 * (j + 1);
-                    ea = exps(kt);
-                    eb = exps(second(kt));
-                }
-                const int b = lone ? j & 1 : c;
-                const uint32_t tS = tbase + lanes + 256 + 128 * b;
-                ok = wait_w(&bar_s[b], lone ? j >> 1 : j);
-                if (!ok) break;
-                fence_after_sync();
-                uint32_t x[kKeys];  // the row's scores (f32 bits)
+            for (int j0 = 0; j0 < n && ok; j0 += kHold) {
+                if (j0 > 0) {
+                    // The leading part of the sum goes to hold, h = the sum in units of a
+                    // power of two that makes the row's largest 32 to 64; what that
+                    // leaves of it stays in D (exactly, as the sum has 24 bits).
+                    ok = wait_w(&bar_s[lone ? j0 & 1 : c], lone ? j0 >> 1 : j0) && (!lone || wait_w(&bar_v, j0 - 1));
+                    if (!ok) break;
+                    fence_after_sync();
+                    uint32_t x[kMaxHD];
 #pragma unroll
-                for (int i = 0; i < kKeys; i += 32) tmem_ld32_issue(tS + i, x + i);
-                tmem_ld_done(x);
-                auto xf = [&](int i) { return __uint_as_float(x[i]); };
-                // scores to base-2 units: one exact factor 2^sn a half (two steps
-                // where 2^sn is not a normal f32)
-                float fsc[2];
+                    for (int i = 0; i < kMaxHD; i += 32) tmem_ld32_issue(tO + i, x + i);
+                    tmem_ld_done(x);
+                    if (j0 > kHold) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int sn = -(qexp + ke[h]);
-                    const bool one = sn >= -126 && sn <= 127;
-                    fsc[h] = one ? pow2f(sn) : 1.f;
-                    if (!one) {
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) x[64 * h + i] = __float_as_uint(mul_pow2(xf(64 * h + i), sn));
+                        for (int i = 0; i < kMaxHD; ++i)
+                            x[i] = __float_as_uint(fmaf(held(hold[i / 4], i & 3), unit, __uint_as_float(x[i])));
                     }
-                }
-                if (base + kKeys > klim) {
+                    float top = 0.f;
 #pragma unroll
-                    for (int i = 0; i < kKeys; ++i) x[i] = base + i < klim ? x[i] : 0xff800000u;
-                }
-                float top = -INFINITY;
+                    for (int i = 0; i < kMaxHD; ++i)  // (columns past the head's width hold anything)
+                        if (i < 16 || i < kHD) top = fmaxf(top, fabsf(__uint_as_float(x[i])));
+                    const int e = max(-100, min(100, static_cast<int>(__float_as_uint(top) >> 23) - 127 - 5));
+                    const float inv = pow2f(-e);
+                    unit = pow2f(e);
+                    constexpr float kMagic = 12582912.f + 128.f;  // 1.5 * 2^23: a sum's low byte is the integer + 128
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float mx[2] = {fmaxf(xf(64 * h), xf(64 * h + 1)), fmaxf(xf(64 * h + 2), xf(64 * h + 3))};
-#pragma unroll
-                    for (int i = 4; i < 64; i += 2) mx[(i >> 1) & 1] = max3(mx[(i >> 1) & 1], xf(64 * h + i), xf(64 * h + i + 1));
-                    top = fmaxf(top, fmaxf(mx[0], mx[1]) * fsc[h]);
-                }
-                const bool move = m_ref != -INFINITY && top > m_ref + kGrow;
-                const float m_use = m_ref == -INFINITY || move ? top : m_ref;
-                const float nm = m_use == -INFINITY ? 0.f : -m_use;
-                const int vmin = min(ve[0], ve[1]);
-                const int c_new = j == 0 ? kPExp + vmin : min(cexp, kPExp + vmin);
-                const float f = move ? ex2(m_ref - m_use) : 1.f;
-                // D moves with the reference or with C (after PV(j - 1): QK(j), done,
-                // followed it, but for a lone chain's); the whole warp takes the
-                // branch, as TMEM accesses are the warp's
-                if (j > 0 && (c_new != cexp || __any_sync(0xffffffffu, move))) {
-                    if (lone) {
-                        ok = wait_w(&bar_v, j - 1);
-                        if (!ok) break;
-                        fence_after_sync();
-                    }
-                    const int d = c_new - cexp;
-#pragma unroll 1
-                    for (int i = 0; i < kHD / 16; ++i) {
+                    for (int i = 0; i < kMaxHD; i += 16) {
+                        if (i >= kHD) continue;
                         float v[16];
-                        tmem_ld16(tO + 16 * i, v);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) v[k] = mul_pow2(v[k] * f, d);
-                        tmem_st16(tO + 16 * i, v);
-                    }
-                }
-                m_ref = m_use;
-                cexp = c_new;
-                // P over S, half by half: two pieces of p * 2^(C - c)
-                uint64_t sum[2] = {0, 0};
-                const uint64_t nm2 = pair(nm, nm);
+                        for (int k = 0; k < 16; k += 4) {
+                            uint32_t t[4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int pe = cexp - ve[h];  // <= kPExp
-                    const float pf = pe >= -126 ? pow2f(pe) : 0.f;
-                    const uint64_t f2 = pair(fsc[h], fsc[h]), pf2 = pair(pf, pf);
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {  // 32 keys
-                        uint32_t p0[16], p1[16];
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const int i = 64 * h + 32 * r + 2 * k;
-                            const float2 e = unpair(fma2(pair(xf(i), xf(i + 1)), f2, nm2));
-                            const uint64_t p = pair(ex2(e.x), ex2(e.y));
-                            sum[k & 1] = add2(sum[k & 1], p);
-                            const float2 y = unpair(mul2(p, pf2));
-                            split2(y.x, y.y, p0[k], p1[k]);
+                            for (int z = 0; z < 4; ++z) {
+                                const float y = __uint_as_float(x[i + k + z]), r = fmaf(y, inv, kMagic);
+                                t[z] = __float_as_uint(r);
+                                v[k + z] = fmaf(kMagic - r, unit, y);
+                            }
+                            hold[(i + k) / 4] =
+                                __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
                         }
-                        tmem_st16u(tS + 32 * h + 16 * r, p0);
-                        tmem_st16u(tS + 64 + 32 * h + 16 * r, p1);
+                        tmem_st16(tO + i, v);
                     }
+                    tmem_st_wait();  // (D may be rescaled next)
                 }
-                const float2 s2 = unpair(add2(sum[0], sum[1]));
-                l_run = fmaf(l_run, f, s2.x + s2.y);
-                tmem_st_wait();
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar_p[b]));
+                for (int j = j0; j < min(n, j0 + kHold); ++j) {
+                    const int base = kbeg + j * kKeys;
+                    const int ke[2] = {ea.x, eb.x}, ve[2] = {ea.y, eb.y};
+                    if (j + 1 < n) {
+                        const int kt = kt0 + 2 * (j + 1);
+                        ea = exps(kt);
+                        eb = exps(second(kt));
+                    }
+                    const int b = lone ? j & 1 : c;
+                    const uint32_t tS = tbase + lanes + 256 + 128 * b;
+                    ok = wait_w(&bar_s[b], lone ? j >> 1 : j);
+                    if (!ok) break;
+                    fence_after_sync();
+                    uint32_t x[kKeys];  // the row's scores (f32 bits)
+#pragma unroll
+                    for (int i = 0; i < kKeys; i += 32) tmem_ld32_issue(tS + i, x + i);
+                    tmem_ld_done(x);
+                    auto xf = [&](int i) { return __uint_as_float(x[i]); };
+                    // scores to base-2 units: one exact factor 2^sn a half (two steps
+                    // where 2^sn is not a normal f32)
+                    float fsc[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int sn = -(qexp + ke[h]);
+                        const bool one = sn >= -126 && sn <= 127;
+                        fsc[h] = one ? pow2f(sn) : 1.f;
+                        if (!one) {
+#pragma unroll
+                            for (int i = 0; i < 64; ++i) x[64 * h + i] = __float_as_uint(mul_pow2(xf(64 * h + i), sn));
+                        }
+                    }
+                    if (base + kKeys > klim) {
+#pragma unroll
+                        for (int i = 0; i < kKeys; ++i) x[i] = base + i < klim ? x[i] : 0xff800000u;
+                    }
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float mx[2] = {fmaxf(xf(64 * h), xf(64 * h + 1)), fmaxf(xf(64 * h + 2), xf(64 * h + 3))};
+#pragma unroll
+                        for (int i = 4; i < 64; i += 2) mx[(i >> 1) & 1] = max3(mx[(i >> 1) & 1], xf(64 * h + i), xf(64 * h + i + 1));
+                        top = fmaxf(top, fmaxf(mx[0], mx[1]) * fsc[h]);
+                    }
+                    const bool move = m_ref != -INFINITY && top > m_ref + kGrow;
+                    const float m_use = m_ref == -INFINITY || move ? top : m_ref;
+                    const float nm = m_use == -INFINITY ? 0.f : -m_use;
+                    const int vmin = min(ve[0], ve[1]);
+                    const int c_new = j == 0 ? kPExp + vmin : min(cexp, kPExp + vmin);
+                    const float f = move ? ex2(m_ref - m_use) : 1.f;
+                    // D moves with the reference or with C (after PV(j - 1): QK(j), done,
+                    // followed it, but for a lone chain's); the whole warp takes the
+                    // branch, as TMEM accesses are the warp's
+                    if (j > 0 && (c_new != cexp || __any_sync(0xffffffffu, move))) {
+                        if (lone) {
+                            ok = wait_w(&bar_v, j - 1);
+                            if (!ok) break;
+                            fence_after_sync();
+                        }
+                        const int d = c_new - cexp;
+                        unit = mul_pow2(unit * f, d);
+#pragma unroll 1
+                        for (int i = 0; i < kHD / 16; ++i) {
+                            float v[16];
+                            tmem_ld16(tO + 16 * i, v);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) v[k] = mul_pow2(v[k] * f, d);
+                            tmem_st16(tO + 16 * i, v);
+                        }
+                    }
+                    m_ref = m_use;
+                    cexp = c_new;
+                    // P over S, half by half: two pieces of p * 2^(C - c)
+                    uint64_t sum[2] = {0, 0};
+                    const uint64_t nm2 = pair(nm, nm);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int pe = cexp - ve[h];  // <= kPExp
+                        const float pf = pe >= -126 ? pow2f(pe) : 0.f;
+                        const uint64_t f2 = pair(fsc[h], fsc[h]), pf2 = pair(pf, pf);
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {  // 32 keys
+                            uint32_t p0[16], p1[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const int i = 64 * h + 32 * r + 2 * k;
+                                const float2 e = unpair(fma2(pair(xf(i), xf(i + 1)), f2, nm2));
+                                const uint64_t p = pair(ex2(e.x), ex2(e.y));
+                                sum[k & 1] = add2(sum[k & 1], p);
+                                const float2 y = unpair(mul2(p, pf2));
+                                split2(y.x, y.y, p0[k], p1[k]);
+                            }
+                            tmem_st16u(tS + 32 * h + 16 * r, p0);
+                            tmem_st16u(tS + 64 + 32 * h + 16 * r, p1);
+                        }
+                    }
+                    const float2 s2 = unpair(add2(sum[0], sum[1]));
+                    l_run = fmaf(l_run, f, s2.x + s2.y);
+                    tmem_st_wait();
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bar_p[b]));
+                }
             }
             if (ok) ok = wait_w(&bar_o[c], 0);
             if (!ok) {
@@ -480,6 +545,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a, 
                     const int nd = min(32, kHD - 32 * i);  // 16 or 32 dims
                     float v[32];
                     tmem_ld32(tO + 32 * i, v);
+                    if (n > kHold) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = fmaf(held(hold[8 * i + k / 4], k & 3), unit, v[k]);
+                    }
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = mul_pow2(v[k] * scl, -cexp);
                     if (!valid) {
