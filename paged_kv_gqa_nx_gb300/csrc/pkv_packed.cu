@@ -67,8 +67,10 @@ __device__ __forceinline__ int seq_of_tile(const PackedSeqs<N> &l, int t) {
 // at once and then both waited.  P of tile j is read by PV(j) before QK(j + 1),
 // issued by the same thread, writes over it.
 //
-// Probabilities are rounded to the operand type (half a step, 2^-9 or 2^-12
-// relative to p, against outputs of the same type); sums use them unrounded.
+// Probabilities are rounded to the operand type (half a step: 2^-8 relative to p
+// in bf16, 2^-11 in f16 and 2^-25 absolute for f16 below 2^-14; the outputs, of the
+// same type, are rounded by as much); sums use them unrounded.  On random rows
+// the output is 1.15 to 1.36 times as far from 64 bits as one of f32 probabilities.
 // The reference maximum moves, and O is rescaled, only where a tile's maximum
 // passes it by more than 2^8, which keeps every p at most 256.
 //

@@ -257,8 +257,11 @@ cudaError_t launch_generic(const Q8Args &a, const Q8Addr &q, const B &blob, cuda
 // than 2^8 (one warp vote per tile finds out); sums stay per lane until the
 // end.  W = p * vs / 2^c with c an exponent of the warp that follows the
 // largest V scale of the tiles (O holds 2^-c times the sum), which keeps W in
-// f16's range: W <= 2^14 after a factor 2^6, and blocks of one 32-key tile may
-// differ by 2^12 in scale before W's pieces lose bits below 2^-19 of p.
+// f16's range: W <= 2^14 after a factor 2^6.  W's second piece ends at 2^-24, half
+// a step of which is 2^-25; as 2^c is at most 2^6 above the tile's largest scale
+// 2^e (or 2^-60 of the largest that the warp has seen), a key's term is off by
+// 2^-25 * 127 * 2^c / 2^6 <= 2^-25 of the tile's largest value (127 * 2^e) whatever
+// its own scale, besides the 2^-22 of itself that two pieces leave out.
 //
 // Shared memory rows keep their 16-byte chunks XOR-swizzled by the key, so
 // that the 8 rows of an ldmatrix fall in distinct bank groups.
@@ -761,9 +764,9 @@ cudaError_t launch_decode_with(const Q8Args &a, const Q8Addr &q, const B &blob, 
 // CTA per (64-key tile, kv head).  The images' power of two needs no look at
 // the values: with 2^t the tile's largest scale every magnitude is at most
 // 127 * 2^t, so 2^(8 - t) brings them below 2^15, and (u - 128) * 2^(8 - t + e)
-// is an f16 value, seven bits -- unless the key's scale 2^e lies more than 2^25
-// below the tile's, where its last bits are dropped -- so piece 1 is left out,
-// as on the other narrow pools.  K goes straight to its image; V's bytes turn
+// is an f16 value -- seven bits times a factor of at least 2^-24, the smallest
+// f16, where the key's scale 2^e lies at most 2^32 below the tile's; below that the
+// factor rounds to 0 -- so piece 1 is left out, as on the other narrow pools.  K goes straight to its image; V's bytes turn
 // through shared memory.  Bound by the images' writes: 24 us for 320 tiles of 8
 // heads of 128 (42 MB read, 84 MB written).
 
