@@ -433,8 +433,9 @@ enum pkv_dtype {
  * after row i - 1 (heads side by side inside a row), and likewise K, V and out,
  * so columns of a fused projection's output can be passed as they are.  dtype:
  * PKV_BF16 or PKV_F16, for all four.  Scores, softmax statistics and the
- * output accumulate in f32; the probabilities are rounded to dtype before they
- * meet V, and the output once at the end.  A key that a query does not see
+ * output accumulate in f32 (on tensor cores, which round sums toward zero: values
+ * of one sign lose up to 1.2e-4 of an output, at any length); the probabilities
+ * are rounded to dtype before they meet V, and the output once at the end.  A key that a query does not see
  * never reaches it, whatever it holds.  Rows of out past the last sequence
  * are left as they were; out may not overlap the inputs.
  *

@@ -74,6 +74,16 @@ __device__ __forceinline__ int seq_of_tile(const PackedSeqs<N> &l, int t) {
 // The reference maximum moves, and O is rescaled, only where a tile's maximum
 // passes it by more than 2^8, which keeps every p at most 256.
 //
+// The tensor core rounds its f32 sums toward zero, which on values of one sign
+// takes 7e-9 of an output a key: 1.1e-4 of it at 16,384 keys, 4.3e-4 at 65,536 and
+// 1.3e-3 at 200,000, past f16's half step (4.9e-4).  In sequences of more than
+// kLongKeys the leading part of O therefore goes to registers after every kHold key
+// tiles, a byte a dim in units of the row's own power of two, and O goes on from the
+// rest: 7.3e-5 at 65,536 keys and 8.8e-5 at 200,000.  It costs 2 to 3% of such a
+// launch (40,000 tokens: 7.93 -> 8.16 ms), and in a kernel for all lengths 2% of a
+// ragged batch, so that a launch without a long sequence has an instance without
+// it.  What a sequence's rows return goes by its own length alone.
+//
 // A zero probability times an infinity is NaN, so V rows behind a sequence's
 // end or in a query's future must not hold one: on the (at most two) tiles
 // that some row of the CTA does not see whole, the compute threads of one chain
@@ -97,6 +107,8 @@ static_assert(256 * kTcComputeRegs + 128 * kTcOtherRegs <= kTcThreads * kTcLaunc
 constexpr uint32_t kTcCols = 512;           // O_c at c * 128, S_c / P_c at 256 + c * 128
 constexpr int kPassLeft = 2;                // MMAs of QK still to issue when the turn passes
 constexpr float kGrow = 8.f;                // log2 headroom of the reference maximum
+constexpr int kLongKeys = 16384;            // in a longer sequence O's leading part is set aside
+constexpr int kHold = 64;                   // after every so many key tiles
 
 template <int D>
 struct TcCfg {
@@ -221,7 +233,7 @@ __device__ __forceinline__ Piece piece_of(const PackedArgs &a, const PackedSeqs<
 //   go[x], look[x]           V of a partly seen tile loaded / looked over
 //   answer                   the number of a further piece
 //   work[x] / wfree[x]       piece handed out / read by the other ten warps
-template <int D, class T, int N>
+template <int D, class T, int N, bool kLong>
 __global__ void __launch_bounds__(kTcThreads, 1)
     packed_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ PackedArgs a,
@@ -476,147 +488,176 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int tok = p.q0 + c * TQ + (m >> log_p);
             const bool valid = tok < p.len;
             const int lim = a.causal ? min(tok + 1, p.len) : p.len;  // keys this row sees
-            float m_ref = -INFINITY, l_run = 0.f;
-            for (int j = 0; j < n; ++j, ++tiles) {
-                const uint32_t look = lk + j - p.look0;
-                if (j >= p.look0 && (c == 1 || j >= p.n1)) {
-                    // this chain looks over V_j: keys up to key0 are seen by every row; a
-                    // key's 128 bytes of each 64 columns are 8 chunks.  (The loading warp
-                    // tells when the slot is at V_j: these warps follow no earlier item.)
-                    const uint32_t i = it + 2 * j + 1;
-                    ok = wait_w(&bar_go[look & 3], look >> 2) && wait_w(&bar_full[slot(i)], rph(i));
-                    if (!ok) break;
-                    uint4 *v = reinterpret_cast<uint4 *>(ring + slot(i) * C::kTile);
-                    const int key0 = max(0, (a.causal ? p.q0 + 1 : p.len) - j * kKeys);
-                    constexpr uint32_t kE = std::is_same<T, bf16>::value ? 0x7f807f80u : 0x7c007c00u;
-                    constexpr uint32_t kOne = std::is_same<T, bf16>::value ? 0x00800080u : 0x04000400u;
-                    uint32_t seen = 0;  // a half's exponent is all ones where adding one to it reaches the sign bit
+            float m_ref = -INFINITY, l_run = 0.f, unit = 0.f;
+            uint32_t hold[kLong ? D / 4 : 1];  // with it the output's sum is O + h * unit
+            if constexpr (kLong) {
 #pragma unroll
-                    for (int x0 = 0; x0 < static_cast<int>(C::kTile / 16); x0 += 128) {
-                        const int x = x0 + m;
-                        if ((x & 1023) >= key0 * 8) {
-                            const uint4 y = v[x];
-                            seen |= ((y.x & kE) + kOne) | ((y.y & kE) + kOne) | ((y.z & kE) + kOne) | ((y.w & kE) + kOne);
+                for (int i = 0; i < D / 4; ++i) hold[i] = 0x80808080u;
+            }
+            const int step = kLong && p.len > kLongKeys ? kHold : n;
+            for (int j0 = 0; j0 < n && ok; j0 += step) {
+                if constexpr (kLong) {
+                    if (j0 > 0) {
+                        ok = wait_w(&bar_s[c], tiles);
+                        if (!ok) break;
+                        fence_after_sync();
+                        uint32_t x[D];
+#pragma unroll
+                        for (int i = 0; i < D; i += 32) tmem_ld32_issue(tO + i, x + i);
+                        tmem_ld_done(x);
+                        unit = set_aside(x, hold, unit, j0 > kHold, D);
+#pragma unroll
+                        for (int i = 0; i < D; i += 16) {
+                            float v[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(x[i + k]);
+                            tmem_st16(tO + i, v);
                         }
+                        tmem_st_wait();  // (O may be rescaled next)
                     }
-                    if (seen & 0x80008000u) {
-                        for (int x = m; x < static_cast<int>(C::kTile / 16); x += 128) {
-                            if ((x & 1023) < key0 * 8) continue;
-                            const uint4 y = v[x];
-                            uint32_t u[4] = {y.x, y.y, y.z, y.w};
+                }
+                for (int j = j0; j < min(n, j0 + step); ++j, ++tiles) {
+                    const uint32_t look = lk + j - p.look0;
+                    if (j >= p.look0 && (c == 1 || j >= p.n1)) {
+                        // this chain looks over V_j: keys up to key0 are seen by every row; a
+                        // key's 128 bytes of each 64 columns are 8 chunks.  (The loading warp
+                        // tells when the slot is at V_j: these warps follow no earlier item.)
+                        const uint32_t i = it + 2 * j + 1;
+                        ok = wait_w(&bar_go[look & 3], look >> 2) && wait_w(&bar_full[slot(i)], rph(i));
+                        if (!ok) break;
+                        uint4 *v = reinterpret_cast<uint4 *>(ring + slot(i) * C::kTile);
+                        const int key0 = max(0, (a.causal ? p.q0 + 1 : p.len) - j * kKeys);
+                        constexpr uint32_t kE = std::is_same<T, bf16>::value ? 0x7f807f80u : 0x7c007c00u;
+                        constexpr uint32_t kOne = std::is_same<T, bf16>::value ? 0x00800080u : 0x04000400u;
+                        uint32_t seen = 0;  // a half's exponent is all ones where adding one to it reaches the sign bit
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                if (not_finite<T>(u[k])) u[k] &= 0xffff0000u;
-                                if (not_finite<T>(u[k] >> 16)) u[k] &= 0xffffu;
+                        for (int x0 = 0; x0 < static_cast<int>(C::kTile / 16); x0 += 128) {
+                            const int x = x0 + m;
+                            if ((x & 1023) >= key0 * 8) {
+                                const uint4 y = v[x];
+                                seen |= ((y.x & kE) + kOne) | ((y.y & kE) + kOne) | ((y.z & kE) + kOne) | ((y.w & kE) + kOne);
                             }
-                            v[x] = make_uint4(u[0], u[1], u[2], u[3]);
                         }
-                        // the flag holds the count of the look it belongs to (+ 1)
-                        *static_cast<volatile uint32_t *>(&dirty[look & 3]) = look + 1;
+                        if (seen & 0x80008000u) {
+                            for (int x = m; x < static_cast<int>(C::kTile / 16); x += 128) {
+                                if ((x & 1023) < key0 * 8) continue;
+                                const uint4 y = v[x];
+                                uint32_t u[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    if (not_finite<T>(u[k])) u[k] &= 0xffff0000u;
+                                    if (not_finite<T>(u[k] >> 16)) u[k] &= 0xffffu;
+                                }
+                                v[x] = make_uint4(u[0], u[1], u[2], u[3]);
+                            }
+                            // the flag holds the count of the look it belongs to (+ 1)
+                            *static_cast<volatile uint32_t *>(&dirty[look & 3]) = look + 1;
+                        }
+                        fence_proxy_async();  // before the MMAs read the tile
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&bar_look[look & 3]));
                     }
-                    fence_proxy_async();  // before the MMAs read the tile
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&bar_look[look & 3]));
-                }
-                ok = wait_w(&bar_s[c], tiles);
-                if (!ok) break;
-                fence_after_sync();
-                uint32_t x[kKeys];  // the row's scores (f32 bits)
-#pragma unroll
-                for (int i = 0; i < kKeys; i += 32) tmem_ld32_issue(tS + i, x + i);
-                tmem_ld_done(x);
-                auto xf = [&](int i) { return __uint_as_float(x[i]); };
-                const int base = j * kKeys;
-                if (base + kKeys > lim) {
-#pragma unroll
-                    for (int i = 0; i < kKeys; ++i) x[i] = base + i < lim ? x[i] : 0xff800000u;
-                }
-                float mx[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mx[i] = fmaxf(xf(2 * i), xf(2 * i + 1));
-#pragma unroll
-                for (int i = 8; i < kKeys; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], xf(i), xf(i + 1));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs;
-                const bool move = top > m_ref + kGrow || m_ref == -INFINITY;
-                const float m_use = move ? top : m_ref;
-                const float nm = m_use == -INFINITY ? 0.f : -m_use;
-                // O moves with the reference (QK(j), already done, followed PV(j - 1))
-                const float f = move && m_ref != -INFINITY ? ex2(m_ref - m_use) : 1.f;
-                if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll 1
-                    for (int i = 0; i < D / 16; ++i) {
-                        float o[16];
-                        tmem_ld16(tO + 16 * i, o);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] *= f;
-                        tmem_st16(tO + 16 * i, o);
-                    }
-                }
-                m_ref = m_use;
-                // P over S
-                uint64_t sum[2] = {0, 0};
-                const uint64_t cs2 = pair(cs, cs), nm2 = pair(nm, nm);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t pr[32];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const float2 e = unpair(fma2(pair(xf(64 * i + 2 * k), xf(64 * i + 2 * k + 1)), cs2, nm2));
-                        const float p0 = ex2(e.x), p1 = ex2(e.y);
-                        sum[k & 1] = add2(sum[k & 1], pair(p0, p1));
-                        pr[k] = pack2(T{}, p0, p1);
-                    }
-                    tmem_st32u(tS + 32 * i, pr);
-                }
-                const float2 s2 = unpair(add2(sum[0], sum[1]));
-                l_run = fmaf(l_run, f, s2.x + s2.y);
-                tmem_st_wait();
-                if (j >= p.look0) {
-                    ok = wait_w(&bar_look[look & 3], look >> 2);
+                    ok = wait_w(&bar_s[c], tiles);
                     if (!ok) break;
-                    if (*static_cast<volatile uint32_t *>(&dirty[look & 3]) == look + 1) {
-                        // this tile's V values that are not finite, key by key (PV(0) of
-                        // the piece writes over O, unless told that O holds something;
-                        // O is this piece's from then on: its reader is this thread)
-                        const T *v = static_cast<const T *>(a.V) + static_cast<int64_t>(p.row0 + base) * a.v_stride +
-                                     static_cast<int64_t>(p.kvh) * a.hd;
-                        const int see = valid ? min(kKeys, lim - base) : 0;
+                    fence_after_sync();
+                    uint32_t x[kKeys];  // the row's scores (f32 bits)
+#pragma unroll
+                    for (int i = 0; i < kKeys; i += 32) tmem_ld32_issue(tS + i, x + i);
+                    tmem_ld_done(x);
+                    auto xf = [&](int i) { return __uint_as_float(x[i]); };
+                    const int base = j * kKeys;
+                    if (base + kKeys > lim) {
+#pragma unroll
+                        for (int i = 0; i < kKeys; ++i) x[i] = base + i < lim ? x[i] : 0xff800000u;
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx[i] = fmaxf(xf(2 * i), xf(2 * i + 1));
+#pragma unroll
+                    for (int i = 8; i < kKeys; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], xf(i), xf(i + 1));
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs;
+                    const bool move = top > m_ref + kGrow || m_ref == -INFINITY;
+                    const float m_use = move ? top : m_ref;
+                    const float nm = m_use == -INFINITY ? 0.f : -m_use;
+                    // O moves with the reference (QK(j), already done, followed PV(j - 1))
+                    const float f = move && m_ref != -INFINITY ? ex2(m_ref - m_use) : 1.f;
+                    if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
                         for (int i = 0; i < D / 16; ++i) {
                             float o[16];
-                            if (j > 0) {
-                                tmem_ld16(tO + 16 * i, o);
-                            } else {
+                            tmem_ld16(tO + 16 * i, o);
 #pragma unroll
-                                for (int k = 0; k < 16; ++k) o[k] = 0.f;
-                            }
-#pragma unroll 1
-                            for (int kk = 0; kk < kKeys / 2; ++kk) {
-                                const uint32_t pw = tmem_ld1(tS + kk);
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    if (2 * kk + e >= see) continue;
-                                    const unsigned short *vr = reinterpret_cast<const unsigned short *>(
-                                        v + static_cast<int64_t>(2 * kk + e) * a.v_stride) + 16 * i;
-                                    const float pe = half_of(T{}, pw, e);
-#pragma unroll
-                                    for (int k = 0; k < 16; ++k) {
-                                        if (16 * i + k >= a.hd) continue;
-                                        const uint32_t b = __ldg(vr + k);
-                                        if (not_finite<T>(b)) o[k] = fmaf(pe, half_of(T{}, b, 0), o[k]);
-                                    }
-                                }
-                                __syncwarp();
-                            }
+                            for (int k = 0; k < 16; ++k) o[k] *= f;
                             tmem_st16(tO + 16 * i, o);
                         }
-                        if (j == 0 && m == 0) *static_cast<volatile uint32_t *>(&held[c]) = 1;
-                        tmem_st_wait();
+                        unit *= f;
                     }
+                    m_ref = m_use;
+                    // P over S
+                    uint64_t sum[2] = {0, 0};
+                    const uint64_t cs2 = pair(cs, cs), nm2 = pair(nm, nm);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t pr[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const float2 e = unpair(fma2(pair(xf(64 * i + 2 * k), xf(64 * i + 2 * k + 1)), cs2, nm2));
+                            const float p0 = ex2(e.x), p1 = ex2(e.y);
+                            sum[k & 1] = add2(sum[k & 1], pair(p0, p1));
+                            pr[k] = pack2(T{}, p0, p1);
+                        }
+                        tmem_st32u(tS + 32 * i, pr);
+                    }
+                    const float2 s2 = unpair(add2(sum[0], sum[1]));
+                    l_run = fmaf(l_run, f, s2.x + s2.y);
+                    tmem_st_wait();
+                    if (j >= p.look0) {
+                        ok = wait_w(&bar_look[look & 3], look >> 2);
+                        if (!ok) break;
+                        if (*static_cast<volatile uint32_t *>(&dirty[look & 3]) == look + 1) {
+                            // this tile's V values that are not finite, key by key (PV(0) of
+                            // the piece writes over O, unless told that O holds something;
+                            // O is this piece's from then on: its reader is this thread)
+                            const T *v = static_cast<const T *>(a.V) + static_cast<int64_t>(p.row0 + base) * a.v_stride +
+                                         static_cast<int64_t>(p.kvh) * a.hd;
+                            const int see = valid ? min(kKeys, lim - base) : 0;
+#pragma unroll 1
+                            for (int i = 0; i < D / 16; ++i) {
+                                float o[16];
+                                if (j > 0) {
+                                    tmem_ld16(tO + 16 * i, o);
+                                } else {
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) o[k] = 0.f;
+                                }
+#pragma unroll 1
+                                for (int kk = 0; kk < kKeys / 2; ++kk) {
+                                    const uint32_t pw = tmem_ld1(tS + kk);
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e) {
+                                        if (2 * kk + e >= see) continue;
+                                        const unsigned short *vr = reinterpret_cast<const unsigned short *>(
+                                            v + static_cast<int64_t>(2 * kk + e) * a.v_stride) + 16 * i;
+                                        const float pe = half_of(T{}, pw, e);
+#pragma unroll
+                                        for (int k = 0; k < 16; ++k) {
+                                            if (16 * i + k >= a.hd) continue;
+                                            const uint32_t b = __ldg(vr + k);
+                                            if (not_finite<T>(b)) o[k] = fmaf(pe, half_of(T{}, b, 0), o[k]);
+                                        }
+                                    }
+                                    __syncwarp();
+                                }
+                                tmem_st16(tO + 16 * i, o);
+                            }
+                            if (j == 0 && m == 0) *static_cast<volatile uint32_t *>(&held[c]) = 1;
+                            tmem_st_wait();
+                        }
+                    }
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bar_p[c]));
                 }
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar_p[c]));
             }
             if (n > 0 && ok) {
                 ok = wait_w(&bar_o[c], pieces);
@@ -629,6 +670,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bar_ofree[c]));
+                if constexpr (kLong) {
+                    if (n > step) {
+#pragma unroll
+                        for (int i = 0; i < D; ++i)
+                            o[i] = __float_as_uint(fmaf(aside(hold[i / 4], i & 3), unit, __uint_as_float(o[i])));
+                    }
+                }
                 const float inv = 1.f / l_run;
                 T *dst = static_cast<T *>(a.out) + static_cast<int64_t>(p.row0 + (valid ? tok : 0)) * a.o_stride +
                          static_cast<int64_t>(p.h0 + (m & (P - 1))) * a.hd;
@@ -669,7 +717,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 //   S [16 x 32] = Q K^T          A, B by ldmatrix
 //   O [16 x DP] += P V           A from S's accumulators, B by transposed ldmatrix
 //
-// Scores are scaled in f32.  A key that a query does not see has probability 0;
+// Scores are scaled in f32.  In sequences of more than kLongKeys each tile's
+// products have a sum of their own, added to O in f32, as the tensor core would
+// round O toward zero twice a tile (10% of the launch, in an instance of its own).
+// A key that a query does not see has probability 0;
 // as zero times an infinity is NaN, a tile that some row does not see whole is
 // looked over, and where it holds a value that is not finite its products are
 // made one by one, over the keys that the row sees.
@@ -739,7 +790,7 @@ __device__ __forceinline__ bool load_rows(unsigned short *dst, const T *src, int
     return bad;
 }
 
-template <class T, int DP, bool kVec, int N>
+template <class T, int DP, bool kVec, bool kLong, int N>
 __global__ void __launch_bounds__(128) packed_general_kernel(const __grid_constant__ PackedArgs a,
                                                              const __grid_constant__ PackedSeqs<N> l) {
     using C = GenCfg<DP>;
@@ -825,15 +876,25 @@ __global__ void __launch_bounds__(128) packed_general_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < DP / 8; ++i) o[i][0] *= al[0], o[i][1] *= al[0], o[i][2] *= al[1], o[i][3] *= al[1];
         if (!single) {
+            const bool own = kLong && len > kLongKeys;  // the tile's products in sums of their own
 #pragma unroll
-            for (int n = 0; n < kGK / 16; ++n)
+            for (int d = 0; d < DP; d += 16) {
+                float t[2][4];
 #pragma unroll
-                for (int d = 0; d < DP; d += 16) {
+                for (int e = 0; e < 4; ++e) t[0][e] = own ? 0.f : o[d / 8][e], t[1][e] = own ? 0.f : o[d / 8 + 1][e];
+#pragma unroll
+                for (int n = 0; n < kGK / 16; ++n) {
                     uint32_t vb[4];
                     ldsm4<true>(vb, Vs + (16 * n + mr + 8 * (mi & 1)) * C::kPitch + d + 8 * (mi >> 1));
-                    mma16<T>(o[d / 8], p[n], vb[0], vb[1]);
-                    mma16<T>(o[d / 8 + 1], p[n], vb[2], vb[3]);
+                    mma16<T>(t[0], p[n], vb[0], vb[1]);
+                    mma16<T>(t[1], p[n], vb[2], vb[3]);
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    o[d / 8][e] = own ? o[d / 8][e] + t[0][e] : t[0][e];
+                    o[d / 8 + 1][e] = own ? o[d / 8 + 1][e] + t[1][e] : t[1][e];
+                }
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < kGK / 8; ++i)
@@ -885,19 +946,19 @@ void fill_seqs(PackedSeqs<N> &l, const int32_t *start, const int32_t *len, int32
     l.tile0[n] = at;
 }
 
-template <class T, int DP, bool kVec, int N>
+template <class T, int DP, bool kVec, bool kLong, int N>
 cudaError_t launch_general_n(const PackedArgs &a, const int32_t *start, const int32_t *len, int32_t n, cudaStream_t s) {
     PackedSeqs<N> l;
     fill_seqs(l, start, len, n, kGQ);
     static PerDeviceOnce configured;  // the attribute is per function and device
     const cudaError_t ce = configured.run([&]() -> cudaError_t {
-        return cudaFuncSetAttribute(packed_general_kernel<T, DP, kVec, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(packed_general_kernel<T, DP, kVec, kLong, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(GenCfg<DP>::kSmem));
     });
     if (ce != cudaSuccess) return ce;
     const long long grid = static_cast<long long>(l.tile0[n]) * a.n_heads;
     if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    packed_general_kernel<T, DP, kVec, N><<<static_cast<unsigned>(grid), 128, GenCfg<DP>::kSmem, s>>>(a, l);
+    packed_general_kernel<T, DP, kVec, kLong, N><<<static_cast<unsigned>(grid), 128, GenCfg<DP>::kSmem, s>>>(a, l);
     return cudaGetLastError();
 }
 
@@ -927,7 +988,7 @@ bool tc_takes(const PackedArgs &a) {
            ok(a.out, a.o_stride) && a.scale_log2 > 0.f && a.scale_log2 <= 3e38f;
 }
 
-template <int D, class T, int N>
+template <int D, class T, int N, bool kLong>
 cudaError_t launch_tc_n(const PackedArgs &a, const int32_t *start, const int32_t *len, int32_t n, cudaStream_t s) {
     using C = TcCfg<D>;
     static PerDeviceOnce configured;  // the attributes are per function and device
@@ -935,10 +996,10 @@ cudaError_t launch_tc_n(const PackedArgs &a, const int32_t *start, const int32_t
         // setmaxnreg.inc waits for registers of the launch's own: launch only
         // if the kernel starts with what the split was sized for
         cudaFuncAttributes fa{};
-        cudaError_t e = cudaFuncGetAttributes(&fa, packed_tc_kernel<D, T, N>);
+        cudaError_t e = cudaFuncGetAttributes(&fa, packed_tc_kernel<D, T, N, kLong>);
         if (e != cudaSuccess) return e;
         if (fa.numRegs < kTcLaunchRegs || fa.maxThreadsPerBlock < kTcThreads) return cudaErrorInvalidConfiguration;
-        return cudaFuncSetAttribute(packed_tc_kernel<D, T, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(packed_tc_kernel<D, T, N, kLong>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(C::kSmem));
     });
     if (ce != cudaSuccess) return ce;
@@ -958,23 +1019,30 @@ cudaError_t launch_tc_n(const PackedArgs &a, const int32_t *start, const int32_t
     if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     PackedArgs b = a;
     b.out32 = a.hd % 16 == 0 && a.o_stride % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
-    packed_tc_kernel<D, T, N><<<static_cast<unsigned>(grid), kTcThreads, C::kSmem, s>>>(mq, mk, mv, b, l, log_p);
+    packed_tc_kernel<D, T, N, kLong><<<static_cast<unsigned>(grid), kTcThreads, C::kSmem, s>>>(mq, mk, mv, b, l, log_p);
     return cudaGetLastError();
 }
 
 template <class T>
 cudaError_t launch_tc(const PackedArgs &a, const int32_t *start, const int32_t *len, int32_t n, cudaStream_t s) {
+    const bool few = n <= 64;
+    if (len[0] > kLongKeys)  // the longest
+        return a.hd <= 64 ? launch_tc_n<64, T, kPackedSeqs, true>(a, start, len, n, s)
+                          : launch_tc_n<128, T, kPackedSeqs, true>(a, start, len, n, s);
     if (a.hd <= 64)
-        return n <= 64 ? launch_tc_n<64, T, 64>(a, start, len, n, s) : launch_tc_n<64, T, kPackedSeqs>(a, start, len, n, s);
-    return n <= 64 ? launch_tc_n<128, T, 64>(a, start, len, n, s) : launch_tc_n<128, T, kPackedSeqs>(a, start, len, n, s);
+        return few ? launch_tc_n<64, T, 64, false>(a, start, len, n, s) : launch_tc_n<64, T, kPackedSeqs, false>(a, start, len, n, s);
+    return few ? launch_tc_n<128, T, 64, false>(a, start, len, n, s) : launch_tc_n<128, T, kPackedSeqs, false>(a, start, len, n, s);
 }
 
 template <class T, int DP>
 cudaError_t launch_general_d(const PackedArgs &a, const int32_t *start, const int32_t *len, int32_t n, cudaStream_t s) {
     auto ok = [](const void *p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0; };
-    if (a.hd % 8 == 0 && ok(a.Q, a.q_stride) && ok(a.K, a.k_stride) && ok(a.V, a.v_stride))
-        return launch_general_n<T, DP, true, kPackedSeqs>(a, start, len, n, s);
-    return launch_general_n<T, DP, false, kPackedSeqs>(a, start, len, n, s);
+    const bool vec = a.hd % 8 == 0 && ok(a.Q, a.q_stride) && ok(a.K, a.k_stride) && ok(a.V, a.v_stride);
+    if (len[0] > kLongKeys)  // the longest
+        return vec ? launch_general_n<T, DP, true, true, kPackedSeqs>(a, start, len, n, s)
+                   : launch_general_n<T, DP, false, true, kPackedSeqs>(a, start, len, n, s);
+    return vec ? launch_general_n<T, DP, true, false, kPackedSeqs>(a, start, len, n, s)
+               : launch_general_n<T, DP, false, false, kPackedSeqs>(a, start, len, n, s);
 }
 template <class T>
 cudaError_t launch_general(const PackedArgs &a, const int32_t *start, const int32_t *len, int32_t n, cudaStream_t s) {

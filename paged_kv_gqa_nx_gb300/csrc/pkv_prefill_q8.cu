@@ -92,11 +92,6 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &p0, uint32_t 
     p1 = *reinterpret_cast<const uint32_t *>(&h1);
 }
 
-// Byte k of a word, h + 128, as h (2^23 + u is the float of bits 0x4b000000 | u).
-__device__ __forceinline__ float held(uint32_t w, int k) {
-    return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 | k)) - (8388608.f + 128.f);
-}
-
 // Gc, Hc: the group and the head width where compiled in (0: taken from g_arg, hd_arg)
 template <int Gc, int Hc>
 __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a, int g_arg, int hd_arg) {
@@ -361,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a, 
             if (lane == 0) mbar_arrive(smem_u32(&bar_q[c]));
 
             float m_ref = -INFINITY, l_run = 0.f;
-            int cexp = 0;  // C: D and h * unit, h of hold's bytes, hold 2^C x the output's sum
+            int cexp = 0;  // C: D + h * unit, h of hold's bytes, is 2^C x the output's sum
             uint32_t hold[kMaxHD / 4];
             float unit = 0.f;
 #pragma unroll
@@ -370,9 +365,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a, 
             int2 ea = exps(kt0), eb = exps(second(kt0));  // the images' exponents (K, V), a tile ahead
             for (int j0 = 0; j0 < n && ok; j0 += kHold) {
                 if (j0 > 0) {
-                    // The leading part of the sum goes to hold, h = the sum in units of a
-                    // power of two that makes the row's largest 32 to 64; what that
-                    // leaves of it stays in D (exactly, as the sum has 24 bits).
                     ok = wait_w(&bar_s[lone ? j0 & 1 : c], lone ? j0 >> 1 : j0) && (!lone || wait_w(&bar_v, j0 - 1));
                     if (!ok) break;
                     fence_after_sync();
@@ -380,35 +372,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a, 
 #pragma unroll
                     for (int i = 0; i < kMaxHD; i += 32) tmem_ld32_issue(tO + i, x + i);
                     tmem_ld_done(x);
-                    if (j0 > kHold) {
-#pragma unroll
-                        for (int i = 0; i < kMaxHD; ++i)
-                            x[i] = __float_as_uint(fmaf(held(hold[i / 4], i & 3), unit, __uint_as_float(x[i])));
-                    }
-                    float top = 0.f;
-#pragma unroll
-                    for (int i = 0; i < kMaxHD; ++i)  // (columns past the head's width hold anything)
-                        if (i < 16 || i < kHD) top = fmaxf(top, fabsf(__uint_as_float(x[i])));
-                    const int e = max(-100, min(100, static_cast<int>(__float_as_uint(top) >> 23) - 127 - 5));
-                    const float inv = pow2f(-e);
-                    unit = pow2f(e);
-                    constexpr float kMagic = 12582912.f + 128.f;  // 1.5 * 2^23: a sum's low byte is the integer + 128
+                    unit = set_aside(x, hold, unit, j0 > kHold, kHD);  // (columns past the width hold anything)
 #pragma unroll
                     for (int i = 0; i < kMaxHD; i += 16) {
                         if (i >= kHD) continue;
                         float v[16];
 #pragma unroll
-                        for (int k = 0; k < 16; k += 4) {
-                            uint32_t t[4];
-#pragma unroll
-                            for (int z = 0; z < 4; ++z) {
-                                const float y = __uint_as_float(x[i + k + z]), r = fmaf(y, inv, kMagic);
-                                t[z] = __float_as_uint(r);
-                                v[k + z] = fmaf(kMagic - r, unit, y);
-                            }
-                            hold[(i + k) / 4] =
-                                __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
-                        }
+                        for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(x[i + k]);
                         tmem_st16(tO + i, v);
                     }
                     tmem_st_wait();  // (D may be rescaled next)
@@ -547,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(PrefillArgs a, 
                     tmem_ld32(tO + 32 * i, v);
                     if (n > kHold) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = fmaf(held(hold[8 * i + k / 4], k & 3), unit, v[k]);
+                        for (int k = 0; k < 32; ++k) v[k] = fmaf(aside(hold[8 * i + k / 4], k & 3), unit, v[k]);
                     }
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = mul_pow2(v[k] * scl, -cexp);

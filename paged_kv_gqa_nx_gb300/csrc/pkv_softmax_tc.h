@@ -106,6 +106,42 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+// The leading part of a row's running sums, out of the tensor core's reach: it
+// rounds toward zero at every addition to a sum, so a long one loses steadily.
+// Byte k of a word, h + 128, as h (2^23 + u is the float of bits 0x4b000000 | u):
+__device__ __forceinline__ float aside(uint32_t w, int k) {
+    return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 | k)) - (8388608.f + 128.f);
+}
+// x (f32 bits; joined by what is set aside already, where there is some) becomes
+// h * unit + x: h in hold's bytes, unit a power of two (returned) that makes the
+// row's largest 32 to 64, x what that leaves, exactly, as a sum has 24 bits.  Only
+// the first `width` of x count.
+template <int N>
+__device__ __forceinline__ float set_aside(uint32_t (&x)[N], uint32_t (&hold)[N / 4], float unit, bool join, int width) {
+    if (join) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = __float_as_uint(fmaf(aside(hold[i / 4], i & 3), unit, __uint_as_float(x[i])));
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < 16 || i < width) top = fmaxf(top, fabsf(__uint_as_float(x[i])));
+    const int e = max(-100, min(100, static_cast<int>(__float_as_uint(top) >> 23) - 127 - 5));
+    const float to = __uint_as_float(static_cast<uint32_t>(127 + e) << 23), inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    constexpr float kMagic = 12582912.f + 128.f;  // 1.5 * 2^23: a sum's low byte is the integer + 128
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        uint32_t t[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float y = __uint_as_float(x[i + k]), r = fmaf(y, inv, kMagic);
+            t[k] = __float_as_uint(r);
+            x[i + k] = __float_as_uint(fmaf(kMagic - r, to, y));
+        }
+        hold[i / 4] = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+    }
+    return to;
+}
 // One lane of a converged warp, chosen in a way that leaves the operands of the
 // instructions it issues in uniform registers (a test of the lane number does
 // not: eight MMAs then took 440 clocks to issue instead of 270).
