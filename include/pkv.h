@@ -141,7 +141,7 @@ PKV_API pkv_pool *pkv_pool_new(int32_t n_blocks, int32_t n_layers, int32_t kv_di
  * same call that the query does not see included) plus 1e-6, on both sides of
  * that rule and at any length, but not by the same: tensor cores round f32 sums
  * toward zero, which takes up to 6e-6 of an output from values of one sign on the
- * tiles and 3e-6 in shorter rows, and on random values leaves an error of 3e-6 and
+ * tiles and 3e-6 in shorter rows (at the default split), and on random values leaves an error of 3e-6 and
  * 6e-7 of the output's norm (f32 arithmetic: 1e-6).  As the error goes by the
  * largest value, an output made of far smaller ones (2^-12 of it and below) has
  * fewer exact bits than f32's; on the tiles a key or value whose scale lies more
@@ -514,7 +514,8 @@ PKV_API int pkv_pool_flush(pkv_pool *pool);
 
 /* Keys per split-K work unit of the decode kernels on f32 pools (default 1024,
  * a multiple of 32 in [32, 65536]); units on bf16 / fp8 pools take 2x / 4x as
- * many keys (the same bytes of K/V), at most 65536.  Tensor-core prefill rows
+ * many keys (the same bytes of K/V), at most 65536; units on 8-bit pools 4x (2x
+ * in rows of at most 8x keys), at most 8192.  Tensor-core prefill rows
  * split every 16 x keys.  Process-wide; every call uses the value current at
  * the call, so results stay bit-exact between calls made under one setting. */
 PKV_API int pkv_set_split_keys(int32_t keys);

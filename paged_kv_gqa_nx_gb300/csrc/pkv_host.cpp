@@ -506,6 +506,11 @@ struct WorkList {
     int64_t n_part = 0;
 };
 
+// The most keys of an 8-bit pool's decode unit.  Its four warps sum a quarter each
+// on tensor cores, which round toward zero: on values of one sign 1,024 keys a warp
+// take 2.6e-6 of an output, 4,096 1.7e-5 and 16,384 8.2e-5.
+constexpr int32_t kMaxSplitQ8 = 8192;
+
 // Rows of an 8-bit pool with few keys are cut into shorter splits than long
 // ones: a row's splits depend on its own length alone.
 struct ShortRows {
@@ -1093,9 +1098,10 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
     // rows, 2 S of bf16, 4 S of fp8 (so a unit's fixed work -- the query
     // pieces, the 4-warp merge -- is amortised alike).  It depends on the
     // pool only, so a row's split boundaries are the same in any batch.
-    const int32_t S_dec = std::min<int32_t>(65536, S * (p->fp8 || p->q8 ? 4 : p->bf16 ? 2 : 1));
+    const int32_t most = p->q8 ? kMaxSplitQ8 : 65536;
+    const int32_t S_dec = std::min<int32_t>(most, S * (p->fp8 || p->q8 ? 4 : p->bf16 ? 2 : 1));
     ShortRows short_rows;
-    if (p->q8) short_rows = {8 * S, std::min<int32_t>(65536, 2 * S)};
+    if (p->q8) short_rows = {8 * S, std::min<int32_t>(most, 2 * S)};
     const int32_t group = attend ? n_heads / n_kv_heads : 0;
     std::vector<Cascade> cas;
     const bool tc_shape = attend && (p->q8 ? prefill_shape_q8(head_dim, group) : prefill_shape(head_dim, group));

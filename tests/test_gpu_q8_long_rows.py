@@ -18,7 +18,7 @@ from test_gpu_q8_pool import Q8Pool, randn
 pytestmark = pytest.mark.gpu
 
 
-def run(mode, past, n, KV, G, hd, bs=16, causal=1):
+def run(mode, past, n, KV, G, hd, bs=16, causal=1, tiles=True):
     H, T, dev = KV * G, past + n, "cuda"
     pool = Q8Pool(-(-T // bs) + 2, 1, KV, hd, bs, max_seqs=2, max_blocks=-(-T // bs))
     try:
@@ -41,7 +41,7 @@ def run(mode, past, n, KV, G, hd, bs=16, causal=1):
         pkv.check(pkv.pkv_attn_batch([s], [n], Q, K[past:].contiguous(), V[past:].contiguous(), H, KV, hd, 0, causal,
                                      scale, out))
         pool.ok()
-        assert pkv.pkv_pool_last_work(pool.p)["prefill_tiles"] > 0
+        assert (pkv.pkv_pool_last_work(pool.p)["prefill_tiles"] > 0) == tiles
         K, V = pool.values(s, T)
         hide = torch.arange(T, device=dev)[None] > past + torch.arange(n, device=dev)[:, None]
         for j in range(KV):
@@ -84,5 +84,18 @@ def test_splits_of_a_row():
         pkv.check(pkv.pkv_set_split_keys(128))      # splits of 2,048
         run("values shrink", 5000, 40, 1, 4, 128)
         run("scores rise", 5000, 40, 3, 1, 128)
+    finally:
+        pkv.check(pkv.pkv_set_split_keys(old))
+
+
+@pytest.mark.parametrize("keys", [32, 1024, 4096, 65536])
+@pytest.mark.parametrize("n", [1, 4])
+def test_decode_units_of_any_split_setting(keys, n):
+    """A decode unit's sums are no longer than its pools' tolerance allows, however many keys a split is set to take."""
+    old = pkv.pkv_get_split_keys()
+    try:
+        pkv.check(pkv.pkv_set_split_keys(keys))
+        for KV, G, hd in [(2, 4, 128), (1, 1, 64), (1, 5, 96)]:
+            run("one sign", 60000, n, KV, G, hd, tiles=False)
     finally:
         pkv.check(pkv.pkv_set_split_keys(old))
