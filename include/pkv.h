@@ -136,19 +136,22 @@ PKV_API pkv_pool *pkv_pool_new(int32_t n_blocks, int32_t n_layers, int32_t kv_di
  * prefixes.  There is no fused append.  A row of n_q >= 32 queries, or of n_q *
  * head_dim * (n_heads / n_kv_heads) >= 12288, takes tensor-core tiles where
  * head_dim is a multiple of 16 up to 128 and a kv head serves at most 64 heads;
- * a shorter one reads its keys once for several queries.  An output is off by
- * at most 1e-5 of the largest |V| among the sequence's keys (the ones of the
- * same call that the query does not see included) plus 1e-6, on both sides of
- * that rule and at any length, but not by the same: tensor cores round f32 sums
- * toward zero, which takes up to 6e-6 of an output from values of one sign on the
- * tiles and 3e-6 in shorter rows (at the default split), and on random values leaves an error of 3e-6 and
- * 6e-7 of the output's norm (f32 arithmetic: 1e-6).  As the error goes by the
- * largest value, an output made of far smaller ones (2^-12 of it and below) has
- * fewer exact bits than f32's; on the tiles a key or value whose scale lies more
- * than 2^32 below the largest one of its 64 keys counts as 0.  Calls that enqueue work
- * on this pool (attention, append, read back, the copies of pkv_ensure_append,
- * pkv_pool_flush) cannot be captured into a CUDA graph: PKV_ERR_ARG, and nothing
- * changes.
+ * a shorter one reads its keys once for several queries.
+ *
+ * Accuracy, besides what the rounding of large f32 scores does: an output is off
+ * by at most 1e-5 of the largest |V| among the sequence's keys (the ones of the
+ * same call that the query does not see included) plus 1e-6, at any length.
+ * Tensor cores round f32 sums toward zero, which takes up to 6e-6 of an output
+ * from values of one sign on the tiles and 3e-6 in shorter rows (at the default
+ * split); on random values the error is 3e-6 and 6e-7 of the output's norm (f32
+ * arithmetic: 1e-6).  As it goes by the largest value, an output made of far
+ * smaller ones (2^-12 of it and below) has fewer exact bits than f32's; on the
+ * tiles a key or value whose scale lies more than 2^32 below the largest one of
+ * its 64 keys counts as 0.
+ *
+ * Calls that enqueue work on this pool (attention, append, read back, the copies
+ * of pkv_ensure_append, pkv_pool_flush) cannot be captured into a CUDA graph:
+ * PKV_ERR_ARG, and nothing changes.
  *
  * k_pool_dev / v_pool_dev and k_scale_dev / v_scale_dev: caller-owned device
  * buffers, 16-byte aligned, all four or none (the library then allocates
