@@ -1090,7 +1090,10 @@ int run_layer(pkv_seq *const *seqs, int32_t M, const int32_t *n_q, const float *
         }
         T += n_q[r];
     }
-    if (T > 0x7fffffffLL / std::max(q_dim, kv_dim)) return fail(PKV_ERR_BAD_DIM, "batch too large");
+    // (the append numbers its warps, a page, a head and K or V each, in 32 bits)
+    if (T > 0x7fffffffLL / std::max(q_dim, kv_dim) ||
+        static_cast<int64_t>(pages.size()) * std::max(1, p->n_kv) > 0x3fffffffLL)
+        return fail(PKV_ERR_BAD_DIM, "batch too large");
 
     WorkList w;
     const int32_t S = g_split_keys.load();

@@ -75,3 +75,24 @@ def test_long_append_bit_exact(KV, hd, bs, pages, dtype):
         assert bool((pool.K[:, 0] == 255).all()) and bool(torch.isnan(pool.Vs[:, 0]).all())    # the other layer
     finally:
         pool.close()
+
+
+def test_more_warps_than_32_bits_count_are_refused():
+    """Pages of one token and a million heads of one element: refused before anything is read or launched."""
+    n, heads = 1025, 1 << 20
+    pool = pkv.pkv_pool_new_q8(n, 1, heads, 1, 1, max_seqs=1, max_blocks_per_seq=n, stream=torch.cuda.current_stream())
+    if not pool:
+        pytest.skip("11 GB of pool: " + pkv.pkv_last_error())
+    try:
+        s = pkv.pkv_seq_new(pool, n)
+        pkv.check(pkv.pkv_ensure_append(s, n))
+        rows = 4096     # no address: the call must not get as far
+        launches = pkv.pkv_launch_count()
+        assert pkv.pkv_append_layer(s, 0, rows, rows, n) == pkv.PKV_ERR_BAD_DIM, pkv.pkv_last_error()
+        assert pkv._lib.pkv_append_packed(pkv.seq_array([s]), 1, pkv.i32_array([n]), 0, rows, heads, rows, heads,
+                                          pkv.PKV_F32) == pkv.PKV_ERR_BAD_DIM
+        assert pkv.pkv_launch_count() == launches
+        assert pkv.pkv_sync_error(pool) == pkv.PKV_OK
+    finally:
+        torch.cuda.synchronize()
+        pkv.pkv_pool_free(pool)
