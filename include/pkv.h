@@ -455,6 +455,91 @@ PKV_API int pkv_attn_packed(const void *Q, int64_t q_stride, const void *K, int6
                             int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t causal,
                             float scale, void *out, int64_t out_stride, pkv_stream_t stream);
 
+/* Attention of packed queries over keys of other lengths, every key visible (no
+ * counterpart on the pages): a decoder's queries over an encoder's states, for
+ * whole prompts and for single tokens.  Sequence s owns q_lens[s] consecutive
+ * rows of Q and out, in order from row 0, and attends the k_lens[s] rows of K
+ * and V from row k_start[s] on (k_start NULL: the sequences' rows lie behind
+ * one another, in order).  Rows may be attended by several sequences (the beams
+ * of a request; neighbours with the same rows read them once):
+ *   out[i, h] = softmax_j(scale * <Q[i, h], K[j, kv(h)]>) V[j, kv(h)]
+ * over those rows, 0 where a sequence has none.  q_lens, k_lens, k_start: host
+ * arrays, entries >= 0.  Element types, strides and head grouping as for
+ * pkv_attn_packed; row counts up to 2^30.  Scores, softmax statistics and
+ * outputs accumulate in f32, and the output is rounded once.  A key row that a
+ * query does not see never reaches it, whatever it holds; one that it does see
+ * and that holds an infinity or a NaN makes outputs infinite or NaN.  Rows of
+ * out past the last sequence are left as they were; out may not overlap the
+ * inputs.
+ *
+ * workspace: device memory for partial results, 16-byte aligned, for work split
+ * over the keys where there are few queries.  pkv_attn_cross_workspace says how
+ * many bytes a call would like (-1 on bad arguments); with fewer, or none, it
+ * splits less and takes longer where it would have split.  The contents need
+ * not be kept or cleared between calls; calls that may run at the same time
+ * (other streams, captured graphs) need one each.  Nothing is uploaded or
+ * allocated; the call can be captured into a CUDA graph (the lengths are then
+ * part of the graph).  Runs on `stream` and the current device.  Checks, in order: lengths and
+ * sizes -> PKV_ERR_BAD_DIM, grouping -> PKV_ERR_BAD_GQA, dtype, strides,
+ * workspace, pointers -> PKV_ERR_ARG. */
+PKV_API int pkv_attn_cross(const void *Q, int64_t q_stride, const int32_t *q_lens, const void *K, int64_t k_stride,
+                           const void *V, int64_t v_stride, const int32_t *k_lens, const int32_t *k_start,
+                           int32_t dtype, int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                           float scale, void *out, int64_t out_stride, void *workspace, int64_t workspace_bytes,
+                           pkv_stream_t stream);
+PKV_API int64_t pkv_attn_cross_workspace(const int32_t *q_lens, const int32_t *k_lens, const int32_t *k_start,
+                                         int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
+
+/* Attention for a batch that shares a long prefix (no counterpart on the pages;
+ * the shared-prefix pass of pkv_attn_batch, see pkv_set_cascade, for packed
+ * 16-bit rows and any number of queries): every sequence sees the prefix_len
+ * rows of K_prefix and V_prefix, and behind them its own k_lens[s] rows of K and
+ * V, the last q_lens[s] of which belong to its queries.  Query i of sequence s
+ * attends the prefix and own rows j <= k_lens[s] - q_lens[s] + i.  k_lens[s] >=
+ * q_lens[s] (PKV_ERR_BAD_DIM); prefix_len 0 and sequences without queries are
+ * fine.  The prefix is read and multiplied once for the rows of all sequences
+ * that have few queries.  Everything else as for pkv_attn_cross. */
+PKV_API int pkv_attn_prefix(const void *Q, int64_t q_stride, const int32_t *q_lens, const void *K_prefix,
+                            int64_t kp_stride, const void *V_prefix, int64_t vp_stride, int32_t prefix_len,
+                            const void *K, int64_t k_stride, const void *V, int64_t v_stride, const int32_t *k_lens,
+                            const int32_t *k_start, int32_t dtype, int32_t n_seqs, int32_t n_heads,
+                            int32_t n_kv_heads, int32_t head_dim, float scale, void *out, int64_t out_stride,
+                            void *workspace, int64_t workspace_bytes, pkv_stream_t stream);
+PKV_API int64_t pkv_attn_prefix_workspace(int32_t prefix_len, const int32_t *q_lens, const int32_t *k_lens,
+                                          int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
+
+/* Which position a frequency pair turns by. */
+enum pkv_rope_order {
+    PKV_ROPE_BLOCKS = 0, /* the first pairs[0] pairs by axis 0, the next pairs[1] by axis 1, ... */
+    PKV_ROPE_TURNS = 1,  /* pair i by axis i mod n_axes while that axis has pairs left (i < n_axes *
+                            pairs[axis]), then by axis 0 */
+    PKV_ROPE_AXIAL = 2   /* as BLOCKS, each axis with a ramp of frequencies of its own */
+};
+
+/* Rotary positions with several axes (time, height and width of images and
+ * video; pkv_attn_batch_rope has one) on packed query and key rows.  Row t has
+ * a position on each of n_axes (1 to 4) axes, positions[axis * pos_stride + t]
+ * (device, int32, any sign).  With r the sum of pairs[] (host array), in every
+ * head and for i < r the pair (x[i], x[i + r]) turns by the angle p * f_i:
+ *   y[i] = x[i] cos - x[i + r] sin,  y[i + r] = x[i] sin + x[i + r] cos,
+ * p the row's position on pair i's axis (`order`), f_i = rope_base^(-i / r), or
+ * with PKV_ROPE_AXIAL rope_base^(-j / pairs[axis]) for the axis's j-th pair.
+ * Elements past 2 r of a head stay.  inverse != 0 turns back, by -p * f_i, which
+ * is also the gradient: the rows' gradients are the outputs' turned back.
+ * The angle is exact to 2^-52 of its own size at any position, its cosine and
+ * sine and the products are f32, and each result is rounded once to the type.
+ * dtype: PKV_F32, PKV_BF16 or PKV_F16 for all rows.  Strides in elements;
+ * outputs are other rows, or the inputs themselves (same address and stride).  Q or K
+ * may be NULL, with its output, and is then left out.  rope_base finite, >= 1.
+ * Needs no scratch, uploads nothing, can be captured into a CUDA graph.  Runs
+ * on `stream` and the current device.  Checks, in order: sizes ->
+ * PKV_ERR_BAD_DIM, dtype, order, base, strides, pointers -> PKV_ERR_ARG. */
+PKV_API int pkv_rope_packed(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, int32_t dtype,
+                            const int32_t *positions, int64_t pos_stride, int32_t n_axes, const int32_t *pairs,
+                            int32_t order, int32_t n_rows, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                            double rope_base, int32_t inverse, void *Q_out, int64_t qo_stride, void *K_out,
+                            int64_t ko_stride, pkv_stream_t stream);
+
 /* pkv_append_layer for a batch of sequences and rows of any type: writes n[r]
  * rows of K and V at positions len .. len + n[r] - 1 of sequence r, converted
  * to the pool's element as an append converts them (f32 -> itself, bf16, fp8

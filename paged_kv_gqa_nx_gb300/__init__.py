@@ -44,6 +44,10 @@ PKV_F32 = 0
 PKV_BF16 = 1
 PKV_F16 = 2
 
+PKV_ROPE_BLOCKS = 0
+PKV_ROPE_TURNS = 1
+PKV_ROPE_AXIAL = 2
+
 PKV_KERNEL_APPEND = 0
 PKV_KERNEL_DECODE = 1
 PKV_KERNEL_MERGE = 2
@@ -82,6 +86,14 @@ _SIGS = {
     "pkv_pool_v_scales": (_vp, [_vp]),
     "pkv_attn_packed": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i32, _pi32, _i32, _i32, _i32, _i32, _i32, _f32,
                                _vp, _i64, _vp]),
+    "pkv_attn_cross": (_int, [_vp, _i64, _pi32, _vp, _i64, _vp, _i64, _pi32, _pi32, _i32, _i32, _i32, _i32, _i32, _f32,
+                              _vp, _i64, _vp, _i64, _vp]),
+    "pkv_attn_cross_workspace": (_i64, [_pi32, _pi32, _pi32, _i32, _i32, _i32, _i32]),
+    "pkv_attn_prefix": (_int, [_vp, _i64, _pi32, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _pi32, _pi32, _i32,
+                               _i32, _i32, _i32, _i32, _f32, _vp, _i64, _vp, _i64, _vp]),
+    "pkv_attn_prefix_workspace": (_i64, [_i32, _pi32, _pi32, _i32, _i32, _i32, _i32]),
+    "pkv_rope_packed": (_int, [_vp, _i64, _vp, _i64, _i32, _vp, _i64, _i32, _pi32, _i32, _i32, _i32, _i32, _i32,
+                               ctypes.c_double, _i32, _vp, _i64, _vp, _i64, _vp]),
     "pkv_append_packed": (_int, [_vp, _i32, _pi32, _i32, _vp, _i64, _vp, _i64, _i32]),
     "pkv_read_packed": (_int, [_vp, _i32, _pi32, _pi32, _i32, _vp, _i64, _vp, _i64, _i32]),
     "pkv_pool_free": (None, [_vp]),
@@ -474,6 +486,123 @@ def pkv_attn_packed(Q, K, V, lens, n_heads, n_kv_heads, head_dim, causal, scale,
         raise TypeError("Q, K, V and out must have one element type")
     return _lib.pkv_attn_packed(q, qs, k, ks, v, vs, t, arr, n, n_heads, n_kv_heads, head_dim, causal,
                                 scale, o, os_, _stream(stream))
+
+
+def _workspace(t):
+    """(address, bytes) of a workspace: a contiguous CUDA tensor, or None."""
+    if t is None:
+        return None, 0
+    try:
+        if not t.is_cuda or not t.is_contiguous():
+            raise TypeError("workspace must be a contiguous CUDA tensor")
+        return t.data_ptr(), t.numel() * t.element_size()
+    except AttributeError:
+        raise TypeError("workspace must be a contiguous CUDA tensor") from None
+
+
+def _stretches(q_lens, k_lens, k_start):
+    """The lengths as int32 arrays, and the rows of Q and of K that they reach."""
+    q, k, n = _i32_array(q_lens), _i32_array(k_lens), len(q_lens)
+    if len(k_lens) != n or (k_start is not None and len(k_start) != n):
+        raise TypeError("q_lens, k_lens and k_start need an entry for each of the %d sequences" % n)
+    if k_start is None:
+        return q, k, None, n, _total(q, n), _total(k, n)
+    k0 = _i32_array(k_start)
+    reach = max((a + b for a, b in zip(k0[:n], k[:n]) if b > 0), default=0)
+    return q, k, k0, n, _total(q, n), reach
+
+
+def pkv_attn_cross_workspace(q_lens, k_lens, n_heads, n_kv_heads, head_dim, k_start=None):
+    """Bytes that pkv_attn_cross would like as workspace; -1 on bad arguments (pkv_last_error())."""
+    q, k, k0, n, _, _ = _stretches(q_lens, k_lens, k_start)
+    return _lib.pkv_attn_cross_workspace(q, k, k0, n, n_heads, n_kv_heads, head_dim)
+
+
+def pkv_attn_cross(Q, q_lens, K, V, k_lens, n_heads, n_kv_heads, head_dim, scale, out, k_start=None,
+                   workspace=None, stream=None):
+    """Q, out: [tokens, n_heads * head_dim], K, V: [key rows, n_kv_heads * head_dim], bfloat16 or float16
+    CUDA tensors with contiguous rows (any row stride); q_lens, k_lens: queries and keys per sequence;
+    k_start: first key row of each (None: behind one another); workspace: a CUDA tensor of
+    pkv_attn_cross_workspace bytes (or fewer, or None)."""
+    ql, kl, k0, n, nq, nk = _stretches(q_lens, k_lens, k_start)
+    _same_device(Q, K, V, out)
+    q, qs, t, _ = _rows(Q, "Q", nq, n_heads * head_dim)
+    k, ks, tk, _ = _rows(K, "K", nk, n_kv_heads * head_dim)
+    v, vs, tv, _ = _rows(V, "V", nk, n_kv_heads * head_dim)
+    o, os_, to, _ = _rows(out, "out", nq, n_heads * head_dim)
+    if not t == tk == tv == to:
+        raise TypeError("Q, K, V and out must have one element type")
+    w, wn = _workspace(workspace)
+    if w is not None and workspace.get_device() != Q.get_device():
+        raise TypeError("the workspace must be on the tensors' device")
+    return _lib.pkv_attn_cross(q, qs, ql, k, ks, v, vs, kl, k0, t, n, n_heads, n_kv_heads, head_dim, scale, o, os_,
+                               w, wn, _stream(stream))
+
+
+def pkv_attn_prefix_workspace(prefix_len, q_lens, k_lens, n_heads, n_kv_heads, head_dim):
+    """Bytes that pkv_attn_prefix would like as workspace; -1 on bad arguments (pkv_last_error())."""
+    q, k, _, n, _, _ = _stretches(q_lens, k_lens, None)
+    return _lib.pkv_attn_prefix_workspace(prefix_len, q, k, n, n_heads, n_kv_heads, head_dim)
+
+
+def pkv_attn_prefix(Q, q_lens, K_prefix, V_prefix, K, V, k_lens, n_heads, n_kv_heads, head_dim, scale, out,
+                    k_start=None, workspace=None, stream=None):
+    """As pkv_attn_cross; K_prefix, V_prefix: [prefix rows, n_kv_heads * head_dim], seen by every sequence;
+    k_lens counts a sequence's own keys, the last q_lens of which belong to its queries."""
+    ql, kl, k0, n, nq, nk = _stretches(q_lens, k_lens, k_start)
+    _same_device(Q, K, V, out)
+    _same_device(Q, K_prefix, V_prefix, out)
+    q, qs, t, _ = _rows(Q, "Q", nq, n_heads * head_dim)
+    k, ks, tk, _ = _rows(K, "K", nk, n_kv_heads * head_dim)
+    v, vs, tv, _ = _rows(V, "V", nk, n_kv_heads * head_dim)
+    p, ps, tp, _ = _rows(K_prefix, "K_prefix", 0, n_kv_heads * head_dim)
+    x, xs, tx, _ = _rows(V_prefix, "V_prefix", 0, n_kv_heads * head_dim)
+    o, os_, to, _ = _rows(out, "out", nq, n_heads * head_dim)
+    if not t == tk == tv == tp == tx == to:
+        raise TypeError("Q, K, V, the prefix and out must have one element type")
+    if K_prefix.shape[0] != V_prefix.shape[0]:
+        raise TypeError("K_prefix and V_prefix must have the same rows")
+    w, wn = _workspace(workspace)
+    if w is not None and workspace.get_device() != Q.get_device():
+        raise TypeError("the workspace must be on the tensors' device")
+    return _lib.pkv_attn_prefix(q, qs, ql, p, ps, x, xs, K_prefix.shape[0], k, ks, v, vs, kl, k0, t, n, n_heads,
+                                n_kv_heads, head_dim, scale, o, os_, w, wn, _stream(stream))
+
+
+def pkv_rope_packed(Q, K, positions, pairs, order, n_heads, n_kv_heads, head_dim, rope_base, Q_out, K_out,
+                    inverse=False, stream=None):
+    """Q, Q_out: [tokens, n_heads * head_dim], K, K_out: [tokens, n_kv_heads * head_dim], float32, bfloat16 or
+    float16 CUDA tensors with contiguous rows (Q or K may be None, with its output; an output may be its
+    input); positions: int32 CUDA tensor [axes, tokens]; pairs: frequency pairs of each axis; order:
+    PKV_ROPE_BLOCKS, PKV_ROPE_TURNS or PKV_ROPE_AXIAL; inverse turns back (the gradient)."""
+    arr = _i32_array(pairs)
+    try:
+        (axes, rows), (pos_stride, inner) = positions.shape, positions.stride()
+        good = positions.is_cuda and str(positions.dtype) == "torch.int32" and (inner == 1 or rows <= 1)
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        raise TypeError("positions must be an int32 CUDA tensor [axes, tokens] with contiguous rows")
+    if axes != len(pairs):
+        raise TypeError("positions has %d axes, pairs %d" % (axes, len(pairs)))
+    q = k = qo = ko = None
+    qs = ks = qos = kos = 0
+    kinds = set()
+    if Q is not None or Q_out is not None:
+        _same_device(positions, Q, Q_out, positions)
+        q, qs, t, _ = _rows(Q, "Q", rows, n_heads * head_dim)
+        qo, qos, to, _ = _rows(Q_out, "Q_out", rows, n_heads * head_dim)
+        kinds.update((t, to))
+    if K is not None or K_out is not None:
+        _same_device(positions, K, K_out, positions)
+        k, ks, t, _ = _rows(K, "K", rows, n_kv_heads * head_dim)
+        ko, kos, to, _ = _rows(K_out, "K_out", rows, n_kv_heads * head_dim)
+        kinds.update((t, to))
+    if len(kinds) > 1:
+        raise TypeError("the rows must have one element type")
+    return _lib.pkv_rope_packed(q, qs, k, ks, kinds.pop() if kinds else PKV_F32, positions.data_ptr(),
+                                max(pos_stride, rows), axes, arr, order, rows, n_heads, n_kv_heads, head_dim,
+                                float(rope_base), 1 if inverse else 0, qo, qos, ko, kos, _stream(stream))
 
 
 def pkv_append_packed(seqs, n, layer, K, V):

@@ -1,0 +1,84 @@
+// pkv_ragged.h -- attention of packed 16-bit query rows over keys of other
+// lengths (cross attention, a shared prefix): what the host plan
+// (pkv_ragged_host.cpp) hands to the kernels.
+//
+// A call's sequences become runs: consecutive query rows that attend the same
+// stretch of key rows, with the shared prefix before it where a launch has one.
+// A run's keys may be split; each (query, split) then leaves a partial record
+// (maximum, sum, unnormalised output of every head) in the caller's workspace
+// and the join launch combines them.
+#pragma once
+
+#include "pkv_internal.h"
+
+namespace pkv {
+
+constexpr int32_t kSees = 0x3fffffff;  // `off` of a run whose queries see every key
+
+struct RaggedRun {
+    int32_t q0, nq;    // first row of Q and out, queries
+    int32_t k0, nk;    // first key row, keys
+    int32_t off;       // query i sees the run's keys j <= off + i
+    int32_t ns;        // splits of the prefix and the run's keys together
+    int32_t rec0;      // record of (query i, split x): rec0 + i * ns + x; -1: one split, written to out
+};
+
+// A query's records: ns of its own keys and pns of the shared prefix.
+struct JoinRun {
+    int32_t q0, nq, rec0, ns, pre0, pns;
+};
+
+// Lists travel in the launch's parameters (no upload), in two sizes as a
+// launch takes longer with more of them.
+constexpr int32_t kRaggedSmall = 64, kRaggedLarge = 900;
+template <class R, int N>
+struct RunList {
+    int32_t n;
+    int32_t unit0[N + 1];  // units of the runs before it
+    R run[N];
+};
+
+struct RaggedArgs {
+    const void *Q, *K, *V;
+    void *out;
+    int64_t q_stride, k_stride, v_stride, o_stride;  // elements per row
+    const void *Kp, *Vp;                              // the shared prefix
+    int64_t kp_stride, vp_stride;
+    int32_t n_pre;                                    // its rows (0: none)
+    int32_t n_heads, n_kv, hd;
+    float scale_log2;
+    Elem type;
+    float *pm, *pl, *pacc;                            // records: [rec][head], [rec][head], [rec][head][hd]
+    int32_t *err;
+    bool vec;       // rows on 16-byte boundaries, heads of whole 16 bytes
+    bool overlap;   // the launch may start before the one in front of it on the stream has ended
+};
+
+// Key rows by warp-level MMAs (pkv_ragged_rows.cu): units of 16 * wide query
+// rows (query, head of the group) of one kv head.
+cudaError_t launch_ragged_rows(const RaggedArgs &a, const RaggedRun *runs, int32_t n, int wide, cudaStream_t s);
+__host__ __device__ constexpr int32_t ragged_row_units(int32_t rows, int wide) { return (rows + 16 * wide - 1) / (16 * wide); }
+cudaError_t launch_ragged_join(const RaggedArgs &a, const JoinRun *runs, int32_t n, cudaStream_t s);
+
+// Rotary positions with several axes (pkv_rope.cu).
+constexpr int32_t kRopeAxes = 4, kRopePairs = 128;
+struct RopePacked {
+    const void *src[2];        // Q, K
+    void *dst[2];
+    int64_t src_stride[2], dst_stride[2];
+    int32_t heads[2];          // 0: left out
+    const int32_t *pos;        // [axis][row]
+    int64_t pos_stride;
+    int32_t n_rows, hd, n_pairs, inverse;
+    Elem type;
+    bool vec;
+    uint64_t step[kRopePairs]; // turns a position, as a fraction of 2^64
+    uint8_t axis[kRopePairs];
+};
+cudaError_t launch_rope_packed(const RopePacked &a, cudaStream_t s);
+
+// pkv_host.cpp: the current device's error word of calls without a pool (its
+// set-up, at the first use, cannot be captured).
+int contiguous_error_word(cudaStream_t s, int32_t **out);
+
+}  // namespace pkv

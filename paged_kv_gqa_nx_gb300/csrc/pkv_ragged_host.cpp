@@ -1,0 +1,446 @@
+// pkv_ragged_host.cpp -- entry points of cross attention, shared-prefix
+// attention and multi-axis rotary positions: argument checks, the plan of a
+// call (which sequences run on which kernel, how their keys are split, where
+// partial records go) and its launches.
+#include "../../include/pkv.h"
+#include "pkv_ragged.h"
+
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <exception>
+#include <vector>
+
+using namespace pkv;
+
+namespace {
+
+constexpr int64_t kMaxRows = int64_t{1} << 30;   // query rows, and key rows, of a call
+constexpr int32_t kSMs = 152;
+
+int refuse(int code, const char *fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return report_error(code, buf);
+}
+
+template <class F>
+int guarded(F &&f) {
+    try {
+        return f();
+    } catch (const std::exception &) {
+        return report_error(PKV_ERR_ARG, "out of host memory");
+    }
+}
+
+template <class F>
+int counted(int kind, cudaStream_t s, const char *what, F &&f) {
+    const cudaError_t e = launch_counted(kind, s, [](void *ctx) { return (*static_cast<std::remove_reference_t<F> *>(ctx))(); }, &f);
+    return e == cudaSuccess ? PKV_OK : refuse(PKV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// ------------------------------------------------------------------ plan ----
+
+struct Shape {
+    int32_t n_heads, n_kv, hd;
+    int32_t group() const { return n_heads / n_kv; }
+};
+
+// One sequence of a call, or several in a row that see the same keys.
+struct Seq {
+    int32_t q0, nq, k0, nk, off;
+};
+
+struct Plan {
+    std::vector<RaggedRun> rows;      // own keys (behind the prefix, unless stacked)
+    std::vector<RaggedRun> rows_pre;  // the prefix, for stacked sequences
+    std::vector<JoinRun> joins;
+    int64_t n_rec = 0;
+    bool stacked = false;
+    int wide = 1, wide_pre = 1;
+};
+
+int64_t record_bytes(int64_t n_rec, const Shape &sh) {
+    return 4 * (2 * static_cast<int64_t>(record_floats(n_rec, sh.n_heads)) + n_rec * sh.n_heads * sh.hd);
+}
+
+// Query rows a unit of the row kernel takes, in sixteens: two where that saves
+// a third of the reads of K and V.
+int pick_wide(const std::vector<RaggedRun> &runs, const Shape &sh) {
+    if (sh.hd > 128) return 1;
+    int64_t one = 0, two = 0;
+    for (const RaggedRun &r : runs) {
+        one += ragged_row_units(r.nq * sh.group(), 1);
+        two += ragged_row_units(r.nq * sh.group(), 2);
+    }
+    return 3 * two <= 2 * one ? 2 : 1;
+}
+
+// Splits of the row kernel: as many keys a split as give the GPU's resident
+// blocks (two a SM, one of wide heads) about three units each, so that the last
+// ones are a small part of the whole; `coarse` times as many where the workspace
+// is short.  A unit of fewer than 256 keys (64 a warp) is mostly latency.
+void split_rows(std::vector<RaggedRun> &runs, const Shape &sh, int wide, int64_t n_pre, int64_t coarse) {
+    int64_t work = 0;
+    auto keys = [&](const RaggedRun &r) { return n_pre + r.nk; };
+    for (const RaggedRun &r : runs) work += static_cast<int64_t>(ragged_row_units(r.nq * sh.group(), wide)) * sh.n_kv * keys(r);
+    const int64_t units = static_cast<int64_t>(kSMs) * (sh.hd > 128 ? 1 : 2) * 3;
+    const int64_t per = std::max<int64_t>(256, (work + units - 1) / units) * coarse;
+    for (RaggedRun &r : runs) r.ns = static_cast<int32_t>(std::clamp<int64_t>((keys(r) + per - 1) / per, 1, 128));
+}
+
+// The plan of up to kRaggedLarge sequences; with less workspace than it would
+// like, keys are split less, or not at all.
+Plan make_plan(const std::vector<Seq> &seqs, const Shape &sh, int32_t n_pre, int64_t workspace) {
+    constexpr int64_t kCoarsest = int64_t{1} << 24;
+    for (int64_t coarse = workspace < record_bytes(1, sh) ? 2 * kCoarsest : 1;; coarse *= 2) {
+        const bool last = coarse > kCoarsest;
+        Plan p;
+        p.stacked = !last && n_pre >= 128 && seqs.size() > 1;
+        for (const Seq &s : seqs) p.rows.push_back(RaggedRun{s.q0, s.nq, s.k0, s.nk, s.off, 1, -1});
+        p.wide = pick_wide(p.rows, sh);
+        if (!last) split_rows(p.rows, sh, p.wide, p.stacked ? 0 : n_pre, coarse);
+        if (p.stacked) {
+            for (const Seq &s : seqs) {
+                if (!p.rows_pre.empty() && p.rows_pre.back().q0 + p.rows_pre.back().nq == s.q0) p.rows_pre.back().nq += s.nq;
+                else p.rows_pre.push_back(RaggedRun{s.q0, s.nq, 0, n_pre, kSees, 1, -1});
+            }
+            p.wide_pre = pick_wide(p.rows_pre, sh);
+            split_rows(p.rows_pre, sh, p.wide_pre, 0, coarse);
+        }
+        // records: of the prefix run by run, of own keys sequence by sequence
+        int64_t at = 0;
+        auto records = [&](RaggedRun &r) {
+            r.rec0 = static_cast<int32_t>(std::min<int64_t>(at, 0x7fffffff));
+            at += static_cast<int64_t>(r.nq) * r.ns;
+        };
+        for (RaggedRun &r : p.rows_pre) records(r);
+        size_t pre = 0;
+        for (RaggedRun &r : p.rows) {
+            if (!p.stacked && r.ns == 1) continue;
+            records(r);
+            JoinRun j{r.q0, r.nq, r.rec0, r.ns, 0, 0};
+            if (p.stacked) {
+                while (p.rows_pre[pre].q0 + p.rows_pre[pre].nq <= r.q0) ++pre;
+                const RaggedRun &b = p.rows_pre[pre];
+                j.pre0 = b.rec0 + (r.q0 - b.q0) * b.ns;
+                j.pns = b.ns;
+            }
+            p.joins.push_back(j);
+        }
+        p.n_rec = at;
+        if (at == 0 || (at <= 0x7fffffff && record_bytes(at, sh) <= workspace)) return p;
+    }
+}
+
+// ------------------------------------------------------------------ calls ----
+
+struct Call {
+    const void *Q, *K, *V, *Kp, *Vp;
+    void *out;
+    int64_t q_stride, k_stride, v_stride, kp_stride, vp_stride, o_stride;
+    int32_t dtype, n_pre;
+    bool causal;  // own keys j <= k_len - q_len + i; otherwise all
+    const int32_t *q_lens, *k_lens, *k_start;
+    int32_t n_seqs;
+    Shape sh;
+    float scale;
+    void *workspace;
+    int64_t workspace_bytes;
+};
+
+// Sizes and grouping of a call, and its sequences with queries.
+int sequences(const Call &c, std::vector<Seq> &seqs, bool *keys) {
+    if (c.n_seqs <= 0 || !c.q_lens || !c.k_lens)
+        return refuse(PKV_ERR_BAD_DIM, "n_seqs must be positive and the lengths non-NULL");
+    if (c.sh.n_heads <= 0 || c.sh.n_kv <= 0 || c.sh.hd <= 0)
+        return refuse(PKV_ERR_BAD_DIM, "n_heads, n_kv_heads and head_dim must be positive");
+    if (c.sh.hd > kMaxHeadDim) return refuse(PKV_ERR_BAD_DIM, "head_dim %d > %d is not supported", c.sh.hd, kMaxHeadDim);
+    if (c.n_pre < 0 || c.n_pre > kMaxRows - 256) return refuse(PKV_ERR_BAD_DIM, "a prefix of %d rows", c.n_pre);
+    int64_t q = 0, k = 0;
+    *keys = false;
+    for (int32_t s = 0; s < c.n_seqs; ++s) {
+        const int32_t nq = c.q_lens[s], nk = c.k_lens[s];
+        if (nq < 0 || nk < 0) return refuse(PKV_ERR_BAD_DIM, "sequence %d has a negative length", s);
+        if (c.causal && nq > nk)
+            return refuse(PKV_ERR_BAD_DIM, "sequence %d has %d queries and %d keys of its own: its queries' keys come last among them", s, nq, nk);
+        const int64_t k0 = c.k_start ? c.k_start[s] : k;
+        if (k0 < 0 || k0 + nk > kMaxRows - 256) return refuse(PKV_ERR_BAD_DIM, "sequence %d: key rows %lld and on", s, static_cast<long long>(k0));
+        if (q + nq > kMaxRows) return refuse(PKV_ERR_BAD_DIM, "too many query rows");
+        if (nq > 0) {
+            const Seq x{static_cast<int32_t>(q), nq, static_cast<int32_t>(k0), nk, c.causal ? nk - nq : kSees};
+            // neighbours that see the same keys (beams of one request) are one
+            if (!c.causal && !seqs.empty() && seqs.back().k0 == x.k0 && seqs.back().nk == nk) seqs.back().nq += nq;
+            else seqs.push_back(x);
+            *keys = *keys || nk > 0;
+        }
+        q += nq;
+        k += nk;
+    }
+    if (q * c.sh.n_heads > 0x7fff0000LL) return refuse(PKV_ERR_BAD_DIM, "%lld query rows of %d heads are too many", static_cast<long long>(q), c.sh.n_heads);
+    if (static_cast<int64_t>(c.sh.n_heads) * c.sh.hd > 0x7fffffffLL) return refuse(PKV_ERR_BAD_DIM, "n_heads * head_dim too large");
+    if (c.sh.n_heads % c.sh.n_kv != 0)
+        return refuse(PKV_ERR_BAD_GQA, "n_heads (%d) is not a multiple of n_kv_heads (%d)", c.sh.n_heads, c.sh.n_kv);
+    return PKV_OK;
+}
+
+template <class F>
+int each_chunk(const std::vector<Seq> &seqs, F &&f) {
+    for (size_t i = 0; i < seqs.size(); i += kRaggedLarge) {
+        const size_t n = std::min<size_t>(kRaggedLarge, seqs.size() - i);
+        const int rc = f(std::vector<Seq>(seqs.begin() + i, seqs.begin() + i + n));
+        if (rc) return rc;
+    }
+    return PKV_OK;
+}
+
+int64_t workspace_of(const Call &c) {
+    std::vector<Seq> seqs;
+    bool keys;
+    if (sequences(c, seqs, &keys)) return -1;
+    int64_t most = 0;
+    each_chunk(seqs, [&](const std::vector<Seq> &part) {
+        most = std::max(most, record_bytes(make_plan(part, c.sh, c.n_pre, int64_t{1} << 62).n_rec, c.sh));
+        return PKV_OK;
+    });
+    return most;
+}
+
+int attend(const Call &c, cudaStream_t st) {
+    std::vector<Seq> seqs;
+    bool keys;
+    int rc = sequences(c, seqs, &keys);
+    if (rc) return rc;
+    if (c.dtype != PKV_BF16 && c.dtype != PKV_F16) return refuse(PKV_ERR_ARG, "packed attention takes PKV_BF16 or PKV_F16 rows");
+    const int64_t q_dim = static_cast<int64_t>(c.sh.n_heads) * c.sh.hd, kv_dim = static_cast<int64_t>(c.sh.n_kv) * c.sh.hd;
+    if (c.q_stride < q_dim || c.o_stride < q_dim || c.k_stride < kv_dim || c.v_stride < kv_dim ||
+        (c.n_pre > 0 && (c.kp_stride < kv_dim || c.vp_stride < kv_dim)))
+        return refuse(PKV_ERR_ARG, "a row stride below the row's width makes rows overlap");
+    if (std::max({c.q_stride, c.o_stride, c.k_stride, c.v_stride, c.kp_stride, c.vp_stride}) > (int64_t{1} << 32))
+        return refuse(PKV_ERR_BAD_DIM, "row stride too large");
+    if (c.workspace_bytes < 0 || (c.workspace_bytes > 0 && !c.workspace)) return refuse(PKV_ERR_ARG, "workspace");
+    if (reinterpret_cast<uintptr_t>(c.workspace) % 16 != 0) return refuse(PKV_ERR_ARG, "the workspace must be aligned to 16 bytes");
+    if (seqs.empty()) return PKV_OK;
+    if (!c.Q || !c.out || (keys && (!c.K || !c.V)) || (c.n_pre > 0 && (!c.Kp || !c.Vp)))
+        return refuse(PKV_ERR_ARG, "NULL data pointer");
+    for (const void *p : {c.Q, c.K, c.V, c.Kp, c.Vp, static_cast<const void *>(c.out)})
+        if (reinterpret_cast<uintptr_t>(p) % 2 != 0) return refuse(PKV_ERR_ARG, "rows must be aligned to their element");
+
+    RaggedArgs a{};
+    a.Q = c.Q;
+    a.K = c.K;
+    a.V = c.V;
+    a.out = c.out;
+    a.q_stride = c.q_stride;
+    a.k_stride = c.k_stride;
+    a.v_stride = c.v_stride;
+    a.o_stride = c.o_stride;
+    a.Kp = c.Kp;
+    a.Vp = c.Vp;
+    a.kp_stride = c.kp_stride;
+    a.vp_stride = c.vp_stride;
+    a.n_heads = c.sh.n_heads;
+    a.n_kv = c.sh.n_kv;
+    a.hd = c.sh.hd;
+    a.scale_log2 = c.scale * 1.4426950408889634f;
+    a.type = c.dtype == PKV_BF16 ? Elem::bf16 : Elem::f16;
+    auto whole = [](const void *p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0; };
+    a.vec = c.sh.hd % 8 == 0 && whole(c.Q, c.q_stride) && whole(c.K, c.k_stride) && whole(c.V, c.v_stride) &&
+            whole(c.out, c.o_stride) && (c.n_pre == 0 || (whole(c.Kp, c.kp_stride) && whole(c.Vp, c.vp_stride)));
+    return each_chunk(seqs, [&](const std::vector<Seq> &part) {
+        const Plan p = make_plan(part, c.sh, c.n_pre, c.workspace_bytes);
+        a.pm = static_cast<float *>(c.workspace);
+        a.pl = a.pm + record_floats(p.n_rec, c.sh.n_heads);
+        a.pacc = a.pl + record_floats(p.n_rec, c.sh.n_heads);
+        bool first = true;
+        auto rows = [&](RaggedArgs b, const std::vector<RaggedRun> &runs, int wide) {
+            if (runs.empty()) return static_cast<int>(PKV_OK);
+            b.overlap = !first;
+            first = false;
+            return counted(PKV_KERNEL_DECODE, st, "ragged attention kernel",
+                           [&] { return launch_ragged_rows(b, runs.data(), static_cast<int32_t>(runs.size()), wide, st); });
+        };
+        RaggedArgs pre = a;
+        pre.K = c.Kp;
+        pre.V = c.Vp;
+        pre.k_stride = c.kp_stride;
+        pre.v_stride = c.vp_stride;
+        int r = rows(pre, p.rows_pre, p.wide_pre);
+        if (r) return r;
+        RaggedArgs own = a;
+        own.n_pre = p.stacked ? 0 : c.n_pre;
+        r = rows(own, p.rows, p.wide);
+        if (r || p.joins.empty()) return r;
+        return counted(PKV_KERNEL_MERGE, st, "ragged join kernel",
+                       [&] { return launch_ragged_join(a, p.joins.data(), static_cast<int32_t>(p.joins.size()), st); });
+    });
+}
+
+// ------------------------------------------------------------------- rope ----
+
+int rope(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, int32_t dtype, const int32_t *pos,
+         int64_t pos_stride, int32_t n_axes, const int32_t *pairs, int32_t order, int32_t n_rows, int32_t n_heads,
+         int32_t n_kv_heads, int32_t head_dim, double base, int32_t inverse, void *Q_out, int64_t qo_stride, void *K_out,
+         int64_t ko_stride, cudaStream_t st) {
+    if (n_rows < 0 || n_rows > kMaxRows) return refuse(PKV_ERR_BAD_DIM, "%d rows", n_rows);
+    if (n_axes <= 0 || n_axes > kRopeAxes || !pairs) return refuse(PKV_ERR_BAD_DIM, "one to %d axes, with their pairs", kRopeAxes);
+    if ((Q && n_heads <= 0) || (K && n_kv_heads <= 0) || head_dim <= 0)
+        return refuse(PKV_ERR_BAD_DIM, "n_heads, n_kv_heads and head_dim must be positive");
+    if (head_dim > kMaxHeadDim) return refuse(PKV_ERR_BAD_DIM, "head_dim %d > %d is not supported", head_dim, kMaxHeadDim);
+    int64_t total = 0;
+    for (int32_t a = 0; a < n_axes; ++a) {
+        if (pairs[a] < 0) return refuse(PKV_ERR_BAD_DIM, "axis %d has %d pairs", a, pairs[a]);
+        total += pairs[a];
+    }
+    if (total <= 0 || 2 * total > head_dim)
+        return refuse(PKV_ERR_BAD_DIM, "%lld pairs in heads of %d", static_cast<long long>(total), head_dim);
+    const int64_t q_dim = Q ? static_cast<int64_t>(n_heads) * head_dim : 0, k_dim = K ? static_cast<int64_t>(n_kv_heads) * head_dim : 0;
+    if (q_dim + k_dim > (1 << 26)) return refuse(PKV_ERR_BAD_DIM, "heads * head_dim too large");
+    if (dtype != PKV_F32 && dtype != PKV_BF16 && dtype != PKV_F16) return refuse(PKV_ERR_ARG, "unknown dtype %d", dtype);
+    if (order != PKV_ROPE_BLOCKS && order != PKV_ROPE_TURNS && order != PKV_ROPE_AXIAL) return refuse(PKV_ERR_ARG, "unknown order %d", order);
+    if (!(base >= 1.0) || !std::isfinite(base)) return refuse(PKV_ERR_ARG, "rope_base must be finite and at least 1");
+    const int32_t n = static_cast<int32_t>(total);
+
+    RopePacked a{};
+    int32_t count[kRopeAxes] = {};
+    for (int32_t i = 0, axis = 0, first = 0; i < n; ++i) {
+        while (i >= first + pairs[axis]) first += pairs[axis++];
+        int32_t mine = axis, number = i, ramp = n;
+        if (order == PKV_ROPE_TURNS) {
+            mine = i % n_axes;
+            if (i >= static_cast<int64_t>(n_axes) * pairs[mine]) mine = 0;
+        } else if (order == PKV_ROPE_AXIAL) {
+            number = i - first;
+            ramp = pairs[axis];
+        }
+        ++count[mine];
+        a.axis[i] = static_cast<uint8_t>(mine);
+        a.step[i] = static_cast<uint64_t>(std::ldexp(std::pow(base, -static_cast<double>(number) / ramp) / 6.283185307179586477, 64));
+    }
+    for (int32_t x = 0; x < n_axes; ++x)
+        if (count[x] != pairs[x])
+            return refuse(PKV_ERR_BAD_DIM, "pairs dealt in turn give axis %d %d of them, not %d", x, count[x], pairs[x]);
+
+    if ((Q && (q_stride < q_dim || qo_stride < q_dim)) || (K && (k_stride < k_dim || ko_stride < k_dim)))
+        return refuse(PKV_ERR_ARG, "a row stride below the row's width makes rows overlap");
+    if (std::max({q_stride, k_stride, qo_stride, ko_stride, pos_stride}) > (int64_t{1} << 32)) return refuse(PKV_ERR_BAD_DIM, "row stride too large");
+    if (n_axes > 1 && pos_stride < n_rows) return refuse(PKV_ERR_ARG, "the axes' positions overlap");
+    if (n_rows == 0) return PKV_OK;
+    if ((!Q && !K) || !pos || (Q && !Q_out) || (K && !K_out) || (!Q && Q_out) || (!K && K_out))
+        return refuse(PKV_ERR_ARG, "NULL data pointer (a left out part has neither rows nor a place for them)");
+    const uintptr_t size = dtype == PKV_F32 ? 4 : 2;
+    for (const void *p : {Q, K, static_cast<const void *>(Q_out), static_cast<const void *>(K_out)})
+        if (reinterpret_cast<uintptr_t>(p) % size != 0) return refuse(PKV_ERR_ARG, "rows must be aligned to their element");
+    if (reinterpret_cast<uintptr_t>(pos) % 4 != 0) return refuse(PKV_ERR_ARG, "positions must be aligned to 4 bytes");
+    if ((Q && Q == Q_out && q_stride != qo_stride) || (K && K == K_out && k_stride != ko_stride))
+        return refuse(PKV_ERR_ARG, "rows turned in place keep their stride");
+    a.src[0] = Q;
+    a.src[1] = K;
+    a.dst[0] = Q_out;
+    a.dst[1] = K_out;
+    a.src_stride[0] = q_stride;
+    a.src_stride[1] = k_stride;
+    a.dst_stride[0] = qo_stride;
+    a.dst_stride[1] = ko_stride;
+    a.heads[0] = Q ? n_heads : 0;
+    a.heads[1] = K ? n_kv_heads : 0;
+    a.pos = pos;
+    a.pos_stride = n_axes > 1 ? pos_stride : 0;
+    a.n_rows = n_rows;
+    a.hd = head_dim;
+    a.n_pairs = n;
+    a.inverse = inverse ? 1 : 0;
+    a.type = dtype == PKV_F32 ? Elem::f32 : dtype == PKV_BF16 ? Elem::bf16 : Elem::f16;
+    return counted(PKV_KERNEL_APPEND, st, "rotary kernel", [&] { return launch_rope_packed(a, st); });
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t pkv_attn_cross_workspace(const int32_t *q_lens, const int32_t *k_lens, const int32_t *k_start, int32_t n_seqs,
+                                 int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
+    int64_t n = -1;
+    const int rc = guarded([&] {
+        Call c{};
+        c.q_lens = q_lens;
+        c.k_lens = k_lens;
+        c.k_start = k_start;
+        c.n_seqs = n_seqs;
+        c.sh = Shape{n_heads, n_kv_heads, head_dim};
+        n = workspace_of(c);
+        return static_cast<int>(PKV_OK);
+    });
+    return rc ? -1 : n;
+}
+
+int64_t pkv_attn_prefix_workspace(int32_t prefix_len, const int32_t *q_lens, const int32_t *k_lens, int32_t n_seqs,
+                                  int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
+    int64_t n = -1;
+    const int rc = guarded([&] {
+        Call c{};
+        c.n_pre = prefix_len;
+        c.causal = true;
+        c.q_lens = q_lens;
+        c.k_lens = k_lens;
+        c.n_seqs = n_seqs;
+        c.sh = Shape{n_heads, n_kv_heads, head_dim};
+        n = workspace_of(c);
+        return static_cast<int>(PKV_OK);
+    });
+    return rc ? -1 : n;
+}
+
+int pkv_attn_cross(const void *Q, int64_t q_stride, const int32_t *q_lens, const void *K, int64_t k_stride,
+                   const void *V, int64_t v_stride, const int32_t *k_lens, const int32_t *k_start, int32_t dtype,
+                   int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float scale, void *out,
+                   int64_t out_stride, void *workspace, int64_t workspace_bytes, pkv_stream_t stream) {
+    return guarded([&] {
+        Call c{};
+        c.Q = Q, c.K = K, c.V = V, c.out = out;
+        c.q_stride = q_stride, c.k_stride = k_stride, c.v_stride = v_stride, c.o_stride = out_stride;
+        c.dtype = dtype;
+        c.q_lens = q_lens, c.k_lens = k_lens, c.k_start = k_start, c.n_seqs = n_seqs;
+        c.sh = Shape{n_heads, n_kv_heads, head_dim};
+        c.scale = scale;
+        c.workspace = workspace, c.workspace_bytes = workspace_bytes;
+        return attend(c, static_cast<cudaStream_t>(stream));
+    });
+}
+
+int pkv_attn_prefix(const void *Q, int64_t q_stride, const int32_t *q_lens, const void *K_prefix, int64_t kp_stride,
+                    const void *V_prefix, int64_t vp_stride, int32_t prefix_len, const void *K, int64_t k_stride,
+                    const void *V, int64_t v_stride, const int32_t *k_lens, const int32_t *k_start, int32_t dtype,
+                    int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float scale, void *out,
+                    int64_t out_stride, void *workspace, int64_t workspace_bytes, pkv_stream_t stream) {
+    return guarded([&] {
+        Call c{};
+        c.Q = Q, c.K = K, c.V = V, c.Kp = K_prefix, c.Vp = V_prefix, c.out = out;
+        c.q_stride = q_stride, c.k_stride = k_stride, c.v_stride = v_stride, c.o_stride = out_stride;
+        c.kp_stride = kp_stride, c.vp_stride = vp_stride;
+        c.dtype = dtype;
+        c.n_pre = prefix_len;
+        c.causal = true;
+        c.q_lens = q_lens, c.k_lens = k_lens, c.k_start = k_start, c.n_seqs = n_seqs;
+        c.sh = Shape{n_heads, n_kv_heads, head_dim};
+        c.scale = scale;
+        c.workspace = workspace, c.workspace_bytes = workspace_bytes;
+        return attend(c, static_cast<cudaStream_t>(stream));
+    });
+}
+
+int pkv_rope_packed(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, int32_t dtype,
+                    const int32_t *positions, int64_t pos_stride, int32_t n_axes, const int32_t *pairs, int32_t order,
+                    int32_t n_rows, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, double rope_base,
+                    int32_t inverse, void *Q_out, int64_t qo_stride, void *K_out, int64_t ko_stride, pkv_stream_t stream) {
+    return guarded([&] {
+        return rope(Q, q_stride, K, k_stride, dtype, positions, pos_stride, n_axes, pairs, order, n_rows, n_heads, n_kv_heads,
+                    head_dim, rope_base, inverse, Q_out, qo_stride, K_out, ko_stride, static_cast<cudaStream_t>(stream));
+    });
+}
+
+}  // extern "C"

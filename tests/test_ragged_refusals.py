@@ -1,0 +1,107 @@
+"""Refusals of the cross, shared-prefix and multi-axis rotary entry points (CPU: every check comes before any CUDA call)."""
+import ctypes
+
+import pytest
+import torch
+
+import paged_kv_gqa_nx_gb300 as pkv
+
+lib = pkv._lib
+BAD_DIM, BAD_GQA, ARG, OK = pkv.PKV_ERR_BAD_DIM, pkv.PKV_ERR_BAD_GQA, pkv.PKV_ERR_ARG, pkv.PKV_OK
+
+
+def arr(v):
+    return (ctypes.c_int32 * max(1, len(v)))(*v) if v is not None else None
+
+
+def cross(ql=(3, 1), kl=(5, 0), k0=None, n=None, H=4, KV=2, hd=16, dtype=pkv.PKV_BF16, Q=4096, K=4096, V=4096, out=4096, qs=64,
+          ks=32, vs=32, os_=64, w=None, wn=0):
+    return lib.pkv_attn_cross(Q, qs, arr(ql), K, ks, V, vs, arr(kl), arr(k0), dtype, len(ql) if n is None else n, H, KV, hd, 0.25,
+                              out, os_, w, wn, None)
+
+
+def prefix(ql=(3, 1), kl=(5, 1), k0=None, P=7, n=None, H=4, KV=2, hd=16, dtype=pkv.PKV_BF16, Q=4096, K=4096, V=4096, Kp=4096,
+           Vp=4096, out=4096, qs=64, ks=32, vs=32, ps=32, xs=32, os_=64, w=None, wn=0):
+    return lib.pkv_attn_prefix(Q, qs, arr(ql), Kp, ps, Vp, xs, P, K, ks, V, vs, arr(kl), arr(k0), dtype,
+                               len(ql) if n is None else n, H, KV, hd, 0.25, out, os_, w, wn, None)
+
+
+BIG = 2 ** 31 - 1
+COMMON = [
+    (dict(n=0), BAD_DIM), (dict(n=-1), BAD_DIM), (dict(kl=None), BAD_DIM), (dict(ql=(3, -1)), BAD_DIM),
+    (dict(kl=(5, -1)), BAD_DIM), (dict(H=0), BAD_DIM), (dict(KV=0), BAD_DIM), (dict(hd=0), BAD_DIM),
+    (dict(hd=257, qs=5000, ks=5000, vs=5000, os_=5000), BAD_DIM), (dict(H=3), BAD_GQA), (dict(dtype=pkv.PKV_F32), ARG),
+    (dict(dtype=9), ARG), (dict(qs=63), ARG), (dict(ks=31), ARG), (dict(vs=31), ARG), (dict(os_=63), ARG),
+    (dict(qs=1 << 40), BAD_DIM), (dict(ks=1 << 40), BAD_DIM), (dict(k0=(0, -1)), BAD_DIM), (dict(k0=(BIG, 0)), BAD_DIM),
+    (dict(kl=(BIG, 1)), BAD_DIM), (dict(Q=None), ARG), (dict(K=None), ARG), (dict(V=None), ARG), (dict(out=None), ARG),
+    (dict(Q=4097), ARG), (dict(K=4097), ARG), (dict(V=4097), ARG), (dict(out=4097), ARG), (dict(w=4104, wn=64), ARG),
+    (dict(w=None, wn=64), ARG), (dict(w=4096, wn=-1), ARG)]
+
+
+@pytest.mark.parametrize("kw,rc", COMMON + [(dict(ql=(BIG, BIG), kl=(1, 1)), BAD_DIM)], ids=str)
+def test_cross_refuses(kw, rc):
+    assert cross(**kw) == rc, pkv.pkv_last_error()
+    assert pkv.pkv_last_error()
+
+
+@pytest.mark.parametrize("kw,rc", COMMON + [
+    (dict(P=-1), BAD_DIM), (dict(P=BIG), BAD_DIM), (dict(ql=(6, 1)), BAD_DIM), (dict(Kp=None), ARG), (dict(Vp=None), ARG),
+    (dict(Kp=4097), ARG), (dict(Vp=4097), ARG), (dict(ps=31), ARG), (dict(xs=31), ARG), (dict(ps=1 << 40), BAD_DIM)], ids=str)
+def test_prefix_refuses(kw, rc):
+    assert prefix(**kw) == rc, pkv.pkv_last_error()
+    assert pkv.pkv_last_error()
+
+
+def test_nothing_to_do_is_ok():
+    none = dict(Q=None, K=None, V=None, out=None)
+    assert cross(ql=(0, 0), **none) == OK and prefix(ql=(0, 0), Kp=None, Vp=None, **none) == OK
+    assert rope(n=0, Q=None, K=None, pos=None, Qo=None, Ko=None) == OK
+
+
+@pytest.mark.parametrize("H,KV,hd", [(32, 8, 128), (3, 3, 64), (4, 1, 160)])
+def test_workspace_sizes(H, KV, hd):
+    """Enough keys and few rows want records; many rows, or too few keys to share out, want none; bad arguments say -1."""
+    size = lambda ql, kl, **kw: lib.pkv_attn_cross_workspace(arr(ql), arr(kl), arr(kw.get("k0")), len(ql), H, KV, hd)
+    per = 4 * H * (hd + 2)
+    assert size((1,), (100_000,)) >= 2 * per
+    assert size((1,), (200,)) == 0
+    assert size((1, 1), (100_000, 50)) % 16 == 0
+    assert size((1,), (-1,)) == -1 and lib.pkv_attn_cross_workspace(arr((1,)), arr((1,)), None, 1, 3, 2, hd) == -1
+    pre = lambda P, ql, kl: lib.pkv_attn_prefix_workspace(P, arr(ql), arr(kl), len(ql), H, KV, hd)
+    assert pre(4000, (1, 1, 1), (3, 9, 1)) >= 2 * 3 * per   # own keys and the prefix apart
+    assert pre(4000, (2,), (1,)) == -1 and pre(-1, (1,), (1,)) == -1
+
+
+def rope(n=5, H=4, KV=2, hd=16, dtype=pkv.PKV_BF16, pairs=(3, 3, 2), order=0, base=1e4, Q=4096, K=4096, Qo=8192, Ko=8192,
+         pos=4096, ps=5, qs=64, ks=32, qos=64, kos=32, axes=None):
+    return lib.pkv_rope_packed(Q, qs, K, ks, dtype, pos, ps, len(pairs) if axes is None else axes, arr(pairs), order, n, H, KV,
+                               hd, base, 0, Qo, qos, Ko, kos, None)
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(n=-1), BAD_DIM), (dict(n=BIG), BAD_DIM), (dict(axes=0), BAD_DIM), (dict(axes=5), BAD_DIM), (dict(pairs=None, axes=1), BAD_DIM),
+    (dict(pairs=(3, -1, 2)), BAD_DIM), (dict(pairs=(0, 0)), BAD_DIM), (dict(pairs=(5, 4)), BAD_DIM), (dict(H=0), BAD_DIM),
+    (dict(KV=0), BAD_DIM), (dict(hd=0), BAD_DIM), (dict(hd=258, qs=5000, ks=5000, qos=5000, kos=5000), BAD_DIM),
+    (dict(order=1, pairs=(1, 3, 4)), BAD_DIM),  # turns that do not come out at the axes' pairs
+    (dict(dtype=3), ARG), (dict(order=3), ARG), (dict(order=-1), ARG), (dict(base=0.5), ARG), (dict(base=float("nan")), ARG),
+    (dict(base=float("inf")), ARG), (dict(qs=63), ARG), (dict(ks=31), ARG), (dict(qos=63), ARG), (dict(kos=31), ARG),
+    (dict(ps=4), ARG), (dict(qs=1 << 40), BAD_DIM), (dict(Q=None), ARG), (dict(Qo=None), ARG), (dict(K=None), ARG),
+    (dict(Ko=None), ARG), (dict(Q=None, Qo=None, K=None, Ko=None), ARG), (dict(pos=None), ARG), (dict(pos=4098), ARG),
+    (dict(Q=4097), ARG), (dict(Ko=4097), ARG), (dict(dtype=pkv.PKV_F32, Q=4098), ARG), (dict(Q=4096, Qo=4096, qos=72), ARG)], ids=str)
+def test_rope_refuses(kw, rc):
+    assert rope(**kw) == rc, pkv.pkv_last_error()
+    assert pkv.pkv_last_error()
+
+
+def test_the_binding_refuses_host_tensors():
+    x, pos = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(3, 4, dtype=torch.int32)
+    with pytest.raises(TypeError):
+        pkv.pkv_attn_cross(x, [4], x, x, [4], 4, 4, 16, 0.25, x)
+    with pytest.raises(TypeError):
+        pkv.pkv_attn_prefix(x, [4], x, x, x, x, [4], 4, 4, 16, 0.25, x)
+    with pytest.raises(TypeError):
+        pkv.pkv_rope_packed(x, x, pos, [3, 3, 2], 0, 4, 4, 16, 1e4, x, x)
+    with pytest.raises(TypeError, match="entry for each"):
+        pkv.pkv_attn_cross(x, [4], x, x, [4, 1], 4, 4, 16, 0.25, x)
+    with pytest.raises(TypeError, match="entry for each"):
+        pkv.pkv_attn_cross_workspace([4], [4], 4, 4, 16, k_start=[0, 1])
