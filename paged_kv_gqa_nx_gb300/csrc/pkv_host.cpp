@@ -12,6 +12,7 @@
 // pool behaviour: "nx_paged_kv_gate.nx source" (KAT, FORK, REWIND sections).
 #include "../../include/pkv.h"
 #include "pkv_internal.h"
+#include "pkv_ragged.h"
 #include "pkv_tma.h"
 
 #include <cuda_runtime.h>
@@ -2375,20 +2376,9 @@ int run_packed(const void *Q, int64_t q_stride, const void *K, int64_t k_stride,
     if (!Q || !K || !V || !out) return fail(PKV_ERR_ARG, "NULL data pointer");
     for (const void *q : {Q, K, V, static_cast<const void *>(out)})
         if (reinterpret_cast<uintptr_t>(q) % 2 != 0) return fail(PKV_ERR_ARG, "rows must be aligned to their element");
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-    if (dev < 0 || dev >= 64) return fail(PKV_ERR_ARG, "device index out of range");
     int32_t *err_word = nullptr;
-    {
-        std::lock_guard<std::mutex> lk(g_contig_mu);
-        if (!g_contig_err[dev]) {
-            rc = refuse_capture(st);  // the word's set-up allocates; a later call captures
-            if (rc) return rc;
-        }
-        e = contig_error_word(dev, &err_word);
-    }
-    if (e != cudaSuccess) return cuda_fail(e, "error word");
+    rc = contiguous_error_word(st, &err_word);
+    if (rc) return rc;
 
     // sequences with tokens, longest first (the grid then ends on its shortest)
     std::vector<int32_t> order, start(n_seqs), len_s, start_s;
@@ -2422,7 +2412,7 @@ int run_packed(const void *Q, int64_t q_stride, const void *K, int64_t k_stride,
     a.err = err_word;
     for (size_t i = 0; i < order.size(); i += kPackedSeqs) {
         const int32_t m = static_cast<int32_t>(std::min<size_t>(kPackedSeqs, order.size() - i));
-        e = launch(PKV_KERNEL_PREFILL, st, [&] { return launch_packed(a, &start_s[i], &len_s[i], m, st); });
+        const cudaError_t e = launch(PKV_KERNEL_PREFILL, st, [&] { return launch_packed(a, &start_s[i], &len_s[i], m, st); });
         if (e != cudaSuccess) return cuda_fail(e, "packed attention kernel");
     }
     return PKV_OK;
@@ -2617,5 +2607,19 @@ cudaError_t launch_counted(int kind, cudaStream_t s, cudaError_t (*fn)(void *), 
 int32_t current_split_keys() { return g_split_keys.load(); }
 
 int report_error(int code, const char *msg) { return fail(code, "%s", msg); }
+
+int contiguous_error_word(cudaStream_t s, int32_t **out) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (dev < 0 || dev >= 64) return fail(PKV_ERR_ARG, "device index out of range");
+    std::lock_guard<std::mutex> lk(g_contig_mu);
+    if (!g_contig_err[dev]) {
+        const int rc = refuse_capture(s);  // the word's set-up allocates; a later call captures
+        if (rc) return rc;
+    }
+    e = contig_error_word(dev, out);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "error word");
+}
 
 }  // namespace pkv

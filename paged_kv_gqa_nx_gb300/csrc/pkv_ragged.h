@@ -50,9 +50,31 @@ struct RaggedArgs {
     Elem type;
     float *pm, *pl, *pacc;                            // records: [rec][head], [rec][head], [rec][head][hd]
     int32_t *err;
+    int32_t out32;  // out's rows and heads start on 32-byte boundaries (set by the launcher)
     bool vec;       // rows on 16-byte boundaries, heads of whole 16 bytes
     bool overlap;   // the launch may start before the one in front of it on the stream has ended
 };
+
+// Tensor-core tiles (pkv_ragged_tc.cu): 128 / P consecutive queries x P heads of
+// a kv head, P the largest power of two up to 16 in the group; a piece is two
+// of them and a split of the 128-key tiles, the prefix's and then the run's.
+constexpr int32_t kRaggedKeyTile = 128;
+inline int ragged_log_p(int group) {
+    int p = 0;
+    while (p < 4 && group % (2 << p) == 0) ++p;
+    return p;
+}
+constexpr int32_t ragged_tile_pairs(int32_t nq, int log_p) { return (nq + (256 >> log_p) - 1) / (256 >> log_p); }
+constexpr int32_t ragged_key_tiles(int32_t n_pre, int32_t nk) {
+    return (n_pre + kRaggedKeyTile - 1) / kRaggedKeyTile + (nk + kRaggedKeyTile - 1) / kRaggedKeyTile;
+}
+constexpr int32_t ragged_split_tiles(int32_t n_pre, const RaggedRun &r) { return (ragged_key_tiles(n_pre, r.nk) + r.ns - 1) / r.ns; }
+// TMA's alignment rules, and a positive finite scale (the kernel masks with
+// -inf before it scales).
+inline bool ragged_tc_takes(const RaggedArgs &a) {
+    return a.vec && a.hd <= 128 && a.scale_log2 > 0.f && a.scale_log2 <= 3e38f;
+}
+cudaError_t launch_ragged_tc(const RaggedArgs &a, const RaggedRun *runs, int32_t n, cudaStream_t s);
 
 // Key rows by warp-level MMAs (pkv_ragged_rows.cu): units of 16 * wide query
 // rows (query, head of the group) of one kv head.

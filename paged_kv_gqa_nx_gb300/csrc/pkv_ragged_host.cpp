@@ -56,8 +56,8 @@ struct Seq {
 };
 
 struct Plan {
-    std::vector<RaggedRun> rows;      // own keys (behind the prefix, unless stacked)
-    std::vector<RaggedRun> rows_pre;  // the prefix, for stacked sequences
+    std::vector<RaggedRun> tiles_pre, rows_pre;  // the prefix, for the stacked rows of sequences with few
+    std::vector<RaggedRun> tiles, rows;          // own keys (behind the prefix, unless stacked)
     std::vector<JoinRun> joins;
     int64_t n_rec = 0;
     bool stacked = false;
@@ -93,47 +93,103 @@ void split_rows(std::vector<RaggedRun> &runs, const Shape &sh, int wide, int64_t
     for (RaggedRun &r : runs) r.ns = static_cast<int32_t>(std::clamp<int64_t>((keys(r) + per - 1) / per, 1, 128));
 }
 
+// Splits of the tensor-core kernel, which runs a block a SM.  Where there are
+// fewer pieces than two rounds of blocks, key tiles are split so that the rounds are full;
+// a piece of one tile would be mostly its first scores and its output.
+void split_tiles(std::vector<RaggedRun> &runs, const Shape &sh, int32_t n_pre, int64_t coarse) {
+    const int log_p = ragged_log_p(sh.group());
+    int64_t pieces = 0, most = 0;
+    auto blocks = [&](const RaggedRun &r) { return static_cast<int64_t>(ragged_tile_pairs(r.nq, log_p)) * (sh.n_heads >> log_p); };
+    for (const RaggedRun &r : runs) {
+        pieces += blocks(r);
+        most = std::max<int64_t>(most, ragged_key_tiles(n_pre, r.nk));
+    }
+    if (pieces > 2 * kSMs) return;
+    const int64_t room = pieces <= kSMs ? kSMs : 2 * kSMs;
+    auto total = [&](int64_t per) {
+        int64_t n = 0;
+        for (const RaggedRun &r : runs) n += blocks(r) * ((ragged_key_tiles(n_pre, r.nk) + per - 1) / per);
+        return n;
+    };
+    int64_t lo = 2, hi = std::max<int64_t>(2, most);  // the least tiles a split that fit
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (total(mid) <= room) hi = mid;
+        else lo = mid + 1;
+    }
+    const int64_t per = lo * coarse;
+    for (RaggedRun &r : runs) r.ns = static_cast<int32_t>((ragged_key_tiles(n_pre, r.nk) + per - 1) / per);
+}
+
+// Query rows of a tensor-core tile (queries x heads of the group) from which a
+// sequence takes it.
+constexpr int64_t kTileRows = 48;
+
 // The plan of up to kRaggedLarge sequences; with less workspace than it would
 // like, keys are split less, or not at all.
-Plan make_plan(const std::vector<Seq> &seqs, const Shape &sh, int32_t n_pre, int64_t workspace) {
+Plan make_plan(const std::vector<Seq> &seqs, const Shape &sh, int32_t n_pre, bool tc, int64_t workspace) {
     constexpr int64_t kCoarsest = int64_t{1} << 24;
+    const int log_p = ragged_log_p(sh.group());
+    auto takes_tiles = [&](int64_t nq, int32_t keys) { return tc && keys > 0 && (nq << log_p) >= kTileRows; };
     for (int64_t coarse = workspace < record_bytes(1, sh) ? 2 * kCoarsest : 1;; coarse *= 2) {
         const bool last = coarse > kCoarsest;
         Plan p;
-        p.stacked = !last && n_pre >= 128 && seqs.size() > 1;
-        for (const Seq &s : seqs) p.rows.push_back(RaggedRun{s.q0, s.nq, s.k0, s.nk, s.off, 1, -1});
+        for (const Seq &s : seqs)
+            (takes_tiles(s.nq, n_pre + s.nk) ? p.tiles : p.rows).push_back(RaggedRun{s.q0, s.nq, s.k0, s.nk, s.off, 1, -1});
+        p.stacked = !last && n_pre >= 128 && p.rows.size() > 1;
         p.wide = pick_wide(p.rows, sh);
-        if (!last) split_rows(p.rows, sh, p.wide, p.stacked ? 0 : n_pre, coarse);
+        if (!last) {
+            split_rows(p.rows, sh, p.wide, p.stacked ? 0 : n_pre, coarse);
+            split_tiles(p.tiles, sh, n_pre, coarse);
+        }
+        std::vector<RaggedRun> runs;  // stacked: neighbours together
         if (p.stacked) {
-            for (const Seq &s : seqs) {
-                if (!p.rows_pre.empty() && p.rows_pre.back().q0 + p.rows_pre.back().nq == s.q0) p.rows_pre.back().nq += s.nq;
-                else p.rows_pre.push_back(RaggedRun{s.q0, s.nq, 0, n_pre, kSees, 1, -1});
+            for (const RaggedRun &r : p.rows) {
+                if (!runs.empty() && runs.back().q0 + runs.back().nq == r.q0) runs.back().nq += r.nq;
+                else runs.push_back(RaggedRun{r.q0, r.nq, 0, n_pre, kSees, 1, -1});
             }
+            for (const RaggedRun &r : runs) (takes_tiles(r.nq, n_pre) ? p.tiles_pre : p.rows_pre).push_back(r);
             p.wide_pre = pick_wide(p.rows_pre, sh);
             split_rows(p.rows_pre, sh, p.wide_pre, 0, coarse);
+            split_tiles(p.tiles_pre, sh, 0, coarse);
         }
-        // records: of the prefix run by run, of own keys sequence by sequence
+        // records, run by run
         int64_t at = 0;
         auto records = [&](RaggedRun &r) {
             r.rec0 = static_cast<int32_t>(std::min<int64_t>(at, 0x7fffffff));
             at += static_cast<int64_t>(r.nq) * r.ns;
         };
         for (RaggedRun &r : p.rows_pre) records(r);
-        size_t pre = 0;
+        for (RaggedRun &r : p.tiles_pre) records(r);
+        size_t next_rows = 0, next_tiles = 0;  // (both lists are in the order of the queries)
+        const RaggedRun *pre = nullptr;
         for (RaggedRun &r : p.rows) {
             if (!p.stacked && r.ns == 1) continue;
             records(r);
             JoinRun j{r.q0, r.nq, r.rec0, r.ns, 0, 0};
             if (p.stacked) {
-                while (p.rows_pre[pre].q0 + p.rows_pre[pre].nq <= r.q0) ++pre;
-                const RaggedRun &b = p.rows_pre[pre];
-                j.pre0 = b.rec0 + (r.q0 - b.q0) * b.ns;
-                j.pns = b.ns;
+                if (!pre || r.q0 >= pre->q0 + pre->nq)
+                    pre = next_rows < p.rows_pre.size() && r.q0 >= p.rows_pre[next_rows].q0 &&
+                                  r.q0 < p.rows_pre[next_rows].q0 + p.rows_pre[next_rows].nq
+                              ? &p.rows_pre[next_rows++]
+                              : &p.tiles_pre[next_tiles++];
+                j.pre0 = pre->rec0 + (r.q0 - pre->q0) * pre->ns;
+                j.pns = pre->ns;
             }
             p.joins.push_back(j);
         }
+        for (RaggedRun &r : p.tiles) {
+            if (r.ns == 1) continue;
+            records(r);
+            p.joins.push_back(JoinRun{r.q0, r.nq, r.rec0, r.ns, 0, 0});
+        }
         p.n_rec = at;
-        if (at == 0 || (at <= 0x7fffffff && record_bytes(at, sh) <= workspace)) return p;
+        if (at > 0 && (at > 0x7fffffff || record_bytes(at, sh) > workspace)) continue;
+        // the longest pieces first: the launch then ends on its shortest
+        std::stable_sort(p.tiles.begin(), p.tiles.end(), [&](const RaggedRun &x, const RaggedRun &y) {
+            return ragged_split_tiles(n_pre, x) > ragged_split_tiles(n_pre, y);
+        });
+        return p;
     }
 }
 
@@ -204,7 +260,9 @@ int64_t workspace_of(const Call &c) {
     if (sequences(c, seqs, &keys)) return -1;
     int64_t most = 0;
     each_chunk(seqs, [&](const std::vector<Seq> &part) {
-        most = std::max(most, record_bytes(make_plan(part, c.sh, c.n_pre, int64_t{1} << 62).n_rec, c.sh));
+        for (const bool tc : {false, true})  // (alignment and scale, which a call's kernels go by, are not known here)
+            most = std::max(most, record_bytes(make_plan(part, c.sh, c.n_pre, tc && c.sh.hd <= 128 && c.sh.hd % 8 == 0,
+                                                         int64_t{1} << 62).n_rec, c.sh));
         return PKV_OK;
     });
     return most;
@@ -251,29 +309,38 @@ int attend(const Call &c, cudaStream_t st) {
     auto whole = [](const void *p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0; };
     a.vec = c.sh.hd % 8 == 0 && whole(c.Q, c.q_stride) && whole(c.K, c.k_stride) && whole(c.V, c.v_stride) &&
             whole(c.out, c.o_stride) && (c.n_pre == 0 || (whole(c.Kp, c.kp_stride) && whole(c.Vp, c.vp_stride)));
+    const bool tc = ragged_tc_takes(a);
     return each_chunk(seqs, [&](const std::vector<Seq> &part) {
-        const Plan p = make_plan(part, c.sh, c.n_pre, c.workspace_bytes);
+        const Plan p = make_plan(part, c.sh, c.n_pre, tc, c.workspace_bytes);
+        if (!a.err && !(p.tiles.empty() && p.tiles_pre.empty())) {
+            const int r = contiguous_error_word(st, &a.err);
+            if (r) return r;
+        }
         a.pm = static_cast<float *>(c.workspace);
         a.pl = a.pm + record_floats(p.n_rec, c.sh.n_heads);
         a.pacc = a.pl + record_floats(p.n_rec, c.sh.n_heads);
         bool first = true;
-        auto rows = [&](RaggedArgs b, const std::vector<RaggedRun> &runs, int wide) {
+        auto run = [&](RaggedArgs b, const std::vector<RaggedRun> &runs, int wide) {  // wide 0: tiles
             if (runs.empty()) return static_cast<int>(PKV_OK);
             b.overlap = !first;
             first = false;
-            return counted(PKV_KERNEL_DECODE, st, "ragged attention kernel",
-                           [&] { return launch_ragged_rows(b, runs.data(), static_cast<int32_t>(runs.size()), wide, st); });
+            const int32_t n = static_cast<int32_t>(runs.size());
+            if (wide == 0)
+                return counted(PKV_KERNEL_PREFILL, st, "ragged attention tiles", [&] { return launch_ragged_tc(b, runs.data(), n, st); });
+            return counted(PKV_KERNEL_DECODE, st, "ragged attention rows", [&] { return launch_ragged_rows(b, runs.data(), n, wide, st); });
         };
-        RaggedArgs pre = a;
+        RaggedArgs pre = a, own = a;  // the prefix as a run's keys; keys of the sequences' own, behind it unless stacked
         pre.K = c.Kp;
         pre.V = c.Vp;
         pre.k_stride = c.kp_stride;
         pre.v_stride = c.vp_stride;
-        int r = rows(pre, p.rows_pre, p.wide_pre);
-        if (r) return r;
-        RaggedArgs own = a;
         own.n_pre = p.stacked ? 0 : c.n_pre;
-        r = rows(own, p.rows, p.wide);
+        RaggedArgs both = a;
+        both.n_pre = c.n_pre;
+        int r = run(both, p.tiles, 0);
+        if (!r) r = run(pre, p.tiles_pre, 0);
+        if (!r) r = run(pre, p.rows_pre, p.wide_pre);
+        if (!r) r = run(own, p.rows, p.wide);
         if (r || p.joins.empty()) return r;
         return counted(PKV_KERNEL_MERGE, st, "ragged join kernel",
                        [&] { return launch_ragged_join(a, p.joins.data(), static_cast<int32_t>(p.joins.size()), st); });
