@@ -21,6 +21,7 @@ struct RaggedRun {
     int32_t off;       // query i sees the run's keys j <= off + i
     int32_t ns;        // splits of the prefix and the run's keys together
     int32_t rec0;      // record of (query i, split x): rec0 + i * ns + x; -1: one split, written to out
+    int32_t on_prefix; // the keys are the prefix's rows themselves (k0 0, nk all of them)
 };
 
 // A query's records: ns of its own keys and pns of the shared prefix.
@@ -30,7 +31,7 @@ struct JoinRun {
 
 // Lists travel in the launch's parameters (no upload), in two sizes as a
 // launch takes longer with more of them.
-constexpr int32_t kRaggedSmall = 64, kRaggedLarge = 900;
+constexpr int32_t kRaggedSmall = 64, kRaggedLarge = 850;
 template <class R, int N>
 struct RunList {
     int32_t n;
@@ -76,10 +77,11 @@ inline bool ragged_tc_takes(const RaggedArgs &a) {
 }
 cudaError_t launch_ragged_tc(const RaggedArgs &a, const RaggedRun *runs, int32_t n, cudaStream_t s);
 
-// Key rows by warp-level MMAs (pkv_ragged_rows.cu): units of 16 * wide query
-// rows (query, head of the group) of one kv head.
+// Few query rows by warp-level MMAs (pkv_ragged_rows.cu): units of 8 * wide
+// rows ((query, head of the group) pairs) of one kv head; wide 1, 2 or, for heads up to 128, 4
+// (2 where rows are not vec).
 cudaError_t launch_ragged_rows(const RaggedArgs &a, const RaggedRun *runs, int32_t n, int wide, cudaStream_t s);
-__host__ __device__ constexpr int32_t ragged_row_units(int32_t rows, int wide) { return (rows + 16 * wide - 1) / (16 * wide); }
+__host__ __device__ constexpr int32_t ragged_row_units(int32_t rows, int wide) { return (rows + 8 * wide - 1) / (8 * wide); }
 cudaError_t launch_ragged_join(const RaggedArgs &a, const JoinRun *runs, int32_t n, cudaStream_t s);
 
 // Rotary positions with several axes (pkv_rope.cu).

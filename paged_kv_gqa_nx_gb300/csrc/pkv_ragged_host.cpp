@@ -56,28 +56,35 @@ struct Seq {
 };
 
 struct Plan {
-    std::vector<RaggedRun> tiles_pre, rows_pre;  // the prefix, for the stacked rows of sequences with few
-    std::vector<RaggedRun> tiles, rows;          // own keys (behind the prefix, unless stacked)
+    std::vector<RaggedRun> tiles_pre;    // the prefix, for the stacked rows of sequences with few
+    std::vector<RaggedRun> tiles, rows;  // own keys (behind the prefix, unless stacked); rows: of the prefix too
     std::vector<JoinRun> joins;
     int64_t n_rec = 0;
     bool stacked = false;
-    int wide = 1, wide_pre = 1;
+    int wide = 1;
+};
+
+// What a call's kernels go by besides its lengths.
+struct Kernels {
+    bool vec, tc;  // rows on 16-byte boundaries; the tensor-core tiles take them
 };
 
 int64_t record_bytes(int64_t n_rec, const Shape &sh) {
     return 4 * (2 * static_cast<int64_t>(record_floats(n_rec, sh.n_heads)) + n_rec * sh.n_heads * sh.hd);
 }
 
-// Query rows a unit of the row kernel takes, in sixteens: two where that saves
-// a third of the reads of K and V.
-int pick_wide(const std::vector<RaggedRun> &runs, const Shape &sh) {
-    if (sh.hd > 128) return 1;
-    int64_t one = 0, two = 0;
-    for (const RaggedRun &r : runs) {
-        one += ragged_row_units(r.nq * sh.group(), 1);
-        two += ragged_row_units(r.nq * sh.group(), 2);
+// Query rows a unit of the row kernel takes, in eights: a unit reads its keys
+// once, which costs about as much as the arithmetic of two eights.
+int pick_wide(const std::vector<RaggedRun> &runs, const Shape &sh, const Kernels &k) {
+    if (!k.vec) return 2;
+    int best = 1;
+    int64_t least = -1;
+    for (int wide = 1; wide <= (sh.hd > 128 ? 2 : 4); wide *= 2) {
+        int64_t cost = 0;
+        for (const RaggedRun &r : runs) cost += static_cast<int64_t>(ragged_row_units(r.nq * sh.group(), wide)) * (2 + wide) * (r.nk + 1);
+        if (least < 0 || cost < least) least = cost, best = wide;
     }
-    return 3 * two <= 2 * one ? 2 : 1;
+    return best;
 }
 
 // Splits of the row kernel: as many keys a split as give the GPU's resident
@@ -86,7 +93,7 @@ int pick_wide(const std::vector<RaggedRun> &runs, const Shape &sh) {
 // is short.  A unit of fewer than 256 keys (64 a warp) is mostly latency.
 void split_rows(std::vector<RaggedRun> &runs, const Shape &sh, int wide, int64_t n_pre, int64_t coarse) {
     int64_t work = 0;
-    auto keys = [&](const RaggedRun &r) { return n_pre + r.nk; };
+    auto keys = [&](const RaggedRun &r) { return (r.on_prefix ? 0 : n_pre) + r.nk; };
     for (const RaggedRun &r : runs) work += static_cast<int64_t>(ragged_row_units(r.nq * sh.group(), wide)) * sh.n_kv * keys(r);
     const int64_t units = static_cast<int64_t>(kSMs) * (sh.hd > 128 ? 1 : 2) * 3;
     const int64_t per = std::max<int64_t>(256, (work + units - 1) / units) * coarse;
@@ -127,30 +134,39 @@ constexpr int64_t kTileRows = 48;
 
 // The plan of up to kRaggedLarge sequences; with less workspace than it would
 // like, keys are split less, or not at all.
-Plan make_plan(const std::vector<Seq> &seqs, const Shape &sh, int32_t n_pre, bool tc, int64_t workspace) {
+Plan make_plan(const std::vector<Seq> &seqs, const Shape &sh, int32_t n_pre, const Kernels &kernels, int64_t workspace) {
     constexpr int64_t kCoarsest = int64_t{1} << 24;
     const int log_p = ragged_log_p(sh.group());
-    auto takes_tiles = [&](int64_t nq, int32_t keys) { return tc && keys > 0 && (nq << log_p) >= kTileRows; };
+    auto takes_tiles = [&](int64_t nq, int32_t keys) { return kernels.tc && keys > 0 && (nq << log_p) >= kTileRows; };
+    std::vector<RaggedRun> own;
+    Plan p;
+    for (const Seq &s : seqs)
+        (takes_tiles(s.nq, n_pre + s.nk) ? p.tiles : own).push_back(RaggedRun{s.q0, s.nq, s.k0, s.nk, s.off, 1, -1, 0});
     for (int64_t coarse = workspace < record_bytes(1, sh) ? 2 * kCoarsest : 1;; coarse *= 2) {
         const bool last = coarse > kCoarsest;
-        Plan p;
-        for (const Seq &s : seqs)
-            (takes_tiles(s.nq, n_pre + s.nk) ? p.tiles : p.rows).push_back(RaggedRun{s.q0, s.nq, s.k0, s.nk, s.off, 1, -1});
-        p.stacked = !last && n_pre >= 128 && p.rows.size() > 1;
-        p.wide = pick_wide(p.rows, sh);
-        if (!last) {
+        p.stacked = !last && n_pre >= 128 && own.size() > 1;
+        p.rows.clear();
+        p.tiles_pre.clear();
+        p.joins.clear();
+        std::vector<RaggedRun> stacks;  // neighbours together, over the prefix
+        if (p.stacked) {
+            for (const RaggedRun &r : own) {
+                if (!stacks.empty() && stacks.back().q0 + stacks.back().nq == r.q0) stacks.back().nq += r.nq;
+                else stacks.push_back(RaggedRun{r.q0, r.nq, 0, n_pre, kSees, 1, -1, 1});
+            }
+            for (RaggedRun &r : stacks) {
+                r.on_prefix = takes_tiles(r.nq, n_pre) ? 0 : 1;
+                (r.on_prefix ? p.rows : p.tiles_pre).push_back(r);
+            }
+        }
+        const size_t n_stacks = p.rows.size();
+        p.rows.insert(p.rows.end(), own.begin(), own.end());
+        p.wide = pick_wide(p.rows, sh, kernels);
+        if (last) {
+            for (RaggedRun &r : p.tiles) r.ns = 1;
+        } else {
             split_rows(p.rows, sh, p.wide, p.stacked ? 0 : n_pre, coarse);
             split_tiles(p.tiles, sh, n_pre, coarse);
-        }
-        std::vector<RaggedRun> runs;  // stacked: neighbours together
-        if (p.stacked) {
-            for (const RaggedRun &r : p.rows) {
-                if (!runs.empty() && runs.back().q0 + runs.back().nq == r.q0) runs.back().nq += r.nq;
-                else runs.push_back(RaggedRun{r.q0, r.nq, 0, n_pre, kSees, 1, -1});
-            }
-            for (const RaggedRun &r : runs) (takes_tiles(r.nq, n_pre) ? p.tiles_pre : p.rows_pre).push_back(r);
-            p.wide_pre = pick_wide(p.rows_pre, sh);
-            split_rows(p.rows_pre, sh, p.wide_pre, 0, coarse);
             split_tiles(p.tiles_pre, sh, 0, coarse);
         }
         // records, run by run
@@ -159,26 +175,28 @@ Plan make_plan(const std::vector<Seq> &seqs, const Shape &sh, int32_t n_pre, boo
             r.rec0 = static_cast<int32_t>(std::min<int64_t>(at, 0x7fffffff));
             at += static_cast<int64_t>(r.nq) * r.ns;
         };
-        for (RaggedRun &r : p.rows_pre) records(r);
         for (RaggedRun &r : p.tiles_pre) records(r);
-        size_t next_rows = 0, next_tiles = 0;  // (both lists are in the order of the queries)
-        const RaggedRun *pre = nullptr;
-        for (RaggedRun &r : p.rows) {
+        size_t rows_at = 0, tiles_at = 0;  // the next stacks (both lists are in the order of the queries)
+        const RaggedRun *stack = nullptr;
+        for (size_t i = 0; i < p.rows.size(); ++i) {
+            RaggedRun &r = p.rows[i];
+            r.rec0 = -1;
             if (!p.stacked && r.ns == 1) continue;
             records(r);
+            if (i < n_stacks) continue;
             JoinRun j{r.q0, r.nq, r.rec0, r.ns, 0, 0};
             if (p.stacked) {
-                if (!pre || r.q0 >= pre->q0 + pre->nq)
-                    pre = next_rows < p.rows_pre.size() && r.q0 >= p.rows_pre[next_rows].q0 &&
-                                  r.q0 < p.rows_pre[next_rows].q0 + p.rows_pre[next_rows].nq
-                              ? &p.rows_pre[next_rows++]
-                              : &p.tiles_pre[next_tiles++];
-                j.pre0 = pre->rec0 + (r.q0 - pre->q0) * pre->ns;
-                j.pns = pre->ns;
+                if (!stack || r.q0 >= stack->q0 + stack->nq)
+                    stack = rows_at < n_stacks && r.q0 >= p.rows[rows_at].q0 && r.q0 < p.rows[rows_at].q0 + p.rows[rows_at].nq
+                                ? &p.rows[rows_at++]
+                                : &p.tiles_pre[tiles_at++];
+                j.pre0 = stack->rec0 + (r.q0 - stack->q0) * stack->ns;
+                j.pns = stack->ns;
             }
             p.joins.push_back(j);
         }
         for (RaggedRun &r : p.tiles) {
+            r.rec0 = -1;
             if (r.ns == 1) continue;
             records(r);
             p.joins.push_back(JoinRun{r.q0, r.nq, r.rec0, r.ns, 0, 0});
@@ -260,9 +278,10 @@ int64_t workspace_of(const Call &c) {
     if (sequences(c, seqs, &keys)) return -1;
     int64_t most = 0;
     each_chunk(seqs, [&](const std::vector<Seq> &part) {
-        for (const bool tc : {false, true})  // (alignment and scale, which a call's kernels go by, are not known here)
-            most = std::max(most, record_bytes(make_plan(part, c.sh, c.n_pre, tc && c.sh.hd <= 128 && c.sh.hd % 8 == 0,
-                                                         int64_t{1} << 62).n_rec, c.sh));
+        // (alignment and scale, which a call's kernels go by too, are not known here)
+        const bool vec = c.sh.hd % 8 == 0, tc = vec && c.sh.hd <= 128;
+        for (const Kernels k : {Kernels{false, false}, Kernels{vec, false}, Kernels{vec, tc}})
+            most = std::max(most, record_bytes(make_plan(part, c.sh, c.n_pre, k, int64_t{1} << 62).n_rec, c.sh));
         return PKV_OK;
     });
     return most;
@@ -301,6 +320,7 @@ int attend(const Call &c, cudaStream_t st) {
     a.Vp = c.Vp;
     a.kp_stride = c.kp_stride;
     a.vp_stride = c.vp_stride;
+    a.n_pre = c.n_pre;
     a.n_heads = c.sh.n_heads;
     a.n_kv = c.sh.n_kv;
     a.hd = c.sh.hd;
@@ -309,9 +329,9 @@ int attend(const Call &c, cudaStream_t st) {
     auto whole = [](const void *p, int64_t stride) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0; };
     a.vec = c.sh.hd % 8 == 0 && whole(c.Q, c.q_stride) && whole(c.K, c.k_stride) && whole(c.V, c.v_stride) &&
             whole(c.out, c.o_stride) && (c.n_pre == 0 || (whole(c.Kp, c.kp_stride) && whole(c.Vp, c.vp_stride)));
-    const bool tc = ragged_tc_takes(a);
+    const Kernels kernels{a.vec, ragged_tc_takes(a)};
     return each_chunk(seqs, [&](const std::vector<Seq> &part) {
-        const Plan p = make_plan(part, c.sh, c.n_pre, tc, c.workspace_bytes);
+        const Plan p = make_plan(part, c.sh, c.n_pre, kernels, c.workspace_bytes);
         if (!a.err && !(p.tiles.empty() && p.tiles_pre.empty())) {
             const int r = contiguous_error_word(st, &a.err);
             if (r) return r;
@@ -320,27 +340,28 @@ int attend(const Call &c, cudaStream_t st) {
         a.pl = a.pm + record_floats(p.n_rec, c.sh.n_heads);
         a.pacc = a.pl + record_floats(p.n_rec, c.sh.n_heads);
         bool first = true;
-        auto run = [&](RaggedArgs b, const std::vector<RaggedRun> &runs, int wide) {  // wide 0: tiles
-            if (runs.empty()) return static_cast<int>(PKV_OK);
-            b.overlap = !first;
-            first = false;
-            const int32_t n = static_cast<int32_t>(runs.size());
-            if (wide == 0)
-                return counted(PKV_KERNEL_PREFILL, st, "ragged attention tiles", [&] { return launch_ragged_tc(b, runs.data(), n, st); });
-            return counted(PKV_KERNEL_DECODE, st, "ragged attention rows", [&] { return launch_ragged_rows(b, runs.data(), n, wide, st); });
+        auto run = [&](RaggedArgs b, const std::vector<RaggedRun> &runs, bool tiles) {
+            for (size_t i = 0; i < runs.size(); i += kRaggedLarge) {
+                const int32_t n = static_cast<int32_t>(std::min<size_t>(kRaggedLarge, runs.size() - i));
+                b.overlap = !first;
+                first = false;
+                const int r = tiles ? counted(PKV_KERNEL_PREFILL, st, "ragged attention tiles", [&] { return launch_ragged_tc(b, &runs[i], n, st); })
+                                    : counted(PKV_KERNEL_DECODE, st, "ragged attention rows",
+                                              [&] { return launch_ragged_rows(b, &runs[i], n, p.wide, st); });
+                if (r) return r;
+            }
+            return static_cast<int>(PKV_OK);
         };
-        RaggedArgs pre = a, own = a;  // the prefix as a run's keys; keys of the sequences' own, behind it unless stacked
+        RaggedArgs pre = a, own = a;  // the prefix as a run's keys; own keys of sequences whose rows are stacked over it
         pre.K = c.Kp;
         pre.V = c.Vp;
         pre.k_stride = c.kp_stride;
         pre.v_stride = c.vp_stride;
+        pre.n_pre = 0;
         own.n_pre = p.stacked ? 0 : c.n_pre;
-        RaggedArgs both = a;
-        both.n_pre = c.n_pre;
-        int r = run(both, p.tiles, 0);
-        if (!r) r = run(pre, p.tiles_pre, 0);
-        if (!r) r = run(pre, p.rows_pre, p.wide_pre);
-        if (!r) r = run(own, p.rows, p.wide);
+        int r = run(a, p.tiles, true);
+        if (!r) r = run(pre, p.tiles_pre, true);
+        if (!r) r = run(own, p.rows, false);
         if (r || p.joins.empty()) return r;
         return counted(PKV_KERNEL_MERGE, st, "ragged join kernel",
                        [&] { return launch_ragged_join(a, p.joins.data(), static_cast<int32_t>(p.joins.size()), st); });

@@ -6,17 +6,18 @@
 //   o[i, h] = sum_j p_ij v[j, h / G] / sum_j p_ij,  p_ij = 2^(s_ij - m_i),
 //   s_ij = scale * log2(e) * <q[i, h], k[j, h / G]>
 //
-// A unit is 16 R query rows ((query, head of the group) pairs, which share
-// their keys) of one kv head and one split of the keys: the shared prefix's
-// rows, then the run's own.  Its four warps take the 16-key tiles in turn, each
-// with its own ring of tiles (cp.async, no block-wide barrier in the loop), its
-// own running maximum and sum; they are joined in shared memory at the end.
+// A unit is 8 W query rows ((query, head of the group) pairs, which share their
+// keys) of one kv head and one split of the keys: the shared prefix's rows,
+// then the run's own.  Its four warps take the key tiles in turn, each with its
+// own ring of tiles (cp.async, no block-wide barrier in the loop), its own running
+// maximum and sum; they are joined in shared memory at the end.
 //
-//   S [16 x 16] = Q K^T     m16n8k16, A and B by ldmatrix
-//   O [16 x DP] += P V      A from S's accumulators, B by transposed ldmatrix
+//   S^T [16 keys x 8] = K Q^T       m16n8k16, A by ldmatrix, B held in registers
+//   O^T [16 dims x 8] += V^T P^T    A by transposed ldmatrix, B from S^T by movmatrix
 //
-// What bounds it is reading K and V once: a tile of 8 KB (128-wide heads) has
-// 16 MMAs for S and 32 for O.  So P is not rounded to 16 bits: it goes in as two
+// Keys and dims lie on the MMA's 16-row side, so that a single token's heads (4 of a group)
+// fill half of the other side and not a quarter.  What has to bound it is reading K and V
+// once: 8 KB a tile of 128-wide heads.  So P is not rounded to 16 bits: it goes in as two
 // pieces, p = hi + lo, each of the type, and what is left of p beyond them is
 // 2^-16 (bf16) or 2^-22 of it.  The tensor core rounds its sums toward zero, so
 // each tile's products have a sum of their own, added to O in f32.
@@ -30,19 +31,19 @@
 namespace pkv {
 namespace {
 
-constexpr int kTile = 16;    // keys of a tile
 constexpr int kRowWarps = 4;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kHeadroom = 8.f;
 
-template <int DP, int R>
+template <int DP, int W>
 struct RowCfg {
+    static constexpr int kTile = DP <= 64 ? 32 : 16;          // keys
     static constexpr int kPitch = DP * 2;                     // bytes of a row
-    static constexpr int kStage = 2 * kTile * kPitch;         // K and V of a tile
-    static constexpr int kStages = DP <= 64 ? 6 : 3;          // 128 KB of K and V on the way a SM
-    static constexpr int kQ = 16 * R * kPitch;
-    static constexpr size_t kSmem = static_cast<size_t>(kQ) + kRowWarps * kStages * kStage;
-    static_assert(static_cast<size_t>(kRowWarps) * 16 * R * DP * 4 <= kSmem, "the warps' outputs");
+    static constexpr int kStage = 2 * kTile * kPitch;         // K and V of a tile: 8 KB (16 of wide heads)
+    static constexpr int kStages = 3;                         // 128 KB of K and V on the way a SM
+    static constexpr size_t kRing = static_cast<size_t>(kRowWarps) * kStages * kStage;
+    static constexpr int kPart = DP + 4;                      // floats of an output row of a warp's part
+    static constexpr size_t kSmem = kRing > sizeof(float) * kRowWarps * 8 * W * kPart ? kRing : sizeof(float) * kRowWarps * 8 * W * kPart;
 };
 
 __device__ __forceinline__ float pow2(float x) {  // 2^x to about 2^-22 relative; 0 for -inf
@@ -50,8 +51,11 @@ __device__ __forceinline__ float pow2(float x) {  // 2^x to about 2^-22 relative
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
 }
-// 16 bytes, or zeros where `there` is false (nothing is read then)
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+// or zeros where `there` is false (nothing is read then)
+__device__ __forceinline__ void copy16_if(uint32_t dst, const void *src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
@@ -73,47 +77,65 @@ __device__ __forceinline__ int run_of(const RunList<R, N> &l, int u) {
     return lo;
 }
 
-// Rows [16][DP] of K or V at tile `t0` (keys of the prefix, then of the run)
-// into shared memory, zeros past `end`.
-template <class T, int DP, bool kVec>
-__device__ __forceinline__ void load_tile(unsigned char *dst, const T *pre, int64_t pre_stride, int n_pre, const T *own,
-                                          int64_t own_stride, int t0, int end, int hd, int lane) {
-    constexpr int kChunks = DP / 8;
+// 8 x 8 elements of the warp, transposed.
+__device__ __forceinline__ uint32_t turned(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Key rows as the two stretches they lie in, of one kv head.
+template <class T>
+struct KeyRows {
+    const T *pre, *own;  // own: of the key behind the prefix
+    int64_t pre_stride, own_stride;
+    int n_pre;
+    __device__ __forceinline__ const T *row(int key) const {
+        return key < n_pre ? pre + key * pre_stride : own + (key - n_pre) * own_stride;
+    }
+};
+
+// Rows [kTile][DP] of K or V from key `t0` on into shared memory, zeros from `end` on.
+template <class T, int DP, int kTile, bool kVec>
+__device__ __forceinline__ void load_tile(unsigned char *dst, const KeyRows<T> &rows, int t0, int end, int hd, int lane) {
     if constexpr (kVec) {
-        constexpr int kRows = 32 / kChunks > 0 ? 32 / kChunks : 1;  // rows a pass of the warp covers
-        constexpr int kAcross = kChunks > 32 ? kChunks / 32 : 1;
-        static_assert(kAcross == 1, "a row is at most 32 chunks");
+        constexpr int kChunks = DP / 8, kRows = 32 / kChunks;  // chunks of a row, rows that the warp copies at a time
         const int c = lane % kChunks, r0 = lane / kChunks;
         if (8 * c >= hd) return;
-        const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+        const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(dst)) + r0 * (DP * 2);
+        const bool pre = t0 + kTile <= rows.n_pre;
+        if (t0 + kTile <= end && (pre || t0 >= rows.n_pre)) {  // rows at one stride
+            const T *src = pre ? rows.pre + (t0 + r0) * rows.pre_stride : rows.own + (t0 - rows.n_pre + r0) * rows.own_stride;
+            const int64_t step = (pre ? rows.pre_stride : rows.own_stride) * kRows;
+            src += 8 * c;
 #pragma unroll
+            for (int i = 0; i < kTile / kRows; ++i, src += step)
+                copy16(base + i * kRows * (DP * 2) + ((c ^ ((r0 + i * kRows) & 7)) << 4), src);
+            return;
+        }
+#pragma unroll 1
         for (int i = 0; i < kTile / kRows; ++i) {
             const int r = r0 + i * kRows, key = t0 + r;
-            const bool there = key < end;
-            const int k = there ? key : t0;
-            const T *src = k < n_pre ? pre + k * pre_stride : own + (k - n_pre) * own_stride;
-            copy16(base + r * (DP * 2) + ((c ^ (r & 7)) << 4), src + 8 * c, there);
+            copy16_if(base + i * kRows * (DP * 2) + ((c ^ (r & 7)) << 4), rows.row(key < end ? key : t0) + 8 * c, key < end);
         }
     } else {
 #pragma unroll 1
         for (int i = lane; i < kTile * DP; i += 32) {
             const int r = i / DP, d = i % DP, key = t0 + r;
             unsigned short x = 0;
-            if (key < end && d < hd) {
-                const T *src = key < n_pre ? pre + key * pre_stride : own + (key - n_pre) * own_stride;
-                x = __ldg(reinterpret_cast<const unsigned short *>(src) + d);
-            }
+            if (key < end && d < hd) x = __ldg(reinterpret_cast<const unsigned short *>(rows.row(key)) + d);
             *reinterpret_cast<unsigned short *>(dst + r * (DP * 2) + (((d >> 3) ^ (r & 7)) << 4) + 2 * (d & 7)) = x;
         }
     }
 }
 
-template <class T, int DP, int R, bool kVec, int N>
+template <class T, int DP, int W, bool kVec, int N>
 __global__ void __launch_bounds__(32 * kRowWarps, DP <= 128 ? 2 : 1)
     ragged_rows_kernel(const __grid_constant__ RaggedArgs a, const __grid_constant__ RunList<RaggedRun, N> l) {
-    using C = RowCfg<DP, R>;
+    using C = RowCfg<DP, W>;
+    constexpr int kTile = C::kTile, kStep = kTile * kRowWarps, MT = kTile / 16;
     extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ float sm_m[kRowWarps][16 * R], sm_l[kRowWarps][16 * R];
+    __shared__ float sm_m[kRowWarps][8 * W], sm_l[kRowWarps][8 * W];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, c = lane & 3, mi = lane >> 3, mr = lane & 7;
     const int G = a.n_heads / a.n_kv, hd = a.hd;
@@ -125,25 +147,27 @@ __global__ void __launch_bounds__(32 * kRowWarps, DP <= 128 ? 2 : 1)
     int u = blockIdx.x - l.unit0[ri];
     const int kvh = u % a.n_kv;
     u /= a.n_kv;
-    const int rows = run.nq * G, n_blocks = ragged_row_units(rows, R);
-    const int split = u / n_blocks, row0 = (u - split * n_blocks) * 16 * R;
-    const int n_rows = min(16 * R, rows - row0);
+    const int rows = run.nq * G, n_blocks = ragged_row_units(rows, W);
+    const int split = u / n_blocks, row0 = (u - split * n_blocks) * 8 * W;
+    const int n_rows = min(8 * W, rows - row0);
     const int first = row0 / G, last = (row0 + n_rows - 1) / G;  // queries of the block
 
-    const int total = a.n_pre + run.nk;
-    const int per = ((total + run.ns - 1) / run.ns + kTile * kRowWarps - 1) / (kTile * kRowWarps) * (kTile * kRowWarps);
-    const long long beg = static_cast<long long>(split) * per;
-    const int kb = static_cast<int>(min(beg, static_cast<long long>(total)));
-    const int seen = a.n_pre + min(run.nk, run.off + last + 1);  // keys that some row sees
-    const int whole = a.n_pre + min(run.nk, run.off + first + 1);  // keys that all rows see
-    const int end = static_cast<int>(min(static_cast<long long>(min(total, seen)), beg + per));
+    const int n_pre = run.on_prefix ? 0 : a.n_pre, total = n_pre + run.nk;
+    const int per = ((total + run.ns - 1) / run.ns + kStep - 1) / kStep * kStep;
+    const int kb = static_cast<int>(min(static_cast<long long>(split) * per, static_cast<long long>(total)));
+    const int seen = n_pre + min(run.nk, run.off + last + 1);    // keys that some row sees
+    const int whole = n_pre + min(run.nk, run.off + first + 1);  // keys that all rows see
+    const int end = static_cast<int>(min(static_cast<long long>(seen), static_cast<long long>(kb) + per));
 
-    const T *Kp = static_cast<const T *>(a.Kp) + static_cast<int64_t>(kvh) * hd;
-    const T *Vp = static_cast<const T *>(a.Vp) + static_cast<int64_t>(kvh) * hd;
-    const T *K = static_cast<const T *>(a.K) + run.k0 * a.k_stride + static_cast<int64_t>(kvh) * hd;
-    const T *V = static_cast<const T *>(a.V) + run.k0 * a.v_stride + static_cast<int64_t>(kvh) * hd;
+    const int64_t head = static_cast<int64_t>(kvh) * hd;
+    KeyRows<T> K{static_cast<const T *>(a.Kp) + head, static_cast<const T *>(a.K) + run.k0 * a.k_stride + head, a.kp_stride, a.k_stride, n_pre};
+    KeyRows<T> V{static_cast<const T *>(a.Vp) + head, static_cast<const T *>(a.V) + run.k0 * a.v_stride + head, a.vp_stride, a.v_stride, n_pre};
+    if (run.on_prefix) {
+        K.own = K.pre, K.own_stride = K.pre_stride;
+        V.own = V.pre, V.own_stride = V.pre_stride;
+    }
 
-    unsigned char *Qs = smem, *ring = smem + C::kQ + warp * C::kStages * C::kStage;
+    unsigned char *ring = smem + warp * C::kStages * C::kStage;
     if (kVec && hd < DP) {  // columns that no copy writes
         const int pad = (DP - hd) / 8;
         for (int i = lane; i < C::kStages * 2 * kTile * pad; i += 32) {
@@ -153,182 +177,192 @@ __global__ void __launch_bounds__(32 * kRowWarps, DP <= 128 ? 2 : 1)
     }
     auto load = [&](int stage, int t0) {
         unsigned char *p = ring + stage * C::kStage;
-        load_tile<T, DP, kVec>(p, Kp, a.kp_stride, a.n_pre, K, a.k_stride, t0, end, hd, lane);
-        load_tile<T, DP, kVec>(p + C::kStage / 2, Vp, a.vp_stride, a.n_pre, V, a.v_stride, t0, end, hd, lane);
+        load_tile<T, DP, kTile, kVec>(p, K, t0, end, hd, lane);
+        load_tile<T, DP, kTile, kVec>(p + C::kStage / 2, V, t0, end, hd, lane);
     };
-    // the block's query rows, zeros behind them
-    for (int i = tid; i < 16 * R * DP / 8; i += 32 * kRowWarps) {
-        const int r = i / (DP / 8), ch = i % (DP / 8);
-        const bool there = r < n_rows && 8 * ch < hd;
-        const int qi = (row0 + (there ? r : 0)) / G, h = kvh * G + (row0 + (there ? r : 0)) % G;
-        const T *q = static_cast<const T *>(a.Q) + (static_cast<int64_t>(run.q0) + qi) * a.q_stride + static_cast<int64_t>(h) * hd;
-        unsigned char *dst = Qs + r * C::kPitch + ((ch ^ (r & 7)) << 4);
-        if constexpr (kVec) {
-            copy16(static_cast<uint32_t>(__cvta_generic_to_shared(dst)), q + (there ? 8 * ch : 0), there);
-        } else {
-            uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (there && 8 * ch + k < hd)
-                    w[k / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short *>(q) + 8 * ch + k)) << (16 * (k & 1));
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-    }
-    copies_commit();
-    const int t_first = kb + warp * kTile, n_tiles = end > t_first ? (end - t_first + kTile * kRowWarps - 1) / (kTile * kRowWarps) : 0;
+    const int t_first = kb + warp * kTile, n_tiles = end > t_first ? (end - t_first + kStep - 1) / kStep : 0;
     auto fill = [&] {
 #pragma unroll
         for (int i = 0; i < C::kStages - 1; ++i) {
-            if (i < n_tiles) load(i, t_first + i * kTile * kRowWarps);
+            if (i < n_tiles) load(i, t_first + i * kStep);
             copies_commit();
         }
     };
     fill();
-    copies_wait<C::kStages - 1>();
-    __syncthreads();
 
-    int lim[2 * R];  // rows g and g + 8 of each sixteen: keys that they see
-    float m[2 * R], sum[2 * R], o[R][DP / 8][4];
+    // Q as B: query rows g of each eight, dims 2c, 2c + 1 and + 8 of each sixteen
+    uint32_t q[W][DP / 16][2];
 #pragma unroll
-    for (int x = 0; x < 2 * R; ++x) {
-        const int r = row0 + 8 * x + g;
-        lim[x] = r < rows ? a.n_pre + min(run.nk, run.off + r / G + 1) : 0;
+    for (int w = 0; w < W; ++w) {
+        const int r = 8 * w + g;
+        const bool there = r < n_rows;
+        const int qi = (row0 + (there ? r : 0)) / G, h = kvh * G + (row0 + (there ? r : 0)) % G;
+        const T *src = static_cast<const T *>(a.Q) + (static_cast<int64_t>(run.q0) + qi) * a.q_stride + static_cast<int64_t>(h) * hd;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int d = 16 * k + 8 * e + 2 * c;
+                uint32_t x = 0;
+                if (there && d < hd) {
+                    if constexpr (kVec) {
+                        x = __ldg(reinterpret_cast<const unsigned int *>(src + d));
+                    } else {
+                        x = __ldg(reinterpret_cast<const unsigned short *>(src) + d);
+                        if (d + 1 < hd) x |= static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short *>(src) + d + 1)) << 16;
+                    }
+                }
+                q[w][k][e] = x;
+            }
     }
+    int lim[W][2];  // rows 2c and 2c + 1 of each eight: keys that they see
+    float m[W][2], sum[W][2], o[W][DP / 16][4];
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int r = row0 + 8 * w + 2 * c + y;
+            lim[w][y] = r < rows ? min(end, n_pre + min(run.nk, run.off + r / G + 1)) : 0;
+        }
     bool careful = false;
     for (;;) {
 #pragma unroll
-        for (int x = 0; x < 2 * R; ++x) m[x] = -INFINITY, sum[x] = 0.f;
+        for (int w = 0; w < W; ++w) {
+            m[w][0] = m[w][1] = -INFINITY;
+            sum[w][0] = sum[w][1] = 0.f;
 #pragma unroll
-        for (int x = 0; x < R; ++x)
-#pragma unroll
-            for (int i = 0; i < DP / 8; ++i) o[x][i][0] = o[x][i][1] = o[x][i][2] = o[x][i][3] = 0.f;
+            for (int i = 0; i < DP / 16; ++i) o[w][i][0] = o[w][i][1] = o[w][i][2] = o[w][i][3] = 0.f;
+        }
         int stage = 0;
 #pragma unroll 1
         for (int it = 0; it < n_tiles; ++it) {
-            const int t0 = t_first + it * kTile * kRowWarps;
+            const int t0 = t_first + it * kStep;
             copies_wait<C::kStages - 2>();
             __syncwarp();  // the tile has landed, and the slot of the one before it has been read
             const int next = it + C::kStages - 1;
-            if (next < n_tiles) load(stage == 0 ? C::kStages - 1 : stage - 1, t_first + next * kTile * kRowWarps);
+            if (next < n_tiles) load(stage == 0 ? C::kStages - 1 : stage - 1, t_first + next * kStep);
             copies_commit();
             unsigned char *Ks = ring + stage * C::kStage, *Vs = Ks + C::kStage / 2;
-            // ---- scores ----
-            float sc[R][2][4];
+            // ---- scores: keys g and g + 8 of each sixteen, rows 2c and 2c + 1 ----
+            float sc[MT][W][4];
 #pragma unroll
-            for (int x = 0; x < R; ++x)
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) sc[x][i][0] = sc[x][i][1] = sc[x][i][2] = sc[x][i][3] = 0.f;
+                for (int w = 0; w < W; ++w) sc[t][w][0] = sc[t][w][1] = sc[t][w][2] = sc[t][w][3] = 0.f;
 #pragma unroll
-            for (int k = 0; k < DP / 16; ++k) {
-                uint32_t kb4[4];  // keys mr (+ 8 by mi / 2), dims 16 k (+ 8 by mi % 2)
-                ldsm4<false>(kb4, Ks + (mr + 8 * (mi >> 1)) * C::kPitch + (((2 * k + (mi & 1)) ^ mr) << 4));
+            for (int k = 0; k < DP / 16; ++k)
 #pragma unroll
-                for (int x = 0; x < R; ++x) {
-                    uint32_t qa[4];
-                    ldsm4<false>(qa, Qs + (16 * x + mr + 8 * (mi & 1)) * C::kPitch + (((2 * k + (mi >> 1)) ^ mr) << 4));
-                    mma16<T>(sc[x][0], qa, kb4[0], kb4[1]);
-                    mma16<T>(sc[x][1], qa, kb4[2], kb4[3]);
+                for (int t = 0; t < MT; ++t) {
+                    uint32_t ka[4];  // keys mr (+ 8 by mi % 2), dims 16 k (+ 8 by mi / 2)
+                    ldsm4<false>(ka, Ks + (16 * t + mr + 8 * (mi & 1)) * C::kPitch + (((2 * k + (mi >> 1)) ^ mr) << 4));
+#pragma unroll
+                    for (int w = 0; w < W; ++w) mma16<T>(sc[t][w], ka, q[w][k][0], q[w][k][1]);
                 }
-            }
             // ---- softmax: reference, probabilities, sum ----
-            uint32_t hi[R][4], lo[R][4];  // as A: keys (2c, 2c + 1) and + 8, rows g and g + 8
+            const bool part = t0 + kTile > whole || t0 + kTile > end;
+            uint32_t hi[MT][W][2], lo[MT][W][2];  // as B
 #pragma unroll
-            for (int x = 0; x < R; ++x) {
+            for (int w = 0; w < W; ++w) {
                 float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int t = 0; t < MT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int key = t0 + 8 * i + 2 * c + (e & 1);
-                        sc[x][i][e] = key < min(lim[2 * x + (e >> 1)], end) ? sc[x][i][e] * a.scale_log2 : -INFINITY;
-                        top[e >> 1] = fmaxf(top[e >> 1], sc[x][i][e]);
+                        sc[t][w][e] *= a.scale_log2;
+                        if (part && t0 + 16 * t + 8 * (e >> 1) + g >= lim[w][e & 1]) sc[t][w][e] = -INFINITY;
+                        top[e & 1] = fmaxf(top[e & 1], sc[t][w][e]);
                     }
-                bool move = false;
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    top[y] = fmaxf(top[y], __shfl_xor_sync(kAll, top[y], 1));
-                    top[y] = fmaxf(top[y], __shfl_xor_sync(kAll, top[y], 2));
-                    move = move || top[y] > m[2 * x + y] + kHeadroom || (m[2 * x + y] == -INFINITY && top[y] != -INFINITY);
-                }
-                if (__any_sync(kAll, move)) {
+                if (__any_sync(kAll, top[0] > m[w][0] + kHeadroom || top[1] > m[w][1] + kHeadroom)) {  // (-inf: any score passes it)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const float mn = fmaxf(m[2 * x + y], top[y]);
-                        const float f = mn == m[2 * x + y] ? 1.f : pow2(m[2 * x + y] - mn);
-                        m[2 * x + y] = mn;
-                        sum[2 * x + y] *= f;
 #pragma unroll
-                        for (int i = 0; i < DP / 8; ++i) o[x][i][2 * y] *= f, o[x][i][2 * y + 1] *= f;
+                        for (int x = 4; x < 32; x <<= 1) top[y] = fmaxf(top[y], __shfl_xor_sync(kAll, top[y], x));
+                        const float mn = fmaxf(m[w][y], top[y]);
+                        const float f = mn == m[w][y] ? 1.f : pow2(m[w][y] - mn);
+                        m[w][y] = mn;
+                        sum[w][y] *= f;
+#pragma unroll
+                        for (int i = 0; i < DP / 16; ++i) o[w][i][y] *= f, o[w][i][2 + y] *= f;
                     }
                 }
+                const float ref[2] = {m[w][0] == -INFINITY ? 0.f : m[w][0], m[w][1] == -INFINITY ? 0.f : m[w][1]};
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int t = 0; t < MT; ++t) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float ref = m[2 * x + (e >> 1)];
-                        sc[x][i][e] = pow2(sc[x][i][e] - (ref == -INFINITY ? 0.f : ref));
-                        sum[2 * x + (e >> 1)] += sc[x][i][e];
+                        sc[t][w][e] = pow2(sc[t][w][e] - ref[e & 1]);
+                        sum[w][e & 1] += sc[t][w][e];
                     }
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const uint32_t h = pack2(T{}, sc[x][i][2 * y], sc[x][i][2 * y + 1]);
-                        hi[x][2 * i + y] = h;
-                        lo[x][2 * i + y] = pack2(T{}, sc[x][i][2 * y] - half_of(T{}, h, 0), sc[x][i][2 * y + 1] - half_of(T{}, h, 1));
+                    for (int e = 0; e < 2; ++e) {
+                        const float p0 = sc[t][w][2 * e], p1 = sc[t][w][2 * e + 1];
+                        const uint32_t h = pack2(T{}, p0, p1);
+                        hi[t][w][e] = turned(h);
+                        lo[t][w][e] = turned(pack2(T{}, p0 - half_of(T{}, h, 0), p1 - half_of(T{}, h, 1)));
                     }
                 }
             }
-            // ---- output ----
+            // ---- output: dims g and g + 8 of each sixteen, rows 2c and 2c + 1 ----
             // Zero times an infinity is NaN: where some row does not see all of the
             // tile, values of V that are not finite are added one by one, to the rows
             // that see them, and leave the tile.
             if (careful || min(t0 + kTile, end) > whole) {
                 constexpr uint32_t kE = std::is_same<T, bf16>::value ? 0x7f807f80u : 0x7c007c00u;
                 constexpr uint32_t kOne = std::is_same<T, bf16>::value ? 0x00800080u : 0x04000400u;
-                uint32_t seen = 0;  // a half's exponent is all ones where adding one to it reaches the sign bit
+                uint32_t odd = 0;  // a half's exponent is all ones where adding one to it reaches the sign bit
                 for (int i = lane; i < kTile * DP / 8; i += 32) {
                     const uint4 y = *reinterpret_cast<const uint4 *>(Vs + 16 * i);
-                    seen |= ((y.x & kE) + kOne) | ((y.y & kE) + kOne) | ((y.z & kE) + kOne) | ((y.w & kE) + kOne);
+                    odd |= ((y.x & kE) + kOne) | ((y.y & kE) + kOne) | ((y.z & kE) + kOne) | ((y.w & kE) + kOne);
                 }
-                if (__any_sync(kAll, seen & 0x80008000u)) {
+                if (__any_sync(kAll, odd & 0x80008000u)) {
 #pragma unroll 1
                     for (int k = 0; k < kTile; ++k)
 #pragma unroll
-                        for (int x = 0; x < 2 * R; ++x) {
-                            const float mine = k & 8 ? (k & 1 ? sc[x >> 1][1][2 * (x & 1) + 1] : sc[x >> 1][1][2 * (x & 1)])
-                                                     : (k & 1 ? sc[x >> 1][0][2 * (x & 1) + 1] : sc[x >> 1][0][2 * (x & 1)]);
-                            const float p = __shfl_sync(kAll, mine, (lane & ~3) | ((k & 7) >> 1));
-                            if (t0 + k >= min(lim[x], end)) continue;
+                        for (int w = 0; w < W; ++w)
 #pragma unroll
-                            for (int i = 0; i < DP / 8; ++i) {
-                                const uint32_t v = *reinterpret_cast<const uint32_t *>(Vs + k * C::kPitch + ((i ^ (k & 7)) << 4) + 4 * c);
-                                float *at = &o[x >> 1][i][2 * (x & 1)];
-                                if (not_finite<T>(v)) at[0] = fmaf(p, half_of(T{}, v, 0), at[0]);
-                                if (not_finite<T>(v >> 16)) at[1] = fmaf(p, half_of(T{}, v, 1), at[1]);
+                            for (int y = 0; y < 2; ++y) {
+                                float mine = sc[0][w][y];
+                                if (k & 8) mine = sc[0][w][2 + y];
+                                if constexpr (MT == 2) {
+                                    if (k & 16) mine = k & 8 ? sc[1][w][2 + y] : sc[1][w][y];
+                                }
+                                const float p = __shfl_sync(kAll, mine, 4 * (k & 7) + c);
+                                if (t0 + k >= lim[w][y]) continue;
+#pragma unroll
+                                for (int i = 0; i < DP / 8; ++i) {
+                                    const uint32_t v = *reinterpret_cast<const unsigned short *>(Vs + k * C::kPitch + ((i ^ (k & 7)) << 4) + 2 * g);
+                                    float &at = o[w][i >> 1][2 * (i & 1) + y];
+                                    if (not_finite<T>(v)) at = fmaf(p, half_of(T{}, v, 0), at);
+                                }
                             }
-                        }
                     __syncwarp();
                     for (int i = lane; i < kTile * DP / 2; i += 32) {
-                        uint32_t *w = reinterpret_cast<uint32_t *>(Vs) + i;
-                        if (not_finite<T>(*w)) *w &= 0xffff0000u;
-                        if (not_finite<T>(*w >> 16)) *w &= 0xffffu;
+                        uint32_t *v = reinterpret_cast<uint32_t *>(Vs) + i;
+                        if (not_finite<T>(*v)) *v &= 0xffff0000u;
+                        if (not_finite<T>(*v >> 16)) *v &= 0xffffu;
                     }
                     __syncwarp();
                 }
             }
 #pragma unroll
-            for (int k = 0; k < DP / 16; ++k) {
-                uint32_t vb[4];  // keys mr (+ 8 by mi % 2), dims 16 k (+ 8 by mi / 2)
-                ldsm4<true>(vb, Vs + (mr + 8 * (mi & 1)) * C::kPitch + (((2 * k + (mi >> 1)) ^ mr) << 4));
+            for (int i = 0; i < DP / 16; ++i) {
+                float t4[W][4];
 #pragma unroll
-                for (int x = 0; x < R; ++x) {
-                    float t[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                    mma16<T>(t[0], hi[x], vb[0], vb[1]);
-                    mma16<T>(t[1], hi[x], vb[2], vb[3]);
-                    mma16<T>(t[0], lo[x], vb[0], vb[1]);
-                    mma16<T>(t[1], lo[x], vb[2], vb[3]);
+                for (int w = 0; w < W; ++w) t4[w][0] = t4[w][1] = t4[w][2] = t4[w][3] = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[x][2 * k][e] += t[0][e], o[x][2 * k + 1][e] += t[1][e];
+                for (int t = 0; t < MT; ++t) {
+                    uint32_t va[4];  // keys mr (+ 8 by mi / 2), dims 16 i (+ 8 by mi % 2)
+                    ldsm4<true>(va, Vs + (16 * t + mr + 8 * (mi >> 1)) * C::kPitch + (((2 * i + (mi & 1)) ^ mr) << 4));
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        mma16<T>(t4[w], va, hi[t][w][0], hi[t][w][1]);
+                        mma16<T>(t4[w], va, lo[t][w][0], lo[t][w][1]);
+                    }
                 }
+#pragma unroll
+                for (int w = 0; w < W; ++w)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[w][i][e] += t4[w][e];
             }
             stage = stage + 1 == C::kStages ? 0 : stage + 1;
         }
@@ -339,11 +373,11 @@ __global__ void __launch_bounds__(32 * kRowWarps, DP <= 128 ? 2 : 1)
         if (careful) break;
         bool bad = false;
 #pragma unroll
-        for (int x = 0; x < R; ++x)
+        for (int w = 0; w < W; ++w)
 #pragma unroll
-            for (int i = 0; i < DP / 8; ++i)
+            for (int i = 0; i < DP / 16; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) bad = bad || o[x][i][e] != o[x][i][e];
+                for (int e = 0; e < 4; ++e) bad = bad || o[w][i][e] != o[w][i][e];
         if (!__any_sync(kAll, bad)) break;
         careful = true;
         __syncwarp();
@@ -352,29 +386,34 @@ __global__ void __launch_bounds__(32 * kRowWarps, DP <= 128 ? 2 : 1)
 
     // ---- the warps' parts ----
 #pragma unroll
-    for (int x = 0; x < 2 * R; ++x) {
-        sum[x] += __shfl_xor_sync(kAll, sum[x], 1);
-        sum[x] += __shfl_xor_sync(kAll, sum[x], 2);
-        if (c == 0) {
-            sm_m[warp][8 * x + g] = m[x];
-            sm_l[warp][8 * x + g] = sum[x];
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) sum[w][y] += __shfl_xor_sync(kAll, sum[w][y], x);
+            if (g == 0) {
+                sm_m[warp][8 * w + 2 * c + y] = m[w][y];
+                sm_l[warp][8 * w + 2 * c + y] = sum[w][y];
+            }
         }
-    }
     __syncthreads();  // (all rings have been read)
-    float *part = reinterpret_cast<float *>(smem);  // [warp][16 R][DP], a row's 16-byte chunks rotated by the row
+    float *out = reinterpret_cast<float *>(smem);  // [warp][8 W][kPart]
 #pragma unroll
-    for (int x = 0; x < 2 * R; ++x) {
-        const int r = 8 * x + g;
-        float top = sm_m[0][r];
+    for (int w = 0; w < W; ++w)
 #pragma unroll
-        for (int w = 1; w < kRowWarps; ++w) top = fmaxf(top, sm_m[w][r]);
-        const float f = pow2(m[x] - (top == -INFINITY ? 0.f : top));
-        float *dst = part + (warp * 16 * R + r) * DP;
+        for (int y = 0; y < 2; ++y) {
+            const int r = 8 * w + 2 * c + y;
+            float top = sm_m[0][r];
 #pragma unroll
-        for (int i = 0; i < DP / 8; ++i)
-            *reinterpret_cast<float2 *>(dst + ((8 * i + 2 * c + 8 * r) & (DP - 1))) =
-                make_float2(o[x >> 1][i][2 * (x & 1)] * f, o[x >> 1][i][2 * (x & 1) + 1] * f);
-    }
+            for (int x = 1; x < kRowWarps; ++x) top = fmaxf(top, sm_m[x][r]);
+            const float f = pow2(m[w][y] - (top == -INFINITY ? 0.f : top));
+            float *dst = out + (warp * 8 * W + r) * C::kPart + g;
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i) {
+                dst[16 * i] = o[w][i][y] * f;
+                dst[16 * i + 8] = o[w][i][2 + y] * f;
+            }
+        }
     __syncthreads();
     const int64_t H = a.n_heads;
     for (int i = tid; i < n_rows * (DP / 4); i += 32 * kRowWarps) {
@@ -387,7 +426,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, DP <= 128 ? 2 : 1)
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w) {
             L += sm_l[w][r] * pow2(sm_m[w][r] - (top == -INFINITY ? 0.f : top));
-            const float4 y = *reinterpret_cast<const float4 *>(part + (w * 16 * R + r) * DP + ((d + 8 * r) & (DP - 1)));
+            const float4 y = *reinterpret_cast<const float4 *>(out + (w * 8 * W + r) * C::kPart + d);
             v[0] += y.x, v[1] += y.y, v[2] += y.z, v[3] += y.w;
         }
         const int qi = (row0 + r) / G, h = kvh * G + (row0 + r) % G;
@@ -489,12 +528,12 @@ cudaError_t start(K *kernel, long long grid, int threads, size_t smem, bool over
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <class T, int DP, int R, bool kVec, int N>
+template <class T, int DP, int W, bool kVec, int N>
 cudaError_t rows_n(const RaggedArgs &a, const RaggedRun *runs, int32_t n, cudaStream_t s) {
-    using C = RowCfg<DP, R>;
+    using C = RowCfg<DP, W>;
     static PerDeviceOnce configured;  // the attribute is per function and device
     const cudaError_t ce = configured.run([&]() -> cudaError_t {
-        return cudaFuncSetAttribute(ragged_rows_kernel<T, DP, R, kVec, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(ragged_rows_kernel<T, DP, W, kVec, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(C::kSmem));
     });
     if (ce != cudaSuccess) return ce;
@@ -504,27 +543,30 @@ cudaError_t rows_n(const RaggedArgs &a, const RaggedRun *runs, int32_t n, cudaSt
     for (int32_t i = 0; i < n; ++i) {
         l.run[i] = runs[i];
         l.unit0[i] = static_cast<int32_t>(at);
-        at += static_cast<long long>(ragged_row_units(runs[i].nq * (a.n_heads / a.n_kv), R)) * runs[i].ns * a.n_kv;
+        at += static_cast<long long>(ragged_row_units(runs[i].nq * (a.n_heads / a.n_kv), W)) * runs[i].ns * a.n_kv;
         if (at > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     }
     l.unit0[n] = static_cast<int32_t>(at);
-    return start(ragged_rows_kernel<T, DP, R, kVec, N>, at, 32 * kRowWarps, C::kSmem, a.overlap, s, a, l);
+    return start(ragged_rows_kernel<T, DP, W, kVec, N>, at, 32 * kRowWarps, C::kSmem, a.overlap, s, a, l);
 }
-template <class T, int DP, int R, bool kVec>
+template <class T, int DP, int W, bool kVec>
 cudaError_t rows_l(const RaggedArgs &a, const RaggedRun *runs, int32_t n, cudaStream_t s) {
-    if (kVec && n <= kRaggedSmall) return rows_n<T, DP, R, kVec, kVec ? kRaggedSmall : kRaggedLarge>(a, runs, n, s);
-    return rows_n<T, DP, R, kVec, kRaggedLarge>(a, runs, n, s);
+    if (kVec && n <= kRaggedSmall) return rows_n<T, DP, W, kVec, kVec ? kRaggedSmall : kRaggedLarge>(a, runs, n, s);
+    return rows_n<T, DP, W, kVec, kRaggedLarge>(a, runs, n, s);
+}
+template <class T, int DP>
+cudaError_t rows_d(const RaggedArgs &a, const RaggedRun *runs, int32_t n, int wide, cudaStream_t s) {
+    if (!a.vec) return wide == 2 ? rows_l<T, DP, 2, false>(a, runs, n, s) : cudaErrorInvalidValue;
+    if (wide == 1) return rows_l<T, DP, 1, true>(a, runs, n, s);
+    if (wide == 2) return rows_l<T, DP, 2, true>(a, runs, n, s);
+    if constexpr (DP <= 128) return rows_l<T, DP, 4, true>(a, runs, n, s);
+    return cudaErrorInvalidValue;
 }
 template <class T>
 cudaError_t rows_t(const RaggedArgs &a, const RaggedRun *runs, int32_t n, int wide, cudaStream_t s) {
-    if (!a.vec) {
-        if (a.hd <= 64) return rows_l<T, 64, 1, false>(a, runs, n, s);
-        if (a.hd <= 128) return rows_l<T, 128, 1, false>(a, runs, n, s);
-        return rows_l<T, 256, 1, false>(a, runs, n, s);
-    }
-    if (a.hd <= 64) return wide == 2 ? rows_l<T, 64, 2, true>(a, runs, n, s) : rows_l<T, 64, 1, true>(a, runs, n, s);
-    if (a.hd <= 128) return wide == 2 ? rows_l<T, 128, 2, true>(a, runs, n, s) : rows_l<T, 128, 1, true>(a, runs, n, s);
-    return rows_l<T, 256, 1, true>(a, runs, n, s);
+    if (a.hd <= 64) return rows_d<T, 64>(a, runs, n, wide, s);
+    if (a.hd <= 128) return rows_d<T, 128>(a, runs, n, wide, s);
+    return rows_d<T, 256>(a, runs, n, wide, s);
 }
 
 template <class T, int N>
