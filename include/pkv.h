@@ -464,7 +464,8 @@ PKV_API int pkv_attn_packed(const void *Q, int64_t q_stride, const void *K, int6
  * of a request; neighbours with the same rows read them once):
  *   out[i, h] = softmax_j(scale * <Q[i, h], K[j, kv(h)]>) V[j, kv(h)]
  * over those rows, 0 where a sequence has none.  q_lens, k_lens, k_start: host
- * arrays, entries >= 0.  Element types, strides and head grouping as for
+ * arrays, entries >= 0.  q_rows: the rows that Q and out have, k_rows: those of K
+ * and V; a call that reaches past them is refused (PKV_ERR_ARG).  Element types, strides and head grouping as for
  * pkv_attn_packed; row counts up to 2^30.  Scores, softmax statistics and
  * outputs accumulate in f32, and the output is rounded once.  A key row that a
  * query does not see never reaches it, whatever it holds; one that it does see
@@ -482,9 +483,9 @@ PKV_API int pkv_attn_packed(const void *Q, int64_t q_stride, const void *K, int6
  * part of the graph).  Runs on `stream` and the current device.  Checks, in order: lengths and
  * sizes -> PKV_ERR_BAD_DIM, grouping -> PKV_ERR_BAD_GQA, dtype, strides,
  * workspace, pointers -> PKV_ERR_ARG. */
-PKV_API int pkv_attn_cross(const void *Q, int64_t q_stride, const int32_t *q_lens, const void *K, int64_t k_stride,
-                           const void *V, int64_t v_stride, const int32_t *k_lens, const int32_t *k_start,
-                           int32_t dtype, int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+PKV_API int pkv_attn_cross(const void *Q, int64_t q_stride, int64_t q_rows, const int32_t *q_lens, const void *K,
+                           int64_t k_stride, const void *V, int64_t v_stride, int64_t k_rows, const int32_t *k_lens,
+                           const int32_t *k_start, int32_t dtype, int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
                            float scale, void *out, int64_t out_stride, void *workspace, int64_t workspace_bytes,
                            pkv_stream_t stream);
 PKV_API int64_t pkv_attn_cross_workspace(const int32_t *q_lens, const int32_t *k_lens, const int32_t *k_start,
@@ -499,10 +500,10 @@ PKV_API int64_t pkv_attn_cross_workspace(const int32_t *q_lens, const int32_t *k
  * q_lens[s] (PKV_ERR_BAD_DIM); prefix_len 0 and sequences without queries are
  * fine.  The prefix is read and multiplied once for the rows of all sequences
  * that have few queries.  Everything else as for pkv_attn_cross. */
-PKV_API int pkv_attn_prefix(const void *Q, int64_t q_stride, const int32_t *q_lens, const void *K_prefix,
-                            int64_t kp_stride, const void *V_prefix, int64_t vp_stride, int32_t prefix_len,
-                            const void *K, int64_t k_stride, const void *V, int64_t v_stride, const int32_t *k_lens,
-                            const int32_t *k_start, int32_t dtype, int32_t n_seqs, int32_t n_heads,
+PKV_API int pkv_attn_prefix(const void *Q, int64_t q_stride, int64_t q_rows, const int32_t *q_lens,
+                            const void *K_prefix, int64_t kp_stride, const void *V_prefix, int64_t vp_stride,
+                            int32_t prefix_len, const void *K, int64_t k_stride, const void *V, int64_t v_stride,
+                            int64_t k_rows, const int32_t *k_lens, const int32_t *k_start, int32_t dtype, int32_t n_seqs, int32_t n_heads,
                             int32_t n_kv_heads, int32_t head_dim, float scale, void *out, int64_t out_stride,
                             void *workspace, int64_t workspace_bytes, pkv_stream_t stream);
 PKV_API int64_t pkv_attn_prefix_workspace(int32_t prefix_len, const int32_t *q_lens, const int32_t *k_lens,

@@ -86,11 +86,11 @@ _SIGS = {
     "pkv_pool_v_scales": (_vp, [_vp]),
     "pkv_attn_packed": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i32, _pi32, _i32, _i32, _i32, _i32, _i32, _f32,
                                _vp, _i64, _vp]),
-    "pkv_attn_cross": (_int, [_vp, _i64, _pi32, _vp, _i64, _vp, _i64, _pi32, _pi32, _i32, _i32, _i32, _i32, _i32, _f32,
+    "pkv_attn_cross": (_int, [_vp, _i64, _i64, _pi32, _vp, _i64, _vp, _i64, _i64, _pi32, _pi32, _i32, _i32, _i32, _i32, _i32, _f32,
                               _vp, _i64, _vp, _i64, _vp]),
     "pkv_attn_cross_workspace": (_i64, [_pi32, _pi32, _pi32, _i32, _i32, _i32, _i32]),
-    "pkv_attn_prefix": (_int, [_vp, _i64, _pi32, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _pi32, _pi32, _i32,
-                               _i32, _i32, _i32, _i32, _f32, _vp, _i64, _vp, _i64, _vp]),
+    "pkv_attn_prefix": (_int, [_vp, _i64, _i64, _pi32, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _i64, _pi32, _pi32,
+                               _i32, _i32, _i32, _i32, _i32, _f32, _vp, _i64, _vp, _i64, _vp]),
     "pkv_attn_prefix_workspace": (_i64, [_i32, _pi32, _pi32, _i32, _i32, _i32, _i32]),
     "pkv_rope_packed": (_int, [_vp, _i64, _vp, _i64, _i32, _vp, _i64, _i32, _pi32, _i32, _i32, _i32, _i32, _i32,
                                ctypes.c_double, _i32, _vp, _i64, _vp, _i64, _vp]),
@@ -183,6 +183,7 @@ def _dev(t, name="tensor", dtypes=("float32",)):
     return t.data_ptr()
 
 
+_int32 = None
 _packed = {}  # torch dtype -> PKV_F32 ..., filled at the first use
 
 
@@ -488,33 +489,68 @@ def pkv_attn_packed(Q, K, V, lens, n_heads, n_kv_heads, head_dim, causal, scale,
                                 scale, o, os_, _stream(stream))
 
 
-def _workspace(t):
-    """(address, bytes) of a workspace: a contiguous CUDA tensor, or None."""
+def _matrix(t, name, width):
+    """(address, row stride, rows) of packed rows, the library checks how many are needed; the callers look at type and
+    device, which _element does for all of a call's tensors."""
+    try:
+        (n, w), (stride, inner) = t.shape, t.stride()
+        if w == width and (inner == 1 or w == 1):
+            return t.data_ptr(), stride if n > 1 or stride > w else w, n
+    except (AttributeError, TypeError, ValueError):
+        raise TypeError("%s must be a CUDA tensor [rows, width]" % name) from None
+    raise TypeError("%s must be %d wide, with contiguous rows" % (name, width))
+
+
+def _element(a, *others):
+    """Element type of a call's rows, which are all of it and on the current device."""
+    if not _packed:
+        import torch
+        _packed.update({torch.float32: PKV_F32, torch.bfloat16: PKV_BF16, torch.float16: PKV_F16})
+    global _current_device
+    if _current_device is None:
+        _same_device(a, a, a, a)
+    try:
+        kind, device = a.dtype, a.get_device()
+        for t in others:
+            if t.dtype is not kind:
+                raise TypeError("the rows must have one element type")
+            if t.get_device() != device:
+                raise TypeError("the tensors must be on one device")
+    except AttributeError:
+        raise TypeError("rows must be CUDA tensors") from None
+    if device < 0:
+        raise TypeError("rows must be CUDA tensors")
+    if device != _current_device():
+        raise TypeError("the tensors must be on the current device")
+    kind = _packed.get(kind)
+    if kind is None:
+        raise TypeError("rows must be float32, bfloat16 or float16")
+    return kind
+
+
+def _workspace(t, like):
+    """(address, bytes) of a workspace: a contiguous CUDA tensor on the device of `like`, or None."""
     if t is None:
         return None, 0
     try:
-        if not t.is_cuda or not t.is_contiguous():
-            raise TypeError("workspace must be a contiguous CUDA tensor")
-        return t.data_ptr(), t.numel() * t.element_size()
+        if t.is_contiguous() and t.get_device() == like.get_device():
+            return t.data_ptr(), t.nbytes
     except AttributeError:
-        raise TypeError("workspace must be a contiguous CUDA tensor") from None
+        pass
+    raise TypeError("workspace must be a contiguous CUDA tensor on the tensors' device")
 
 
-def _stretches(q_lens, k_lens, k_start):
-    """The lengths as int32 arrays, and the rows of Q and of K that they reach."""
-    q, k, n = _i32_array(q_lens), _i32_array(k_lens), len(q_lens)
+def _lengths(q_lens, k_lens, k_start):
+    """The lengths as int32 arrays, and how many sequences there are."""
+    n = len(q_lens)
     if len(k_lens) != n or (k_start is not None and len(k_start) != n):
         raise TypeError("q_lens, k_lens and k_start need an entry for each of the %d sequences" % n)
-    if k_start is None:
-        return q, k, None, n, _total(q, n), _total(k, n)
-    k0 = _i32_array(k_start)
-    reach = max((a + b for a, b in zip(k0[:n], k[:n]) if b > 0), default=0)
-    return q, k, k0, n, _total(q, n), reach
+    return _i32_array(q_lens), _i32_array(k_lens), None if k_start is None else _i32_array(k_start), n
 
 
 def pkv_attn_cross_workspace(q_lens, k_lens, n_heads, n_kv_heads, head_dim, k_start=None):
     """Bytes that pkv_attn_cross would like as workspace; -1 on bad arguments (pkv_last_error())."""
-    q, k, k0, n, _, _ = _stretches(q_lens, k_lens, k_start)
+    q, k, k0, n = _lengths(q_lens, k_lens, k_start)
     return _lib.pkv_attn_cross_workspace(q, k, k0, n, n_heads, n_kv_heads, head_dim)
 
 
@@ -524,24 +560,20 @@ def pkv_attn_cross(Q, q_lens, K, V, k_lens, n_heads, n_kv_heads, head_dim, scale
     CUDA tensors with contiguous rows (any row stride); q_lens, k_lens: queries and keys per sequence;
     k_start: first key row of each (None: behind one another); workspace: a CUDA tensor of
     pkv_attn_cross_workspace bytes (or fewer, or None)."""
-    ql, kl, k0, n, nq, nk = _stretches(q_lens, k_lens, k_start)
-    _same_device(Q, K, V, out)
-    q, qs, t, _ = _rows(Q, "Q", nq, n_heads * head_dim)
-    k, ks, tk, _ = _rows(K, "K", nk, n_kv_heads * head_dim)
-    v, vs, tv, _ = _rows(V, "V", nk, n_kv_heads * head_dim)
-    o, os_, to, _ = _rows(out, "out", nq, n_heads * head_dim)
-    if not t == tk == tv == to:
-        raise TypeError("Q, K, V and out must have one element type")
-    w, wn = _workspace(workspace)
-    if w is not None and workspace.get_device() != Q.get_device():
-        raise TypeError("the workspace must be on the tensors' device")
-    return _lib.pkv_attn_cross(q, qs, ql, k, ks, v, vs, kl, k0, t, n, n_heads, n_kv_heads, head_dim, scale, o, os_,
-                               w, wn, _stream(stream))
+    ql, kl, k0, n = _lengths(q_lens, k_lens, k_start)
+    kind, qw, kw = _element(Q, K, V, out), n_heads * head_dim, n_kv_heads * head_dim
+    q, qs, qn = _matrix(Q, "Q", qw)
+    k, ks, kn = _matrix(K, "K", kw)
+    v, vs, vn = _matrix(V, "V", kw)
+    o, os_, on = _matrix(out, "out", qw)
+    w, wn = _workspace(workspace, Q)
+    return _lib.pkv_attn_cross(q, qs, qn if qn < on else on, ql, k, ks, v, vs, kn if kn < vn else vn, kl, k0, kind, n,
+                               n_heads, n_kv_heads, head_dim, scale, o, os_, w, wn, _stream(stream))
 
 
 def pkv_attn_prefix_workspace(prefix_len, q_lens, k_lens, n_heads, n_kv_heads, head_dim):
     """Bytes that pkv_attn_prefix would like as workspace; -1 on bad arguments (pkv_last_error())."""
-    q, k, _, n, _, _ = _stretches(q_lens, k_lens, None)
+    q, k, _, n = _lengths(q_lens, k_lens, None)
     return _lib.pkv_attn_prefix_workspace(prefix_len, q, k, n, n_heads, n_kv_heads, head_dim)
 
 
@@ -549,24 +581,19 @@ def pkv_attn_prefix(Q, q_lens, K_prefix, V_prefix, K, V, k_lens, n_heads, n_kv_h
                     k_start=None, workspace=None, stream=None):
     """As pkv_attn_cross; K_prefix, V_prefix: [prefix rows, n_kv_heads * head_dim], seen by every sequence;
     k_lens counts a sequence's own keys, the last q_lens of which belong to its queries."""
-    ql, kl, k0, n, nq, nk = _stretches(q_lens, k_lens, k_start)
-    _same_device(Q, K, V, out)
-    _same_device(Q, K_prefix, V_prefix, out)
-    q, qs, t, _ = _rows(Q, "Q", nq, n_heads * head_dim)
-    k, ks, tk, _ = _rows(K, "K", nk, n_kv_heads * head_dim)
-    v, vs, tv, _ = _rows(V, "V", nk, n_kv_heads * head_dim)
-    p, ps, tp, _ = _rows(K_prefix, "K_prefix", 0, n_kv_heads * head_dim)
-    x, xs, tx, _ = _rows(V_prefix, "V_prefix", 0, n_kv_heads * head_dim)
-    o, os_, to, _ = _rows(out, "out", nq, n_heads * head_dim)
-    if not t == tk == tv == tp == tx == to:
-        raise TypeError("Q, K, V, the prefix and out must have one element type")
-    if K_prefix.shape[0] != V_prefix.shape[0]:
+    ql, kl, k0, n = _lengths(q_lens, k_lens, k_start)
+    kind, qw, kw = _element(Q, K, V, K_prefix, V_prefix, out), n_heads * head_dim, n_kv_heads * head_dim
+    q, qs, qn = _matrix(Q, "Q", qw)
+    k, ks, kn = _matrix(K, "K", kw)
+    v, vs, vn = _matrix(V, "V", kw)
+    p, ps, pn = _matrix(K_prefix, "K_prefix", kw)
+    x, xs, xn = _matrix(V_prefix, "V_prefix", kw)
+    o, os_, on = _matrix(out, "out", qw)
+    if pn != xn:
         raise TypeError("K_prefix and V_prefix must have the same rows")
-    w, wn = _workspace(workspace)
-    if w is not None and workspace.get_device() != Q.get_device():
-        raise TypeError("the workspace must be on the tensors' device")
-    return _lib.pkv_attn_prefix(q, qs, ql, p, ps, x, xs, K_prefix.shape[0], k, ks, v, vs, kl, k0, t, n, n_heads,
-                                n_kv_heads, head_dim, scale, o, os_, w, wn, _stream(stream))
+    w, wn = _workspace(workspace, Q)
+    return _lib.pkv_attn_prefix(q, qs, qn if qn < on else on, ql, p, ps, x, xs, pn, k, ks, v, vs, kn if kn < vn else vn,
+                                kl, k0, kind, n, n_heads, n_kv_heads, head_dim, scale, o, os_, w, wn, _stream(stream))
 
 
 def pkv_rope_packed(Q, K, positions, pairs, order, n_heads, n_kv_heads, head_dim, rope_base, Q_out, K_out,
@@ -575,34 +602,47 @@ def pkv_rope_packed(Q, K, positions, pairs, order, n_heads, n_kv_heads, head_dim
     float16 CUDA tensors with contiguous rows (Q or K may be None, with its output; an output may be its
     input); positions: int32 CUDA tensor [axes, tokens]; pairs: frequency pairs of each axis; order:
     PKV_ROPE_BLOCKS, PKV_ROPE_TURNS or PKV_ROPE_AXIAL; inverse turns back (the gradient)."""
-    arr = _i32_array(pairs)
+    global _int32
+    if _int32 is None:
+        import torch
+        _int32 = torch.int32
+    if Q is not None and K is not None:
+        kind = _element(Q, K, Q_out, K_out)
+    elif Q is not None or K is not None:
+        kind = _element(Q, Q_out) if K is None else _element(K, K_out)
+    else:
+        raise TypeError("Q or K must be given")
     try:
         (axes, rows), (pos_stride, inner) = positions.shape, positions.stride()
-        good = positions.is_cuda and str(positions.dtype) == "torch.int32" and (inner == 1 or rows <= 1)
-    except (AttributeError, TypeError, ValueError):
-        good = False
-    if not good:
+        if positions.dtype is not _int32 or not (inner == 1 or rows <= 1):
+            axes = -1
+        if positions.get_device() != (Q if Q is not None else K).get_device():
+            raise TypeError("positions must be on the rows' device")
+    except (AttributeError, ValueError):
+        axes = -1
+    if axes < 0:
         raise TypeError("positions must be an int32 CUDA tensor [axes, tokens] with contiguous rows")
     if axes != len(pairs):
         raise TypeError("positions has %d axes, pairs %d" % (axes, len(pairs)))
     q = k = qo = ko = None
     qs = ks = qos = kos = 0
-    kinds = set()
-    if Q is not None or Q_out is not None:
-        _same_device(positions, Q, Q_out, positions)
-        q, qs, t, _ = _rows(Q, "Q", rows, n_heads * head_dim)
-        qo, qos, to, _ = _rows(Q_out, "Q_out", rows, n_heads * head_dim)
-        kinds.update((t, to))
-    if K is not None or K_out is not None:
-        _same_device(positions, K, K_out, positions)
-        k, ks, t, _ = _rows(K, "K", rows, n_kv_heads * head_dim)
-        ko, kos, to, _ = _rows(K_out, "K_out", rows, n_kv_heads * head_dim)
-        kinds.update((t, to))
-    if len(kinds) > 1:
-        raise TypeError("the rows must have one element type")
-    return _lib.pkv_rope_packed(q, qs, k, ks, kinds.pop() if kinds else PKV_F32, positions.data_ptr(),
-                                max(pos_stride, rows), axes, arr, order, rows, n_heads, n_kv_heads, head_dim,
-                                float(rope_base), 1 if inverse else 0, qo, qos, ko, kos, _stream(stream))
+    if Q is not None:
+        q, qs, n = _matrix(Q, "Q", n_heads * head_dim)
+        qo, qos, m = _matrix(Q_out, "Q_out", n_heads * head_dim)
+        if n < rows or m < rows:
+            raise TypeError("Q and Q_out need %d rows" % rows)
+    elif Q_out is not None:
+        raise TypeError("Q_out without Q")
+    if K is not None:
+        k, ks, n = _matrix(K, "K", n_kv_heads * head_dim)
+        ko, kos, m = _matrix(K_out, "K_out", n_kv_heads * head_dim)
+        if n < rows or m < rows:
+            raise TypeError("K and K_out need %d rows" % rows)
+    elif K_out is not None:
+        raise TypeError("K_out without K")
+    return _lib.pkv_rope_packed(q, qs, k, ks, kind, positions.data_ptr(), pos_stride if pos_stride > rows else rows, axes,
+                                _i32_array(pairs), order, rows, n_heads, n_kv_heads, head_dim, rope_base,
+                                1 if inverse else 0, qo, qos, ko, kos, _stream(stream))
 
 
 def pkv_append_packed(seqs, n, layer, K, V):

@@ -163,7 +163,7 @@ __device__ __forceinline__ int work_of(uint32_t answer) {
 // Whole prompts: every sequence's queries attend its own keys.
 template <int N>
 struct WholePrompts {
-    static constexpr bool kRuns = false;
+    static constexpr bool kRuns = false, kStacks = false;
     using Args = PackedArgs;
     using List = PackedSeqs<N>;
     // What block index w of the grid stands for.
@@ -204,7 +204,7 @@ struct WholePrompts {
 // chain, seen or not, so that every row's record is written.
 template <int N>
 struct Runs {
-    static constexpr bool kRuns = true;
+    static constexpr bool kRuns = true, kStacks = false;
     using Args = RaggedArgs;
     using List = RunList<RaggedRun, N>;
     struct Piece {
@@ -253,6 +253,58 @@ struct Runs {
     __device__ __forceinline__ static int key0(const Args &a, const Piece &p, int j) {
         return max(0, min(p.nk, p.off + p.q0 + 1) - (p.j0 + j - (a.n_pre + kKeys - 1) / kKeys) * kKeys);
     }
+};
+
+// The queries of neighbouring sequences as one stretch of rows behind the
+// shared prefix, own key rows in the same order: a tile may hold rows of several
+// sequences, and its own keys are those of all of them, of which a row
+// sees a stretch.  A list holds one such stretch.
+template <int N>
+struct Stacks : Runs<N> {
+    static constexpr bool kStacks = true;
+    using typename Runs<N>::Args;
+    using typename Runs<N>::List;
+    using typename Runs<N>::Piece;
+    // The sequence of row t of the stretch.
+    __device__ __forceinline__ static int seq(const List &l, int t) {
+        const int q = l.run[0].q0 + t;
+        int lo = 0, hi = l.n - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (l.run[mid].q0 <= q) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo;
+    }
+    // Key row behind the last one that row t sees.
+    __device__ __forceinline__ static int end(const RaggedRun &r, const List &l, int t) {
+        return r.k0 + r.off + (l.run[0].q0 + t - r.q0) + 1;
+    }
+    __device__ __forceinline__ static Piece piece(const Args &a, const List &l, int log_p, int w) {
+        Piece p;
+        const int TQ = 128 >> log_p, n_ht = a.n_heads >> log_p;
+        const int u = w / n_ht, ht = w - u * n_ht;
+        p.row0 = l.run[0].q0;
+        p.len = l.run[l.n - 1].q0 + l.run[l.n - 1].nq - p.row0;
+        p.ns = l.run[0].ns;
+        const int pairs = (p.len + 2 * TQ - 1) / (2 * TQ), split = u / pairs;
+        p.q0 = (pairs - 1 - (u - split * pairs)) * 2 * TQ;
+        p.h0 = ht << log_p;
+        p.kvh = p.h0 / (a.n_heads / a.n_kv);
+        p.rec = l.run[0].rec0 < 0 ? -1 : l.run[0].rec0 + split;
+        p.off = p.pad0 = p.pad1 = 0;
+        const int last0 = min(p.q0 + TQ, p.len) - 1, last = min(p.q0 + 2 * TQ, p.len) - 1;
+        p.k0 = l.run[seq(l, p.q0)].k0;
+        p.nk = end(l.run[seq(l, last)], l, last) - p.k0;
+        const int pre = (a.n_pre + kKeys - 1) / kKeys, all = pre + (p.nk + kKeys - 1) / kKeys, per = (all + p.ns - 1) / p.ns;
+        p.j0 = split * per;
+        const int mid = end(l.run[seq(l, last0)], l, last0) - p.k0;
+        p.n0 = max(1, min(pre + (mid + kKeys - 1) / kKeys - p.j0, per));
+        p.n1 = last == last0 ? 0 : max(1, min(all - p.j0, per));
+        p.look0 = max(0, pre - p.j0);
+        return p;
+    }
+    __device__ __forceinline__ static int key0(const Args &, const Piece &, int) { return 0; }
 };
 
 // Barriers.  Every role counts ring items (K_0, V_0, K_1, ... of one piece after
@@ -541,8 +593,12 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
             const int n = c ? p.n1 : p.n0;
             const int tok = p.q0 + c * TQ + (m >> log_p);
             const bool valid = tok < p.len;
-            int lim;  // keys this row sees (Runs: of the run's own)
-            if constexpr (F::kRuns) lim = min(p.nk, p.off + tok + 1);
+            int lim, from = 0;  // keys this row sees (Runs: of the run's own)
+            if constexpr (F::kStacks) {
+                const RaggedRun &r = l.run[F::seq(l, valid ? tok : p.q0)];
+                from = r.k0 - p.k0;
+                lim = F::end(r, l, valid ? tok : p.q0) - p.k0;
+            } else if constexpr (F::kRuns) lim = min(p.nk, p.off + tok + 1);
             else lim = a.causal ? min(tok + 1, p.len) : p.len;
             float m_ref = -INFINITY, l_run = 0.f, unit = 0.f;
             uint32_t hold[kLong ? D / 4 : 1];  // with it the output's sum is O + h * unit
@@ -626,6 +682,12 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
                         const int t = p.j0 + j, pre = (a.n_pre + kKeys - 1) / kKeys;
                         base = (t < pre ? t : t - pre) * kKeys;
                         end = t < pre ? a.n_pre : lim;
+                        if constexpr (F::kStacks) {
+                            if (t >= pre && base < from) {
+#pragma unroll
+                                for (int i = 0; i < kKeys; ++i) x[i] = base + i >= from ? x[i] : 0xff800000u;
+                            }
+                        }
                     }
                     if (base + kKeys > end) {
 #pragma unroll
@@ -698,6 +760,9 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
 #pragma unroll
                                     for (int e = 0; e < 2; ++e) {
                                         if (2 * kk + e >= see) continue;
+                                        if constexpr (F::kStacks) {
+                                            if (base + 2 * kk + e < from) continue;
+                                        }
                                         const unsigned short *vr = reinterpret_cast<const unsigned short *>(
                                             v + static_cast<int64_t>(2 * kk + e) * a.v_stride) + 16 * i;
                                         const float pe = half_of(T{}, pw, e);

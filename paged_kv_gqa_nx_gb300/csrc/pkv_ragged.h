@@ -15,13 +15,17 @@ namespace pkv {
 
 constexpr int32_t kSees = 0x3fffffff;  // `off` of a run whose queries see every key
 
+// What a run of the row kernel is: its own keys (behind the prefix, where the
+// launch has one), or the prefix's rows themselves (k0 0, nk all of them).
+constexpr int32_t kOwnKeys = 0, kOnPrefix = 1;
+
 struct RaggedRun {
     int32_t q0, nq;    // first row of Q and out, queries
     int32_t k0, nk;    // first key row, keys
     int32_t off;       // query i sees the run's keys j <= off + i
     int32_t ns;        // splits of the prefix and the run's keys together
     int32_t rec0;      // record of (query i, split x): rec0 + i * ns + x; -1: one split, written to out
-    int32_t on_prefix; // the keys are the prefix's rows themselves (k0 0, nk all of them)
+    int32_t kind;
 };
 
 // A query's records: ns of its own keys and pns of the shared prefix.
@@ -51,6 +55,7 @@ struct RaggedArgs {
     Elem type;
     float *pm, *pl, *pacc;                            // records: [rec][head], [rec][head], [rec][head][hd]
     int32_t *err;
+    int32_t cluster;  // blocks of a cluster (1: none), which split a unit's keys in place of ns
     int32_t out32;  // out's rows and heads start on 32-byte boundaries (set by the launcher)
     bool vec;       // rows on 16-byte boundaries, heads of whole 16 bytes
     bool overlap;   // the launch may start before the one in front of it on the stream has ended
@@ -75,7 +80,9 @@ constexpr int32_t ragged_split_tiles(int32_t n_pre, const RaggedRun &r) { return
 inline bool ragged_tc_takes(const RaggedArgs &a) {
     return a.vec && a.hd <= 128 && a.scale_log2 > 0.f && a.scale_log2 <= 3e38f;
 }
-cudaError_t launch_ragged_tc(const RaggedArgs &a, const RaggedRun *runs, int32_t n, cudaStream_t s);
+// stack: the runs are sequences whose queries and own key rows follow one
+// another; their tiles are those of the whole stretch (ns and rec0 of the first count).
+cudaError_t launch_ragged_tc(const RaggedArgs &a, const RaggedRun *runs, int32_t n, bool stack, cudaStream_t s);
 
 // Few query rows by warp-level MMAs (pkv_ragged_rows.cu): units of 8 * wide
 // rows ((query, head of the group) pairs) of one kv head; wide 1, 2 or, for heads up to 128, 4

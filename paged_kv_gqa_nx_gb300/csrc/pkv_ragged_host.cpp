@@ -58,10 +58,11 @@ struct Seq {
 struct Plan {
     std::vector<RaggedRun> tiles_pre;    // the prefix, for the stacked rows of sequences with few
     std::vector<RaggedRun> tiles, rows;  // own keys (behind the prefix, unless stacked); rows: of the prefix too
+    std::vector<std::vector<RaggedRun>> stretches;  // sequences that share tiles, behind the prefix
     std::vector<JoinRun> joins;
     int64_t n_rec = 0;
     bool stacked = false;
-    int wide = 1;
+    int wide = 1, cluster = 1;
 };
 
 // What a call's kernels go by besides its lengths.
@@ -72,6 +73,10 @@ struct Kernels {
 int64_t record_bytes(int64_t n_rec, const Shape &sh) {
     return 4 * (2 * static_cast<int64_t>(record_floats(n_rec, sh.n_heads)) + n_rec * sh.n_heads * sh.hd);
 }
+
+// Keys of a cluster's block up to which a cluster is worth it: with more, more
+// blocks than a cluster has are.
+constexpr int64_t kClusterKeys = 512;
 
 // Query rows a unit of the row kernel takes, in eights: a unit reads its keys
 // once, which costs about as much as the arithmetic of two eights.
@@ -87,17 +92,62 @@ int pick_wide(const std::vector<RaggedRun> &runs, const Shape &sh, const Kernels
     return best;
 }
 
-// Splits of the row kernel: as many keys a split as give the GPU's resident
-// blocks (two a SM, one of wide heads) about three units each, so that the last
-// ones are a small part of the whole; `coarse` times as many where the workspace
-// is short.  A unit of fewer than 256 keys (64 a warp) is mostly latency.
+// Units of the row kernel that the GPU holds at once: four blocks a SM, two of wide heads.
+int64_t row_slots(const Shape &sh) { return static_cast<int64_t>(kSMs) * (sh.hd > 128 ? 2 : 4); }
+
+// The least number of keys (or key tiles) a split, from `least` to `most`, with which
+// no more than `room` units come out; total(per) counts them.
+template <class F>
+int64_t least_split(int64_t least, int64_t most, int64_t room, F &&total) {
+    while (least < most) {
+        const int64_t mid = least + (most - least) / 2;
+        if (total(mid) <= room) most = mid;
+        else least = mid + 1;
+    }
+    return least;
+}
+
+// Splits of the row kernel.  Where there are few units, three quarters of what the GPU holds at once
+// (three documents of 50,000 to 120,000 keys: 208 us, with all of it 218, with twice as
+// many 216); where whole runs nearly fill it, runs
+// longer than two thirds of a slot's share are split, so that the last ones end
+// with the others.  `coarse` times as many keys a split where the workspace is
+// short.  A split below 256 keys is mostly latency.
 void split_rows(std::vector<RaggedRun> &runs, const Shape &sh, int wide, int64_t n_pre, int64_t coarse) {
-    int64_t work = 0;
-    auto keys = [&](const RaggedRun &r) { return (r.on_prefix ? 0 : n_pre) + r.nk; };
-    for (const RaggedRun &r : runs) work += static_cast<int64_t>(ragged_row_units(r.nq * sh.group(), wide)) * sh.n_kv * keys(r);
-    const int64_t units = static_cast<int64_t>(kSMs) * (sh.hd > 128 ? 1 : 2) * 3;
-    const int64_t per = std::max<int64_t>(256, (work + units - 1) / units) * coarse;
+    int64_t work = 0, units = 0, most = 256;
+    auto keys = [&](const RaggedRun &r) { return (r.kind == kOnPrefix ? 0 : n_pre) + r.nk; };
+    auto blocks = [&](const RaggedRun &r) { return static_cast<int64_t>(ragged_row_units(r.nq * sh.group(), wide)) * sh.n_kv; };
+    for (const RaggedRun &r : runs) {
+        units += blocks(r);
+        work += blocks(r) * keys(r);
+        most = std::max(most, keys(r));
+    }
+    const int64_t slots = row_slots(sh), room = slots * 3 / 2, few = slots * 3 / 4;
+    int64_t per = (work + room - 1) / room;
+    if (2 * units <= slots)
+        per = least_split(256, most, few, [&](int64_t x) {
+            int64_t n = 0;
+            for (const RaggedRun &r : runs) n += blocks(r) * ((keys(r) + x - 1) / x);
+            return n;
+        });
+    per = std::max<int64_t>(256, per) * coarse;
     for (RaggedRun &r : runs) r.ns = static_cast<int32_t>(std::clamp<int64_t>((keys(r) + per - 1) / per, 1, 128));
+}
+
+// Blocks of a cluster that share a unit's keys, for launches so small that
+// every block of every cluster runs at once and a join launch behind would
+// take as long as they do; 1: not such a launch.
+int pick_cluster(const std::vector<RaggedRun> &runs, const Shape &sh, const Kernels &k, int32_t n_pre) {
+    const int wide = pick_wide(runs, sh, k);
+    int64_t units = 0, most = 0;
+    for (const RaggedRun &r : runs) {
+        units += static_cast<int64_t>(ragged_row_units(r.nq * sh.group(), wide)) * sh.n_kv;
+        most = std::max<int64_t>(most, n_pre + r.nk);
+    }
+    const int64_t room = row_slots(sh);
+    int n = 1;
+    while (n < 8 && units * 2 * n <= room && most > 64 * n) n *= 2;
+    return most <= kClusterKeys * n ? n : 1;
 }
 
 // Splits of the tensor-core kernel, which runs a block a SM.  Where there are
@@ -113,18 +163,11 @@ void split_tiles(std::vector<RaggedRun> &runs, const Shape &sh, int32_t n_pre, i
     }
     if (pieces > 2 * kSMs) return;
     const int64_t room = pieces <= kSMs ? kSMs : 2 * kSMs;
-    auto total = [&](int64_t per) {
+    const int64_t per = coarse * least_split(2, std::max<int64_t>(2, most), room, [&](int64_t x) {
         int64_t n = 0;
-        for (const RaggedRun &r : runs) n += blocks(r) * ((ragged_key_tiles(n_pre, r.nk) + per - 1) / per);
+        for (const RaggedRun &r : runs) n += blocks(r) * ((ragged_key_tiles(n_pre, r.nk) + x - 1) / x);
         return n;
-    };
-    int64_t lo = 2, hi = std::max<int64_t>(2, most);  // the least tiles a split that fit
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) / 2;
-        if (total(mid) <= room) hi = mid;
-        else lo = mid + 1;
-    }
-    const int64_t per = lo * coarse;
+    });
     for (RaggedRun &r : runs) r.ns = static_cast<int32_t>((ragged_key_tiles(n_pre, r.nk) + per - 1) / per);
 }
 
@@ -132,19 +175,59 @@ void split_tiles(std::vector<RaggedRun> &runs, const Shape &sh, int32_t n_pre, i
 // sequence takes it.
 constexpr int64_t kTileRows = 48;
 
+// Stretches of neighbouring sequences that share tiles.  A tile's rows
+// multiply the own keys of all its sequences, so a sequence takes part where that is
+// no more than two tiles of keys, or half of the prefix, on top: a few tokens behind a long history of
+// their own do not.  More than four stretches (launches) and the rest go by themselves.
+std::vector<std::vector<Seq>> find_stretches(std::vector<Seq> &seqs, const Shape &sh, int32_t n_pre) {
+    const int log_p = ragged_log_p(sh.group());
+    const int64_t pair = 256 >> log_p, most = std::max<int64_t>(2, ragged_key_tiles(n_pre, 0) / 2);
+    std::vector<std::vector<Seq>> found;
+    std::vector<Seq> alone, run;
+    int64_t rows = 0;
+    auto close = [&] {
+        const bool take = run.size() > 1 && found.size() < 4 && (rows << log_p) >= kTileRows;
+        if (take) found.push_back(run);
+        else alone.insert(alone.end(), run.begin(), run.end());
+        run.clear();
+        rows = 0;
+    };
+    for (const Seq &s : seqs) {
+        const bool fits = s.off != kSees && s.off * pair <= 128 * most * s.nq && n_pre + s.nk <= 16384 - 256;
+        const bool follows = !run.empty() && s.q0 == run.back().q0 + run.back().nq && s.k0 >= run.back().k0 + run.back().nk &&
+                             s.k0 - (run.back().k0 + run.back().nk) <= 32;
+        if (!fits || (!run.empty() && !follows)) close();
+        if (!fits) {
+            alone.push_back(s);
+            continue;
+        }
+        run.push_back(s);
+        rows += s.nq;
+    }
+    close();
+    seqs = alone;
+    return found;
+}
+
 // The plan of up to kRaggedLarge sequences; with less workspace than it would
 // like, keys are split less, or not at all.
-Plan make_plan(const std::vector<Seq> &seqs, const Shape &sh, int32_t n_pre, const Kernels &kernels, int64_t workspace) {
+Plan make_plan(std::vector<Seq> seqs, const Shape &sh, int32_t n_pre, const Kernels &kernels, int64_t workspace) {
     constexpr int64_t kCoarsest = int64_t{1} << 24;
     const int log_p = ragged_log_p(sh.group());
     auto takes_tiles = [&](int64_t nq, int32_t keys) { return kernels.tc && keys > 0 && (nq << log_p) >= kTileRows; };
     std::vector<RaggedRun> own;
     Plan p;
+    if (kernels.tc)
+        for (const std::vector<Seq> &part : find_stretches(seqs, sh, n_pre)) {
+            p.stretches.emplace_back();
+            for (const Seq &s : part) p.stretches.back().push_back(RaggedRun{s.q0, s.nq, s.k0, s.nk, s.off, 1, -1, kOwnKeys});
+        }
     for (const Seq &s : seqs)
-        (takes_tiles(s.nq, n_pre + s.nk) ? p.tiles : own).push_back(RaggedRun{s.q0, s.nq, s.k0, s.nk, s.off, 1, -1, 0});
+        (takes_tiles(s.nq, n_pre + s.nk) ? p.tiles : own).push_back(RaggedRun{s.q0, s.nq, s.k0, s.nk, s.off, 1, -1, kOwnKeys});
     for (int64_t coarse = workspace < record_bytes(1, sh) ? 2 * kCoarsest : 1;; coarse *= 2) {
         const bool last = coarse > kCoarsest;
-        p.stacked = !last && n_pre >= 128 && own.size() > 1;
+        p.cluster = pick_cluster(own, sh, kernels, n_pre);
+        p.stacked = !last && p.cluster == 1 && n_pre >= 128 && own.size() > 1;
         p.rows.clear();
         p.tiles_pre.clear();
         p.joins.clear();
@@ -152,11 +235,12 @@ Plan make_plan(const std::vector<Seq> &seqs, const Shape &sh, int32_t n_pre, con
         if (p.stacked) {
             for (const RaggedRun &r : own) {
                 if (!stacks.empty() && stacks.back().q0 + stacks.back().nq == r.q0) stacks.back().nq += r.nq;
-                else stacks.push_back(RaggedRun{r.q0, r.nq, 0, n_pre, kSees, 1, -1, 1});
+                else stacks.push_back(RaggedRun{r.q0, r.nq, 0, n_pre, kSees, 1, -1, kOnPrefix});
             }
             for (RaggedRun &r : stacks) {
-                r.on_prefix = takes_tiles(r.nq, n_pre) ? 0 : 1;
-                (r.on_prefix ? p.rows : p.tiles_pre).push_back(r);
+                const bool tiles = takes_tiles(r.nq, n_pre);
+                r.kind = tiles ? kOwnKeys : kOnPrefix;
+                (tiles ? p.tiles_pre : p.rows).push_back(r);
             }
         }
         const size_t n_stacks = p.rows.size();
@@ -164,8 +248,17 @@ Plan make_plan(const std::vector<Seq> &seqs, const Shape &sh, int32_t n_pre, con
         p.wide = pick_wide(p.rows, sh, kernels);
         if (last) {
             for (RaggedRun &r : p.tiles) r.ns = 1;
+            for (std::vector<RaggedRun> &part : p.stretches) part[0].ns = 1;
         } else {
-            split_rows(p.rows, sh, p.wide, p.stacked ? 0 : n_pre, coarse);
+            for (std::vector<RaggedRun> &part : p.stretches) {  // (all pairs of tiles as the one with the most keys)
+                std::vector<RaggedRun> one(1, part[0]);
+                one[0].nq = part.back().q0 + part.back().nq - part[0].q0;
+                one[0].nk = 0;
+                for (const RaggedRun &r : part) one[0].nk = std::max(one[0].nk, r.nk);
+                split_tiles(one, sh, n_pre, coarse);
+                part[0].ns = one[0].ns;
+            }
+            if (p.cluster == 1) split_rows(p.rows, sh, p.wide, p.stacked ? 0 : n_pre, coarse);
             split_tiles(p.tiles, sh, n_pre, coarse);
             split_tiles(p.tiles_pre, sh, 0, coarse);
         }
@@ -181,25 +274,37 @@ Plan make_plan(const std::vector<Seq> &seqs, const Shape &sh, int32_t n_pre, con
         for (size_t i = 0; i < p.rows.size(); ++i) {
             RaggedRun &r = p.rows[i];
             r.rec0 = -1;
-            if (!p.stacked && r.ns == 1) continue;
-            records(r);
-            if (i < n_stacks) continue;
-            JoinRun j{r.q0, r.nq, r.rec0, r.ns, 0, 0};
-            if (p.stacked) {
-                if (!stack || r.q0 >= stack->q0 + stack->nq)
-                    stack = rows_at < n_stacks && r.q0 >= p.rows[rows_at].q0 && r.q0 < p.rows[rows_at].q0 + p.rows[rows_at].nq
-                                ? &p.rows[rows_at++]
-                                : &p.tiles_pre[tiles_at++];
-                j.pre0 = stack->rec0 + (r.q0 - stack->q0) * stack->ns;
-                j.pns = stack->ns;
+            if (i < n_stacks) {
+                records(r);
+                continue;
             }
-            p.joins.push_back(j);
+            if (!p.stacked) {
+                if (r.ns == 1) continue;
+                records(r);
+                p.joins.push_back(JoinRun{r.q0, r.nq, r.rec0, r.ns, 0, 0});
+                continue;
+            }
+            if (!stack || r.q0 >= stack->q0 + stack->nq)
+                stack = rows_at < n_stacks && r.q0 >= p.rows[rows_at].q0 && r.q0 < p.rows[rows_at].q0 + p.rows[rows_at].nq
+                            ? &p.rows[rows_at++]
+                            : &p.tiles_pre[tiles_at++];
+            records(r);
+            p.joins.push_back(JoinRun{r.q0, r.nq, r.rec0, r.ns, stack->rec0 + (r.q0 - stack->q0) * stack->ns, stack->ns});
         }
         for (RaggedRun &r : p.tiles) {
             r.rec0 = -1;
             if (r.ns == 1) continue;
             records(r);
             p.joins.push_back(JoinRun{r.q0, r.nq, r.rec0, r.ns, 0, 0});
+        }
+        for (std::vector<RaggedRun> &part : p.stretches) {
+            RaggedRun &r = part[0];
+            r.rec0 = -1;
+            if (r.ns == 1) continue;
+            r.rec0 = static_cast<int32_t>(std::min<int64_t>(at, 0x7fffffff));
+            const int32_t nq = part.back().q0 + part.back().nq - r.q0;
+            at += static_cast<int64_t>(nq) * r.ns;
+            p.joins.push_back(JoinRun{r.q0, nq, r.rec0, r.ns, 0, 0});
         }
         p.n_rec = at;
         if (at > 0 && (at > 0x7fffffff || record_bytes(at, sh) > workspace)) continue;
@@ -217,6 +322,7 @@ struct Call {
     const void *Q, *K, *V, *Kp, *Vp;
     void *out;
     int64_t q_stride, k_stride, v_stride, kp_stride, vp_stride, o_stride;
+    int64_t q_rows, k_rows;  // that Q and out, and K and V, have
     int32_t dtype, n_pre;
     bool causal;  // own keys j <= k_len - q_len + i; otherwise all
     const int32_t *q_lens, *k_lens, *k_start;
@@ -228,7 +334,7 @@ struct Call {
 };
 
 // Sizes and grouping of a call, and its sequences with queries.
-int sequences(const Call &c, std::vector<Seq> &seqs, bool *keys) {
+int sequences(const Call &c, std::vector<Seq> &seqs, int64_t *q_reach, int64_t *k_reach) {
     if (c.n_seqs <= 0 || !c.q_lens || !c.k_lens)
         return refuse(PKV_ERR_BAD_DIM, "n_seqs must be positive and the lengths non-NULL");
     if (c.sh.n_heads <= 0 || c.sh.n_kv <= 0 || c.sh.hd <= 0)
@@ -236,7 +342,7 @@ int sequences(const Call &c, std::vector<Seq> &seqs, bool *keys) {
     if (c.sh.hd > kMaxHeadDim) return refuse(PKV_ERR_BAD_DIM, "head_dim %d > %d is not supported", c.sh.hd, kMaxHeadDim);
     if (c.n_pre < 0 || c.n_pre > kMaxRows - 256) return refuse(PKV_ERR_BAD_DIM, "a prefix of %d rows", c.n_pre);
     int64_t q = 0, k = 0;
-    *keys = false;
+    *k_reach = 0;
     for (int32_t s = 0; s < c.n_seqs; ++s) {
         const int32_t nq = c.q_lens[s], nk = c.k_lens[s];
         if (nq < 0 || nk < 0) return refuse(PKV_ERR_BAD_DIM, "sequence %d has a negative length", s);
@@ -250,11 +356,12 @@ int sequences(const Call &c, std::vector<Seq> &seqs, bool *keys) {
             // neighbours that see the same keys (beams of one request) are one
             if (!c.causal && !seqs.empty() && seqs.back().k0 == x.k0 && seqs.back().nk == nk) seqs.back().nq += nq;
             else seqs.push_back(x);
-            *keys = *keys || nk > 0;
         }
+        if (nk > 0) *k_reach = std::max(*k_reach, k0 + nk);
         q += nq;
         k += nk;
     }
+    *q_reach = q;
     if (q * c.sh.n_heads > 0x7fff0000LL) return refuse(PKV_ERR_BAD_DIM, "%lld query rows of %d heads are too many", static_cast<long long>(q), c.sh.n_heads);
     if (static_cast<int64_t>(c.sh.n_heads) * c.sh.hd > 0x7fffffffLL) return refuse(PKV_ERR_BAD_DIM, "n_heads * head_dim too large");
     if (c.sh.n_heads % c.sh.n_kv != 0)
@@ -274,8 +381,8 @@ int each_chunk(const std::vector<Seq> &seqs, F &&f) {
 
 int64_t workspace_of(const Call &c) {
     std::vector<Seq> seqs;
-    bool keys;
-    if (sequences(c, seqs, &keys)) return -1;
+    int64_t q, k;
+    if (sequences(c, seqs, &q, &k)) return -1;
     int64_t most = 0;
     each_chunk(seqs, [&](const std::vector<Seq> &part) {
         // (alignment and scale, which a call's kernels go by too, are not known here)
@@ -289,8 +396,8 @@ int64_t workspace_of(const Call &c) {
 
 int attend(const Call &c, cudaStream_t st) {
     std::vector<Seq> seqs;
-    bool keys;
-    int rc = sequences(c, seqs, &keys);
+    int64_t q, k;
+    int rc = sequences(c, seqs, &q, &k);
     if (rc) return rc;
     if (c.dtype != PKV_BF16 && c.dtype != PKV_F16) return refuse(PKV_ERR_ARG, "packed attention takes PKV_BF16 or PKV_F16 rows");
     const int64_t q_dim = static_cast<int64_t>(c.sh.n_heads) * c.sh.hd, kv_dim = static_cast<int64_t>(c.sh.n_kv) * c.sh.hd;
@@ -301,8 +408,11 @@ int attend(const Call &c, cudaStream_t st) {
         return refuse(PKV_ERR_BAD_DIM, "row stride too large");
     if (c.workspace_bytes < 0 || (c.workspace_bytes > 0 && !c.workspace)) return refuse(PKV_ERR_ARG, "workspace");
     if (reinterpret_cast<uintptr_t>(c.workspace) % 16 != 0) return refuse(PKV_ERR_ARG, "the workspace must be aligned to 16 bytes");
+    if (q > c.q_rows || k > c.k_rows)
+        return refuse(PKV_ERR_ARG, "the sequences reach over %lld query and %lld key rows, there are %lld and %lld", static_cast<long long>(q),
+                      static_cast<long long>(k), static_cast<long long>(c.q_rows), static_cast<long long>(c.k_rows));
     if (seqs.empty()) return PKV_OK;
-    if (!c.Q || !c.out || (keys && (!c.K || !c.V)) || (c.n_pre > 0 && (!c.Kp || !c.Vp)))
+    if (!c.Q || !c.out || (k > 0 && (!c.K || !c.V)) || (c.n_pre > 0 && (!c.Kp || !c.Vp)))
         return refuse(PKV_ERR_ARG, "NULL data pointer");
     for (const void *p : {c.Q, c.K, c.V, c.Kp, c.Vp, static_cast<const void *>(c.out)})
         if (reinterpret_cast<uintptr_t>(p) % 2 != 0) return refuse(PKV_ERR_ARG, "rows must be aligned to their element");
@@ -321,6 +431,7 @@ int attend(const Call &c, cudaStream_t st) {
     a.kp_stride = c.kp_stride;
     a.vp_stride = c.vp_stride;
     a.n_pre = c.n_pre;
+    a.cluster = 1;
     a.n_heads = c.sh.n_heads;
     a.n_kv = c.sh.n_kv;
     a.hd = c.sh.hd;
@@ -332,7 +443,7 @@ int attend(const Call &c, cudaStream_t st) {
     const Kernels kernels{a.vec, ragged_tc_takes(a)};
     return each_chunk(seqs, [&](const std::vector<Seq> &part) {
         const Plan p = make_plan(part, c.sh, c.n_pre, kernels, c.workspace_bytes);
-        if (!a.err && !(p.tiles.empty() && p.tiles_pre.empty())) {
+        if (!a.err && !(p.tiles.empty() && p.tiles_pre.empty() && p.stretches.empty())) {
             const int r = contiguous_error_word(st, &a.err);
             if (r) return r;
         }
@@ -340,14 +451,16 @@ int attend(const Call &c, cudaStream_t st) {
         a.pl = a.pm + record_floats(p.n_rec, c.sh.n_heads);
         a.pacc = a.pl + record_floats(p.n_rec, c.sh.n_heads);
         bool first = true;
-        auto run = [&](RaggedArgs b, const std::vector<RaggedRun> &runs, bool tiles) {
+        enum { kRows, kTiles, kStretch };
+        auto run = [&](RaggedArgs b, const std::vector<RaggedRun> &runs, int how) {
             for (size_t i = 0; i < runs.size(); i += kRaggedLarge) {
                 const int32_t n = static_cast<int32_t>(std::min<size_t>(kRaggedLarge, runs.size() - i));
                 b.overlap = !first;
                 first = false;
-                const int r = tiles ? counted(PKV_KERNEL_PREFILL, st, "ragged attention tiles", [&] { return launch_ragged_tc(b, &runs[i], n, st); })
-                                    : counted(PKV_KERNEL_DECODE, st, "ragged attention rows",
-                                              [&] { return launch_ragged_rows(b, &runs[i], n, p.wide, st); });
+                const int r = how == kRows ? counted(PKV_KERNEL_DECODE, st, "ragged attention rows",
+                                                     [&] { return launch_ragged_rows(b, &runs[i], n, p.wide, st); })
+                                           : counted(PKV_KERNEL_PREFILL, st, "ragged attention tiles",
+                                                     [&] { return launch_ragged_tc(b, &runs[i], n, how == kStretch, st); });
                 if (r) return r;
             }
             return static_cast<int>(PKV_OK);
@@ -359,9 +472,13 @@ int attend(const Call &c, cudaStream_t st) {
         pre.v_stride = c.vp_stride;
         pre.n_pre = 0;
         own.n_pre = p.stacked ? 0 : c.n_pre;
-        int r = run(a, p.tiles, true);
-        if (!r) r = run(pre, p.tiles_pre, true);
-        if (!r) r = run(own, p.rows, false);
+        own.cluster = p.cluster;
+        int r = PKV_OK;
+        for (const std::vector<RaggedRun> &part : p.stretches)
+            if (!r) r = run(a, part, kStretch);
+        if (!r) r = run(a, p.tiles, kTiles);
+        if (!r) r = run(pre, p.tiles_pre, kTiles);
+        if (!r) r = run(own, p.rows, kRows);
         if (r || p.joins.empty()) return r;
         return counted(PKV_KERNEL_MERGE, st, "ragged join kernel",
                        [&] { return launch_ragged_join(a, p.joins.data(), static_cast<int32_t>(p.joins.size()), st); });
@@ -483,14 +600,15 @@ int64_t pkv_attn_prefix_workspace(int32_t prefix_len, const int32_t *q_lens, con
     return rc ? -1 : n;
 }
 
-int pkv_attn_cross(const void *Q, int64_t q_stride, const int32_t *q_lens, const void *K, int64_t k_stride,
-                   const void *V, int64_t v_stride, const int32_t *k_lens, const int32_t *k_start, int32_t dtype,
-                   int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float scale, void *out,
+int pkv_attn_cross(const void *Q, int64_t q_stride, int64_t q_rows, const int32_t *q_lens, const void *K, int64_t k_stride,
+                   const void *V, int64_t v_stride, int64_t k_rows, const int32_t *k_lens, const int32_t *k_start,
+                   int32_t dtype, int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float scale, void *out,
                    int64_t out_stride, void *workspace, int64_t workspace_bytes, pkv_stream_t stream) {
     return guarded([&] {
         Call c{};
         c.Q = Q, c.K = K, c.V = V, c.out = out;
         c.q_stride = q_stride, c.k_stride = k_stride, c.v_stride = v_stride, c.o_stride = out_stride;
+        c.q_rows = q_rows, c.k_rows = k_rows;
         c.dtype = dtype;
         c.q_lens = q_lens, c.k_lens = k_lens, c.k_start = k_start, c.n_seqs = n_seqs;
         c.sh = Shape{n_heads, n_kv_heads, head_dim};
@@ -500,16 +618,17 @@ int pkv_attn_cross(const void *Q, int64_t q_stride, const int32_t *q_lens, const
     });
 }
 
-int pkv_attn_prefix(const void *Q, int64_t q_stride, const int32_t *q_lens, const void *K_prefix, int64_t kp_stride,
-                    const void *V_prefix, int64_t vp_stride, int32_t prefix_len, const void *K, int64_t k_stride,
-                    const void *V, int64_t v_stride, const int32_t *k_lens, const int32_t *k_start, int32_t dtype,
-                    int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float scale, void *out,
+int pkv_attn_prefix(const void *Q, int64_t q_stride, int64_t q_rows, const int32_t *q_lens, const void *K_prefix,
+                    int64_t kp_stride, const void *V_prefix, int64_t vp_stride, int32_t prefix_len, const void *K,
+                    int64_t k_stride, const void *V, int64_t v_stride, int64_t k_rows, const int32_t *k_lens,
+                    const int32_t *k_start, int32_t dtype, int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, float scale, void *out,
                     int64_t out_stride, void *workspace, int64_t workspace_bytes, pkv_stream_t stream) {
     return guarded([&] {
         Call c{};
         c.Q = Q, c.K = K, c.V = V, c.Kp = K_prefix, c.Vp = V_prefix, c.out = out;
         c.q_stride = q_stride, c.k_stride = k_stride, c.v_stride = v_stride, c.o_stride = out_stride;
         c.kp_stride = kp_stride, c.vp_stride = vp_stride;
+        c.q_rows = q_rows, c.k_rows = k_rows;
         c.dtype = dtype;
         c.n_pre = prefix_len;
         c.causal = true;

@@ -8,9 +8,13 @@
 //
 // A unit is 8 W query rows ((query, head of the group) pairs, which share their
 // keys) of one kv head and one split of the keys: the shared prefix's rows,
-// then the run's own.  Its four warps take the key tiles in turn, each with its
+// then the run's own.  Its two warps take the key tiles in turn, each with its
 // own ring of tiles (cp.async, no block-wide barrier in the loop), its own running
 // maximum and sum; they are joined in shared memory at the end.
+//
+// Small launches have a cluster of blocks a unit, a split each, and join them
+// through each other's shared memory: one launch.  Larger ones write partial records
+// that the join launch combines.
 //
 //   S^T [16 keys x 8] = K Q^T       m16n8k16, A by ldmatrix, B held in registers
 //   O^T [16 dims x 8] += V^T P^T    A by transposed ldmatrix, B from S^T by movmatrix
@@ -31,7 +35,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kRowWarps = 4;
+constexpr int kRowWarps = 2;  // (four a block and half the blocks: XX)
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kHeadroom = 8.f;
 
@@ -43,7 +47,8 @@ struct RowCfg {
     static constexpr int kStages = 3;                         // 128 KB of K and V on the way a SM
     static constexpr size_t kRing = static_cast<size_t>(kRowWarps) * kStages * kStage;
     static constexpr int kPart = DP + 4;                      // floats of an output row of a warp's part
-    static constexpr size_t kSmem = kRing > sizeof(float) * kRowWarps * 8 * W * kPart ? kRing : sizeof(float) * kRowWarps * 8 * W * kPart;
+    static constexpr size_t kParts = sizeof(float) * (kRowWarps + 1) * 8 * W * kPart;  // the warps', and the block's
+    static constexpr size_t kSmem = kRing > kParts ? kRing : kParts;
 };
 
 __device__ __forceinline__ float pow2(float x) {  // 2^x to about 2^-22 relative; 0 for -inf
@@ -62,6 +67,36 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+// Blocks of a cluster: their number, this one's place, a barrier over all of
+// them, and shared memory of another.
+__device__ __forceinline__ int cluster_size() {
+    uint32_t x;
+    asm("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(x));
+    return static_cast<int>(x);
+}
+__device__ __forceinline__ int cluster_rank() {
+    uint32_t x;
+    asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(x));
+    return static_cast<int>(x);
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ uint32_t in_block(const void *p, int rank) {
+    uint32_t y;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(y) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+    return y;
+}
+__device__ __forceinline__ float ld_block(uint32_t a) {
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(x) : "r"(a) : "memory");
+    return x;
+}
+__device__ __forceinline__ float4 ld_block4(uint32_t a) {
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(a) : "memory");
+    return x;
 }
 __device__ __forceinline__ void wait_launch_before() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void let_next_launch_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
@@ -130,7 +165,7 @@ __device__ __forceinline__ void load_tile(unsigned char *dst, const KeyRows<T> &
 }
 
 template <class T, int DP, int W, bool kVec, int N>
-__global__ void __launch_bounds__(32 * kRowWarps, DP <= 128 ? 2 : 1)
+__global__ void __launch_bounds__(32 * kRowWarps, DP <= 128 ? 4 : 2)
     ragged_rows_kernel(const __grid_constant__ RaggedArgs a, const __grid_constant__ RunList<RaggedRun, N> l) {
     using C = RowCfg<DP, W>;
     constexpr int kTile = C::kTile, kStep = kTile * kRowWarps, MT = kTile / 16;
@@ -142,18 +177,20 @@ __global__ void __launch_bounds__(32 * kRowWarps, DP <= 128 ? 2 : 1)
     let_next_launch_start();
 
     // the unit: neighbouring blocks take the kv heads of the same keys
-    const int ri = run_of(l, blockIdx.x);
+    const int n_ranks = cluster_size(), rank = cluster_rank(), unit = blockIdx.x / n_ranks;
+    const int ri = run_of(l, unit);
     const RaggedRun run = l.run[ri];
-    int u = blockIdx.x - l.unit0[ri];
+    int u = unit - l.unit0[ri];
     const int kvh = u % a.n_kv;
     u /= a.n_kv;
-    const int rows = run.nq * G, n_blocks = ragged_row_units(rows, W);
-    const int split = u / n_blocks, row0 = (u - split * n_blocks) * 8 * W;
+    const int rows = run.nq * G, n_blocks = ragged_row_units(rows, W), ns = n_ranks > 1 ? n_ranks : run.ns;
+    const int split = n_ranks > 1 ? rank : u / n_blocks, row0 = u % n_blocks * 8 * W;
     const int n_rows = min(8 * W, rows - row0);
     const int first = row0 / G, last = (row0 + n_rows - 1) / G;  // queries of the block
 
-    const int n_pre = run.on_prefix ? 0 : a.n_pre, total = n_pre + run.nk;
-    const int per = ((total + run.ns - 1) / run.ns + kStep - 1) / kStep * kStep;
+    const int n_pre = run.kind == kOnPrefix ? 0 : a.n_pre, total = n_pre + run.nk;
+    // a cluster's blocks have few keys each: whole tiles; otherwise as many tiles a warp
+    const int grain = n_ranks > 1 ? kTile : kStep, per = ((total + ns - 1) / ns + grain - 1) / grain * grain;
     const int kb = static_cast<int>(min(static_cast<long long>(split) * per, static_cast<long long>(total)));
     const int seen = n_pre + min(run.nk, run.off + last + 1);    // keys that some row sees
     const int whole = n_pre + min(run.nk, run.off + first + 1);  // keys that all rows see
@@ -162,7 +199,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, DP <= 128 ? 2 : 1)
     const int64_t head = static_cast<int64_t>(kvh) * hd;
     KeyRows<T> K{static_cast<const T *>(a.Kp) + head, static_cast<const T *>(a.K) + run.k0 * a.k_stride + head, a.kp_stride, a.k_stride, n_pre};
     KeyRows<T> V{static_cast<const T *>(a.Vp) + head, static_cast<const T *>(a.V) + run.k0 * a.v_stride + head, a.vp_stride, a.v_stride, n_pre};
-    if (run.on_prefix) {
+    if (run.kind == kOnPrefix) {
         K.own = K.pre, K.own_stride = K.pre_stride;
         V.own = V.pre, V.own_stride = V.pre_stride;
     }
@@ -415,19 +452,51 @@ __global__ void __launch_bounds__(32 * kRowWarps, DP <= 128 ? 2 : 1)
             }
         }
     __syncthreads();
-    const int64_t H = a.n_heads;
-    for (int i = tid; i < n_rows * (DP / 4); i += 32 * kRowWarps) {
-        const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
-        if (d >= hd) continue;
-        float top = sm_m[0][r], L = 0.f;
+    // four dims of a row, over the block's warps
+    auto of_block = [&](int r, int d, float &top, float &L, float (&v)[4]) {
+        top = sm_m[0][r];
+        L = 0.f;
 #pragma unroll
         for (int w = 1; w < kRowWarps; ++w) top = fmaxf(top, sm_m[w][r]);
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        v[0] = v[1] = v[2] = v[3] = 0.f;
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w) {
             L += sm_l[w][r] * pow2(sm_m[w][r] - (top == -INFINITY ? 0.f : top));
             const float4 y = *reinterpret_cast<const float4 *>(out + (w * 8 * W + r) * C::kPart + d);
             v[0] += y.x, v[1] += y.y, v[2] += y.z, v[3] += y.w;
+        }
+    };
+    const int64_t H = a.n_heads;
+    float *joined = out + kRowWarps * 8 * W * C::kPart;
+    if (n_ranks > 1) {
+        for (int i = tid; i < n_rows * (DP / 4); i += 32 * kRowWarps) {
+            const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
+            if (d >= hd) continue;
+            float top, L, v[4];
+            of_block(r, d, top, L, v);
+            *reinterpret_cast<float4 *>(joined + r * C::kPart + d) = make_float4(v[0], v[1], v[2], v[3]);
+            if (d == 0) joined[r * C::kPart + DP] = top, joined[r * C::kPart + DP + 1] = L;
+        }
+        cluster_sync();
+    }
+    wait_launch_before();  // so that the join behind this launch has both
+    for (int i = (n_ranks > 1 ? rank * 32 * kRowWarps : 0) + tid; i < n_rows * (DP / 4); i += n_ranks * 32 * kRowWarps) {
+        const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
+        if (d >= hd) continue;
+        float top, L, v[4];
+        if (n_ranks > 1) {
+            top = -INFINITY, L = 0.f;
+            v[0] = v[1] = v[2] = v[3] = 0.f;
+            for (int x = 0; x < n_ranks; ++x) top = fmaxf(top, ld_block(in_block(joined + r * C::kPart + DP, x)));
+            for (int x = 0; x < n_ranks; ++x) {
+                const uint32_t at = in_block(joined + r * C::kPart, x);
+                const float f = pow2(ld_block(at + 4 * DP) - (top == -INFINITY ? 0.f : top));
+                const float4 y = ld_block4(at + 4 * d);
+                L += f * ld_block(at + 4 * DP + 4);
+                v[0] = fmaf(f, y.x, v[0]), v[1] = fmaf(f, y.y, v[1]), v[2] = fmaf(f, y.z, v[2]), v[3] = fmaf(f, y.w, v[3]);
+            }
+        } else {
+            of_block(r, d, top, L, v);
         }
         const int qi = (row0 + r) / G, h = kvh * G + (row0 + r) % G;
         if (run.rec0 >= 0) {
@@ -441,90 +510,120 @@ __global__ void __launch_bounds__(32 * kRowWarps, DP <= 128 ? 2 : 1)
                 for (int k = 0; k < 4; ++k)
                     if (d + k < hd) dst[k] = v[k];
             }
+            continue;
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;  // a row without keys is 0
+        T *dst = static_cast<T *>(a.out) + (static_cast<int64_t>(run.q0) + qi) * a.o_stride + static_cast<int64_t>(h) * hd + d;
+        if constexpr (kVec) {
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2(T{}, v[0] * inv, v[1] * inv), pack2(T{}, v[2] * inv, v[3] * inv));
         } else {
-            const float inv = L == 0.f ? 0.f : 1.f / L;  // a row without keys is 0
-            T *dst = static_cast<T *>(a.out) + (static_cast<int64_t>(run.q0) + qi) * a.o_stride + static_cast<int64_t>(h) * hd + d;
-            if constexpr (kVec) {
-                *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2(T{}, v[0] * inv, v[1] * inv), pack2(T{}, v[2] * inv, v[3] * inv));
-            } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (d + k < hd) narrow(dst + k, v[k] * inv);
-            }
+            for (int k = 0; k < 4; ++k)
+                if (d + k < hd) narrow(dst + k, v[k] * inv);
         }
     }
-    wait_launch_before();  // so that the join behind this launch has both
+    if (n_ranks > 1) cluster_sync();  // the others may still read this block's part
 }
 
-// One (query, head) a block: its records' maximum and sum, then four warps add
-// every fourth record's output.
+// The records of a (query, head), by one warp or, where there are few of them,
+// by the four of a block (`together`).  A lane takes a record's maximum and
+// sum, then the records' outputs are added with eight on the way.
 template <class T, int N>
 __global__ void __launch_bounds__(128)
-    ragged_join_kernel(const __grid_constant__ RaggedArgs a, const __grid_constant__ RunList<JoinRun, N> l) {
+    ragged_join_kernel(const __grid_constant__ RaggedArgs a, const __grid_constant__ RunList<JoinRun, N> l, int together) {
     __shared__ float part[4][256];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x % a.n_heads, t = blockIdx.x / a.n_heads;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t H = a.n_heads;
+    const int64_t item = together ? blockIdx.x : 4 * static_cast<int64_t>(blockIdx.x) + warp;
+    const int first = together ? warp : 0, step = together ? 4 : 1;  // of this warp's records
+    wait_launch_before();
+    if (item >= l.unit0[l.n] * H) return;  // (whole blocks, where warps meet below)
+    const int h = static_cast<int>(item % H), t = static_cast<int>(item / H);
     const int ri = run_of(l, t), qi = t - l.unit0[ri];
     const JoinRun run = l.run[ri];
-    const int64_t own = run.rec0 + static_cast<int64_t>(qi) * run.ns, pre = run.pre0 + static_cast<int64_t>(qi) * run.pns;
+    const int64_t own = (run.rec0 + static_cast<int64_t>(qi) * run.ns) * H + h, pre = (run.pre0 + static_cast<int64_t>(qi) * run.pns) * H + h;
     const int n = run.ns + run.pns;
-    auto record = [&](int x) { return (x < run.ns ? own + x : pre + (x - run.ns)) * a.n_heads + h; };
-    wait_launch_before();
-    float top = -INFINITY;
-    for (int x = lane; x < n; x += 32) top = fmaxf(top, a.pm[record(x)]);
+    auto record = [&](int x) { return x < run.ns ? own + x * H : pre + (x - run.ns) * H; };
+    float top = -INFINITY, L = 0.f;
+    for (int x = lane; x < n; x += 32) {
+        const int64_t r = record(x);
+        const float m = __ldcg(a.pm + r), sum = __ldcg(a.pl + r);
+        const float mn = fmaxf(top, m), ref = mn == -INFINITY ? 0.f : mn;
+        L = L * pow2(top - ref) + sum * pow2(m - ref);
+        top = mn;
+    }
+    float all = top;
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, s));
-    const float ref = top == -INFINITY ? 0.f : top;
-    float L = 0.f;
-    for (int x = lane; x < n; x += 32) L += a.pl[record(x)] * pow2(a.pm[record(x)] - ref);
+    for (int s = 16; s > 0; s >>= 1) all = fmaxf(all, __shfl_xor_sync(kAll, all, s));
+    const float ref = all == -INFINITY ? 0.f : all;
+    L *= pow2(top - ref);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) L += __shfl_xor_sync(kAll, L, s);
     const float inv = L == 0.f ? 0.f : 1.f / L;
     float o[2][4] = {};
     const bool vec = (a.hd & 3) == 0;
-    for (int x = warp; x < n; x += 4) {
-        const int64_t r = record(x);
-        if (a.pl[r] == 0.f) continue;  // no key of the split is seen: no output was written
-        const float f = pow2(a.pm[r] - ref);
-        const float *src = a.pacc + r * a.hd;
+    for (int x0 = 0; x0 < n; x0 += 32) {  // a lane's weight of record x0 + lane
+        float f = 0.f;
+        if (x0 + lane < n) {
+            const int64_t r = record(x0 + lane);
+            if (__ldcg(a.pl + r) != 0.f) f = pow2(__ldcg(a.pm + r) - ref);  // (0: no key of it is seen, no output was written)
+        }
+        const int m = min(32, n - x0);
+#pragma unroll 8
+        for (int y = first; y < m; y += step) {
+            const float w = __shfl_sync(kAll, f, y);
+            const float *src = a.pacc + record(x0 + y) * a.hd;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int d = 4 * lane + 128 * j;
-            if (d >= a.hd) continue;
-            if (vec) {
-                const float4 y = *reinterpret_cast<const float4 *>(src + d);
-                o[j][0] = fmaf(f, y.x, o[j][0]), o[j][1] = fmaf(f, y.y, o[j][1]);
-                o[j][2] = fmaf(f, y.z, o[j][2]), o[j][3] = fmaf(f, y.w, o[j][3]);
-            } else {
+            for (int j = 0; j < 2; ++j) {
+                const int d = 4 * lane + 128 * j;
+                if (w == 0.f || d >= a.hd) continue;
+                if (vec) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + d));
+                    o[j][0] = fmaf(w, v.x, o[j][0]), o[j][1] = fmaf(w, v.y, o[j][1]);
+                    o[j][2] = fmaf(w, v.z, o[j][2]), o[j][3] = fmaf(w, v.w, o[j][3]);
+                } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (d + k < a.hd) o[j][k] = fmaf(f, src[d + k], o[j][k]);
+                    for (int k = 0; k < 4; ++k)
+                        if (d + k < a.hd) o[j][k] = fmaf(w, __ldcg(src + d + k), o[j][k]);
+                }
             }
         }
     }
+    T *dst = static_cast<T *>(a.out) + (static_cast<int64_t>(run.q0) + qi) * a.o_stride + static_cast<int64_t>(h) * a.hd;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) part[warp][4 * lane + 128 * j + k] = o[j][k];
-    __syncthreads();
-    T *dst = static_cast<T *>(a.out) + (static_cast<int64_t>(run.q0) + qi) * a.o_stride + static_cast<int64_t>(h) * a.hd;
-    for (int d = tid; d < a.hd; d += 128) narrow(dst + d, (part[0][d] + part[1][d] + part[2][d] + part[3][d]) * inv);
+    if (together) {
+        __syncthreads();
+        for (int d = threadIdx.x; d < a.hd; d += 128) narrow(dst + d, (part[0][d] + part[1][d] + part[2][d] + part[3][d]) * inv);
+    } else {
+        __syncwarp();
+        for (int d = lane; d < a.hd; d += 32) narrow(dst + d, part[warp][d] * inv);
+    }
 }
 
 // A launch that may overlap the one in front of it, or a plain one.
 template <class K, class... A>
-cudaError_t start(K *kernel, long long grid, int threads, size_t smem, bool overlap, cudaStream_t s, const A &...args) {
+cudaError_t start(K *kernel, long long grid, int cluster, int threads, size_t smem, bool overlap, cudaStream_t s, const A &...args) {
     if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = overlap ? 1 : 0;
+    cudaLaunchAttribute at[2] = {};
+    if (overlap) {
+        at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        at[cfg.numAttrs].val.clusterDim.x = static_cast<unsigned>(cluster);
+        at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    cfg.attrs = at;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -547,7 +646,7 @@ cudaError_t rows_n(const RaggedArgs &a, const RaggedRun *runs, int32_t n, cudaSt
         if (at > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     }
     l.unit0[n] = static_cast<int32_t>(at);
-    return start(ragged_rows_kernel<T, DP, W, kVec, N>, at, 32 * kRowWarps, C::kSmem, a.overlap, s, a, l);
+    return start(ragged_rows_kernel<T, DP, W, kVec, N>, at * a.cluster, a.cluster, 32 * kRowWarps, C::kSmem, a.overlap, s, a, l);
 }
 template <class T, int DP, int W, bool kVec>
 cudaError_t rows_l(const RaggedArgs &a, const RaggedRun *runs, int32_t n, cudaStream_t s) {
@@ -581,7 +680,9 @@ cudaError_t join_n(const RaggedArgs &a, const JoinRun *runs, int32_t n, cudaStre
         if (at > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     }
     l.unit0[n] = static_cast<int32_t>(at);
-    return start(ragged_join_kernel<T, N>, at * a.n_heads, 128, 0, true, s, a, l);
+    // a block a record set while that leaves the GPU room: eight of its blocks a SM
+    const int together = at * a.n_heads <= 8 * 152;
+    return start(ragged_join_kernel<T, N>, together ? at * a.n_heads : (at * a.n_heads + 3) / 4, 1, 128, 0, true, s, a, l, together);
 }
 template <class T>
 cudaError_t join_t(const RaggedArgs &a, const JoinRun *runs, int32_t n, cudaStream_t s) {

@@ -12,16 +12,19 @@
 // 1/50 of the f32 rate).  The nearest quarter turn is taken off in whole
 // numbers, the rest, at most an eighth of a turn, goes through sincospi in f32.
 //
-// A block computes its rows' sines once for all heads, with the first of its
-// loads on the way, and turns each pair of 16-byte pieces in registers; what
-// bounds it is one read and one write of every row.
+// A thread takes one piece of a row's pairs (16 bytes of each half of a head)
+// for several heads: its cosines and sines stay in registers, and all its loads
+// are on their way before the sines, which the block computes once a row, are
+// there.  What bounds it is one read and one write of every row.
 #include "pkv_half.h"
 #include "pkv_ragged.h"
+
+#include <algorithm>
 
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 256, kMaxRows = 4, kUnroll = 4;
+constexpr int kThreads = 256, kMaxRows = 32, kHeads = 4;  // of a block, of a block, of a thread at a time
 
 template <int B>
 struct Piece;
@@ -62,89 +65,93 @@ __device__ __forceinline__ float2 cos_sin(uint64_t turn) {
     return quarter & 2 ? make_float2(-x, -y) : make_float2(x, y);
 }
 
-// E elements a piece; n_tok rows a block.
+// E elements a piece; the block takes n_tok rows, each by `lanes` threads a piece.
 template <class T, int E>
-__global__ void __launch_bounds__(kThreads) rope_packed_kernel(const __grid_constant__ RopePacked a, int n_tok) {
+__global__ void __launch_bounds__(kThreads) rope_packed_kernel(const __grid_constant__ RopePacked a, int n_tok, int lanes) {
     using P = typename Piece<E * sizeof(T)>::type;
-    __shared__ float2 cs[kMaxRows][kRopePairs];
-    const int r = a.n_pairs, tid = threadIdx.x;
+    extern __shared__ float2 cs[];  // [n_tok][n_pairs]
+    const int r = a.n_pairs, tid = threadIdx.x, per_head = r / E, per_row = per_head * lanes;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * n_tok;
     const int rows = static_cast<int>(min(static_cast<int64_t>(n_tok), a.n_rows - row0));
-    const int per_head = r / E, heads = a.heads[0] + a.heads[1], per_row = heads * per_head, units = rows * per_row;
-
-    struct At {
-        const T *src;
-        T *dst;
-        int row, pair;
+    const int mine = tid / per_row, in_row = tid - mine * per_row, lane = in_row / per_head, pair = (in_row - lane * per_head) * E;
+    const bool works = mine < rows;
+    const int64_t row = row0 + (works ? mine : 0);
+    const int heads = a.heads[0] + a.heads[1];
+    auto src = [&](int h) {
+        const int w = h >= a.heads[0];
+        return static_cast<const T *>(a.src[w]) + row * a.src_stride[w] + static_cast<int64_t>(w ? h - a.heads[0] : h) * a.hd + pair;
     };
-    auto place = [&](int u) {
-        const int row = u / per_row, v = u - row * per_row, h = v / per_head, j = v - h * per_head;
-        const int w = h >= a.heads[0], hh = w ? h - a.heads[0] : h;
-        const int64_t in_row = static_cast<int64_t>(hh) * a.hd + E * j;
-        return At{static_cast<const T *>(a.src[w]) + (row0 + row) * a.src_stride[w] + in_row,
-                  static_cast<T *>(a.dst[w]) + (row0 + row) * a.dst_stride[w] + in_row, row, E * j};
+    auto dst = [&](int h) {
+        const int w = h >= a.heads[0];
+        return static_cast<T *>(a.dst[w]) + row * a.dst_stride[w] + static_cast<int64_t>(w ? h - a.heads[0] : h) * a.hd + pair;
     };
-    bool ready = false;
-    for (int u0 = tid; u0 < units || !ready; u0 += kUnroll * kThreads) {
-        P x[kUnroll], y[kUnroll];
+    P x[kHeads], y[kHeads];
+    auto load = [&](int h0) {
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            const int u = u0 + k * kThreads;
-            if (u < units) {
-                const At at = place(u);
-                x[k] = *reinterpret_cast<const P *>(at.src);
-                y[k] = *reinterpret_cast<const P *>(at.src + r);
+        for (int k = 0; k < kHeads; ++k)
+            if (works && h0 + k * lanes < heads) {
+                const T *p = src(h0 + k * lanes);
+                x[k] = *reinterpret_cast<const P *>(p);
+                y[k] = *reinterpret_cast<const P *>(p + r);
             }
-        }
-        if (!ready) {
-            for (int i = tid; i < rows * r; i += kThreads) {
-                const int row = i / r, p = i - row * r;
-                const int64_t pos = __ldg(a.pos + a.axis[p] * a.pos_stride + row0 + row);
-                const uint64_t turn = static_cast<uint64_t>(pos) * a.step[p];
-                cs[row][p] = cos_sin(a.inverse ? 0 - turn : turn);
-            }
-            __syncthreads();
-            ready = true;
-        }
+    };
+    load(lane);
+    for (int i = tid; i < rows * r; i += blockDim.x) {
+        const int t = i / r, p = i - t * r;
+        const int64_t pos = __ldg(a.pos + a.axis[p] * a.pos_stride + row0 + t);
+        const uint64_t turn = static_cast<uint64_t>(pos) * a.step[p];
+        cs[i] = cos_sin(a.inverse ? 0 - turn : turn);
+    }
+    __syncthreads();
+    if (works) {
+        float2 f[E];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            const int u = u0 + k * kThreads;
-            if (u >= units) continue;
-            const At at = place(u);
-            P s, t;
-            const T *px = reinterpret_cast<const T *>(&x[k]), *py = reinterpret_cast<const T *>(&y[k]);
-            T *ps = reinterpret_cast<T *>(&s), *pt = reinterpret_cast<T *>(&t);
+        for (int e = 0; e < E; ++e) f[e] = cs[mine * r + pair + e];
+        for (int h0 = lane; h0 < heads; h0 += kHeads * lanes) {
+            if (h0 != lane) load(h0);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float2 f = cs[at.row][at.pair + e];
-                const float p0 = widen(px, e), p1 = widen(py, e);
-                put(ps + e, fmaf(p0, f.x, -(p1 * f.y)));
-                put(pt + e, fmaf(p0, f.y, p1 * f.x));
+            for (int k = 0; k < kHeads; ++k) {
+                if (h0 + k * lanes >= heads) continue;
+                const T *px = reinterpret_cast<const T *>(&x[k]), *py = reinterpret_cast<const T *>(&y[k]);
+                P s, t;
+                T *ps = reinterpret_cast<T *>(&s), *pt = reinterpret_cast<T *>(&t);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const float p0 = widen(px, e), p1 = widen(py, e);
+                    put(ps + e, fmaf(p0, f[e].x, -(p1 * f[e].y)));
+                    put(pt + e, fmaf(p0, f[e].y, p1 * f[e].x));
+                }
+                T *p = dst(h0 + k * lanes);
+                *reinterpret_cast<P *>(p) = s;
+                *reinterpret_cast<P *>(p + r) = t;
             }
-            *reinterpret_cast<P *>(at.dst) = s;
-            *reinterpret_cast<P *>(at.dst + r) = t;
         }
     }
     // columns that are not turned
     const int rest = a.hd - 2 * r;
     if (rest > 0) {
-        for (int i = tid; i < rows * heads * rest; i += kThreads) {
-            const int row = i / (heads * rest), v = i - row * heads * rest, h = v / rest;
+        for (int i = tid; i < rows * heads * rest; i += blockDim.x) {
+            const int t = i / (heads * rest), v = i - t * heads * rest, h = v / rest;
             const int w = h >= a.heads[0], hh = w ? h - a.heads[0] : h;
             if (a.src[w] == a.dst[w]) continue;
             const int64_t at = static_cast<int64_t>(hh) * a.hd + 2 * r + (v - h * rest);
-            static_cast<T *>(a.dst[w])[(row0 + row) * a.dst_stride[w] + at] =
-                static_cast<const T *>(a.src[w])[(row0 + row) * a.src_stride[w] + at];
+            static_cast<T *>(a.dst[w])[(row0 + t) * a.dst_stride[w] + at] =
+                static_cast<const T *>(a.src[w])[(row0 + t) * a.src_stride[w] + at];
         }
     }
 }
 
 template <class T, int E>
 cudaError_t launch_e(const RopePacked &a, cudaStream_t s) {
-    // A row a block while that fills the GPU no more than twice.
-    const int n_tok = a.n_rows <= 8 * 152 ? 1 : kMaxRows;
+    // As many threads a row as give each its kHeads heads at most, where that fits
+    // a block; a block's rows fewer where the launch would not reach every SM twice.
+    const int per_head = a.n_pairs / E, heads = a.heads[0] + a.heads[1];
+    const int lanes = std::max(1, std::min((heads + kHeads - 1) / kHeads, kThreads / per_head));
+    const int per_row = per_head * lanes;
+    const int n_tok = std::max(1, std::min({kThreads / per_row, kMaxRows, a.n_rows / (2 * 152)}));
     const int64_t grid = (static_cast<int64_t>(a.n_rows) + n_tok - 1) / n_tok;
-    rope_packed_kernel<T, E><<<static_cast<unsigned>(grid), kThreads, 0, s>>>(a, n_tok);
+    const size_t smem = sizeof(float2) * n_tok * a.n_pairs;
+    rope_packed_kernel<T, E><<<static_cast<unsigned>(grid), (n_tok * per_row + 31) / 32 * 32, smem, s>>>(a, n_tok, lanes);
     return cudaGetLastError();
 }
 template <class T>

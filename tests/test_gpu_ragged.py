@@ -240,3 +240,39 @@ def test_offsets_past_32_bits():
     p = Case([1, 33], [4, 600], 2, 1, hd, BF16, prefix=640)
     p.kp, p.vp = c.k, c.v
     p.check()
+
+
+# ---- short sequences whose tiles hold the rows of several ----
+
+SHORT = [([7, 1, 30, 2, 64, 65, 1, 1, 200, 3], 0), ([5] * 60, 0), ([1] * 130, 0), ([24, 9, 40, 33], 6), ([300, 2, 290, 5], 3)]
+
+
+@pytest.mark.parametrize("ql,more", SHORT, ids=["mixed", "fives", "ones", "behind_own_keys", "long_and_short"])
+@pytest.mark.parametrize("prefix", [0, 100, 640, 2000])
+@pytest.mark.parametrize("H,KV,hd", [(8, 2, 128), (3, 3, 64), (7, 1, 80), (32, 2, 128)])
+@DTYPES
+def test_short_sequences_behind_one_another(ql, more, prefix, H, KV, hd, dtype):
+    c = Case(ql, [n + more for n in ql], H, KV, hd, dtype, prefix=prefix, gap=more, seed=len(ql))
+    c.check()
+    c.check(workspace=None)
+
+
+@pytest.mark.parametrize("hd", [128, 64])
+@BAD
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("gap", [0, 5])
+def test_a_shared_tile_keeps_sequences_apart(hd, bad, which, gap):
+    ql = [20, 7, 60, 1, 33, 90, 4]
+    c = Case(ql, ql, 4, 2, hd, BF16, prefix=300, gap=gap, seed=3)
+    clean = c.call()
+    rows = getattr(c, which)
+    for s, n in zip(c.start, c.kl):
+        rows[s + n:s + n + gap] = bad
+    got = c.call()
+    torch.cuda.synchronize()
+    assert torch.equal(got, clean)
+    rows[c.start[2] + 25] = bad  # seen by queries 25 .. 59 of sequence 2: rows 52 .. 86
+    got = c.call()
+    torch.cuda.synchronize()
+    assert torch.equal(got[:52], clean[:52]) and torch.equal(got[87:], clean[87:])
+    assert not bool(torch.isfinite(got[52:87].float()).all(dim=1).any())

@@ -15,14 +15,14 @@ def arr(v):
 
 
 def cross(ql=(3, 1), kl=(5, 0), k0=None, n=None, H=4, KV=2, hd=16, dtype=pkv.PKV_BF16, Q=4096, K=4096, V=4096, out=4096, qs=64,
-          ks=32, vs=32, os_=64, w=None, wn=0):
-    return lib.pkv_attn_cross(Q, qs, arr(ql), K, ks, V, vs, arr(kl), arr(k0), dtype, len(ql) if n is None else n, H, KV, hd, 0.25,
+          ks=32, vs=32, os_=64, w=None, wn=0, qn=1 << 20, kn=1 << 20):
+    return lib.pkv_attn_cross(Q, qs, qn, arr(ql), K, ks, V, vs, kn, arr(kl), arr(k0), dtype, len(ql) if n is None else n, H, KV, hd, 0.25,
                               out, os_, w, wn, None)
 
 
 def prefix(ql=(3, 1), kl=(5, 1), k0=None, P=7, n=None, H=4, KV=2, hd=16, dtype=pkv.PKV_BF16, Q=4096, K=4096, V=4096, Kp=4096,
-           Vp=4096, out=4096, qs=64, ks=32, vs=32, ps=32, xs=32, os_=64, w=None, wn=0):
-    return lib.pkv_attn_prefix(Q, qs, arr(ql), Kp, ps, Vp, xs, P, K, ks, V, vs, arr(kl), arr(k0), dtype,
+           Vp=4096, out=4096, qs=64, ks=32, vs=32, ps=32, xs=32, os_=64, w=None, wn=0, qn=1 << 20, kn=1 << 20):
+    return lib.pkv_attn_prefix(Q, qs, qn, arr(ql), Kp, ps, Vp, xs, P, K, ks, V, vs, kn, arr(kl), arr(k0), dtype,
                                len(ql) if n is None else n, H, KV, hd, 0.25, out, os_, w, wn, None)
 
 
@@ -35,7 +35,7 @@ COMMON = [
     (dict(qs=1 << 40), BAD_DIM), (dict(ks=1 << 40), BAD_DIM), (dict(k0=(0, -1)), BAD_DIM), (dict(k0=(BIG, 0)), BAD_DIM),
     (dict(kl=(BIG, 1)), BAD_DIM), (dict(Q=None), ARG), (dict(K=None), ARG), (dict(V=None), ARG), (dict(out=None), ARG),
     (dict(Q=4097), ARG), (dict(K=4097), ARG), (dict(V=4097), ARG), (dict(out=4097), ARG), (dict(w=4104, wn=64), ARG),
-    (dict(w=None, wn=64), ARG), (dict(w=4096, wn=-1), ARG)]
+    (dict(w=None, wn=64), ARG), (dict(w=4096, wn=-1), ARG), (dict(qn=3), ARG), (dict(kn=4), ARG), (dict(kn=14, k0=(10, 0)), ARG)]
 
 
 @pytest.mark.parametrize("kw,rc", COMMON + [(dict(ql=(BIG, BIG), kl=(1, 1)), BAD_DIM)], ids=str)
@@ -68,7 +68,8 @@ def test_workspace_sizes(H, KV, hd):
     assert size((1, 1), (100_000, 50)) % 16 == 0
     assert size((1,), (-1,)) == -1 and lib.pkv_attn_cross_workspace(arr((1,)), arr((1,)), None, 1, 3, 2, hd) == -1
     pre = lambda P, ql, kl: lib.pkv_attn_prefix_workspace(P, arr(ql), arr(kl), len(ql), H, KV, hd)
-    assert pre(4000, (1, 1, 1), (3, 9, 1)) >= 2 * 3 * per   # own keys and the prefix apart
+    assert pre(40_000, (1, 1, 1), (3, 9, 1)) >= 2 * 3 * per   # own keys and the prefix apart
+    assert pre(4000, (1, 1), (3, 9)) == 0                       # so small that clusters of blocks share the keys
     assert pre(4000, (2,), (1,)) == -1 and pre(-1, (1,), (1,)) == -1
 
 
