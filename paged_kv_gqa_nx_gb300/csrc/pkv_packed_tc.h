@@ -164,6 +164,11 @@ __device__ __forceinline__ int work_of(uint32_t answer) {
 template <int N>
 struct WholePrompts {
     static constexpr bool kRuns = false, kStacks = false;
+    // Tokens of a tile, token and head of its row m; `tile` is log2 of its heads.
+    __device__ __forceinline__ static int tokens(int tile) { return 128 >> tile; }
+    __device__ __forceinline__ static int token(int m, int tile) { return m >> tile; }
+    __device__ __forceinline__ static int head(int m, int tile) { return m & ((1 << tile) - 1); }
+    __device__ __forceinline__ static int rows(int) { return 128; }
     using Args = PackedArgs;
     using List = PackedSeqs<N>;
     // What block index w of the grid stands for.
@@ -205,6 +210,11 @@ struct WholePrompts {
 template <int N>
 struct Runs {
     static constexpr bool kRuns = true, kStacks = false;
+    // `tile` is the number of its heads; rows past the last whole token are not used.
+    __device__ __forceinline__ static int tokens(int tile) { return 128 / tile; }
+    __device__ __forceinline__ static int token(int m, int tile) { return m / tile; }
+    __device__ __forceinline__ static int head(int m, int tile) { return m % tile; }
+    __device__ __forceinline__ static int rows(int tile) { return 128 / tile * tile; }
     using Args = RaggedArgs;
     using List = RunList<RaggedRun, N>;
     struct Piece {
@@ -216,9 +226,9 @@ struct Runs {
         __device__ __forceinline__ int n_max() const { return max(n0, n1); }
         __device__ __forceinline__ int looks() const { return max(0, n_max() - look0); }
     };
-    __device__ __forceinline__ static Piece piece(const Args &a, const List &l, int log_p, int w) {
+    __device__ __forceinline__ static Piece piece(const Args &a, const List &l, int tile, int w) {
         Piece p;
-        const int TQ = 128 >> log_p, n_ht = a.n_heads >> log_p;
+        const int TQ = 128 / tile, n_ht = a.n_heads / tile;
         const int t = w / n_ht, ht = w - t * n_ht;
         int lo = 0, hi = l.n - 1;
         while (lo < hi) {
@@ -231,7 +241,7 @@ struct Runs {
         p.len = r.nq;
         p.row0 = r.q0;
         p.q0 = (pairs - 1 - (u - split * pairs)) * 2 * TQ;
-        p.h0 = ht << log_p;
+        p.h0 = ht * tile;
         p.kvh = p.h0 / (a.n_heads / a.n_kv);
         p.k0 = r.k0;
         p.nk = r.nk;
@@ -280,16 +290,16 @@ struct Stacks : Runs<N> {
     __device__ __forceinline__ static int end(const RaggedRun &r, const List &l, int t) {
         return r.k0 + r.off + (l.run[0].q0 + t - r.q0) + 1;
     }
-    __device__ __forceinline__ static Piece piece(const Args &a, const List &l, int log_p, int w) {
+    __device__ __forceinline__ static Piece piece(const Args &a, const List &l, int tile, int w) {
         Piece p;
-        const int TQ = 128 >> log_p, n_ht = a.n_heads >> log_p;
+        const int TQ = 128 / tile, n_ht = a.n_heads / tile;
         const int u = w / n_ht, ht = w - u * n_ht;
         p.row0 = l.run[0].q0;
         p.len = l.run[l.n - 1].q0 + l.run[l.n - 1].nq - p.row0;
         p.ns = l.run[0].ns;
         const int pairs = (p.len + 2 * TQ - 1) / (2 * TQ), split = u / pairs;
         p.q0 = (pairs - 1 - (u - split * pairs)) * 2 * TQ;
-        p.h0 = ht << log_p;
+        p.h0 = ht * tile;
         p.kvh = p.h0 / (a.n_heads / a.n_kv);
         p.rec = l.run[0].rec0 < 0 ? -1 : l.run[0].rec0 + split;
         p.off = p.pad0 = p.pad1 = 0;
@@ -322,7 +332,7 @@ struct Stacks : Runs<N> {
 template <int D, class T, bool kLong, class F>
 __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                                           const CUtensorMap &mkp, const CUtensorMap &mvp, const typename F::Args &a,
-                                          const typename F::List &l, int log_p) {
+                                          const typename F::List &l, int tile) {
     using C = TcCfg<D>;
     using Piece = typename F::Piece;
     constexpr int NS = C::kSlots;
@@ -348,6 +358,12 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
     if (warp == 0) {
         tmem_alloc(smem_u32(&tslot), kTcCols);
         tmem_relinquish();
+    }
+    if constexpr (F::kRuns) {  // rows of Q that no load writes
+        const int at = F::rows(tile) * 128, n = (static_cast<int>(C::kBlock) - at) / 16;
+        for (int i = tid; i < 2 * (D / 64) * n; i += kTcThreads)
+            *reinterpret_cast<uint4 *>(sm + i / n * C::kBlock + at + i % n * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async();
     }
     if (tid == 32 * kWarpLoad) {
         for (int i = 0; i < NS; ++i) {
@@ -414,7 +430,7 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
                         asm volatile("prefetch.tensormap [%0];\n" ::"l"(m) : "memory");
                 }
             }
-            Piece p = F::piece(a, l, log_p, blockIdx.x);
+            Piece p = F::piece(a, l, tile, blockIdx.x);
             for (;;) {
                 // the others' copy (len 0: nothing is left)
                 {
@@ -460,11 +476,11 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
                             if (qn[c] > 0) ok = wait_w(&bar_qfree[c], qn[c] - 1);
                             if (!ok) break;
                             if (lane == 0) {
-                                mbar_expect_tx(smem_u32(&bar_q[c]), C::kTile);
+                                mbar_expect_tx(smem_u32(&bar_q[c]), F::rows(tile) * (D * 2));
 #pragma unroll
                                 for (int x = 0; x < D / 64; ++x)
                                     tma_load3(smem_u32(sm + c * C::kTile + x * C::kBlock), &mq, 64 * x, p.h0,
-                                              p.row0 + p.q0 + c * (128 >> log_p), smem_u32(&bar_q[c]));
+                                              p.row0 + p.q0 + c * F::tokens(tile), smem_u32(&bar_q[c]));
                             }
                             ++qn[c];
                             __syncwarp();
@@ -484,7 +500,7 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
                 if (!ok) break;
                 const int w = __shfl_sync(0xffffffffu, work_of(smem_u32(&answer)), 0);
                 __syncwarp();
-                if (w >= 0) p = F::piece(a, l, log_p, w);
+                if (w >= 0) p = F::piece(a, l, tile, w);
                 else p.len = 0;
             }
             // the last copies land before the CTA's shared memory is given up (bounded)
@@ -583,7 +599,7 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
     } else {
         // -------------- compute warps: one thread per row and chain --------------
         setmaxnreg_inc<kTcComputeRegs>();
-        const int c = warp >> 2, m = tid & 127, P = 1 << log_p, TQ = 128 >> log_p;
+        const int c = warp >> 2, m = tid & 127, TQ = F::tokens(tile), head = F::head(m, tile);
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t tS = tbase + lanes + 256 + 128 * c, tO = tbase + lanes + 128 * c;
         const float cs = a.scale_log2;  // > 0
@@ -591,8 +607,8 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
         Piece p;
         while (next_piece(p)) {
             const int n = c ? p.n1 : p.n0;
-            const int tok = p.q0 + c * TQ + (m >> log_p);
-            const bool valid = tok < p.len;
+            const int tok = p.q0 + c * TQ + F::token(m, tile);
+            const bool valid = tok < p.len && m < F::rows(tile);
             int lim, from = 0;  // keys this row sees (Runs: of the run's own)
             if constexpr (F::kStacks) {
                 const RaggedRun &r = l.run[F::seq(l, valid ? tok : p.q0)];
@@ -808,7 +824,7 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
                 if constexpr (F::kRuns) record = p.rec >= 0;
                 if (record) {
                     if constexpr (F::kRuns) {
-                        const int64_t r = (p.rec + static_cast<int64_t>(tok) * p.ns) * a.n_heads + p.h0 + (m & (P - 1));
+                        const int64_t r = (p.rec + static_cast<int64_t>(tok) * p.ns) * a.n_heads + p.h0 + head;
                         float *dst = a.pacc + r * a.hd;
                         if (valid) {
                             a.pm[r] = m_ref;
@@ -827,7 +843,7 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
                 }
                 const float inv = 1.f / l_run;
                 T *dst = static_cast<T *>(a.out) + static_cast<int64_t>(p.row0 + (valid ? tok : 0)) * a.o_stride +
-                         static_cast<int64_t>(p.h0 + (m & (P - 1))) * a.hd;
+                         static_cast<int64_t>(p.h0 + head) * a.hd;
                 auto two = [&](int i) { return pack2(T{}, __uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv); };
                 if (a.out32) {  // whole 32-byte sectors
 #pragma unroll

@@ -62,15 +62,15 @@ struct RaggedArgs {
 };
 
 // Tensor-core tiles (pkv_ragged_tc.cu): 128 / P consecutive queries x P heads of
-// a kv head, P the largest power of two up to 16 in the group; a piece is two
-// of them and a split of the 128-key tiles, the prefix's and then the run's.
+// a kv head, P the largest divisor of the group up to 16 (117 rows of 128 at worst);
+// a piece is two of them and a split of the 128-key tiles, the prefix's and then the run's.
 constexpr int32_t kRaggedKeyTile = 128;
-inline int ragged_log_p(int group) {
-    int p = 0;
-    while (p < 4 && group % (2 << p) == 0) ++p;
+inline int ragged_tile_heads(int group) {
+    int p = group < 16 ? group : 16;
+    while (group % p != 0) --p;
     return p;
 }
-constexpr int32_t ragged_tile_pairs(int32_t nq, int log_p) { return (nq + (256 >> log_p) - 1) / (256 >> log_p); }
+constexpr int32_t ragged_tile_pairs(int32_t nq, int heads) { return (nq + 2 * (128 / heads) - 1) / (2 * (128 / heads)); }
 constexpr int32_t ragged_key_tiles(int32_t n_pre, int32_t nk) {
     return (n_pre + kRaggedKeyTile - 1) / kRaggedKeyTile + (nk + kRaggedKeyTile - 1) / kRaggedKeyTile;
 }

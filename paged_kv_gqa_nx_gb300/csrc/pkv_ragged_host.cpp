@@ -152,17 +152,20 @@ int pick_cluster(const std::vector<RaggedRun> &runs, const Shape &sh, const Kern
 
 // Splits of the tensor-core kernel, which runs a block a SM.  Where there are
 // fewer pieces than two rounds of blocks, key tiles are split so that the rounds are full;
-// a piece of one tile would be mostly its first scores and its output.
-void split_tiles(std::vector<RaggedRun> &runs, const Shape &sh, int32_t n_pre, int64_t coarse) {
-    const int log_p = ragged_log_p(sh.group());
+// a piece of one tile would be mostly its first scores and its output.  Records
+// and the join cost as much as eight tiles (64 queries over 1,024 keys: 17 us in one piece
+// each, 21 split), unless they are joined with others anyway.
+void split_tiles(std::vector<RaggedRun> &runs, const Shape &sh, int32_t n_pre, int64_t coarse, bool joined = false) {
+    const int heads = ragged_tile_heads(sh.group());  // of a tile
     int64_t pieces = 0, most = 0;
-    auto blocks = [&](const RaggedRun &r) { return static_cast<int64_t>(ragged_tile_pairs(r.nq, log_p)) * (sh.n_heads >> log_p); };
+    auto blocks = [&](const RaggedRun &r) { return static_cast<int64_t>(ragged_tile_pairs(r.nq, heads)) * (sh.n_heads / heads); };
     for (const RaggedRun &r : runs) {
         pieces += blocks(r);
         most = std::max<int64_t>(most, ragged_key_tiles(n_pre, r.nk));
     }
-    if (pieces > 2 * kSMs) return;
-    const int64_t room = pieces <= kSMs ? kSMs : 2 * kSMs;
+    if (pieces > 2 * kSMs || (most <= 8 && !joined)) return;
+    // (with other rows to attend at the same time, three quarters of the SMs)
+    const int64_t room = joined ? kSMs * 3 / 4 : pieces <= kSMs ? kSMs : 2 * kSMs;
     const int64_t per = coarse * least_split(2, std::max<int64_t>(2, most), room, [&](int64_t x) {
         int64_t n = 0;
         for (const RaggedRun &r : runs) n += blocks(r) * ((ragged_key_tiles(n_pre, r.nk) + x - 1) / x);
@@ -172,21 +175,22 @@ void split_tiles(std::vector<RaggedRun> &runs, const Shape &sh, int32_t n_pre, i
 }
 
 // Query rows of a tensor-core tile (queries x heads of the group) from which a
-// sequence takes it.
-constexpr int64_t kTileRows = 48;
+// sequence takes it: 24 sequences over 700 to 1,500 keys take 38 us there and 54 on the row kernel at 6
+// queries of 4 heads a kv head, 43 to 48 and 42 to 43 at 12 of one.
+constexpr int64_t kTileRows = 24;
 
 // Stretches of neighbouring sequences that share tiles.  A tile's rows
 // multiply the own keys of all its sequences, so a sequence takes part where that is
 // no more than two tiles of keys, or half of the prefix, on top: a few tokens behind a long history of
 // their own do not.  More than four stretches (launches) and the rest go by themselves.
 std::vector<std::vector<Seq>> find_stretches(std::vector<Seq> &seqs, const Shape &sh, int32_t n_pre) {
-    const int log_p = ragged_log_p(sh.group());
-    const int64_t pair = 256 >> log_p, most = std::max<int64_t>(2, ragged_key_tiles(n_pre, 0) / 2);
+    const int heads = ragged_tile_heads(sh.group());  // of a tile
+    const int64_t pair = 2 * (128 / heads), most = std::max<int64_t>(2, ragged_key_tiles(n_pre, 0) / 2);
     std::vector<std::vector<Seq>> found;
     std::vector<Seq> alone, run;
     int64_t rows = 0;
     auto close = [&] {
-        const bool take = run.size() > 1 && found.size() < 4 && (rows << log_p) >= kTileRows;
+        const bool take = run.size() > 1 && found.size() < 4 && rows * heads >= kTileRows;
         if (take) found.push_back(run);
         else alone.insert(alone.end(), run.begin(), run.end());
         run.clear();
@@ -213,8 +217,8 @@ std::vector<std::vector<Seq>> find_stretches(std::vector<Seq> &seqs, const Shape
 // like, keys are split less, or not at all.
 Plan make_plan(std::vector<Seq> seqs, const Shape &sh, int32_t n_pre, const Kernels &kernels, int64_t workspace) {
     constexpr int64_t kCoarsest = int64_t{1} << 24;
-    const int log_p = ragged_log_p(sh.group());
-    auto takes_tiles = [&](int64_t nq, int32_t keys) { return kernels.tc && keys > 0 && (nq << log_p) >= kTileRows; };
+    const int heads = ragged_tile_heads(sh.group());  // of a tile
+    auto takes_tiles = [&](int64_t nq, int32_t keys) { return kernels.tc && keys > 0 && nq * heads >= kTileRows; };
     std::vector<RaggedRun> own;
     Plan p;
     if (kernels.tc)
@@ -260,7 +264,7 @@ Plan make_plan(std::vector<Seq> seqs, const Shape &sh, int32_t n_pre, const Kern
             }
             if (p.cluster == 1) split_rows(p.rows, sh, p.wide, p.stacked ? 0 : n_pre, coarse);
             split_tiles(p.tiles, sh, n_pre, coarse);
-            split_tiles(p.tiles_pre, sh, 0, coarse);
+            split_tiles(p.tiles_pre, sh, 0, coarse, true);
         }
         // records, run by run
         int64_t at = 0;

@@ -525,75 +525,94 @@ __global__ void __launch_bounds__(32 * kRowWarps, DP <= 128 ? 4 : 2)
     if (n_ranks > 1) cluster_sync();  // the others may still read this block's part
 }
 
-// The records of a (query, head), by one warp or, where there are few of them,
-// by the four of a block (`together`).  A lane takes a record's maximum and
-// sum, then the records' outputs are added with eight on the way.
-template <class T, int N>
-__global__ void __launch_bounds__(128)
+// The records of a (query, head), by one warp or, where all such blocks run at
+// once, by the four of a block (`together`).  A lane takes a record's maximum and
+// sum, then the records' outputs are added, kBatch on the way at a time.  What
+// it takes is the latency of two dependent reads, so registers are few and blocks many
+// (17 records each of 2,048 rows and heads: 17 us one load after another, XX so).
+constexpr int kBatch = 4;
+template <class T, int N, int J>  // J: 128 dims each
+__global__ void __launch_bounds__(128, 8)
     ragged_join_kernel(const __grid_constant__ RaggedArgs a, const __grid_constant__ RunList<JoinRun, N> l, int together) {
-    __shared__ float part[4][256];
+    __shared__ __align__(16) float part[4][128 * J];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t H = a.n_heads;
     const int64_t item = together ? blockIdx.x : 4 * static_cast<int64_t>(blockIdx.x) + warp;
     const int first = together ? warp : 0, step = together ? 4 : 1;  // of this warp's records
-    wait_launch_before();
     if (item >= l.unit0[l.n] * H) return;  // (whole blocks, where warps meet below)
     const int h = static_cast<int>(item % H), t = static_cast<int>(item / H);
     const int ri = run_of(l, t), qi = t - l.unit0[ri];
     const JoinRun run = l.run[ri];
     const int64_t own = (run.rec0 + static_cast<int64_t>(qi) * run.ns) * H + h, pre = (run.pre0 + static_cast<int64_t>(qi) * run.pns) * H + h;
     const int n = run.ns + run.pns;
-    auto record = [&](int x) { return x < run.ns ? own + x * H : pre + (x - run.ns) * H; };
-    float top = -INFINITY, L = 0.f;
-    for (int x = lane; x < n; x += 32) {
-        const int64_t r = record(x);
-        const float m = __ldcg(a.pm + r), sum = __ldcg(a.pl + r);
-        const float mn = fmaxf(top, m), ref = mn == -INFINITY ? 0.f : mn;
-        L = L * pow2(top - ref) + sum * pow2(m - ref);
-        top = mn;
+    auto record = [&](int x) { return (x < run.ns ? own : pre - run.ns * H) + x * H; };
+    const float *own_out = a.pacc + own * a.hd + 4 * lane, *pre_out = a.pacc + (pre - run.ns * H) * a.hd + 4 * lane;
+    const int64_t out_step = H * a.hd;
+    wait_launch_before();
+    float m0 = -INFINITY, l0 = 0.f;  // of the lane's first record
+    if (lane < n) {
+        const int64_t r = record(lane);
+        m0 = __ldcg(a.pm + r), l0 = __ldcg(a.pl + r);
     }
-    float all = top;
+    float top = m0;
+    for (int x = 32 + lane; x < n; x += 32) top = fmaxf(top, __ldcg(a.pm + record(x)));
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) all = fmaxf(all, __shfl_xor_sync(kAll, all, s));
-    const float ref = all == -INFINITY ? 0.f : all;
-    L *= pow2(top - ref);
+    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, s));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float L = 0.f, o[J][4] = {};
+    const bool vec = (a.hd & 3) == 0;
+    for (int x0 = 0; x0 < n; x0 += 32) {
+        if (x0 > 0) {
+            m0 = -INFINITY, l0 = 0.f;
+            if (x0 + lane < n) {
+                const int64_t r = record(x0 + lane);
+                m0 = __ldcg(a.pm + r), l0 = __ldcg(a.pl + r);
+            }
+        }
+        const float f = l0 == 0.f ? 0.f : pow2(m0 - ref);  // (0: no key of it is seen, no output was written)
+        L = fmaf(l0, f, L);
+        const int m = min(32, n - x0);
+        for (int y0 = first; y0 < m; y0 += kBatch * step) {
+            float w[kBatch];
+            float4 v[kBatch][J];
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+                const int y = y0 + e * step;
+                w[e] = __shfl_sync(kAll, f, y & 31);
+                if (y >= m) w[e] = 0.f;
+                const int x = x0 + min(y, m - 1);
+                const float *src = (x < run.ns ? own_out : pre_out) + x * out_step;
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    v[e][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (w[e] == 0.f) continue;
+                    const int left = a.hd - 4 * lane - 128 * j;
+                    if (vec) {
+                        if (left > 0) v[e][j] = __ldcg(reinterpret_cast<const float4 *>(src + 128 * j));
+                    } else {
+                        if (left > 0) v[e][j].x = __ldcg(src + 128 * j);
+                        if (left > 1) v[e][j].y = __ldcg(src + 128 * j + 1);
+                        if (left > 2) v[e][j].z = __ldcg(src + 128 * j + 2);
+                        if (left > 3) v[e][j].w = __ldcg(src + 128 * j + 3);
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e)
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    o[j][0] = fmaf(w[e], v[e][j].x, o[j][0]), o[j][1] = fmaf(w[e], v[e][j].y, o[j][1]);
+                    o[j][2] = fmaf(w[e], v[e][j].z, o[j][2]), o[j][3] = fmaf(w[e], v[e][j].w, o[j][3]);
+                }
+        }
+    }
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) L += __shfl_xor_sync(kAll, L, s);
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    float o[2][4] = {};
-    const bool vec = (a.hd & 3) == 0;
-    for (int x0 = 0; x0 < n; x0 += 32) {  // a lane's weight of record x0 + lane
-        float f = 0.f;
-        if (x0 + lane < n) {
-            const int64_t r = record(x0 + lane);
-            if (__ldcg(a.pl + r) != 0.f) f = pow2(__ldcg(a.pm + r) - ref);  // (0: no key of it is seen, no output was written)
-        }
-        const int m = min(32, n - x0);
-#pragma unroll 8
-        for (int y = first; y < m; y += step) {
-            const float w = __shfl_sync(kAll, f, y);
-            const float *src = a.pacc + record(x0 + y) * a.hd;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int d = 4 * lane + 128 * j;
-                if (w == 0.f || d >= a.hd) continue;
-                if (vec) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + d));
-                    o[j][0] = fmaf(w, v.x, o[j][0]), o[j][1] = fmaf(w, v.y, o[j][1]);
-                    o[j][2] = fmaf(w, v.z, o[j][2]), o[j][3] = fmaf(w, v.w, o[j][3]);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (d + k < a.hd) o[j][k] = fmaf(w, __ldcg(src + d + k), o[j][k]);
-                }
-            }
-        }
-    }
     T *dst = static_cast<T *>(a.out) + (static_cast<int64_t>(run.q0) + qi) * a.o_stride + static_cast<int64_t>(h) * a.hd;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) part[warp][4 * lane + 128 * j + k] = o[j][k];
+    for (int j = 0; j < J; ++j)
+        *reinterpret_cast<float4 *>(&part[warp][4 * lane + 128 * j]) = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
     if (together) {
         __syncthreads();
         for (int d = threadIdx.x; d < a.hd; d += 128) narrow(dst + d, (part[0][d] + part[1][d] + part[2][d] + part[3][d]) * inv);
@@ -680,9 +699,10 @@ cudaError_t join_n(const RaggedArgs &a, const JoinRun *runs, int32_t n, cudaStre
         if (at > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     }
     l.unit0[n] = static_cast<int32_t>(at);
-    // a block a record set while that leaves the GPU room: eight of its blocks a SM
-    const int together = at * a.n_heads <= 8 * 152;
-    return start(ragged_join_kernel<T, N>, together ? at * a.n_heads : (at * a.n_heads + 3) / 4, 1, 128, 0, true, s, a, l, together);
+    const int together = at * a.n_heads <= 14 * 152;
+    const long long grid = together ? at * a.n_heads : (at * a.n_heads + 3) / 4;
+    if (a.hd > 128) return start(ragged_join_kernel<T, N, 2>, grid, 1, 128, 0, true, s, a, l, together);
+    return start(ragged_join_kernel<T, N, 1>, grid, 1, 128, 0, true, s, a, l, together);
 }
 template <class T>
 cudaError_t join_t(const RaggedArgs &a, const JoinRun *runs, int32_t n, cudaStream_t s) {

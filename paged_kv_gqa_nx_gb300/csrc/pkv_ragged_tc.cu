@@ -23,9 +23,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     ragged_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mkp,
                      const __grid_constant__ CUtensorMap mvp, const __grid_constant__ RaggedArgs a,
-                     const __grid_constant__ RunList<RaggedRun, N> l, int log_p) {
+                     const __grid_constant__ RunList<RaggedRun, N> l, int heads) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    packed_tc<D, T, kLong, F>(mq, mk, mv, mkp, mvp, a, l, log_p);
+    packed_tc<D, T, kLong, F>(mq, mk, mv, mkp, mvp, a, l, heads);
     asm volatile("griddepcontrol.wait;\n" ::: "memory");  // so that the join behind this launch has all of them
 }
 
@@ -44,26 +44,26 @@ cudaError_t tc_n(const RaggedArgs &a, const RaggedRun *runs, int32_t n, cudaStre
                                     static_cast<int>(C::kSmem));
     });
     if (e != cudaSuccess) return e;
-    const int log_p = ragged_log_p(a.n_heads / a.n_kv);
+    const int heads = ragged_tile_heads(a.n_heads / a.n_kv);  // of a tile
     RunList<RaggedRun, N> l;
     l.n = n;
     int64_t at = 0, q_rows = 0, k_rows = 0;
     for (int32_t i = 0; i < n; ++i) {
         l.run[i] = runs[i];
         l.unit0[i] = static_cast<int32_t>(at);
-        if (!F::kStacks) at += static_cast<int64_t>(ragged_tile_pairs(runs[i].nq, log_p)) * runs[i].ns;
+        if (!F::kStacks) at += static_cast<int64_t>(ragged_tile_pairs(runs[i].nq, heads)) * runs[i].ns;
         q_rows = std::max<int64_t>(q_rows, static_cast<int64_t>(runs[i].q0) + runs[i].nq);
         k_rows = std::max<int64_t>(k_rows, static_cast<int64_t>(runs[i].k0) + runs[i].nk);
         if (at > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     }
     l.unit0[n] = static_cast<int32_t>(at);
-    if (F::kStacks) at = static_cast<int64_t>(ragged_tile_pairs(runs[n - 1].q0 + runs[n - 1].nq - runs[0].q0, log_p)) * runs[0].ns;
-    const int64_t grid = at * (a.n_heads >> log_p);
+    if (F::kStacks) at = static_cast<int64_t>(ragged_tile_pairs(runs[n - 1].q0 + runs[n - 1].nq - runs[0].q0, heads)) * runs[0].ns;
+    const int64_t grid = at * (a.n_heads / heads);
     if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     EncodeTiled f;
     CUtensorMap mq, mk, mv, mkp, mvp;
     e = encode_tiled(&f);
-    if (e == cudaSuccess) e = rows_map(&mq, f, a.type, a.hd, q_rows, a.Q, a.q_stride, a.n_heads, 1 << log_p, 128 >> log_p);
+    if (e == cudaSuccess) e = rows_map(&mq, f, a.type, a.hd, q_rows, a.Q, a.q_stride, a.n_heads, heads, 128 / heads);
     if (e == cudaSuccess) e = rows_map(&mk, f, a.type, a.hd, k_rows, a.K, a.k_stride, a.n_kv, 1, kKeys);
     if (e == cudaSuccess) e = rows_map(&mv, f, a.type, a.hd, k_rows, a.V, a.v_stride, a.n_kv, 1, kKeys);
     mkp = mk;
@@ -85,7 +85,7 @@ cudaError_t tc_n(const RaggedArgs &a, const RaggedRun *runs, int32_t n, cudaStre
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = a.overlap ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, ragged_tc_kernel<D, T, N, kLong, F>, mq, mk, mv, mkp, mvp, b, l, log_p);
+    return cudaLaunchKernelEx(&cfg, ragged_tc_kernel<D, T, N, kLong, F>, mq, mk, mv, mkp, mvp, b, l, heads);
 }
 
 template <int D, class T>
