@@ -832,8 +832,12 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
                         }
                         if (valid && l_run != 0.f) {
 #pragma unroll
-                            for (int i = 0; i < D; i += 4)
-                                if (i < a.hd) *reinterpret_cast<uint4 *>(dst + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                            for (int i = 0; i < D; i += 8)  // whole sectors
+                                if (i < a.hd)
+                                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + i),
+                                                 "r"(o[i]), "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]),
+                                                 "r"(o[i + 5]), "r"(o[i + 6]), "r"(o[i + 7])
+                                                 : "memory");
                         }
                     }
                     ++pieces;

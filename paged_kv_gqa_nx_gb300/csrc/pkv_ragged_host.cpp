@@ -70,8 +70,11 @@ struct Kernels {
     bool vec, tc;  // rows on 16-byte boundaries; the tensor-core tiles take them
 };
 
+// Maxima, sums and outputs of records start on 32-byte boundaries, as the
+// tensor-core kernel stores whole sectors; the workspace itself on 16.
+int64_t record_stats(int64_t n_rec, const Shape &sh) { return (n_rec * sh.n_heads + 7) & ~int64_t{7}; }
 int64_t record_bytes(int64_t n_rec, const Shape &sh) {
-    return 4 * (2 * static_cast<int64_t>(record_floats(n_rec, sh.n_heads)) + n_rec * sh.n_heads * sh.hd);
+    return n_rec == 0 ? 0 : 16 + 4 * (2 * record_stats(n_rec, sh) + n_rec * sh.n_heads * sh.hd);
 }
 
 // Keys of a cluster's block up to which a cluster is worth it: with more, more
@@ -107,11 +110,11 @@ int64_t least_split(int64_t least, int64_t most, int64_t room, F &&total) {
     return least;
 }
 
-// Splits of the row kernel.  Where there are few units, three quarters of what the GPU holds at once
-// (three documents of 50,000 to 120,000 keys: 208 us, with all of it 218, with twice as
-// many 216); where whole runs nearly fill it, runs
-// longer than two thirds of a slot's share are split, so that the last ones end
-// with the others.  `coarse` times as many keys a split where the workspace is
+// Splits of the row kernel.  Where there are few units, three quarters of what the
+// GPU holds at once (three documents of 50,000 to 120,000 keys: 208 us, with all of
+// it 218, with twice as many 216); where whole runs nearly fill it, runs longer than
+// a slot's share are split (200 runs of 100 to 2,000 keys: 84 us, with half the
+// share 92).  `coarse` times as many keys a split where the workspace is
 // short.  A split below 256 keys is mostly latency.
 void split_rows(std::vector<RaggedRun> &runs, const Shape &sh, int wide, int64_t n_pre, int64_t coarse) {
     int64_t work = 0, units = 0, most = 256;
@@ -122,8 +125,8 @@ void split_rows(std::vector<RaggedRun> &runs, const Shape &sh, int wide, int64_t
         work += blocks(r) * keys(r);
         most = std::max(most, keys(r));
     }
-    const int64_t slots = row_slots(sh), room = slots * 3 / 2, few = slots * 3 / 4;
-    int64_t per = (work + room - 1) / room;
+    const int64_t slots = row_slots(sh), few = slots * 3 / 4;
+    int64_t per = (work + slots - 1) / slots;
     if (2 * units <= slots)
         per = least_split(256, most, few, [&](int64_t x) {
             int64_t n = 0;
@@ -312,7 +315,8 @@ Plan make_plan(std::vector<Seq> seqs, const Shape &sh, int32_t n_pre, const Kern
         }
         p.n_rec = at;
         if (at > 0 && (at > 0x7fffffff || record_bytes(at, sh) > workspace)) continue;
-        // the longest pieces first: the launch then ends on its shortest
+        // the longest pieces and splits first: the launches then end on their shortest
+        std::stable_sort(p.rows.begin(), p.rows.end(), [&](const RaggedRun &x, const RaggedRun &y) { return x.nk / x.ns > y.nk / y.ns; });
         std::stable_sort(p.tiles.begin(), p.tiles.end(), [&](const RaggedRun &x, const RaggedRun &y) {
             return ragged_split_tiles(n_pre, x) > ragged_split_tiles(n_pre, y);
         });
@@ -451,9 +455,9 @@ int attend(const Call &c, cudaStream_t st) {
             const int r = contiguous_error_word(st, &a.err);
             if (r) return r;
         }
-        a.pm = static_cast<float *>(c.workspace);
-        a.pl = a.pm + record_floats(p.n_rec, c.sh.n_heads);
-        a.pacc = a.pl + record_floats(p.n_rec, c.sh.n_heads);
+        a.pm = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(c.workspace) + 31) & ~uintptr_t{31});
+        a.pl = a.pm + record_stats(p.n_rec, c.sh);
+        a.pacc = a.pl + record_stats(p.n_rec, c.sh);
         bool first = true;
         enum { kRows, kTiles, kStretch };
         auto run = [&](RaggedArgs b, const std::vector<RaggedRun> &runs, int how) {
@@ -516,6 +520,7 @@ int rope(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, int32
 
     RopePacked a{};
     int32_t count[kRopeAxes] = {};
+    double turns = 0.0, fall = 1.0;
     for (int32_t i = 0, axis = 0, first = 0; i < n; ++i) {
         while (i >= first + pairs[axis]) first += pairs[axis++];
         int32_t mine = axis, number = i, ramp = n;
@@ -528,7 +533,15 @@ int rope(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, int32
         }
         ++count[mine];
         a.axis[i] = static_cast<uint8_t>(mine);
-        a.step[i] = static_cast<uint64_t>(std::ldexp(std::pow(base, -static_cast<double>(number) / ramp) / 6.283185307179586477, 64));
+        // turns a position; a ramp falls by one factor a pair, with a power every
+        // eighth (64 powers take 1 us, products between them cost a few last places)
+        if (number % 8 == 0) {
+            turns = std::pow(base, -static_cast<double>(number) / ramp) / 6.283185307179586477;
+            if (number == 0) fall = std::pow(base, -1.0 / ramp);
+        } else {
+            turns *= fall;
+        }
+        a.step[i] = static_cast<uint64_t>(std::ldexp(turns, 64));
     }
     for (int32_t x = 0; x < n_axes; ++x)
         if (count[x] != pairs[x])

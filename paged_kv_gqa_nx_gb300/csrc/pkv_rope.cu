@@ -67,7 +67,7 @@ __device__ __forceinline__ float2 cos_sin(uint64_t turn) {
 
 // E elements a piece; the block takes n_tok rows, each by `lanes` threads a piece.
 template <class T, int E>
-__global__ void __launch_bounds__(kThreads) rope_packed_kernel(const __grid_constant__ RopePacked a, int n_tok, int lanes) {
+__global__ void __launch_bounds__(kThreads, 3) rope_packed_kernel(const __grid_constant__ RopePacked a, int n_tok, int lanes) {
     using P = typename Piece<E * sizeof(T)>::type;
     extern __shared__ float2 cs[];  // [n_tok][n_pairs]
     const int r = a.n_pairs, tid = threadIdx.x, per_head = r / E, per_row = per_head * lanes;
