@@ -1,6 +1,6 @@
 // pkv_packed_tc.h -- the tensor-core kernel of packed 16-bit rows: whole prompts
 // (pkv_packed.cu) and runs of queries over keys of other lengths, behind a
-// shared prefix or not (pkv_ragged_tc.cu).
+// shared prefix or not (pkv_ragged_tc.h).
 #pragma once
 
 #include "pkv_half.h"
@@ -99,8 +99,10 @@ template <int D>
 struct TcCfg {
     static constexpr uint32_t kTile = kKeys * D * 2;         // bytes of a Q, K or V tile
     static constexpr uint32_t kBlock = kKeys * 128;          // 64 columns of it
-    static constexpr int kSlots = D == 128 ? 5 : 8;
-    static constexpr size_t kSmem = (2 + kSlots) * kTile + 1024;  // + alignment slack
+    // Heads wider than 128: one chain, whose O takes the columns of both
+    static constexpr int kChains = D > 128 ? 1 : 2;
+    static constexpr int kSlots = D == 64 ? 8 : D == 128 ? 5 : D == 192 ? 3 : 2;
+    static constexpr size_t kSmem = (kChains + kSlots) * kTile + 1024;  // + alignment slack
 };
 
 __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t mbar) {
@@ -207,7 +209,7 @@ struct WholePrompts {
 // Runs of queries over keys of their own, behind a shared prefix or not, the
 // key tiles (the prefix's, then the run's) split or not.  A piece has at least one key tile a
 // chain, seen or not, so that every row's record is written.
-template <int N>
+template <int N, int kChains>
 struct Runs {
     static constexpr bool kRuns = true, kStacks = false;
     // `tile` is the number of its heads; rows past the last whole token are not used.
@@ -237,10 +239,10 @@ struct Runs {
             else hi = mid - 1;
         }
         const RaggedRun r = l.run[lo];
-        const int pairs = (r.nq + 2 * TQ - 1) / (2 * TQ), u = t - l.unit0[lo], split = u / pairs;
+        const int pairs = (r.nq + kChains * TQ - 1) / (kChains * TQ), u = t - l.unit0[lo], split = u / pairs;
         p.len = r.nq;
         p.row0 = r.q0;
-        p.q0 = (pairs - 1 - (u - split * pairs)) * 2 * TQ;
+        p.q0 = (pairs - 1 - (u - split * pairs)) * kChains * TQ;
         p.h0 = ht * tile;
         p.kvh = p.h0 / (a.n_heads / a.n_kv);
         p.k0 = r.k0;
@@ -255,7 +257,7 @@ struct Runs {
             return min(pre + (min(r.nk, r.off + q + 1) + kKeys - 1) / kKeys - p.j0, per);
         };
         p.n0 = max(1, tiles(min(p.q0 + TQ, r.nq) - 1));
-        p.n1 = p.q0 + TQ >= r.nq ? 0 : max(1, tiles(min(p.q0 + 2 * TQ, r.nq) - 1));
+        p.n1 = kChains == 1 || p.q0 + TQ >= r.nq ? 0 : max(1, tiles(min(p.q0 + 2 * TQ, r.nq) - 1));
         p.look0 = max(0, pre + min(r.nk, r.off + p.q0 + 1) / kKeys - p.j0);
         return p;
     }
@@ -269,12 +271,12 @@ struct Runs {
 // shared prefix, own key rows in the same order: a tile may hold rows of several
 // sequences, and its own keys are those of all of them, of which a row
 // sees a stretch.  A list holds one such stretch.
-template <int N>
-struct Stacks : Runs<N> {
+template <int N, int kChains>
+struct Stacks : Runs<N, kChains> {
     static constexpr bool kStacks = true;
-    using typename Runs<N>::Args;
-    using typename Runs<N>::List;
-    using typename Runs<N>::Piece;
+    using typename Runs<N, kChains>::Args;
+    using typename Runs<N, kChains>::List;
+    using typename Runs<N, kChains>::Piece;
     // The sequence of row t of the stretch.
     __device__ __forceinline__ static int seq(const List &l, int t) {
         const int q = l.run[0].q0 + t;
@@ -297,13 +299,13 @@ struct Stacks : Runs<N> {
         p.row0 = l.run[0].q0;
         p.len = l.run[l.n - 1].q0 + l.run[l.n - 1].nq - p.row0;
         p.ns = l.run[0].ns;
-        const int pairs = (p.len + 2 * TQ - 1) / (2 * TQ), split = u / pairs;
-        p.q0 = (pairs - 1 - (u - split * pairs)) * 2 * TQ;
+        const int pairs = (p.len + kChains * TQ - 1) / (kChains * TQ), split = u / pairs;
+        p.q0 = (pairs - 1 - (u - split * pairs)) * kChains * TQ;
         p.h0 = ht * tile;
         p.kvh = p.h0 / (a.n_heads / a.n_kv);
         p.rec = l.run[0].rec0 < 0 ? -1 : l.run[0].rec0 + split;
         p.off = p.pad0 = p.pad1 = 0;
-        const int last0 = min(p.q0 + TQ, p.len) - 1, last = min(p.q0 + 2 * TQ, p.len) - 1;
+        const int last0 = min(p.q0 + TQ, p.len) - 1, last = min(p.q0 + kChains * TQ, p.len) - 1;
         p.k0 = l.run[seq(l, p.q0)].k0;
         p.nk = end(l.run[seq(l, last)], l, last) - p.k0;
         const int pre = (a.n_pre + kKeys - 1) / kKeys, all = pre + (p.nk + kKeys - 1) / kKeys, per = (all + p.ns - 1) / p.ns;
@@ -335,11 +337,12 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
                                           const typename F::List &l, int tile) {
     using C = TcCfg<D>;
     using Piece = typename F::Piece;
+    static_assert(!kLong || D <= 128, "sums are set aside in registers");
     constexpr int NS = C::kSlots;
     extern __shared__ __align__(1024) unsigned char smraw[];
     unsigned char *sm = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smraw) + 1023) & ~static_cast<uintptr_t>(1023));
-    unsigned char *ring = sm + 2 * C::kTile;  // Q_c at c * kTile
+    unsigned char *ring = sm + C::kChains * C::kTile;  // Q_c at c * kTile
     __shared__ uint64_t bar_full[NS], bar_free[NS], bar_q[2], bar_qfree[2], bar_s[2], bar_p[2], bar_o[2], bar_ofree[2];
     __shared__ uint64_t bar_go[4], bar_look[4], bar_answer, bar_work[2], bar_wfree[2];
     __shared__ __align__(16) uint4 answer;
@@ -361,7 +364,7 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
     }
     if constexpr (F::kRuns) {  // rows of Q that no load writes
         const int at = F::rows(tile) * 128, n = (static_cast<int>(C::kBlock) - at) / 16;
-        for (int i = tid; i < 2 * (D / 64) * n; i += kTcThreads)
+        for (int i = tid; i < C::kChains * (D / 64) * n; i += kTcThreads)
             *reinterpret_cast<uint4 *>(sm + i / n * C::kBlock + at + i % n * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async();
     }
@@ -806,62 +809,63 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
                 ok = wait_w(&bar_o[c], pieces);
                 if (!ok) break;
                 fence_after_sync();
-                uint32_t o[D];
+                constexpr int kPart = D > 128 ? 64 : D;  // columns at a time
+#pragma unroll 1
+                for (int i0 = 0; i0 < D; i0 += kPart) {
+                    uint32_t o[kPart];
 #pragma unroll
-                for (int i = 0; i < D; i += 32) tmem_ld32_issue(tO + i, o + i);
-                tmem_ld_done(o);
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar_ofree[c]));
-                if constexpr (kLong) {
-                    if (n > step) {
-#pragma unroll
-                        for (int i = 0; i < D; ++i)
-                            o[i] = __float_as_uint(fmaf(aside(hold[i / 4], i & 3), unit, __uint_as_float(o[i])));
+                    for (int i = 0; i < kPart; i += 32) tmem_ld32_issue(tO + i0 + i, o + i);
+                    tmem_ld_done(o);
+                    if (i0 + kPart == D) {
+                        fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&bar_ofree[c]));
                     }
-                }
-                bool record = false;
-                if constexpr (F::kRuns) record = p.rec >= 0;
-                if (record) {
+                    if constexpr (kLong) {
+                        if (n > step) {
+#pragma unroll
+                            for (int i = 0; i < D; ++i)
+                                o[i] = __float_as_uint(fmaf(aside(hold[i / 4], i & 3), unit, __uint_as_float(o[i])));
+                        }
+                    }
                     if constexpr (F::kRuns) {
-                        const int64_t r = (p.rec + static_cast<int64_t>(tok) * p.ns) * a.n_heads + p.h0 + head;
-                        float *dst = a.pacc + r * a.hd;
-                        if (valid) {
-                            a.pm[r] = m_ref;
-                            a.pl[r] = l_run;
-                        }
-                        if (valid && l_run != 0.f) {
+                        if (p.rec >= 0) {
+                            const int64_t r = (p.rec + static_cast<int64_t>(tok) * p.ns) * a.n_heads + p.h0 + head;
+                            float *dst = a.pacc + r * a.hd + i0;
+                            if (valid && i0 == 0) {
+                                a.pm[r] = m_ref;
+                                a.pl[r] = l_run;
+                            }
+                            if (valid && l_run != 0.f) {
 #pragma unroll
-                            for (int i = 0; i < D; i += 8)  // whole sectors
-                                if (i < a.hd)
-                                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + i),
-                                                 "r"(o[i]), "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]),
-                                                 "r"(o[i + 5]), "r"(o[i + 6]), "r"(o[i + 7])
-                                                 : "memory");
+                                for (int i = 0; i < kPart; i += 8)  // whole sectors
+                                    if (i0 + i < a.hd)
+                                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + i),
+                                                     "r"(o[i]), "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]),
+                                                     "r"(o[i + 5]), "r"(o[i + 6]), "r"(o[i + 7])
+                                                     : "memory");
+                            }
+                            continue;
                         }
                     }
-                    ++pieces;
-                    it += 2 * p.n_max();
-                    lk += p.looks();
-                    continue;
-                }
-                const float inv = 1.f / l_run;
-                T *dst = static_cast<T *>(a.out) + static_cast<int64_t>(p.row0 + (valid ? tok : 0)) * a.o_stride +
-                         static_cast<int64_t>(p.h0 + head) * a.hd;
-                auto two = [&](int i) { return pack2(T{}, __uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv); };
-                if (a.out32) {  // whole 32-byte sectors
+                    const float inv = 1.f / l_run;
+                    T *dst = static_cast<T *>(a.out) + static_cast<int64_t>(p.row0 + (valid ? tok : 0)) * a.o_stride +
+                             static_cast<int64_t>(p.h0 + head) * a.hd + i0;
+                    auto two = [&](int i) { return pack2(T{}, __uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv); };
+                    if (a.out32) {  // whole 32-byte sectors
 #pragma unroll
-                    for (int i = 0; i < D; i += 16)
-                        if (valid && i < a.hd)
-                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + i),
-                                         "r"(two(i)), "r"(two(i + 2)), "r"(two(i + 4)), "r"(two(i + 6)), "r"(two(i + 8)),
-                                         "r"(two(i + 10)), "r"(two(i + 12)), "r"(two(i + 14))
-                                         : "memory");
-                } else {
+                        for (int i = 0; i < kPart; i += 16)
+                            if (valid && i0 + i < a.hd)
+                                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + i),
+                                             "r"(two(i)), "r"(two(i + 2)), "r"(two(i + 4)), "r"(two(i + 6)), "r"(two(i + 8)),
+                                             "r"(two(i + 10)), "r"(two(i + 12)), "r"(two(i + 14))
+                                             : "memory");
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < D; i += 8)
-                        if (valid && i < a.hd)
-                            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(two(i), two(i + 2), two(i + 4), two(i + 6));
+                        for (int i = 0; i < kPart; i += 8)
+                            if (valid && i0 + i < a.hd)
+                                *reinterpret_cast<uint4 *>(dst + i) = make_uint4(two(i), two(i + 2), two(i + 4), two(i + 6));
+                    }
                 }
                 ++pieces;
             }

@@ -61,28 +61,34 @@ struct RaggedArgs {
     bool overlap;   // the launch may start before the one in front of it on the stream has ended
 };
 
-// Tensor-core tiles (pkv_ragged_tc.cu): 128 / P consecutive queries x P heads of
+// Tensor-core tiles (pkv_ragged_tc.h): 128 / P consecutive queries x P heads of
 // a kv head, P the largest divisor of the group up to 16 (117 rows of 128 at worst);
-// a piece is two of them and a split of the 128-key tiles, the prefix's and then the run's.
+// a piece is two of them, one of heads wider than 128, and a split of the 128-key
+// tiles, the prefix's and then the run's.
 constexpr int32_t kRaggedKeyTile = 128;
 inline int ragged_tile_heads(int group) {
     int p = group < 16 ? group : 16;
     while (group % p != 0) --p;
     return p;
 }
-constexpr int32_t ragged_tile_pairs(int32_t nq, int heads) { return (nq + 2 * (128 / heads) - 1) / (2 * (128 / heads)); }
+constexpr int32_t ragged_piece_tokens(int heads, int hd) { return (hd > 128 ? 1 : 2) * (128 / heads); }
+constexpr int32_t ragged_pieces(int32_t nq, int tokens) { return (nq + tokens - 1) / tokens; }
 constexpr int32_t ragged_key_tiles(int32_t n_pre, int32_t nk) {
     return (n_pre + kRaggedKeyTile - 1) / kRaggedKeyTile + (nk + kRaggedKeyTile - 1) / kRaggedKeyTile;
 }
 constexpr int32_t ragged_split_tiles(int32_t n_pre, const RaggedRun &r) { return (ragged_key_tiles(n_pre, r.nk) + r.ns - 1) / r.ns; }
 // TMA's alignment rules, and a positive finite scale (the kernel masks with
 // -inf before it scales).
-inline bool ragged_tc_takes(const RaggedArgs &a) {
-    return a.vec && a.hd <= 128 && a.scale_log2 > 0.f && a.scale_log2 <= 3e38f;
-}
+inline bool ragged_tc_takes(const RaggedArgs &a) { return a.vec && a.scale_log2 > 0.f && a.scale_log2 <= 3e38f; }
+// Keys that a piece of heads wider than 128, or of sequences that share tiles,
+// may add up (the tensor core rounds sums toward zero; other pieces set longer
+// ones aside).
+constexpr int32_t kRaggedSumKeys = 16384 - 2 * kRaggedKeyTile;
 // stack: the runs are sequences whose queries and own key rows follow one
 // another; their tiles are those of the whole stretch (ns and rec0 of the first count).
 cudaError_t launch_ragged_tc(const RaggedArgs &a, const RaggedRun *runs, int32_t n, bool stack, cudaStream_t s);
+cudaError_t launch_ragged_tc_bf16(const RaggedArgs &a, const RaggedRun *runs, int32_t n, bool stack, cudaStream_t s);
+cudaError_t launch_ragged_tc_f16(const RaggedArgs &a, const RaggedRun *runs, int32_t n, bool stack, cudaStream_t s);
 
 // Few query rows by warp-level MMAs (pkv_ragged_rows.cu): units of 8 * wide
 // rows ((query, head of the group) pairs) of one kv head; wide 1, 2 or, for heads up to 128, 4

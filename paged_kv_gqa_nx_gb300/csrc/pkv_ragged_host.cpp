@@ -161,7 +161,7 @@ int pick_cluster(const std::vector<RaggedRun> &runs, const Shape &sh, const Kern
 void split_tiles(std::vector<RaggedRun> &runs, const Shape &sh, int32_t n_pre, int64_t coarse, bool joined = false) {
     const int heads = ragged_tile_heads(sh.group());  // of a tile
     int64_t pieces = 0, most = 0;
-    auto blocks = [&](const RaggedRun &r) { return static_cast<int64_t>(ragged_tile_pairs(r.nq, heads)) * (sh.n_heads / heads); };
+    auto blocks = [&](const RaggedRun &r) { return static_cast<int64_t>(ragged_pieces(r.nq, ragged_piece_tokens(heads, sh.hd))) * (sh.n_heads / heads); };
     for (const RaggedRun &r : runs) {
         pieces += blocks(r);
         most = std::max<int64_t>(most, ragged_key_tiles(n_pre, r.nk));
@@ -188,7 +188,7 @@ constexpr int64_t kTileRows = 24;
 // their own do not.  More than four stretches (launches) and the rest go by themselves.
 std::vector<std::vector<Seq>> find_stretches(std::vector<Seq> &seqs, const Shape &sh, int32_t n_pre) {
     const int heads = ragged_tile_heads(sh.group());  // of a tile
-    const int64_t pair = 2 * (128 / heads), most = std::max<int64_t>(2, ragged_key_tiles(n_pre, 0) / 2);
+    const int64_t pair = ragged_piece_tokens(heads, sh.hd), most = std::max<int64_t>(2, ragged_key_tiles(n_pre, 0) / 2);
     std::vector<std::vector<Seq>> found;
     std::vector<Seq> alone, run;
     int64_t rows = 0;
@@ -200,7 +200,7 @@ std::vector<std::vector<Seq>> find_stretches(std::vector<Seq> &seqs, const Shape
         rows = 0;
     };
     for (const Seq &s : seqs) {
-        const bool fits = s.off != kSees && s.off * pair <= 128 * most * s.nq && n_pre + s.nk <= 16384 - 256;
+        const bool fits = s.off != kSees && s.off * pair <= 128 * most * s.nq && n_pre + s.nk <= kRaggedSumKeys;
         const bool follows = !run.empty() && s.q0 == run.back().q0 + run.back().nq && s.k0 >= run.back().k0 + run.back().nk &&
                              s.k0 - (run.back().k0 + run.back().nk) <= 32;
         if (!fits || (!run.empty() && !follows)) close();
@@ -221,7 +221,9 @@ std::vector<std::vector<Seq>> find_stretches(std::vector<Seq> &seqs, const Shape
 Plan make_plan(std::vector<Seq> seqs, const Shape &sh, int32_t n_pre, const Kernels &kernels, int64_t workspace) {
     constexpr int64_t kCoarsest = int64_t{1} << 24;
     const int heads = ragged_tile_heads(sh.group());  // of a tile
-    auto takes_tiles = [&](int64_t nq, int32_t keys) { return kernels.tc && keys > 0 && nq * heads >= kTileRows; };
+    auto takes_tiles = [&](int64_t nq, int32_t keys) {
+        return kernels.tc && keys > 0 && nq * heads >= kTileRows && (sh.hd <= 128 || keys <= kRaggedSumKeys);
+    };
     std::vector<RaggedRun> own;
     Plan p;
     if (kernels.tc)
@@ -394,7 +396,7 @@ int64_t workspace_of(const Call &c) {
     int64_t most = 0;
     each_chunk(seqs, [&](const std::vector<Seq> &part) {
         // (alignment and scale, which a call's kernels go by too, are not known here)
-        const bool vec = c.sh.hd % 8 == 0, tc = vec && c.sh.hd <= 128;
+        const bool vec = c.sh.hd % 8 == 0, tc = vec;
         for (const Kernels k : {Kernels{false, false}, Kernels{vec, false}, Kernels{vec, tc}})
             most = std::max(most, record_bytes(make_plan(part, c.sh, c.n_pre, k, int64_t{1} << 62).n_rec, c.sh));
         return PKV_OK;

@@ -1,4 +1,4 @@
-// pkv_ragged_tc.cu -- many query rows over keys of other lengths (cross
+// pkv_ragged_tc.h -- many query rows over keys of other lengths (cross
 // attention's prompts, prompts behind a shared prefix, the stacked rows of a
 // batch over the prefix) on the tensor-core kernel of packed rows
 // (pkv_packed_tc.h): its tiles, chains and turns, with keys from two stretches
@@ -11,6 +11,8 @@
 //
 // The prefix's last tile is filled up with zeros by its own tensor map, so only
 // tiles of a run's own keys are looked over for values that are not finite.
+#pragma once
+
 #include "pkv_packed_tc.h"
 
 #include <algorithm>
@@ -44,20 +46,20 @@ cudaError_t tc_n(const RaggedArgs &a, const RaggedRun *runs, int32_t n, cudaStre
                                     static_cast<int>(C::kSmem));
     });
     if (e != cudaSuccess) return e;
-    const int heads = ragged_tile_heads(a.n_heads / a.n_kv);  // of a tile
+    const int heads = ragged_tile_heads(a.n_heads / a.n_kv), tokens = ragged_piece_tokens(heads, a.hd);  // of a tile, of a piece
     RunList<RaggedRun, N> l;
     l.n = n;
     int64_t at = 0, q_rows = 0, k_rows = 0;
     for (int32_t i = 0; i < n; ++i) {
         l.run[i] = runs[i];
         l.unit0[i] = static_cast<int32_t>(at);
-        if (!F::kStacks) at += static_cast<int64_t>(ragged_tile_pairs(runs[i].nq, heads)) * runs[i].ns;
+        if (!F::kStacks) at += static_cast<int64_t>(ragged_pieces(runs[i].nq, tokens)) * runs[i].ns;
         q_rows = std::max<int64_t>(q_rows, static_cast<int64_t>(runs[i].q0) + runs[i].nq);
         k_rows = std::max<int64_t>(k_rows, static_cast<int64_t>(runs[i].k0) + runs[i].nk);
         if (at > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     }
     l.unit0[n] = static_cast<int32_t>(at);
-    if (F::kStacks) at = static_cast<int64_t>(ragged_tile_pairs(runs[n - 1].q0 + runs[n - 1].nq - runs[0].q0, heads)) * runs[0].ns;
+    if (F::kStacks) at = static_cast<int64_t>(ragged_pieces(runs[n - 1].q0 + runs[n - 1].nq - runs[0].q0, tokens)) * runs[0].ns;
     const int64_t grid = at * (a.n_heads / heads);
     if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     EncodeTiled f;
@@ -90,25 +92,26 @@ cudaError_t tc_n(const RaggedArgs &a, const RaggedRun *runs, int32_t n, cudaStre
 
 template <int D, class T>
 cudaError_t tc_d(const RaggedArgs &a, const RaggedRun *runs, int32_t n, bool stack, cudaStream_t s) {
-    if (stack)
-        return n <= kRaggedSmall ? tc_n<D, T, kRaggedSmall, false, Stacks<kRaggedSmall>>(a, runs, n, s)
-                                 : tc_n<D, T, kRaggedLarge, false, Stacks<kRaggedLarge>>(a, runs, n, s);
+    constexpr int kC = TcCfg<D>::kChains, kS = kRaggedSmall, kL = kRaggedLarge;
     bool is_long = false;  // some piece adds more keys than a sum takes
-    for (int32_t i = 0; i < n; ++i) is_long = is_long || ragged_split_tiles(a.n_pre, runs[i]) * kKeys > kLongKeys;
-    if (is_long) return tc_n<D, T, kRaggedLarge, true, Runs<kRaggedLarge>>(a, runs, n, s);
-    return n <= kRaggedSmall ? tc_n<D, T, kRaggedSmall, false, Runs<kRaggedSmall>>(a, runs, n, s)
-                             : tc_n<D, T, kRaggedLarge, false, Runs<kRaggedLarge>>(a, runs, n, s);
+    for (int32_t i = 0; i < n && !stack; ++i) is_long = is_long || ragged_split_tiles(a.n_pre, runs[i]) * kKeys > kLongKeys;
+    if constexpr (D > 128) {
+        if (is_long) return cudaErrorInvalidValue;
+        return stack ? tc_n<D, T, kL, false, Stacks<kL, kC>>(a, runs, n, s) : tc_n<D, T, kL, false, Runs<kL, kC>>(a, runs, n, s);
+    } else {
+        if (stack) return n <= kS ? tc_n<D, T, kS, false, Stacks<kS, kC>>(a, runs, n, s) : tc_n<D, T, kL, false, Stacks<kL, kC>>(a, runs, n, s);
+        if (is_long) return tc_n<D, T, kL, true, Runs<kL, kC>>(a, runs, n, s);
+        return n <= kS ? tc_n<D, T, kS, false, Runs<kS, kC>>(a, runs, n, s) : tc_n<D, T, kL, false, Runs<kL, kC>>(a, runs, n, s);
+    }
 }
 template <class T>
 cudaError_t tc_t(const RaggedArgs &a, const RaggedRun *runs, int32_t n, bool stack, cudaStream_t s) {
-    return a.hd <= 64 ? tc_d<64, T>(a, runs, n, stack, s) : tc_d<128, T>(a, runs, n, stack, s);
+    if (a.hd <= 64) return tc_d<64, T>(a, runs, n, stack, s);
+    if (a.hd <= 128) return tc_d<128, T>(a, runs, n, stack, s);
+    if (a.hd <= 192) return tc_d<192, T>(a, runs, n, stack, s);
+    return tc_d<256, T>(a, runs, n, stack, s);
 }
 
 }  // namespace
-
-cudaError_t launch_ragged_tc(const RaggedArgs &a, const RaggedRun *runs, int32_t n, bool stack, cudaStream_t s) {
-    if (n <= 0 || n > kRaggedLarge || !ragged_tc_takes(a)) return cudaErrorInvalidValue;
-    return a.type == Elem::bf16 ? tc_t<bf16>(a, runs, n, stack, s) : tc_t<f16>(a, runs, n, stack, s);
-}
 
 }  // namespace pkv

@@ -51,6 +51,16 @@ def test_prefix_heads_and_widths(H, KV, hd, dtype):
     Case([3, 1, 70, 1, 1], [30, 17, 71, 200, 1], H, KV, hd, dtype, prefix=333, gap=3, seed=hd).check()
 
 
+@pytest.mark.parametrize("hd", [136, 160, 192, 200, 256])
+@DTYPES
+def test_wide_heads_on_tiles(hd, dtype):
+    """One chain a piece; lengths around its tiles, split keys, and more keys than one sum takes."""
+    Case([1, 129, 64, 65, 300], [700, 128, 129, 1, 255], 4, 2, hd, dtype, seed=hd).check()
+    Case([130, 1], [6000, 16], 2, 1, hd, dtype, seed=hd).check()
+    Case([100], [17_000], 1, 1, hd, dtype, seed=hd).check()
+    Case([90, 1, 40], [400, 30, 40], 3, 1, hd, dtype, prefix=1000, gap=40, seed=hd).check()
+
+
 def test_more_sequences_than_one_launch_takes():
     n = 2003
     r = torch.Generator().manual_seed(5)
@@ -249,7 +259,7 @@ SHORT = [([7, 1, 30, 2, 64, 65, 1, 1, 200, 3], 0), ([5] * 60, 0), ([1] * 130, 0)
 
 @pytest.mark.parametrize("ql,more", SHORT, ids=["mixed", "fives", "ones", "behind_own_keys", "long_and_short"])
 @pytest.mark.parametrize("prefix", [0, 100, 640, 2000])
-@pytest.mark.parametrize("H,KV,hd", [(8, 2, 128), (3, 3, 64), (7, 1, 80), (32, 2, 128)])
+@pytest.mark.parametrize("H,KV,hd", [(8, 2, 128), (3, 3, 64), (7, 1, 80), (32, 2, 128), (6, 2, 160), (2, 1, 256)])
 @DTYPES
 def test_short_sequences_behind_one_another(ql, more, prefix, H, KV, hd, dtype):
     c = Case(ql, [n + more for n in ql], H, KV, hd, dtype, prefix=prefix, gap=more, seed=len(ql))
@@ -257,7 +267,7 @@ def test_short_sequences_behind_one_another(ql, more, prefix, H, KV, hd, dtype):
     c.check(workspace=None)
 
 
-@pytest.mark.parametrize("hd", [128, 64])
+@pytest.mark.parametrize("hd", [128, 64, 160])
 @BAD
 @pytest.mark.parametrize("which", ["k", "v"])
 @pytest.mark.parametrize("gap", [0, 5])
