@@ -465,13 +465,19 @@ PKV_API int pkv_attn_packed(const void *Q, int64_t q_stride, const void *K, int6
  *   out[i, h] = softmax_j(scale * <Q[i, h], K[j, kv(h)]>) V[j, kv(h)]
  * over those rows, 0 where a sequence has none.  q_lens, k_lens, k_start: host
  * arrays, entries >= 0.  q_rows: the rows that Q and out have, k_rows: those of K
- * and V; a call that reaches past them is refused (PKV_ERR_ARG).  Element types, strides and head grouping as for
- * pkv_attn_packed; row counts up to 2^30.  Scores, softmax statistics and
- * outputs accumulate in f32, and the output is rounded once.  A key row that a
- * query does not see never reaches it, whatever it holds; one that it does see
- * and that holds an infinity or a NaN makes outputs infinite or NaN.  Rows of
- * out past the last sequence are left as they were; out may not overlap the
- * inputs.
+ * and V; a call that reaches past them is refused (PKV_ERR_ARG).  Element types,
+ * strides and head grouping as for pkv_attn_packed, row counts up to 2^30.
+ *
+ * Scores, softmax statistics and outputs accumulate in f32, and the output is
+ * rounded once.  Where a sequence's queries fill tensor-core tiles (24 (query,
+ * head of a kv head) pairs and more, rows and heads on 16-byte boundaries, a
+ * positive scale) the probabilities are rounded to dtype before they meet V, as
+ * in pkv_attn_packed; otherwise they keep at least 16 bits.  A call gives the same
+ * bits every time; the same sequence in another batch may be split elsewhere and
+ * differ within these roundings.  A key row that a query does not see never
+ * reaches it, whatever it holds; one that it does see and that holds an infinity
+ * or a NaN makes outputs infinite or NaN.  Rows of out past the last sequence are
+ * left as they were; out may not overlap the inputs.
  *
  * workspace: device memory for partial results, 16-byte aligned, for work split
  * over the keys where there are few queries.  pkv_attn_cross_workspace says how
@@ -480,9 +486,11 @@ PKV_API int pkv_attn_packed(const void *Q, int64_t q_stride, const void *K, int6
  * not be kept or cleared between calls; calls that may run at the same time
  * (other streams, captured graphs) need one each.  Nothing is uploaded or
  * allocated; the call can be captured into a CUDA graph (the lengths are then
- * part of the graph).  Runs on `stream` and the current device.  Checks, in order: lengths and
- * sizes -> PKV_ERR_BAD_DIM, grouping -> PKV_ERR_BAD_GQA, dtype, strides,
- * workspace, pointers -> PKV_ERR_ARG. */
+ * part of the graph), provided that an earlier call outside a capture set up the
+ * device's error word.  Runs on `stream` and the current device.  Checks, in
+ * order: lengths and sizes -> PKV_ERR_BAD_DIM, grouping -> PKV_ERR_BAD_GQA, dtype,
+ * strides, workspace, rows, pointers -> PKV_ERR_ARG.  Failures found on the
+ * device: pkv_contiguous_sync_error. */
 PKV_API int pkv_attn_cross(const void *Q, int64_t q_stride, int64_t q_rows, const int32_t *q_lens, const void *K,
                            int64_t k_stride, const void *V, int64_t v_stride, int64_t k_rows, const int32_t *k_lens,
                            const int32_t *k_start, int32_t dtype, int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,

@@ -298,7 +298,8 @@ Plan make_plan(std::vector<Seq> seqs, const Shape &sh, int32_t n_pre, const Kern
                             ? &p.rows[rows_at++]
                             : &p.tiles_pre[tiles_at++];
             records(r);
-            p.joins.push_back(JoinRun{r.q0, r.nq, r.rec0, r.ns, stack->rec0 + (r.q0 - stack->q0) * stack->ns, stack->ns});
+            const int64_t pre0 = stack->rec0 + static_cast<int64_t>(r.q0 - stack->q0) * stack->ns;
+            p.joins.push_back(JoinRun{r.q0, r.nq, r.rec0, r.ns, static_cast<int32_t>(std::min<int64_t>(pre0, 0x7fffffff)), stack->ns});
         }
         for (RaggedRun &r : p.tiles) {
             r.rec0 = -1;

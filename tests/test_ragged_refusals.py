@@ -106,3 +106,58 @@ def test_the_binding_refuses_host_tensors():
         pkv.pkv_attn_cross(x, [4], x, x, [4, 1], 4, 4, 16, 0.25, x)
     with pytest.raises(TypeError, match="entry for each"):
         pkv.pkv_attn_cross_workspace([4], [4], 4, 4, 16, k_start=[0, 1])
+
+
+def test_the_binding_wants_the_current_device_and_one_type(monkeypatch):
+    from test_q8_refusals import Rows
+
+    class Space:
+        nbytes = 64
+
+        def __init__(self, device):
+            self.device = device
+
+        def is_contiguous(self):
+            return True
+
+        def get_device(self):
+            return self.device
+
+        def data_ptr(self):
+            return 4096
+
+    done = staticmethod(lambda *a: 0)
+    monkeypatch.setattr(pkv, "_current_device", lambda: 0)
+    monkeypatch.setattr(pkv, "_lib", type("Lib", (), {n: done for n in ("pkv_attn_cross", "pkv_attn_prefix", "pkv_rope_packed")}))
+
+    def one(which, i, **kw):
+        r = [Rows(9, w) for w in ((64, 32, 32, 64) if which == "cross" else (64, 32, 32, 32, 32, 64))]
+        if i is not None:
+            r[i] = Rows(9, kw.get("w", r[i].shape[1]), kw.get("device", 0), dtype=kw.get("dtype", torch.bfloat16))
+        space = Space(kw.get("space", 0))
+        if which == "cross":
+            return pkv.pkv_attn_cross(r[0], [9], r[1], r[2], [9], 4, 2, 16, 0.25, r[3], workspace=space)
+        return pkv.pkv_attn_prefix(r[0], [9], r[1], r[2], r[3], r[4], [9], 4, 2, 16, 0.25, r[5], workspace=space)
+
+    for which, n in (("cross", 4), ("prefix", 6)):
+        assert one(which, None) == 0
+        with pytest.raises(TypeError, match="workspace"):
+            one(which, None, space=1)
+        for i in range(n):
+            with pytest.raises(TypeError, match="device"):
+                one(which, i, device=1)
+            with pytest.raises(TypeError, match="type"):
+                one(which, i, dtype=torch.float16)
+            with pytest.raises(TypeError, match="wide"):
+                one(which, i, w=48)
+
+    def turn(q=Rows(9, 64), k=Rows(9, 32), qo=Rows(9, 64), ko=Rows(9, 32), pos=None, pairs=(3, 3, 2)):
+        return pkv.pkv_rope_packed(q, k, pos or Rows(3, 9, dtype=torch.int32), list(pairs), 0, 4, 2, 16, 1e4, qo, ko)
+
+    assert turn() == 0 and turn(q=None, qo=None) == 0 and turn(k=None, ko=None) == 0
+    for kw in (dict(q=None), dict(qo=None), dict(k=None), dict(ko=None), dict(q=None, qo=None, k=None, ko=None),
+               dict(q=Rows(8, 64)), dict(ko=Rows(8, 32)), dict(q=Rows(9, 60)), dict(q=Rows(9, 64, 1)),
+               dict(ko=Rows(9, 32, dtype=torch.float32)), dict(pos=Rows(3, 9, dtype=torch.int64)), dict(pos=Rows(2, 9, dtype=torch.int32)),
+               dict(pos=Rows(3, 9, 1, dtype=torch.int32)), dict(pos=Rows(3, 10, dtype=torch.int32))):
+        with pytest.raises(TypeError):
+            turn(**kw)
