@@ -165,7 +165,7 @@ __device__ __forceinline__ int work_of(uint32_t answer) {
 // Whole prompts: every sequence's queries attend its own keys.
 template <int N>
 struct WholePrompts {
-    static constexpr bool kRuns = false, kStacks = false;
+    static constexpr bool kRuns = false, kStacks = false, kAlt = false;
     // Tokens of a tile, token and head of its row m; `tile` is log2 of its heads.
     __device__ __forceinline__ static int tokens(int tile) { return 128 >> tile; }
     __device__ __forceinline__ static int token(int m, int tile) { return m >> tile; }
@@ -209,9 +209,13 @@ struct WholePrompts {
 // Runs of queries over keys of their own, behind a shared prefix or not, the
 // key tiles (the prefix's, then the run's) split or not.  A piece has at least one key tile a
 // chain, seen or not, so that every row's record is written.
-template <int N, int kChains>
+//
+// With kTurns a piece of one query tile takes its key tiles on both chains in
+// turn, the even ones on chain 0, and the chains' parts are joined at the end: one chain
+// by itself waits for its own softmax.
+template <int N, int kChains, bool kTurns>
 struct Runs {
-    static constexpr bool kRuns = true, kStacks = false;
+    static constexpr bool kRuns = true, kStacks = false, kAlt = kTurns;
     // `tile` is the number of its heads; rows past the last whole token are not used.
     __device__ __forceinline__ static int tokens(int tile) { return 128 / tile; }
     __device__ __forceinline__ static int token(int m, int tile) { return m / tile; }
@@ -224,8 +228,15 @@ struct Runs {
         int len, row0, q0, h0, kvh;  // queries of the run, its first row, first query of chain 0's tile, heads
         int n0, n1, look0;           // counted from tile j0 on
         int j0, k0, nk, off;         // first tile of the split; key rows
-        int rec, ns, pad0, pad1;     // record of query 0 (-1: none), records a query
-        __device__ __forceinline__ int n_max() const { return max(n0, n1); }
+        int rec, ns, alt, pad;       // record of query 0 (-1: none), records a query; the chains take key tiles in turn
+        __device__ __forceinline__ int n_max() const { return alt ? n0 + n1 : max(n0, n1); }
+        __device__ __forceinline__ void turns() {
+            alt = kTurns && n1 == 0 && n0 > 1;
+            if (alt) {
+                n1 = n0 / 2;
+                n0 -= n1;
+            }
+        }
         __device__ __forceinline__ int looks() const { return max(0, n_max() - look0); }
     };
     __device__ __forceinline__ static Piece piece(const Args &a, const List &l, int tile, int w) {
@@ -250,7 +261,7 @@ struct Runs {
         p.off = r.off;
         p.rec = r.rec0 < 0 ? -1 : r.rec0 + split;
         p.ns = r.ns;
-        p.pad0 = p.pad1 = 0;
+        p.pad = 0;
         const int pre = (a.n_pre + kKeys - 1) / kKeys, all = pre + (r.nk + kKeys - 1) / kKeys, per = (all + r.ns - 1) / r.ns;
         p.j0 = split * per;
         auto tiles = [&](int q) {  // up to the last key that query q sees
@@ -259,6 +270,7 @@ struct Runs {
         p.n0 = max(1, tiles(min(p.q0 + TQ, r.nq) - 1));
         p.n1 = kChains == 1 || p.q0 + TQ >= r.nq ? 0 : max(1, tiles(min(p.q0 + 2 * TQ, r.nq) - 1));
         p.look0 = max(0, pre + min(r.nk, r.off + p.q0 + 1) / kKeys - p.j0);
+        p.turns();
         return p;
     }
     __device__ __forceinline__ static bool is_long(const Piece &p) { return p.n_max() * kKeys > kLongKeys; }
@@ -271,12 +283,12 @@ struct Runs {
 // shared prefix, own key rows in the same order: a tile may hold rows of several
 // sequences, and its own keys are those of all of them, of which a row
 // sees a stretch.  A list holds one such stretch.
-template <int N, int kChains>
-struct Stacks : Runs<N, kChains> {
+template <int N, int kChains, bool kTurns>
+struct Stacks : Runs<N, kChains, kTurns> {
     static constexpr bool kStacks = true;
-    using typename Runs<N, kChains>::Args;
-    using typename Runs<N, kChains>::List;
-    using typename Runs<N, kChains>::Piece;
+    using typename Runs<N, kChains, kTurns>::Args;
+    using typename Runs<N, kChains, kTurns>::List;
+    using typename Runs<N, kChains, kTurns>::Piece;
     // The sequence of row t of the stretch.
     __device__ __forceinline__ static int seq(const List &l, int t) {
         const int q = l.run[0].q0 + t;
@@ -304,7 +316,7 @@ struct Stacks : Runs<N, kChains> {
         p.h0 = ht * tile;
         p.kvh = p.h0 / (a.n_heads / a.n_kv);
         p.rec = l.run[0].rec0 < 0 ? -1 : l.run[0].rec0 + split;
-        p.off = p.pad0 = p.pad1 = 0;
+        p.off = p.pad = 0;
         const int last0 = min(p.q0 + TQ, p.len) - 1, last = min(p.q0 + kChains * TQ, p.len) - 1;
         p.k0 = l.run[seq(l, p.q0)].k0;
         p.nk = end(l.run[seq(l, last)], l, last) - p.k0;
@@ -314,6 +326,7 @@ struct Stacks : Runs<N, kChains> {
         p.n0 = max(1, min(pre + (mid + kKeys - 1) / kKeys - p.j0, per));
         p.n1 = last == last0 ? 0 : max(1, min(all - p.j0, per));
         p.look0 = max(0, pre - p.j0);
+        p.turns();
         return p;
     }
     __device__ __forceinline__ static int key0(const Args &, const Piece &, int) { return 0; }
@@ -330,6 +343,7 @@ struct Stacks : Runs<N, kChains> {
 //   go[x], look[x]           V of a partly seen tile loaded / looked over
 //   answer                   the number of a further piece
 //   work[x] / wfree[x]       piece handed out / read by the other ten warps
+//   part[x]                  chain 1's part of a piece taken in turn written (four warps)
 // mkp, mvp: of the shared prefix (Runs).
 template <int D, class T, bool kLong, class F>
 __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
@@ -348,12 +362,20 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
     __shared__ __align__(16) uint4 answer;
     __shared__ int4 pieces_s[2][Piece::kWords];  // decoded by the loading warp for the others
     __shared__ uint32_t tslot, dirty[4], held[2];  // held[c]: O_c already holds something before PV(0)
+    // Chain 1's maxima and sums of a piece taken in turn; two, as it may end the next
+    // such piece before chain 0 has read them (not the one after: its product waits for O_1).
+    __shared__ uint64_t bar_part[2];
+    __shared__ float2 part_s[2][F::kAlt ? 128 : 1];
 
     // (values that the compiler knows to be the same in a warp stay in uniform
     // registers, where the MMA instructions want their operands)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     auto wait_w = [&](uint64_t *bar, uint32_t parity) {  // bounded; the warp agrees on the outcome
         return __all_sync(0xffffffffu, wait_phase(smem_u32(bar), parity & 1u)) != 0;
+    };
+    auto in_turn = [](const Piece &p) {
+        if constexpr (F::kAlt) return p.alt != 0;
+        else return false;
     };
     auto slot = [](uint32_t i) { return static_cast<int>(i % NS); };
     auto rph = [](uint32_t i) { return i / NS; };
@@ -385,6 +407,7 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
             held[c] = 0;
         }
         mbar_init(smem_u32(&bar_answer), 1);
+        for (int x = 0; x < 2; ++x) mbar_init(smem_u32(&bar_part[x]), 4);
         for (int x = 0; x < 4; ++x) {
             mbar_init(smem_u32(&bar_go[x]), 1);
             mbar_init(smem_u32(&bar_look[x]), 4);
@@ -412,7 +435,7 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
         auto same = [](int y) { return __shfl_sync(0xffffffffu, y, 0); };
         if constexpr (F::kRuns)
             p = Piece{same(u[0].x), same(u[0].y), same(u[0].z), same(u[0].w), same(u[1].x), same(u[1].y), same(u[1].z), same(u[1].w),
-                      same(u[2].x), same(u[2].y), same(u[2].z), same(u[2].w), same(u[3].x), same(u[3].y), 0, 0};
+                      same(u[2].x), same(u[2].y), same(u[2].z), same(u[2].w), same(u[3].x), same(u[3].y), F::kAlt ? same(u[3].z) : 0, 0};
         else
             p = Piece{same(u[0].x), same(u[0].y), same(u[0].z), same(u[0].w), same(u[1].x), same(u[1].y), same(u[1].z), same(u[1].w)};
         return p.len > 0;
@@ -444,7 +467,7 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
                         pieces_s[x][1] = make_int4(p.kvh, p.n0, p.n1, p.look0);
                         if constexpr (F::kRuns) {
                             pieces_s[x][2] = make_int4(p.j0, p.k0, p.nk, p.off);
-                            pieces_s[x][3] = make_int4(p.rec, p.ns, 0, 0);
+                            pieces_s[x][3] = make_int4(p.rec, p.ns, p.alt, 0);
                         }
                         mbar_arrive(smem_u32(&bar_work[x]));
                     }
@@ -483,7 +506,7 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
 #pragma unroll
                                 for (int x = 0; x < D / 64; ++x)
                                     tma_load3(smem_u32(sm + c * C::kTile + x * C::kBlock), &mq, 64 * x, p.h0,
-                                              p.row0 + p.q0 + c * F::tokens(tile), smem_u32(&bar_q[c]));
+                                              p.row0 + p.q0 + (in_turn(p) ? 0 : c * F::tokens(tile)), smem_u32(&bar_q[c]));
                             }
                             ++qn[c];
                             __syncwarp();
@@ -539,20 +562,37 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
             Piece p;
             while (next_piece(p)) {
                 const int n = c ? p.n1 : p.n0, n_max = p.n_max();
+                const bool alt = in_turn(p);
+                // Items of the other chain's tiles, as far as `end`: free as far as this
+                // chain goes.  (All items are waited for in order: a wait for a later use of
+                // a slot would take the phase before an unfinished one for its own.)
+                uint32_t seen = it;
+                auto pass_over = [&](uint32_t end) {
+                    for (; seen < end && ok; ++seen) {
+                        if (((seen - it) >> 1 & 1) == static_cast<uint32_t>(c)) continue;
+                        ok = wait_w(&bar_full[slot(seen)], rph(seen));
+                        if (ok && elect_lane()) mbar_arrive(smem_u32(&bar_free[slot(seen)]));
+                    }
+                };
+                auto tile_of = [&](int j) { return alt ? 2 * j + c : j; };  // of the piece
                 if (n > 0) {
-                    ok = wait_w(&bar_q[c], pieces) && wait_w(&bar_full[slot(it)], rph(it));
+                    const uint32_t ik = it + 2 * tile_of(0);
+                    if (alt) pass_over(ik);
+                    ok = ok && wait_w(&bar_q[c], pieces) && wait_w(&bar_full[slot(ik)], rph(ik));
                     if (!ok) break;
                     fence_after_sync();
-                    qk(it, false, n == 1);
+                    qk(ik, false, n == 1);
                 }
                 for (int j = 0; j < n && ok; ++j, ++tiles) {
-                    const uint32_t iv = it + 2 * j + 1;
+                    const int jt = tile_of(j);
+                    const uint32_t iv = it + 2 * jt + 1, ik = it + 2 * tile_of(j + 1);
                     const int sv = slot(iv);
                     ok = wait_w(&bar_full[sv], rph(iv));
-                    if (ok && j + 1 < n) ok = wait_w(&bar_full[slot(iv + 1)], rph(iv + 1));
+                    if (alt) pass_over(min(ik, it + 2 * n_max));
+                    if (ok && j + 1 < n) ok = wait_w(&bar_full[slot(ik)], rph(ik));
                     if (ok && j == 0 && pieces > 0) ok = wait_w(&bar_ofree[c], pieces - 1);
-                    if (ok && j >= p.look0) {
-                        const uint32_t x = lk + j - p.look0;
+                    if (ok && jt >= p.look0) {
+                        const uint32_t x = lk + jt - p.look0;
                         ok = wait_w(&bar_look[x & 3], x >> 2);
                     }
                     // P, and this chain's turn: the other chain's products before these
@@ -582,20 +622,21 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
                     // the other chain's products follow (chain 1's last are followed
                     // by chain 0's first of the next piece)
                     const bool pass = c ? j + 1 < p.n0 || j + 1 == n : j < p.n1;
-                    if (j + 1 < n) qk(iv + 1, pass, j + 2 == n);
+                    if (j + 1 < n) qk(ik, pass, j + 2 == n);
                     else if (pass && elect_lane()) mbar_arrive(smem_u32(&bar_p[c ^ 1]));
                     __syncwarp();
                 }
                 // items past the chain's last tile are free as far as this chain goes
                 // (counted once they have landed, so that each counts for its own phase)
-                for (uint32_t i = it + 2 * n; i < it + 2 * n_max && ok; ++i) {
+                if (alt) pass_over(it + 2 * n_max);
+                for (uint32_t i = it + 2 * n; i < it + 2 * n_max && ok && !alt; ++i) {
                     ok = wait_w(&bar_full[slot(i)], rph(i));
                     if (ok && elect_lane()) mbar_arrive(smem_u32(&bar_free[slot(i)]));
                 }
                 it += 2 * n_max;
                 lk += p.looks();
                 if (n > 0) ++pieces;
-                owed = p.n1 > 0;
+                owed = p.n1 > 0 && p.n0 <= p.n1;
             }
             if (!ok && lane == 0 && a.err) atomicOr(a.err, 2);
         }
@@ -606,11 +647,12 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t tS = tbase + lanes + 256 + 128 * c, tO = tbase + lanes + 128 * c;
         const float cs = a.scale_log2;  // > 0
-        uint32_t it = 0, lk = 0, tiles = 0, pieces = 0;
+        uint32_t it = 0, lk = 0, tiles = 0, pieces = 0, pieces1 = 0, parts = 0;  // pieces of chain 1, taken in turn
         Piece p;
         while (next_piece(p)) {
             const int n = c ? p.n1 : p.n0;
-            const int tok = p.q0 + c * TQ + F::token(m, tile);
+            const bool alt = in_turn(p);
+            const int tok = p.q0 + (alt ? 0 : c * TQ) + F::token(m, tile);
             const bool valid = tok < p.len && m < F::rows(tile);
             int lim, from = 0;  // keys this row sees (Runs: of the run's own)
             if constexpr (F::kStacks) {
@@ -648,16 +690,17 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
                     }
                 }
                 for (int j = j0; j < min(n, j0 + step); ++j, ++tiles) {
-                    const uint32_t look = lk + j - p.look0;
-                    if (j >= p.look0 && (c == 1 || j >= p.n1)) {
+                    const int jt = alt ? 2 * j + c : j;  // of the piece
+                    const uint32_t look = lk + jt - p.look0;
+                    if (jt >= p.look0 && (c == 1 || alt || j >= p.n1)) {
                         // this chain looks over V_j: keys up to key0 are seen by every row; a
                         // key's 128 bytes of each 64 columns are 8 chunks.  (The loading warp
                         // tells when the slot is at V_j: these warps follow no earlier item.)
-                        const uint32_t i = it + 2 * j + 1;
+                        const uint32_t i = it + 2 * jt + 1;
                         ok = wait_w(&bar_go[look & 3], look >> 2) && wait_w(&bar_full[slot(i)], rph(i));
                         if (!ok) break;
                         uint4 *v = reinterpret_cast<uint4 *>(ring + slot(i) * C::kTile);
-                        const int key0 = F::key0(a, p, j);
+                        const int key0 = F::key0(a, p, jt);
                         constexpr uint32_t kE = std::is_same<T, bf16>::value ? 0x7f807f80u : 0x7c007c00u;
                         constexpr uint32_t kOne = std::is_same<T, bf16>::value ? 0x00800080u : 0x04000400u;
                         uint32_t seen = 0;  // a half's exponent is all ones where adding one to it reaches the sign bit
@@ -696,9 +739,9 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
                     for (int i = 0; i < kKeys; i += 32) tmem_ld32_issue(tS + i, x + i);
                     tmem_ld_done(x);
                     auto xf = [&](int i) { return __uint_as_float(x[i]); };
-                    int base = j * kKeys, end = lim;  // the tile's first key, and the first that this row does not see
+                    int base = jt * kKeys, end = lim;  // the tile's first key, and the first that this row does not see
                     if constexpr (F::kRuns) {
-                        const int t = p.j0 + j, pre = (a.n_pre + kKeys - 1) / kKeys;
+                        const int t = p.j0 + jt, pre = (a.n_pre + kKeys - 1) / kKeys;
                         base = (t < pre ? t : t - pre) * kKeys;
                         end = t < pre ? a.n_pre : lim;
                         if constexpr (F::kStacks) {
@@ -753,7 +796,7 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
                     const float2 s2 = unpair(add2(sum[0], sum[1]));
                     l_run = fmaf(l_run, f, s2.x + s2.y);
                     tmem_st_wait();
-                    if (j >= p.look0) {
+                    if (jt >= p.look0) {
                         ok = wait_w(&bar_look[look & 3], look >> 2);
                         if (!ok) break;
                         if (*static_cast<volatile uint32_t *>(&dirty[look & 3]) == look + 1) {
@@ -805,10 +848,37 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
                     if (lane == 0) mbar_arrive(smem_u32(&bar_p[c]));
                 }
             }
-            if (n > 0 && ok) {
+            if (F::kAlt && alt && c == 1) {
+                if (!ok) break;
+                part_s[parts & 1][F::kAlt ? m : 0] = make_float2(m_ref, l_run);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar_part[parts & 1]));
+            } else if (n > 0 && ok) {
                 ok = wait_w(&bar_o[c], pieces);
+                // (chain 1's part first: with it the piece before is surely behind its O_1)
+                if (F::kAlt && alt) ok = ok && wait_w(&bar_part[parts & 1], parts >> 1) && wait_w(&bar_o[1], pieces1);
                 if (!ok) break;
                 fence_after_sync();
+                if (F::kAlt && alt) {  // chain 1's part of these rows (of the same lanes) into chain 0's
+                    const float2 other = part_s[parts & 1][F::kAlt ? m : 0];
+                    const float top = fmaxf(m_ref, other.x), ref = top == -INFINITY ? 0.f : top;
+                    const float f0 = ex2(m_ref - ref), f1 = ex2(other.x - ref);
+                    m_ref = top;
+                    l_run = l_run * f0 + other.y * f1;
+#pragma unroll 1
+                    for (int i = 0; i < D; i += 16) {
+                        float x0[16], x1[16];
+                        tmem_ld16(tO + i, x0);
+                        tmem_ld16(tO + 128 + i, x1);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) x0[k] = fmaf(x1[k], f1, x0[k] * f0);
+                        tmem_st16(tO + i, x0);
+                    }
+                    tmem_st_wait();
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bar_ofree[1]));
+                }
                 constexpr int kPart = D > 128 ? 64 : D;  // columns at a time
 #pragma unroll 1
                 for (int i0 = 0; i0 < D; i0 += kPart) {
@@ -867,8 +937,10 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
                                 *reinterpret_cast<uint4 *>(dst + i) = make_uint4(two(i), two(i + 2), two(i + 4), two(i + 6));
                     }
                 }
-                ++pieces;
             }
+            if (n > 0) ++pieces;
+            if (p.n1 > 0) ++pieces1;
+            if (alt) ++parts;
             it += 2 * p.n_max();
             lk += p.looks();
         }

@@ -539,10 +539,10 @@ __global__ void __launch_bounds__(128, 8)
     __shared__ __align__(16) float part[4][128 * J];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t H = a.n_heads;
-    const int64_t item = together ? blockIdx.x : 4 * static_cast<int64_t>(blockIdx.x) + warp;
+    const uint32_t item = together ? blockIdx.x : 4 * blockIdx.x + warp;  // (rows times heads stay below 2^31)
     const int first = together ? warp : 0, step = together ? 4 : 1;  // of this warp's records
-    if (item >= l.unit0[l.n] * H) return;  // (whole blocks, where warps meet below)
-    const int h = static_cast<int>(item % H), t = static_cast<int>(item / H);
+    const int t = static_cast<int>(item / static_cast<uint32_t>(a.n_heads)), h = static_cast<int>(item % static_cast<uint32_t>(a.n_heads));
+    if (t >= l.unit0[l.n]) return;  // (whole blocks, where warps meet below)
     const int ri = run_of(l, t), qi = t - l.unit0[ri];
     const JoinRun run = l.run[ri];
     const int64_t own = (run.rec0 + static_cast<int64_t>(qi) * run.ns) * H + h, pre = (run.pre0 + static_cast<int64_t>(qi) * run.pns) * H + h;

@@ -92,16 +92,17 @@ cudaError_t tc_n(const RaggedArgs &a, const RaggedRun *runs, int32_t n, cudaStre
 
 template <int D, class T>
 cudaError_t tc_d(const RaggedArgs &a, const RaggedRun *runs, int32_t n, bool stack, cudaStream_t s) {
+    constexpr bool kT = D == 64;  // (128-wide heads have ring slots for two and a half tiles only)
     constexpr int kC = TcCfg<D>::kChains, kS = kRaggedSmall, kL = kRaggedLarge;
     bool is_long = false;  // some piece adds more keys than a sum takes
     for (int32_t i = 0; i < n && !stack; ++i) is_long = is_long || ragged_split_tiles(a.n_pre, runs[i]) * kKeys > kLongKeys;
     if constexpr (D > 128) {
         if (is_long) return cudaErrorInvalidValue;
-        return stack ? tc_n<D, T, kL, false, Stacks<kL, kC>>(a, runs, n, s) : tc_n<D, T, kL, false, Runs<kL, kC>>(a, runs, n, s);
+        return stack ? tc_n<D, T, kL, false, Stacks<kL, kC, kT>>(a, runs, n, s) : tc_n<D, T, kL, false, Runs<kL, kC, kT>>(a, runs, n, s);
     } else {
-        if (stack) return n <= kS ? tc_n<D, T, kS, false, Stacks<kS, kC>>(a, runs, n, s) : tc_n<D, T, kL, false, Stacks<kL, kC>>(a, runs, n, s);
-        if (is_long) return tc_n<D, T, kL, true, Runs<kL, kC>>(a, runs, n, s);
-        return n <= kS ? tc_n<D, T, kS, false, Runs<kS, kC>>(a, runs, n, s) : tc_n<D, T, kL, false, Runs<kL, kC>>(a, runs, n, s);
+        if (stack) return n <= kS ? tc_n<D, T, kS, false, Stacks<kS, kC, kT>>(a, runs, n, s) : tc_n<D, T, kL, false, Stacks<kL, kC, kT>>(a, runs, n, s);
+        if (is_long) return tc_n<D, T, kL, true, Runs<kL, kC, false>>(a, runs, n, s);  // (sums set aside stay with their chain)
+        return n <= kS ? tc_n<D, T, kS, false, Runs<kS, kC, kT>>(a, runs, n, s) : tc_n<D, T, kL, false, Runs<kL, kC, kT>>(a, runs, n, s);
     }
 }
 template <class T>

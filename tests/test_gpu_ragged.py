@@ -12,6 +12,8 @@ DTYPES = pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "f16"])
 SHAPES = [(8, 2, 128), (3, 3, 64), (7, 1, 80), (16, 1, 128), (32, 1, 64), (4, 2, 24), (4, 2, 160), (2, 2, 256), (4, 2, 20),
           (2, 1, 131), (3, 1, 1)]
 
+BAD = pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+
 CROSS = [([1], [1]), ([1, 1, 0, 1], [0, 5, 7, 33]), ([130, 1, 17], [129, 640, 64]), ([5, 33, 64, 2], [16, 128, 0, 255]),
          ([300], [700]), ([1, 1], [9000, 300]), ([40, 3], [5000, 2500])]
 
@@ -59,6 +61,37 @@ def test_wide_heads_on_tiles(hd, dtype):
     Case([130, 1], [6000, 16], 2, 1, hd, dtype, seed=hd).check()
     Case([100], [17_000], 1, 1, hd, dtype, seed=hd).check()
     Case([90, 1, 40], [400, 30, 40], 3, 1, hd, dtype, prefix=1000, gap=40, seed=hd).check()
+
+
+@pytest.mark.parametrize("H,KV,hd", [(20, 20, 64), (8, 4, 40), (6, 2, 56)])
+@DTYPES
+def test_one_tile_of_queries_takes_its_keys_on_both_chains(H, KV, hd, dtype):
+    """Pieces of one query tile and one to many key tiles, after one another and among whole ones, many to a block."""
+    ql = [24, 128, 1, 100, 300, 33, 129, 50, 64, 90, 260, 40]
+    kl = [1, 128, 700, 129, 900, 255, 256, 257, 385, 1500, 640, 513]
+    Case(ql, kl, H, KV, hd, dtype, seed=hd).check()
+    Case(ql, kl, H, KV, hd, dtype, seed=hd).check(workspace=None)
+    Case([60], [15_000], H, KV, hd, dtype, seed=hd).check()
+    Case([30, 100, 128, 70], [300, 100, 500, 70], H, KV, hd, dtype, prefix=700, gap=90, seed=hd).check()
+    Case([60] * 90, [400 + 130 * (i % 4) for i in range(90)], H, KV, hd, dtype, seed=hd).check()
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@BAD
+def test_both_chains_keep_values_out_of_sight(which, bad):
+    c = Case([100, 60, 128, 90], [130, 389, 600, 257], 3, 3, 64, BF16, gap=3, seed=1)
+    clean = c.call()
+    rows = getattr(c, which)
+    for s, n in zip(c.start, c.kl):
+        rows[s + n:s + n + 3] = bad
+    assert torch.equal(c.call(), clean)
+    p = Case([100, 60, 90], [400, 389, 257], 3, 3, 64, BF16, prefix=200, gap=90, seed=1)
+    clean = p.call()
+    getattr(p, which)[p.start[1] + 360] = bad  # seen by queries 31 .. of sequence 1
+    got = p.call()
+    torch.cuda.synchronize()
+    assert torch.equal(got[:131], clean[:131]) and torch.equal(got[160:], clean[160:])
+    assert not bool(torch.isfinite(got[131:160].float()).all(dim=1).any())
 
 
 def test_more_sequences_than_one_launch_takes():
@@ -133,7 +166,6 @@ def test_rising_scores_move_the_reference():
     c.check(scale=0.125)
 
 
-BAD = pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 
 
 @pytest.mark.parametrize("hd", [128, 64, 20, 160])
