@@ -320,9 +320,8 @@ Plan make_plan(std::vector<Seq> seqs, const Shape &sh, int32_t n_pre, const Kern
         if (at > 0 && (at > 0x7fffffff || record_bytes(at, sh) > workspace)) continue;
         // the longest pieces and splits first: the launches then end on their shortest
         std::stable_sort(p.rows.begin(), p.rows.end(), [&](const RaggedRun &x, const RaggedRun &y) { return x.nk / x.ns > y.nk / y.ns; });
-        std::stable_sort(p.tiles.begin(), p.tiles.end(), [&](const RaggedRun &x, const RaggedRun &y) {
-            return ragged_split_tiles(n_pre, x) > ragged_split_tiles(n_pre, y);
-        });
+        auto length = [&](const RaggedRun &r) { return ragged_split_tiles(n_pre, r) * (r.nq * heads > 128 ? 2 : 1); };
+        std::stable_sort(p.tiles.begin(), p.tiles.end(), [&](const RaggedRun &x, const RaggedRun &y) { return length(x) > length(y); });
         return p;
     }
 }
