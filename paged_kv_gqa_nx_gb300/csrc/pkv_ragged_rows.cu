@@ -527,14 +527,15 @@ __global__ void __launch_bounds__(32 * kRowWarps, DP <= 128 ? 4 : 2)
     if (n_ranks > 1) cluster_sync();  // the others may still read this block's part
 }
 
-// The records of a (query, head), by one warp or, where all such blocks run at
-// once, by the four of a block (`together`).  A lane takes a record's maximum and
-// sum, then the records' outputs are added, kBatch on the way at a time.  What
-// it takes is the latency of two dependent reads, so registers are few and blocks many
-// (the step of 64 behind 8,192 tokens, 17 records a row and head: 47 us with one load after another, 41 so).
-constexpr int kBatch = 4;
+// The records of a (query, head), by one warp or, where there are few of them, by
+// the four of a block (`together`).  A lane takes a record's maximum and sum, then
+// the records' outputs are added, kBatch on the way at a time: what it takes is
+// the latency of two dependent reads, and a warp's own instructions (64 queries
+// behind 8,192 keys, 14 records of each of 2,048 rows and heads: the three launches
+// take 47 us with one read after another, 39 with four at a time by four warps, 35 so).
+constexpr int kBatch = 12;
 template <class T, int N, int J>  // J: 128 dims each
-__global__ void __launch_bounds__(128, 8)
+__global__ void __launch_bounds__(128, 4)
     ragged_join_kernel(const __grid_constant__ RaggedArgs a, const __grid_constant__ RunList<JoinRun, N> l, int together) {
     __shared__ __align__(16) float part[4][128 * J];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -701,7 +702,7 @@ cudaError_t join_n(const RaggedArgs &a, const JoinRun *runs, int32_t n, cudaStre
         if (at > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     }
     l.unit0[n] = static_cast<int32_t>(at);
-    const int together = at * a.n_heads <= 14 * 152;
+    const int together = at * a.n_heads <= 2 * 152;
     const long long grid = together ? at * a.n_heads : (at * a.n_heads + 3) / 4;
     if (a.hd > 128) return start(ragged_join_kernel<T, N, 2>, grid, 1, 128, 0, true, s, a, l, together);
     return start(ragged_join_kernel<T, N, 1>, grid, 1, 128, 0, true, s, a, l, together);
