@@ -533,10 +533,10 @@ __global__ void __launch_bounds__(32 * kRowWarps, DP <= 128 ? 4 : 2)
 // the latency of two dependent reads, and a warp's own instructions (64 queries
 // behind 8,192 keys, 14 records of each of 2,048 rows and heads: the three launches
 // take 47 us with one read after another, 39 with four at a time by four warps, 35 so).
-constexpr int kBatch = 12;
 template <class T, int N, int J>  // J: 128 dims each
 __global__ void __launch_bounds__(128, 4)
     ragged_join_kernel(const __grid_constant__ RaggedArgs a, const __grid_constant__ RunList<JoinRun, N> l, int together) {
+    constexpr int kBatch = J == 1 ? 12 : 6;
     __shared__ __align__(16) float part[4][128 * J];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t H = a.n_heads;
