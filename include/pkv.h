@@ -535,7 +535,7 @@ enum pkv_rope_order {
  * with PKV_ROPE_AXIAL rope_base^(-j / pairs[axis]) for the axis's j-th pair.
  * Elements past 2 r of a head stay.  inverse != 0 turns back, by -p * f_i, which
  * is also the gradient: the rows' gradients are the outputs' turned back.
- * The angle is exact to 2^-52 of its own size at any position, its cosine and
+ * The angle is exact to 2^-50 of its own size at any position, its cosine and
  * sine and the products are f32, and each result is rounded once to the type.
  * dtype: PKV_F32, PKV_BF16 or PKV_F16 for all rows.  Strides in elements;
  * outputs are other rows, or the inputs themselves (same address and stride).  Q or K

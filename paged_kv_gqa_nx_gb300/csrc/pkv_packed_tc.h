@@ -279,19 +279,18 @@ struct Runs {
     }
 };
 
-// The queries of neighbouring sequences as one stretch of rows behind the
-// shared prefix, own key rows in the same order: a tile may hold rows of several
-// sequences, and its own keys are those of all of them, of which a row
-// sees a stretch.  A list holds one such stretch.
+// The queries of neighbouring sequences as stretches of rows behind the shared
+// prefix, own key rows in the same order: a tile may hold rows of several
+// sequences, and its own keys are those of all of them, of which a row sees some.
+// A list's runs are in the order of their queries.
 template <int N, int kChains, bool kTurns>
 struct Stacks : Runs<N, kChains, kTurns> {
     static constexpr bool kStacks = true;
     using typename Runs<N, kChains, kTurns>::Args;
     using typename Runs<N, kChains, kTurns>::List;
     using typename Runs<N, kChains, kTurns>::Piece;
-    // The sequence of row t of the stretch.
-    __device__ __forceinline__ static int seq(const List &l, int t) {
-        const int q = l.run[0].q0 + t;
+    // The sequence of query row q.
+    __device__ __forceinline__ static int seq(const List &l, int q) {
         int lo = 0, hi = l.n - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -300,30 +299,36 @@ struct Stacks : Runs<N, kChains, kTurns> {
         }
         return lo;
     }
-    // Key row behind the last one that row t sees.
-    __device__ __forceinline__ static int end(const RaggedRun &r, const List &l, int t) {
-        return r.k0 + r.off + (l.run[0].q0 + t - r.q0) + 1;
-    }
+    // Key row behind the last one that query row q, of run r, sees.
+    __device__ __forceinline__ static int end(const RaggedRun &r, int q) { return r.k0 + r.off + (q - r.q0) + 1; }
     __device__ __forceinline__ static Piece piece(const Args &a, const List &l, int tile, int w) {
         Piece p;
         const int TQ = 128 / tile, n_ht = a.n_heads / tile;
-        const int u = w / n_ht, ht = w - u * n_ht;
-        p.row0 = l.run[0].q0;
-        p.len = l.run[l.n - 1].q0 + l.run[l.n - 1].nq - p.row0;
-        p.ns = l.run[0].ns;
+        const int t = w / n_ht, ht = w - t * n_ht;
+        int x = 0, hi = a.n_stretches - 1;
+        while (x < hi) {
+            const int mid = (x + hi + 1) >> 1;
+            if (l.unit0[mid] <= t) x = mid;
+            else hi = mid - 1;
+        }
+        const int u = t - l.unit0[x];
+        const RaggedRun &f = l.run[l.run[x].kind], &e = l.run[(x + 1 < a.n_stretches ? l.run[x + 1].kind : l.n) - 1];
+        p.row0 = f.q0;
+        p.len = e.q0 + e.nq - p.row0;
+        p.ns = f.ns;
         const int pairs = (p.len + kChains * TQ - 1) / (kChains * TQ), split = u / pairs;
         p.q0 = (pairs - 1 - (u - split * pairs)) * kChains * TQ;
         p.h0 = ht * tile;
         p.kvh = p.h0 / (a.n_heads / a.n_kv);
-        p.rec = l.run[0].rec0 < 0 ? -1 : l.run[0].rec0 + split;
+        p.rec = f.rec0 < 0 ? -1 : f.rec0 + split;
         p.off = p.pad = 0;
         const int last0 = min(p.q0 + TQ, p.len) - 1, last = min(p.q0 + kChains * TQ, p.len) - 1;
-        p.k0 = l.run[seq(l, p.q0)].k0;
-        p.nk = end(l.run[seq(l, last)], l, last) - p.k0;
+        p.k0 = l.run[seq(l, p.row0 + p.q0)].k0;
+        p.nk = end(l.run[seq(l, p.row0 + last)], p.row0 + last) - p.k0;
         const int pre = (a.n_pre + kKeys - 1) / kKeys, all = pre + (p.nk + kKeys - 1) / kKeys, per = (all + p.ns - 1) / p.ns;
         p.j0 = split * per;
-        const int mid = end(l.run[seq(l, last0)], l, last0) - p.k0;
-        p.n0 = max(1, min(pre + (mid + kKeys - 1) / kKeys - p.j0, per));
+        const int keys0 = end(l.run[seq(l, p.row0 + last0)], p.row0 + last0) - p.k0;
+        p.n0 = max(1, min(pre + (keys0 + kKeys - 1) / kKeys - p.j0, per));
         p.n1 = last == last0 ? 0 : max(1, min(all - p.j0, per));
         p.look0 = max(0, pre - p.j0);
         p.turns();
@@ -656,9 +661,10 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
             const bool valid = tok < p.len && m < F::rows(tile);
             int lim, from = 0;  // keys this row sees (Runs: of the run's own)
             if constexpr (F::kStacks) {
-                const RaggedRun &r = l.run[F::seq(l, valid ? tok : p.q0)];
+                const int q = p.row0 + (valid ? tok : p.q0);
+                const RaggedRun &r = l.run[F::seq(l, q)];
                 from = r.k0 - p.k0;
-                lim = F::end(r, l, valid ? tok : p.q0) - p.k0;
+                lim = F::end(r, q) - p.k0;
             } else if constexpr (F::kRuns) lim = min(p.nk, p.off + tok + 1);
             else lim = a.causal ? min(tok + 1, p.len) : p.len;
             float m_ref = -INFINITY, l_run = 0.f, unit = 0.f;

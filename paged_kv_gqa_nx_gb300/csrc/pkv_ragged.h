@@ -56,6 +56,7 @@ struct RaggedArgs {
     float *pm, *pl, *pacc;                            // records: [rec][head], [rec][head], [rec][head][hd]
     int32_t *err;
     int32_t cluster;  // blocks of a cluster (1: none), which split a unit's keys in place of ns
+    int32_t n_stretches;  // of the tiles' list (set by the launcher); run[x].kind is the first run of stretch x
     int32_t out32;  // out's rows and heads start on 32-byte boundaries (set by the launcher)
     bool vec;       // rows on 16-byte boundaries, heads of whole 16 bytes
     bool overlap;   // the launch may start before the one in front of it on the stream has ended
@@ -84,11 +85,15 @@ inline bool ragged_tc_takes(const RaggedArgs &a) { return a.vec && a.scale_log2 
 // may add up (the tensor core rounds sums toward zero; other pieces set longer
 // ones aside).
 constexpr int32_t kRaggedSumKeys = 16384 - 2 * kRaggedKeyTile;
-// stack: the runs are sequences whose queries and own key rows follow one
-// another; their tiles are those of the whole stretch (ns and rec0 of the first count).
-cudaError_t launch_ragged_tc(const RaggedArgs &a, const RaggedRun *runs, int32_t n, bool stack, cudaStream_t s);
-cudaError_t launch_ragged_tc_bf16(const RaggedArgs &a, const RaggedRun *runs, int32_t n, bool stack, cudaStream_t s);
-cudaError_t launch_ragged_tc_f16(const RaggedArgs &a, const RaggedRun *runs, int32_t n, bool stack, cudaStream_t s);
+// With n_stretches, run[first[x]] .. are sequences whose queries and own key rows
+// follow one another; their tiles are those of the whole stretch (ns and rec0 of its first
+// run count).  Stretches in the order of their queries.
+cudaError_t launch_ragged_tc(const RaggedArgs &a, const RaggedRun *runs, int32_t n, const int32_t *first, int32_t n_stretches,
+                             cudaStream_t s);
+cudaError_t launch_ragged_tc_bf16(const RaggedArgs &a, const RaggedRun *runs, int32_t n, const int32_t *first, int32_t n_stretches,
+                                  cudaStream_t s);
+cudaError_t launch_ragged_tc_f16(const RaggedArgs &a, const RaggedRun *runs, int32_t n, const int32_t *first, int32_t n_stretches,
+                                 cudaStream_t s);
 
 // Few query rows by warp-level MMAs (pkv_ragged_rows.cu): units of 8 * wide
 // rows ((query, head of the group) pairs) of one kv head; wide 1, 2 or, for heads up to 128, 4

@@ -58,7 +58,8 @@ struct Seq {
 struct Plan {
     std::vector<RaggedRun> tiles_pre;    // the prefix, for the stacked rows of sequences with few
     std::vector<RaggedRun> tiles, rows;  // own keys (behind the prefix, unless stacked); rows: of the prefix too
-    std::vector<std::vector<RaggedRun>> stretches;  // sequences that share tiles, behind the prefix
+    std::vector<RaggedRun> shared;       // sequences that share tiles, behind the prefix, in stretches
+    std::vector<int32_t> first;          // of the stretches
     std::vector<JoinRun> joins;
     int64_t n_rec = 0;
     bool stacked = false;
@@ -153,27 +154,31 @@ int pick_cluster(const std::vector<RaggedRun> &runs, const Shape &sh, const Kern
     return most <= kClusterKeys * n ? n : 1;
 }
 
-// Splits of the tensor-core kernel, which runs a block a SM.  Where there are
-// fewer pieces than two rounds of blocks, key tiles are split so that the rounds are full;
-// a piece of one tile would be mostly its first scores and its output.  Records
-// and the join cost as much as eight tiles (64 queries over 1,024 keys: 17 us in one piece
-// each, 21 split), unless they are joined with others anyway.
+// Splits of the tensor-core kernel, which runs a block a SM: the least key tiles a
+// split with which there is one round of blocks, where that is sooner done by
+// the times measured, in hundredths of a us: a piece takes 4 and 1.3 a key
+// tile, 3 more with records to write, the join of n rows and heads 3 and 1 a thousand (64 queries
+// over 1,024 keys, 8 tiles: 17 us in one piece a kv head, 21 split; over 2,048:
+// 28 and 20).  `joined`: the records are joined with others anyway, and other rows
+// are attended at the same time, which a quarter of the SMs is left to.
 void split_tiles(std::vector<RaggedRun> &runs, const Shape &sh, int32_t n_pre, int64_t coarse, bool joined = false) {
     const int heads = ragged_tile_heads(sh.group());  // of a tile
-    int64_t pieces = 0, most = 0;
+    int64_t pieces = 0, most = 0, rows = 0;
     auto blocks = [&](const RaggedRun &r) { return static_cast<int64_t>(ragged_pieces(r.nq, ragged_piece_tokens(heads, sh.hd))) * (sh.n_heads / heads); };
-    for (const RaggedRun &r : runs) {
+    for (RaggedRun &r : runs) {
+        r.ns = 1;
         pieces += blocks(r);
         most = std::max<int64_t>(most, ragged_key_tiles(n_pre, r.nk));
+        rows += static_cast<int64_t>(r.nq) * sh.n_heads;
     }
-    if (pieces > 2 * kSMs || (most <= 8 && !joined)) return;
-    // (with other rows to attend at the same time, three quarters of the SMs)
-    const int64_t room = joined ? kSMs * 3 / 4 : pieces <= kSMs ? kSMs : 2 * kSMs;
-    const int64_t per = coarse * least_split(2, std::max<int64_t>(2, most), room, [&](int64_t x) {
+    const int64_t room = joined ? kSMs * 3 / 4 : kSMs;
+    if (pieces > room || most < 4) return;
+    const int64_t per = coarse * least_split(2, most, room, [&](int64_t x) {
         int64_t n = 0;
         for (const RaggedRun &r : runs) n += blocks(r) * ((ragged_key_tiles(n_pre, r.nk) + x - 1) / x);
         return n;
     });
+    if (!joined && 400 + 130 * most <= 700 + 130 * per + 300 + rows / 10) return;
     for (RaggedRun &r : runs) r.ns = static_cast<int32_t>((ragged_key_tiles(n_pre, r.nk) + per - 1) / per);
 }
 
@@ -185,7 +190,10 @@ constexpr int64_t kTileRows = 24;
 // Stretches of neighbouring sequences that share tiles.  A tile's rows
 // multiply the own keys of all its sequences, so a sequence takes part where that is
 // no more than two tiles of keys, or half of the prefix, on top: a few tokens behind a long history of
-// their own do not.  More than four stretches (launches) and the rest go by themselves.
+// their own do not, nor do sequences in slots far apart.  (64-wide heads have less to
+// gain, as a tile by itself takes both chains: 121 sequences of 84 to 110 queries in slots of 400
+// rows behind 1,493, 20 heads of 64: 222 us by themselves, 239 together; 39 of 25 to 209 in
+// slots of 216, 12 heads of 80: 91 and 79.)
 std::vector<std::vector<Seq>> find_stretches(std::vector<Seq> &seqs, const Shape &sh, int32_t n_pre) {
     const int heads = ragged_tile_heads(sh.group());  // of a tile
     const int64_t pair = ragged_piece_tokens(heads, sh.hd), most = std::max<int64_t>(2, ragged_key_tiles(n_pre, 0) / 2);
@@ -193,7 +201,7 @@ std::vector<std::vector<Seq>> find_stretches(std::vector<Seq> &seqs, const Shape
     std::vector<Seq> alone, run;
     int64_t rows = 0;
     auto close = [&] {
-        const bool take = run.size() > 1 && found.size() < 4 && rows * heads >= kTileRows;
+        const bool take = run.size() > 1 && rows * heads >= kTileRows;
         if (take) found.push_back(run);
         else alone.insert(alone.end(), run.begin(), run.end());
         run.clear();
@@ -201,8 +209,9 @@ std::vector<std::vector<Seq>> find_stretches(std::vector<Seq> &seqs, const Shape
     };
     for (const Seq &s : seqs) {
         const bool fits = s.off != kSees && s.off * pair <= 128 * most * s.nq && n_pre + s.nk <= kRaggedSumKeys;
-        const bool follows = !run.empty() && s.q0 == run.back().q0 + run.back().nq && s.k0 >= run.back().k0 + run.back().nk &&
-                             s.k0 - (run.back().k0 + run.back().nk) <= 32;
+        const int64_t gap = run.empty() ? 0 : int64_t{s.k0} - run.back().k0 - run.back().nk;  // key rows between that nobody sees
+        const bool follows = !run.empty() && s.q0 == run.back().q0 + run.back().nq && gap >= 0 && (s.off + gap) * pair <= 128 * most * s.nq &&
+                             (sh.hd > 64 || gap <= 32);
         if (!fits || (!run.empty() && !follows)) close();
         if (!fits) {
             alone.push_back(s);
@@ -228,9 +237,16 @@ Plan make_plan(std::vector<Seq> seqs, const Shape &sh, int32_t n_pre, const Kern
     Plan p;
     if (kernels.tc)
         for (const std::vector<Seq> &part : find_stretches(seqs, sh, n_pre)) {
-            p.stretches.emplace_back();
-            for (const Seq &s : part) p.stretches.back().push_back(RaggedRun{s.q0, s.nq, s.k0, s.nk, s.off, 1, -1, kOwnKeys});
+            p.first.push_back(static_cast<int32_t>(p.shared.size()));
+            for (const Seq &s : part) p.shared.push_back(RaggedRun{s.q0, s.nq, s.k0, s.nk, s.off, 1, -1, kOwnKeys});
         }
+    // a stretch as one run, with the own keys of an average piece
+    std::vector<RaggedRun> whole;
+    for (size_t x = 0; x < p.first.size(); ++x) {
+        const RaggedRun &f = p.shared[p.first[x]], &e = p.shared[(x + 1 < p.first.size() ? p.first[x + 1] : p.shared.size()) - 1];
+        const int32_t nq = e.q0 + e.nq - f.q0, pieces = ragged_pieces(nq, ragged_piece_tokens(heads, sh.hd));
+        whole.push_back(RaggedRun{f.q0, nq, f.k0, std::max(std::max(f.nk, e.nk), (e.k0 + e.nk - f.k0 + pieces - 1) / pieces), 0, 1, -1, kOwnKeys});
+    }
     for (const Seq &s : seqs)
         (takes_tiles(s.nq, n_pre + s.nk) ? p.tiles : own).push_back(RaggedRun{s.q0, s.nq, s.k0, s.nk, s.off, 1, -1, kOwnKeys});
     for (int64_t coarse = workspace < record_bytes(1, sh) ? 2 * kCoarsest : 1;; coarse *= 2) {
@@ -257,16 +273,9 @@ Plan make_plan(std::vector<Seq> seqs, const Shape &sh, int32_t n_pre, const Kern
         p.wide = pick_wide(p.rows, sh, kernels);
         if (last) {
             for (RaggedRun &r : p.tiles) r.ns = 1;
-            for (std::vector<RaggedRun> &part : p.stretches) part[0].ns = 1;
+            for (RaggedRun &r : whole) r.ns = 1;
         } else {
-            for (std::vector<RaggedRun> &part : p.stretches) {  // (all pairs of tiles as the one with the most keys)
-                std::vector<RaggedRun> one(1, part[0]);
-                one[0].nq = part.back().q0 + part.back().nq - part[0].q0;
-                one[0].nk = 0;
-                for (const RaggedRun &r : part) one[0].nk = std::max(one[0].nk, r.nk);
-                split_tiles(one, sh, n_pre, coarse);
-                part[0].ns = one[0].ns;
-            }
+            split_tiles(whole, sh, n_pre, coarse);
             if (p.cluster == 1) split_rows(p.rows, sh, p.wide, p.stacked ? 0 : n_pre, coarse);
             split_tiles(p.tiles, sh, n_pre, coarse);
             split_tiles(p.tiles_pre, sh, 0, coarse, true);
@@ -307,14 +316,15 @@ Plan make_plan(std::vector<Seq> seqs, const Shape &sh, int32_t n_pre, const Kern
             records(r);
             p.joins.push_back(JoinRun{r.q0, r.nq, r.rec0, r.ns, 0, 0});
         }
-        for (std::vector<RaggedRun> &part : p.stretches) {
-            RaggedRun &r = part[0];
+        for (size_t x = 0; x < whole.size(); ++x) {
+            RaggedRun &r = whole[x], &f = p.shared[p.first[x]];
             r.rec0 = -1;
-            if (r.ns == 1) continue;
-            r.rec0 = static_cast<int32_t>(std::min<int64_t>(at, 0x7fffffff));
-            const int32_t nq = part.back().q0 + part.back().nq - r.q0;
-            at += static_cast<int64_t>(nq) * r.ns;
-            p.joins.push_back(JoinRun{r.q0, nq, r.rec0, r.ns, 0, 0});
+            if (r.ns > 1) {
+                records(r);
+                p.joins.push_back(JoinRun{r.q0, r.nq, r.rec0, r.ns, 0, 0});
+            }
+            f.ns = r.ns;
+            f.rec0 = r.rec0;
         }
         p.n_rec = at;
         if (at > 0 && (at > 0x7fffffff || record_bytes(at, sh) > workspace)) continue;
@@ -453,7 +463,7 @@ int attend(const Call &c, cudaStream_t st) {
     const Kernels kernels{a.vec, ragged_tc_takes(a)};
     return each_chunk(seqs, [&](const std::vector<Seq> &part) {
         const Plan p = make_plan(part, c.sh, c.n_pre, kernels, c.workspace_bytes);
-        if (!a.err && !(p.tiles.empty() && p.tiles_pre.empty() && p.stretches.empty())) {
+        if (!a.err && !(p.tiles.empty() && p.tiles_pre.empty() && p.shared.empty())) {
             const int r = contiguous_error_word(st, &a.err);
             if (r) return r;
         }
@@ -461,7 +471,7 @@ int attend(const Call &c, cudaStream_t st) {
         a.pl = a.pm + record_stats(p.n_rec, c.sh);
         a.pacc = a.pl + record_stats(p.n_rec, c.sh);
         bool first = true;
-        enum { kRows, kTiles, kStretch };
+        enum { kRows, kTiles, kShared };
         auto run = [&](RaggedArgs b, const std::vector<RaggedRun> &runs, int how) {
             for (size_t i = 0; i < runs.size(); i += kRaggedLarge) {
                 const int32_t n = static_cast<int32_t>(std::min<size_t>(kRaggedLarge, runs.size() - i));
@@ -470,7 +480,10 @@ int attend(const Call &c, cudaStream_t st) {
                 const int r = how == kRows ? counted(PKV_KERNEL_DECODE, st, "ragged attention rows",
                                                      [&] { return launch_ragged_rows(b, &runs[i], n, p.wide, st); })
                                            : counted(PKV_KERNEL_PREFILL, st, "ragged attention tiles",
-                                                     [&] { return launch_ragged_tc(b, &runs[i], n, how == kStretch, st); });
+                                                     [&] {
+                                                         return launch_ragged_tc(b, &runs[i], n, p.first.data(),
+                                                                                 how == kShared ? static_cast<int32_t>(p.first.size()) : 0, st);
+                                                     });
                 if (r) return r;
             }
             return static_cast<int>(PKV_OK);
@@ -483,9 +496,7 @@ int attend(const Call &c, cudaStream_t st) {
         pre.n_pre = 0;
         own.n_pre = p.stacked ? 0 : c.n_pre;
         own.cluster = p.cluster;
-        int r = PKV_OK;
-        for (const std::vector<RaggedRun> &part : p.stretches)
-            if (!r) r = run(a, part, kStretch);
+        int r = run(a, p.shared, kShared);
         if (!r) r = run(a, p.tiles, kTiles);
         if (!r) r = run(pre, p.tiles_pre, kTiles);
         if (!r) r = run(own, p.rows, kRows);
@@ -536,8 +547,8 @@ int rope(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, int32
         ++count[mine];
         a.axis[i] = static_cast<uint8_t>(mine);
         // turns a position; a ramp falls by one factor a pair, with a power every
-        // eighth (64 powers take 1 us, products between them cost a few last places)
-        if (number % 8 == 0) {
+        // fourth (64 powers take 1 us; three products between cost 2^-51 at most)
+        if (number % 4 == 0) {
             turns = std::pow(base, -static_cast<double>(number) / ramp) / 6.283185307179586477;
             if (number == 0) fall = std::pow(base, -1.0 / ramp);
         } else {

@@ -5,8 +5,8 @@
 // of rows (the prefix's, then the run's own) and, where a launch has few
 // pieces, the key tiles split and partial records written in place of outputs.
 //
-// Sequences whose own key rows lie in the order of their queries go as one
-// stretch of rows, so that short ones share tiles: 300 answers of 2 to 24
+// Sequences whose own key rows lie in the order of their queries go as stretches
+// of rows, so that short ones share tiles: 300 answers of 2 to 24
 // tokens behind a prefix of 1,100, 28 heads over 4: 176 us by sequences of their own, 51 so.
 //
 // The prefix's last tile is filled up with zeros by its own tensor map, so only
@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 template <int D, class T, int N, bool kLong, class F>
-cudaError_t tc_n(const RaggedArgs &a, const RaggedRun *runs, int32_t n, cudaStream_t s) {
+cudaError_t tc_n(const RaggedArgs &a, const RaggedRun *runs, int32_t n, const int32_t *first, int32_t n_stretches, cudaStream_t s) {
     using C = TcCfg<D>;
     static PerDeviceOnce configured;  // the attributes are per function and device
     cudaError_t e = configured.run([&]() -> cudaError_t {
@@ -59,7 +59,13 @@ cudaError_t tc_n(const RaggedArgs &a, const RaggedRun *runs, int32_t n, cudaStre
         if (at > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     }
     l.unit0[n] = static_cast<int32_t>(at);
-    if (F::kStacks) at = static_cast<int64_t>(ragged_pieces(runs[n - 1].q0 + runs[n - 1].nq - runs[0].q0, tokens)) * runs[0].ns;
+    for (int32_t x = 0; F::kStacks && x < n_stretches; ++x) {
+        const RaggedRun &f = runs[first[x]], &e = runs[(x + 1 < n_stretches ? first[x + 1] : n) - 1];
+        l.unit0[x] = static_cast<int32_t>(at);
+        l.run[x].kind = first[x];
+        at += static_cast<int64_t>(ragged_pieces(e.q0 + e.nq - f.q0, tokens)) * f.ns;
+        if (at > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    }
     const int64_t grid = at * (a.n_heads / heads);
     if (grid <= 0 || grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     EncodeTiled f;
@@ -76,6 +82,7 @@ cudaError_t tc_n(const RaggedArgs &a, const RaggedRun *runs, int32_t n, cudaStre
     }
     if (e != cudaSuccess) return e;
     RaggedArgs b = a;
+    b.n_stretches = n_stretches;
     b.out32 = a.hd % 16 == 0 && a.o_stride % 16 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -91,26 +98,27 @@ cudaError_t tc_n(const RaggedArgs &a, const RaggedRun *runs, int32_t n, cudaStre
 }
 
 template <int D, class T>
-cudaError_t tc_d(const RaggedArgs &a, const RaggedRun *runs, int32_t n, bool stack, cudaStream_t s) {
+cudaError_t tc_d(const RaggedArgs &a, const RaggedRun *runs, int32_t n, const int32_t *first, int32_t n_stretches, cudaStream_t s) {
+    const bool stack = n_stretches > 0;
     constexpr bool kT = D == 64;  // (128-wide heads have ring slots for two and a half tiles only)
     constexpr int kC = TcCfg<D>::kChains, kS = kRaggedSmall, kL = kRaggedLarge;
     bool is_long = false;  // some piece adds more keys than a sum takes
     for (int32_t i = 0; i < n && !stack; ++i) is_long = is_long || ragged_split_tiles(a.n_pre, runs[i]) * kKeys > kLongKeys;
     if constexpr (D > 128) {
         if (is_long) return cudaErrorInvalidValue;
-        return stack ? tc_n<D, T, kL, false, Stacks<kL, kC, kT>>(a, runs, n, s) : tc_n<D, T, kL, false, Runs<kL, kC, kT>>(a, runs, n, s);
+        return stack ? tc_n<D, T, kL, false, Stacks<kL, kC, kT>>(a, runs, n, first, n_stretches, s) : tc_n<D, T, kL, false, Runs<kL, kC, kT>>(a, runs, n, first, n_stretches, s);
     } else {
-        if (stack) return n <= kS ? tc_n<D, T, kS, false, Stacks<kS, kC, kT>>(a, runs, n, s) : tc_n<D, T, kL, false, Stacks<kL, kC, kT>>(a, runs, n, s);
-        if (is_long) return tc_n<D, T, kL, true, Runs<kL, kC, false>>(a, runs, n, s);  // (sums set aside stay with their chain)
-        return n <= kS ? tc_n<D, T, kS, false, Runs<kS, kC, kT>>(a, runs, n, s) : tc_n<D, T, kL, false, Runs<kL, kC, kT>>(a, runs, n, s);
+        if (stack) return n <= kS ? tc_n<D, T, kS, false, Stacks<kS, kC, kT>>(a, runs, n, first, n_stretches, s) : tc_n<D, T, kL, false, Stacks<kL, kC, kT>>(a, runs, n, first, n_stretches, s);
+        if (is_long) return tc_n<D, T, kL, true, Runs<kL, kC, false>>(a, runs, n, first, n_stretches, s);  // (sums set aside stay with their chain)
+        return n <= kS ? tc_n<D, T, kS, false, Runs<kS, kC, kT>>(a, runs, n, first, n_stretches, s) : tc_n<D, T, kL, false, Runs<kL, kC, kT>>(a, runs, n, first, n_stretches, s);
     }
 }
 template <class T>
-cudaError_t tc_t(const RaggedArgs &a, const RaggedRun *runs, int32_t n, bool stack, cudaStream_t s) {
-    if (a.hd <= 64) return tc_d<64, T>(a, runs, n, stack, s);
-    if (a.hd <= 128) return tc_d<128, T>(a, runs, n, stack, s);
-    if (a.hd <= 192) return tc_d<192, T>(a, runs, n, stack, s);
-    return tc_d<256, T>(a, runs, n, stack, s);
+cudaError_t tc_t(const RaggedArgs &a, const RaggedRun *runs, int32_t n, const int32_t *first, int32_t n_stretches, cudaStream_t s) {
+    if (a.hd <= 64) return tc_d<64, T>(a, runs, n, first, n_stretches, s);
+    if (a.hd <= 128) return tc_d<128, T>(a, runs, n, first, n_stretches, s);
+    if (a.hd <= 192) return tc_d<192, T>(a, runs, n, first, n_stretches, s);
+    return tc_d<256, T>(a, runs, n, first, n_stretches, s);
 }
 
 }  // namespace

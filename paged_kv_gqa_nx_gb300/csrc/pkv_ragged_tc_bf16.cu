@@ -3,13 +3,15 @@
 
 namespace pkv {
 
-cudaError_t launch_ragged_tc_bf16(const RaggedArgs &a, const RaggedRun *runs, int32_t n, bool stack, cudaStream_t s) {
-    return tc_t<bf16>(a, runs, n, stack, s);
+cudaError_t launch_ragged_tc_bf16(const RaggedArgs &a, const RaggedRun *runs, int32_t n, const int32_t *first, int32_t n_stretches,
+                             cudaStream_t s) {
+    return tc_t<bf16>(a, runs, n, first, n_stretches, s);
 }
 
-cudaError_t launch_ragged_tc(const RaggedArgs &a, const RaggedRun *runs, int32_t n, bool stack, cudaStream_t s) {
+cudaError_t launch_ragged_tc(const RaggedArgs &a, const RaggedRun *runs, int32_t n, const int32_t *first, int32_t n_stretches,
+                             cudaStream_t s) {
     if (n <= 0 || n > kRaggedLarge || a.hd > kMaxHeadDim || !ragged_tc_takes(a)) return cudaErrorInvalidValue;
-    return a.type == Elem::bf16 ? launch_ragged_tc_bf16(a, runs, n, stack, s) : launch_ragged_tc_f16(a, runs, n, stack, s);
+    return a.type == Elem::bf16 ? launch_ragged_tc_bf16(a, runs, n, first, n_stretches, s) : launch_ragged_tc_f16(a, runs, n, first, n_stretches, s);
 }
 
 }  // namespace pkv

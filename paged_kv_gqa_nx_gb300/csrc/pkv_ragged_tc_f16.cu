@@ -3,8 +3,9 @@
 
 namespace pkv {
 
-cudaError_t launch_ragged_tc_f16(const RaggedArgs &a, const RaggedRun *runs, int32_t n, bool stack, cudaStream_t s) {
-    return tc_t<f16>(a, runs, n, stack, s);
+cudaError_t launch_ragged_tc_f16(const RaggedArgs &a, const RaggedRun *runs, int32_t n, const int32_t *first, int32_t n_stretches,
+                             cudaStream_t s) {
+    return tc_t<f16>(a, runs, n, first, n_stretches, s);
 }
 
 }  // namespace pkv

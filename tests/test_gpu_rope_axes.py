@@ -3,7 +3,8 @@
 Tolerance of an output y = x0 cos - x1 sin (or x0 sin + x1 cos): half a step of the type, u |y|, and
 (|x0| + |x1|) e with e = 2^-21 + |p| 2^-51: cosine and sine are within 2^-22 (the angle's rest rounded to f32, at most
 pi/4 2^-24, and two last places of the f32 sine), two products' and a sum's f32 roundings add 2^-23, and the angle itself is off
-by 2^-52 of its size here and in the plain form.
+by 2^-53 of its size in the plain form and, here, by up to 2^-51 of it at the pairs between two powers, whose
+frequencies have fallen below 3/4.
 """
 import math
 
