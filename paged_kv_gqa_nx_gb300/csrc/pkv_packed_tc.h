@@ -808,7 +808,13 @@ __device__ __forceinline__ void packed_tc(const CUtensorMap &mq, const CUtensorM
                         if (*static_cast<volatile uint32_t *>(&dirty[look & 3]) == look + 1) {
                             // this tile's V values that are not finite, key by key (PV(0) of
                             // the piece writes over O, unless told that O holds something;
-                            // O is this piece's from then on: its reader is this thread)
+                            // O is this piece's from then on: its reader is this thread,
+                            // but for an O_1 of tiles taken in turn, which chain 0 reads)
+                            if (F::kAlt && c == 1 && j == 0 && pieces > 0) {
+                                ok = wait_w(&bar_ofree[1], pieces - 1);
+                                if (!ok) break;
+                                fence_after_sync();
+                            }
                             int64_t row = p.row0 + base;
                             if constexpr (F::kRuns) row = p.k0 + base;  // (a tile of the run's own)
                             const T *v = static_cast<const T *>(a.V) + row * a.v_stride + static_cast<int64_t>(p.kvh) * a.hd;

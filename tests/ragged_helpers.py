@@ -94,7 +94,7 @@ class Case:
                 A = torch.einsum("gij,jd->igd", p, V[:, j].abs())
                 es = (hd + 4) * 2.0 ** -23 * w.amax(-1).t()[:, :, None]
                 tol[s, g] = A * (2 * u + 2 * es) + K.shape[0] * 2.0 ** -24 * V[:, j].abs().max()
-        return out.view(T, -1), tol.view(T, -1)
+        return out.view(T, H * hd), tol.view(T, H * hd)
 
     def check(self, got=None, scale=None, **kw):
         got = self.call(scale=scale, **kw) if got is None else got

@@ -76,6 +76,26 @@ def test_one_tile_of_queries_takes_its_keys_on_both_chains(H, KV, hd, dtype):
     Case([60] * 90, [400 + 130 * (i % 4) for i in range(90)], H, KV, hd, dtype, seed=hd).check()
 
 
+@pytest.mark.parametrize("workspace", ["full", None])
+@pytest.mark.parametrize("hd", [8, 64])
+@BAD
+def test_a_piece_with_hidden_values_waits_for_the_output_before_it(hd, bad, workspace):
+    """Blocks go from pieces whose last tile, on one chain, hides rows that are not finite to pieces where the other
+    chain's first tile does: its output there still holds its part of the piece before."""
+    ql = [53, 62, 58, 80, 1, 1, 12, 1, 58, 5, 97, 1, 1, 40, 80, 3, 1, 46, 41, 1, 77, 28, 1, 44, 1, 38, 56, 29, 1, 26, 1, 1, 1,
+          61, 1, 2, 81, 1, 36, 1, 1, 85, 1, 1, 52, 1]
+    kl = [53, 62, 58, 80, 1, 168, 516, 75, 80, 5, 124, 1, 211, 40, 80, 3, 368, 46, 238, 1, 90, 415, 1, 44, 226, 38, 56, 29, 45,
+          468, 1, 1, 498, 61, 22, 2, 81, 1, 36, 1, 1, 85, 1, 1, 52, 1]
+    c = Case(ql, kl, 17, 1, hd, BF16, prefix=128, gap=7, seed=hd)
+    for s, n in zip(c.start, c.kl):
+        c.v[s + n:s + n + 7] = bad
+    c.check(workspace=c.workspace() if workspace else None)
+    c = Case([40] * 90, [300] * 45 + [200] * 45, 6, 6, hd, BF16, gap=3, seed=hd)
+    for s, n in zip(c.start, c.kl):
+        c.v[s + n:s + n + 3] = bad
+    c.check(workspace=c.workspace() if workspace else None)
+
+
 @pytest.mark.parametrize("which", ["k", "v"])
 @BAD
 def test_both_chains_keep_values_out_of_sight(which, bad):
