@@ -239,14 +239,29 @@ bool worth_stacking(const std::vector<RaggedRun> &runs, const Shape &sh, const K
     return units * n_pre * sh.hd * 4 / 6000 > 15000 + rows;  // ns
 }
 
+// Whether sequences with few queries go with the others' tiles, which saves a launch of
+// their own: where they add no more than twice the others' key tiles.  24 prompts of
+// 4 to 448 queries, 7 of them with few, over 700 to 1,500 keys, 20 heads of 64: 58 us in
+// two launches, 49 in one; with one of few, 32 heads over 8 of 128: 58 and 42; one prompt and one
+// token: 10 and 7 to 9; but 200 tokens and one prompt, over 1,000 keys each: 165 and 201.
+template <class Can, class Takes>
+bool goes_along(const std::vector<Seq> &seqs, const Shape &sh, Can &&can, Takes &&takes) {
+    const int32_t tokens = ragged_piece_tokens(ragged_tile_heads(sh.group()), sh.hd);
+    int64_t few = 0, many = 0;
+    for (const Seq &s : seqs) {
+        if (!can(s.nk)) continue;
+        (takes(s.nq, s.nk) ? many : few) += static_cast<int64_t>(ragged_pieces(s.nq, tokens)) * ragged_key_tiles(0, s.nk);
+    }
+    return few > 0 && few <= 2 * many;
+}
+
 // The plan of up to kRaggedLarge sequences; with less workspace than it would
 // like, keys are split less, or not at all.
 Plan make_plan(std::vector<Seq> seqs, const Shape &sh, int32_t n_pre, const Kernels &kernels, int64_t workspace) {
     constexpr int64_t kCoarsest = int64_t{1} << 24;
     const int heads = ragged_tile_heads(sh.group());  // of a tile
-    auto takes_tiles = [&](int64_t nq, int32_t keys) {
-        return kernels.tc && keys > 0 && nq * heads >= kTileRows && (sh.hd <= 128 || keys <= kRaggedSumKeys);
-    };
+    auto can_take_tiles = [&](int32_t keys) { return kernels.tc && keys > 0 && (sh.hd <= 128 || keys <= kRaggedSumKeys); };
+    auto takes_tiles = [&](int64_t nq, int32_t keys) { return can_take_tiles(keys) && nq * heads >= kTileRows; };
     std::vector<RaggedRun> own;
     Plan p;
     if (kernels.tc)
@@ -261,8 +276,9 @@ Plan make_plan(std::vector<Seq> seqs, const Shape &sh, int32_t n_pre, const Kern
         const int32_t nq = e.q0 + e.nq - f.q0, pieces = ragged_pieces(nq, ragged_piece_tokens(heads, sh.hd));
         whole.push_back(RaggedRun{f.q0, nq, f.k0, std::max(std::max(f.nk, e.nk), (e.k0 + e.nk - f.k0 + pieces - 1) / pieces), 0, 1, -1, kOwnKeys});
     }
+    const bool along = n_pre == 0 && goes_along(seqs, sh, can_take_tiles, takes_tiles);
     for (const Seq &s : seqs)
-        (takes_tiles(s.nq, n_pre + s.nk) ? p.tiles : own).push_back(RaggedRun{s.q0, s.nq, s.k0, s.nk, s.off, 1, -1, kOwnKeys});
+        ((along && can_take_tiles(s.nk)) || takes_tiles(s.nq, n_pre + s.nk) ? p.tiles : own).push_back(RaggedRun{s.q0, s.nq, s.k0, s.nk, s.off, 1, -1, kOwnKeys});
     for (int64_t coarse = workspace < record_bytes(1, sh) ? 2 * kCoarsest : 1;; coarse *= 2) {
         const bool last = coarse > kCoarsest;
         p.cluster = pick_cluster(own, sh, kernels, n_pre);

@@ -114,6 +114,17 @@ def test_both_chains_keep_values_out_of_sight(which, bad):
     assert not bool(torch.isfinite(got[131:160].float()).all(dim=1).any())
 
 
+@pytest.mark.parametrize("ql,kl", [([100, 1, 3, 60], [700, 700, 1, 129]), ([100, 1, 1, 1, 1], [300, 600, 600, 300, 4]),
+                                   ([1, 300, 0, 2, 1], [128, 1000, 50, 0, 2000]), ([60, 1], [20, 5000])],
+                         ids=["along", "too_many", "one_without_keys", "too_long"])
+@pytest.mark.parametrize("H,KV,hd", [(20, 20, 64), (8, 2, 128), (4, 4, 80), (4, 2, 256)])
+@DTYPES
+def test_tokens_among_prompts(ql, kl, dtype, H, KV, hd):
+    c = Case(ql, kl, H, KV, hd, dtype, seed=hd)
+    c.check()
+    c.check(workspace=None)
+
+
 def test_more_sequences_than_one_launch_takes():
     n = 2003
     r = torch.Generator().manual_seed(5)
