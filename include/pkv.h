@@ -528,7 +528,8 @@ enum pkv_rope_order {
 /* Rotary positions with several axes (time, height and width of images and
  * video; pkv_attn_batch_rope has one) on packed query and key rows.  Row t has
  * a position on each of n_axes (1 to 4) axes, positions[axis * pos_stride + t]
- * (device, int32, any sign).  With r the sum of pairs[] (host array), in every
+ * (device, int32, any sign; pos_stride at least n_rows, or 0 where the axes
+ * share their positions).  With r the sum of pairs[] (host array), in every
  * head and for i < r the pair (x[i], x[i + r]) turns by the angle p * f_i:
  *   y[i] = x[i] cos - x[i + r] sin,  y[i + r] = x[i] sin + x[i + r] cos,
  * p the row's position on pair i's axis (`order`), f_i = rope_base^(-i / r), or

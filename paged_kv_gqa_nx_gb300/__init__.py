@@ -600,7 +600,8 @@ def pkv_rope_packed(Q, K, positions, pairs, order, n_heads, n_kv_heads, head_dim
                     inverse=False, stream=None):
     """Q, Q_out: [tokens, n_heads * head_dim], K, K_out: [tokens, n_kv_heads * head_dim], float32, bfloat16 or
     float16 CUDA tensors with contiguous rows (Q or K may be None, with its output; an output may be its
-    input); positions: int32 CUDA tensor [axes, tokens]; pairs: frequency pairs of each axis; order:
+    input); positions: int32 CUDA tensor [axes, tokens], any row stride (positions that all axes share may be
+    expanded, rows that overlap are refused); pairs: frequency pairs of each axis; order:
     PKV_ROPE_BLOCKS, PKV_ROPE_TURNS or PKV_ROPE_AXIAL; inverse turns back (the gradient)."""
     global _int32
     if _int32 is None:
@@ -640,7 +641,7 @@ def pkv_rope_packed(Q, K, positions, pairs, order, n_heads, n_kv_heads, head_dim
             raise TypeError("K and K_out need %d rows" % rows)
     elif K_out is not None:
         raise TypeError("K_out without K")
-    return _lib.pkv_rope_packed(q, qs, k, ks, kind, positions.data_ptr(), pos_stride if pos_stride > rows else rows, axes,
+    return _lib.pkv_rope_packed(q, qs, k, ks, kind, positions.data_ptr(), pos_stride if axes > 1 else rows, axes,
                                 _i32_array(pairs), order, rows, n_heads, n_kv_heads, head_dim, rope_base,
                                 1 if inverse else 0, qo, qos, ko, kos, _stream(stream))
 

@@ -593,7 +593,7 @@ int rope(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, int32
     if ((Q && (q_stride < q_dim || qo_stride < q_dim)) || (K && (k_stride < k_dim || ko_stride < k_dim)))
         return refuse(PKV_ERR_ARG, "a row stride below the row's width makes rows overlap");
     if (std::max({q_stride, k_stride, qo_stride, ko_stride, pos_stride}) > (int64_t{1} << 32)) return refuse(PKV_ERR_BAD_DIM, "row stride too large");
-    if (n_axes > 1 && pos_stride < n_rows) return refuse(PKV_ERR_ARG, "the axes' positions overlap");
+    if (n_axes > 1 && pos_stride != 0 && pos_stride < n_rows) return refuse(PKV_ERR_ARG, "the axes' positions overlap");
     if (n_rows == 0) return PKV_OK;
     if ((!Q && !K) || !pos || (Q && !Q_out) || (K && !K_out) || (!Q && Q_out) || (!K && K_out))
         return refuse(PKV_ERR_ARG, "NULL data pointer (a left out part has neither rows nor a place for them)");
