@@ -572,7 +572,9 @@ __global__ void __launch_bounds__(128, 4)
                 m0 = __ldcg(a.pm + r), l0 = __ldcg(a.pl + r);
             }
         }
-        const float f = l0 == 0.f ? 0.f : pow2(m0 - ref);  // (0: no key of it is seen, no output was written)
+        // A record without a key in sight (sum 0) holds no output and is passed over: -1.  One whose weight
+        // is 0 counts: what it holds may be infinite, and 0 times that is NaN however the keys are split.
+        const float f = l0 == 0.f ? -1.f : pow2(m0 - ref);
         L = fmaf(l0, f, L);
         const int m = min(32, n - x0);
         for (int y0 = first; y0 < m; y0 += kBatch * step) {
@@ -582,13 +584,13 @@ __global__ void __launch_bounds__(128, 4)
             for (int e = 0; e < kBatch; ++e) {
                 const int y = y0 + e * step;
                 w[e] = __shfl_sync(kAll, f, y & 31);
-                if (y >= m) w[e] = 0.f;
+                if (y >= m) w[e] = -1.f;
                 const int x = x0 + min(y, m - 1);
                 const float *src = (x < run.ns ? own_out : pre_out) + x * out_step;
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
                     v[e][j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (w[e] == 0.f) continue;
+                    if (w[e] < 0.f) continue;
                     const int left = a.hd - 4 * lane - 128 * j;
                     if (vec) {
                         if (left > 0) v[e][j] = __ldcg(reinterpret_cast<const float4 *>(src + 128 * j));
