@@ -507,7 +507,12 @@ PKV_API int64_t pkv_attn_cross_workspace(const int32_t *q_lens, const int32_t *k
  * attends the prefix and own rows j <= k_lens[s] - q_lens[s] + i.  k_lens[s] >=
  * q_lens[s] (PKV_ERR_BAD_DIM); prefix_len 0 and sequences without queries are
  * fine.  The prefix is read and multiplied once for the rows of all sequences
- * that have few queries.  Everything else as for pkv_attn_cross. */
+ * that have few queries.  Everything else as for pkv_attn_cross.
+ *
+ * How much workspace a call would like goes by where its rows lie too, as short
+ * sequences share tiles where their rows follow one another:
+ * pkv_attn_prefix_workspace_at takes the call's k_start, pkv_attn_prefix_workspace
+ * is the same for k_start NULL. */
 PKV_API int pkv_attn_prefix(const void *Q, int64_t q_stride, int64_t q_rows, const int32_t *q_lens,
                             const void *K_prefix, int64_t kp_stride, const void *V_prefix, int64_t vp_stride,
                             int32_t prefix_len, const void *K, int64_t k_stride, const void *V, int64_t v_stride,
@@ -516,6 +521,9 @@ PKV_API int pkv_attn_prefix(const void *Q, int64_t q_stride, int64_t q_rows, con
                             void *workspace, int64_t workspace_bytes, pkv_stream_t stream);
 PKV_API int64_t pkv_attn_prefix_workspace(int32_t prefix_len, const int32_t *q_lens, const int32_t *k_lens,
                                           int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
+PKV_API int64_t pkv_attn_prefix_workspace_at(int32_t prefix_len, const int32_t *q_lens, const int32_t *k_lens,
+                                             const int32_t *k_start, int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads,
+                                             int32_t head_dim);
 
 /* Which position a frequency pair turns by. */
 enum pkv_rope_order {

@@ -92,6 +92,7 @@ _SIGS = {
     "pkv_attn_prefix": (_int, [_vp, _i64, _i64, _pi32, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _i64, _pi32, _pi32,
                                _i32, _i32, _i32, _i32, _i32, _f32, _vp, _i64, _vp, _i64, _vp]),
     "pkv_attn_prefix_workspace": (_i64, [_i32, _pi32, _pi32, _i32, _i32, _i32, _i32]),
+    "pkv_attn_prefix_workspace_at": (_i64, [_i32, _pi32, _pi32, _pi32, _i32, _i32, _i32, _i32]),
     "pkv_rope_packed": (_int, [_vp, _i64, _vp, _i64, _i32, _vp, _i64, _i32, _pi32, _i32, _i32, _i32, _i32, _i32,
                                ctypes.c_double, _i32, _vp, _i64, _vp, _i64, _vp]),
     "pkv_append_packed": (_int, [_vp, _i32, _pi32, _i32, _vp, _i64, _vp, _i64, _i32]),
@@ -571,16 +572,23 @@ def pkv_attn_cross(Q, q_lens, K, V, k_lens, n_heads, n_kv_heads, head_dim, scale
                                n_heads, n_kv_heads, head_dim, scale, o, os_, w, wn, _stream(stream))
 
 
-def pkv_attn_prefix_workspace(prefix_len, q_lens, k_lens, n_heads, n_kv_heads, head_dim):
-    """Bytes that pkv_attn_prefix would like as workspace; -1 on bad arguments (pkv_last_error())."""
-    q, k, _, n = _lengths(q_lens, k_lens, None)
-    return _lib.pkv_attn_prefix_workspace(prefix_len, q, k, n, n_heads, n_kv_heads, head_dim)
+def pkv_attn_prefix_workspace_at(prefix_len, q_lens, k_lens, k_start, n_heads, n_kv_heads, head_dim):
+    """Bytes that pkv_attn_prefix would like as workspace for rows at k_start (None: behind one another); -1 on
+    bad arguments (pkv_last_error())."""
+    q, k, k0, n = _lengths(q_lens, k_lens, k_start)
+    return _lib.pkv_attn_prefix_workspace_at(prefix_len, q, k, k0, n, n_heads, n_kv_heads, head_dim)
+
+
+def pkv_attn_prefix_workspace(prefix_len, q_lens, k_lens, n_heads, n_kv_heads, head_dim, k_start=None):
+    """pkv_attn_prefix_workspace_at with the arguments in the order of pkv_attn_cross_workspace."""
+    return pkv_attn_prefix_workspace_at(prefix_len, q_lens, k_lens, k_start, n_heads, n_kv_heads, head_dim)
 
 
 def pkv_attn_prefix(Q, q_lens, K_prefix, V_prefix, K, V, k_lens, n_heads, n_kv_heads, head_dim, scale, out,
                     k_start=None, workspace=None, stream=None):
-    """As pkv_attn_cross; K_prefix, V_prefix: [prefix rows, n_kv_heads * head_dim], seen by every sequence;
-    k_lens counts a sequence's own keys, the last q_lens of which belong to its queries."""
+    """As pkv_attn_cross (workspace: pkv_attn_prefix_workspace bytes, for the same k_start); K_prefix, V_prefix:
+    [prefix rows, n_kv_heads * head_dim], seen by every sequence; k_lens counts a sequence's own keys, the last
+    q_lens of which belong to its queries."""
     ql, kl, k0, n = _lengths(q_lens, k_lens, k_start)
     kind, qw, kw = _element(Q, K, V, K_prefix, V_prefix, out), n_heads * head_dim, n_kv_heads * head_dim
     q, qs, qn = _matrix(Q, "Q", qw)

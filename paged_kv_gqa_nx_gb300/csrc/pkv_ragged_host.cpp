@@ -643,8 +643,8 @@ int64_t pkv_attn_cross_workspace(const int32_t *q_lens, const int32_t *k_lens, c
     return rc ? -1 : n;
 }
 
-int64_t pkv_attn_prefix_workspace(int32_t prefix_len, const int32_t *q_lens, const int32_t *k_lens, int32_t n_seqs,
-                                  int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
+int64_t pkv_attn_prefix_workspace_at(int32_t prefix_len, const int32_t *q_lens, const int32_t *k_lens, const int32_t *k_start,
+                                     int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
     int64_t n = -1;
     const int rc = guarded([&] {
         Call c{};
@@ -652,12 +652,18 @@ int64_t pkv_attn_prefix_workspace(int32_t prefix_len, const int32_t *q_lens, con
         c.causal = true;
         c.q_lens = q_lens;
         c.k_lens = k_lens;
+        c.k_start = k_start;
         c.n_seqs = n_seqs;
         c.sh = Shape{n_heads, n_kv_heads, head_dim};
         n = workspace_of(c);
         return static_cast<int>(PKV_OK);
     });
     return rc ? -1 : n;
+}
+
+int64_t pkv_attn_prefix_workspace(int32_t prefix_len, const int32_t *q_lens, const int32_t *k_lens, int32_t n_seqs,
+                                  int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
+    return pkv_attn_prefix_workspace_at(prefix_len, q_lens, k_lens, nullptr, n_seqs, n_heads, n_kv_heads, head_dim);
 }
 
 int pkv_attn_cross(const void *Q, int64_t q_stride, int64_t q_rows, const int32_t *q_lens, const void *K, int64_t k_stride,
