@@ -212,8 +212,8 @@ def prepare(case, seed):
     if own:
         import paged_kv_gqa_nx_gb300 as pkv
         heads = (case["heads"], case["kv"], case["hd"])
-        n = (pkv.pkv_attn_cross_workspace(s["n_q"], s["n_k"], *heads) if case["op"] == "cross" else
-             pkv.pkv_attn_prefix_workspace(case["prefix"], s["n_q"], s["n_k"], *heads))
+        n = (pkv.pkv_attn_cross_workspace(s["n_q"], s["n_k"], *heads, k_start=s["k0"]) if case["op"] == "cross" else
+             pkv.pkv_attn_prefix_workspace(case["prefix"], s["n_q"], s["n_k"], *heads, k_start=s["k0"]))
         s["workspace"] = torch.empty(n, dtype=torch.uint8, device="cuda")
     return s
 
