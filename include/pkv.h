@@ -469,12 +469,18 @@ PKV_API int pkv_attn_packed(const void *Q, int64_t q_stride, const void *K, int6
  * strides and head grouping as for pkv_attn_packed, row counts up to 2^30.
  *
  * Scores, softmax statistics and outputs accumulate in f32, and the output is
- * rounded once.  Where a sequence's queries fill tensor-core tiles (24 (query,
- * head of a kv head) pairs and more, rows and heads on 16-byte boundaries, a
- * positive scale) the probabilities are rounded to dtype before they meet V, as
- * in pkv_attn_packed; otherwise they keep at least 16 bits.  A call gives the same
- * bits every time; the same sequence in another batch may be split elsewhere and
- * differ within these roundings.  A key row that a query does not see never
+ * rounded once.  The probabilities of a row on the tensor-core tiles are rounded to
+ * dtype before they meet V, as in pkv_attn_packed (by half a step, 2^-8 of each in
+ * bf16 and 2^-11 in f16); of other rows they keep at least 16 bits.  Which rows take
+ * tiles is a matter of the whole call: those of a sequence with 24 (query, head of a
+ * kv head) pairs and more, but also a single token's beside such a sequence, among
+ * others as short with which it shares a tile, or on its way over a shared prefix.
+ * All rows keep 16 bits in a call whose rows or heads are off 16-byte boundaries
+ * or whose scale is not positive, in a pkv_attn_cross whose sequences all have fewer
+ * pairs (neighbours over the same rows count as one), and in a pkv_attn_prefix of one
+ * sequence with fewer.  A call gives the same bits every time; the same sequence in
+ * another batch may take other tiles or splits and differ within these roundings.
+ * A key row that a query does not see never
  * reaches it, whatever it holds; one that it does see and that holds an infinity
  * or a NaN makes outputs infinite or NaN.  Rows of out past the last sequence are
  * left as they were; out may not overlap the inputs.
