@@ -480,10 +480,13 @@ PKV_API int pkv_attn_packed(const void *Q, int64_t q_stride, const void *K, int6
  * pairs (neighbours over the same rows count as one), and in a pkv_attn_prefix of one
  * sequence with fewer.  A call gives the same bits every time; the same sequence in
  * another batch may take other tiles or splits and differ within these roundings.
- * A key row that a query does not see never
- * reaches it, whatever it holds; one that it does see and that holds an infinity
- * or a NaN makes outputs infinite or NaN.  Rows of out past the last sequence are
- * left as they were; out may not overlap the inputs.
+ *
+ * A key row that a query does not see never reaches it, whatever it holds.  One that
+ * it does see counts as in the formula: an infinity or a NaN in V makes outputs
+ * infinite or NaN, however small its weight; a score of infinity or NaN makes them
+ * NaN; a score of minus infinity is a weight of 0, and its V row may be left out (a row
+ * that sees no other score comes out as 0 or NaN).  Rows of out past the last sequence
+ * are left as they were; out may not overlap the inputs.
  *
  * workspace: device memory for partial results, 16-byte aligned, for work split
  * over the keys where there are few queries.  pkv_attn_cross_workspace says how
@@ -492,8 +495,8 @@ PKV_API int pkv_attn_packed(const void *Q, int64_t q_stride, const void *K, int6
  * not be kept or cleared between calls; calls that may run at the same time
  * (other streams, captured graphs) need one each.  Nothing is uploaded or
  * allocated; the call can be captured into a CUDA graph (the lengths are then
- * part of the graph), provided that an earlier call outside a capture set up the
- * device's error word.  Runs on `stream` and the current device.  Checks, in
+ * part of the graph), provided that the device's error word was set up outside a
+ * capture before: by a call of the same lengths, or by any pkv_attn_packed.  Runs on `stream` and the current device.  Checks, in
  * order: lengths and sizes -> PKV_ERR_BAD_DIM, grouping -> PKV_ERR_BAD_GQA, dtype,
  * strides, workspace, rows, pointers -> PKV_ERR_ARG.  Failures found on the
  * device: pkv_contiguous_sync_error. */

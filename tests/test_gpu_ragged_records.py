@@ -65,3 +65,26 @@ def test_splits_that_see_no_key_leave_nothing():
     got = c.call()
     torch.cuda.synchronize()
     assert bool(torch.isfinite(got[[0, 1, 3]].float()).all()) and not bool(torch.isfinite(got[2].float()).any())
+
+
+@pytest.mark.parametrize("hd", [128, 64, 20, 160])
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("workspace", ["full", None])
+@pytest.mark.parametrize("ql", [[1, 1], [60, 1]], ids=["tokens", "tiles"])
+def test_scores_that_are_infinite(ql, workspace, dtype, hd):
+    """A score of minus infinity is a weight of 0, as if its key were not there; one of infinity makes the row NaN."""
+    c = Case(ql, [3001, 200], 4, 2, hd, dtype, gap=0)
+    c.q.copy_(c.q.abs() + 0.5)
+    c.k[3000, 3] = -float("inf")  # of kv head 0
+    got = c.call(workspace=workspace)
+    short = Case(ql, [3000, 200], 4, 2, hd, dtype, k_start=[0, 3001])
+    short.q, short.k, short.v = c.q, c.k, c.v
+    exp, tol = short.plain()
+    whole, tol1 = c.plain()
+    exp[:, 2 * hd:], tol[:, 2 * hd:] = whole[:, 2 * hd:], tol1[:, 2 * hd:]  # kv head 1 sees all its keys
+    assert bool(((got.double() - exp).abs() <= tol).all())
+    c.k[3000, 3] = float("inf")
+    bad = c.call(workspace=workspace)
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(bad[:ql[0], :2 * hd].float()).all())
+    assert torch.equal(bad[:, 2 * hd:], got[:, 2 * hd:]) and torch.equal(bad[ql[0]:], got[ql[0]:])
