@@ -553,8 +553,10 @@ enum pkv_rope_order {
  * with PKV_ROPE_AXIAL rope_base^(-j / pairs[axis]) for the axis's j-th pair.
  * Elements past 2 r of a head stay.  inverse != 0 turns back, by -p * f_i, which
  * is also the gradient: the rows' gradients are the outputs' turned back.
- * The angle is exact to 2^-50 of its own size at any position, its cosine and
- * sine and the products are f32, and each result is rounded once to the type.
+ * The angle is off by at most 2^-50 of its own size and |p| 2^-64 of a turn (steps
+ * are whole 2^-64 turns a position: slow pairs lose relative bits, 2^-42 at a base of
+ * 10^6), its cosine and sine and the products are f32, and each result is rounded
+ * once to the type.
  * dtype: PKV_F32, PKV_BF16 or PKV_F16 for all rows.  Strides in elements;
  * outputs are other rows, or the inputs themselves (same address and stride).  Q or K
  * may be NULL, with its output, and is then left out.  rope_base finite, >= 1.

@@ -577,7 +577,8 @@ int rope(const void *Q, int64_t q_stride, const void *K, int64_t k_stride, int32
         ++count[mine];
         a.axis[i] = static_cast<uint8_t>(mine);
         // turns a position; a ramp falls by one factor a pair, with a power every
-        // fourth (64 powers take 1 us; three products between cost 2^-51 at most)
+        // fourth (64 powers take 1 us; three products between cost 2^-50 at most); the
+        // step is cut to whole 2^-64 turns
         if (number % 4 == 0) {
             turns = std::pow(base, -static_cast<double>(number) / ramp) / 6.283185307179586477;
             if (number == 0) fall = std::pow(base, -1.0 / ramp);

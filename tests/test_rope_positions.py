@@ -1,6 +1,9 @@
 """pkv_rope_packed with positions as a view: the axes of text rows share one row of positions (`pos.expand(3, n)`), rows of
-positions lie apart or overlap.  What the binding hands on is looked at with a stand-in for the library, on the CPU."""
+positions lie apart or overlap.  What the binding hands on is looked at with a stand-in for the library, on the CPU.
+And with positions and bases that make its angles very small or very large."""
 import ctypes
+import math
+from decimal import Decimal, getcontext
 
 import pytest
 import torch
@@ -74,3 +77,33 @@ def test_shared_positions_turn_as_a_copy_of_them(n, order, pairs):
             pkv.check(pkv.pkv_rope_packed(q, k, p, pairs, order, 4, 2, 128, 1e6, qo, ko, stream=torch.cuda.current_stream()))
         assert all(torch.equal(a, b) for a, b in zip(*outs))
         assert all(bool(torch.isfinite(x.float()).all()) for x in outs[0])
+
+
+PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("base", [1e4, 1e6, 1e8, 1e15])
+def test_sines_of_slow_pairs_and_far_positions(base):
+    """A pair (0, 1) turns into (-sin, cos).  Bound: the angle's, 2^-50 of its size and |p| 2^-64 of a turn, and 2^-21 of the
+    sine or cosine (the rest of an angle rounded to f32, two last places of the f32 function)."""
+    getcontext().prec = 50
+    r, places = 32, [0, 1, -1, 7, 1000, -12345, 131071, 1 << 20, 999_999_937, -(1 << 30) - 3, (1 << 31) - 1, -(1 << 31)]
+    x = torch.cat([torch.zeros(len(places), r), torch.ones(len(places), r)], dim=1).cuda()
+    pos = torch.tensor([places], dtype=torch.int32, device="cuda")
+    out = torch.empty_like(x)
+    pkv.check(pkv.pkv_rope_packed(x, None, pos, [r], pkv.PKV_ROPE_BLOCKS, 1, 0, 2 * r, base, out, None,
+                                  stream=torch.cuda.current_stream()))
+    got = out.double().cpu()
+    for i in range(r):
+        f = Decimal(int(base)) ** (Decimal(-i) / Decimal(r))
+        for t, p in enumerate(places):
+            a = p * f
+            turn = a / (2 * PI) % 1
+            near = float((turn - (turn * 4).to_integral_value() / 4) * 2 * PI)  # less the nearest quarter turn
+            quarter = int((turn * 4).to_integral_value()) % 4
+            s, c = [(math.sin(near), math.cos(near)), (math.cos(near), -math.sin(near)), (-math.sin(near), -math.cos(near)),
+                    (-math.cos(near), math.sin(near))][quarter]
+            off = abs(float(a)) * 2.0 ** -50 + abs(p) * 2.0 ** -64 * 2 * math.pi
+            for y, exact in ((-float(got[t, i]), s), (float(got[t, i + r]), c)):
+                assert abs(y - exact) <= off + 2.0 ** -21 * abs(exact), (i, p, y, exact, off)
