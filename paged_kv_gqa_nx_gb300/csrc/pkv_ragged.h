@@ -13,6 +13,8 @@
 
 namespace pkv {
 
+constexpr int32_t kSMs = 152;  // of the GPU that the plans and grids are made for
+
 constexpr int32_t kSees = 0x3fffffff;  // `off` of a run whose queries see every key
 
 // What a run of the row kernel is: its own keys (behind the prefix, where the

@@ -17,7 +17,6 @@ using namespace pkv;
 namespace {
 
 constexpr int64_t kMaxRows = int64_t{1} << 30;   // query rows, and key rows, of a call
-constexpr int32_t kSMs = 152;
 
 int refuse(int code, const char *fmt, ...) {
     char buf[512];

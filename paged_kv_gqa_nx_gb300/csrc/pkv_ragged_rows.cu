@@ -704,7 +704,7 @@ cudaError_t join_n(const RaggedArgs &a, const JoinRun *runs, int32_t n, cudaStre
         if (at > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     }
     l.unit0[n] = static_cast<int32_t>(at);
-    const int together = at * a.n_heads <= 2 * 152;
+    const int together = at * a.n_heads <= 2 * kSMs;
     const long long grid = together ? at * a.n_heads : (at * a.n_heads + 3) / 4;
     if (a.hd > 128) return start(ragged_join_kernel<T, N, 2>, grid, 1, 128, 0, true, s, a, l, together);
     return start(ragged_join_kernel<T, N, 1>, grid, 1, 128, 0, true, s, a, l, together);

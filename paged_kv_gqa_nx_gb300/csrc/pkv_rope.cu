@@ -148,7 +148,7 @@ cudaError_t launch_e(const RopePacked &a, cudaStream_t s) {
     const int per_head = a.n_pairs / E, heads = a.heads[0] + a.heads[1];
     const int lanes = std::max(1, std::min((heads + kHeads - 1) / kHeads, kThreads / per_head));
     const int per_row = per_head * lanes;
-    const int n_tok = std::max(1, std::min({kThreads / per_row, kMaxRows, a.n_rows / (2 * 152)}));
+    const int n_tok = std::max(1, std::min({kThreads / per_row, kMaxRows, a.n_rows / (2 * kSMs)}));
     const int64_t grid = (static_cast<int64_t>(a.n_rows) + n_tok - 1) / n_tok;
     const size_t smem = sizeof(float2) * n_tok * a.n_pairs;
     rope_packed_kernel<T, E><<<static_cast<unsigned>(grid), (n_tok * per_row + 31) / 32 * 32, smem, s>>>(a, n_tok, lanes);
