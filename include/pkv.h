@@ -496,10 +496,11 @@ PKV_API int pkv_attn_packed(const void *Q, int64_t q_stride, const void *K, int6
  * (other streams, captured graphs) need one each.  Nothing is uploaded or
  * allocated; the call can be captured into a CUDA graph (the lengths are then
  * part of the graph), provided that the device's error word was set up outside a
- * capture before: by a call of the same lengths, or by any pkv_attn_packed.  Runs on `stream` and the current device.  Checks, in
- * order: lengths and sizes -> PKV_ERR_BAD_DIM, grouping -> PKV_ERR_BAD_GQA, dtype,
- * strides, workspace, rows, pointers -> PKV_ERR_ARG.  Failures found on the
- * device: pkv_contiguous_sync_error. */
+ * capture before: by a call of the same lengths, or by any pkv_attn_packed.  Runs on
+ * `stream` and the current device.  Checks, in order: lengths and sizes ->
+ * PKV_ERR_BAD_DIM, grouping -> PKV_ERR_BAD_GQA, dtype, strides, workspace, rows,
+ * pointers -> PKV_ERR_ARG.  Failures found on the device:
+ * pkv_contiguous_sync_error. */
 PKV_API int pkv_attn_cross(const void *Q, int64_t q_stride, int64_t q_rows, const int32_t *q_lens, const void *K,
                            int64_t k_stride, const void *V, int64_t v_stride, int64_t k_rows, const int32_t *k_lens,
                            const int32_t *k_start, int32_t dtype, int32_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,

@@ -9,8 +9,9 @@
 // The angle is kept in turns, as a fraction of 2^64: position * step mod 2^64
 // is exact however far the position, for a step cut to whole 2^-64 turns (an
 // f32 angle of position 100,000 is off by 4e-3, and f64 sines would take longer
-// than the rows: 150 operations a pair at 1/50 of the f32 rate).  The nearest quarter turn is taken off in whole
-// numbers, the rest, at most an eighth of a turn, goes through sincospi in f32.
+// than the rows: 150 operations a pair at 1/50 of the f32 rate).  The nearest
+// quarter turn is taken off in whole numbers, the rest, at most an eighth of a
+// turn, goes through sincospi in f32.
 //
 // A thread takes one piece of a row's pairs (16 bytes of each half of a head)
 // for several heads: its cosines and sines stay in registers, and all its loads
